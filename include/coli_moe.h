@@ -292,6 +292,148 @@ int coli_permute_noalloc(const int32_t* topk_idx, const void* x, int32_t T, int3
                          int32_t E, int32_t k, int32_t act, int32_t* counts, int32_t* offsets,
                          int32_t* row_token, int32_t* assign_row, void* x_perm, void* stream);
 
+/* ---- beside the layer: rotary positions, paged KV cache, decode attention --
+ * The attention half of a transformer block at decode time, around the same
+ * weights-in-HBM serving loop as the layer above (the pages keep a KV cache
+ * next to the experts: overview page section 3.4). Activations are bf16 or
+ * f32 with fp32 arithmetic; the cache keeps keys and values in the library's
+ * own formats. These calls take no handle: every buffer is the caller's, the
+ * structs below are read during the call and may be temporary. Rows of heads
+ * ([T][n_heads][head_dim]) take a stride in ELEMENTS between tokens, so a
+ * slice of a fused projection's output can be passed as it is; pointers and
+ * strides must keep every row 16-byte aligned. */
+
+/* Pairs turned together: elements i and i + rot_dim/2 (HALF), or 2i and
+ * 2i + 1 (INTERLEAVED), for i < rot_dim/2. Elements from rot_dim on are kept. */
+typedef enum { COLI_ROPE_HALF = 0, COLI_ROPE_INTERLEAVED = 1 } coli_rope_layout;
+
+/* Frequencies w_i = base^(-2i/rot_dim), i < rot_dim/2, scaled for contexts
+ * longer than the trained ones:
+ *   NONE    w_i;
+ *   LINEAR  w_i / factor (position interpolation);
+ *   NTK     base replaced by base * factor^(rot_dim/(rot_dim-2));
+ *   YARN    w_i * g_i + (w_i / factor) * (1 - g_i), where
+ *           g_i = clamp((turns_i - beta_slow) / (beta_fast - beta_slow), 0, 1)
+ *           and turns_i = original_positions * w_i / (2 pi). */
+typedef enum {
+  COLI_ROPE_NONE = 0,
+  COLI_ROPE_LINEAR = 1,
+  COLI_ROPE_NTK = 2,
+  COLI_ROPE_YARN = 3
+} coli_rope_scaling;
+
+typedef struct {
+  int32_t rot_dim;            /* even, 2..256 */
+  int32_t scaling;            /* coli_rope_scaling */
+  int32_t original_positions; /* YARN: trained context length (> 0) */
+  double base;                /* > 0 */
+  double factor;              /* LINEAR, NTK, YARN: context factor (> 0) */
+  double beta_fast;           /* YARN: turns above which w_i is kept (> beta_slow) */
+  double beta_slow;           /* YARN: turns below which w_i is divided */
+  double amplitude;           /* factor on cosines and sines (1; YaRN: 0.1 ln(factor) + 1) */
+} coli_rope_config;
+
+/* table [n_positions][rot_dim/2][2] f32 = amplitude * (cos, sin)(p * w_i),
+ * evaluated in fp64 and rounded once; built once, shared by every layer. */
+int coli_rope_table(const coli_rope_config* cfg, int32_t n_positions, float* table, void* stream);
+
+typedef struct {
+  const float* table;  /* [n_positions][rot_dim/2][2] (cos, sin), 16-byte aligned */
+  int32_t n_positions;
+  int32_t rot_dim;     /* even, 2..head_dim */
+  int32_t layout;      /* coli_rope_layout */
+  int32_t inverse;     /* 1: turn back (the sine's sign flipped). It is also the
+                          rotation's gradient: dx = inverse(dy) */
+} coli_rotary;
+
+/* Rotates the heads of q [T][n_q_heads][head_dim] and, unless k is NULL, of k
+ * [T][n_kv_heads][head_dim] (both `act` dtype) by their token's position:
+ * (a, b) -> (a cos - b sin, b cos + a sin) in fp32, rounded once. head_dim is
+ * a multiple of 8 up to 256. q_out / k_out may be q / k themselves (same
+ * stride) but must not overlap them otherwise. A token whose position is
+ * outside [0, n_positions) is copied unrotated and latches COLI_EDEVICE. */
+int coli_rope_apply(const coli_rotary* rotary, const int32_t* positions, int32_t T,
+                    int32_t head_dim, int32_t act, const void* q, size_t q_stride,
+                    int32_t n_q_heads, void* q_out, size_t q_out_stride, const void* k,
+                    size_t k_stride, int32_t n_kv_heads, void* k_out, size_t k_out_stride,
+                    void* stream);
+
+/* Pages of keys and of values, each [n_pages][n_kv_heads][page_size][row]:
+ *   COLI_F32   row = head_dim floats (f32 activations);
+ *   COLI_BF16  row = head_dim bf16 (bf16 activations, as the formats below);
+ *   COLI_MXFP8 row = head_dim E4M3 bytes;
+ *   COLI_MXFP4 row = head_dim/2 bytes of E2M1 nibbles (low = even element);
+ * MX: scales [n_pages][n_kv_heads][page_size][S], one E8M0 byte per 32
+ * elements, S = head_dim/32 rounded up to a multiple of 4 (the bytes from
+ * head_dim/32 on are neither read nor written). Place ("slot") of a token:
+ * page * page_size + offset in the page. Pools may pass 4 GiB. */
+typedef struct {
+  void* k;            /* 16-byte aligned */
+  void* v;
+  uint8_t* k_scale;   /* MX: 4-byte aligned; else ignored */
+  uint8_t* v_scale;
+  int32_t n_pages;    /* n_pages * page_size < 2^31 */
+  int32_t page_size;  /* multiple of 16, 16..4096 */
+  int32_t n_kv_heads; /* 1..256 */
+  int32_t head_dim;   /* multiple of 8 (MX: of 32), up to 256 */
+  int32_t dtype;      /* coli_dtype */
+} coli_kv_cache;
+
+/* Writes token t's keys k[t] and values v[t] ([T][n_kv_heads][head_dim], act
+ * dtype: f32 for an F32 cache, else bf16) at slot slots[t]; a slot of -1 skips
+ * the token. With `rotary` the keys are rotated by positions[t] on the way
+ * (fp32, not rounded before they are stored), and q [T][n_q_heads][head_dim],
+ * unless NULL, is rotated into q_out in the same launch (q_out may be q).
+ * MX blocks: scale 2^(floor(log2 max|x|) - emax), emax = 8 (E4M3) or 2
+ * (E2M1), exponent kept in [-127, 127], byte 127 for a block of zeros;
+ * elements rounded to nearest even and saturated; a block with a NaN or an
+ * infinity gets scale byte 255, which reads back as NaN throughout. Slots
+ * outside the pool and positions outside the table are not written and latch
+ * COLI_EDEVICE (q is copied unrotated there). Two tokens with one slot in one
+ * call leave either's row. */
+int coli_kv_append(const coli_kv_cache* cache, const void* k, size_t k_stride, const void* v,
+                   size_t v_stride, const int32_t* slots, int32_t T, const coli_rotary* rotary,
+                   const int32_t* positions, const void* q, size_t q_stride, int32_t n_q_heads,
+                   void* q_out, size_t q_out_stride, void* stream);
+
+/* Reads slots back: k_out[i], v_out[i] ([N][n_kv_heads][head_dim] act dtype,
+ * either may be NULL) = the decoded row of slots[i], zeros for -1 and for a
+ * slot outside the pool (which latches COLI_EDEVICE). MX values are exact in
+ * bf16 but for those below its normal range or beyond it, rounded to it. */
+int coli_kv_read(const coli_kv_cache* cache, const int32_t* slots, int32_t N, void* k_out,
+                 size_t k_out_stride, void* v_out, size_t v_out_stride, void* stream);
+
+typedef struct {
+  int32_t n_q_heads; /* multiple of n_kv_heads, up to 1024; query head i reads key head
+                        i / (n_q_heads / n_kv_heads) */
+  int32_t window;    /* 0, or only the last `window` tokens are seen */
+  float scale;       /* on the dot products (1/sqrt(head_dim) for most models) */
+} coli_attn_config;
+
+/* Attention of one new token a sequence over its cached context (the new
+ * token's own key and value appended before): for b < B and each query head,
+ *   out[b] = sum_j softmax_j(scale * q[b] . k_j) v_j,
+ * j over the last min(seq_lens[b], window) of the sequence's seq_lens[b]
+ * tokens, token j in page block_table[b][j / page_size]. q and out are
+ * [B][n_q_heads][head_dim] in the act dtype of the cache; lse
+ * [B][n_q_heads] f32 (or NULL) receives log sum_j exp(scale * q . k_j), with
+ * which results over parts of a context can be joined. A sequence of length
+ * 0, or whose every weight is 0 (scores of -inf), gives zeros and lse -inf.
+ * What lies past a sequence's end in its last page, NaN included, has no
+ * influence. block_table is [B][max_pages]; entries past a sequence's last
+ * page are not read. A page outside [0, n_pages) is left out, as are tokens
+ * past max_pages pages; a negative length counts as 0; each latches
+ * COLI_EDEVICE. Scores, softmax and sums are fp32 throughout. scratch:
+ * 16-byte aligned, coli_paged_attention_scratch_bytes(...) bytes, contents
+ * irrelevant; calls that may overlap need their own. */
+size_t coli_paged_attention_scratch_bytes(const coli_kv_cache* cache, int32_t B,
+                                          int32_t n_q_heads);
+int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg, const void* q,
+                         size_t q_stride, int32_t B, const int32_t* block_table,
+                         int32_t max_pages, const int32_t* seq_lens, void* out,
+                         size_t out_stride, float* lse, void* scratch, size_t scratch_bytes,
+                         void* stream);
+
 /* ---- fault-handling self-test ------------------------------------------ */
 /* Launches one block that waits on a shared-memory barrier nothing will ever
  * complete, giving up after spin_limit polls: it latches COLI_ETIMEOUT and

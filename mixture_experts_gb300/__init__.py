@@ -17,6 +17,8 @@ import threading
 
 F32, BF16, I4G128, MXFP8, MXFP4 = 0, 1, 2, 3, 4
 PATH_AUTO, PATH_DECODE, PATH_PREFILL = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 STATUS = {0: "COLI_OK", -1: "COLI_EINVAL", -2: "COLI_ENOMEM", -3: "COLI_ECUDA",
           -4: "COLI_EUNSUPPORTED", -5: "COLI_EDEVICE", -6: "COLI_ETIMEOUT"}
 COLI_OK, COLI_EINVAL, COLI_ENOMEM, COLI_ECUDA = 0, -1, -2, -3
@@ -45,6 +47,26 @@ class coli_moe_config(ctypes.Structure):
 class coli_moe_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "w_router", "b_router", "w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down")]
+
+
+class coli_rope_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rot_dim", "scaling", "original_positions")] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "beta_fast", "beta_slow", "amplitude")]
+
+
+class coli_rotary(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p)] + [(n, ctypes.c_int32) for n in (
+        "n_positions", "rot_dim", "layout", "inverse")]
+
+
+class coli_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim", "dtype")]
+
+
+class coli_attn_config(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 def build(force: bool = False) -> str:
@@ -80,6 +102,14 @@ _SIGS = {
     "coli_selftest_bounded_wait": ("I", ["I", "P"]),
     "coli_permute_noalloc": ("I", ["P", "P", "I", "I", "I", "I", "I", "P", "P", "P", "P", "P",
                                    "P"]),
+    "coli_rope_table": ("I", ["P", "I", "P", "P"]),
+    "coli_rope_apply": ("I", ["P", "P", "I", "I", "I"] + ["P", "Z", "I", "P", "Z"] * 2 + ["P"]),
+    "coli_kv_append": ("I", ["P", "P", "Z", "P", "Z", "P", "I", "P", "P", "P", "Z", "I", "P", "Z",
+                             "P"]),
+    "coli_kv_read": ("I", ["P", "P", "I", "P", "Z", "P", "Z", "P"]),
+    "coli_paged_attention_scratch_bytes": ("Z", ["P", "I", "I"]),
+    "coli_paged_attention": ("I", ["P", "P", "P", "Z", "I", "P", "I", "P", "P", "Z", "P", "P",
+                                   "Z", "P"]),
 }
 _CT = {"P": ctypes.c_void_p, "I": ctypes.c_int32, "Z": ctypes.c_size_t, "s": ctypes.c_char_p,
        None: None}
@@ -260,6 +290,50 @@ def coli_selftest_bounded_wait(spin_limit: int, stream=None) -> int:
     return lib().coli_selftest_bounded_wait(spin_limit, _stream(stream))
 
 
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def coli_rope_table(cfg: coli_rope_config, n_positions, table, stream=None) -> int:
+    return lib().coli_rope_table(_ref(cfg), n_positions, _ptr(table), _stream(stream))
+
+
+def coli_rope_apply(rotary: coli_rotary, positions, T, head_dim, act, q, q_stride, n_q_heads,
+                    q_out, q_out_stride, k=None, k_stride=0, n_kv_heads=0, k_out=None,
+                    k_out_stride=0, stream=None) -> int:
+    return lib().coli_rope_apply(_ref(rotary), _ptr(positions), T, head_dim, act, _ptr(q),
+                                 q_stride, n_q_heads, _ptr(q_out), q_out_stride, _ptr(k),
+                                 k_stride, n_kv_heads, _ptr(k_out), k_out_stride,
+                                 _stream(stream))
+
+
+def coli_kv_append(cache: coli_kv_cache, k, k_stride, v, v_stride, slots, T, rotary=None,
+                   positions=None, q=None, q_stride=0, n_q_heads=0, q_out=None, q_out_stride=0,
+                   stream=None) -> int:
+    return lib().coli_kv_append(_ref(cache), _ptr(k), k_stride, _ptr(v), v_stride, _ptr(slots), T,
+                                _ref(rotary), _ptr(positions), _ptr(q), q_stride, n_q_heads,
+                                _ptr(q_out), q_out_stride, _stream(stream))
+
+
+def coli_kv_read(cache: coli_kv_cache, slots, N, k_out, k_out_stride, v_out, v_out_stride,
+                 stream=None) -> int:
+    return lib().coli_kv_read(_ref(cache), _ptr(slots), N, _ptr(k_out), k_out_stride, _ptr(v_out),
+                              v_out_stride, _stream(stream))
+
+
+def coli_paged_attention_scratch_bytes(cache: coli_kv_cache, B: int, n_q_heads: int) -> int:
+    return lib().coli_paged_attention_scratch_bytes(_ref(cache), B, n_q_heads)
+
+
+def coli_paged_attention(cache: coli_kv_cache, cfg: coli_attn_config, q, q_stride, B, block_table,
+                         max_pages, seq_lens, out, out_stride, lse=None, scratch=None,
+                         scratch_bytes=0, stream=None) -> int:
+    return lib().coli_paged_attention(_ref(cache), _ref(cfg), _ptr(q), q_stride, B,
+                                      _ptr(block_table), max_pages, _ptr(seq_lens), _ptr(out),
+                                      out_stride, _ptr(lse), _ptr(scratch), scratch_bytes,
+                                      _stream(stream))
+
+
 # ---- convenience -------------------------------------------------------------------
 class MoELayer:
     """One MoE layer on the current CUDA device (weights copied at creation).
@@ -337,3 +411,216 @@ class MoELayer:
             self.close()
         except Exception:
             pass
+
+
+def _head_rows(name, x, n_heads, head_dim, dtype) -> int:
+    """Token stride (elements) of x [T][n_heads][head_dim], whose heads are
+    contiguous; raises ValueError on anything the kernels would misread."""
+    if x.dim() != 3 or x.dtype != dtype or not x.is_cuda:
+        raise ValueError(f"{name}: need a CUDA {dtype} tensor [T][heads][head_dim], got "
+                         f"{x.device} {x.dtype} {tuple(x.shape)}")
+    T, h, d = x.shape
+    s = x.stride()
+    if (n_heads is not None and h != n_heads) or (head_dim is not None and d != head_dim):
+        raise ValueError(f"{name}: shape {tuple(x.shape)} does not fit {n_heads} heads of "
+                         f"{head_dim}")
+    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        raise ValueError(f"{name}: a token's heads must be contiguous, strides {s}")
+    return s[0] if T > 1 else h * d
+
+
+def _ids(name, x, n):
+    """int32 contiguous CUDA vector of n entries."""
+    if str(x.dtype) != "torch.int32" or not x.is_cuda or x.dim() != 1 or x.shape[0] != n or \
+            (n > 1 and x.stride(0) != 1):
+        raise ValueError(f"{name}: need a contiguous int32 CUDA vector of {n}, got {x.device} "
+                         f"{x.dtype} {tuple(x.shape)}")
+    return x
+
+
+def _on(stream):
+    """Context in which `stream` (a torch stream or a raw handle) is the current
+    one, so that what a call allocates belongs to the stream that uses it."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+class Rotary:
+    """A rotary table ([n_positions][rot_dim/2][2] f32, cosines and sines) with
+    the layout it is applied in: "half" or "interleaved" (or ROPE_*)."""
+
+    def __init__(self, table, layout="half"):
+        lay = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}.get(layout, layout)
+        if table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous() or \
+                str(table.dtype) != "torch.float32" or not table.is_cuda:
+            raise ValueError("table: need a contiguous f32 CUDA tensor [n_positions][rot/2][2]")
+        self.table = table
+        self.c = coli_rotary(table.data_ptr(), table.shape[0], 2 * table.shape[1], lay, 0)
+        self.c_inverse = coli_rotary(table.data_ptr(), table.shape[0], 2 * table.shape[1], lay, 1)
+
+    @classmethod
+    def build(cls, rot_dim, n_positions, base=10000.0, layout="half", scaling=ROPE_NONE,
+              factor=1.0, original_positions=0, beta_fast=32.0, beta_slow=1.0, amplitude=1.0,
+              stream=None):
+        """Builds the table (coli_rope_table) and keeps it."""
+        import torch
+        if stream is not None:
+            with _on(stream):
+                return cls.build(rot_dim, n_positions, base, layout, scaling, factor,
+                                 original_positions, beta_fast, beta_slow, amplitude)
+        table = torch.empty(n_positions, rot_dim // 2, 2, dtype=torch.float32, device="cuda")
+        cfg = coli_rope_config(rot_dim, scaling, original_positions, base, factor, beta_fast,
+                               beta_slow, amplitude)
+        _check(coli_rope_table(cfg, n_positions, table), "coli_rope_table")
+        return cls(table, layout)
+
+
+def rope(rotary: Rotary, positions, q, k=None, q_out=None, k_out=None, inverse=False,
+         stream=None):
+    """Rotated q and k (or (q, None)); q_out / k_out may be q / k themselves.
+    inverse=True turns back, which is also the gradient with respect to q and k."""
+    import torch
+    if stream is not None:
+        with _on(stream):
+            return rope(rotary, positions, q, k, q_out, k_out, inverse)
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"q: need f32 or bf16, got {q.dtype}")
+    T, hq, d = q.shape if q.dim() == 3 else (0, 0, 0)
+    qs = _head_rows("q", q, hq, d, q.dtype)
+    if q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device)
+    qos = _head_rows("q_out", q_out, hq, d, q.dtype)
+    hk = ks = kos = 0
+    if k is not None:
+        hk = k.shape[1]
+        ks = _head_rows("k", k, hk, d, q.dtype)
+        if k_out is None:
+            k_out = torch.empty((T, hk, d), dtype=q.dtype, device=q.device)
+        kos = _head_rows("k_out", k_out, hk, d, q.dtype)
+        if k.shape[0] != T or k_out.shape[0] != T:
+            raise ValueError("q and k need the same number of tokens")
+    if q_out.shape[0] != T:
+        raise ValueError("q and q_out need the same number of tokens")
+    _check(coli_rope_apply(rotary.c_inverse if inverse else rotary.c, _ids("positions", positions, T),
+                           T, d, F32 if q.dtype == torch.float32 else BF16, q, qs, hq, q_out, qos,
+                           k, ks, hk, k_out, kos), "coli_rope_apply")
+    return q_out, k_out
+
+
+class PagedKVCache:
+    """Pages of keys and values in the caller's tensors: k, v
+    [n_pages][n_kv_heads][page_size][row] of float32, bfloat16 or (MX) uint8,
+    with MX scales [..][page_size][S] uint8, S = head_dim/32 rounded up to a
+    multiple of 4. The format follows from the type and the row length."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, head_dim=None):
+        import torch
+        self._torch = torch
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or \
+                not (k.is_contiguous() and v.is_contiguous() and k.is_cuda and v.is_cuda):
+            raise ValueError("k and v: need equal contiguous CUDA tensors "
+                             "[n_pages][n_kv_heads][page_size][row]")
+        n_pages, hk, page, row = k.shape
+        head_dim = row if head_dim is None else head_dim
+        dtype = {(torch.float32, head_dim): F32, (torch.bfloat16, head_dim): BF16,
+                 (torch.uint8, head_dim): MXFP8, (torch.uint8, head_dim // 2): MXFP4}.get(
+                     (k.dtype, row))
+        if dtype is None:
+            raise ValueError(f"rows of {row} x {k.dtype} hold no format of head_dim {head_dim}")
+        if dtype in (MXFP8, MXFP4):
+            want = (n_pages, hk, page, (head_dim // 32 + 3) // 4 * 4)
+            for s in (k_scale, v_scale):
+                if s is None or tuple(s.shape) != want or s.dtype != torch.uint8 or \
+                        not s.is_contiguous() or not s.is_cuda:
+                    raise ValueError(f"k_scale and v_scale: need contiguous uint8 CUDA {want}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_kv_heads, self.head_dim, self.page_size = hk, head_dim, page
+        self.act_torch = torch.float32 if dtype == F32 else torch.bfloat16
+        self.c = coli_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), n_pages, page, hk,
+                               head_dim, dtype)
+
+    @classmethod
+    def empty(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=BF16):
+        """A zeroed pool in format F32, BF16, MXFP8 or MXFP4."""
+        import torch
+        shape = (n_pages, n_kv_heads, page_size)
+        t = {F32: torch.float32, BF16: torch.bfloat16}.get(dtype, torch.uint8)
+        row = head_dim // 2 if dtype == MXFP4 else head_dim
+        pools = [torch.zeros(*shape, row, dtype=t, device="cuda") for _ in range(2)]
+        if dtype in (MXFP8, MXFP4):
+            s = (head_dim // 32 + 3) // 4 * 4
+            pools += [torch.zeros(*shape, s, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        return cls(*pools, head_dim=head_dim)
+
+    def append(self, k, v, slots, rotary: Rotary = None, positions=None, q=None, q_out=None,
+               stream=None):
+        """Stores token t's k[t], v[t] at slots[t] (-1: skipped), keys rotated
+        when `rotary` is given; returns the rotated q (None without q)."""
+        if stream is not None:
+            with _on(stream):
+                return self.append(k, v, slots, rotary, positions, q, q_out)
+        T = k.shape[0]
+        ks = _head_rows("k", k, self.n_kv_heads, self.head_dim, self.act_torch)
+        vs = _head_rows("v", v, self.n_kv_heads, self.head_dim, self.act_torch)
+        if v.shape[0] != T:
+            raise ValueError("k and v need the same number of tokens")
+        hq = qs = qos = 0
+        if q is not None:
+            hq = q.shape[1]
+            qs = _head_rows("q", q, hq, self.head_dim, self.act_torch)
+            if q_out is None:
+                q_out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            qos = _head_rows("q_out", q_out, hq, self.head_dim, self.act_torch)
+            if q.shape[0] != T or q_out.shape[0] != T:
+                raise ValueError("q and k need the same number of tokens")
+        if rotary is not None:
+            if positions is None:
+                raise ValueError("a rotary needs positions")
+            _ids("positions", positions, T)
+        _check(coli_kv_append(self.c, k, ks, v, vs, _ids("slots", slots, T), T,
+                              rotary.c if rotary is not None else None, positions, q, qs, hq,
+                              q_out if q is not None else None, qos), "coli_kv_append")
+        return q_out if q is not None else None
+
+    def read(self, slots, stream=None):
+        """(k, v) rows [N][n_kv_heads][head_dim] of slots, zeros for -1."""
+        if stream is not None:
+            with _on(stream):
+                return self.read(slots)
+        N = slots.shape[0]
+        out = [self._torch.empty((N, self.n_kv_heads, self.head_dim), dtype=self.act_torch,
+                                 device=self.k.device) for _ in range(2)]
+        s = self.n_kv_heads * self.head_dim
+        _check(coli_kv_read(self.c, _ids("slots", slots, N), N, out[0], s, out[1], s),
+               "coli_kv_read")
+        return out[0], out[1]
+
+    def attend(self, q, block_table, seq_lens, scale=None, window=0, out=None, return_lse=False,
+               stream=None):
+        """Attention of one new token a sequence: q [B][n_q_heads][head_dim],
+        block_table [B][max_pages] int32, seq_lens [B] int32 -> out like q
+        (and lse [B][n_q_heads] f32). scale defaults to head_dim^-0.5."""
+        torch = self._torch
+        if stream is not None:
+            with _on(stream):
+                return self.attend(q, block_table, seq_lens, scale, window, out, return_lse)
+        B, hq = q.shape[0], q.shape[1]
+        qs = _head_rows("q", q, hq, self.head_dim, self.act_torch)
+        if out is None:
+            out = torch.empty((B, hq, self.head_dim), dtype=q.dtype, device=q.device)
+        os_ = _head_rows("out", out, hq, self.head_dim, self.act_torch)
+        if out.shape[0] != B:
+            raise ValueError("q and out need the same number of sequences")
+        if block_table.dim() != 2 or block_table.shape[0] != B or not block_table.is_cuda or \
+                block_table.dtype != torch.int32 or not block_table.is_contiguous():
+            raise ValueError(f"block_table: need a contiguous int32 CUDA tensor [{B}][max_pages]")
+        lse = torch.empty((B, hq), dtype=torch.float32, device=q.device) if return_lse else None
+        n = coli_paged_attention_scratch_bytes(self.c, B, hq) if B else 0
+        scratch = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        cfg = coli_attn_config(hq, window, self.head_dim ** -0.5 if scale is None else scale)
+        _check(coli_paged_attention(self.c, cfg, q, qs, B, block_table, block_table.shape[1],
+                                    _ids("seq_lens", seq_lens, B), out, os_, lse, scratch, n),
+               "coli_paged_attention")
+        return (out, lse) if return_lse else out
