@@ -420,7 +420,8 @@ typedef struct {
  * which results over parts of a context can be joined. A sequence of length
  * 0, or whose every weight is 0 (scores of -inf), gives zeros and lse -inf.
  * What lies past a sequence's end in its last page, NaN included, has no
- * influence. block_table is [B][max_pages]; entries past a sequence's last
+ * influence. An infinite value in sight makes its output element infinite or
+ * NaN. out must not overlap q. block_table is [B][max_pages]; entries past a sequence's last
  * page are not read. A page outside [0, n_pages) is left out, as are tokens
  * past max_pages pages; a negative length counts as 0; each latches
  * COLI_EDEVICE. Scores, softmax and sums are fp32 throughout. scratch:

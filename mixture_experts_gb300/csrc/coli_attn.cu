@@ -270,6 +270,7 @@ int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg
   const int act = act_of(c);
   if (int rc = check_rows("q", q, q_stride, cfg->n_q_heads, c.head_dim, act)) return rc;
   if (int rc = check_rows("out", out, out_stride, cfg->n_q_heads, c.head_dim, act)) return rc;
+  if (q == out) return reject(COLI_EINVAL, "out must not be q");
   if (block_table == nullptr || seq_lens == nullptr)
     return reject(COLI_EINVAL, "block_table and seq_lens must be set");
   if (max_pages < 1 || static_cast<int64_t>(max_pages) * c.page_size > INT32_MAX)

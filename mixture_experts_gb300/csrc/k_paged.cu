@@ -1,130 +1,213 @@
-// Attention of one new token a sequence over its paged context.
-//
-// One block per (sequence, query head); its warps take the keys in turn. A
-// warp holds its query in registers (lane l: elements l, l + 32, ...), keeps
-// the running maximum m and sum l of the softmax over its keys and the
-// weighted values o, and rescales them when the maximum grows; the block joins
-// its warps at the end:  m = max m_w,  l = sum l_w 2^(m_w - m),  o likewise.
-#include <math.h>
-
-#include "attn.h"
-#include "common.cuh"
-#include "mx.cuh"
+// Paged decode attention: choice of the kernel's form, and the join of the
+// segments that block borders cut.
+#include "paged_launch.cuh"
 
 namespace coli {
+namespace paged {
 namespace {
 
-constexpr int kWarps = 8;
-
-template <int FMT>
-COLI_DEV float element(const char* row, const uint8_t* scales, int d) {
-  if constexpr (FMT == DT_F32) return reinterpret_cast<const float*>(row)[d];
-  if constexpr (FMT == DT_BF16)
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d]);
-  uint32_t h[4];
-  if constexpr (FMT == DT_MXFP8) {
-    e4m3x8_f16(static_cast<uint8_t>(row[d]), 0, h);
-  } else {
-    const uint32_t byte = static_cast<uint8_t>(row[d / 2]);
-    e2m1x8_f16(d % 2 ? byte >> 4 : byte & 15u, h);
+// Block (c, y) joins the segment that starts in block c of the main kernel and
+// ends in a later one: its partial sums o, l with maxima m, in the order of the
+// blocks, o = sum o_k 2^(m_k - m). A group of registers is one 16 x 8 tile of
+// O^T. With gridDim.y = 1 a warp takes whole groups; otherwise block y takes
+// group y and its warps share the partials.
+template <int DP, int NT, bool F32>
+__global__ void __launch_bounds__(256) k_join(const Params p) {
+  constexpr int kGroups = DP / 16 * NT, kRegs = kGroups * 4;
+  constexpr int kPart = kRegs * 32 + 16 * NT;
+  __shared__ float s_o[8][4][32], s_ml[8][4][4];
+  const int lane = lane_id(), w = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
+  const PagedArgs& a = p.a;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 sp = p.span[blockIdx.x];
+  if (sp.w == 0) return;
+  const bool shared = gridDim.y > 1;
+  const int step = shared ? 8 : 1, D = a.c.head_dim;
+  for (int gr = shared ? blockIdx.y : w; gr < kGroups; gr += shared ? kGroups : 8) {
+    const int i = gr / NT, nt = gr - i * NT;
+    float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kBatch = 4;
+    for (int k = shared ? w : 0; k < sp.w; k += step * kBatch) {
+      float pm[kBatch][2], pl[kBatch][2], po[kBatch][4];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int kk = k + e * step;
+        const bool in = kk < sp.w;
+        const float* src =
+            p.part + static_cast<size_t>(2 * (blockIdx.x + kk) + (kk == 0 ? sp.z : 0)) * kPart;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          pm[e][c] = in ? src[kRegs * 32 + nt * 8 + 2 * t + c] : -FLT_MAX;
+          pl[e][c] = in ? src[kRegs * 32 + 8 * NT + nt * 8 + 2 * t + c] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) po[e][c] = in ? src[gr * 128 + c * 32 + lane] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float top = fmaxf(m[c], pm[e][c]);
+          const float f = ex2(m[c] - top), fk = ex2(pm[e][c] - top);
+          m[c] = top;
+          l[c] = l[c] * f + pl[e][c] * fk;
+          o[c] = o[c] * f + po[e][c] * fk;
+          o[c + 2] = o[c + 2] * f + po[e][c + 2] * fk;
+        }
+    }
+    if (shared) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s_o[w][c][lane] = o[c];
+      if (g == 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) s_ml[w][t][c] = m[c], s_ml[w][t][2 + c] = l[c];
+      }
+      __syncthreads();
+      if (w != 0) return;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[c] = -FLT_MAX;
+        for (int k = 0; k < 8; ++k) m[c] = fmaxf(m[c], s_ml[k][t][c]);
+        l[c] = o[c] = o[c + 2] = 0.f;
+        for (int k = 0; k < 8; ++k) {
+          const float f = ex2(s_ml[k][t][c] - m[c]);
+          l[c] += s_ml[k][t][2 + c] * f;
+          o[c] += s_o[k][c][lane] * f;
+          o[c + 2] += s_o[k][c + 2][lane] * f;
+        }
+      }
+    }
+    const int b = sp.x, h = sp.y / p.blocks, row0 = (sp.y - h * p.blocks) * 8 * NT;
+    const int d = (i / 4) * 64 + g * 8 + (i % 4) * 2;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = row0 + nt * 8 + 2 * t + c;
+      if (r >= p.group) continue;
+      const int hq = h * p.group + r;
+      const float inv = l[c] == 0.f ? 0.f : 1.f / l[c];
+      if (d < D) {
+        const size_t at = static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(hq) * D + d;
+        const float y0 = l[c] == 0.f ? 0.f : o[c] * inv;
+        const float y1 = l[c] == 0.f ? 0.f : o[c + 2] * inv;
+        if constexpr (F32)
+          *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(y0, y1);
+        else
+          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+              pack_bf16x2(y0, y1);
+      }
+      if (a.lse != nullptr && i == 0 && g == 0)
+        a.lse[static_cast<size_t>(b) * a.n_q_heads + hq] =
+            l[c] == 0.f ? -INFINITY : (m[c] + log2f(l[c])) * 0.6931471805599453f;
+    }
   }
-  float x[8];
-  f16x8_f32(h, x);
-  return x[0] * e8m0_f32(scales[d / kMxBlock]);
 }
 
+// The join is launched so that its blocks may be placed while the main kernel
+// drains; they wait for its end (griddepcontrol.wait) before they read.
+template <int DP, int NT, bool F32>
+cudaError_t launch_join(const Params& p, int grid, int ys, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, ys);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_join<DP, NT, F32>, p);
+}
+
+int sm_count() {
+  static int n[128] = {};
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 152;
+  if (n[dev] == 0 &&
+      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    n[dev] = v;
+  return n[dev] ? n[dev] : 152;
+}
+
+struct Form {
+  int dp, nt, blocks, per_sm, warps;
+  size_t part;  // floats of a partial slot
+};
+
 template <int FMT>
-__global__ void __launch_bounds__(kWarps * 32) k_paged(const PagedArgs a) {
-  constexpr int kPer = kMaxHeadDim / 32;
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][kMaxHeadDim];
-  const int b = blockIdx.y, hq = blockIdx.x, D = a.c.head_dim;
-  const int h = hq / (a.n_q_heads / a.c.n_heads);
-  const int w = threadIdx.x / 32, lane = lane_id();
-  int len = a.seq_lens[b];
-  const int most = a.max_pages * a.c.page_size;
-  if (len < 0 || len > most) {
-    if (threadIdx.x == 0) latch_error(a.status, kErrDevice);
-    len = len < 0 ? 0 : most;
+int per_sm_of(int dp, int nt, int* warps) {
+  if (dp == 64) {
+    *warps = Cfg<FMT, 64, 1>::kWarps;
+    return nt == 2 ? Cfg<FMT, 64, 2>::kPerSm : Cfg<FMT, 64, 1>::kPerSm;
   }
-  const int start = a.window > 0 && len > a.window ? len - a.window : 0;
-  const size_t qo = b * a.q_stride + static_cast<size_t>(hq) * D;
-  float q[kPer], o[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int d = lane + 32 * i;
-    o[i] = q[i] = 0.f;
-    if (d < D)
-      q[i] = FMT == DT_F32 ? static_cast<const float*>(a.q)[qo + d]
-                           : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[qo + d]);
+  if (dp == 128) {
+    *warps = Cfg<FMT, 128, 1>::kWarps;
+    return nt == 2 ? Cfg<FMT, 128, 2>::kPerSm : Cfg<FMT, 128, 1>::kPerSm;
   }
-  float m = -INFINITY, l = 0.f;
-  for (int j = start + w; j < len; j += kWarps) {
-    const int pi = j / a.c.page_size;
-    const int page = a.block_table[static_cast<size_t>(b) * a.max_pages + pi];
-    if (page < 0 || page >= a.c.n_pages) {
-      if (lane == 0) latch_error(a.status, kErrDevice);
-      continue;
-    }
-    const size_t row = kv_row(a.c, page, h, j - pi * a.c.page_size);
-    const char* kr = a.c.k + row * a.c.row_bytes;
-    const char* vr = a.c.v + row * a.c.row_bytes;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int d = lane + 32 * i;
-      if (d < D) s += q[i] * element<FMT>(kr, a.c.k_scale + row * a.c.scale_stride, d);
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale;
-    const float mn = fmaxf(m, s);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float old = expf(m - base), p = expf(s - base);
-    l = l * old + p;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int d = lane + 32 * i;
-      if (d < D) o[i] = o[i] * old + p * element<FMT>(vr, a.c.v_scale + row * a.c.scale_stride, d);
-    }
-    m = mn;
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (lane + 32 * i < D) so[w][lane + 32 * i] = o[i];
-  if (lane == 0) sm[w] = m, sl[w] = l;
-  __syncthreads();
-  float mm = -INFINITY;
-  for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, sm[i]);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f;
-  for (int i = 0; i < kWarps; ++i) ll += sl[i] * expf(sm[i] - base);
-  const size_t oo = b * a.out_stride + static_cast<size_t>(hq) * D;
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float x = 0.f;
-    for (int i = 0; i < kWarps; ++i) x += so[i][d] * expf(sm[i] - base);
-    x = ll == 0.f ? 0.f : x / ll;
-    if constexpr (FMT == DT_F32)
-      static_cast<float*>(a.out)[oo + d] = x;
-    else
-      static_cast<__nv_bfloat16*>(a.out)[oo + d] = __float2bfloat16_rn(x);
-  }
-  if (a.lse != nullptr && threadIdx.x == 0)
-    a.lse[static_cast<size_t>(b) * a.n_q_heads + hq] = ll == 0.f ? -INFINITY : logf(ll) + base;
+  *warps = Cfg<FMT, 256, 1>::kWarps;
+  return Cfg<FMT, 256, 1>::kPerSm;
+}
+
+Form form_of(const KvView& c, int n_q_heads) {
+  Form f{};
+  const int group = n_q_heads / c.n_heads;
+  f.dp = c.head_dim <= 64 ? 64 : (c.head_dim <= 128 ? 128 : 256);
+  f.nt = group <= 8 || f.dp == 256 || c.dtype == DT_F32 ? 1 : 2;
+  f.blocks = (group + 8 * f.nt - 1) / (8 * f.nt);
+  f.per_sm = c.dtype == DT_F32     ? per_sm_of<DT_F32>(f.dp, f.nt, &f.warps)
+             : c.dtype == DT_BF16  ? per_sm_of<DT_BF16>(f.dp, f.nt, &f.warps)
+             : c.dtype == DT_MXFP8 ? per_sm_of<DT_MXFP8>(f.dp, f.nt, &f.warps)
+                                   : per_sm_of<DT_MXFP4>(f.dp, f.nt, &f.warps);
+  f.part = static_cast<size_t>(f.dp / 16 * 4 * f.nt) * 32 + 16 * f.nt;
+  return f;
 }
 
 }  // namespace
+}  // namespace paged
 
-size_t paged_scratch_bytes(const KvView& c, int B, int n_q_heads) { return 0; }
+size_t paged_scratch_bytes(const KvView& c, int B, int n_q_heads) {
+  const paged::Form f = paged::form_of(c, n_q_heads);
+  const size_t blocks = static_cast<size_t>(paged::sm_count()) * f.per_sm;
+  return blocks * (2 * f.part * sizeof(float) + sizeof(int4));
+}
 
 cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
-  const dim3 grid(a.n_q_heads, a.B);
+  using namespace paged;
+  const Form f = form_of(a.c, a.n_q_heads);
+  const int most = sm_count() * f.per_sm;
+  Params p{};
+  p.a = a;
+  p.group = a.n_q_heads / a.c.n_heads;
+  p.blocks = f.blocks;
+  p.part = a.scratch;
+  p.span = reinterpret_cast<int4*>(a.scratch + 2 * f.part * most);
+  // no more blocks than pieces of one tile a warp
+  const int64_t segments = static_cast<int64_t>(a.B) * a.c.n_heads * f.blocks;
+  const int64_t tiles = static_cast<int64_t>(a.max_pages) * (a.c.page_size / kTile);
+  const int64_t pieces = (segments * tiles + f.warps - 1) / f.warps;
+  const int grid = pieces < most ? static_cast<int>(pieces) : most;
+  cudaError_t e;
   switch (a.c.dtype) {
-    case DT_F32: k_paged<DT_F32><<<grid, kWarps * 32, 0, st>>>(a); break;
-    case DT_BF16: k_paged<DT_BF16><<<grid, kWarps * 32, 0, st>>>(a); break;
-    case DT_MXFP8: k_paged<DT_MXFP8><<<grid, kWarps * 32, 0, st>>>(a); break;
-    default: k_paged<DT_MXFP4><<<grid, kWarps * 32, 0, st>>>(a); break;
+    case DT_F32: e = launch_f32(p, f.dp, f.nt, grid, st); break;
+    case DT_BF16: e = launch_bf16(p, f.dp, f.nt, grid, st); break;
+    case DT_MXFP8: e = launch_mxfp8(p, f.dp, f.nt, grid, st); break;
+    default: e = launch_mxfp4(p, f.dp, f.nt, grid, st); break;
   }
-  return cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // long segments (many partials each): the warps of a block share a group
+  const int groups = f.dp / 16 * f.nt;
+  const int ys = segments * 4 < grid ? groups : 1;
+  if (a.c.dtype == DT_F32) {
+    if (f.dp == 64) return launch_join<64, 1, true>(p, grid, ys, st);
+    if (f.dp == 128) return launch_join<128, 1, true>(p, grid, ys, st);
+    return launch_join<256, 1, true>(p, grid, ys, st);
+  }
+  if (f.dp == 64)
+    return f.nt == 2 ? launch_join<64, 2, false>(p, grid, ys, st)
+                     : launch_join<64, 1, false>(p, grid, ys, st);
+  if (f.dp == 128)
+    return f.nt == 2 ? launch_join<128, 2, false>(p, grid, ys, st)
+                     : launch_join<128, 1, false>(p, grid, ys, st);
+  return launch_join<256, 1, false>(p, grid, ys, st);
 }
 
 }  // namespace coli

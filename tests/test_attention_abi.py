@@ -131,7 +131,7 @@ def test_read_rejects():
 
 @pytest.mark.parametrize("kw,word", [
     (dict(B=-1), "B="), (dict(B=65536), "B="), (dict(q=None), "q must"),
-    (dict(q_stride=128), "stride"), (dict(out=FAKE + 4), "aligned"),
+    (dict(q_stride=128), "stride"), (dict(out=FAKE), "must not be q"), (dict(out=FAKE + 4), "aligned"),
     (dict(block_table=None), "block_table"), (dict(seq_lens=None), "seq_lens"),
     (dict(max_pages=0), "max_pages"), (dict(max_pages=1 << 27), "max_pages"),
     (dict(cfg=moe.coli_attn_config(3, 0, 1.0)), "multiple"),
@@ -141,7 +141,7 @@ def test_read_rejects():
     (dict(cfg=moe.coli_attn_config(4, 0, math.nan)), "scale")])
 def test_attention_rejects(kw, word):
     a = dict(cache=cache(), cfg=moe.coli_attn_config(4, 0, 0.125), q=FAKE, q_stride=256, B=2,
-             block_table=FAKE, max_pages=4, seq_lens=FAKE, out=FAKE, out_stride=256,
+             block_table=FAKE, max_pages=4, seq_lens=FAKE, out=2 * FAKE, out_stride=256,
              scratch=FAKE, scratch_bytes=1 << 40)
     a.update(kw)
     assert moe.coli_paged_attention(**a, stream=0) == moe.COLI_EINVAL
