@@ -118,6 +118,8 @@ _CT = {"P": ctypes.c_void_p, "I": ctypes.c_int32, "Z": ctypes.c_size_t, "s": cty
 def lib():
     """The loaded library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -413,29 +415,48 @@ class MoELayer:
             pass
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported at the first use of a wrapper that takes tensors."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _current_stream(x) -> int:
+    """Raw handle of the current stream of tensor x's device: what
+    torch.cuda.current_stream(x.device).cuda_stream gives, without building the
+    stream object (a decode step's small calls are bound by the host)."""
+    return _torch._C._cuda_getCurrentRawStream(x.get_device())
+
+
 def _head_rows(name, x, n_heads, head_dim, dtype) -> int:
     """Token stride (elements) of x [T][n_heads][head_dim], whose heads are
     contiguous; raises ValueError on anything the kernels would misread."""
-    if x.dim() != 3 or x.dtype != dtype or not x.is_cuda:
+    if x.dim() != 3 or x.dtype is not dtype or not x.is_cuda:
         raise ValueError(f"{name}: need a CUDA {dtype} tensor [T][heads][head_dim], got "
                          f"{x.device} {x.dtype} {tuple(x.shape)}")
     T, h, d = x.shape
-    s = x.stride()
-    if (n_heads is not None and h != n_heads) or (head_dim is not None and d != head_dim):
+    if h != n_heads or d != head_dim:
         raise ValueError(f"{name}: shape {tuple(x.shape)} does not fit {n_heads} heads of "
                          f"{head_dim}")
-    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
-        raise ValueError(f"{name}: a token's heads must be contiguous, strides {s}")
-    return s[0] if T > 1 else h * d
+    s0, s1, s2 = x.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous, strides {x.stride()}")
+    return s0 if T > 1 else h * d
 
 
-def _ids(name, x, n):
-    """int32 contiguous CUDA vector of n entries."""
-    if str(x.dtype) != "torch.int32" or not x.is_cuda or x.dim() != 1 or x.shape[0] != n or \
-            (n > 1 and x.stride(0) != 1):
+def _ids(name, x, n) -> int:
+    """Address of a contiguous int32 CUDA vector of n entries."""
+    if x.dtype is not _torch.int32 or not x.is_cuda or x.dim() != 1 or x.shape[0] != n or \
+            not x.is_contiguous():
         raise ValueError(f"{name}: need a contiguous int32 CUDA vector of {n}, got {x.device} "
                          f"{x.dtype} {tuple(x.shape)}")
-    return x
+    return x.data_ptr()
 
 
 def _on(stream):
@@ -452,20 +473,22 @@ class Rotary:
     the layout it is applied in: "half" or "interleaved" (or ROPE_*)."""
 
     def __init__(self, table, layout="half"):
+        torch = _t()
         lay = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}.get(layout, layout)
         if table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous() or \
-                str(table.dtype) != "torch.float32" or not table.is_cuda:
+                table.dtype is not torch.float32 or not table.is_cuda:
             raise ValueError("table: need a contiguous f32 CUDA tensor [n_positions][rot/2][2]")
         self.table = table
         self.c = coli_rotary(table.data_ptr(), table.shape[0], 2 * table.shape[1], lay, 0)
         self.c_inverse = coli_rotary(table.data_ptr(), table.shape[0], 2 * table.shape[1], lay, 1)
+        self._ref, self._ref_inverse = ctypes.byref(self.c), ctypes.byref(self.c_inverse)
 
     @classmethod
     def build(cls, rot_dim, n_positions, base=10000.0, layout="half", scaling=ROPE_NONE,
               factor=1.0, original_positions=0, beta_fast=32.0, beta_slow=1.0, amplitude=1.0,
               stream=None):
         """Builds the table (coli_rope_table) and keeps it."""
-        import torch
+        torch = _t()
         if stream is not None:
             with _on(stream):
                 return cls.build(rot_dim, n_positions, base, layout, scaling, factor,
@@ -481,31 +504,46 @@ def rope(rotary: Rotary, positions, q, k=None, q_out=None, k_out=None, inverse=F
          stream=None):
     """Rotated q and k (or (q, None)); q_out / k_out may be q / k themselves.
     inverse=True turns back, which is also the gradient with respect to q and k."""
-    import torch
     if stream is not None:
         with _on(stream):
             return rope(rotary, positions, q, k, q_out, k_out, inverse)
-    if q.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"q: need f32 or bf16, got {q.dtype}")
-    T, hq, d = q.shape if q.dim() == 3 else (0, 0, 0)
-    qs = _head_rows("q", q, hq, d, q.dtype)
+    torch = _torch
+    dt = q.dtype
+    if dt is torch.bfloat16:
+        act = BF16
+    elif dt is torch.float32:
+        act = F32
+    else:
+        raise ValueError(f"q: need f32 or bf16, got {dt}")
+    if q.dim() != 3:
+        raise ValueError(f"q: need [T][heads][head_dim], got {tuple(q.shape)}")
+    T, hq, d = q.shape
+    qs = _head_rows("q", q, hq, d, dt)
     if q_out is None:
-        q_out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device)
-    qos = _head_rows("q_out", q_out, hq, d, q.dtype)
+        q_out = q.new_empty((T, hq, d))
+        qos = hq * d
+    else:
+        qos = _head_rows("q_out", q_out, hq, d, dt)
+        if q_out.shape[0] != T:
+            raise ValueError("q and q_out need the same number of tokens")
+    kp = kop = None
     hk = ks = kos = 0
     if k is not None:
         hk = k.shape[1]
-        ks = _head_rows("k", k, hk, d, q.dtype)
+        ks = _head_rows("k", k, hk, d, dt)
         if k_out is None:
-            k_out = torch.empty((T, hk, d), dtype=q.dtype, device=q.device)
-        kos = _head_rows("k_out", k_out, hk, d, q.dtype)
+            k_out = k.new_empty((k.shape[0], hk, d))
+            kos = hk * d
+        else:
+            kos = _head_rows("k_out", k_out, hk, d, dt)
         if k.shape[0] != T or k_out.shape[0] != T:
             raise ValueError("q and k need the same number of tokens")
-    if q_out.shape[0] != T:
-        raise ValueError("q and q_out need the same number of tokens")
-    _check(coli_rope_apply(rotary.c_inverse if inverse else rotary.c, _ids("positions", positions, T),
-                           T, d, F32 if q.dtype == torch.float32 else BF16, q, qs, hq, q_out, qos,
-                           k, ks, hk, k_out, kos), "coli_rope_apply")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    rc = lib().coli_rope_apply(rotary._ref_inverse if inverse else rotary._ref,
+                               _ids("positions", positions, T), T, d, act, q.data_ptr(), qs, hq,
+                               q_out.data_ptr(), qos, kp, ks, hk, kop, kos, _current_stream(q))
+    if rc:
+        _check(rc, "coli_rope_apply")
     return q_out, k_out
 
 
@@ -516,8 +554,7 @@ class PagedKVCache:
     multiple of 4. The format follows from the type and the row length."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None, head_dim=None):
-        import torch
-        self._torch = torch
+        torch = _t()
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or \
                 not (k.is_contiguous() and v.is_contiguous() and k.is_cuda and v.is_cuda):
             raise ValueError("k and v: need equal contiguous CUDA tensors "
@@ -540,11 +577,12 @@ class PagedKVCache:
         self.act_torch = torch.float32 if dtype == F32 else torch.bfloat16
         self.c = coli_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), n_pages, page, hk,
                                head_dim, dtype)
+        self._ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=BF16):
         """A zeroed pool in format F32, BF16, MXFP8 or MXFP4."""
-        import torch
+        torch = _t()
         shape = (n_pages, n_kv_heads, page_size)
         t = {F32: torch.float32, BF16: torch.bfloat16}.get(dtype, torch.uint8)
         row = head_dim // 2 if dtype == MXFP4 else head_dim
@@ -561,27 +599,33 @@ class PagedKVCache:
         if stream is not None:
             with _on(stream):
                 return self.append(k, v, slots, rotary, positions, q, q_out)
-        T = k.shape[0]
-        ks = _head_rows("k", k, self.n_kv_heads, self.head_dim, self.act_torch)
-        vs = _head_rows("v", v, self.n_kv_heads, self.head_dim, self.act_torch)
+        T, hk, d, dt = k.shape[0], self.n_kv_heads, self.head_dim, self.act_torch
+        ks = _head_rows("k", k, hk, d, dt)
+        vs = _head_rows("v", v, hk, d, dt)
         if v.shape[0] != T:
             raise ValueError("k and v need the same number of tokens")
+        rp = pp = qp = qop = None
         hq = qs = qos = 0
-        if q is not None:
-            hq = q.shape[1]
-            qs = _head_rows("q", q, hq, self.head_dim, self.act_torch)
-            if q_out is None:
-                q_out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            qos = _head_rows("q_out", q_out, hq, self.head_dim, self.act_torch)
-            if q.shape[0] != T or q_out.shape[0] != T:
-                raise ValueError("q and k need the same number of tokens")
         if rotary is not None:
             if positions is None:
                 raise ValueError("a rotary needs positions")
-            _ids("positions", positions, T)
-        _check(coli_kv_append(self.c, k, ks, v, vs, _ids("slots", slots, T), T,
-                              rotary.c if rotary is not None else None, positions, q, qs, hq,
-                              q_out if q is not None else None, qos), "coli_kv_append")
+            rp, pp = rotary._ref, _ids("positions", positions, T)
+        if q is not None:
+            hq = q.shape[1]
+            qs = _head_rows("q", q, hq, d, dt)
+            if q_out is None:
+                q_out = q.new_empty((q.shape[0], hq, d))
+                qos = hq * d
+            else:
+                qos = _head_rows("q_out", q_out, hq, d, dt)
+            if q.shape[0] != T or q_out.shape[0] != T:
+                raise ValueError("q and k need the same number of tokens")
+            qp, qop = q.data_ptr(), q_out.data_ptr()
+        rc = lib().coli_kv_append(self._ref, k.data_ptr(), ks, v.data_ptr(), vs,
+                                  _ids("slots", slots, T), T, rp, pp, qp, qs, hq, qop, qos,
+                                  _current_stream(k))
+        if rc:
+            _check(rc, "coli_kv_append")
         return q_out if q is not None else None
 
     def read(self, slots, stream=None):
@@ -589,38 +633,46 @@ class PagedKVCache:
         if stream is not None:
             with _on(stream):
                 return self.read(slots)
-        N = slots.shape[0]
-        out = [self._torch.empty((N, self.n_kv_heads, self.head_dim), dtype=self.act_torch,
-                                 device=self.k.device) for _ in range(2)]
-        s = self.n_kv_heads * self.head_dim
-        _check(coli_kv_read(self.c, _ids("slots", slots, N), N, out[0], s, out[1], s),
-               "coli_kv_read")
-        return out[0], out[1]
+        N, h, d = slots.shape[0], self.n_kv_heads, self.head_dim
+        k = slots.new_empty((N, h, d), dtype=self.act_torch)
+        v = slots.new_empty((N, h, d), dtype=self.act_torch)
+        rc = lib().coli_kv_read(self._ref, _ids("slots", slots, N), N, k.data_ptr(), h * d,
+                                v.data_ptr(), h * d, _current_stream(k))
+        if rc:
+            _check(rc, "coli_kv_read")
+        return k, v
 
     def attend(self, q, block_table, seq_lens, scale=None, window=0, out=None, return_lse=False,
                stream=None):
         """Attention of one new token a sequence: q [B][n_q_heads][head_dim],
         block_table [B][max_pages] int32, seq_lens [B] int32 -> out like q
         (and lse [B][n_q_heads] f32). scale defaults to head_dim^-0.5."""
-        torch = self._torch
         if stream is not None:
             with _on(stream):
                 return self.attend(q, block_table, seq_lens, scale, window, out, return_lse)
+        torch, d, dt = _torch, self.head_dim, self.act_torch
         B, hq = q.shape[0], q.shape[1]
-        qs = _head_rows("q", q, hq, self.head_dim, self.act_torch)
+        qs = _head_rows("q", q, hq, d, dt)
         if out is None:
-            out = torch.empty((B, hq, self.head_dim), dtype=q.dtype, device=q.device)
-        os_ = _head_rows("out", out, hq, self.head_dim, self.act_torch)
-        if out.shape[0] != B:
-            raise ValueError("q and out need the same number of sequences")
+            out = q.new_empty((B, hq, d))
+            os_ = hq * d
+        else:
+            os_ = _head_rows("out", out, hq, d, dt)
+            if out.shape[0] != B:
+                raise ValueError("q and out need the same number of sequences")
         if block_table.dim() != 2 or block_table.shape[0] != B or not block_table.is_cuda or \
-                block_table.dtype != torch.int32 or not block_table.is_contiguous():
+                block_table.dtype is not torch.int32 or not block_table.is_contiguous():
             raise ValueError(f"block_table: need a contiguous int32 CUDA tensor [{B}][max_pages]")
-        lse = torch.empty((B, hq), dtype=torch.float32, device=q.device) if return_lse else None
-        n = coli_paged_attention_scratch_bytes(self.c, B, hq) if B else 0
-        scratch = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-        cfg = coli_attn_config(hq, window, self.head_dim ** -0.5 if scale is None else scale)
-        _check(coli_paged_attention(self.c, cfg, q, qs, B, block_table, block_table.shape[1],
-                                    _ids("seq_lens", seq_lens, B), out, os_, lse, scratch, n),
-               "coli_paged_attention")
+        lse = q.new_empty((B, hq), dtype=torch.float32) if return_lse else None
+        L = lib()
+        n = L.coli_paged_attention_scratch_bytes(self._ref, B, hq) if B else 0
+        scratch = q.new_empty((n,), dtype=torch.uint8)
+        cfg = coli_attn_config(hq, window, d ** -0.5 if scale is None else scale)
+        rc = L.coli_paged_attention(self._ref, ctypes.byref(cfg), q.data_ptr(), qs, B,
+                                    block_table.data_ptr(), block_table.shape[1],
+                                    _ids("seq_lens", seq_lens, B), out.data_ptr(), os_,
+                                    None if lse is None else lse.data_ptr(), scratch.data_ptr(),
+                                    n, _current_stream(q))
+        if rc:
+            _check(rc, "coli_paged_attention")
         return (out, lse) if return_lse else out

@@ -133,18 +133,22 @@ struct Form {
   size_t part;  // floats of a partial slot
 };
 
+template <int FMT, int DP, int NT>
+void fill(Form* f) {
+  using C = Cfg<FMT, DP, NT>;
+  f->per_sm = C::kPerSm;
+  f->warps = C::kWarps;
+  f->part = C::kPart;
+}
+
 template <int FMT>
-int per_sm_of(int dp, int nt, int* warps) {
-  if (dp == 64) {
-    *warps = Cfg<FMT, 64, 1>::kWarps;
-    return nt == 2 ? Cfg<FMT, 64, 2>::kPerSm : Cfg<FMT, 64, 1>::kPerSm;
+void fill_format(Form* f) {
+  if constexpr (FMT != DT_F32) {
+    if (f->nt == 2) return f->dp == 64 ? fill<FMT, 64, 2>(f) : fill<FMT, 128, 2>(f);
   }
-  if (dp == 128) {
-    *warps = Cfg<FMT, 128, 1>::kWarps;
-    return nt == 2 ? Cfg<FMT, 128, 2>::kPerSm : Cfg<FMT, 128, 1>::kPerSm;
-  }
-  *warps = Cfg<FMT, 256, 1>::kWarps;
-  return Cfg<FMT, 256, 1>::kPerSm;
+  if (f->dp == 64) return fill<FMT, 64, 1>(f);
+  if (f->dp == 128) return fill<FMT, 128, 1>(f);
+  fill<FMT, 256, 1>(f);
 }
 
 Form form_of(const KvView& c, int n_q_heads) {
@@ -153,11 +157,12 @@ Form form_of(const KvView& c, int n_q_heads) {
   f.dp = c.head_dim <= 64 ? 64 : (c.head_dim <= 128 ? 128 : 256);
   f.nt = group <= 8 || f.dp == 256 || c.dtype == DT_F32 ? 1 : 2;
   f.blocks = (group + 8 * f.nt - 1) / (8 * f.nt);
-  f.per_sm = c.dtype == DT_F32     ? per_sm_of<DT_F32>(f.dp, f.nt, &f.warps)
-             : c.dtype == DT_BF16  ? per_sm_of<DT_BF16>(f.dp, f.nt, &f.warps)
-             : c.dtype == DT_MXFP8 ? per_sm_of<DT_MXFP8>(f.dp, f.nt, &f.warps)
-                                   : per_sm_of<DT_MXFP4>(f.dp, f.nt, &f.warps);
-  f.part = static_cast<size_t>(f.dp / 16 * 4 * f.nt) * 32 + 16 * f.nt;
+  switch (c.dtype) {
+    case DT_F32: fill_format<DT_F32>(&f); break;
+    case DT_BF16: fill_format<DT_BF16>(&f); break;
+    case DT_MXFP8: fill_format<DT_MXFP8>(&f); break;
+    default: fill_format<DT_MXFP4>(&f);
+  }
   return f;
 }
 

@@ -47,11 +47,13 @@ struct Cfg {
   static constexpr int kBits = FMT == DT_F32 ? 32 : FMT == DT_BF16 ? 16 : FMT == DT_MXFP8 ? 8 : 4;
   static constexpr int kRow = DP * kBits / 8;          // bytes of a row in shared memory
   static constexpr int kScaleRow = kMx ? (DP > 128 ? 8 : 4) : 0;
-  static constexpr int kSlot = kTile * (kRow + kScaleRow);
+  // whole 128-byte lines: addresses within a line are XORed
+  static constexpr int kSlot = (kTile * (kRow + kScaleRow) + 127) / 128 * 128;
   static constexpr int kRegs = DP / 16 * 4 * NT;       // O^T registers of a lane
-  static constexpr int kWarps = kSlot > 8192 + 256 ? 4 : 8;
-  static constexpr int kPerSm = DP * NT <= 128 && kSlot <= 4096 + 256 ? 2 : 1;
-  static constexpr int kBudget = (kPerSm == 2 ? 112 : 224) * 1024;
+  static constexpr int kWarps = kSlot > 8192 + 256 || NT * DP == 256 && NT == 2 ? 4 : 8;
+  static constexpr int kPerSm =
+      DP * NT <= 128 && kSlot <= 4096 + 256 ? 2 : (NT == 2 && DP * NT == 256 ? 3 : 1);
+  static constexpr int kBudget = (kPerSm == 3 ? 74 : (kPerSm == 2 ? 112 : 224)) * 1024;
   static constexpr int kFit = kBudget / (kWarps * kSlot);
   // odd, so key and value slots alternate through the ring with one lead
   static constexpr int kRing = kFit >= 7 ? 7 : (kFit >= 5 ? 5 : 3);
@@ -134,41 +136,58 @@ COLI_DEV uint32_t lds8(uint32_t addr) {
 // (lane 4g + t holds 8 elements from 8t on of every 32), rows 2t when values
 // are (8 elements from 8g on of every 64).
 template <int FMT, int ROW, bool KEYS>
-COLI_DEV uint32_t piece(int r, int c) {
-  uint32_t f;
-  if constexpr (KEYS) {
-    if constexpr (FMT == DT_F32) f = r & 1;
-    else if constexpr (FMT == DT_BF16) f = (r & 1) << 2;
-    else if constexpr (FMT == DT_MXFP8) f = ROW >= 128 ? (r & 3) << 1 : ((r >> 1) & 1) << 1;
-    else f = ROW >= 128 ? r & 7 : (ROW >= 64 ? (r >> 1) & 3 : (r >> 2) & 1);
-  } else {
-    if constexpr (FMT == DT_F32) f = ((r >> 1) & 1) | (((r >> 2) & 1) << 2);
-    else f = ROW >= 64 ? r & 6 : ((r >> 2) & 1) << 1;
+COLI_DEV constexpr uint32_t row_xor(int r) {
+  if (KEYS) {
+    if (FMT == DT_F32) return r & 1;
+    if (FMT == DT_BF16) return (r & 1) << 2;
+    if (FMT == DT_MXFP8) return ROW >= 128 ? (r & 3) << 1 : ((r >> 1) & 1) << 1;
+    return ROW >= 128 ? r & 7 : (ROW >= 64 ? (r >> 1) & 3 : (r >> 2) & 1);
   }
-  return ((r * (ROW / 16) + c) ^ f) * 16;
+  if (FMT == DT_F32) return ((r >> 1) & 1) | (((r >> 2) & 1) << 2);
+  return ROW >= 64 ? r & 6 : ((r >> 2) & 1) << 1;
 }
+template <int FMT, int ROW, bool KEYS>
+COLI_DEV uint32_t piece(int r, int c) {
+  return ((r * (ROW / 16) + c) ^ row_xor<FMT, ROW, KEYS>(r)) * 16;
+}
+// Address `off` bytes further on in a tile, for offsets whose bits the lane's
+// own place leaves clear: within a 128-byte line they are XORed too.
+COLI_DEV uint32_t further(uint32_t at, uint32_t off) { return (at ^ (off & 127u)) + (off & ~127u); }
 
-// Starts the copy of one tile's keys or values (and scales) into a slot.
-// Rows outside [r0, r1) and bytes past row_bytes become zeros.
+// Starts the copy of one tile's keys or values into a slot (a multiple of 128).
+// Lane l takes the pieces l, l + 32, ... of the tile's memory: `place` is its
+// first piece's place, src its address. Rows outside [r0, r1) and bytes past
+// row_bytes become zeros.
 template <class C, int FMT, bool KEYS>
-COLI_DEV void copy_tile(uint32_t slot, const char* src, const uint8_t* scale, int row_bytes,
-                        int r0, int r1, int lane) {
+COLI_DEV void copy_tile(uint32_t slot, uint32_t place, const char* src, int row_bytes, int r0,
+                        int r1, int lane) {
   constexpr int kPieces = C::kRow / 16;
   constexpr int kIters = kTile * kPieces / 32;
+  const uint32_t dst = slot + place;
+  if (r0 <= 0 && r1 >= kTile && row_bytes == C::kRow) {
 #pragma unroll
-  for (int i = 0; i < kIters; ++i) {
-    const int p = i * 32 + lane, r = p / kPieces, c = p % kPieces;
-    const bool in = r >= r0 && r < r1 && c * 16 < row_bytes;
-    cp_async16_n(slot + piece<FMT, C::kRow, KEYS>(r, c), src + (in ? r * row_bytes + c * 16 : 0),
-                 in ? 16 : 0);
-  }
-  if constexpr (C::kMx) {
-    constexpr int kWords = C::kScaleRow / 4;
-    if (lane < kTile * kWords) {
-      const int r = lane / kWords;
-      const bool in = r >= r0 && r < r1;
-      cp_async4_n(slot + kTile * C::kRow + lane * 4, scale + (in ? lane * 4 : 0), in ? 4 : 0);
+    for (int i = 0; i < kIters; ++i)
+      cp_async16_n((dst ^ (row_xor<FMT, C::kRow, KEYS>(i * 32 / kPieces) * 16)) + i * 512,
+                   src + i * 512, 16);
+  } else {
+    const char* tile = src - lane * 16;
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
+      const int p = i * 32 + lane, r = p / kPieces, c = p % kPieces;
+      const bool in = r >= r0 && r < r1 && c * 16 < row_bytes;
+      cp_async16_n((dst ^ (row_xor<FMT, C::kRow, KEYS>(i * 32 / kPieces) * 16)) + i * 512,
+                   in ? tile + r * row_bytes + c * 16 : src, in ? 16 : 0);
     }
+  }
+}
+
+// And of its scales, one word a lane.
+template <class C>
+COLI_DEV void copy_scales(uint32_t slot, const uint8_t* src, int r0, int r1, int lane) {
+  constexpr int kWords = C::kScaleRow / 4;
+  if (lane < kTile * kWords) {
+    const int r = lane / kWords;
+    cp_async4_n(slot + kTile * C::kRow + lane * 4, src + lane * 4, r >= r0 && r < r1 ? 4 : 0);
   }
 }
 
@@ -296,6 +315,27 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   float* s_l = s_m + W * 8 * NT;
   const float sl = a.scale * 1.4426950408889634f;
   const int tiles_per_page = a.c.page_size / kTile;
+  // bytes of a page, of a head in it and of a tile (all below 2^31)
+  const uint32_t head_bytes = a.c.page_size * a.c.row_bytes;
+  const uint32_t page_bytes = head_bytes * a.c.n_heads, tile_bytes = kTile * a.c.row_bytes;
+  const uint32_t head_scales = a.c.page_size * C::kScaleRow;
+  const uint32_t page_scales = head_scales * a.c.n_heads;
+  // this lane's places in a tile: where its copies go, where its reads start
+  constexpr int kPieces = C::kRow / 16;
+  const uint32_t put_k = piece<FMT, C::kRow, true>(lane / kPieces, lane % kPieces);
+  const uint32_t put_v = piece<FMT, C::kRow, false>(lane / kPieces, lane % kPieces);
+  const uint32_t get_k =
+      FMT == DT_BF16    ? piece<FMT, C::kRow, true>(g, t)
+      : FMT == DT_F32   ? piece<FMT, C::kRow, true>(g, t * 2)
+      : FMT == DT_MXFP8 ? piece<FMT, C::kRow, true>(g, t >> 1) + (t & 1) * 8
+                        : piece<FMT, C::kRow, true>(g, 0) + t * 4;
+  const uint32_t get_v =
+      FMT == DT_BF16    ? piece<FMT, C::kRow, false>(2 * t, g)
+      : FMT == DT_F32   ? piece<FMT, C::kRow, false>(2 * t, g * 2)
+      : FMT == DT_MXFP8 ? piece<FMT, C::kRow, false>(2 * t, g >> 1) + (g & 1) * 8
+                        : piece<FMT, C::kRow, false>(2 * t, g >> 2) + (g & 3) * 4;
+  // MX: of two rows' scale words, the bytes of this lane's blocks 2v + g/4
+  const uint32_t pick = (g >> 2) * 0x1111u + 0x6420u;
   uint32_t live[2];  // the scale bytes of the head's blocks
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -368,7 +408,10 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     }
 
     float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
-    int ref[kMx ? kV : 1];  // MX: acc holds O^T / 2^(ref - 127) of the lane's value block
+    // MX: acc holds O^T / 2^(ref - 127) of the lane's value block 2v + g/4; bias
+    // is 0x1000 - ref in both halves. Blocks past the head read scale 0 = ref.
+    int ref[kMx ? kV : 1];
+    uint32_t bias[kMx ? kV : 1], mine[kMx ? kV : 1], hot = 0;
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i)
 #pragma unroll
@@ -379,21 +422,26 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -FLT_MAX, l[nt][0] = l[nt][1] = 0.f;
     if constexpr (kMx) {
 #pragma unroll
-      for (int v = 0; v < kV; ++v) ref[v] = -1000;
+      for (int v = 0; v < kV; ++v) {
+        const bool in = (v * 2 + (g >> 2)) * kMxBlock < D;
+        ref[v] = in ? -1000 : 0;
+        bias[v] = (0x1000 - ref[v]) * 0x10001;
+        mine[v] = in ? 0x00ff00ffu : 0u;
+      }
     }
 
     // ---- this warp's tiles ---------------------------------------------------------------
     const int n_it = (t1 - t0 - w + W - 1) / W;  // <= 0: none
     const int start = a.window > 0 && sq.len > a.window ? sq.len - a.window : 0;
-    int page_of = 0;  // lane i: the page of the warp's tile (batch of 32) + i
+    int page_of = 0, off_of = 0;  // lane i: page, and tile in it, of the warp's tile batch + i
     int batch = -32;
-    // tile `it` of this warp: its row in the pool and its rows in sight
     auto pages = [&](int it) {  // loads the pages of tiles it .. it + 31
       batch = it;
       const int k = it + lane;
       page_of = -1;
       if (k < n_it) {
-        const int pi = (sq.first + t0 + w + k * W) / tiles_per_page;
+        const int tile = sq.first + t0 + w + k * W, pi = tile / tiles_per_page;
+        off_of = tile - pi * tiles_per_page;
         page_of = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
         if (page_of < 0 || page_of >= a.c.n_pages) {
           latch_error(a.status, kErrDevice);
@@ -406,33 +454,39 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       s += C::kSlot;
       return s == ring + C::kRing * C::kSlot ? ring : s;
     };
-    size_t lead_row = 0;
+    // the tile being fetched: offsets of its keys (and values) and scales, rows in sight
+    uint64_t lead = 0, lead_sc = 0;
     int lead_r0 = 0, lead_r1 = 0;
     uint32_t hidden = 0;  // bit it % 32: tile `it` lies in a page that is left out
     auto issue_k = [&](int it) {
       __syncwarp();
       if (it < n_it) {
         if (it >= batch + 32) pages(it);
-        const int tile = sq.first + t0 + w + it * W;
         const int page = __shfl_sync(0xffffffffu, page_of, it - batch);
-        const int off = tile - tile / tiles_per_page * tiles_per_page;
-        lead_row = kv_row(a.c, page < 0 ? 0 : page, h, off * kTile);
-        lead_r0 = start - tile * kTile;
-        lead_r1 = page < 0 ? 0 : sq.len - tile * kTile;
+        const uint32_t off = __shfl_sync(0xffffffffu, off_of, it - batch);
+        const uint32_t pg = page < 0 ? 0 : page;
+        lead = static_cast<uint64_t>(pg) * page_bytes + (h * head_bytes + off * tile_bytes + lane * 16);
+        const int key = (sq.first + t0 + w + it * W) * kTile;
+        lead_r0 = start - key;
+        lead_r1 = page < 0 ? 0 : sq.len - key;
         hidden = (hidden & ~(1u << (it & 31))) | (page < 0 ? 1u : 0u) << (it & 31);
-        copy_tile<C, FMT, true>(fill, a.c.k + lead_row * a.c.row_bytes,
-                                a.c.k_scale + lead_row * C::kScaleRow, a.c.row_bytes, lead_r0,
-                                lead_r1, lane);
+        copy_tile<C, FMT, true>(fill, put_k, a.c.k + lead, a.c.row_bytes, lead_r0, lead_r1, lane);
+        if constexpr (kMx) {
+          lead_sc = static_cast<uint64_t>(pg) * page_scales +
+                    (h * head_scales + off * (kTile * C::kScaleRow));
+          copy_scales<C>(fill, a.c.k_scale + lead_sc, lead_r0, lead_r1, lane);
+        }
       }
       cp_async_commit();
       fill = next(fill);
     };
     auto issue_v = [&](int it) {
       __syncwarp();
-      if (it < n_it)
-        copy_tile<C, FMT, false>(fill, a.c.v + lead_row * a.c.row_bytes,
-                                 a.c.v_scale + lead_row * C::kScaleRow, a.c.row_bytes, lead_r0,
-                                 lead_r1, lane);
+      if (it < n_it) {
+        copy_tile<C, FMT, false>(fill, put_v, a.c.v + lead, a.c.row_bytes, lead_r0, lead_r1, lane);
+        if constexpr (kMx)
+          copy_scales<C>(fill, a.c.v_scale + lead_sc, lead_r0, lead_r1, lane);
+      }
       cp_async_commit();
       fill = next(fill);
     };
@@ -444,7 +498,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         float ka[8], kb[8];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t at = at0 + piece<FMT, C::kRow, true>(g, j * 8 + t * 2 + hf);
+          const uint32_t at = further(at0 + get_k, j * 128 + hf * 16);
           const uint4 va = lds128(at), vb = lds128(at + 8 * C::kRow);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -492,10 +546,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       float x[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
-      uint32_t sc0[2], sc1[2];
-      bool odd = false;
+      float f0[kMx ? kJ : 1], f1[kMx ? kJ : 1];  // the blocks' scales of keys g and g + 8
       if constexpr (kMx) {
         const uint32_t at = slot + kTile * C::kRow + g * C::kScaleRow;
+        uint32_t sc0[2], sc1[2];
+        bool odd = false;
 #pragma unroll
         for (int i = 0; i < C::kScaleRow / 4; ++i) {
           // bytes past the head's blocks may hold anything: 1
@@ -503,59 +558,70 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           sc1[i] = (lds32(at + 8 * C::kScaleRow + 4 * i) & live[i]) | (0x7f7f7f7fu & ~live[i]);
           odd = odd || odd_scales(sc0[i]) || odd_scales(sc1[i]);
         }
+        if (!__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            constexpr uint32_t kExp = 0x7f800000u;
+            const int up = 23 - 8 * (j % 4);
+            f0[j] = __uint_as_float((up > 0 ? sc0[j / 4] << (up & 31) : sc0[j / 4] >> 1) & kExp);
+            f1[j] = __uint_as_float((up > 0 ? sc1[j / 4] << (up & 31) : sc1[j / 4] >> 1) & kExp);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            f0[j] = e8m0_f32((sc0[j / 4] >> (8 * (j % 4))) & 255u);
+            f1[j] = e8m0_f32((sc1[j / 4] >> (8 * (j % 4))) & 255u);
+          }
+        }
       }
 #pragma unroll
       for (int j = 0; j < kJ; ++j) {
         if constexpr (FMT == DT_BF16) {
-          const uint32_t at = slot + piece<FMT, C::kRow, true>(g, j * 4 + t);
+          const uint32_t at = further(slot + get_k, j * 64);
           const uint4 ka = lds128(at), kb = lds128(at + 8 * C::kRow);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_bf16_16816(x[nt], ka.x, kb.x, ka.y, kb.y, q[nt][j].x, q[nt][j].y);
             mma_bf16_16816(x[nt], ka.z, kb.z, ka.w, kb.w, q[nt][j].z, q[nt][j].w);
           }
-        } else if constexpr (kF32) {
-          score_f32(x, slot, j, false);
-        } else if (j * 32 < D) {
+        } else if (kMx && j * 32 < D) {
           uint32_t ka[4], kb[4];
           if constexpr (FMT == DT_MXFP8) {
-            const uint32_t at = slot + piece<FMT, C::kRow, true>(g, j * 2 + (t >> 1)) + (t & 1) * 8;
+            const uint32_t at = further(slot + get_k, j * 32);
             const uint2 va = lds64(at), vb = lds64(at + 8 * C::kRow);
             e4m3x8_f16(va.x, va.y, ka);
             e4m3x8_f16(vb.x, vb.y, kb);
           } else {
-            const uint32_t at = slot + piece<FMT, C::kRow, true>(g, j) + t * 4;
+            const uint32_t at = further(slot + get_k, j * 16);
             e2m1x8_f16(lds32(at), ka);
             e2m1x8_f16(lds32(at + 8 * C::kRow), kb);
           }
           // the block's scale goes on its partial score: codes are exact in fp16
-          const uint32_t s0 = (sc0[j / 4] >> (8 * (j % 4))) & 255u;
-          const uint32_t s1 = (sc1[j / 4] >> (8 * (j % 4))) & 255u;
-          float f0 = __uint_as_float(s0 << 23), f1 = __uint_as_float(s1 << 23);
-          if (odd) f0 = e8m0_f32(s0), f1 = e8m0_f32(s1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float d[4] = {0.f, 0.f, 0.f, 0.f};
             mma_f16_16816(d, ka[0], kb[0], ka[1], kb[1], q[nt][j].x, q[nt][j].y);
             mma_f16_16816(d, ka[2], kb[2], ka[3], kb[3], q[nt][j].z, q[nt][j].w);
-            x[nt][0] = fmaf(d[0], f0, x[nt][0]);
-            x[nt][1] = fmaf(d[1], f0, x[nt][1]);
-            x[nt][2] = fmaf(d[2], f1, x[nt][2]);
-            x[nt][3] = fmaf(d[3], f1, x[nt][3]);
+            x[nt][0] = fmaf(d[0], f0[j], x[nt][0]);
+            x[nt][1] = fmaf(d[1], f0[j], x[nt][1]);
+            x[nt][2] = fmaf(d[2], f1[j], x[nt][2]);
+            x[nt][3] = fmaf(d[3], f1[j], x[nt][3]);
           }
         }
       }
       if constexpr (kF32) {
-        bool nan = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) nan |= x[nt][c] != x[nt][c];
-        if (__any_sync(0xffffffffu, nan)) {
+#pragma unroll 1
+        for (int careful = 0; careful < 2; ++careful) {
+          bool nan = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
 #pragma unroll
-          for (int j = 0; j < kJ; ++j) score_f32(x, slot, j, true);
+          for (int j = 0; j < kJ; ++j) score_f32(x, slot, j, careful != 0);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) nan |= x[nt][c] != x[nt][c];
+          if (!__any_sync(0xffffffffu, nan)) break;
         }
       }
       const int tile_key = (sq.first + t0 + w + it * W) * kTile;
@@ -578,7 +644,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) up |= x[nt][c] > m[nt][c & 1] + kSlack;
+        for (int c = 0; c < 2; ++c) up |= fmaxf(x[nt][c], x[nt][c + 2]) > m[nt][c] + kSlack;
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -635,10 +701,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       if constexpr (FMT == DT_BF16) {
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-          const uint4 r_0 = lds128(slot + piece<FMT, C::kRow, false>(2 * t, v * 8 + g));
-          const uint4 r_1 = lds128(slot + piece<FMT, C::kRow, false>(2 * t + 1, v * 8 + g));
-          const uint4 r_2 = lds128(slot + piece<FMT, C::kRow, false>(2 * t + 8, v * 8 + g));
-          const uint4 r_3 = lds128(slot + piece<FMT, C::kRow, false>(2 * t + 9, v * 8 + g));
+          const uint32_t at = slot + get_v;
+          const uint4 r_0 = lds128(further(at, v * 128));
+          const uint4 r_1 = lds128(further(at, v * 128 + C::kRow));
+          const uint4 r_2 = lds128(further(at, v * 128 + C::kRow * 8));
+          const uint4 r_3 = lds128(further(at, v * 128 + C::kRow * 9));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t w0 = word_of(r_0, i), w1 = word_of(r_1, i), w2 = word_of(r_2, i),
@@ -660,8 +727,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             uint4 r[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              r[k] = lds128(slot + piece<FMT, C::kRow, false>(2 * t + (k & 1) + (k >> 1) * 8,
-                                                              v * 16 + g * 2 + hf));
+              r[k] = lds128(further(slot + get_v, v * 256 + hf * 16 +
+                                                      ((k & 1) + (k >> 1) * 8) * C::kRow));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -688,34 +755,58 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       } else {
         // Value codes are exact in fp16, and so is a code times 2^(s - ref) for
         // scales s in [ref - 14, ref + 7]: ref follows the largest scale of the
-        // lane's block (the four lanes of a g share it), and a tile with a scale
-        // below that range, or a NaN one, takes bf16 operands instead.
-        int s[kV][4];
-        // So does one with a weight too small for fp16.
-        bool rise = false, wide = false;
+        // lane's block (the four lanes of a g share it). sd holds s - ref + 0x1000
+        // for the keys of a pair in its halves. A tile with a scale out of that
+        // range, a NaN one or a weight too small for fp16 takes the careful way.
+        uint32_t sd[kV][2];
+        uint32_t bad = 0;
+        const bool part = r0 > 0 || r1 < kTile;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t at = slot + kTile * C::kRow + (2 * t + 8 * k) * C::kScaleRow;
+#pragma unroll
+          for (int i = 0; i < C::kScaleRow / 4; ++i) {
+            uint32_t w0, w1;
+            if constexpr (C::kScaleRow == 4) {
+              const uint2 v = lds64(at);
+              w0 = v.x, w1 = v.y;
+            } else {
+              w0 = lds32(at + 4 * i), w1 = lds32(at + 8 + 4 * i);
+            }
+            const uint32_t by = __byte_perm(w0, w1, pick);
+            sd[2 * i][k] = (by & mine[2 * i]) + bias[2 * i];
+            if constexpr (kV > 1) sd[2 * i + 1][k] = (by >> 8 & mine[2 * i + 1]) + bias[2 * i + 1];
+          }
+          if (part) {  // rows out of sight hold zeros, whatever their scale
+            const int row = 2 * t + 8 * k;
+            const uint32_t lo = row < r0 || row >= r1 ? 0xffffu : 0u;
+            const uint32_t hi = row + 1 < r0 || row + 1 >= r1 ? 0xffff0000u : 0u;
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+              sd[v][k] = (sd[v][k] & ~(lo | hi)) | (0x10001000u & (lo | hi));
+          }
+#pragma unroll
+          for (int v = 0; v < kV; ++v) bad |= (sd[v][k] - 0x0ff20ff2u) | (0x10071007u - sd[v][k]);
+        }
+        bad = (bad & 0x80008000u) | hot;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) wide |= x[nt][c] > 0.f && x[nt][c] < 0x1p-16f;
-#pragma unroll
-        for (int v = 0; v < kV; ++v) {
-          const int blk = v * 2 + (g >> 2);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int row = 2 * t + (k & 1) + (k >> 1) * 8;
-            s[v][k] = lds8(slot + kTile * C::kRow + row * C::kScaleRow + blk);
-            // rows out of sight hold zeros, whatever their scale
-            if (row < r0 || row >= r1 || blk * 32 >= D) s[v][k] = ref[v];
-            rise |= s[v][k] > ref[v] + 7 && s[v][k] != 255;
-          }
-        }
-        if (__any_sync(0xffffffffu, rise)) {
+          for (int c = 0; c < 4; ++c)  // 0 < weight < 2^-16
+            bad |= __float_as_uint(x[nt][c]) - 1u < 0x377fffffu ? 1u : 0u;
+        bool wide = false;
+        float fw[kV][4];  // the careful way's factors
+        if (__any_sync(0xffffffffu, bad != 0)) {
+          int s[kV][4];
+          hot = 0;
 #pragma unroll
           for (int v = 0; v < kV; ++v) {
             int top = -1000;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k) {
+              s[v][k] = static_cast<int>(sd[v][k >> 1] >> (16 * (k & 1)) & 0xffffu) - 0x1000 + ref[v];
               if (s[v][k] != 255) top = max(top, s[v][k]);
+            }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             if (top > ref[v] + 7) {
@@ -726,69 +817,72 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                   for (int c = 0; c < 4; ++c) acc[v * 4 + i][nt][c] *= f;
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (s[v][k] == ref[v]) {
-                  const int row = 2 * t + (k & 1) + (k >> 1) * 8;
-                  if (row < r0 || row >= r1 || (v * 2 + (g >> 2)) * 32 >= D) s[v][k] = top;
-                }
               ref[v] = top;
+              bias[v] = (0x1000 - top) * 0x10001;
             }
+            if (ref[v] > 247) hot = 1;  // a NaN scale would pass for 2^128
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = 2 * t + (k & 1) + (k >> 1) * 8;
+              if (row < r0 || row >= r1) s[v][k] = ref[v];
+              const int e = s[v][k] - ref[v];
+              wide |= e < -14 || e > 7 || s[v][k] == 255;
+              fw[v][k] = s[v][k] == 255 ? __uint_as_float(0x7fc00000u)
+                                        : __uint_as_float(static_cast<uint32_t>(e < -127 ? 0 : e + 127) << 23);
+            }
+            sd[v][0] = (s[v][0] - ref[v] + 0x1000) | (s[v][1] - ref[v] + 0x1000) << 16;
+            sd[v][1] = (s[v][2] - ref[v] + 0x1000) | (s[v][3] - ref[v] + 0x1000) << 16;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) wide |= __float_as_uint(x[nt][c]) - 1u < 0x377fffffu;
+          wide = __any_sync(0xffffffffu, wide);
+        }
+        if (!wide) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            pb[nt][0] = transpose8(pack_f16x2(x[nt][0], x[nt][1]));
+            pb[nt][1] = transpose8(pack_f16x2(x[nt][2], x[nt][3]));
+          }
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            pb[nt][0] = transpose8(pack_bf16x2(x[nt][0], x[nt][1]));
+            pb[nt][1] = transpose8(pack_bf16x2(x[nt][2], x[nt][3]));
           }
         }
 #pragma unroll
-        for (int v = 0; v < kV; ++v)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            wide |= static_cast<unsigned>(s[v][k] - ref[v] + 14) > 21u;
-        wide = __any_sync(0xffffffffu, wide);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          pb[nt][0] = transpose8(wide ? pack_bf16x2(x[nt][0], x[nt][1])
-                                      : pack_f16x2(x[nt][0], x[nt][1]));
-          pb[nt][1] = transpose8(wide ? pack_bf16x2(x[nt][2], x[nt][3])
-                                      : pack_f16x2(x[nt][2], x[nt][3]));
-        }
-#pragma unroll
         for (int v = 0; v < kV; ++v) {
-          // words of codes with the keys of a pair interleaved: cw[k][i], pair
-          // k = 0: keys 2t, 2t + 1, 1: + 8; element pair i -> two fp16 operands
-          uint32_t op[2][8];  // [key pair][element]
+          uint32_t op[2][8];  // [keys 2t, 2t + 1 or + 8][element]: the two keys' codes in fp16
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int row = 2 * t + 8 * k;
+            const uint32_t off = v * (C::kBits * 8) + k * 8 * C::kRow;
+            uint32_t h4[4];
             if constexpr (FMT == DT_MXFP8) {
-              const uint2 e0 = lds64(slot + piece<FMT, C::kRow, false>(row, v * 4 + (g >> 1)) +
-                                     (g & 1) * 8);
-              const uint2 e1 = lds64(slot + piece<FMT, C::kRow, false>(row + 1, v * 4 + (g >> 1)) +
-                                     (g & 1) * 8);
-              uint32_t h[4];
-              e4m3x8_f16(__byte_perm(e0.x, e1.x, 0x5140), __byte_perm(e0.x, e1.x, 0x7362), h);
+              const uint2 e0 = lds64(further(slot + get_v, off));
+              const uint2 e1 = lds64(further(slot + get_v, off + C::kRow));
+              e4m3x8_f16(__byte_perm(e0.x, e1.x, 0x5140), __byte_perm(e0.x, e1.x, 0x7362), h4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) op[k][i] = h[i];
-              e4m3x8_f16(__byte_perm(e0.y, e1.y, 0x5140), __byte_perm(e0.y, e1.y, 0x7362), h);
+              for (int i = 0; i < 4; ++i) op[k][i] = h4[i];
+              e4m3x8_f16(__byte_perm(e0.y, e1.y, 0x5140), __byte_perm(e0.y, e1.y, 0x7362), h4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) op[k][4 + i] = h[i];
+              for (int i = 0; i < 4; ++i) op[k][4 + i] = h4[i];
             } else {
-              const uint32_t e0 = lds32(slot + piece<FMT, C::kRow, false>(row, v * 2 + (g >> 2)) +
-                                        (g & 3) * 4);
-              const uint32_t e1 =
-                  lds32(slot + piece<FMT, C::kRow, false>(row + 1, v * 2 + (g >> 2)) + (g & 3) * 4);
-              uint32_t h[4];
-              e2m1x8_f16((e0 & 0x0f0f0f0fu) | ((e1 & 0x0f0f0f0fu) << 4), h);
+              const uint32_t e0 = lds32(further(slot + get_v, off));
+              const uint32_t e1 = lds32(further(slot + get_v, off + C::kRow));
+              e2m1x8_f16((e0 & 0x0f0f0f0fu) | ((e1 & 0x0f0f0f0fu) << 4), h4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) op[k][2 * i] = h[i];
-              e2m1x8_f16(((e0 >> 4) & 0x0f0f0f0fu) | (e1 & 0xf0f0f0f0u), h);
+              for (int i = 0; i < 4; ++i) op[k][2 * i] = h4[i];
+              e2m1x8_f16(((e0 >> 4) & 0x0f0f0f0fu) | (e1 & 0xf0f0f0f0u), h4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) op[k][2 * i + 1] = h[i];
+              for (int i = 0; i < 4; ++i) op[k][2 * i + 1] = h4[i];
             }
           }
           if (!wide) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t f =
-                  static_cast<uint32_t>(s[v][2 * k] - ref[v] + 15) << 10 |
-                  static_cast<uint32_t>(s[v][2 * k + 1] - ref[v] + 15) << 26;
+              const uint32_t f = (sd[v][k] - 0x0ff10ff1u) << 10;  // 2^(s - ref), both keys
 #pragma unroll
               for (int i = 0; i < 8; ++i) op[k][i] = mul_f16x2(op[k][i], f);
             }
@@ -800,14 +894,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
                               op[1][2 * i + 1], pb[nt][0], pb[nt][1]);
           } else {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float f[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int sv = s[v][2 * k + e], x2 = sv - ref[v] + 127;
-                f[e] = sv == 255 ? __uint_as_float(0x7fc00000u)
-                                 : __uint_as_float(static_cast<uint32_t>(x2 < 0 ? 0 : x2) << 23);
-              }
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 float lo, hi;
@@ -815,9 +902,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
                     "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
                     : "=f"(lo), "=f"(hi)
                     : "r"(op[k][i]));
-                op[k][i] = pack_bf16x2(lo * f[0], hi * f[1]);
+                op[k][i] = pack_bf16x2(lo * fw[v][2 * k], hi * fw[v][2 * k + 1]);
               }
-            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
