@@ -520,7 +520,7 @@ def rope(rotary: Rotary, positions, q, k=None, q_out=None, k_out=None, inverse=F
     T, hq, d = q.shape
     qs = _head_rows("q", q, hq, d, dt)
     if q_out is None:
-        q_out = q.new_empty((T, hq, d))
+        q_out = torch.empty((T, hq, d), dtype=dt, device=q.device)
         qos = hq * d
     else:
         qos = _head_rows("q_out", q_out, hq, d, dt)
@@ -532,7 +532,7 @@ def rope(rotary: Rotary, positions, q, k=None, q_out=None, k_out=None, inverse=F
         hk = k.shape[1]
         ks = _head_rows("k", k, hk, d, dt)
         if k_out is None:
-            k_out = k.new_empty((k.shape[0], hk, d))
+            k_out = torch.empty((k.shape[0], hk, d), dtype=dt, device=q.device)
             kos = hk * d
         else:
             kos = _head_rows("k_out", k_out, hk, d, dt)
@@ -614,7 +614,7 @@ class PagedKVCache:
             hq = q.shape[1]
             qs = _head_rows("q", q, hq, d, dt)
             if q_out is None:
-                q_out = q.new_empty((q.shape[0], hq, d))
+                q_out = _torch.empty((q.shape[0], hq, d), dtype=dt, device=q.device)
                 qos = hq * d
             else:
                 qos = _head_rows("q_out", q_out, hq, d, dt)
@@ -634,8 +634,8 @@ class PagedKVCache:
             with _on(stream):
                 return self.read(slots)
         N, h, d = slots.shape[0], self.n_kv_heads, self.head_dim
-        k = slots.new_empty((N, h, d), dtype=self.act_torch)
-        v = slots.new_empty((N, h, d), dtype=self.act_torch)
+        k = _torch.empty((N, h, d), dtype=self.act_torch, device=slots.device)
+        v = _torch.empty((N, h, d), dtype=self.act_torch, device=slots.device)
         rc = lib().coli_kv_read(self._ref, _ids("slots", slots, N), N, k.data_ptr(), h * d,
                                 v.data_ptr(), h * d, _current_stream(k))
         if rc:
@@ -654,7 +654,7 @@ class PagedKVCache:
         B, hq = q.shape[0], q.shape[1]
         qs = _head_rows("q", q, hq, d, dt)
         if out is None:
-            out = q.new_empty((B, hq, d))
+            out = torch.empty((B, hq, d), dtype=dt, device=q.device)
             os_ = hq * d
         else:
             os_ = _head_rows("out", out, hq, d, dt)
@@ -663,10 +663,10 @@ class PagedKVCache:
         if block_table.dim() != 2 or block_table.shape[0] != B or not block_table.is_cuda or \
                 block_table.dtype is not torch.int32 or not block_table.is_contiguous():
             raise ValueError(f"block_table: need a contiguous int32 CUDA tensor [{B}][max_pages]")
-        lse = q.new_empty((B, hq), dtype=torch.float32) if return_lse else None
+        lse = torch.empty((B, hq), dtype=torch.float32, device=q.device) if return_lse else None
         L = lib()
         n = L.coli_paged_attention_scratch_bytes(self._ref, B, hq) if B else 0
-        scratch = q.new_empty((n,), dtype=torch.uint8)
+        scratch = torch.empty((n,), dtype=torch.uint8, device=q.device)
         cfg = coli_attn_config(hq, window, d ** -0.5 if scale is None else scale)
         rc = L.coli_paged_attention(self._ref, ctypes.byref(cfg), q.data_ptr(), qs, B,
                                     block_table.data_ptr(), block_table.shape[1],

@@ -9,7 +9,10 @@
 // One thread holds 16 bytes of one head row and reads the pair partners it
 // needs from the same row (the other half of the head, in L1); a row's threads
 // are in one block, which reads all its rows before it stores any, so q_out may
-// be q. The token's cosines and sines stay in registers over HPT heads.
+// be q. A thread takes HPT heads of its token, whose loads it has in flight
+// together, and keeps the token's cosines and sines in registers over them.
+// Blocks are q's, then k's, then v's, so what a block does with its rows is
+// known to all its threads.
 #include "attn.h"
 #include "common.cuh"
 #include "mx.cuh"
@@ -21,12 +24,14 @@ constexpr int kThreads = 256;
 constexpr int kRowsOnly = -1;  // no cache: both outputs are rows
 
 struct RotateArgs {
-  HeadRows q, k, v;
+  HeadRows rows[3];     // q, k, v
   RotaryView r;
   KvView c;
   const int32_t* slots;
-  int T, head_dim, heads;  // heads: q + k (+ v)
-  int groups;              // threads' heads: n * groups + g
+  int T, head_dim;
+  int groups[3];        // threads' heads of each kind: n * groups + g, n < HPT
+  unsigned first[3];    // first block of k, of v, and past v
+  int page_shift;       // log2(page_size), or -1
   int* status;
 };
 
@@ -61,115 +66,120 @@ COLI_DEV uint4 pack(const float (&x)[Chunk<A>::N]) {
   }
 }
 
-template <typename A, int FMT, bool INTER, int HPT>
-__global__ void __launch_bounds__(kThreads) k_rotate(const RotateArgs p) {
-  constexpr int N = Chunk<A>::N;
-  const int cpr = p.head_dim / N;        // chunks (threads) per row
-  const int rows = kThreads / cpr;       // rows a block holds at once
-  const int local = threadIdx.x / cpr, c = threadIdx.x % cpr;
-  const uint32_t slot_id = blockIdx.x * static_cast<uint32_t>(rows) + local;
-  const uint32_t t = slot_id / p.groups;
-  const int g = slot_id % p.groups;
-  const bool live = local < rows && t < static_cast<uint32_t>(p.T);
-  const int d0 = c * N, half = p.r.rot_dim / 2;
+// max(|a|, |b|), NaN if either is (the sign is not used).
+COLI_DEV float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
-  bool turn = live && p.r.table != nullptr && d0 < p.r.rot_dim, bad_pos = false;
-  int pos = 0;
-  if (live && p.r.table != nullptr) {
-    pos = p.r.positions[t];
-    bad_pos = static_cast<uint32_t>(pos) >= static_cast<uint32_t>(p.r.n_positions);
-    if (bad_pos) {
-      turn = false;
-      if (c == 0 && g == 0) latch_error(p.status, kErrDevice);
-    }
-  }
-  // the cosine and signed sine of each element's pair; (1, 0) past rot_dim
+// One block's rows of kind KIND (0 q, 1 k, 2 v).
+template <typename A, int FMT, bool INTER, int HPT, int KIND>
+COLI_DEV void rotate_rows(const RotateArgs& p, unsigned block) {
+  constexpr int N = Chunk<A>::N;
+  constexpr bool kStore = FMT != kRowsOnly && KIND > 0;  // rows go to the cache
+  constexpr bool kMx = kStore && (FMT == DT_MXFP8 || FMT == DT_MXFP4);
+  const int cpr = p.head_dim / N;   // chunks (threads) per row
+  const int rows = kThreads / cpr;  // rows a block holds at once
+  const int local = threadIdx.x / cpr, c = threadIdx.x - local * cpr;
+  const int groups = p.groups[KIND];
+  const uint32_t id = block * static_cast<uint32_t>(rows) + local;
+  const uint32_t t = id / groups;
+  const int g = id - t * groups;
+  const bool live = local < rows && t < static_cast<uint32_t>(p.T);
+  const HeadRows& hr = p.rows[KIND];
+  const int d0 = c * N, half = p.r.rot_dim / 2;
+  const int step = groups * p.head_dim;  // elements between a thread's heads
+
+  const A* src = static_cast<const A*>(hr.in) + (live ? t * hr.in_stride : 0) + g * p.head_dim + d0;
+  uint4 own[HPT];
+#pragma unroll
+  for (int n = 0; n < HPT; ++n)
+    if (live && n * groups + g < hr.n_heads)
+      own[n] = *reinterpret_cast<const uint4*>(src + static_cast<size_t>(n) * step);
+
+  // the cosine and signed sine of each element's pair
   float cs[N], sn[N];
+  uint4 other[HPT];
+  bool turn = false, bad_pos = false;
+  if (KIND < 2 && live && p.r.table != nullptr) {
+    const int pos = p.r.positions[t];
+    bad_pos = static_cast<uint32_t>(pos) >= static_cast<uint32_t>(p.r.n_positions);
+    if (bad_pos && c == 0 && g == 0) latch_error(p.status, kErrDevice);
+    turn = !bad_pos && d0 < p.r.rot_dim;
+    if (turn) {
+      const float2* row =
+          reinterpret_cast<const float2*>(p.r.table) + static_cast<size_t>(pos) * half;
+      if constexpr (INTER) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) cs[i] = 1.f, sn[i] = 0.f;
-  const bool aligned = half % N == 0;  // partner chunk and table rows are whole vectors
-  if (turn) {
-    const float2* row = reinterpret_cast<const float2*>(p.r.table) + static_cast<size_t>(pos) * half;
-    if constexpr (INTER) {
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        if (d0 + 2 * i < p.r.rot_dim) {
-          const float2 v = __ldg(row + d0 / 2 + i);
+        for (int i = 0; i < N / 2; ++i) {
+          const float2 v = d0 + 2 * i < p.r.rot_dim ? __ldg(row + d0 / 2 + i) : make_float2(1, 0);
           cs[2 * i] = cs[2 * i + 1] = v.x;
           sn[2 * i + 1] = v.y * p.r.sine_sign;
           sn[2 * i] = -sn[2 * i + 1];
         }
-      }
-    } else if (aligned) {
-      const int i0 = d0 < half ? d0 : d0 - half;
-      const float sgn = d0 < half ? -p.r.sine_sign : p.r.sine_sign;
+      } else if (half % N == 0) {  // partner chunk and table entries are whole vectors
+        const bool low = d0 < half;
+        const float sgn = low ? -p.r.sine_sign : p.r.sine_sign;
+        const float2* at = row + (low ? d0 : d0 - half);
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(row + i0 + i));
-        cs[i] = v.x, sn[i] = v.y * sgn, cs[i + 1] = v.z, sn[i + 1] = v.w * sgn;
-      }
-    } else {
+        for (int i = 0; i < N; i += 2) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(at + i));
+          cs[i] = v.x, sn[i] = v.y * sgn, cs[i + 1] = v.z, sn[i + 1] = v.w * sgn;
+        }
+        const A* po = src + (low ? half : -half);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int d = d0 + i;
-        if (d < p.r.rot_dim) {
-          const float2 v = __ldg(row + (d < half ? d : d - half));
+        for (int n = 0; n < HPT; ++n)
+          if (n * groups + g < hr.n_heads)
+            other[n] = *reinterpret_cast<const uint4*>(po + static_cast<size_t>(n) * step);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int d = d0 + i;
+          const float2 v = d < p.r.rot_dim ? __ldg(row + (d < half ? d : d - half))
+                                           : make_float2(1, 0);
           cs[i] = v.x;
           sn[i] = v.y * (d < half ? -p.r.sine_sign : p.r.sine_sign);
         }
-      }
-    }
-  }
-  // where the keys and values go
-  int page = 0, off = 0;
-  bool store = false;
-  if constexpr (FMT != kRowsOnly) {
-    if (live) {
-      const int slot = p.slots[t];
-      const bool bad = slot < -1 || slot >= p.c.n_pages * p.c.page_size;
-      if (bad && c == 0 && g == 0) latch_error(p.status, kErrDevice);
-      store = slot >= 0 && !bad && !bad_pos;
-      page = store ? slot / p.c.page_size : 0;
-      off = store ? slot - page * p.c.page_size : 0;
-    }
-  }
-
-  uint4 own[HPT], other[HPT];
-  const int hq = p.q.n_heads, hk = hq + p.k.n_heads;
 #pragma unroll
-  for (int n = 0; n < HPT; ++n) {
-    const int h = n * p.groups + g;
-    if (!live || h >= p.heads) continue;
-    const HeadRows& src = h < hq ? p.q : (h < hk ? p.k : p.v);
-    const int hh = h < hq ? h : (h < hk ? h - hq : h - hk);
-    const A* row = static_cast<const A*>(src.in) + t * src.in_stride +
-                   static_cast<size_t>(hh) * p.head_dim;
-    own[n] = *reinterpret_cast<const uint4*>(row + d0);
-    if constexpr (!INTER) {
-      if (turn && h < hk) {
-        if (aligned) {
-          other[n] = *reinterpret_cast<const uint4*>(row + (d0 < half ? d0 + half : d0 - half));
-        } else {
+        for (int n = 0; n < HPT; ++n) {
+          if (n * groups + g >= hr.n_heads) continue;
           A e[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const int d = d0 + i;
-            e[i] = row[d >= p.r.rot_dim ? d : (d < half ? d + half : d - half)];
+            e[i] = src[static_cast<int64_t>(n) * step + i +
+                       (d >= p.r.rot_dim ? 0 : (d < half ? half : -half))];
           }
           other[n] = *reinterpret_cast<const uint4*>(e);
         }
       }
     }
   }
-  __syncthreads();  // q_out may be q: every row is read before any is stored
+  // where the row goes
+  A* dst = nullptr;
+  size_t row = 0;
+  bool put = live;
+  if constexpr (!kStore) {
+    dst = static_cast<A*>(hr.out) + (live ? t * hr.out_stride : 0) + g * p.head_dim + d0;
+  } else if (live) {
+    const int slot = p.slots[t];
+    const bool bad = slot < -1 || slot >= p.c.n_pages * p.c.page_size;
+    if (bad && c == 0 && g == 0) latch_error(p.status, kErrDevice);
+    if (KIND == 2 && p.r.table != nullptr)
+      bad_pos = static_cast<uint32_t>(p.r.positions[t]) >= static_cast<uint32_t>(p.r.n_positions);
+    put = slot >= 0 && !bad && !bad_pos;
+    const int page = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.c.page_size;
+    if (put) row = kv_row(p.c, page, g, slot - page * p.c.page_size);
+  }
+  if constexpr (!kStore) __syncthreads();  // q_out may be q: all rows are read before any is stored
 #pragma unroll
   for (int n = 0; n < HPT; ++n) {
-    const int h = n * p.groups + g;
-    const bool here = live && h < p.heads;
+    const bool here = live && n * groups + g < hr.n_heads;
     float x[N];
     if (here) {
       unpack<A>(own[n], x);
-      if (turn && h < hk) {
+      if (turn) {
         float y[N];
         if constexpr (INTER) {
 #pragma unroll
@@ -180,45 +190,42 @@ __global__ void __launch_bounds__(kThreads) k_rotate(const RotateArgs p) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           // elements past rot_dim keep their value (and their sign of zero)
-          if (d0 + i < p.r.rot_dim)
-            x[i] = __fadd_rn(__fmul_rn(x[i], cs[i]), __fmul_rn(y[i], sn[i]));
+          const float v = __fadd_rn(__fmul_rn(x[i], cs[i]), __fmul_rn(y[i], sn[i]));
+          if (d0 + N <= p.r.rot_dim || d0 + i < p.r.rot_dim) x[i] = v;
         }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = 0.f;
     }
-    if (here && (FMT == kRowsOnly || h < hq)) {
-      const HeadRows& dst = h < hq ? p.q : p.k;
-      const int hh = h < hq ? h : h - hq;
-      A* row = static_cast<A*>(dst.out) + t * dst.out_stride + static_cast<size_t>(hh) * p.head_dim;
-      *reinterpret_cast<uint4*>(row + d0) = pack<A>(x);
-    }
-    if constexpr (FMT != kRowsOnly) {
-      const bool is_k = h < hk;
-      const bool put = here && h >= hq && store;
-      const size_t row = put ? kv_row(p.c, page, is_k ? h - hq : h - hk, off) : 0;
-      char* dst = (is_k ? p.c.k : p.c.v) + row * p.c.row_bytes;
-      if constexpr (FMT == DT_F32 || FMT == DT_BF16) {
-        if (put) *reinterpret_cast<uint4*>(dst + c * 16) = pack<A>(x);
+    if constexpr (!kStore) {
+      if (here) *reinterpret_cast<uint4*>(dst + static_cast<size_t>(n) * step) = pack<A>(x);
+    } else {
+      const size_t r = row + static_cast<size_t>(n * groups) * p.c.page_size;
+      char* to = (KIND == 1 ? p.c.k : p.c.v) + r * p.c.row_bytes;
+      if constexpr (!kMx) {
+        if (here && put) *reinterpret_cast<uint4*>(to + c * 16) = pack<A>(x);
       } else {
         // a block's 32 elements are in four neighbouring lanes
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        float top = max_abs(max_abs(max_abs(x[0], x[1]), max_abs(x[2], x[3])),
+                            max_abs(max_abs(x[4], x[5]), max_abs(x[6], x[7])));
+        top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t amax = __float_as_uint(top) & 0x7fffffffu;
         float inv;
         const uint32_t s = mx_scale<FMT == DT_MXFP8 ? 8 : 2>(amax, &inv);
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = inv == 0.f ? 0.f : x[i] * inv;
-        if (put) {
-          if constexpr (FMT == DT_MXFP8)
-            *reinterpret_cast<uint2*>(dst + c * 8) = pack_e4m3x8(x);
-          else
-            *reinterpret_cast<uint32_t*>(dst + c * 4) = pack_e2m1x8(x);
+        for (int i = 0; i < N; ++i) x[i] *= inv;
+        if (here && put) {
+          if constexpr (FMT == DT_MXFP8) {
+            const uint2 code = pack_e4m3x8(x);
+            *reinterpret_cast<uint2*>(to + c * 8) = s == 255u ? make_uint2(0, 0) : code;
+          } else {
+            const uint32_t code = pack_e2m1x8(x);
+            *reinterpret_cast<uint32_t*>(to + c * 4) = s == 255u ? 0u : code;
+          }
           if (c % 4 == 0)
-            (is_k ? p.c.k_scale : p.c.v_scale)[row * p.c.scale_stride + c / 4] =
+            (KIND == 1 ? p.c.k_scale : p.c.v_scale)[r * p.c.scale_stride + c / 4] =
                 static_cast<uint8_t>(s);
         }
       }
@@ -226,16 +233,37 @@ __global__ void __launch_bounds__(kThreads) k_rotate(const RotateArgs p) {
   }
 }
 
+template <typename A, int FMT, bool INTER, int HPT>
+__global__ void __launch_bounds__(kThreads) k_rotate(const RotateArgs p) {
+  if (blockIdx.x < p.first[0])
+    rotate_rows<A, FMT, INTER, HPT, 0>(p, blockIdx.x);
+  else if (blockIdx.x < p.first[1])
+    rotate_rows<A, FMT, INTER, HPT, 1>(p, blockIdx.x - p.first[0]);
+  else if constexpr (FMT != kRowsOnly)
+    rotate_rows<A, FMT, INTER, HPT, 2>(p, blockIdx.x - p.first[1]);
+}
+
 template <typename A, int FMT, bool INTER>
 cudaError_t launch_hpt(RotateArgs& p, cudaStream_t st) {
   const int rows = kThreads / (p.head_dim / Chunk<A>::N);
+  int heads = 0;
+  for (const HeadRows& h : p.rows) heads += h.n_heads;
   // few rows: one head a thread, for the shortest chain of loads; many: four
   // heads a thread share the token's table row
-  const int hpt = static_cast<int64_t>(p.T) * p.heads <= 152 * 8 * rows ? 1 : 4;
-  p.groups = (p.heads + hpt - 1) / hpt;
-  const int64_t slots = static_cast<int64_t>(p.T) * p.groups;
-  const int64_t blocks = (slots + rows - 1) / rows;
-  if (slots + rows > INT32_MAX) return cudaErrorInvalidValue;
+  const int hpt = static_cast<int64_t>(p.T) * heads <= 152 * 8 * rows ? 1 : 4;
+  int64_t blocks = 0;
+  for (int k = 0; k < 3; ++k) {
+    p.groups[k] = (p.rows[k].n_heads + hpt - 1) / hpt;
+    const int64_t ids = static_cast<int64_t>(p.T) * p.groups[k];
+    if (ids + rows > INT32_MAX) return cudaErrorInvalidValue;
+    if (p.groups[k] == 0) p.groups[k] = 1;  // no heads: no blocks
+    else blocks += (ids + rows - 1) / rows;
+    p.first[k] = static_cast<unsigned>(blocks);
+  }
+  p.page_shift = -1;
+  for (int i = 0; i < 13; ++i)
+    if (p.c.page_size == 1 << i) p.page_shift = i;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   if (hpt == 1)
     k_rotate<A, FMT, INTER, 1><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
   else
@@ -280,12 +308,11 @@ cudaError_t launch_rope_table(const RopeFreq& f, int rot_dim, int n_positions, f
 cudaError_t launch_rotate(const HeadRows& q, const HeadRows& k, const RotaryView& r, int T,
                           int head_dim, int act, int* status, cudaStream_t st) {
   RotateArgs p{};
-  p.q = q;
-  p.k = k;
+  p.rows[0] = q;
+  p.rows[1] = k;
   p.r = r;
   p.T = T;
   p.head_dim = head_dim;
-  p.heads = q.n_heads + k.n_heads;
   p.status = status;
   return act == DT_F32 ? launch_layout<float, kRowsOnly>(p, st)
                        : launch_layout<__nv_bfloat16, kRowsOnly>(p, st);
@@ -295,15 +322,14 @@ cudaError_t launch_kv_append(const KvView& c, const HeadRows& q, const HeadRows&
                              const HeadRows& v, const RotaryView& r, const int32_t* slots, int T,
                              int* status, cudaStream_t st) {
   RotateArgs p{};
-  p.q = q;
-  p.k = k;
-  p.v = v;
+  p.rows[0] = q;
+  p.rows[1] = k;
+  p.rows[2] = v;
   p.r = r;
   p.c = c;
   p.slots = slots;
   p.T = T;
   p.head_dim = c.head_dim;
-  p.heads = q.n_heads + 2 * c.n_heads;
   p.status = status;
   switch (c.dtype) {
     case DT_F32: return launch_layout<float, DT_F32>(p, st);

@@ -24,6 +24,8 @@
 
 #include <float.h>
 
+#include <type_traits>
+
 #include "attn.h"
 #include "common.cuh"
 #include "mx.cuh"
@@ -47,8 +49,12 @@ struct Cfg {
   static constexpr int kBits = FMT == DT_F32 ? 32 : FMT == DT_BF16 ? 16 : FMT == DT_MXFP8 ? 8 : 4;
   static constexpr int kRow = DP * kBits / 8;          // bytes of a row in shared memory
   static constexpr int kScaleRow = kMx ? (DP > 128 ? 8 : 4) : 0;
+  // Tiles a warp takes in one step: two of an MX cache, whose small tiles leave
+  // the step's fixed work (pages, waits, votes) as long as the tile's own.
+  static constexpr int kStep = kMx && DP <= 128 ? 2 : 1;
+  static constexpr int kTileBytes = kTile * kRow, kTileScales = kTile * kScaleRow;
   // whole 128-byte lines: addresses within a line are XORed
-  static constexpr int kSlot = (kTile * (kRow + kScaleRow) + 127) / 128 * 128;
+  static constexpr int kSlot = (kStep * (kTileBytes + kTileScales) + 127) / 128 * 128;
   static constexpr int kRegs = DP / 16 * 4 * NT;       // O^T registers of a lane
   static constexpr int kWarps = kSlot > 8192 + 256 || NT * DP == 256 && NT == 2 ? 4 : 8;
   static constexpr int kPerSm =
@@ -93,6 +99,14 @@ COLI_DEV void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d = A x B (a zero accumulator input).
+COLI_DEV void mma_f16_16816_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 COLI_DEV void mma_tf32_1688(float (&d)[4], const float (&a)[4], const float (&b)[2]) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 "
@@ -183,16 +197,16 @@ COLI_DEV void copy_tile(uint32_t slot, uint32_t place, const char* src, int row_
 
 // And of its scales, one word a lane.
 template <class C>
-COLI_DEV void copy_scales(uint32_t slot, const uint8_t* src, int r0, int r1, int lane) {
+COLI_DEV void copy_scales(uint32_t dst, const uint8_t* src, int r0, int r1, int lane) {
   constexpr int kWords = C::kScaleRow / 4;
   if (lane < kTile * kWords) {
     const int r = lane / kWords;
-    cp_async4_n(slot + kTile * C::kRow + lane * 4, src + lane * 4, r >= r0 && r < r1 ? 4 : 0);
+    cp_async4_n(dst + lane * 4, src + lane * 4, r >= r0 && r < r1 ? 4 : 0);
   }
 }
 
 // Bytes equal to 0 or 255 in a word of scales (2^-127 and NaN need care).
-COLI_DEV bool odd_scales(uint32_t w) {
+COLI_DEV uint32_t odd_scales(uint32_t w) {
   const uint32_t n = ~w;
   return (((w - 0x01010101u) & n) | ((n - 0x01010101u) & w)) & 0x80808080u;
 }
@@ -247,7 +261,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     }
     total = __shfl_sync(0xffffffffu, s, 31) * hr_n;
     per = (total + gridDim.x - 1) / gridDim.x;
-    per = per < W ? W : per;
+    per = per < W * C::kStep ? W * C::kStep : per;
     u0 = blockIdx.x * per;
     u1 = u0 + per < total ? u0 + per : total;
     const uint32_t past = __ballot_sync(0xffffffffu, s * hr_n > u0);
@@ -286,7 +300,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       if (pass == 0) {
         total = sum * hr_n;
         per = (total + gridDim.x - 1) / gridDim.x;
-        per = per < W ? W : per;
+        per = per < W * C::kStep ? W * C::kStep : per;
         u0 = blockIdx.x * per;
         u1 = u0 + per < total ? u0 + per : total;
         if (u0 >= total) break;
@@ -430,17 +444,20 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       }
     }
 
-    // ---- this warp's tiles ---------------------------------------------------------------
-    const int n_it = (t1 - t0 - w + W - 1) / W;  // <= 0: none
+    // ---- this warp's steps of kStep tiles ----------------------------------------------
+    constexpr int S = C::kStep, kScales = S * C::kTileBytes;  // scales' place in a slot
+    const int n_it = ((t1 - t0 + S - 1) / S - w + W - 1) / W;  // <= 0: none
     const int start = a.window > 0 && sq.len > a.window ? sq.len - a.window : 0;
-    int page_of = 0, off_of = 0;  // lane i: page, and tile in it, of the warp's tile batch + i
+    const int tile0 = sq.first + t0 + w * S;  // step `it` takes tiles tile0 + it W S ...
+    const int key_end = min(sq.len, (sq.first + t1) * kTile);  // keys of this piece end here
+    int page_of = 0, off_of = 0;  // lane S k + i: page, and tile in it, of tile i of step batch + k
     int batch = -32;
-    auto pages = [&](int it) {  // loads the pages of tiles it .. it + 31
+    auto pages = [&](int it) {  // loads the pages of the next 32 / S steps
       batch = it;
-      const int k = it + lane;
+      const int tile = tile0 + (it + lane / S) * (W * S) + lane % S;
       page_of = -1;
-      if (k < n_it) {
-        const int tile = sq.first + t0 + w + k * W, pi = tile / tiles_per_page;
+      if (tile * kTile < key_end) {
+        const int pi = tile / tiles_per_page;
         off_of = tile - pi * tiles_per_page;
         page_of = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
         if (page_of < 0 || page_of >= a.c.n_pages) {
@@ -454,46 +471,44 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       s += C::kSlot;
       return s == ring + C::kRing * C::kSlot ? ring : s;
     };
-    // the tile being fetched: offsets of its keys (and values) and scales, rows in sight
-    uint64_t lead = 0, lead_sc = 0;
-    int lead_r0 = 0, lead_r1 = 0;
-    uint32_t hidden = 0;  // bit it % 32: tile `it` lies in a page that is left out
-    auto issue_k = [&](int it) {
+    uint32_t hidden = 0;  // bit (it S + i) % 32: that tile's page is left out (or past the end)
+    auto issue = [&](int it, auto keys) {
+      constexpr bool K = decltype(keys)::value;
       __syncwarp();
       if (it < n_it) {
-        if (it >= batch + 32) pages(it);
-        const int page = __shfl_sync(0xffffffffu, page_of, it - batch);
-        const uint32_t off = __shfl_sync(0xffffffffu, off_of, it - batch);
-        const uint32_t pg = page < 0 ? 0 : page;
-        lead = static_cast<uint64_t>(pg) * page_bytes + (h * head_bytes + off * tile_bytes + lane * 16);
-        const int key = (sq.first + t0 + w + it * W) * kTile;
-        lead_r0 = start - key;
-        lead_r1 = page < 0 ? 0 : sq.len - key;
-        hidden = (hidden & ~(1u << (it & 31))) | (page < 0 ? 1u : 0u) << (it & 31);
-        copy_tile<C, FMT, true>(fill, put_k, a.c.k + lead, a.c.row_bytes, lead_r0, lead_r1, lane);
-        if constexpr (kMx) {
-          lead_sc = static_cast<uint64_t>(pg) * page_scales +
-                    (h * head_scales + off * (kTile * C::kScaleRow));
-          copy_scales<C>(fill, a.c.k_scale + lead_sc, lead_r0, lead_r1, lane);
+        if (K && it >= batch + 32 / S) pages(it);
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const int page = __shfl_sync(0xffffffffu, page_of, (it - batch) * S + i);
+          const uint32_t off = __shfl_sync(0xffffffffu, off_of, (it - batch) * S + i);
+          const uint32_t pg = page < 0 ? 0 : page;
+          const int key = (tile0 + it * (W * S) + i) * kTile;
+          const int r0 = start - key, r1 = page < 0 ? 0 : key_end - key;
+          if (K) {
+            const int bit = (it * S + i) & 31;
+            hidden = (hidden & ~(1u << bit)) | (page < 0 ? 1u : 0u) << bit;
+          }
+          const uint64_t at = static_cast<uint64_t>(pg) * page_bytes +
+                              (h * head_bytes + (page < 0 ? 0 : off * tile_bytes) + lane * 16);
+          copy_tile<C, FMT, K>(fill + i * C::kTileBytes, K ? put_k : put_v,
+                               (K ? a.c.k : a.c.v) + at, a.c.row_bytes, r0, r1, lane);
+          if constexpr (kMx) {
+            const uint64_t sc = static_cast<uint64_t>(pg) * page_scales +
+                                (h * head_scales + (page < 0 ? 0 : off * C::kTileScales));
+            copy_scales<C>(fill + kScales + i * C::kTileScales,
+                           (K ? a.c.k_scale : a.c.v_scale) + sc, r0, r1, lane);
+          }
         }
       }
       cp_async_commit();
       fill = next(fill);
     };
-    auto issue_v = [&](int it) {
-      __syncwarp();
-      if (it < n_it) {
-        copy_tile<C, FMT, false>(fill, put_v, a.c.v + lead, a.c.row_bytes, lead_r0, lead_r1, lane);
-        if constexpr (kMx)
-          copy_scales<C>(fill, a.c.v_scale + lead_sc, lead_r0, lead_r1, lane);
-      }
-      cp_async_commit();
-      fill = next(fill);
-    };
+    using Keys = std::integral_constant<bool, true>;
+    using Values = std::integral_constant<bool, false>;
     // Scores of 32 elements in three tf32 products (hi hi + hi lo + lo hi). An
     // infinity times a part that is 0 would be NaN: `careful` leaves such
     // operands out of the cross products.
-    auto score_f32 = [&](float(&d)[NT][4], uint32_t at0, int j, bool careful) {
+    auto score_f32 = [&](float(&d)[S][NT][4], uint32_t at0, int j, bool careful) {
       if constexpr (kF32) {
         float ka[8], kb[8];
 #pragma unroll
@@ -518,15 +533,15 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             float qh[2], ql[2];
             split_tf32(qf[nt][j][2 * i], &qh[0], &ql[0]);
             split_tf32(qf[nt][j][2 * i + 1], &qh[1], &ql[1]);
-            mma_tf32_1688(d[nt], hi, qh);
+            mma_tf32_1688(d[0][nt], hi, qh);
             if (careful) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) hi[k] = fabsf(hi[k]) == INFINITY ? 0.f : hi[k];
 #pragma unroll
               for (int k = 0; k < 2; ++k) qh[k] = fabsf(qh[k]) == INFINITY ? 0.f : qh[k];
             }
-            mma_tf32_1688(d[nt], lo, qh);
-            mma_tf32_1688(d[nt], hi, ql);
+            mma_tf32_1688(d[0][nt], lo, qh);
+            mma_tf32_1688(d[0][nt], hi, ql);
           }
         }
       }
@@ -534,31 +549,58 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     constexpr int kLead = (C::kRing - 1) / 2;
 #pragma unroll
     for (int i = 0; i < kLead; ++i) {
-      issue_k(i);
-      issue_v(i);
+      issue(i, Keys());
+      issue(i, Values());
     }
     uint32_t slot = ring;
     for (int it = 0; it < n_it; ++it) {
-      // ---- scores ----------------------------------------------------------------------
-      issue_k(it + kLead);
+      // ---- scores: lane 4g + t gets keys g, g + 8 of heads 2t, 2t + 1 --------------------
+      issue(it + kLead, Keys());
       cp_async_wait<C::kRing - 1>();
       __syncwarp();
-      float x[NT][4];
+      float x[S][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
-      float f0[kMx ? kJ : 1], f1[kMx ? kJ : 1];  // the blocks' scales of keys g and g + 8
-      if constexpr (kMx) {
-        const uint32_t at = slot + kTile * C::kRow + g * C::kScaleRow;
-        uint32_t sc0[2], sc1[2];
-        bool odd = false;
+      for (int i = 0; i < S; ++i) {
+        const uint32_t tile = slot + i * C::kTileBytes;
+        if constexpr (FMT == DT_BF16) {
 #pragma unroll
-        for (int i = 0; i < C::kScaleRow / 4; ++i) {
-          // bytes past the head's blocks may hold anything: 1
-          sc0[i] = (lds32(at + 4 * i) & live[i]) | (0x7f7f7f7fu & ~live[i]);
-          sc1[i] = (lds32(at + 8 * C::kScaleRow + 4 * i) & live[i]) | (0x7f7f7f7fu & ~live[i]);
-          odd = odd || odd_scales(sc0[i]) || odd_scales(sc1[i]);
-        }
-        if (!__any_sync(0xffffffffu, odd)) {
+          for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            const uint32_t at = further(tile + get_k, j * 64);
+            const uint4 ka = lds128(at), kb = lds128(at + 8 * C::kRow);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_bf16_16816(x[i][nt], ka.x, kb.x, ka.y, kb.y, q[nt][j].x, q[nt][j].y);
+              mma_bf16_16816(x[i][nt], ka.z, kb.z, ka.w, kb.w, q[nt][j].z, q[nt][j].w);
+            }
+          }
+        } else if constexpr (kF32) {
+#pragma unroll 1
+          for (int careful = 0; careful < 2; ++careful) {
+            bool nan = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) score_f32(x, tile, j, careful != 0);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) nan |= x[i][nt][c] != x[i][nt][c];
+            if (!__any_sync(0xffffffffu, nan)) break;
+          }
+        } else {
+          // the blocks' scales of keys g and g + 8
+          float f0[kJ], f1[kJ];
+          const uint32_t sat = slot + kScales + i * C::kTileScales + g * C::kScaleRow;
+          uint32_t sc0[2], sc1[2], odd = 0;
+#pragma unroll
+          for (int k = 0; k < C::kScaleRow / 4; ++k) {
+            // bytes past the head's blocks may hold anything: 1
+            sc0[k] = (lds32(sat + 4 * k) & live[k]) | (0x7f7f7f7fu & ~live[k]);
+            sc1[k] = (lds32(sat + 8 * C::kScaleRow + 4 * k) & live[k]) | (0x7f7f7f7fu & ~live[k]);
+            odd |= odd_scales(sc0[k]) | odd_scales(sc1[k]);
+          }
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
             constexpr uint32_t kExp = 0x7f800000u;
@@ -566,139 +608,123 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             f0[j] = __uint_as_float((up > 0 ? sc0[j / 4] << (up & 31) : sc0[j / 4] >> 1) & kExp);
             f1[j] = __uint_as_float((up > 0 ? sc1[j / 4] << (up & 31) : sc1[j / 4] >> 1) & kExp);
           }
-        } else {
+          if (__any_sync(0xffffffffu, odd != 0)) {
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+              f0[j] = e8m0_f32((sc0[j / 4] >> (8 * (j % 4))) & 255u);
+              f1[j] = e8m0_f32((sc1[j / 4] >> (8 * (j % 4))) & 255u);
+            }
+          }
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
-            f0[j] = e8m0_f32((sc0[j / 4] >> (8 * (j % 4))) & 255u);
-            f1[j] = e8m0_f32((sc1[j / 4] >> (8 * (j % 4))) & 255u);
+            uint32_t ka[4], kb[4];
+            if constexpr (FMT == DT_MXFP8) {
+              const uint32_t at = further(tile + get_k, j * 32);
+              const uint2 va = lds64(at), vb = lds64(at + 8 * C::kRow);
+              e4m3x8_f16(va.x, va.y, ka);
+              e4m3x8_f16(vb.x, vb.y, kb);
+            } else {
+              const uint32_t at = further(tile + get_k, j * 16);
+              e2m1x8_f16(lds32(at), ka);
+              e2m1x8_f16(lds32(at + 8 * C::kRow), kb);
+            }
+            // the scale goes on the block's partial score: codes are exact in fp16
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float d[4];
+              mma_f16_16816_z(d, ka[0], kb[0], ka[1], kb[1], q[nt][j].x, q[nt][j].y);
+              mma_f16_16816(d, ka[2], kb[2], ka[3], kb[3], q[nt][j].z, q[nt][j].w);
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                x[i][nt][c] = j == 0 ? d[c] * (c < 2 ? f0[j] : f1[j])
+                                     : fmaf(d[c], c < 2 ? f0[j] : f1[j], x[i][nt][c]);
+            }
           }
         }
       }
+      // rows of this step's tiles in sight
+      int r0[S], r1[S];
+      bool part = false;
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        if constexpr (FMT == DT_BF16) {
-          const uint32_t at = further(slot + get_k, j * 64);
-          const uint4 ka = lds128(at), kb = lds128(at + 8 * C::kRow);
+      for (int i = 0; i < S; ++i) {
+        const int key = (tile0 + it * (W * S) + i) * kTile;
+        r0[i] = start - key;
+        r1[i] = hidden >> ((it * S + i) & 31) & 1u ? 0 : key_end - key;
+        part |= r0[i] > 0 || r1[i] < kTile;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[i][nt][c] *= xs[nt][c & 1];
+      }
+      if (part) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const bool in0 = g >= r0[i] && g < r1[i], in1 = g + 8 >= r0[i] && g + 8 < r1[i];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16_16816(x[nt], ka.x, kb.x, ka.y, kb.y, q[nt][j].x, q[nt][j].y);
-            mma_bf16_16816(x[nt], ka.z, kb.z, ka.w, kb.w, q[nt][j].z, q[nt][j].w);
+            if (!in0) x[i][nt][0] = x[i][nt][1] = -INFINITY;
+            if (!in1) x[i][nt][2] = x[i][nt][3] = -INFINITY;
           }
-        } else if (kMx && j * 32 < D) {
-          uint32_t ka[4], kb[4];
-          if constexpr (FMT == DT_MXFP8) {
-            const uint32_t at = further(slot + get_k, j * 32);
-            const uint2 va = lds64(at), vb = lds64(at + 8 * C::kRow);
-            e4m3x8_f16(va.x, va.y, ka);
-            e4m3x8_f16(vb.x, vb.y, kb);
-          } else {
-            const uint32_t at = further(slot + get_k, j * 16);
-            e2m1x8_f16(lds32(at), ka);
-            e2m1x8_f16(lds32(at + 8 * C::kRow), kb);
-          }
-          // the block's scale goes on its partial score: codes are exact in fp16
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16_16816(d, ka[0], kb[0], ka[1], kb[1], q[nt][j].x, q[nt][j].y);
-            mma_f16_16816(d, ka[2], kb[2], ka[3], kb[3], q[nt][j].z, q[nt][j].w);
-            x[nt][0] = fmaf(d[0], f0[j], x[nt][0]);
-            x[nt][1] = fmaf(d[1], f0[j], x[nt][1]);
-            x[nt][2] = fmaf(d[2], f1[j], x[nt][2]);
-            x[nt][3] = fmaf(d[3], f1[j], x[nt][3]);
-          }
-        }
-      }
-      if constexpr (kF32) {
-#pragma unroll 1
-        for (int careful = 0; careful < 2; ++careful) {
-          bool nan = false;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
-#pragma unroll
-          for (int j = 0; j < kJ; ++j) score_f32(x, slot, j, careful != 0);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) nan |= x[nt][c] != x[nt][c];
-          if (!__any_sync(0xffffffffu, nan)) break;
-        }
-      }
-      const int tile_key = (sq.first + t0 + w + it * W) * kTile;
-      // rows in sight of this tile
-      const int r0 = start - tile_key, r1 = hidden >> (it & 31) & 1u ? 0 : sq.len - tile_key;
-      bool up = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[nt][c] *= xs[nt][c & 1];
-      if (r0 > 0 || r1 < kTile) {
-        const bool in0 = g >= r0 && g < r1, in1 = g + 8 >= r0 && g + 8 < r1;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (!in0) x[nt][0] = x[nt][1] = -INFINITY;
-          if (!in1) x[nt][2] = x[nt][3] = -INFINITY;
         }
       }
       // ---- weights ---------------------------------------------------------------------
+      bool up = false;
+      float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) up |= fmaxf(x[nt][c], x[nt][c + 2]) > m[nt][c] + kSlack;
+        for (int c = 0; c < 2; ++c) {
+          top[nt][c] = fmaxf(x[0][nt][c], x[0][nt][c + 2]);
+          if constexpr (S == 2) top[nt][c] = fmaxf(top[nt][c], fmaxf(x[1][nt][c], x[1][nt][c + 2]));
+          up |= top[nt][c] > m[nt][c] + kSlack;
+        }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(x[nt][c], x[nt][c + 2]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top, m[nt][c]);
-            const float f = ex2(m[nt][c] - top);
-            m[nt][c] = top;
+            float v = top[nt][c];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            v = fmaxf(v, m[nt][c]);
+            const float f = ex2(m[nt][c] - v);
+            m[nt][c] = v;
             l[nt][c] *= f;
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) acc[i][nt][c] *= f, acc[i][nt][c + 2] *= f;
           }
       }
+      uint32_t small = 0;  // MX: a weight in (0, 2^-16)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < S; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          x[nt][c] = ex2(x[nt][c] - (m[nt][c & 1] - kLift));
-          l[nt][c & 1] += x[nt][c];
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            x[i][nt][c] = ex2(x[i][nt][c] - (m[nt][c & 1] - kLift));
+            l[nt][c & 1] += x[i][nt][c];
+            if (kMx) small |= __float_as_uint(x[i][nt][c]) - 1u < 0x377fffffu ? 1u : 0u;
+          }
       slot = next(slot);
 
-      // ---- values ------------------------------------------------------------------------
-      // the weights as the other product's operand: keys 2t, 2t + 1 (and + 8) of head g
-      uint32_t pb[NT][2], pl[NT][2];
-      float pf[kF32 ? NT : 1][4];
+      // ---- values: O^T += V^T P^T ----------------------------------------------------------
+      issue(it + kLead, Values());
+      // the weights as the product's operand: keys 2t, 2t + 1 (and + 8) of head g
+      if constexpr (FMT == DT_BF16) {
+        uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if constexpr (FMT == DT_BF16) {
+        for (int nt = 0; nt < NT; ++nt) {
           // bf16 weights and, beside them, what the rounding left: 16 bits together
-          const uint32_t h0 = pack_bf16x2(x[nt][0], x[nt][1]);
-          const uint32_t h1 = pack_bf16x2(x[nt][2], x[nt][3]);
+          const float(&y)[4] = x[0][nt];
+          const uint32_t h0 = pack_bf16x2(y[0], y[1]), h1 = pack_bf16x2(y[2], y[3]);
           pb[nt][0] = transpose8(h0);
           pb[nt][1] = transpose8(h1);
-          pl[nt][0] = transpose8(pack_bf16x2(x[nt][0] - bf16_lo(h0), x[nt][1] - bf16_hi(h0)));
-          pl[nt][1] = transpose8(pack_bf16x2(x[nt][2] - bf16_lo(h1), x[nt][3] - bf16_hi(h1)));
-        } else if constexpr (kF32) {
-          const int src = 8 * t + (g >> 1);  // lane of key 2t, head g
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {      // keys 2t, 2t + 1, 2t + 8, 2t + 9
-            const float e0 = __shfl_sync(0xffffffffu, x[nt][(k >> 1) * 2], src + (k & 1) * 4);
-            const float e1 = __shfl_sync(0xffffffffu, x[nt][(k >> 1) * 2 + 1], src + (k & 1) * 4);
-            pf[nt][k] = g & 1 ? e1 : e0;
-          }
+          pl[nt][0] = transpose8(pack_bf16x2(y[0] - bf16_lo(h0), y[1] - bf16_hi(h0)));
+          pl[nt][1] = transpose8(pack_bf16x2(y[2] - bf16_lo(h1), y[3] - bf16_hi(h1)));
         }
-      }
-      issue_v(it + kLead);
-      cp_async_wait<C::kRing - 1>();
-      __syncwarp();
-      if constexpr (FMT == DT_BF16) {
+        cp_async_wait<C::kRing - 1>();
+        __syncwarp();
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
           const uint32_t at = slot + get_v;
@@ -720,6 +746,19 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           }
         }
       } else if constexpr (kF32) {
+        float pf[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int src = 8 * t + (g >> 1);  // lane of key 2t, head g
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {      // keys 2t, 2t + 1, 2t + 8, 2t + 9
+            const float e0 = __shfl_sync(0xffffffffu, x[0][nt][(k >> 1) * 2], src + (k & 1) * 4);
+            const float e1 = __shfl_sync(0xffffffffu, x[0][nt][(k >> 1) * 2 + 1], src + (k & 1) * 4);
+            pf[nt][k] = g & 1 ? e1 : e0;
+          }
+        }
+        cp_async_wait<C::kRing - 1>();
+        __syncwarp();
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
 #pragma unroll
@@ -753,163 +792,182 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           }
         }
       } else {
+        cp_async_wait<C::kRing - 1>();
+        __syncwarp();
         // Value codes are exact in fp16, and so is a code times 2^(s - ref) for
         // scales s in [ref - 14, ref + 7]: ref follows the largest scale of the
         // lane's block (the four lanes of a g share it). sd holds s - ref + 0x1000
-        // for the keys of a pair in its halves. A tile with a scale out of that
-        // range, a NaN one or a weight too small for fp16 takes the careful way.
-        uint32_t sd[kV][2];
+        // for the keys of a pair in its halves. A step with a scale out of that
+        // range, a NaN one or a weight too small for fp16 is done with bf16 operands.
+        uint32_t sd[S][kV][2];
         uint32_t bad = 0;
-        const bool part = r0 > 0 || r1 < kTile;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t at = slot + kTile * C::kRow + (2 * t + 8 * k) * C::kScaleRow;
+        for (int i = 0; i < S; ++i) {
+          const uint32_t sat = slot + kScales + i * C::kTileScales + 2 * t * C::kScaleRow;
 #pragma unroll
-          for (int i = 0; i < C::kScaleRow / 4; ++i) {
-            uint32_t w0, w1;
-            if constexpr (C::kScaleRow == 4) {
-              const uint2 v = lds64(at);
-              w0 = v.x, w1 = v.y;
-            } else {
-              w0 = lds32(at + 4 * i), w1 = lds32(at + 8 + 4 * i);
+          for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int e = 0; e < C::kScaleRow / 4; ++e) {
+              uint32_t w0, w1;
+              if constexpr (C::kScaleRow == 4) {
+                const uint2 v = lds64(sat + 8 * k * C::kScaleRow);
+                w0 = v.x, w1 = v.y;
+              } else {
+                w0 = lds32(sat + 8 * k * C::kScaleRow + 4 * e);
+                w1 = lds32(sat + 8 * k * C::kScaleRow + 8 + 4 * e);
+              }
+              const uint32_t by = __byte_perm(w0, w1, pick);
+              sd[i][2 * e][k] = (by & mine[2 * e]) + bias[2 * e];
+              if constexpr (kV > 1)
+                sd[i][2 * e + 1][k] = (by >> 8 & mine[2 * e + 1]) + bias[2 * e + 1];
             }
-            const uint32_t by = __byte_perm(w0, w1, pick);
-            sd[2 * i][k] = (by & mine[2 * i]) + bias[2 * i];
-            if constexpr (kV > 1) sd[2 * i + 1][k] = (by >> 8 & mine[2 * i + 1]) + bias[2 * i + 1];
-          }
-          if (part) {  // rows out of sight hold zeros, whatever their scale
-            const int row = 2 * t + 8 * k;
-            const uint32_t lo = row < r0 || row >= r1 ? 0xffffu : 0u;
-            const uint32_t hi = row + 1 < r0 || row + 1 >= r1 ? 0xffff0000u : 0u;
+            if (part) {  // rows out of sight hold zeros, whatever their scale
+              const int row = 2 * t + 8 * k;
+              const uint32_t lo = row < r0[i] || row >= r1[i] ? 0xffffu : 0u;
+              const uint32_t hi = row + 1 < r0[i] || row + 1 >= r1[i] ? 0xffff0000u : 0u;
+#pragma unroll
+              for (int v = 0; v < kV; ++v)
+                sd[i][v][k] = (sd[i][v][k] & ~(lo | hi)) | (0x10001000u & (lo | hi));
+            }
 #pragma unroll
             for (int v = 0; v < kV; ++v)
-              sd[v][k] = (sd[v][k] & ~(lo | hi)) | (0x10001000u & (lo | hi));
+              bad |= (sd[i][v][k] - 0x0ff20ff2u) | (0x10071007u - sd[i][v][k]);
           }
-#pragma unroll
-          for (int v = 0; v < kV; ++v) bad |= (sd[v][k] - 0x0ff20ff2u) | (0x10071007u - sd[v][k]);
         }
         bad = (bad & 0x80008000u) | hot;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)  // 0 < weight < 2^-16
-            bad |= __float_as_uint(x[nt][c]) - 1u < 0x377fffffu ? 1u : 0u;
-        bool wide = false;
-        float fw[kV][4];  // the careful way's factors
         if (__any_sync(0xffffffffu, bad != 0)) {
-          int s[kV][4];
+          // raise ref where a scale is above its range; is everything in range then?
+          bool wide = false;
           hot = 0;
 #pragma unroll
           for (int v = 0; v < kV; ++v) {
-            int top = -1000;
+            int sv[S][4], most = -1000;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              s[v][k] = static_cast<int>(sd[v][k >> 1] >> (16 * (k & 1)) & 0xffffu) - 0x1000 + ref[v];
-              if (s[v][k] != 255) top = max(top, s[v][k]);
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            if (top > ref[v] + 7) {
-              const float f = ex2(static_cast<float>(ref[v] - top));
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                sv[i][k] = static_cast<int>(sd[i][v][k >> 1] >> (16 * (k & 1)) & 0xffffu) - 0x1000 +
+                           ref[v];
+                if (sv[i][k] != 255) most = max(most, sv[i][k]);
+              }
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            if (most > ref[v] + 7) {
+              const float f = ex2(static_cast<float>(ref[v] - most));
 #pragma unroll
               for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                   for (int c = 0; c < 4; ++c) acc[v * 4 + i][nt][c] *= f;
-              ref[v] = top;
-              bias[v] = (0x1000 - top) * 0x10001;
+              ref[v] = most;
+              bias[v] = (0x1000 - most) * 0x10001;
             }
             if (ref[v] > 247) hot = 1;  // a NaN scale would pass for 2^128
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int row = 2 * t + (k & 1) + (k >> 1) * 8;
-              if (row < r0 || row >= r1) s[v][k] = ref[v];
-              const int e = s[v][k] - ref[v];
-              wide |= e < -14 || e > 7 || s[v][k] == 255;
-              fw[v][k] = s[v][k] == 255 ? __uint_as_float(0x7fc00000u)
-                                        : __uint_as_float(static_cast<uint32_t>(e < -127 ? 0 : e + 127) << 23);
-            }
-            sd[v][0] = (s[v][0] - ref[v] + 0x1000) | (s[v][1] - ref[v] + 0x1000) << 16;
-            sd[v][1] = (s[v][2] - ref[v] + 0x1000) | (s[v][3] - ref[v] + 0x1000) << 16;
-          }
+            for (int i = 0; i < S; ++i) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) wide |= __float_as_uint(x[nt][c]) - 1u < 0x377fffffu;
-          wide = __any_sync(0xffffffffu, wide);
-        }
-        if (!wide) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            pb[nt][0] = transpose8(pack_f16x2(x[nt][0], x[nt][1]));
-            pb[nt][1] = transpose8(pack_f16x2(x[nt][2], x[nt][3]));
-          }
-        } else {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            pb[nt][0] = transpose8(pack_bf16x2(x[nt][0], x[nt][1]));
-            pb[nt][1] = transpose8(pack_bf16x2(x[nt][2], x[nt][3]));
-          }
-        }
-#pragma unroll
-        for (int v = 0; v < kV; ++v) {
-          uint32_t op[2][8];  // [keys 2t, 2t + 1 or + 8][element]: the two keys' codes in fp16
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t off = v * (C::kBits * 8) + k * 8 * C::kRow;
-            uint32_t h4[4];
-            if constexpr (FMT == DT_MXFP8) {
-              const uint2 e0 = lds64(further(slot + get_v, off));
-              const uint2 e1 = lds64(further(slot + get_v, off + C::kRow));
-              e4m3x8_f16(__byte_perm(e0.x, e1.x, 0x5140), __byte_perm(e0.x, e1.x, 0x7362), h4);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) op[k][i] = h4[i];
-              e4m3x8_f16(__byte_perm(e0.y, e1.y, 0x5140), __byte_perm(e0.y, e1.y, 0x7362), h4);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) op[k][4 + i] = h4[i];
-            } else {
-              const uint32_t e0 = lds32(further(slot + get_v, off));
-              const uint32_t e1 = lds32(further(slot + get_v, off + C::kRow));
-              e2m1x8_f16((e0 & 0x0f0f0f0fu) | ((e1 & 0x0f0f0f0fu) << 4), h4);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) op[k][2 * i] = h4[i];
-              e2m1x8_f16(((e0 >> 4) & 0x0f0f0f0fu) | (e1 & 0xf0f0f0f0u), h4);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) op[k][2 * i + 1] = h4[i];
+              for (int k = 0; k < 4; ++k) {
+                const int row = 2 * t + (k & 1) + (k >> 1) * 8;
+                if (row < r0[i] || row >= r1[i]) sv[i][k] = ref[v];
+                // below 2^-100 of ref nothing is left of a value beside the largest
+                const int e = max(sv[i][k] - ref[v], -100);
+                wide |= e < -14 || sv[i][k] == 255;
+                sv[i][k] = sv[i][k] == 255 ? 255 : e;  // 255: NaN (e is at most 7)
+              }
+              sd[i][v][0] = (sv[i][0] + 0x1000) | (sv[i][1] + 0x1000) << 16;
+              sd[i][v][1] = (sv[i][2] + 0x1000) | (sv[i][3] + 0x1000) << 16;
             }
           }
+          small |= wide ? 1u : 0u;
+        }
+        const bool wide = __any_sync(0xffffffffu, small != 0);
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          uint32_t pb[NT][2], pl[NT][2];
           if (!wide) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t f = (sd[v][k] - 0x0ff10ff1u) << 10;  // 2^(s - ref), both keys
-#pragma unroll
-              for (int i = 0; i < 8; ++i) op[k][i] = mul_f16x2(op[k][i], f);
+            for (int nt = 0; nt < NT; ++nt) {
+              pb[nt][0] = transpose8(pack_f16x2(x[i][nt][0], x[i][nt][1]));
+              pb[nt][1] = transpose8(pack_f16x2(x[i][nt][2], x[i][nt][3]));
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16_16816(acc[v * 4 + i][nt], op[0][2 * i], op[0][2 * i + 1], op[1][2 * i],
-                              op[1][2 * i + 1], pb[nt][0], pb[nt][1]);
           } else {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int nt = 0; nt < NT; ++nt) {
+              const float(&y)[4] = x[i][nt];
+              const uint32_t h0 = pack_bf16x2(y[0], y[1]), h1 = pack_bf16x2(y[2], y[3]);
+              pb[nt][0] = transpose8(h0);
+              pb[nt][1] = transpose8(h1);
+              pl[nt][0] = transpose8(pack_bf16x2(y[0] - bf16_lo(h0), y[1] - bf16_hi(h0)));
+              pl[nt][1] = transpose8(pack_bf16x2(y[2] - bf16_lo(h1), y[3] - bf16_hi(h1)));
+            }
+          }
+          const uint32_t at = slot + i * C::kTileBytes + get_v;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float lo, hi;
-                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-                    "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-                    : "=f"(lo), "=f"(hi)
-                    : "r"(op[k][i]));
-                op[k][i] = pack_bf16x2(lo * fw[v][2 * k], hi * fw[v][2 * k + 1]);
+          for (int v = 0; v < kV; ++v) {
+            uint32_t op[2][8];  // [keys 2t, 2t + 1 or + 8][element]: the two keys' codes in fp16
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t off = v * (C::kBits * 8) + k * 8 * C::kRow;
+              uint32_t h4[4];
+              if constexpr (FMT == DT_MXFP8) {
+                const uint2 e0 = lds64(further(at, off)), e1 = lds64(further(at, off + C::kRow));
+                e4m3x8_f16(__byte_perm(e0.x, e1.x, 0x5140), __byte_perm(e0.x, e1.x, 0x7362), h4);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) op[k][c] = h4[c];
+                e4m3x8_f16(__byte_perm(e0.y, e1.y, 0x5140), __byte_perm(e0.y, e1.y, 0x7362), h4);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) op[k][4 + c] = h4[c];
+              } else {
+                const uint32_t e0 = lds32(further(at, off)), e1 = lds32(further(at, off + C::kRow));
+                e2m1x8_f16((e0 & 0x0f0f0f0fu) | ((e1 & 0x0f0f0f0fu) << 4), h4);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) op[k][2 * c] = h4[c];
+                e2m1x8_f16(((e0 >> 4) & 0x0f0f0f0fu) | (e1 & 0xf0f0f0f0u), h4);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) op[k][2 * c + 1] = h4[c];
+              }
+            }
+            if (!wide) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t f = (sd[i][v][k] - 0x0ff10ff1u) << 10;  // 2^(s - ref), both keys
+#pragma unroll
+                for (int c = 0; c < 8; ++c) op[k][c] = mul_f16x2(op[k][c], f);
               }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_bf16_16816(acc[v * 4 + i][nt], op[0][2 * i], op[0][2 * i + 1], op[1][2 * i],
-                               op[1][2 * i + 1], pb[nt][0], pb[nt][1]);
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16_16816(acc[v * 4 + c][nt], op[0][2 * c], op[0][2 * c + 1], op[1][2 * c],
+                                op[1][2 * c + 1], pb[nt][0], pb[nt][1]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int e0 = static_cast<int>(sd[i][v][k] & 0xffffu) - 0x1000;
+                const int e1 = static_cast<int>(sd[i][v][k] >> 16) - 0x1000;
+                const float f0 = __uint_as_float(e0 == 255 ? 0x7fc00000u : (e0 + 127u) << 23);
+                const float f1 = __uint_as_float(e1 == 255 ? 0x7fc00000u : (e1 + 127u) << 23);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  float lo, hi;
+                  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                      "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+                      : "=f"(lo), "=f"(hi)
+                      : "r"(op[k][c]));
+                  op[k][c] = pack_bf16x2(lo * f0, hi * f1);
+                }
+              }
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma_bf16_16816(acc[v * 4 + c][nt], op[0][2 * c], op[0][2 * c + 1], op[1][2 * c],
+                                 op[1][2 * c + 1], pb[nt][0], pb[nt][1]);
+                  mma_bf16_16816(acc[v * 4 + c][nt], op[0][2 * c], op[0][2 * c + 1], op[1][2 * c],
+                                 op[1][2 * c + 1], pl[nt][0], pl[nt][1]);
+                }
+            }
           }
         }
       }
