@@ -6,11 +6,15 @@
 // on how a caller's own fp32 check is compiled, and an MX block's scale and
 // codes follow from it bit for bit.
 //
-// One thread holds 16 bytes of one head row and reads the pair partners it
-// needs from the same row (the other half of the head, in L1); a row's threads
-// are in one block, which reads all its rows before it stores any, so q_out may
-// be q. A thread takes HPT heads of its token, whose loads it has in flight
-// together, and keeps the token's cosines and sines in registers over them.
+// A row's threads are in one block, which reads all its rows before it stores
+// any, so q_out may be q. A thread takes HPT heads of its token, whose loads it
+// has in flight together, and keeps the token's cosines and sines in registers
+// over them. Three ways to share a row among threads:
+//   kInter  16 bytes a thread (pairs are neighbours);
+//   kPair   16 bytes of the first half and their partners in the second, where
+//           both are whole vectors (and, for an MX cache, whole blocks lie in
+//           four neighbouring lanes);
+//   kHalf   16 bytes a thread, partners read one by one: any other rot_dim.
 // Blocks are q's, then k's, then v's, so what a block does with its rows is
 // known to all its threads.
 #include "attn.h"
@@ -22,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRowsOnly = -1;  // no cache: both outputs are rows
+enum { kInter = 0, kPair = 1, kHalf = 2 };
 
 struct RotateArgs {
   HeadRows rows[3];     // q, k, v
@@ -66,6 +71,10 @@ COLI_DEV uint4 pack(const float (&x)[Chunk<A>::N]) {
   }
 }
 
+// 16 bytes that this kernel touches once (evict-first).
+COLI_DEV uint4 ld_once(const void* p) { return __ldcs(static_cast<const uint4*>(p)); }
+COLI_DEV void st_once(void* p, const uint4& v) { __stcs(static_cast<uint4*>(p), v); }
+
 // max(|a|, |b|), NaN if either is (the sign is not used).
 COLI_DEV float max_abs(float a, float b) {
   float r;
@@ -74,89 +83,88 @@ COLI_DEV float max_abs(float a, float b) {
 }
 
 // One block's rows of kind KIND (0 q, 1 k, 2 v).
-template <typename A, int FMT, bool INTER, int HPT, int KIND>
+template <typename A, int FMT, int MODE, int HPT, int KIND>
 COLI_DEV void rotate_rows(const RotateArgs& p, unsigned block) {
-  constexpr int N = Chunk<A>::N;
+  constexpr int N = Chunk<A>::N, CH = MODE == kPair ? 2 : 1;
   constexpr bool kStore = FMT != kRowsOnly && KIND > 0;  // rows go to the cache
   constexpr bool kMx = kStore && (FMT == DT_MXFP8 || FMT == DT_MXFP4);
-  const int cpr = p.head_dim / N;   // chunks (threads) per row
-  const int rows = kThreads / cpr;  // rows a block holds at once
-  const int local = threadIdx.x / cpr, c = threadIdx.x - local * cpr;
+  const int tpr = p.head_dim / (N * CH);  // threads per row
+  const int rows = kThreads / tpr;        // rows a block holds at once
+  const int local = threadIdx.x / tpr, u = threadIdx.x - local * tpr;
   const int groups = p.groups[KIND];
   const uint32_t id = block * static_cast<uint32_t>(rows) + local;
   const uint32_t t = id / groups;
   const int g = id - t * groups;
   const bool live = local < rows && t < static_cast<uint32_t>(p.T);
   const HeadRows& hr = p.rows[KIND];
-  const int d0 = c * N, half = p.r.rot_dim / 2;
-  const int step = groups * p.head_dim;  // elements between a thread's heads
+  const int rot = p.r.rot_dim, half = rot / 2;
+  // elements from d0 on, and `apart` further (kPair: partners, or two pieces past rot_dim)
+  int d0 = u * N, apart = 0;
+  if constexpr (MODE == kPair) {
+    const bool in = d0 < half;
+    d0 = in ? d0 : d0 + half;
+    apart = in ? half : (p.head_dim - rot) / 2;
+  }
+  const int n_in = live ? (hr.n_heads - g + groups - 1) / groups : 0;  // heads of this thread
+  const int step = groups * p.head_dim;  // elements between them
 
   const A* src = static_cast<const A*>(hr.in) + (live ? t * hr.in_stride : 0) + g * p.head_dim + d0;
-  uint4 own[HPT];
+  uint4 own[HPT][CH];
 #pragma unroll
   for (int n = 0; n < HPT; ++n)
-    if (live && n * groups + g < hr.n_heads)
-      own[n] = *reinterpret_cast<const uint4*>(src + static_cast<size_t>(n) * step);
+    if (n < n_in) {
+      own[n][0] = ld_once(src + n * step);
+      if constexpr (CH == 2) own[n][1] = ld_once(src + n * step + apart);
+    }
 
-  // the cosine and signed sine of each element's pair
-  float cs[N], sn[N];
-  uint4 other[HPT];
+  // the cosine and sine of each pair; kHalf: of each element's, signed
+  constexpr int kAngles = MODE == kInter ? N / 2 : N;
+  float cs[kAngles], sn[kAngles];
+  uint4 other[MODE == kHalf ? HPT : 1];
   bool turn = false, bad_pos = false;
   if (KIND < 2 && live && p.r.table != nullptr) {
     const int pos = p.r.positions[t];
     bad_pos = static_cast<uint32_t>(pos) >= static_cast<uint32_t>(p.r.n_positions);
-    if (bad_pos && c == 0 && g == 0) latch_error(p.status, kErrDevice);
-    turn = !bad_pos && d0 < p.r.rot_dim;
+    if (bad_pos && u == 0 && g == 0) latch_error(p.status, kErrDevice);
+    turn = !bad_pos && d0 < rot;
     if (turn) {
       const float2* row =
           reinterpret_cast<const float2*>(p.r.table) + static_cast<size_t>(pos) * half;
-      if constexpr (INTER) {
+      if constexpr (MODE == kInter) {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-          const float2 v = d0 + 2 * i < p.r.rot_dim ? __ldg(row + d0 / 2 + i) : make_float2(1, 0);
-          cs[2 * i] = cs[2 * i + 1] = v.x;
-          sn[2 * i + 1] = v.y * p.r.sine_sign;
-          sn[2 * i] = -sn[2 * i + 1];
+          const float2 v = d0 + 2 * i < rot ? __ldg(row + d0 / 2 + i) : make_float2(1, 0);
+          cs[i] = v.x, sn[i] = v.y * p.r.sine_sign;
         }
-      } else if (half % N == 0) {  // partner chunk and table entries are whole vectors
-        const bool low = d0 < half;
-        const float sgn = low ? -p.r.sine_sign : p.r.sine_sign;
-        const float2* at = row + (low ? d0 : d0 - half);
+      } else if constexpr (MODE == kPair) {
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-          const float4 v = __ldg(reinterpret_cast<const float4*>(at + i));
-          cs[i] = v.x, sn[i] = v.y * sgn, cs[i + 1] = v.z, sn[i + 1] = v.w * sgn;
+          const float4 v = __ldg(reinterpret_cast<const float4*>(row + d0 + i));
+          cs[i] = v.x, sn[i] = v.y * p.r.sine_sign, cs[i + 1] = v.z, sn[i + 1] = v.w * p.r.sine_sign;
         }
-        const A* po = src + (low ? half : -half);
-#pragma unroll
-        for (int n = 0; n < HPT; ++n)
-          if (n * groups + g < hr.n_heads)
-            other[n] = *reinterpret_cast<const uint4*>(po + static_cast<size_t>(n) * step);
       } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int d = d0 + i;
-          const float2 v = d < p.r.rot_dim ? __ldg(row + (d < half ? d : d - half))
-                                           : make_float2(1, 0);
+          const float2 v = d < rot ? __ldg(row + (d < half ? d : d - half)) : make_float2(1, 0);
           cs[i] = v.x;
           sn[i] = v.y * (d < half ? -p.r.sine_sign : p.r.sine_sign);
         }
 #pragma unroll
         for (int n = 0; n < HPT; ++n) {
-          if (n * groups + g >= hr.n_heads) continue;
+          if (n >= n_in) continue;
           A e[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const int d = d0 + i;
-            e[i] = src[static_cast<int64_t>(n) * step + i +
-                       (d >= p.r.rot_dim ? 0 : (d < half ? half : -half))];
+            e[i] = src[n * step + i + (d >= rot ? 0 : (d < half ? half : -half))];
           }
           other[n] = *reinterpret_cast<const uint4*>(e);
         }
       }
     }
   }
-  // where the row goes
+  // where the rows go
   A* dst = nullptr;
   size_t row = 0;
   bool put = live;
@@ -165,7 +173,7 @@ COLI_DEV void rotate_rows(const RotateArgs& p, unsigned block) {
   } else if (live) {
     const int slot = p.slots[t];
     const bool bad = slot < -1 || slot >= p.c.n_pages * p.c.page_size;
-    if (bad && c == 0 && g == 0) latch_error(p.status, kErrDevice);
+    if (bad && u == 0 && g == 0) latch_error(p.status, kErrDevice);
     if (KIND == 2 && p.r.table != nullptr)
       bad_pos = static_cast<uint32_t>(p.r.positions[t]) >= static_cast<uint32_t>(p.r.n_positions);
     put = slot >= 0 && !bad && !bad_pos;
@@ -173,84 +181,116 @@ COLI_DEV void rotate_rows(const RotateArgs& p, unsigned block) {
     if (put) row = kv_row(p.c, page, g, slot - page * p.c.page_size);
   }
   if constexpr (!kStore) __syncthreads();  // q_out may be q: all rows are read before any is stored
+  const int row_step = groups * p.c.page_size;
 #pragma unroll
   for (int n = 0; n < HPT; ++n) {
-    const bool here = live && n * groups + g < hr.n_heads;
-    float x[N];
-    if (here) {
-      unpack<A>(own[n], x);
+    float x[CH][N];
+    if (n < n_in) {
+#pragma unroll
+      for (int k = 0; k < CH; ++k) unpack<A>(own[n][k], x[k]);
       if (turn) {
-        float y[N];
-        if constexpr (INTER) {
+        if constexpr (MODE == kPair) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) y[i] = x[i ^ 1];
+          for (int i = 0; i < N; ++i) {
+            const float a = x[0][i], b = x[CH - 1][i];
+            x[0][i] = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(b, sn[i]));
+            x[CH - 1][i] = __fadd_rn(__fmul_rn(b, cs[i]), __fmul_rn(a, sn[i]));
+          }
         } else {
-          unpack<A>(other[n], y);
-        }
+          float v[N];
+          if constexpr (MODE == kInter) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          // elements past rot_dim keep their value (and their sign of zero)
-          const float v = __fadd_rn(__fmul_rn(x[i], cs[i]), __fmul_rn(y[i], sn[i]));
-          if (d0 + N <= p.r.rot_dim || d0 + i < p.r.rot_dim) x[i] = v;
+            for (int i = 0; i < N / 2; ++i) {
+              const float a = x[0][2 * i], b = x[0][2 * i + 1];
+              v[2 * i] = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(b, sn[i]));
+              v[2 * i + 1] = __fadd_rn(__fmul_rn(b, cs[i]), __fmul_rn(a, sn[i]));
+            }
+          } else {
+            unpack<A>(other[n], v);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              v[i] = __fadd_rn(__fmul_rn(x[0][i], cs[i]), __fmul_rn(v[i], sn[i]));
+          }
+          if (d0 + N <= rot) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[0][i] = v[i];
+          } else {  // elements past rot_dim keep their bits
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (d0 + i < rot) x[0][i] = v[i];
+          }
         }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = 0.f;
+      for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[k][i] = 0.f;
     }
     if constexpr (!kStore) {
-      if (here) *reinterpret_cast<uint4*>(dst + static_cast<size_t>(n) * step) = pack<A>(x);
+      if (n < n_in) {
+        st_once(dst + n * step, pack<A>(x[0]));
+        if constexpr (CH == 2) st_once(dst + n * step + apart, pack<A>(x[CH - 1]));
+      }
     } else {
-      const size_t r = row + static_cast<size_t>(n * groups) * p.c.page_size;
+      const size_t r = row + static_cast<size_t>(n) * row_step;
       char* to = (KIND == 1 ? p.c.k : p.c.v) + r * p.c.row_bytes;
-      if constexpr (!kMx) {
-        if (here && put) *reinterpret_cast<uint4*>(to + c * 16) = pack<A>(x);
-      } else {
-        // a block's 32 elements are in four neighbouring lanes
-        float top = max_abs(max_abs(max_abs(x[0], x[1]), max_abs(x[2], x[3])),
-                            max_abs(max_abs(x[4], x[5]), max_abs(x[6], x[7])));
-        top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t amax = __float_as_uint(top) & 0x7fffffffu;
-        float inv;
-        const uint32_t s = mx_scale<FMT == DT_MXFP8 ? 8 : 2>(amax, &inv);
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] *= inv;
-        if (here && put) {
-          if constexpr (FMT == DT_MXFP8) {
-            const uint2 code = pack_e4m3x8(x);
-            *reinterpret_cast<uint2*>(to + c * 8) = s == 255u ? make_uint2(0, 0) : code;
-          } else {
-            const uint32_t code = pack_e2m1x8(x);
-            *reinterpret_cast<uint32_t*>(to + c * 4) = s == 255u ? 0u : code;
+      for (int k = 0; k < CH; ++k) {
+        const int c = (d0 + k * apart) / N;  // piece of the row
+        if constexpr (!kMx) {
+          if (n < n_in && put) *reinterpret_cast<uint4*>(to + c * 16) = pack<A>(x[k]);
+        } else {
+          // a block's 32 elements are in four neighbouring lanes
+          float top = max_abs(max_abs(max_abs(x[k][0], x[k][1]), max_abs(x[k][2], x[k][3])),
+                              max_abs(max_abs(x[k][4], x[k][5]), max_abs(x[k][6], x[k][7])));
+          top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const uint32_t amax = __float_as_uint(top) & 0x7fffffffu;
+          float inv;
+          const uint32_t s = mx_scale<FMT == DT_MXFP8 ? 8 : 2>(amax, &inv);
+#pragma unroll
+          for (int i = 0; i < N; ++i) x[k][i] *= inv;
+          if (n < n_in && put) {
+            if constexpr (FMT == DT_MXFP8) {
+              const uint2 code = pack_e4m3x8(x[k]);
+              *reinterpret_cast<uint2*>(to + c * 8) = s == 255u ? make_uint2(0, 0) : code;
+            } else {
+              const uint32_t code = pack_e2m1x8(x[k]);
+              *reinterpret_cast<uint32_t*>(to + c * 4) = s == 255u ? 0u : code;
+            }
+            if (c % 4 == 0)
+              (KIND == 1 ? p.c.k_scale : p.c.v_scale)[r * p.c.scale_stride + c / 4] =
+                  static_cast<uint8_t>(s);
           }
-          if (c % 4 == 0)
-            (KIND == 1 ? p.c.k_scale : p.c.v_scale)[r * p.c.scale_stride + c / 4] =
-                static_cast<uint8_t>(s);
         }
       }
     }
   }
 }
 
-template <typename A, int FMT, bool INTER, int HPT>
-__global__ void __launch_bounds__(kThreads) k_rotate(const RotateArgs p) {
+template <typename A, int FMT, int MODE, int HPT>
+__global__ void __launch_bounds__(kThreads, HPT > 1 && MODE != kHalf ? 4 : 1) k_rotate(const RotateArgs p) {
   if (blockIdx.x < p.first[0])
-    rotate_rows<A, FMT, INTER, HPT, 0>(p, blockIdx.x);
+    rotate_rows<A, FMT, MODE, HPT, 0>(p, blockIdx.x);
   else if (blockIdx.x < p.first[1])
-    rotate_rows<A, FMT, INTER, HPT, 1>(p, blockIdx.x - p.first[0]);
+    rotate_rows<A, FMT, MODE, HPT, 1>(p, blockIdx.x - p.first[0]);
   else if constexpr (FMT != kRowsOnly)
-    rotate_rows<A, FMT, INTER, HPT, 2>(p, blockIdx.x - p.first[1]);
+    rotate_rows<A, FMT, MODE, HPT, 2>(p, blockIdx.x - p.first[1]);
 }
 
-template <typename A, int FMT, bool INTER>
+template <typename A, int FMT, int MODE>
 cudaError_t launch_hpt(RotateArgs& p, cudaStream_t st) {
-  const int rows = kThreads / (p.head_dim / Chunk<A>::N);
+  constexpr int CH = MODE == kPair ? 2 : 1;
+  // measured at 16384 tokens of 40 (48) heads of 128, us: pairs 2 / 4 heads a
+  // thread 75.9 / 70.4 (4 blocks an SM; 5: 80), neighbours 4 / 8 heads 59.5 / 55.8
+  constexpr int kMany = MODE == kInter ? 8 : 4;
+  const int rows = kThreads / (p.head_dim / (Chunk<A>::N * CH));
   int heads = 0;
   for (const HeadRows& h : p.rows) heads += h.n_heads;
-  // few rows: one head a thread, for the shortest chain of loads; many: four
-  // heads a thread share the token's table row
-  const int hpt = static_cast<int64_t>(p.T) * heads <= 152 * 8 * rows ? 1 : 4;
+  // few rows: one head a thread, for the shortest chain of loads; many: the
+  // heads of a thread share the token's table row
+  const int hpt = static_cast<int64_t>(p.T) * heads <= 152 * 8 * rows ? 1 : kMany;
   int64_t blocks = 0;
   for (int k = 0; k < 3; ++k) {
     p.groups[k] = (p.rows[k].n_heads + hpt - 1) / hpt;
@@ -265,15 +305,21 @@ cudaError_t launch_hpt(RotateArgs& p, cudaStream_t st) {
     if (p.c.page_size == 1 << i) p.page_shift = i;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   if (hpt == 1)
-    k_rotate<A, FMT, INTER, 1><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
+    k_rotate<A, FMT, MODE, 1><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
   else
-    k_rotate<A, FMT, INTER, 4><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
+    k_rotate<A, FMT, MODE, kMany><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename A, int FMT>
 cudaError_t launch_layout(RotateArgs& p, cudaStream_t st) {
-  return p.r.interleaved ? launch_hpt<A, FMT, true>(p, st) : launch_hpt<A, FMT, false>(p, st);
+  constexpr bool kMx = FMT == DT_MXFP8 || FMT == DT_MXFP4;
+  constexpr int kUnit = kMx ? kMxBlock : Chunk<A>::N;
+  if (p.r.interleaved) return launch_hpt<A, FMT, kInter>(p, st);
+  // without a rotation any split in two will do: rot_dim is 0 then
+  const int half = p.r.rot_dim / 2, rest = p.head_dim - p.r.rot_dim;
+  if (half % kUnit == 0 && rest % (2 * kUnit) == 0) return launch_hpt<A, FMT, kPair>(p, st);
+  return launch_hpt<A, FMT, kHalf>(p, st);
 }
 
 // w_i evaluated per entry in fp64: one table serves every layer and step of a

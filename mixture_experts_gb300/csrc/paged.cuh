@@ -51,7 +51,10 @@ struct Cfg {
   static constexpr int kScaleRow = kMx ? (DP > 128 ? 8 : 4) : 0;
   // Tiles a warp takes in one step: two of an MX cache, whose small tiles leave
   // the step's fixed work (pages, waits, votes) as long as the tile's own.
-  static constexpr int kStep = kMx && DP <= 128 ? 2 : 1;
+#ifndef COLI_STEP
+#define COLI_STEP 2
+#endif
+  static constexpr int kStep = kMx && DP <= 128 ? COLI_STEP : 1;
   static constexpr int kTileBytes = kTile * kRow, kTileScales = kTile * kScaleRow;
   // whole 128-byte lines: addresses within a line are XORed
   static constexpr int kSlot = (kStep * (kTileBytes + kTileScales) + 127) / 128 * 128;
@@ -104,6 +107,22 @@ COLI_DEV void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2
 COLI_DEV void mma_f16_16816_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                               uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// e4m3 x e4m3, 32 indices: twice the f16 form's work an instruction, summed in
+// fp32 as exactly (checked to 24 bits within an instruction and across).
+COLI_DEV void mma_e4m3_16832(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+COLI_DEV void mma_e4m3_16832_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -392,8 +411,13 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         }
       }
       if constexpr (kMx) {
-        // fp16 queries: the head's largest element is brought to [2^14, 2^15),
-        // an exact power of two that goes into the scores' scale
+        // The head's largest element is brought to [2^kTop, 2^(kTop + 1)), an exact
+        // power of two that goes into the scores' scale. MXFP4 keys meet fp16
+        // queries (exact but for elements below 2^-28 of the largest). MXFP8 keys
+        // are an operand as they are: the query is cut in two e4m3 terms, the second
+        // 32 times what the first leaves. bf16's 8 bits fit the two exactly down to
+        // 2^-14 of the largest element; below, 2^-22 of it is lost at most.
+        constexpr int kTop = FMT == DT_MXFP8 ? 7 : 14;
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < kJ; ++j)
@@ -406,16 +430,31 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e = static_cast<int>(top >> 23) - 127;
         e = e < -112 ? -112 : e;
-        const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+        const float up = __uint_as_float(static_cast<uint32_t>(kTop - e + 127) << 23);
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
           const uint4 v = q[nt][j];
-          q[nt][j] = make_uint4(pack_f16x2(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
-                                pack_f16x2(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
-                                pack_f16x2(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
-                                pack_f16x2(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+          const float y[8] = {bf16_lo(v.x) * up, bf16_hi(v.x) * up, bf16_lo(v.y) * up,
+                              bf16_hi(v.y) * up, bf16_lo(v.z) * up, bf16_hi(v.z) * up,
+                              bf16_lo(v.w) * up, bf16_hi(v.w) * up};
+          if constexpr (FMT == DT_MXFP8) {
+            const uint2 hi = pack_e4m3x8(y);
+            uint32_t h4[4];
+            float z[8];
+            e4m3x8_f16(hi.x, hi.y, h4);
+            f16x8_f32(h4, z);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = (y[i] - z[i]) * 32.f;
+            const uint2 lo = pack_e4m3x8(z);
+            q[nt][j] = make_uint4(hi.x, hi.y, lo.x, lo.y);
+          } else {
+            q[nt][j] = make_uint4(pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3]),
+                                  pack_f16x2(y[4], y[5]), pack_f16x2(y[6], y[7]));
+          }
         }
-        const float down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+        // (an infinite or NaN query: NaN scores)
+        const float down = e > 127 ? __uint_as_float(0x7fc00000u)
+                                   : __uint_as_float(static_cast<uint32_t>(e - kTop + 127) << 23);
         xs[nt][0] = sl * __shfl_sync(0xffffffffu, down, 8 * t);
         xs[nt][1] = sl * __shfl_sync(0xffffffffu, down, 8 * t + 4);
       }
@@ -621,19 +660,25 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             if constexpr (FMT == DT_MXFP8) {
               const uint32_t at = further(tile + get_k, j * 32);
               const uint2 va = lds64(at), vb = lds64(at + 8 * C::kRow);
-              e4m3x8_f16(va.x, va.y, ka);
-              e4m3x8_f16(vb.x, vb.y, kb);
+              ka[0] = va.x, ka[1] = va.y, kb[0] = vb.x, kb[1] = vb.y;
             } else {
               const uint32_t at = further(tile + get_k, j * 16);
               e2m1x8_f16(lds32(at), ka);
               e2m1x8_f16(lds32(at + 8 * C::kRow), kb);
             }
-            // the scale goes on the block's partial score: codes are exact in fp16
+            // the scale goes on the block's partial score: codes are exact operands
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float d[4];
-              mma_f16_16816_z(d, ka[0], kb[0], ka[1], kb[1], q[nt][j].x, q[nt][j].y);
-              mma_f16_16816(d, ka[2], kb[2], ka[3], kb[3], q[nt][j].z, q[nt][j].w);
+              if constexpr (FMT == DT_MXFP8) {
+                mma_e4m3_16832_z(d, ka[0], kb[0], ka[1], kb[1], q[nt][j].z, q[nt][j].w);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) d[c] *= 0.03125f;
+                mma_e4m3_16832(d, ka[0], kb[0], ka[1], kb[1], q[nt][j].x, q[nt][j].y);
+              } else {
+                mma_f16_16816_z(d, ka[0], kb[0], ka[1], kb[1], q[nt][j].x, q[nt][j].y);
+                mma_f16_16816(d, ka[2], kb[2], ka[3], kb[3], q[nt][j].z, q[nt][j].w);
+              }
 #pragma unroll
               for (int c = 0; c < 4; ++c)
                 x[i][nt][c] = j == 0 ? d[c] * (c < 2 ? f0[j] : f1[j])
@@ -695,7 +740,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             for (int i = 0; i < DP / 16; ++i) acc[i][nt][c] *= f, acc[i][nt][c + 2] *= f;
           }
       }
-      uint32_t small = 0;  // MX: a weight in (0, 2^-16)
+      uint32_t least = 0xffffffffu;  // MX: the smallest weight above 0 (its bits less 1)
 #pragma unroll
       for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -704,7 +749,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           for (int c = 0; c < 4; ++c) {
             x[i][nt][c] = ex2(x[i][nt][c] - (m[nt][c & 1] - kLift));
             l[nt][c & 1] += x[i][nt][c];
-            if (kMx) small |= __float_as_uint(x[i][nt][c]) - 1u < 0x377fffffu ? 1u : 0u;
+            if (kMx) least = min(least, __float_as_uint(x[i][nt][c]) - 1u);
           }
       slot = next(slot);
 
@@ -879,9 +924,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
               sd[i][v][1] = (sv[i][2] + 0x1000) | (sv[i][3] + 0x1000) << 16;
             }
           }
-          small |= wide ? 1u : 0u;
+          if (wide) least = 0;
         }
-        const bool wide = __any_sync(0xffffffffu, small != 0);
+        const bool wide = __any_sync(0xffffffffu, least < 0x377fffffu);  // 2^-16
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           uint32_t pb[NT][2], pl[NT][2];
