@@ -85,6 +85,10 @@ int check_cache(const coli_kv_cache* c, KvView* out) {
   if (c->n_pages < 1 || static_cast<int64_t>(c->n_pages) * c->page_size > INT32_MAX)
     return reject(COLI_EINVAL, "n_pages=%d: need at least 1 and n_pages * page_size < 2^31",
                   c->n_pages);
+  // tiles of 16 rows are numbered in 32 bits (2^36 rows of at least 16 bytes: over a TiB)
+  if (static_cast<int64_t>(c->n_pages) * c->page_size / 16 * c->n_kv_heads >= UINT32_MAX)
+    return reject(COLI_EINVAL, "cache of %d pages of %d tokens and %d heads is too large",
+                  c->n_pages, c->page_size, c->n_kv_heads);
   if (!c->k || !c->v || misaligned(c->k, 16) || misaligned(c->v, 16))
     return reject(COLI_EINVAL, "cache k and v must be set and 16-byte aligned");
   if (mx && (!c->k_scale || !c->v_scale || misaligned(c->k_scale, 4) || misaligned(c->v_scale, 4)))

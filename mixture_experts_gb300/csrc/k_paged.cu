@@ -11,7 +11,7 @@ namespace {
 // blocks, o = sum o_k 2^(m_k - m). A group of registers is one 16 x 8 tile of
 // O^T. With gridDim.y = 1 a warp takes whole groups; otherwise block y takes
 // group y and its warps share the partials.
-template <int DP, int NT, bool F32>
+template <int DP, int NT, bool F32, bool IN_ORDER>
 __global__ void __launch_bounds__(256) k_join(const Params p) {
   constexpr int kGroups = DP / 16 * NT, kRegs = kGroups * 4;
   constexpr int kPart = kRegs * 32 + 16 * NT;
@@ -78,23 +78,15 @@ __global__ void __launch_bounds__(256) k_join(const Params p) {
       }
     }
     const int b = sp.x, h = sp.y / p.blocks, row0 = (sp.y - h * p.blocks) * 8 * NT;
-    const int d = (i / 4) * 64 + g * 8 + (i % 4) * 2;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int r = row0 + nt * 8 + 2 * t + c;
       if (r >= p.group) continue;
       const int hq = h * p.group + r;
       const float inv = l[c] == 0.f ? 0.f : 1.f / l[c];
-      if (d < D) {
-        const size_t at = static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(hq) * D + d;
-        const float y0 = l[c] == 0.f ? 0.f : o[c] * inv;
-        const float y1 = l[c] == 0.f ? 0.f : o[c + 2] * inv;
-        if constexpr (F32)
-          *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(y0, y1);
-        else
-          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at) =
-              pack_bf16x2(y0, y1);
-      }
+      store_out<IN_ORDER, F32>(
+          a, static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(hq) * D, i, g,
+          l[c] == 0.f ? 0.f : o[c] * inv, l[c] == 0.f ? 0.f : o[c + 2] * inv);
       if (a.lse != nullptr && i == 0 && g == 0)
         a.lse[static_cast<size_t>(b) * a.n_q_heads + hq] =
             l[c] == 0.f ? -INFINITY : (m[c] + log2f(l[c])) * 0.6931471805599453f;
@@ -104,7 +96,7 @@ __global__ void __launch_bounds__(256) k_join(const Params p) {
 
 // The join is launched so that its blocks may be placed while the main kernel
 // drains; they wait for its end (griddepcontrol.wait) before they read.
-template <int DP, int NT, bool F32>
+template <int DP, int NT, bool F32, bool IN_ORDER>
 cudaError_t launch_join(const Params& p, int grid, int ys, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, ys);
@@ -115,7 +107,7 @@ cudaError_t launch_join(const Params& p, int grid, int ys, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_join<DP, NT, F32>, p);
+  return cudaLaunchKernelEx(&cfg, k_join<DP, NT, F32, IN_ORDER>, p);
 }
 
 int sm_count() {
@@ -166,6 +158,18 @@ Form form_of(const KvView& c, int n_q_heads) {
   return f;
 }
 
+template <bool F32, bool IN_ORDER>
+cudaError_t launch_joins(const Params& p, const Form& f, int grid, int ys, cudaStream_t st) {
+  if constexpr (!F32) {
+    if (f.nt == 2)
+      return f.dp == 64 ? launch_join<64, 2, F32, IN_ORDER>(p, grid, ys, st)
+                        : launch_join<128, 2, F32, IN_ORDER>(p, grid, ys, st);
+  }
+  if (f.dp == 64) return launch_join<64, 1, F32, IN_ORDER>(p, grid, ys, st);
+  if (f.dp == 128) return launch_join<128, 1, F32, IN_ORDER>(p, grid, ys, st);
+  return launch_join<256, 1, F32, IN_ORDER>(p, grid, ys, st);
+}
+
 }  // namespace
 }  // namespace paged
 
@@ -201,18 +205,11 @@ cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
   // long segments (many partials each): the warps of a block share a group
   const int groups = f.dp / 16 * f.nt;
   const int ys = segments * 4 < grid ? groups : 1;
-  if (a.c.dtype == DT_F32) {
-    if (f.dp == 64) return launch_join<64, 1, true>(p, grid, ys, st);
-    if (f.dp == 128) return launch_join<128, 1, true>(p, grid, ys, st);
-    return launch_join<256, 1, true>(p, grid, ys, st);
+  switch (a.c.dtype) {
+    case DT_F32: return launch_joins<true, false>(p, f, grid, ys, st);
+    case DT_BF16: return launch_joins<false, true>(p, f, grid, ys, st);
+    default: return launch_joins<false, false>(p, f, grid, ys, st);
   }
-  if (f.dp == 64)
-    return f.nt == 2 ? launch_join<64, 2, false>(p, grid, ys, st)
-                     : launch_join<64, 1, false>(p, grid, ys, st);
-  if (f.dp == 128)
-    return f.nt == 2 ? launch_join<128, 2, false>(p, grid, ys, st)
-                     : launch_join<128, 1, false>(p, grid, ys, st);
-  return launch_join<256, 1, false>(p, grid, ys, st);
 }
 
 }  // namespace coli

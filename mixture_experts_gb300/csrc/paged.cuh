@@ -8,9 +8,11 @@
 // with a running maximum m. Both products are taken transposed, keys and value
 // channels on the MMA's 16 rows and 8 query heads on its columns:
 //   S^T[16 keys][8 heads] = K[16 x D] Q^T,     O^T[D][8 heads] += V^T[D x 16] P^T,
-// so a group of up to 8 heads fills its tile, and the tile of S^T becomes the
-// other product's operand by two 8x8 register transposes. m is only raised
-// when a score passes it by kSlack: one vote a tile instead of a reduction.
+// so a group of up to 8 heads fills its tile, the 16-row operands come out of
+// shared memory in the MMA's own order (ldmatrix, transposed for bf16 values),
+// and the tile of S^T becomes the other product's operand by two 8x8 register
+// transposes. m is only raised when a score passes it by kSlack: one vote a step
+// instead of a reduction.
 //
 // Work split. The tiles of 16 keys of every (sequence, key head, block of
 // heads) lie on one line that is cut into equal pieces, one per block, so
@@ -66,10 +68,11 @@ struct Cfg {
   static constexpr int kFit = kBudget / (kWarps * kSlot);
   // odd, so key and value slots alternate through the ring with one lead
   static constexpr int kRing = kFit >= 7 ? 7 : (kFit >= 5 ? 5 : 3);
+  static constexpr int kQBytes = FMT == DT_F32 ? DP / 8 * 512 : 0;  // fp32 queries in two parts
   static constexpr int kRingBytes = kRing * kWarps * kSlot;
   static constexpr int kMergeBytes = kWarps * kRegs * 128;
   static constexpr int kMain = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
-  static constexpr int kSmem = kMain + kWarps * 8 * NT * 8;
+  static constexpr int kSmem = kMain + kQBytes + kWarps * 8 * NT * 8;
   static_assert(kRing * kWarps * kSlot <= kBudget, "ring does not fit");
   static constexpr int kPart = kRegs * 32 + 16 * NT;   // floats of a partial slot
 };
@@ -89,6 +92,19 @@ COLI_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+// Four 8x8 matrices of 16-bit elements (lane l: the row address of row l % 8 of
+// matrix l / 8) -> lane 4g + t: row g, elements 2t, 2t + 1 of each; or, transposed,
+// elements g of rows 2t, 2t + 1.
+COLI_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+COLI_DEV void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
 }
 // 8x8 transpose of 16-bit elements over the warp (lane 4g + t: row g, columns 2t, 2t + 1).
 COLI_DEV uint32_t transpose8(uint32_t v) {
@@ -165,19 +181,35 @@ COLI_DEV uint32_t lds8(uint32_t addr) {
 
 // Where 16-byte piece c of row r lies in a tile: the piece's place XORed, within
 // its 128 bytes, with a number of the row chosen so that the lanes of one
-// shared-memory phase meet 8 different pieces: rows g = 0..7 when keys are read
-// (lane 4g + t holds 8 elements from 8t on of every 32), rows 2t when values
-// are (8 elements from 8g on of every 64).
+// shared-memory phase meet 8 different pieces. ldmatrix reads one piece of rows
+// 0-7 (or 8-15) at once; the other reads take rows g = 0..7 of MXFP4 keys (lane
+// 4g + t: 4 bytes) and, of values, rows 2t (8 elements from 8g on of every 64).
 template <int FMT, int ROW, bool KEYS>
 COLI_DEV constexpr uint32_t row_xor(int r) {
-  if (KEYS) {
-    if (FMT == DT_F32) return r & 1;
-    if (FMT == DT_BF16) return (r & 1) << 2;
-    if (FMT == DT_MXFP8) return ROW >= 128 ? (r & 3) << 1 : ((r >> 1) & 1) << 1;
-    return ROW >= 128 ? r & 7 : (ROW >= 64 ? (r >> 1) & 3 : (r >> 2) & 1);
-  }
+  if (KEYS || FMT == DT_BF16) return ROW >= 128 ? r & 7 : (ROW >= 64 ? (r >> 1) & 3 : (r >> 2) & 1);
   if (FMT == DT_F32) return ((r >> 1) & 1) | (((r >> 2) & 1) << 2);
   return ROW >= 64 ? r & 6 : ((r >> 2) & 1) << 1;
+}
+// Channel of register c (0-3) of accumulator tile i: bf16 values come transposed
+// in order, the others as pairs out of the lane's 8 elements.
+template <bool IN_ORDER>
+COLI_DEV int channel(int i, int g, int c) {
+  return IN_ORDER ? i * 16 + g + (c >> 1) * 8 : (i >> 2) * 64 + g * 8 + (i & 3) * 2 + (c >> 1);
+}
+// Two outputs (channels of c and c + 2) of one head.
+template <bool IN_ORDER, bool F32>
+COLI_DEV void store_out(const PagedArgs& a, size_t row, int i, int g, float y0, float y1) {
+  const int d = channel<IN_ORDER>(i, g, 0), e = channel<IN_ORDER>(i, g, 2), D = a.c.head_dim;
+  if constexpr (IN_ORDER) {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + row;
+    if (d < D) o[d] = __float2bfloat16_rn(y0);
+    if (e < D) o[e] = __float2bfloat16_rn(y1);
+  } else if (d < D) {
+    if constexpr (F32)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + row + d) = make_float2(y0, y1);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row + d) = pack_bf16x2(y0, y1);
+  }
 }
 template <int FMT, int ROW, bool KEYS>
 COLI_DEV uint32_t piece(int r, int c) {
@@ -189,15 +221,15 @@ COLI_DEV uint32_t further(uint32_t at, uint32_t off) { return (at ^ (off & 127u)
 
 // Starts the copy of one tile's keys or values into a slot (a multiple of 128).
 // Lane l takes the pieces l, l + 32, ... of the tile's memory: `place` is its
-// first piece's place, src its address. Rows outside [r0, r1) and bytes past
-// row_bytes become zeros.
+// first piece's place, src its address. Unless `full`, rows outside [r0, r1) and
+// bytes past row_bytes become zeros.
 template <class C, int FMT, bool KEYS>
-COLI_DEV void copy_tile(uint32_t slot, uint32_t place, const char* src, int row_bytes, int r0,
-                        int r1, int lane) {
+COLI_DEV void copy_tile(uint32_t slot, uint32_t place, const char* src, bool full, int row_bytes,
+                        int r0, int r1, int lane) {
   constexpr int kPieces = C::kRow / 16;
   constexpr int kIters = kTile * kPieces / 32;
   const uint32_t dst = slot + place;
-  if (r0 <= 0 && r1 >= kTile && row_bytes == C::kRow) {
+  if (full) {
 #pragma unroll
     for (int i = 0; i < kIters; ++i)
       cp_async16_n((dst ^ (row_xor<FMT, C::kRow, KEYS>(i * 32 / kPieces) * 16)) + i * 512,
@@ -222,12 +254,6 @@ COLI_DEV void copy_scales(uint32_t dst, const uint8_t* src, int r0, int r1, int 
     const int r = lane / kWords;
     cp_async4_n(dst + lane * 4, src + lane * 4, r >= r0 && r < r1 ? 4 : 0);
   }
-}
-
-// Bytes equal to 0 or 255 in a word of scales (2^-127 and NaN need care).
-COLI_DEV uint32_t odd_scales(uint32_t w) {
-  const uint32_t n = ~w;
-  return (((w - 0x01010101u) & n) | ((n - 0x01010101u) & w)) & 0x80808080u;
 }
 
 // The line of work: tiles of sequence b, in tiles of 16 keys counted from the
@@ -344,26 +370,21 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 
   const int D = a.c.head_dim;
   const uint32_t ring = smem_u32(smem) + w * (C::kRing * C::kSlot);
-  float* s_m = reinterpret_cast<float*>(smem + C::kMain);  // [W][8 NT] maxima, then sums
+  float* s_m = reinterpret_cast<float*>(smem + C::kMain + C::kQBytes);  // [W][8 NT] maxima, sums
   float* s_l = s_m + W * 8 * NT;
+  uint4* s_q = reinterpret_cast<uint4*>(smem + C::kMain) + lane;  // F32: step f at s_q[32 f]
   const float sl = a.scale * 1.4426950408889634f;
   const int tiles_per_page = a.c.page_size / kTile;
-  // bytes of a page, of a head in it and of a tile (all below 2^31)
-  const uint32_t head_bytes = a.c.page_size * a.c.row_bytes;
-  const uint32_t page_bytes = head_bytes * a.c.n_heads, tile_bytes = kTile * a.c.row_bytes;
-  const uint32_t head_scales = a.c.page_size * C::kScaleRow;
-  const uint32_t page_scales = head_scales * a.c.n_heads;
+  const uint32_t tile_bytes = kTile * a.c.row_bytes;
   // this lane's places in a tile: where its copies go, where its reads start
   constexpr int kPieces = C::kRow / 16;
   const uint32_t put_k = piece<FMT, C::kRow, true>(lane / kPieces, lane % kPieces);
   const uint32_t put_v = piece<FMT, C::kRow, false>(lane / kPieces, lane % kPieces);
-  const uint32_t get_k =
-      FMT == DT_BF16    ? piece<FMT, C::kRow, true>(g, t)
-      : FMT == DT_F32   ? piece<FMT, C::kRow, true>(g, t * 2)
-      : FMT == DT_MXFP8 ? piece<FMT, C::kRow, true>(g, t >> 1) + (t & 1) * 8
-                        : piece<FMT, C::kRow, true>(g, 0) + t * 4;
+  // keys: rows l % 8 (+ 8) of ldmatrix's four parts, two pieces; or row g's words
+  const uint32_t get_k = FMT == DT_MXFP4 ? piece<FMT, C::kRow, true>(g, 0) + t * 4
+                                         : piece<FMT, C::kRow, true>(lane & 15, lane >> 4);
   const uint32_t get_v =
-      FMT == DT_BF16    ? piece<FMT, C::kRow, false>(2 * t, g)
+      FMT == DT_BF16    ? piece<FMT, C::kRow, false>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1)
       : FMT == DT_F32   ? piece<FMT, C::kRow, false>(2 * t, g * 2)
       : FMT == DT_MXFP8 ? piece<FMT, C::kRow, false>(2 * t, g >> 1) + (g & 1) * 8
                         : piece<FMT, C::kRow, false>(2 * t, g >> 2) + (g & 3) * 4;
@@ -385,9 +406,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     const int t1 = sq.n - t0 < u1 - u ? sq.n : t0 + static_cast<int>(u1 - u);
     const int h = hr / p.blocks, row0 = (hr - h * p.blocks) * 8 * NT;
 
-    // ---- the queries: lane 4g + t holds elements 32j + 8t .. + 7 of head g --------------
-    uint4 q[NT][kJ];
-    float qf[kF32 ? NT : 1][kF32 ? kJ : 1][8];
+    // ---- the queries, head g's (+ 8 nt) elements in the order of the keys' reads ---------
+    uint4 q[kF32 ? 1 : NT][kJ];
     float xs[NT][2];  // scale of the scores of this lane's columns (heads 2t, 2t + 1)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -395,19 +415,39 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       const size_t at = static_cast<size_t>(b) * a.q_stride +
                         static_cast<size_t>(h * p.group + r) * D;
       xs[nt][0] = xs[nt][1] = sl;
+      if constexpr (kF32) {
+        // in shared memory, once a block: per 8 elements t and t + 4 in two tf32 parts
+        if (w == 0) {
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        const int d = j * 32 + t * 8;
-        const bool in = r < p.group && d < D;
-        if constexpr (kF32) {
-          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + d);
-          const float4 lo = in ? __ldg(src) : make_float4(0, 0, 0, 0);
-          const float4 hi = in ? __ldg(src + 1) : make_float4(0, 0, 0, 0);
-          qf[nt][j][0] = lo.x, qf[nt][j][1] = lo.y, qf[nt][j][2] = lo.z, qf[nt][j][3] = lo.w;
-          qf[nt][j][4] = hi.x, qf[nt][j][5] = hi.y, qf[nt][j][6] = hi.z, qf[nt][j][7] = hi.w;
-        } else {
-          q[nt][j] = in ? ldg_keep(static_cast<const __nv_bfloat16*>(a.q) + at + d)
-                        : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < DP / 8; ++i) {
+            const float* src = static_cast<const float*>(a.q) + at + i * 8 + t;
+            const bool in = r < p.group && i * 8 < D;
+            float hi[2], lo[2];
+            split_tf32(in ? __ldg(src) : 0.f, &hi[0], &lo[0]);
+            split_tf32(in ? __ldg(src + 4) : 0.f, &hi[1], &lo[1]);
+            s_q[32 * i] = make_uint4(__float_as_uint(hi[0]), __float_as_uint(hi[1]),
+                                     __float_as_uint(lo[0]), __float_as_uint(lo[1]));
+          }
+        }
+      } else {
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + at;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          q[nt][j] = make_uint4(0, 0, 0, 0);
+          if (r >= p.group || j * 32 >= D) continue;
+          if constexpr (FMT == DT_BF16) {  // elements 2t, 2t + 1 of every 8
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(src + j * 32) + t;
+            q[nt][j].x = __ldg(u);
+            if (j * 32 + 8 < D) q[nt][j].y = __ldg(u + 4);
+            if (j * 32 + 16 < D) q[nt][j].z = __ldg(u + 8);
+            if (j * 32 + 24 < D) q[nt][j].w = __ldg(u + 12);
+          } else if constexpr (FMT == DT_MXFP8) {  // 4t .. + 3 of every 16
+            const uint2* u = reinterpret_cast<const uint2*>(src + j * 32) + t;
+            const uint2 lo = __ldg(u), hi = __ldg(u + 4);
+            q[nt][j] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          } else {  // 8t .. + 7 of every 32
+            q[nt][j] = ldg_keep(src + j * 32 + t * 8);
+          }
         }
       }
       if constexpr (kMx) {
@@ -455,10 +495,12 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         // (an infinite or NaN query: NaN scores)
         const float down = e > 127 ? __uint_as_float(0x7fc00000u)
                                    : __uint_as_float(static_cast<uint32_t>(e - kTop + 127) << 23);
-        xs[nt][0] = sl * __shfl_sync(0xffffffffu, down, 8 * t);
-        xs[nt][1] = sl * __shfl_sync(0xffffffffu, down, 8 * t + 4);
+        // scales below carry a factor 1 + 2^-23
+        xs[nt][0] = sl * __shfl_sync(0xffffffffu, down, 8 * t) * (1.f - 0x1p-23f);
+        xs[nt][1] = sl * __shfl_sync(0xffffffffu, down, 8 * t + 4) * (1.f - 0x1p-23f);
       }
     }
+    if constexpr (kF32) __syncthreads();
 
     float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
     // MX: acc holds O^T / 2^(ref - 127) of the lane's value block 2v + g/4; bias
@@ -489,20 +531,21 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     const int start = a.window > 0 && sq.len > a.window ? sq.len - a.window : 0;
     const int tile0 = sq.first + t0 + w * S;  // step `it` takes tiles tile0 + it W S ...
     const int key_end = min(sq.len, (sq.first + t1) * kTile);  // keys of this piece end here
-    int page_of = 0, off_of = 0;  // lane S k + i: page, and tile in it, of tile i of step batch + k
+    constexpr uint32_t kNone = 0xffffffffu;
+    uint32_t tile_of = 0;  // lane S k + i: the pool's tile (16 rows) of tile i of step batch + k
     int batch = -32;
-    auto pages = [&](int it) {  // loads the pages of the next 32 / S steps
+    auto pages = [&](int it) {  // looks up the tiles of the next 32 / S steps
       batch = it;
       const int tile = tile0 + (it + lane / S) * (W * S) + lane % S;
-      page_of = -1;
+      tile_of = kNone;
       if (tile * kTile < key_end) {
         const int pi = tile / tiles_per_page;
-        off_of = tile - pi * tiles_per_page;
-        page_of = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
-        if (page_of < 0 || page_of >= a.c.n_pages) {
+        const int page = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
+        if (page < 0 || page >= a.c.n_pages)
           latch_error(a.status, kErrDevice);
-          page_of = -1;
-        }
+        else
+          tile_of = (static_cast<uint32_t>(page) * a.c.n_heads + h) * tiles_per_page +
+                    (tile - pi * tiles_per_page);
       }
     };
     uint32_t fill = ring;  // slot the next copy goes to
@@ -516,27 +559,26 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       __syncwarp();
       if (it < n_it) {
         if (K && it >= batch + 32 / S) pages(it);
+        const char* pool = (K ? a.c.k : a.c.v) + lane * 16;
+        const uint8_t* scales = K ? a.c.k_scale : a.c.v_scale;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-          const int page = __shfl_sync(0xffffffffu, page_of, (it - batch) * S + i);
-          const uint32_t off = __shfl_sync(0xffffffffu, off_of, (it - batch) * S + i);
-          const uint32_t pg = page < 0 ? 0 : page;
+          const uint32_t tile = __shfl_sync(0xffffffffu, tile_of, (it - batch) * S + i);
           const int key = (tile0 + it * (W * S) + i) * kTile;
-          const int r0 = start - key, r1 = page < 0 ? 0 : key_end - key;
-          if (K) {
+          const bool none = tile == kNone;
+          const uint32_t at = none ? 0 : tile;
+          const int r0 = start - key, r1 = none ? 0 : key_end - key;
+          const bool full = r0 <= 0 && r1 >= kTile;
+          if (K && (none || hidden != 0)) {
             const int bit = (it * S + i) & 31;
-            hidden = (hidden & ~(1u << bit)) | (page < 0 ? 1u : 0u) << bit;
+            hidden = (hidden & ~(1u << bit)) | (none ? 1u : 0u) << bit;
           }
-          const uint64_t at = static_cast<uint64_t>(pg) * page_bytes +
-                              (h * head_bytes + (page < 0 ? 0 : off * tile_bytes) + lane * 16);
           copy_tile<C, FMT, K>(fill + i * C::kTileBytes, K ? put_k : put_v,
-                               (K ? a.c.k : a.c.v) + at, a.c.row_bytes, r0, r1, lane);
-          if constexpr (kMx) {
-            const uint64_t sc = static_cast<uint64_t>(pg) * page_scales +
-                                (h * head_scales + (page < 0 ? 0 : off * C::kTileScales));
+                               pool + static_cast<uint64_t>(at) * tile_bytes,
+                               full && a.c.row_bytes == C::kRow, a.c.row_bytes, r0, r1, lane);
+          if constexpr (kMx)
             copy_scales<C>(fill + kScales + i * C::kTileScales,
-                           (K ? a.c.k_scale : a.c.v_scale) + sc, r0, r1, lane);
-          }
+                           scales + static_cast<uint64_t>(at) * C::kTileScales, r0, r1, lane);
         }
       }
       cp_async_commit();
@@ -544,47 +586,6 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     };
     using Keys = std::integral_constant<bool, true>;
     using Values = std::integral_constant<bool, false>;
-    // Scores of 32 elements in three tf32 products (hi hi + hi lo + lo hi). An
-    // infinity times a part that is 0 would be NaN: `careful` leaves such
-    // operands out of the cross products.
-    auto score_f32 = [&](float(&d)[S][NT][4], uint32_t at0, int j, bool careful) {
-      if constexpr (kF32) {
-        float ka[8], kb[8];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t at = further(at0 + get_k, j * 128 + hf * 16);
-          const uint4 va = lds128(at), vb = lds128(at + 8 * C::kRow);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            ka[hf * 4 + i] = __uint_as_float(word_of(va, i));
-            kb[hf * 4 + i] = __uint_as_float(word_of(vb, i));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float hi[4], lo[4];
-          split_tf32(ka[2 * i], &hi[0], &lo[0]);
-          split_tf32(kb[2 * i], &hi[1], &lo[1]);
-          split_tf32(ka[2 * i + 1], &hi[2], &lo[2]);
-          split_tf32(kb[2 * i + 1], &hi[3], &lo[3]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float qh[2], ql[2];
-            split_tf32(qf[nt][j][2 * i], &qh[0], &ql[0]);
-            split_tf32(qf[nt][j][2 * i + 1], &qh[1], &ql[1]);
-            mma_tf32_1688(d[0][nt], hi, qh);
-            if (careful) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) hi[k] = fabsf(hi[k]) == INFINITY ? 0.f : hi[k];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) qh[k] = fabsf(qh[k]) == INFINITY ? 0.f : qh[k];
-            }
-            mma_tf32_1688(d[0][nt], lo, qh);
-            mma_tf32_1688(d[0][nt], hi, ql);
-          }
-        }
-      }
-    };
     constexpr int kLead = (C::kRing - 1) / 2;
 #pragma unroll
     for (int i = 0; i < kLead; ++i) {
@@ -605,84 +606,95 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
 #pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            const uint32_t at = further(tile + get_k, j * 64);
-            const uint4 ka = lds128(at), kb = lds128(at + 8 * C::kRow);
+          for (int j = 0; j < DP / 16; ++j) {
+            uint32_t k4[4];
+            ldsm4(k4, further(tile + get_k, j * 32));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16_16816(x[i][nt], ka.x, kb.x, ka.y, kb.y, q[nt][j].x, q[nt][j].y);
-              mma_bf16_16816(x[i][nt], ka.z, kb.z, ka.w, kb.w, q[nt][j].z, q[nt][j].w);
+              const uint4& u = q[nt][j / 2];
+              mma_bf16_16816(x[i][nt], k4[0], k4[1], k4[2], k4[3], j % 2 ? u.z : u.x,
+                             j % 2 ? u.w : u.y);
             }
           }
         } else if constexpr (kF32) {
+          // Three tf32 products, hi hi + lo hi + hi lo. An infinity times a part that is 0
+          // would be NaN: where a score is NaN it is formed again with such operands left
+          // out of the cross products.
 #pragma unroll 1
           for (int careful = 0; careful < 2; ++careful) {
             bool nan = false;
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
+            for (int j = 0; j < DP / 8; ++j) {
+              uint32_t k4[4];
+              ldsm4(k4, further(tile + get_k, j * 32));
+              const uint4 qv = s_q[32 * j];
+              float hi[4], lo[4];
+              float qh[2] = {__uint_as_float(qv.x), __uint_as_float(qv.y)};
+              const float ql[2] = {__uint_as_float(qv.z), __uint_as_float(qv.w)};
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) score_f32(x, tile, j, careful != 0);
+              for (int k = 0; k < 4; ++k) split_tf32(__uint_as_float(k4[k]), &hi[k], &lo[k]);
+              mma_tf32_1688(d, hi, qh);
+              if (careful) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int k = 0; k < 4; ++k) hi[k] = fabsf(hi[k]) == INFINITY ? 0.f : hi[k];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) nan |= x[i][nt][c] != x[i][nt][c];
+                for (int k = 0; k < 2; ++k) qh[k] = fabsf(qh[k]) == INFINITY ? 0.f : qh[k];
+              }
+              mma_tf32_1688(d, lo, qh);
+              mma_tf32_1688(d, hi, ql);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              x[i][0][c] = d[c];
+              nan |= d[c] != d[c];
+            }
             if (!__any_sync(0xffffffffu, nan)) break;
           }
         } else {
-          // the blocks' scales of keys g and g + 8
-          float f0[kJ], f1[kJ];
+          // The blocks' scales of keys g and g + 8, as fp32 bits with the last bit set: byte
+          // 255 is then NaN by itself (and byte 0, 2^-127, counts as 0). A scale goes on its
+          // block's partial score: codes are exact operands.
           const uint32_t sat = slot + kScales + i * C::kTileScales + g * C::kScaleRow;
-          uint32_t sc0[2], sc1[2], odd = 0;
+          uint32_t sc0[2], sc1[2];
 #pragma unroll
           for (int k = 0; k < C::kScaleRow / 4; ++k) {
             // bytes past the head's blocks may hold anything: 1
             sc0[k] = (lds32(sat + 4 * k) & live[k]) | (0x7f7f7f7fu & ~live[k]);
             sc1[k] = (lds32(sat + 8 * C::kScaleRow + 4 * k) & live[k]) | (0x7f7f7f7fu & ~live[k]);
-            odd |= odd_scales(sc0[k]) | odd_scales(sc1[k]);
           }
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
-            constexpr uint32_t kExp = 0x7f800000u;
             const int up = 23 - 8 * (j % 4);
-            f0[j] = __uint_as_float((up > 0 ? sc0[j / 4] << (up & 31) : sc0[j / 4] >> 1) & kExp);
-            f1[j] = __uint_as_float((up > 0 ? sc1[j / 4] << (up & 31) : sc1[j / 4] >> 1) & kExp);
-          }
-          if (__any_sync(0xffffffffu, odd != 0)) {
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-              f0[j] = e8m0_f32((sc0[j / 4] >> (8 * (j % 4))) & 255u);
-              f1[j] = e8m0_f32((sc1[j / 4] >> (8 * (j % 4))) & 255u);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            uint32_t ka[4], kb[4];
+            const float f0 = __uint_as_float(
+                ((up > 0 ? sc0[j / 4] << (up & 31) : sc0[j / 4] >> 1) & 0x7f800000u) | 1u);
+            const float f1 = __uint_as_float(
+                ((up > 0 ? sc1[j / 4] << (up & 31) : sc1[j / 4] >> 1) & 0x7f800000u) | 1u);
+            uint32_t k4[4], ka[4], kb[4];
             if constexpr (FMT == DT_MXFP8) {
-              const uint32_t at = further(tile + get_k, j * 32);
-              const uint2 va = lds64(at), vb = lds64(at + 8 * C::kRow);
-              ka[0] = va.x, ka[1] = va.y, kb[0] = vb.x, kb[1] = vb.y;
+              ldsm4(k4, further(tile + get_k, j * 32));
             } else {
               const uint32_t at = further(tile + get_k, j * 16);
               e2m1x8_f16(lds32(at), ka);
               e2m1x8_f16(lds32(at + 8 * C::kRow), kb);
             }
-            // the scale goes on the block's partial score: codes are exact operands
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float d[4];
+              const uint4& u = q[nt][j];
               if constexpr (FMT == DT_MXFP8) {
-                mma_e4m3_16832_z(d, ka[0], kb[0], ka[1], kb[1], q[nt][j].z, q[nt][j].w);
+                mma_e4m3_16832_z(d, k4[0], k4[1], k4[2], k4[3], u.z, u.w);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) d[c] *= 0.03125f;
-                mma_e4m3_16832(d, ka[0], kb[0], ka[1], kb[1], q[nt][j].x, q[nt][j].y);
+                mma_e4m3_16832(d, k4[0], k4[1], k4[2], k4[3], u.x, u.y);
               } else {
-                mma_f16_16816_z(d, ka[0], kb[0], ka[1], kb[1], q[nt][j].x, q[nt][j].y);
-                mma_f16_16816(d, ka[2], kb[2], ka[3], kb[3], q[nt][j].z, q[nt][j].w);
+                mma_f16_16816_z(d, ka[0], kb[0], ka[1], kb[1], u.x, u.y);
+                mma_f16_16816(d, ka[2], kb[2], ka[3], kb[3], u.z, u.w);
               }
 #pragma unroll
               for (int c = 0; c < 4; ++c)
-                x[i][nt][c] = j == 0 ? d[c] * (c < 2 ? f0[j] : f1[j])
-                                     : fmaf(d[c], c < 2 ? f0[j] : f1[j], x[i][nt][c]);
+                x[i][nt][c] = j == 0 ? d[c] * (c < 2 ? f0 : f1)
+                                     : fmaf(d[c], c < 2 ? f0 : f1, x[i][nt][c]);
             }
           }
         }
@@ -713,14 +725,18 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         }
       }
       // ---- weights ---------------------------------------------------------------------
-      bool up = false;
-      float top[NT][2];
+      bool up = false, wide = false;  // wide (MX): a weight below 2^-30
+      float top[NT][2], low[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           top[nt][c] = fmaxf(x[0][nt][c], x[0][nt][c + 2]);
-          if constexpr (S == 2) top[nt][c] = fmaxf(top[nt][c], fmaxf(x[1][nt][c], x[1][nt][c + 2]));
+          low[nt][c] = fminf(x[0][nt][c], x[0][nt][c + 2]);
+          if constexpr (S == 2) {
+            top[nt][c] = fmaxf(top[nt][c], fmaxf(x[1][nt][c], x[1][nt][c + 2]));
+            low[nt][c] = fminf(low[nt][c], fminf(x[1][nt][c], x[1][nt][c + 2]));
+          }
           up |= top[nt][c] > m[nt][c] + kSlack;
         }
       if (__any_sync(0xffffffffu, up)) {
@@ -740,7 +756,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             for (int i = 0; i < DP / 16; ++i) acc[i][nt][c] *= f, acc[i][nt][c + 2] *= f;
           }
       }
-      uint32_t least = 0xffffffffu;  // MX: the smallest weight above 0 (its bits less 1)
+      if constexpr (kMx) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          wide |= low[nt][0] < m[nt][0] - (kLift + 16.f) || low[nt][1] < m[nt][1] - (kLift + 16.f);
+      }
 #pragma unroll
       for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -749,7 +769,6 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           for (int c = 0; c < 4; ++c) {
             x[i][nt][c] = ex2(x[i][nt][c] - (m[nt][c & 1] - kLift));
             l[nt][c & 1] += x[i][nt][c];
-            if (kMx) least = min(least, __float_as_uint(x[i][nt][c]) - 1u);
           }
       slot = next(slot);
 
@@ -771,23 +790,13 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         cp_async_wait<C::kRing - 1>();
         __syncwarp();
 #pragma unroll
-        for (int v = 0; v < kV; ++v) {
-          const uint32_t at = slot + get_v;
-          const uint4 r_0 = lds128(further(at, v * 128));
-          const uint4 r_1 = lds128(further(at, v * 128 + C::kRow));
-          const uint4 r_2 = lds128(further(at, v * 128 + C::kRow * 8));
-          const uint4 r_3 = lds128(further(at, v * 128 + C::kRow * 9));
+        for (int i = 0; i < DP / 16; ++i) {
+          uint32_t v4[4];
+          ldsm4_t(v4, further(slot + get_v, i * 32));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t w0 = word_of(r_0, i), w1 = word_of(r_1, i), w2 = word_of(r_2, i),
-                           w3 = word_of(r_3, i);
-            const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
-            const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16_16816(acc[v * 4 + i][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-              mma_bf16_16816(acc[v * 4 + i][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16_16816(acc[i][nt], v4[0], v4[1], v4[2], v4[3], pb[nt][0], pb[nt][1]);
+            mma_bf16_16816(acc[i][nt], v4[0], v4[1], v4[2], v4[3], pl[nt][0], pl[nt][1]);
           }
         }
       } else if constexpr (kF32) {
@@ -882,7 +891,6 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         bad = (bad & 0x80008000u) | hot;
         if (__any_sync(0xffffffffu, bad != 0)) {
           // raise ref where a scale is above its range; is everything in range then?
-          bool wide = false;
           hot = 0;
 #pragma unroll
           for (int v = 0; v < kV; ++v) {
@@ -924,9 +932,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
               sd[i][v][1] = (sv[i][2] + 0x1000) | (sv[i][3] + 0x1000) << 16;
             }
           }
-          if (wide) least = 0;
         }
-        const bool wide = __any_sync(0xffffffffu, least < 0x377fffffu);  // 2^-16
+        wide = __any_sync(0xffffffffu, wide);
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           uint32_t pb[NT][2], pl[NT][2];
@@ -1098,23 +1105,15 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           }
         }
       } else {
-        const int d = (i / 4) * 64 + g * 8 + (i % 4) * 2;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int r = row0 + nt * 8 + 2 * t + c;
           if (r >= p.group) continue;
           const int hq = h * p.group + r;
           const float inv = sum[c] == 0.f ? 0.f : 1.f / sum[c];
-          if (d < D) {
-            const size_t at = static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(hq) * D + d;
-            const float y0 = sum[c] == 0.f ? 0.f : o[c] * inv;
-            const float y1 = sum[c] == 0.f ? 0.f : o[c + 2] * inv;
-            if constexpr (kF32)
-              *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(y0, y1);
-            else
-              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at) =
-                  pack_bf16x2(y0, y1);
-          }
+          store_out<FMT == DT_BF16, kF32>(
+              a, static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(hq) * D, i, g,
+              sum[c] == 0.f ? 0.f : o[c] * inv, sum[c] == 0.f ? 0.f : o[c + 2] * inv);
           if (a.lse != nullptr && i == 0 && g == 0)
             a.lse[static_cast<size_t>(b) * a.n_q_heads + hq] =
                 sum[c] == 0.f ? -INFINITY : (mx[c] + log2f(sum[c])) * 0.6931471805599453f;
