@@ -59,7 +59,7 @@ struct Cfg {
   static constexpr int kStep = kMx && DP <= 128 ? COLI_STEP : 1;
   static constexpr int kTileBytes = kTile * kRow, kTileScales = kTile * kScaleRow;
   // whole 128-byte lines: addresses within a line are XORed
-  static constexpr int kSlot = (kStep * (kTileBytes + kTileScales) + 127) / 128 * 128;
+  static constexpr int kSlot = (kStep * (kTileBytes + 2 * kTileScales) + 127) / 128 * 128;
   static constexpr int kRegs = DP / 16 * 4 * NT;       // O^T registers of a lane
   static constexpr int kWarps = kSlot > 8192 + 256 || NT * DP == 256 && NT == 2 ? 4 : 8;
   static constexpr int kPerSm =
@@ -221,38 +221,28 @@ COLI_DEV uint32_t further(uint32_t at, uint32_t off) { return (at ^ (off & 127u)
 
 // Starts the copy of one tile's keys or values into a slot (a multiple of 128).
 // Lane l takes the pieces l, l + 32, ... of the tile's memory: `place` is its
-// first piece's place, src its address. Unless `full`, rows outside [r0, r1) and
-// bytes past row_bytes become zeros.
+// first piece's place, src its address.
 template <class C, int FMT, bool KEYS>
-COLI_DEV void copy_tile(uint32_t slot, uint32_t place, const char* src, bool full, int row_bytes,
-                        int r0, int r1, int lane) {
+COLI_DEV void copy_tile(uint32_t slot, uint32_t place, const char* src) {
   constexpr int kPieces = C::kRow / 16;
-  constexpr int kIters = kTile * kPieces / 32;
-  const uint32_t dst = slot + place;
-  if (full) {
 #pragma unroll
-    for (int i = 0; i < kIters; ++i)
-      cp_async16_n((dst ^ (row_xor<FMT, C::kRow, KEYS>(i * 32 / kPieces) * 16)) + i * 512,
-                   src + i * 512, 16);
-  } else {
-    const char* tile = src - lane * 16;
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-      const int p = i * 32 + lane, r = p / kPieces, c = p % kPieces;
-      const bool in = r >= r0 && r < r1 && c * 16 < row_bytes;
-      cp_async16_n((dst ^ (row_xor<FMT, C::kRow, KEYS>(i * 32 / kPieces) * 16)) + i * 512,
-                   in ? tile + r * row_bytes + c * 16 : src, in ? 16 : 0);
-    }
-  }
+  for (int i = 0; i < kTile * kPieces / 32; ++i)
+    cp_async16_n(((slot + place) ^ (row_xor<FMT, C::kRow, KEYS>(i * 32 / kPieces) * 16)) + i * 512,
+                 src + i * 512, 16);
 }
 
-// And of its scales, one word a lane.
-template <class C>
-COLI_DEV void copy_scales(uint32_t dst, const uint8_t* src, int r0, int r1, int lane) {
-  constexpr int kWords = C::kScaleRow / 4;
-  if (lane < kTile * kWords) {
-    const int r = lane / kWords;
-    cp_async4_n(dst + lane * 4, src + lane * 4, r >= r0 && r < r1 ? 4 : 0);
+// The same with zeros for rows outside [r0, r1) and bytes past row_bytes.
+template <class C, int FMT, bool KEYS>
+COLI_DEV void copy_part(uint32_t slot, uint32_t place, const char* src, int row_bytes, int r0,
+                        int r1, int lane) {
+  constexpr int kPieces = C::kRow / 16;
+  const char* tile = src - lane * 16;
+#pragma unroll
+  for (int i = 0; i < kTile * kPieces / 32; ++i) {
+    const int p = i * 32 + lane, r = p / kPieces, c = p % kPieces;
+    const bool in = r >= r0 && r < r1 && c * 16 < row_bytes;
+    cp_async16_n(((slot + place) ^ (row_xor<FMT, C::kRow, KEYS>(i * 32 / kPieces) * 16)) + i * 512,
+                 in ? tile + r * row_bytes + c * 16 : src, in ? 16 : 0);
   }
 }
 
@@ -390,6 +380,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
                         : piece<FMT, C::kRow, false>(2 * t, g >> 2) + (g & 3) * 4;
   // MX: of two rows' scale words, the bytes of this lane's blocks 2v + g/4
   const uint32_t pick = (g >> 2) * 0x1111u + 0x6420u;
+  // MX: a lane copies one word of the keys' scales (lanes 0-15) or the values'
+  // (two, of rows of 8 bytes)
+  const uint8_t* scale_src = (lane < 16 ? a.c.k_scale : a.c.v_scale) + (lane & 15) * 4;
   uint32_t live[2];  // the scale bytes of the head's blocks
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -553,32 +546,59 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       s += C::kSlot;
       return s == ring + C::kRing * C::kSlot ? ring : s;
     };
-    uint32_t hidden = 0;  // bit (it S + i) % 32: that tile's page is left out (or past the end)
+    // Both scales of a tile go into its keys' slot: the keys' rows, then the values'.
+    auto copy_scales = [&](int it, int i, uint32_t tile, int r0, int r1) {
+      const uint32_t dst = fill + kScales + i * 2 * C::kTileScales;
+      const uint8_t* src = scale_src + static_cast<uint64_t>(tile) * C::kTileScales;
+      if constexpr (C::kScaleRow == 4) {
+        const int r = lane & 15;
+        cp_async4_n(dst + lane * 4, src, r >= r0 && r < r1 ? 4 : 0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = (lane & 15) / 2 + 8 * e;
+          cp_async4_n(dst + (lane >> 4) * C::kTileScales + (lane & 15) * 4 + e * 64, src + e * 64,
+                      r >= r0 && r < r1 ? 4 : 0);
+        }
+      }
+    };
+    // Steps [whole_a, whole_b) are tiles in sight from end to end; once a page is left
+    // out none is, and bit (it S + i) % 32 of `hidden` says which tiles are.
+    uint32_t hidden = 0;
+    const int key0 = tile0 * kTile;
+    int whole_a = start > key0 ? 1 : 0;
+    int whole_b = a.c.row_bytes == C::kRow && key_end - key0 >= S * kTile
+                      ? (key_end - key0 - S * kTile) / (W * S * kTile) + 1
+                      : 0;
     auto issue = [&](int it, auto keys) {
       constexpr bool K = decltype(keys)::value;
       __syncwarp();
       if (it < n_it) {
         if (K && it >= batch + 32 / S) pages(it);
         const char* pool = (K ? a.c.k : a.c.v) + lane * 16;
-        const uint8_t* scales = K ? a.c.k_scale : a.c.v_scale;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           const uint32_t tile = __shfl_sync(0xffffffffu, tile_of, (it - batch) * S + i);
-          const int key = (tile0 + it * (W * S) + i) * kTile;
-          const bool none = tile == kNone;
-          const uint32_t at = none ? 0 : tile;
-          const int r0 = start - key, r1 = none ? 0 : key_end - key;
-          const bool full = r0 <= 0 && r1 >= kTile;
-          if (K && (none || hidden != 0)) {
-            const int bit = (it * S + i) & 31;
-            hidden = (hidden & ~(1u << bit)) | (none ? 1u : 0u) << bit;
+          if (K && tile == kNone) {
+            if (hidden == 0) whole_b = 0;
+            hidden |= 1u << ((it * S + i) & 31);
+          } else if (K && hidden != 0) {
+            hidden &= ~(1u << ((it * S + i) & 31));
           }
-          copy_tile<C, FMT, K>(fill + i * C::kTileBytes, K ? put_k : put_v,
-                               pool + static_cast<uint64_t>(at) * tile_bytes,
-                               full && a.c.row_bytes == C::kRow, a.c.row_bytes, r0, r1, lane);
-          if constexpr (kMx)
-            copy_scales<C>(fill + kScales + i * C::kTileScales,
-                           scales + static_cast<uint64_t>(at) * C::kTileScales, r0, r1, lane);
+          const uint32_t dst = fill + i * C::kTileBytes;
+          if (it >= whole_a && it < whole_b) {
+            copy_tile<C, FMT, K>(dst, K ? put_k : put_v,
+                                 pool + static_cast<uint64_t>(tile) * tile_bytes);
+            if (K && kMx) copy_scales(it, i, tile, 0, kTile);
+          } else {
+            const uint32_t at = tile == kNone ? 0 : tile;
+            const int key = key0 + (it * (W * S) + i) * kTile;
+            const int r0 = start - key, r1 = tile == kNone ? 0 : key_end - key;
+            copy_part<C, FMT, K>(dst, K ? put_k : put_v,
+                                 pool + static_cast<uint64_t>(at) * tile_bytes, a.c.row_bytes, r0,
+                                 r1, lane);
+            if (K && kMx) copy_scales(it, i, at, r0, r1);
+          }
         }
       }
       cp_async_commit();
@@ -599,6 +619,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       cp_async_wait<C::kRing - 1>();
       __syncwarp();
       float x[S][NT][4];
+      // MX: bytes of the values' scales, of keys 2t, 2t + 1 (+ 8 k) and this lane's blocks
+      uint32_t vs[S][2][2];
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         const uint32_t tile = slot + i * C::kTileBytes;
@@ -655,13 +677,26 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           // The blocks' scales of keys g and g + 8, as fp32 bits with the last bit set: byte
           // 255 is then NaN by itself (and byte 0, 2^-127, counts as 0). A scale goes on its
           // block's partial score: codes are exact operands.
-          const uint32_t sat = slot + kScales + i * C::kTileScales + g * C::kScaleRow;
+          const uint32_t sat = slot + kScales + i * 2 * C::kTileScales + g * C::kScaleRow;
           uint32_t sc0[2], sc1[2];
 #pragma unroll
           for (int k = 0; k < C::kScaleRow / 4; ++k) {
             // bytes past the head's blocks may hold anything: 1
             sc0[k] = (lds32(sat + 4 * k) & live[k]) | (0x7f7f7f7fu & ~live[k]);
             sc1[k] = (lds32(sat + 8 * C::kScaleRow + 4 * k) & live[k]) | (0x7f7f7f7fu & ~live[k]);
+          }
+          // the values' scales too: this slot is filled again before they are needed
+          const uint32_t vat = slot + kScales + (2 * i + 1) * C::kTileScales + 2 * t * C::kScaleRow;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if constexpr (C::kScaleRow == 4) {
+              const uint2 v = lds64(vat + 8 * k * C::kScaleRow);
+              vs[i][k][0] = __byte_perm(v.x, v.y, pick);
+            } else {
+              const uint4 v = lds128(vat + 8 * k * C::kScaleRow);
+              vs[i][k][0] = __byte_perm(v.x, v.z, pick);
+              vs[i][k][1] = __byte_perm(v.y, v.w, pick);
+            }
           }
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
@@ -699,24 +734,25 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           }
         }
       }
-      // rows of this step's tiles in sight
-      int r0[S], r1[S];
-      bool part = false;
+      const bool part = it < whole_a || it >= whole_b;
+      // first and last row of a tile in sight
+      auto rows = [&](int i, int* r0, int* r1) {
+        const int key = key0 + (it * (W * S) + i) * kTile;
+        *r0 = start - key;
+        *r1 = hidden >> ((it * S + i) & 31) & 1u ? 0 : key_end - key;
+      };
 #pragma unroll
-      for (int i = 0; i < S; ++i) {
-        const int key = (tile0 + it * (W * S) + i) * kTile;
-        r0[i] = start - key;
-        r1[i] = hidden >> ((it * S + i) & 31) & 1u ? 0 : key_end - key;
-        part |= r0[i] > 0 || r1[i] < kTile;
+      for (int i = 0; i < S; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) x[i][nt][c] *= xs[nt][c & 1];
-      }
       if (part) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-          const bool in0 = g >= r0[i] && g < r1[i], in1 = g + 8 >= r0[i] && g + 8 < r1[i];
+          int r0, r1;
+          rows(i, &r0, &r1);
+          const bool in0 = g >= r0 && g < r1, in1 = g + 8 >= r0 && g + 8 < r1;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if (!in0) x[i][nt][0] = x[i][nt][1] = -INFINITY;
@@ -857,28 +893,21 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         uint32_t bad = 0;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-          const uint32_t sat = slot + kScales + i * C::kTileScales + 2 * t * C::kScaleRow;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
 #pragma unroll
             for (int e = 0; e < C::kScaleRow / 4; ++e) {
-              uint32_t w0, w1;
-              if constexpr (C::kScaleRow == 4) {
-                const uint2 v = lds64(sat + 8 * k * C::kScaleRow);
-                w0 = v.x, w1 = v.y;
-              } else {
-                w0 = lds32(sat + 8 * k * C::kScaleRow + 4 * e);
-                w1 = lds32(sat + 8 * k * C::kScaleRow + 8 + 4 * e);
-              }
-              const uint32_t by = __byte_perm(w0, w1, pick);
+              const uint32_t by = vs[i][k][e];
               sd[i][2 * e][k] = (by & mine[2 * e]) + bias[2 * e];
               if constexpr (kV > 1)
                 sd[i][2 * e + 1][k] = (by >> 8 & mine[2 * e + 1]) + bias[2 * e + 1];
             }
             if (part) {  // rows out of sight hold zeros, whatever their scale
+              int r0, r1;
+              rows(i, &r0, &r1);
               const int row = 2 * t + 8 * k;
-              const uint32_t lo = row < r0[i] || row >= r1[i] ? 0xffffu : 0u;
-              const uint32_t hi = row + 1 < r0[i] || row + 1 >= r1[i] ? 0xffff0000u : 0u;
+              const uint32_t lo = row < r0 || row >= r1 ? 0xffffu : 0u;
+              const uint32_t hi = row + 1 < r0 || row + 1 >= r1 ? 0xffff0000u : 0u;
 #pragma unroll
               for (int v = 0; v < kV; ++v)
                 sd[i][v][k] = (sd[i][v][k] & ~(lo | hi)) | (0x10001000u & (lo | hi));
@@ -921,8 +950,10 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             for (int i = 0; i < S; ++i) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
+                int r0, r1;
+                rows(i, &r0, &r1);
                 const int row = 2 * t + (k & 1) + (k >> 1) * 8;
-                if (row < r0[i] || row >= r1[i]) sv[i][k] = ref[v];
+                if (row < r0 || row >= r1) sv[i][k] = ref[v];
                 // below 2^-100 of ref nothing is left of a value beside the largest
                 const int e = max(sv[i][k] - ref[v], -100);
                 wide |= e < -14 || sv[i][k] == 255;
@@ -933,95 +964,91 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             }
           }
         }
-        wide = __any_sync(0xffffffffu, wide);
+        auto product = [&](auto way) {
+          constexpr bool kWide = decltype(way)::value;
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-          uint32_t pb[NT][2], pl[NT][2];
-          if (!wide) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              pb[nt][0] = transpose8(pack_f16x2(x[i][nt][0], x[i][nt][1]));
-              pb[nt][1] = transpose8(pack_f16x2(x[i][nt][2], x[i][nt][3]));
-            }
-          } else {
+          for (int i = 0; i < S; ++i) {
+            uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float(&y)[4] = x[i][nt];
-              const uint32_t h0 = pack_bf16x2(y[0], y[1]), h1 = pack_bf16x2(y[2], y[3]);
-              pb[nt][0] = transpose8(h0);
-              pb[nt][1] = transpose8(h1);
-              pl[nt][0] = transpose8(pack_bf16x2(y[0] - bf16_lo(h0), y[1] - bf16_hi(h0)));
-              pl[nt][1] = transpose8(pack_bf16x2(y[2] - bf16_lo(h1), y[3] - bf16_hi(h1)));
-            }
-          }
-          const uint32_t at = slot + i * C::kTileBytes + get_v;
-#pragma unroll
-          for (int v = 0; v < kV; ++v) {
-            uint32_t op[2][8];  // [keys 2t, 2t + 1 or + 8][element]: the two keys' codes in fp16
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t off = v * (C::kBits * 8) + k * 8 * C::kRow;
-              uint32_t h4[4];
-              if constexpr (FMT == DT_MXFP8) {
-                const uint2 e0 = lds64(further(at, off)), e1 = lds64(further(at, off + C::kRow));
-                e4m3x8_f16(__byte_perm(e0.x, e1.x, 0x5140), __byte_perm(e0.x, e1.x, 0x7362), h4);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) op[k][c] = h4[c];
-                e4m3x8_f16(__byte_perm(e0.y, e1.y, 0x5140), __byte_perm(e0.y, e1.y, 0x7362), h4);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) op[k][4 + c] = h4[c];
+              if constexpr (!kWide) {
+                pb[nt][0] = transpose8(pack_f16x2(y[0], y[1]));
+                pb[nt][1] = transpose8(pack_f16x2(y[2], y[3]));
               } else {
-                const uint32_t e0 = lds32(further(at, off)), e1 = lds32(further(at, off + C::kRow));
-                e2m1x8_f16((e0 & 0x0f0f0f0fu) | ((e1 & 0x0f0f0f0fu) << 4), h4);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) op[k][2 * c] = h4[c];
-                e2m1x8_f16(((e0 >> 4) & 0x0f0f0f0fu) | (e1 & 0xf0f0f0f0u), h4);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) op[k][2 * c + 1] = h4[c];
+                const uint32_t h0 = pack_bf16x2(y[0], y[1]), h1 = pack_bf16x2(y[2], y[3]);
+                pb[nt][0] = transpose8(h0);
+                pb[nt][1] = transpose8(h1);
+                pl[nt][0] = transpose8(pack_bf16x2(y[0] - bf16_lo(h0), y[1] - bf16_hi(h0)));
+                pl[nt][1] = transpose8(pack_bf16x2(y[2] - bf16_lo(h1), y[3] - bf16_hi(h1)));
               }
             }
-            if (!wide) {
+            const uint32_t at = slot + i * C::kTileBytes + get_v;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+              uint32_t op[2][8];  // [keys 2t, 2t + 1 or + 8][element]: the two keys' codes in fp16
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint32_t f = (sd[i][v][k] - 0x0ff10ff1u) << 10;  // 2^(s - ref), both keys
+                const uint32_t off = v * (C::kBits * 8) + k * 8 * C::kRow;
+                uint32_t h4[4];
+                if constexpr (FMT == DT_MXFP8) {
+                  const uint2 e0 = lds64(further(at, off)), e1 = lds64(further(at, off + C::kRow));
+                  e4m3x8_f16(__byte_perm(e0.x, e1.x, 0x5140), __byte_perm(e0.x, e1.x, 0x7362), h4);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) op[k][c] = mul_f16x2(op[k][c], f);
-              }
+                  for (int c = 0; c < 4; ++c) op[k][c] = h4[c];
+                  e4m3x8_f16(__byte_perm(e0.y, e1.y, 0x5140), __byte_perm(e0.y, e1.y, 0x7362), h4);
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+                  for (int c = 0; c < 4; ++c) op[k][4 + c] = h4[c];
+                } else {
+                  const uint32_t e0 = lds32(further(at, off)), e1 = lds32(further(at, off + C::kRow));
+                  e2m1x8_f16((e0 & 0x0f0f0f0fu) | ((e1 & 0x0f0f0f0fu) << 4), h4);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma_f16_16816(acc[v * 4 + c][nt], op[0][2 * c], op[0][2 * c + 1], op[1][2 * c],
-                                op[1][2 * c + 1], pb[nt][0], pb[nt][1]);
-            } else {
+                  for (int c = 0; c < 4; ++c) op[k][2 * c] = h4[c];
+                  e2m1x8_f16(((e0 >> 4) & 0x0f0f0f0fu) | (e1 & 0xf0f0f0f0u), h4);
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int e0 = static_cast<int>(sd[i][v][k] & 0xffffu) - 0x1000;
-                const int e1 = static_cast<int>(sd[i][v][k] >> 16) - 0x1000;
-                const float f0 = __uint_as_float(e0 == 255 ? 0x7fc00000u : (e0 + 127u) << 23);
-                const float f1 = __uint_as_float(e1 == 255 ? 0x7fc00000u : (e1 + 127u) << 23);
+                  for (int c = 0; c < 4; ++c) op[k][2 * c + 1] = h4[c];
+                }
+                if constexpr (!kWide) {
+                  const uint32_t f = (sd[i][v][k] - 0x0ff10ff1u) << 10;  // 2^(s - ref), both keys
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  float lo, hi;
-                  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-                      "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-                      : "=f"(lo), "=f"(hi)
-                      : "r"(op[k][c]));
-                  op[k][c] = pack_bf16x2(lo * f0, hi * f1);
+                  for (int c = 0; c < 8; ++c) op[k][c] = mul_f16x2(op[k][c], f);
+                } else {
+                  const int e0 = static_cast<int>(sd[i][v][k] & 0xffffu) - 0x1000;
+                  const int e1 = static_cast<int>(sd[i][v][k] >> 16) - 0x1000;
+                  const float f0 = __uint_as_float(e0 == 255 ? 0x7fc00000u : (e0 + 127u) << 23);
+                  const float f1 = __uint_as_float(e1 == 255 ? 0x7fc00000u : (e1 + 127u) << 23);
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) {
+                    float lo, hi;
+                    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                        "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+                        : "=f"(lo), "=f"(hi)
+                        : "r"(op[k][c]));
+                    op[k][c] = pack_bf16x2(lo * f0, hi * f1);
+                  }
                 }
               }
 #pragma unroll
               for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  mma_bf16_16816(acc[v * 4 + c][nt], op[0][2 * c], op[0][2 * c + 1], op[1][2 * c],
-                                 op[1][2 * c + 1], pb[nt][0], pb[nt][1]);
-                  mma_bf16_16816(acc[v * 4 + c][nt], op[0][2 * c], op[0][2 * c + 1], op[1][2 * c],
-                                 op[1][2 * c + 1], pl[nt][0], pl[nt][1]);
+                  float(&d)[4] = acc[v * 4 + c][nt];
+                  const uint32_t a0 = op[0][2 * c], a1 = op[0][2 * c + 1], a2 = op[1][2 * c],
+                                 a3 = op[1][2 * c + 1];
+                  if constexpr (!kWide) {
+                    mma_f16_16816(d, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                  } else {
+                    mma_bf16_16816(d, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                    mma_bf16_16816(d, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                  }
                 }
             }
           }
-        }
+        };
+        if (__any_sync(0xffffffffu, wide))
+          product(std::integral_constant<bool, true>());
+        else
+          product(std::integral_constant<bool, false>());
       }
       slot = next(slot);
     }
