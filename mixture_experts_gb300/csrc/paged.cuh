@@ -53,17 +53,20 @@ struct Cfg {
   static constexpr int kScaleRow = kMx ? (DP > 128 ? 8 : 4) : 0;
   // Tiles a warp takes in one step: two of an MX cache, whose small tiles leave
   // the step's fixed work (pages, waits, votes) as long as the tile's own.
-#ifndef COLI_STEP
-#define COLI_STEP 2
-#endif
-  static constexpr int kStep = kMx && DP <= 128 ? COLI_STEP : 1;
+  static constexpr int kStep = kMx && DP <= 128 ? 2 : 1;
   static constexpr int kTileBytes = kTile * kRow, kTileScales = kTile * kScaleRow;
   // whole 128-byte lines: addresses within a line are XORed
   static constexpr int kSlot = (kStep * (kTileBytes + 2 * kTileScales) + 127) / 128 * 128;
   static constexpr int kRegs = DP / 16 * 4 * NT;       // O^T registers of a lane
-  static constexpr int kWarps = kSlot > 8192 + 256 || NT * DP == 256 && NT == 2 ? 4 : 8;
-  static constexpr int kPerSm =
-      DP * NT <= 128 && kSlot <= 4096 + 256 ? 2 : (NT == 2 && DP * NT == 256 ? 3 : 1);
+  // Warps of a block and blocks of an SM: what the registers of the widest step allow
+  // without spills (measured for MX heads of 128: 12 warps of 168 registers 210 us,
+  // 16 of 128 with spills 236 us on 64 contexts; 16-head groups 8 warps of 255).
+  static constexpr int kAcc = DP * NT;
+  static constexpr int kWarps = kSlot > 8448 || (kMx && kAcc >= 128 && DP <= 128) || NT * DP == 256 && NT == 2 ? 4 : 8;
+  static constexpr int kPerSm = kMx && DP <= 128 ? (kAcc == 256 ? 2 : (kAcc == 128 ? 3 : 2))
+                                : kAcc <= 128 && kSlot <= 4096 ? 2
+                                : NT == 2 && kAcc == 256       ? 3
+                                                               : 1;
   static constexpr int kBudget = (kPerSm == 3 ? 74 : (kPerSm == 2 ? 112 : 224)) * 1024;
   static constexpr int kFit = kBudget / (kWarps * kSlot);
   // odd, so key and value slots alternate through the ring with one lead
@@ -399,6 +402,123 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     const int t1 = sq.n - t0 < u1 - u ? sq.n : t0 + static_cast<int>(u1 - u);
     const int h = hr / p.blocks, row0 = (hr - h * p.blocks) * 8 * NT;
 
+    float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
+    // MX: acc holds O^T / 2^(ref - 127) of the lane's value block 2v + g/4; bias
+    // is 0x1000 - ref in both halves. Blocks past the head read scale 0 = ref.
+    int ref[kMx ? kV : 1];
+    uint32_t bias[kMx ? kV : 1], mine[kMx ? kV : 1], hot = 0;
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][nt][c] = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -FLT_MAX, l[nt][0] = l[nt][1] = 0.f;
+    if constexpr (kMx) {
+#pragma unroll
+      for (int v = 0; v < kV; ++v) {
+        const bool in = (v * 2 + (g >> 2)) * kMxBlock < D;
+        ref[v] = in ? -1000 : 0;
+        bias[v] = (0x1000 - ref[v]) * 0x10001;
+        mine[v] = in ? 0x00ff00ffu : 0u;
+      }
+    }
+
+    // ---- this warp's steps of kStep tiles ----------------------------------------------
+    constexpr int S = C::kStep, kScales = S * C::kTileBytes;  // scales' place in a slot
+    const int n_it = ((t1 - t0 + S - 1) / S - w + W - 1) / W;  // <= 0: none
+    const int start = a.window > 0 && sq.len > a.window ? sq.len - a.window : 0;
+    const int tile0 = sq.first + t0 + w * S;  // step `it` takes tiles tile0 + it W S ...
+    const int key_end = min(sq.len, (sq.first + t1) * kTile);  // keys of this piece end here
+    constexpr uint32_t kNone = 0xffffffffu;
+    uint32_t tile_of = 0;  // lane S k + i: the pool's tile (16 rows) of tile i of step batch + k
+    int batch = -32;
+    auto pages = [&](int it) {  // looks up the tiles of the next 32 / S steps
+      batch = it;
+      const int tile = tile0 + (it + lane / S) * (W * S) + lane % S;
+      tile_of = kNone;
+      if (tile * kTile < key_end) {
+        const int pi = tile / tiles_per_page;
+        const int page = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
+        if (page < 0 || page >= a.c.n_pages)
+          latch_error(a.status, kErrDevice);
+        else
+          tile_of = (static_cast<uint32_t>(page) * a.c.n_heads + h) * tiles_per_page +
+                    (tile - pi * tiles_per_page);
+      }
+    };
+    uint32_t fill = ring;  // slot the next copy goes to
+    auto next = [&](uint32_t s) {
+      s += C::kSlot;
+      return s == ring + C::kRing * C::kSlot ? ring : s;
+    };
+    // Both scales of a tile go into its keys' slot: the keys' rows, then the values'.
+    auto copy_scales = [&](int it, int i, uint32_t tile, int r0, int r1) {
+      const uint32_t dst = fill + kScales + i * 2 * C::kTileScales;
+      const uint8_t* src = scale_src + static_cast<uint64_t>(tile) * C::kTileScales;
+      if constexpr (C::kScaleRow == 4) {
+        const int r = lane & 15;
+        cp_async4_n(dst + lane * 4, src, r >= r0 && r < r1 ? 4 : 0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = (lane & 15) / 2 + 8 * e;
+          cp_async4_n(dst + (lane >> 4) * C::kTileScales + (lane & 15) * 4 + e * 64, src + e * 64,
+                      r >= r0 && r < r1 ? 4 : 0);
+        }
+      }
+    };
+    // whole_n steps from whole_a on are tiles in sight from end to end; once a page is left
+    // out none is, and bit (it S + i) % 32 of `hidden` says which tiles are.
+    uint32_t hidden = 0;
+    const int key0 = tile0 * kTile;
+    const int whole_a = start > key0 ? 1 : 0;
+    unsigned whole_n = a.c.row_bytes == C::kRow && key_end - key0 >= S * kTile
+                           ? (key_end - key0 - S * kTile) / (W * S * kTile) + 1 - whole_a
+                           : 0;
+    auto issue = [&](int it, auto keys) {
+      constexpr bool K = decltype(keys)::value;
+      __syncwarp();
+      if (it < n_it) {
+        if (K && it >= batch + 32 / S) pages(it);
+        const char* pool = (K ? a.c.k : a.c.v) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const uint32_t tile = __shfl_sync(0xffffffffu, tile_of, (it - batch) * S + i);
+          if (K && tile == kNone) {
+            whole_n = 0;
+            hidden |= 1u << ((it * S + i) & 31);
+          } else if (K && hidden != 0) {
+            hidden &= ~(1u << ((it * S + i) & 31));
+          }
+          const uint32_t dst = fill + i * C::kTileBytes;
+          if (static_cast<unsigned>(it - whole_a) < whole_n) {
+            copy_tile<C, FMT, K>(dst, K ? put_k : put_v,
+                                 pool + static_cast<uint64_t>(tile) * tile_bytes);
+            if (K && kMx) copy_scales(it, i, tile, 0, kTile);
+          } else {
+            const uint32_t at = tile == kNone ? 0 : tile;
+            const int key = key0 + (it * (W * S) + i) * kTile;
+            const int r0 = start - key, r1 = tile == kNone ? 0 : key_end - key;
+            copy_part<C, FMT, K>(dst, K ? put_k : put_v,
+                                 pool + static_cast<uint64_t>(at) * tile_bytes, a.c.row_bytes, r0,
+                                 r1, lane);
+            if (K && kMx) copy_scales(it, i, at, r0, r1);
+          }
+        }
+      }
+      cp_async_commit();
+      fill = next(fill);
+    };
+    using Keys = std::integral_constant<bool, true>;
+    using Values = std::integral_constant<bool, false>;
+    constexpr int kLead = (C::kRing - 1) / 2;
+#pragma unroll
+    for (int i = 0; i < kLead; ++i) {
+      issue(i, Keys());
+      issue(i, Values());
+    }
     // ---- the queries, head g's (+ 8 nt) elements in the order of the keys' reads ---------
     uint4 q[kF32 ? 1 : NT][kJ];
     float xs[NT][2];  // scale of the scores of this lane's columns (heads 2t, 2t + 1)
@@ -495,123 +615,6 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     }
     if constexpr (kF32) __syncthreads();
 
-    float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
-    // MX: acc holds O^T / 2^(ref - 127) of the lane's value block 2v + g/4; bias
-    // is 0x1000 - ref in both halves. Blocks past the head read scale 0 = ref.
-    int ref[kMx ? kV : 1];
-    uint32_t bias[kMx ? kV : 1], mine[kMx ? kV : 1], hot = 0;
-#pragma unroll
-    for (int i = 0; i < DP / 16; ++i)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][nt][c] = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -FLT_MAX, l[nt][0] = l[nt][1] = 0.f;
-    if constexpr (kMx) {
-#pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        const bool in = (v * 2 + (g >> 2)) * kMxBlock < D;
-        ref[v] = in ? -1000 : 0;
-        bias[v] = (0x1000 - ref[v]) * 0x10001;
-        mine[v] = in ? 0x00ff00ffu : 0u;
-      }
-    }
-
-    // ---- this warp's steps of kStep tiles ----------------------------------------------
-    constexpr int S = C::kStep, kScales = S * C::kTileBytes;  // scales' place in a slot
-    const int n_it = ((t1 - t0 + S - 1) / S - w + W - 1) / W;  // <= 0: none
-    const int start = a.window > 0 && sq.len > a.window ? sq.len - a.window : 0;
-    const int tile0 = sq.first + t0 + w * S;  // step `it` takes tiles tile0 + it W S ...
-    const int key_end = min(sq.len, (sq.first + t1) * kTile);  // keys of this piece end here
-    constexpr uint32_t kNone = 0xffffffffu;
-    uint32_t tile_of = 0;  // lane S k + i: the pool's tile (16 rows) of tile i of step batch + k
-    int batch = -32;
-    auto pages = [&](int it) {  // looks up the tiles of the next 32 / S steps
-      batch = it;
-      const int tile = tile0 + (it + lane / S) * (W * S) + lane % S;
-      tile_of = kNone;
-      if (tile * kTile < key_end) {
-        const int pi = tile / tiles_per_page;
-        const int page = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
-        if (page < 0 || page >= a.c.n_pages)
-          latch_error(a.status, kErrDevice);
-        else
-          tile_of = (static_cast<uint32_t>(page) * a.c.n_heads + h) * tiles_per_page +
-                    (tile - pi * tiles_per_page);
-      }
-    };
-    uint32_t fill = ring;  // slot the next copy goes to
-    auto next = [&](uint32_t s) {
-      s += C::kSlot;
-      return s == ring + C::kRing * C::kSlot ? ring : s;
-    };
-    // Both scales of a tile go into its keys' slot: the keys' rows, then the values'.
-    auto copy_scales = [&](int it, int i, uint32_t tile, int r0, int r1) {
-      const uint32_t dst = fill + kScales + i * 2 * C::kTileScales;
-      const uint8_t* src = scale_src + static_cast<uint64_t>(tile) * C::kTileScales;
-      if constexpr (C::kScaleRow == 4) {
-        const int r = lane & 15;
-        cp_async4_n(dst + lane * 4, src, r >= r0 && r < r1 ? 4 : 0);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = (lane & 15) / 2 + 8 * e;
-          cp_async4_n(dst + (lane >> 4) * C::kTileScales + (lane & 15) * 4 + e * 64, src + e * 64,
-                      r >= r0 && r < r1 ? 4 : 0);
-        }
-      }
-    };
-    // Steps [whole_a, whole_b) are tiles in sight from end to end; once a page is left
-    // out none is, and bit (it S + i) % 32 of `hidden` says which tiles are.
-    uint32_t hidden = 0;
-    const int key0 = tile0 * kTile;
-    int whole_a = start > key0 ? 1 : 0;
-    int whole_b = a.c.row_bytes == C::kRow && key_end - key0 >= S * kTile
-                      ? (key_end - key0 - S * kTile) / (W * S * kTile) + 1
-                      : 0;
-    auto issue = [&](int it, auto keys) {
-      constexpr bool K = decltype(keys)::value;
-      __syncwarp();
-      if (it < n_it) {
-        if (K && it >= batch + 32 / S) pages(it);
-        const char* pool = (K ? a.c.k : a.c.v) + lane * 16;
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-          const uint32_t tile = __shfl_sync(0xffffffffu, tile_of, (it - batch) * S + i);
-          if (K && tile == kNone) {
-            if (hidden == 0) whole_b = 0;
-            hidden |= 1u << ((it * S + i) & 31);
-          } else if (K && hidden != 0) {
-            hidden &= ~(1u << ((it * S + i) & 31));
-          }
-          const uint32_t dst = fill + i * C::kTileBytes;
-          if (it >= whole_a && it < whole_b) {
-            copy_tile<C, FMT, K>(dst, K ? put_k : put_v,
-                                 pool + static_cast<uint64_t>(tile) * tile_bytes);
-            if (K && kMx) copy_scales(it, i, tile, 0, kTile);
-          } else {
-            const uint32_t at = tile == kNone ? 0 : tile;
-            const int key = key0 + (it * (W * S) + i) * kTile;
-            const int r0 = start - key, r1 = tile == kNone ? 0 : key_end - key;
-            copy_part<C, FMT, K>(dst, K ? put_k : put_v,
-                                 pool + static_cast<uint64_t>(at) * tile_bytes, a.c.row_bytes, r0,
-                                 r1, lane);
-            if (K && kMx) copy_scales(it, i, at, r0, r1);
-          }
-        }
-      }
-      cp_async_commit();
-      fill = next(fill);
-    };
-    using Keys = std::integral_constant<bool, true>;
-    using Values = std::integral_constant<bool, false>;
-    constexpr int kLead = (C::kRing - 1) / 2;
-#pragma unroll
-    for (int i = 0; i < kLead; ++i) {
-      issue(i, Keys());
-      issue(i, Values());
-    }
     uint32_t slot = ring;
     for (int it = 0; it < n_it; ++it) {
       // ---- scores: lane 4g + t gets keys g, g + 8 of heads 2t, 2t + 1 --------------------
@@ -734,7 +737,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           }
         }
       }
-      const bool part = it < whole_a || it >= whole_b;
+      const bool part = static_cast<unsigned>(it - whole_a) >= whole_n;
       // first and last row of a tile in sight
       auto rows = [&](int i, int* r0, int* r1) {
         const int key = key0 + (it * (W * S) + i) * kTile;
@@ -769,9 +772,10 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         for (int c = 0; c < 2; ++c) {
           top[nt][c] = fmaxf(x[0][nt][c], x[0][nt][c + 2]);
           low[nt][c] = fminf(x[0][nt][c], x[0][nt][c + 2]);
-          if constexpr (S == 2) {
-            top[nt][c] = fmaxf(top[nt][c], fmaxf(x[1][nt][c], x[1][nt][c + 2]));
-            low[nt][c] = fminf(low[nt][c], fminf(x[1][nt][c], x[1][nt][c + 2]));
+#pragma unroll
+          for (int i = 1; i < S; ++i) {
+            top[nt][c] = fmaxf(top[nt][c], fmaxf(x[i][nt][c], x[i][nt][c + 2]));
+            low[nt][c] = fminf(low[nt][c], fminf(x[i][nt][c], x[i][nt][c + 2]));
           }
           up |= top[nt][c] > m[nt][c] + kSlack;
         }
