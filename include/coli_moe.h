@@ -426,7 +426,9 @@ typedef struct {
  * past max_pages pages; a negative length counts as 0; each latches
  * COLI_EDEVICE. Scores, softmax and sums are fp32 throughout. scratch:
  * 16-byte aligned, coli_paged_attention_scratch_bytes(...) bytes, contents
- * irrelevant; calls that may overlap need their own. */
+ * irrelevant; calls that may overlap need their own. It is not used, and may be
+ * NULL, when max_pages * page_size <= COLI_PAGED_DIRECT_TOKENS. */
+#define COLI_PAGED_DIRECT_TOKENS 1024
 size_t coli_paged_attention_scratch_bytes(const coli_kv_cache* cache, int32_t B,
                                           int32_t n_q_heads);
 int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg, const void* q,

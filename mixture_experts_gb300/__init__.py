@@ -24,6 +24,7 @@ STATUS = {0: "COLI_OK", -1: "COLI_EINVAL", -2: "COLI_ENOMEM", -3: "COLI_ECUDA",
 COLI_OK, COLI_EINVAL, COLI_ENOMEM, COLI_ECUDA = 0, -1, -2, -3
 COLI_EUNSUPPORTED, COLI_EDEVICE, COLI_ETIMEOUT = -4, -5, -6
 COLI_PERMUTE_STATIC_SCRATCH_BYTES = 65536
+COLI_PAGED_DIRECT_TOKENS = 1024
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcoli_moe.so")
@@ -578,6 +579,7 @@ class PagedKVCache:
         self.c = coli_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), n_pages, page, hk,
                                head_dim, dtype)
         self._ref = ctypes.byref(self.c)
+        self._calls = {}
 
     @classmethod
     def empty(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=BF16):
@@ -665,14 +667,23 @@ class PagedKVCache:
             raise ValueError(f"block_table: need a contiguous int32 CUDA tensor [{B}][max_pages]")
         lse = torch.empty((B, hq), dtype=torch.float32, device=q.device) if return_lse else None
         L = lib()
-        n = L.coli_paged_attention_scratch_bytes(self._ref, B, hq) if B else 0
-        scratch = torch.empty((n,), dtype=torch.uint8, device=q.device)
-        cfg = coli_attn_config(hq, window, d ** -0.5 if scale is None else scale)
-        rc = L.coli_paged_attention(self._ref, ctypes.byref(cfg), q.data_ptr(), qs, B,
-                                    block_table.data_ptr(), block_table.shape[1],
+        pages = block_table.shape[1]
+        call = self._calls.get((hq, window, scale, B, pages))
+        if call is None:  # the call's settings and scratch size, kept for the next step
+            cfg = coli_attn_config(hq, window, d ** -0.5 if scale is None else scale)
+            n = 0 if B == 0 or pages * self.page_size <= COLI_PAGED_DIRECT_TOKENS else \
+                L.coli_paged_attention_scratch_bytes(self._ref, B, hq)
+            if len(self._calls) >= 64:
+                self._calls.clear()
+            call = self._calls[(hq, window, scale, B, pages)] = (cfg, ctypes.byref(cfg), n)
+        _, cfg_ref, n = call
+        scratch = torch.empty((n,), dtype=torch.uint8, device=q.device) if n else None
+        rc = L.coli_paged_attention(self._ref, cfg_ref, q.data_ptr(), qs, B,
+                                    block_table.data_ptr(), pages,
                                     _ids("seq_lens", seq_lens, B), out.data_ptr(), os_,
-                                    None if lse is None else lse.data_ptr(), scratch.data_ptr(),
-                                    n, _current_stream(q))
+                                    None if lse is None else lse.data_ptr(),
+                                    None if scratch is None else scratch.data_ptr(), n,
+                                    _current_stream(q))
         if rc:
             _check(rc, "coli_paged_attention")
         return (out, lse) if return_lse else out

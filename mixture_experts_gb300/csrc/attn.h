@@ -74,6 +74,7 @@ struct PagedArgs {
   int* status;
 };
 size_t paged_scratch_bytes(const KvView& c, int B, int n_q_heads);
+bool paged_direct(const KvView& c, int max_pages);  // needs no scratch
 cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st);
 
 }  // namespace coli

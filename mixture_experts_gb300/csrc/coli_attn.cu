@@ -271,6 +271,8 @@ int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg
   if (cfg->window < 0) return reject(COLI_EINVAL, "window=%d is negative", cfg->window);
   if (!isfinite(cfg->scale)) return reject(COLI_EINVAL, "scale must be finite");
   if (B == 0) return COLI_OK;
+  if (static_cast<int64_t>(B) * cfg->n_q_heads > INT32_MAX / 2)
+    return reject(COLI_EINVAL, "B=%d sequences of %d heads are too many", B, cfg->n_q_heads);
   const int act = act_of(c);
   if (int rc = check_rows("q", q, q_stride, cfg->n_q_heads, c.head_dim, act)) return rc;
   if (int rc = check_rows("out", out, out_stride, cfg->n_q_heads, c.head_dim, act)) return rc;
@@ -280,7 +282,8 @@ int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg
   if (max_pages < 1 || static_cast<int64_t>(max_pages) * c.page_size > INT32_MAX)
     return reject(COLI_EINVAL, "max_pages=%d: need 1 or more and max_pages * page_size < 2^31",
                   max_pages);
-  const size_t need = paged_scratch_bytes(c, B, cfg->n_q_heads);
+  const size_t need =
+      paged_direct(c, max_pages) ? 0 : paged_scratch_bytes(c, B, cfg->n_q_heads);
   if (scratch_bytes < need || (need > 0 && (scratch == nullptr || misaligned(scratch, 16))))
     return reject(COLI_EINVAL, "scratch: need %zu bytes, 16-byte aligned, got %zu", need,
                   scratch_bytes);

@@ -1,5 +1,6 @@
 // Paged decode attention: choice of the kernel's form, and the join of the
 // segments that block borders cut.
+#include "../../include/coli_moe.h"
 #include "paged_launch.cuh"
 
 namespace coli {
@@ -179,6 +180,10 @@ size_t paged_scratch_bytes(const KvView& c, int B, int n_q_heads) {
   return blocks * (2 * f.part * sizeof(float) + sizeof(int4));
 }
 
+bool paged_direct(const KvView& c, int max_pages) {
+  return static_cast<int64_t>(max_pages) * c.page_size <= COLI_PAGED_DIRECT_TOKENS;
+}
+
 cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
   using namespace paged;
   const Form f = form_of(a.c, a.n_q_heads);
@@ -193,7 +198,15 @@ cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
   const int64_t segments = static_cast<int64_t>(a.B) * a.c.n_heads * f.blocks;
   const int64_t tiles = static_cast<int64_t>(a.max_pages) * (a.c.page_size / kTile);
   const int64_t pieces = (segments * tiles + f.warps - 1) / f.warps;
-  const int grid = pieces < most ? static_cast<int>(pieces) : most;
+  // One block a segment, nothing cut, where the block table holds 1024 tokens at most,
+  // or 2048 and the segments fill the GPU. Direct against cut and joined, us, 32 / 8
+  // heads of 128, bf16: B 1, 300 tokens 6.6 / 9.3, 1000 9.7 / 9.8, 2000 14.4 / 9.8; B 16,
+  // 1000 10.3 / 13.9; B 128, 2000 104 / 117. MXFP4, 64 / 4 heads, B 64, 2000 41.7 / 34.4.
+  p.direct = paged_direct(a.c, a.max_pages) ||
+             (static_cast<int64_t>(a.max_pages) * a.c.page_size <= 2 * COLI_PAGED_DIRECT_TOKENS &&
+              segments >= most);
+  const int grid = p.direct ? static_cast<int>(segments)
+                            : (pieces < most ? static_cast<int>(pieces) : most);
   cudaError_t e;
   switch (a.c.dtype) {
     case DT_F32: e = launch_f32(p, f.dp, f.nt, grid, st); break;
@@ -201,7 +214,7 @@ cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
     case DT_MXFP8: e = launch_mxfp8(p, f.dp, f.nt, grid, st); break;
     default: e = launch_mxfp4(p, f.dp, f.nt, grid, st); break;
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.direct) return e;
   // long segments (many partials each): the warps of a block share a group
   const int groups = f.dp / 16 * f.nt;
   const int ys = segments * 4 < grid ? groups : 1;

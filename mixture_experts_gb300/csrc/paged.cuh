@@ -43,6 +43,7 @@ struct Params {
   int blocks;      // blocks of 8 * NT heads a group is cut into
   float* part;     // partial sums, two slots a block
   int4* span;      // per block: the cut segment that starts in it
+  int direct;      // one block a segment: nothing is cut, nothing joined
 };
 
 template <int FMT, int DP, int NT>
@@ -53,7 +54,7 @@ struct Cfg {
   static constexpr int kScaleRow = kMx ? (DP > 128 ? 8 : 4) : 0;
   // Tiles a warp takes in one step: two of an MX cache, whose small tiles leave
   // the step's fixed work (pages, waits, votes) as long as the tile's own.
-  static constexpr int kStep = kMx && DP <= 128 ? 2 : 1;
+  static constexpr int kStep = kMx && DP <= 128 && DP * NT <= 128 ? 2 : 1;
   static constexpr int kTileBytes = kTile * kRow, kTileScales = kTile * kScaleRow;
   // whole 128-byte lines: addresses within a line are XORed
   static constexpr int kSlot = (kStep * (kTileBytes + 2 * kTileScales) + 127) / 128 * 128;
@@ -63,20 +64,27 @@ struct Cfg {
   // 16 of 128 with spills 236 us on 64 contexts; 16-head groups 8 warps of 255).
   static constexpr int kAcc = DP * NT;
   static constexpr int kWarps = kSlot > 8448 || (kMx && kAcc >= 128 && DP <= 128) || NT * DP == 256 && NT == 2 ? 4 : 8;
-  static constexpr int kPerSm = kMx && DP <= 128 ? (kAcc == 256 ? 2 : (kAcc == 128 ? 3 : 2))
+  static constexpr int kPerSm = kMx && DP <= 128 ? (kAcc >= 128 ? 3 : 2)
                                 : kAcc <= 128 && kSlot <= 4096 ? 2
                                 : NT == 2 && kAcc == 256       ? 3
                                                                : 1;
-  static constexpr int kBudget = (kPerSm == 3 ? 74 : (kPerSm == 2 ? 112 : 224)) * 1024;
+  // Queries in shared memory, 16 bytes a lane: fp32 ones in two parts; those of two
+  // column tiles of MX heads, whose registers are worth more warps
+  static constexpr bool kQShared = FMT == DT_F32 || (kMx && NT == 2);
+  static constexpr int kQBytes = FMT == DT_F32 ? DP / 8 * 512 : (kQShared ? NT * DP / 32 * 512 : 0);
+  // The warps' sums are joined half the registers at a time, beside the rings: the
+  // next segment's copies are in flight meanwhile.
+  static constexpr int kMergeBytes = kWarps * kRegs * 64;
+  static constexpr int kState = kWarps * 8 * NT * 8;  // maxima and sums
+  // shared memory of a block less the system's 1 KB and the static part
+  static constexpr int kBudget = 228 * 1024 / kPerSm - 1280 - kMergeBytes - kQBytes - kState;
   static constexpr int kFit = kBudget / (kWarps * kSlot);
   // odd, so key and value slots alternate through the ring with one lead
   static constexpr int kRing = kFit >= 7 ? 7 : (kFit >= 5 ? 5 : 3);
-  static constexpr int kQBytes = FMT == DT_F32 ? DP / 8 * 512 : 0;  // fp32 queries in two parts
   static constexpr int kRingBytes = kRing * kWarps * kSlot;
-  static constexpr int kMergeBytes = kWarps * kRegs * 128;
-  static constexpr int kMain = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
-  static constexpr int kSmem = kMain + kQBytes + kWarps * 8 * NT * 8;
-  static_assert(kRing * kWarps * kSlot <= kBudget, "ring does not fit");
+  static constexpr int kMain = kRingBytes + kMergeBytes;
+  static constexpr int kSmem = kMain + kQBytes + kState;
+  static_assert(kRingBytes <= kBudget, "ring does not fit");
   static constexpr int kPart = kRegs * 32 + 16 * NT;   // floats of a partial slot
 };
 
@@ -249,6 +257,12 @@ COLI_DEV void copy_part(uint32_t slot, uint32_t place, const char* src, int row_
   }
 }
 
+// a / b, both positive; the line is rarely longer than 32 bits.
+COLI_DEV long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // The line of work: tiles of sequence b, in tiles of 16 keys counted from the
 // context's start.
 struct Seq {
@@ -282,14 +296,22 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   const int lane = lane_id(), w = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
   const int hr_n = a.c.n_heads * p.blocks;  // segments of a sequence
 
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) p.span[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (!p.direct) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 0) p.span[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
 
   // ---- this block's piece of the line --------------------------------------------------
   int b = 0;
   long long before = 0, total = 0;  // tiles before sequence b, tiles in all
   long long u0 = 0, u1 = 0, per = 0;
-  if (a.B <= 32) {  // every warp scans the lengths itself
+  if (p.direct) {
+    b = blockIdx.x / hr_n;
+    const int n = seq_of(a, b, threadIdx.x == 0 && blockIdx.x % hr_n == 0).n;
+    u0 = static_cast<long long>(blockIdx.x - b * hr_n) * n;  // counted from the sequence's start
+    u1 = total = u0 + n;
+    per = n;
+  } else if (a.B <= 32) {  // every warp scans the lengths itself
     const int n = lane < a.B ? seq_of(a, lane, blockIdx.x == 0 && w == 0).n : 0;
     long long s = n;
 #pragma unroll
@@ -298,7 +320,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       if (lane >= i) s += o;
     }
     total = __shfl_sync(0xffffffffu, s, 31) * hr_n;
-    per = (total + gridDim.x - 1) / gridDim.x;
+    per = quotient(total + gridDim.x - 1, gridDim.x);
     per = per < W * C::kStep ? W * C::kStep : per;
     u0 = blockIdx.x * per;
     u1 = u0 + per < total ? u0 + per : total;
@@ -337,7 +359,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       }
       if (pass == 0) {
         total = sum * hr_n;
-        per = (total + gridDim.x - 1) / gridDim.x;
+        per = quotient(total + gridDim.x - 1, gridDim.x);
         per = per < W * C::kStep ? W * C::kStep : per;
         u0 = blockIdx.x * per;
         u1 = u0 + per < total ? u0 + per : total;
@@ -365,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   const uint32_t ring = smem_u32(smem) + w * (C::kRing * C::kSlot);
   float* s_m = reinterpret_cast<float*>(smem + C::kMain + C::kQBytes);  // [W][8 NT] maxima, sums
   float* s_l = s_m + W * 8 * NT;
-  uint4* s_q = reinterpret_cast<uint4*>(smem + C::kMain) + lane;  // F32: step f at s_q[32 f]
+  uint4* s_q = reinterpret_cast<uint4*>(smem + C::kMain) + lane;  // kQShared: piece f at s_q[32 f]
   const float sl = a.scale * 1.4426950408889634f;
   const int tiles_per_page = a.c.page_size / kTile;
   const uint32_t tile_bytes = kTile * a.c.row_bytes;
@@ -395,45 +417,21 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 
   Seq sq = seq_of(a, b, false);
   long long into = u0 - before * hr_n;
-  int hr = static_cast<int>(into / sq.n), t0 = static_cast<int>(into - static_cast<long long>(hr) * sq.n);
+  int hr = static_cast<int>(quotient(into, sq.n)), t0 = static_cast<int>(into - static_cast<long long>(hr) * sq.n);
   long long u = u0;
   bool first_seg = true;
-  while (u < u1) {
-    const int t1 = sq.n - t0 < u1 - u ? sq.n : t0 + static_cast<int>(u1 - u);
-    const int h = hr / p.blocks, row0 = (hr - h * p.blocks) * 8 * NT;
+  // the segment at hand: tiles [t0, t1) of sequence b, key head h, query heads from row0 on
+  int t1 = 0, h = 0, row0 = 0;
+  constexpr int S = C::kStep, kScales = S * C::kTileBytes;  // scales' place in a slot
+  constexpr int kLead = (C::kRing - 1) / 2;
+  constexpr uint32_t kNone = 0xffffffffu;
+  int n_it = 0, start = 0, tile0 = 0, key0 = 0, key_end = 0, batch = 0, whole_a = 0;
+  unsigned whole_n = 0;
+  uint32_t tile_of = 0, hidden = 0, fill = ring;
 
-    float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
-    // MX: acc holds O^T / 2^(ref - 127) of the lane's value block 2v + g/4; bias
-    // is 0x1000 - ref in both halves. Blocks past the head read scale 0 = ref.
-    int ref[kMx ? kV : 1];
-    uint32_t bias[kMx ? kV : 1], mine[kMx ? kV : 1], hot = 0;
-#pragma unroll
-    for (int i = 0; i < DP / 16; ++i)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][nt][c] = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -FLT_MAX, l[nt][0] = l[nt][1] = 0.f;
-    if constexpr (kMx) {
-#pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        const bool in = (v * 2 + (g >> 2)) * kMxBlock < D;
-        ref[v] = in ? -1000 : 0;
-        bias[v] = (0x1000 - ref[v]) * 0x10001;
-        mine[v] = in ? 0x00ff00ffu : 0u;
-      }
-    }
-
-    // ---- this warp's steps of kStep tiles ----------------------------------------------
-    constexpr int S = C::kStep, kScales = S * C::kTileBytes;  // scales' place in a slot
-    const int n_it = ((t1 - t0 + S - 1) / S - w + W - 1) / W;  // <= 0: none
-    const int start = a.window > 0 && sq.len > a.window ? sq.len - a.window : 0;
-    const int tile0 = sq.first + t0 + w * S;  // step `it` takes tiles tile0 + it W S ...
-    const int key_end = min(sq.len, (sq.first + t1) * kTile);  // keys of this piece end here
-    constexpr uint32_t kNone = 0xffffffffu;
-    uint32_t tile_of = 0;  // lane S k + i: the pool's tile (16 rows) of tile i of step batch + k
-    int batch = -32;
+  // ---- a warp's steps of kStep tiles -------------------------------------------------
+  // n_it steps (<= 0: none), step `it` takes the tiles tile0 + it W S ...; keys of the piece
+  // end at key_end. Lane S k + i keeps the pool's tile (16 rows) of tile i of step batch + k.
     auto pages = [&](int it) {  // looks up the tiles of the next 32 / S steps
       batch = it;
       const int tile = tile0 + (it + lane / S) * (W * S) + lane % S;
@@ -448,7 +446,6 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
                     (tile - pi * tiles_per_page);
       }
     };
-    uint32_t fill = ring;  // slot the next copy goes to
     auto next = [&](uint32_t s) {
       s += C::kSlot;
       return s == ring + C::kRing * C::kSlot ? ring : s;
@@ -471,12 +468,6 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     };
     // whole_n steps from whole_a on are tiles in sight from end to end; once a page is left
     // out none is, and bit (it S + i) % 32 of `hidden` says which tiles are.
-    uint32_t hidden = 0;
-    const int key0 = tile0 * kTile;
-    const int whole_a = start > key0 ? 1 : 0;
-    unsigned whole_n = a.c.row_bytes == C::kRow && key_end - key0 >= S * kTile
-                           ? (key_end - key0 - S * kTile) / (W * S * kTile) + 1 - whole_a
-                           : 0;
     auto issue = [&](int it, auto keys) {
       constexpr bool K = decltype(keys)::value;
       __syncwarp();
@@ -513,12 +504,54 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     };
     using Keys = std::integral_constant<bool, true>;
     using Values = std::integral_constant<bool, false>;
-    constexpr int kLead = (C::kRing - 1) / 2;
+    // sets a segment up and starts its first copies
+    auto begin = [&]() {
+      t1 = sq.n - t0 < u1 - u ? sq.n : t0 + static_cast<int>(u1 - u);
+      h = hr / p.blocks;
+      row0 = (hr - h * p.blocks) * 8 * NT;
+      n_it = ((t1 - t0 + S - 1) / S - w + W - 1) / W;
+      start = a.window > 0 && sq.len > a.window ? sq.len - a.window : 0;
+      tile0 = sq.first + t0 + w * S;
+      key0 = tile0 * kTile;
+      key_end = min(sq.len, (sq.first + t1) * kTile);
+      whole_a = start > key0 ? 1 : 0;
+      whole_n = a.c.row_bytes == C::kRow && key_end - key0 >= S * kTile
+                    ? (key_end - key0 - S * kTile) / (W * S * kTile) + 1 - whole_a
+                    : 0;
+      batch = -32;
+      hidden = 0;
+      fill = ring;
 #pragma unroll
-    for (int i = 0; i < kLead; ++i) {
-      issue(i, Keys());
-      issue(i, Values());
+      for (int i = 0; i < kLead; ++i) {
+        issue(i, Keys());
+        issue(i, Values());
+      }
+    };
+    begin();
+  while (true) {
+    float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
+    // MX: acc holds O^T / 2^(ref - 127) of the lane's value block 2v + g/4; bias
+    // is 0x1000 - ref in both halves. Blocks past the head read scale 0 = ref.
+    int ref[kMx ? kV : 1];
+    uint32_t bias[kMx ? kV : 1], mine[kMx ? kV : 1], hot = 0;
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][nt][c] = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -FLT_MAX, l[nt][0] = l[nt][1] = 0.f;
+    if constexpr (kMx) {
+#pragma unroll
+      for (int v = 0; v < kV; ++v) {
+        const bool in = (v * 2 + (g >> 2)) * kMxBlock < D;
+        ref[v] = in ? -1000 : 0;
+        bias[v] = (0x1000 - ref[v]) * 0x10001;
+        mine[v] = in ? 0x00ff00ffu : 0u;
+      }
     }
+
     // ---- the queries, head g's (+ 8 nt) elements in the order of the keys' reads ---------
     uint4 q[kF32 ? 1 : NT][kJ];
     float xs[NT][2];  // scale of the scores of this lane's columns (heads 2t, 2t + 1)
@@ -611,6 +644,12 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         // scales below carry a factor 1 + 2^-23
         xs[nt][0] = sl * __shfl_sync(0xffffffffu, down, 8 * t) * (1.f - 0x1p-23f);
         xs[nt][1] = sl * __shfl_sync(0xffffffffu, down, 8 * t + 4) * (1.f - 0x1p-23f);
+      }
+      if constexpr (kMx && C::kQShared) {
+        // every warp of the block writes the same values, and reads its own
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) s_q[32 * (j * NT + nt)] = q[nt][j];
+        __syncwarp();
       }
     }
     if constexpr (kF32) __syncthreads();
@@ -719,7 +758,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float d[4];
-              const uint4& u = q[nt][j];
+              const uint4 u = C::kQShared ? s_q[32 * (j * NT + nt)] : q[nt][j];
               if constexpr (FMT == DT_MXFP8) {
                 mma_e4m3_16832_z(d, k4[0], k4[1], k4[2], k4[3], u.z, u.w);
 #pragma unroll
@@ -1056,7 +1095,24 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       }
       slot = next(slot);
     }
-    cp_async_wait<0>();
+
+    // ---- the next segment's first copies fly while this one is joined ------------------
+    const int ob = b, ohr = hr, oh = h, orow0 = row0, on = sq.n;
+    const bool whole = t0 == 0 && t1 == sq.n, opens = t0 == 0 && !whole, slot1 = !first_seg;
+    const long long ou = u;
+    u += t1 - t0;
+    first_seg = false;
+    t0 = 0;
+    const bool more = u < u1;
+    if (more) {
+      if (++hr == hr_n) {
+        hr = 0;
+        do {
+          sq = seq_of(a, ++b, false);
+        } while (sq.n == 0);
+      }
+      begin();
+    }
 
     // ---- join the warps ------------------------------------------------------------------
     if constexpr (kMx) {
@@ -1085,7 +1141,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
         for (int c = 0; c < 2; ++c) s_m[w * 8 * NT + nt * 8 + 2 * t + c] = m[nt][c];
     }
-    __syncthreads();  // maxima in place, every ring drained
+    __syncthreads();  // maxima in place
     float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -1101,22 +1157,26 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         for (int i = 0; i < DP / 16; ++i) acc[i][nt][c] *= f, acc[i][nt][c + 2] *= f;
         if (g == 0) s_l[w * 8 * NT + nt * 8 + 2 * t + c] = l[nt][c];
       }
-    float* buf = reinterpret_cast<float*>(smem) + w * C::kRegs * 32 + lane;
+    float* merge = reinterpret_cast<float*>(smem + C::kRingBytes) + lane;
+    float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (slot1 ? 1 : 0)) * C::kPart;
+    constexpr int kHalf = DP / 32 * NT;  // groups (one MMA tile of 16 x 8 each) of half the registers
 #pragma unroll
-    for (int i = 0; i < DP / 16; ++i)
+    for (int rd = 0; rd < 2; ++rd) {
+#pragma unroll
+    for (int i = 0; i < DP / 32; ++i)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) buf[((i * NT + nt) * 4 + c) * 32] = acc[i][nt][c];
+        for (int c = 0; c < 4; ++c)
+          merge[(w * kHalf + i * NT + nt) * 128 + c * 32] = acc[rd * (DP / 32) + i][nt][c];
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == sq.n;
-    float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (first_seg ? 0 : 1)) * C::kPart;
-    // warp w adds the register groups w, w + W, ... (one MMA tile of 16 x 8) of all warps
-    for (int gr = w; gr < DP / 16 * NT; gr += W) {
+    // warp w adds the groups w, w + W, ... of all warps
+    for (int k0 = w; k0 < kHalf; k0 += W) {
+      const int gr = rd * kHalf + k0;
       const int i = gr / NT, nt = gr - i * NT;
       float o[4] = {0.f, 0.f, 0.f, 0.f}, sum[2] = {0.f, 0.f}, mx[2] = {-FLT_MAX, -FLT_MAX};
       for (int k = 0; k < W; ++k) {
-        const float* src = reinterpret_cast<const float*>(smem) + k * C::kRegs * 32 + gr * 128 + lane;
+        const float* src = merge + (k * kHalf + k0) * 128;
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[c] += src[c * 32];
 #pragma unroll
@@ -1138,37 +1198,27 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int r = row0 + nt * 8 + 2 * t + c;
+          const int r = orow0 + nt * 8 + 2 * t + c;
           if (r >= p.group) continue;
-          const int hq = h * p.group + r;
+          const int hq = oh * p.group + r;
           const float inv = sum[c] == 0.f ? 0.f : 1.f / sum[c];
           store_out<FMT == DT_BF16, kF32>(
-              a, static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(hq) * D, i, g,
+              a, static_cast<size_t>(ob) * a.out_stride + static_cast<size_t>(hq) * D, i, g,
               sum[c] == 0.f ? 0.f : o[c] * inv, sum[c] == 0.f ? 0.f : o[c + 2] * inv);
           if (a.lse != nullptr && i == 0 && g == 0)
-            a.lse[static_cast<size_t>(b) * a.n_q_heads + hq] =
+            a.lse[static_cast<size_t>(ob) * a.n_q_heads + hq] =
                 sum[c] == 0.f ? -INFINITY : (mx[c] + log2f(sum[c])) * 0.6931471805599453f;
         }
       }
     }
-    if (t0 == 0 && !whole && threadIdx.x == 0) {
+    __syncthreads();
+    }
+    if (opens && threadIdx.x == 0) {
       // the segment starts here and ends in a later block
-      const long long end = u + sq.n;
-      p.span[blockIdx.x] = make_int4(b, hr, first_seg ? 0 : 1,
-                                     static_cast<int>((end - 1) / per) - blockIdx.x + 1);
+      p.span[blockIdx.x] = make_int4(ob, ohr, slot1 ? 1 : 0,
+                                     static_cast<int>(quotient(ou + on - 1, per)) - blockIdx.x + 1);
     }
-    __syncthreads();  // the buffers become rings again
-
-    // ---- the next segment -----------------------------------------------------------------
-    u += t1 - t0;
-    first_seg = false;
-    t0 = 0;
-    if (u < u1 && ++hr == hr_n) {
-      hr = 0;
-      do {
-        sq = seq_of(a, ++b, false);
-      } while (sq.n == 0);
-    }
+    if (!more) break;
   }
 }
 

@@ -400,6 +400,122 @@ def test_attention_growing_scores(fmt):
     check(got, lse, attn_ref.attend(q, rows["k"], rows["v"], [n] * 3, 1, D ** -0.5), fmt)
 
 
+def one_sequence(fmt, k, v, page=16):
+    """A cache holding k, v [n][heads][D] as one sequence -> (cache, table, lengths, rows)."""
+    n, hk, D = k.shape
+    c = moe.PagedKVCache.empty(-(-n // page) + 1, page, hk, D, FMT[fmt])
+    slots = torch.arange(n).int().cuda() + page          # from page 1 on
+    c.append(k.to(act(fmt)).cuda(), v.to(act(fmt)).cuda(), slots)
+    dec = {s: attn_ref.decode(*stored(c, slots.long(), s), fmt) for s in "kv"}
+    table = (torch.arange(-(-n // page)) + 1).int().cuda()[None]
+    rows = {s: (lambda b, h, s=s: dec[s][:, h]) for s in "kv"}
+    return c, table, torch.tensor([n]).int().cuda(), rows
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("hq", [4, 16])
+def test_attention_values_of_very_different_size(fmt, hq):
+    """Value rows scaled by 2^-40 .. 2^40, in blocks of channels of their own sizes."""
+    g = gen(41, hq)
+    n, D = 700, 64
+    k = torch.randn(n, 1, D, generator=g)
+    v = torch.randn(n, 1, D, generator=g)
+    v = v * torch.exp2(torch.randint(-40, 41, (n, 1, 1), generator=g).float())
+    v[..., 32:] *= 2.0 ** -20
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = randn(g, 1, hq, D, dtype=act(fmt))
+    got, lse = c.attend(q, table, sl, return_lse=True)
+    check(got, lse, attn_ref.attend(q, rows["k"], rows["v"], [n], 1, D ** -0.5), fmt)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("hq", [2, 12])
+def test_attention_large_values_under_tiny_weights(fmt, hq):
+    """The largest values belong to keys of weight 2^-50 and less; the rest decide."""
+    g = gen(43, hq)
+    n, D = 400, 64
+    k = torch.randn(n, 1, D, generator=g) * 0.1
+    v = torch.randn(n, 1, D, generator=g)
+    far = torch.arange(n) % 5 == 0
+    k[far] = -1.0
+    v[far] *= 2.0 ** 30
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = (torch.ones(1, hq, D) * 6.0 + 0.1 * torch.randn(1, hq, D, generator=g)).to(act(fmt)).cuda()
+    got, lse = c.attend(q, table, sl, return_lse=True)
+    check(got, lse, attn_ref.attend(q, rows["k"], rows["v"], [n], 1, D ** -0.5), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_attention_extreme_scales(fmt):
+    """Blocks at the ends of E8M0: keys of 2^100 and 2^-100 against queries of the other
+    size, and values of 2^-120."""
+    g = gen(47)
+    n, D = 100, 64
+    k = torch.randn(n, 1, D, generator=g) * 2.0 ** 100
+    k[::3] *= 2.0 ** -200
+    v = torch.randn(n, 1, D, generator=g) * 2.0 ** -118
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = (torch.randn(1, 4, D, generator=g) * 2.0 ** -101).to(act(fmt)).cuda()
+    got, lse = c.attend(q, table, sl, return_lse=True)
+    check(got, lse, attn_ref.attend(q, rows["k"], rows["v"], [n], 1, D ** -0.5), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_attention_nan_blocks_and_codes(fmt):
+    """A NaN scale, whatever its codes, and an E4M3 NaN code: in a key the head's
+    outputs are NaN, in a value the channels of the block (or the code's own)."""
+    g = gen(53)
+    n, D = 90, 64
+    base = one_sequence(fmt, torch.randn(n, 1, D, generator=g), torch.randn(n, 1, D, generator=g))
+    q = randn(g, 1, 3, D, dtype=torch.bfloat16)
+    c, table, sl, rows = base
+    want, _, tol, _ = attn_ref.attend(q, rows["k"], rows["v"], [n], 1, D ** -0.5)
+    page, off = 1 + 40 // 16, 40 % 16
+    c.v_scale[page, 0, off, 1] = 255                     # channels 32..63 of key 40
+    got = c.attend(q, table, sl)
+    assert got[..., 32:].isnan().all()
+    err = (got.cpu().double() - want).abs()[..., :32]
+    assert (err <= (tol + 2.0 ** -8 * want.abs())[..., :32]).all()
+    c.v_scale[page, 0, off, 1] = 120
+    if fmt == "mxfp8":
+        old = int(c.v[page, 0, off, 5])
+        c.v[page, 0, off, 5] = 0x7f
+        got = c.attend(q, table, sl)
+        assert got[..., 5].isnan().all()
+        keep = torch.arange(D) != 5
+        assert not got[..., keep].isnan().any()
+        c.v[page, 0, off, 5] = old
+        c.k[page, 0, off, 9] = 0xff
+        assert c.attend(q, table, sl).isnan().all()
+        c.k[page, 0, off, 9] = 0
+    c.k_scale[page, 0, off, 0] = 255
+    out, lse = c.attend(q, table, sl, return_lse=True)
+    assert out.isnan().all() and lse.isnan().all()
+    # out of sight it does not matter
+    got = c.attend(q, table, sl, window=90 - 41)
+    assert not got.isnan().any()
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_attention_sequences_share_pages(fmt):
+    """Two sequences with a common prefix in the same pages, different lengths."""
+    g = gen(59)
+    D, page = 64, 16
+    k, v = torch.randn(64, 2, D, generator=g), torch.randn(64, 2, D, generator=g)
+    c = moe.PagedKVCache.empty(5, page, 2, D, FMT[fmt])
+    slots = torch.arange(64).int().cuda()
+    c.append(k.to(act(fmt)).cuda(), v.to(act(fmt)).cuda(), slots)
+    dec = {s: attn_ref.decode(*stored(c, slots.long(), s), fmt) for s in "kv"}
+    table = torch.tensor([[0, 1, 2], [0, 1, 3]]).int().cuda()
+    order = [list(range(48)), list(range(32)) + list(range(48, 64))]
+    lens = [41, 48]
+    q = randn(g, 2, 4, D, dtype=act(fmt))
+    got, lse = c.attend(q, table, torch.tensor(lens).int().cuda(), return_lse=True)
+    ref = attn_ref.attend(q, lambda b, h: dec["k"][order[b], h], lambda b, h: dec["v"][order[b], h],
+                          lens, 2, D ** -0.5)
+    check(got, lse, ref, fmt)
+
+
 @pytest.mark.parametrize("fmt", list(FMT))
 def test_attention_many_ragged_sequences(fmt):
     g = gen(77)
