@@ -137,7 +137,8 @@ void fill(Form* f) {
 template <int FMT>
 void fill_format(Form* f) {
   if constexpr (FMT != DT_F32) {
-    if (f->nt == 2) return f->dp == 64 ? fill<FMT, 64, 2>(f) : fill<FMT, 128, 2>(f);
+    if (f->nt == 2)
+      return f->dp == 64 ? fill<FMT, 64, 2>(f) : (f->dp == 128 ? fill<FMT, 128, 2>(f) : fill<FMT, 256, 2>(f));
   }
   if (f->dp == 64) return fill<FMT, 64, 1>(f);
   if (f->dp == 128) return fill<FMT, 128, 1>(f);
@@ -148,7 +149,7 @@ Form form_of(const KvView& c, int n_q_heads) {
   Form f{};
   const int group = n_q_heads / c.n_heads;
   f.dp = c.head_dim <= 64 ? 64 : (c.head_dim <= 128 ? 128 : 256);
-  f.nt = group <= 8 || f.dp == 256 || c.dtype == DT_F32 ? 1 : 2;
+  f.nt = group <= 8 || c.dtype == DT_F32 ? 1 : 2;
   f.blocks = (group + 8 * f.nt - 1) / (8 * f.nt);
   switch (c.dtype) {
     case DT_F32: fill_format<DT_F32>(&f); break;
@@ -163,8 +164,9 @@ template <bool F32, bool IN_ORDER>
 cudaError_t launch_joins(const Params& p, const Form& f, int grid, int ys, cudaStream_t st) {
   if constexpr (!F32) {
     if (f.nt == 2)
-      return f.dp == 64 ? launch_join<64, 2, F32, IN_ORDER>(p, grid, ys, st)
-                        : launch_join<128, 2, F32, IN_ORDER>(p, grid, ys, st);
+      return f.dp == 64    ? launch_join<64, 2, F32, IN_ORDER>(p, grid, ys, st)
+             : f.dp == 128 ? launch_join<128, 2, F32, IN_ORDER>(p, grid, ys, st)
+                           : launch_join<256, 2, F32, IN_ORDER>(p, grid, ys, st);
   }
   if (f.dp == 64) return launch_join<64, 1, F32, IN_ORDER>(p, grid, ys, st);
   if (f.dp == 128) return launch_join<128, 1, F32, IN_ORDER>(p, grid, ys, st);
@@ -197,7 +199,7 @@ cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
   // no more blocks than pieces of one tile a warp
   const int64_t segments = static_cast<int64_t>(a.B) * a.c.n_heads * f.blocks;
   const int64_t tiles = static_cast<int64_t>(a.max_pages) * (a.c.page_size / kTile);
-  const int64_t pieces = (segments * tiles + f.warps - 1) / f.warps;
+  const int64_t pieces = (segments * (tiles + 8) + f.warps - 1) / f.warps;
   // One block a segment, nothing cut, where the block table holds 1024 tokens at most,
   // or 2048 and the segments fill the GPU. Direct against cut and joined, us, 32 / 8
   // heads of 128, bf16: B 1, 300 tokens 6.6 / 9.3, 1000 9.7 / 9.8, 2000 14.4 / 9.8; B 16,

@@ -15,8 +15,9 @@
 // instead of a reduction.
 //
 // Work split. The tiles of 16 keys of every (sequence, key head, block of
-// heads) lie on one line that is cut into equal pieces, one per block, so
-// ragged lengths load every SM alike. A block that covers a whole segment
+// heads) lie on one line, each such segment behind kOpen empty places for what
+// its start and join cost, and the line is cut into equal pieces, one per block,
+// so ragged lengths load every SM alike and tiny segments do not queue up. A block that covers a whole segment
 // writes its output; a segment cut by block borders leaves partial sums that
 // k_join adds in order of the blocks (no atomics: the same bits every time).
 // Within a block warp w takes tiles w, w + W, ... with its own ring of
@@ -59,18 +60,23 @@ struct Cfg {
   // whole 128-byte lines: addresses within a line are XORed
   static constexpr int kSlot = (kStep * (kTileBytes + 2 * kTileScales) + 127) / 128 * 128;
   static constexpr int kRegs = DP / 16 * 4 * NT;       // O^T registers of a lane
+  static constexpr int kOpen = 8;  // a segment's fixed cost, in tiles (3 us at 2.7 tiles a us)
   // Warps of a block and blocks of an SM: what the registers of the widest step allow
   // without spills (measured for MX heads of 128: 12 warps of 168 registers 210 us,
   // 16 of 128 with spills 236 us on 64 contexts; 16-head groups 8 warps of 255).
   static constexpr int kAcc = DP * NT;
-  static constexpr int kWarps = kSlot > 8448 || (kMx && kAcc >= 128 && DP <= 128) || NT * DP == 256 && NT == 2 ? 4 : 8;
+  static constexpr int kWarps = kAcc == 512 ? (kMx ? 8 : 6)
+                                : kSlot > 8448 || (kMx && kAcc >= 128 && DP <= 128) ||
+                                          (NT == 2 && kAcc == 256)
+                                    ? 4
+                                    : 8;
   static constexpr int kPerSm = kMx && DP <= 128 ? (kAcc >= 128 ? 3 : 2)
                                 : kAcc <= 128 && kSlot <= 4096 ? 2
                                 : NT == 2 && kAcc == 256       ? 3
                                                                : 1;
   // Queries in shared memory, 16 bytes a lane: fp32 ones in two parts; those of two
   // column tiles of MX heads, whose registers are worth more warps
-  static constexpr bool kQShared = FMT == DT_F32 || (kMx && NT == 2);
+  static constexpr bool kQShared = FMT == DT_F32 || (NT == 2 && (kMx || DP == 256));
   static constexpr int kQBytes = FMT == DT_F32 ? DP / 8 * 512 : (kQShared ? NT * DP / 32 * 512 : 0);
   // The warps' sums are joined half the registers at a time, beside the rings: the
   // next segment's copies are in flight meanwhile.
@@ -242,7 +248,21 @@ COLI_DEV void copy_tile(uint32_t slot, uint32_t place, const char* src) {
                  src + i * 512, 16);
 }
 
-// The same with zeros for rows outside [r0, r1) and bytes past row_bytes.
+// The same for rows of row_bytes < kRow bytes, with zeros after them: src is the
+// address of the lane's first piece.
+template <class C, int FMT, bool KEYS>
+COLI_DEV void copy_narrow(uint32_t slot, uint32_t place, const char* src, int row_bytes, int lane) {
+  constexpr int kPieces = C::kRow / 16;
+#pragma unroll
+  for (int i = 0; i < kTile * kPieces / 32; ++i) {
+    const int c = (i * 32 + lane) % kPieces;
+    cp_async16_n(((slot + place) ^ (row_xor<FMT, C::kRow, KEYS>(i * 32 / kPieces) * 16)) + i * 512,
+                 src + (i * 32 / kPieces) * row_bytes + (kPieces > 32 ? i * 32 % kPieces * 16 : 0),
+                 c * 16 < row_bytes ? 16 : 0);
+  }
+}
+
+// And with zeros for rows outside [r0, r1) too; src as for whole rows.
 template <class C, int FMT, bool KEYS>
 COLI_DEV void copy_part(uint32_t slot, uint32_t place, const char* src, int row_bytes, int r0,
                         int r1, int lane) {
@@ -301,18 +321,19 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     if (threadIdx.x == 0) p.span[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
 
+  auto places = [](int n) { return n > 0 ? n + C::kOpen : 0; };  // of a segment of n tiles
   // ---- this block's piece of the line --------------------------------------------------
   int b = 0;
   long long before = 0, total = 0;  // tiles before sequence b, tiles in all
   long long u0 = 0, u1 = 0, per = 0;
   if (p.direct) {
     b = blockIdx.x / hr_n;
-    const int n = seq_of(a, b, threadIdx.x == 0 && blockIdx.x % hr_n == 0).n;
+    const int n = places(seq_of(a, b, threadIdx.x == 0 && blockIdx.x % hr_n == 0).n);
     u0 = static_cast<long long>(blockIdx.x - b * hr_n) * n;  // counted from the sequence's start
     u1 = total = u0 + n;
     per = n;
   } else if (a.B <= 32) {  // every warp scans the lengths itself
-    const int n = lane < a.B ? seq_of(a, lane, blockIdx.x == 0 && w == 0).n : 0;
+    const int n = lane < a.B ? places(seq_of(a, lane, blockIdx.x == 0 && w == 0).n) : 0;
     long long s = n;
 #pragma unroll
     for (int i = 1; i < 32; i <<= 1) {
@@ -333,7 +354,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       long long sum = 0;
       for (int base = 0; base < a.B; base += W * 32) {
         const int i = base + threadIdx.x;
-        const int n = i < a.B ? seq_of(a, i, blockIdx.x == 0 && pass == 0).n : 0;
+        const int n = i < a.B ? places(seq_of(a, i, blockIdx.x == 0 && pass == 0).n) : 0;
         long long s = n;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
@@ -393,6 +414,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   const uint32_t tile_bytes = kTile * a.c.row_bytes;
   // this lane's places in a tile: where its copies go, where its reads start
   constexpr int kPieces = C::kRow / 16;
+  const int narrow = (lane / kPieces) * (a.c.row_bytes - C::kRow);  // where rows are shorter
   const uint32_t put_k = piece<FMT, C::kRow, true>(lane / kPieces, lane % kPieces);
   const uint32_t put_v = piece<FMT, C::kRow, false>(lane / kPieces, lane % kPieces);
   // keys: rows l % 8 (+ 8) of ldmatrix's four parts, two pieces; or row g's words
@@ -417,11 +439,13 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 
   Seq sq = seq_of(a, b, false);
   long long into = u0 - before * hr_n;
-  int hr = static_cast<int>(quotient(into, sq.n)), t0 = static_cast<int>(into - static_cast<long long>(hr) * sq.n);
+  int hr = static_cast<int>(quotient(into, places(sq.n)));
+  // place of the segment at hand where this block starts (tile + kOpen)
+  int x0 = static_cast<int>(into - static_cast<long long>(hr) * places(sq.n));
   long long u = u0;
   bool first_seg = true;
   // the segment at hand: tiles [t0, t1) of sequence b, key head h, query heads from row0 on
-  int t1 = 0, h = 0, row0 = 0;
+  int t0 = 0, t1 = 0, h = 0, row0 = 0;
   constexpr int S = C::kStep, kScales = S * C::kTileBytes;  // scales' place in a slot
   constexpr int kLead = (C::kRing - 1) / 2;
   constexpr uint32_t kNone = 0xffffffffu;
@@ -485,8 +509,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           }
           const uint32_t dst = fill + i * C::kTileBytes;
           if (static_cast<unsigned>(it - whole_a) < whole_n) {
-            copy_tile<C, FMT, K>(dst, K ? put_k : put_v,
-                                 pool + static_cast<uint64_t>(tile) * tile_bytes);
+            const char* src = pool + static_cast<uint64_t>(tile) * tile_bytes;
+            if (a.c.row_bytes == C::kRow)
+              copy_tile<C, FMT, K>(dst, K ? put_k : put_v, src);
+            else
+              copy_narrow<C, FMT, K>(dst, K ? put_k : put_v, src + narrow, a.c.row_bytes, lane);
             if (K && kMx) copy_scales(it, i, tile, 0, kTile);
           } else {
             const uint32_t at = tile == kNone ? 0 : tile;
@@ -506,7 +533,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     using Values = std::integral_constant<bool, false>;
     // sets a segment up and starts its first copies
     auto begin = [&]() {
-      t1 = sq.n - t0 < u1 - u ? sq.n : t0 + static_cast<int>(u1 - u);
+      const int x1 = places(sq.n) - x0 < u1 - u ? places(sq.n) : x0 + static_cast<int>(u1 - u);
+      t0 = max(x0 - C::kOpen, 0);
+      t1 = max(x1 - C::kOpen, 0);
       h = hr / p.blocks;
       row0 = (hr - h * p.blocks) * 8 * NT;
       n_it = ((t1 - t0 + S - 1) / S - w + W - 1) / W;
@@ -515,7 +544,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       key0 = tile0 * kTile;
       key_end = min(sq.len, (sq.first + t1) * kTile);
       whole_a = start > key0 ? 1 : 0;
-      whole_n = a.c.row_bytes == C::kRow && key_end - key0 >= S * kTile
+      whole_n = key_end - key0 >= S * kTile
                     ? (key_end - key0 - S * kTile) / (W * S * kTile) + 1 - whole_a
                     : 0;
       batch = -32;
@@ -527,7 +556,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         issue(i, Values());
       }
     };
-    begin();
+  if (x0 + (u1 - u) <= C::kOpen) return;  // nothing but empty places
+  begin();
   while (true) {
     float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
     // MX: acc holds O^T / 2^(ref - 127) of the lane's value block 2v + g/4; bias
@@ -645,7 +675,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         xs[nt][0] = sl * __shfl_sync(0xffffffffu, down, 8 * t) * (1.f - 0x1p-23f);
         xs[nt][1] = sl * __shfl_sync(0xffffffffu, down, 8 * t + 4) * (1.f - 0x1p-23f);
       }
-      if constexpr (kMx && C::kQShared) {
+      if constexpr (!kF32 && C::kQShared) {
         // every warp of the block writes the same values, and reads its own
 #pragma unroll
         for (int j = 0; j < kJ; ++j) s_q[32 * (j * NT + nt)] = q[nt][j];
@@ -675,7 +705,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             ldsm4(k4, further(tile + get_k, j * 32));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint4& u = q[nt][j / 2];
+              const uint4 u = C::kQShared ? s_q[32 * (j / 2 * NT + nt)] : q[nt][j / 2];
               mma_bf16_16816(x[i][nt], k4[0], k4[1], k4[2], k4[3], j % 2 ? u.z : u.x,
                              j % 2 ? u.w : u.y);
             }
@@ -1099,11 +1129,12 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     // ---- the next segment's first copies fly while this one is joined ------------------
     const int ob = b, ohr = hr, oh = h, orow0 = row0, on = sq.n;
     const bool whole = t0 == 0 && t1 == sq.n, opens = t0 == 0 && !whole, slot1 = !first_seg;
-    const long long ou = u;
-    u += t1 - t0;
+    const long long oend = u - x0 + places(on);  // the segment's end on the line
+    u = oend;
     first_seg = false;
-    t0 = 0;
-    const bool more = u < u1;
+    x0 = 0;
+    // another segment, unless only its empty places are left
+    const bool more = u + C::kOpen < u1;
     if (more) {
       if (++hr == hr_n) {
         hr = 0;
@@ -1216,7 +1247,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     if (opens && threadIdx.x == 0) {
       // the segment starts here and ends in a later block
       p.span[blockIdx.x] = make_int4(ob, ohr, slot1 ? 1 : 0,
-                                     static_cast<int>(quotient(ou + on - 1, per)) - blockIdx.x + 1);
+                                     static_cast<int>(quotient(oend - 1, per)) - blockIdx.x + 1);
     }
     if (!more) break;
   }

@@ -39,6 +39,8 @@ cudaError_t launch_format(const Params& p, int dp, int nt, int grid, cudaStream_
       if (nt == 2) return launch_main<FMT, 128, 2>(p, grid, st);
     return launch_main<FMT, 128, 1>(p, grid, st);
   }
+  if constexpr (FMT != DT_F32)
+    if (nt == 2) return launch_main<FMT, 256, 2>(p, grid, st);
   return launch_main<FMT, 256, 1>(p, grid, st);
 }
 

@@ -517,6 +517,42 @@ def test_attention_sequences_share_pages(fmt):
 
 
 @pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("D", [160, 256])
+@pytest.mark.parametrize("hq", [24, 40])
+def test_attention_wide_heads_in_large_groups(D, hq, fmt):
+    lens = [1500, 0, 33, 400]
+    c, table, sl, rows, g = make_context(fmt, lens, 2, D, 32, seed=D + hq)
+    q = randn(g, 4, hq, D, dtype=act(fmt))
+    got, lse = c.attend(q, table, sl, return_lse=True)
+    check(got, lse, attn_ref.attend(q, rows["k"], rows["v"], lens, 2, D ** -0.5), fmt)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("window", [1, 17, 200])
+def test_attention_small_windows_of_long_contexts(window, fmt):
+    """Many segments of a tile or two beside a few whole ones."""
+    g = gen(61, window)
+    lens = [3000, 1, 0, 2999] + torch.randint(1, 3000, (41,), generator=g).tolist()
+    c, table, sl, rows, g = make_context(fmt, lens, 2, 64, 16, seed=8)
+    q = randn(g, len(lens), 6, 64, dtype=act(fmt))
+    got, lse = c.attend(q, table, sl, window=window, return_lse=True)
+    check(got, lse, attn_ref.attend(q, rows["k"], rows["v"], lens, 2, 0.125, window), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("B", [1, 3, 31, 33, 300])
+def test_attention_batches_past_the_block_table_of_one_launch(B, fmt):
+    """Lengths from 0 to 2500 under a table of more than 1024 tokens, any batch size."""
+    g = gen(67, B)
+    lens = (torch.rand(B, generator=g) ** 4 * 2500).int().tolist()
+    lens[0] = 2500
+    c, table, sl, rows, g = make_context(fmt, lens, 1, 64, 16, seed=B)
+    q = randn(g, B, 4, 64, dtype=act(fmt))
+    got, lse = c.attend(q, table, sl, return_lse=True)
+    check(got, lse, attn_ref.attend(q, rows["k"], rows["v"], lens, 1, 0.125), fmt)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
 def test_attention_many_ragged_sequences(fmt):
     g = gen(77)
     lens = torch.randint(0, 400, (150,), generator=g).tolist()
