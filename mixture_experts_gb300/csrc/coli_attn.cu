@@ -51,7 +51,8 @@ int check_heads(const char* name, int n) {
 
 int check_head_dim(int head_dim) {
   if (head_dim < 8 || head_dim > kMaxHeadDim || head_dim % 8)
-    return reject(COLI_EINVAL, "head_dim=%d is not a multiple of 8 in 8..%d", head_dim, kMaxHeadDim);
+    return reject(COLI_EINVAL, "head_dim=%d is not a multiple of 8 in 8..%d", head_dim,
+                  kMaxHeadDim);
   return COLI_OK;
 }
 

@@ -93,7 +93,8 @@ int read_and_clear_status(cudaStream_t st, char* err, size_t err_len) {
   const int zero = 0;
   CUDA_TRY(cudaMemcpyToSymbol(g_device_status, &zero, sizeof zero));
   if (v == COLI_EDEVICE)
-    return fail(err, err_len, COLI_EDEVICE, "a kernel found an out-of-range expert id or row");
+    return fail(err, err_len, COLI_EDEVICE,
+                "a kernel found an out-of-range id, row, page, slot, length or position");
   if (v == COLI_ETIMEOUT)
     return fail(err, err_len, COLI_ETIMEOUT, "a bounded device-side wait ran out");
   if (v != 0) return fail(err, err_len, COLI_EDEVICE, "device status %d", v);

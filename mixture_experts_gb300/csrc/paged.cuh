@@ -17,12 +17,22 @@
 // Work split. The tiles of 16 keys of every (sequence, key head, block of
 // heads) lie on one line, each such segment behind kOpen empty places for what
 // its start and join cost, and the line is cut into equal pieces, one per block,
-// so ragged lengths load every SM alike and tiny segments do not queue up. A block that covers a whole segment
-// writes its output; a segment cut by block borders leaves partial sums that
-// k_join adds in order of the blocks (no atomics: the same bits every time).
-// Within a block warp w takes tiles w, w + W, ... with its own ring of
-// shared-memory slots filled by cp.async (rows past the context zero-filled),
-// so no warp waits for another before the segment's end.
+// so ragged lengths load every SM alike and tiny segments do not queue up. A
+// block that covers a whole segment writes its output; a segment cut by block
+// borders leaves partial sums that k_join adds in the order of the blocks (no
+// atomics: the same bits every time). Within a block warp w takes steps w, w + W,
+// ... with its own ring of shared-memory slots filled by cp.async (rows past the
+// context zero-filled), so no warp waits for another before the segment's end,
+// and the next segment's first copies fly while the warps' sums are joined.
+//
+// What bounds it (GB300, 32 query and 8 key heads of 128 unless said, against the
+// 6.8 TB/s of a copy): bf16 HBM: 6.9 TB/s on one context of 500009 tokens, 6.05 TB/s
+// on 32 ragged ones (586 MB, 97 us). fp32 HBM (6.6 TB/s, 8 heads, 7 x 26157 tokens).
+// MXFP8 5.5 TB/s on 64 contexts (1168 MB, 211 us): at 16 bytes of cache for every
+// 32 elements it is the ALU pipe (54% busy: widening value codes to fp16, their
+// scales) and instruction issue. MXFP4, 64 query heads on 4: 2.0 TB/s (282 MB,
+// 138 us): issue and latency of the same work at half the bytes and twice the heads.
+
 #pragma once
 
 #include <float.h>
@@ -54,7 +64,8 @@ struct Cfg {
   static constexpr int kRow = DP * kBits / 8;          // bytes of a row in shared memory
   static constexpr int kScaleRow = kMx ? (DP > 128 ? 8 : 4) : 0;
   // Tiles a warp takes in one step: two of an MX cache, whose small tiles leave
-  // the step's fixed work (pages, waits, votes) as long as the tile's own.
+  // the step's fixed work (pages, waits, votes) as long as the tile's own (64 MXFP8
+  // contexts: two 210 us, one 215 us; groups of 16 heads: two spill, 146 against 143 us).
   static constexpr int kStep = kMx && DP <= 128 && DP * NT <= 128 ? 2 : 1;
   static constexpr int kTileBytes = kTile * kRow, kTileScales = kTile * kScaleRow;
   // whole 128-byte lines: addresses within a line are XORed
@@ -62,8 +73,9 @@ struct Cfg {
   static constexpr int kRegs = DP / 16 * 4 * NT;       // O^T registers of a lane
   static constexpr int kOpen = 8;  // a segment's fixed cost, in tiles (3 us at 2.7 tiles a us)
   // Warps of a block and blocks of an SM: what the registers of the widest step allow
-  // without spills (measured for MX heads of 128: 12 warps of 168 registers 210 us,
-  // 16 of 128 with spills 236 us on 64 contexts; 16-head groups 8 warps of 255).
+  // without many spills. MXFP8 heads of 128, 64 contexts: 12 warps of 168 registers
+  // 210 us, 16 of 128 236 us, 8 of 255 262 us; MXFP4 groups of 16 heads, 160 windowed
+  // contexts: 12 warps 143 us, 8 warps 153 us, 16 warps 195 us.
   static constexpr int kAcc = DP * NT;
   static constexpr int kWarps = kAcc == 512 ? (kMx ? 8 : 6)
                                 : kSlot > 8448 || (kMx && kAcc >= 128 && DP <= 128) ||
@@ -225,7 +237,8 @@ COLI_DEV void store_out(const PagedArgs& a, size_t row, int i, int g, float y0, 
     if constexpr (F32)
       *reinterpret_cast<float2*>(static_cast<float*>(a.out) + row + d) = make_float2(y0, y1);
     else
-      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row + d) = pack_bf16x2(y0, y1);
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row + d) =
+          pack_bf16x2(y0, y1);
   }
 }
 template <int FMT, int ROW, bool KEYS>
@@ -249,16 +262,16 @@ COLI_DEV void copy_tile(uint32_t slot, uint32_t place, const char* src) {
 }
 
 // The same for rows of row_bytes < kRow bytes, with zeros after them: src is the
-// address of the lane's first piece.
+// address of the lane's first piece (of its row, where the piece lies past the row).
 template <class C, int FMT, bool KEYS>
 COLI_DEV void copy_narrow(uint32_t slot, uint32_t place, const char* src, int row_bytes, int lane) {
   constexpr int kPieces = C::kRow / 16;
 #pragma unroll
   for (int i = 0; i < kTile * kPieces / 32; ++i) {
-    const int c = (i * 32 + lane) % kPieces;
+    const bool in = (i * 32 + lane) % kPieces * 16 < row_bytes;
+    const int more = kPieces > 32 && in ? i * 32 % kPieces * 16 : 0;
     cp_async16_n(((slot + place) ^ (row_xor<FMT, C::kRow, KEYS>(i * 32 / kPieces) * 16)) + i * 512,
-                 src + (i * 32 / kPieces) * row_bytes + (kPieces > 32 ? i * 32 % kPieces * 16 : 0),
-                 c * 16 < row_bytes ? 16 : 0);
+                 src + (i * 32 / kPieces) * row_bytes + more, in ? 16 : 0);
   }
 }
 
@@ -414,7 +427,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   const uint32_t tile_bytes = kTile * a.c.row_bytes;
   // this lane's places in a tile: where its copies go, where its reads start
   constexpr int kPieces = C::kRow / 16;
-  const int narrow = (lane / kPieces) * (a.c.row_bytes - C::kRow);  // where rows are shorter
+  // where rows are shorter: from lane * 16 to the lane's piece
+  const int narrow = (lane / kPieces) * (a.c.row_bytes - C::kRow) -
+                     (lane % kPieces * 16 < a.c.row_bytes ? 0 : lane % kPieces * 16);
   const uint32_t put_k = piece<FMT, C::kRow, true>(lane / kPieces, lane % kPieces);
   const uint32_t put_v = piece<FMT, C::kRow, false>(lane / kPieces, lane % kPieces);
   // keys: rows l % 8 (+ 8) of ldmatrix's four parts, two pieces; or row g's words
@@ -449,113 +464,114 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   constexpr int S = C::kStep, kScales = S * C::kTileBytes;  // scales' place in a slot
   constexpr int kLead = (C::kRing - 1) / 2;
   constexpr uint32_t kNone = 0xffffffffu;
-  int n_it = 0, start = 0, tile0 = 0, key0 = 0, key_end = 0, batch = 0, whole_a = 0;
+  int n_it = 0, start = 0, tile0 = 0, tile_end = 0, key0 = 0, key_end = 0, batch = 0, whole_a = 0;
   unsigned whole_n = 0;
   uint32_t tile_of = 0, hidden = 0, fill = ring;
 
   // ---- a warp's steps of kStep tiles -------------------------------------------------
   // n_it steps (<= 0: none), step `it` takes the tiles tile0 + it W S ...; keys of the piece
   // end at key_end. Lane S k + i keeps the pool's tile (16 rows) of tile i of step batch + k.
-    auto pages = [&](int it) {  // looks up the tiles of the next 32 / S steps
-      batch = it;
-      const int tile = tile0 + (it + lane / S) * (W * S) + lane % S;
-      tile_of = kNone;
-      if (tile * kTile < key_end) {
-        const int pi = tile / tiles_per_page;
-        const int page = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
-        if (page < 0 || page >= a.c.n_pages)
-          latch_error(a.status, kErrDevice);
-        else
-          tile_of = (static_cast<uint32_t>(page) * a.c.n_heads + h) * tiles_per_page +
-                    (tile - pi * tiles_per_page);
-      }
-    };
-    auto next = [&](uint32_t s) {
-      s += C::kSlot;
-      return s == ring + C::kRing * C::kSlot ? ring : s;
-    };
-    // Both scales of a tile go into its keys' slot: the keys' rows, then the values'.
-    auto copy_scales = [&](int it, int i, uint32_t tile, int r0, int r1) {
-      const uint32_t dst = fill + kScales + i * 2 * C::kTileScales;
-      const uint8_t* src = scale_src + static_cast<uint64_t>(tile) * C::kTileScales;
-      if constexpr (C::kScaleRow == 4) {
-        const int r = lane & 15;
-        cp_async4_n(dst + lane * 4, src, r >= r0 && r < r1 ? 4 : 0);
-      } else {
+  auto pages = [&](int it) {  // looks up the tiles of the next 32 / S steps
+    batch = it;
+    const int tile = tile0 + (it + lane / S) * (W * S) + lane % S;
+    tile_of = kNone;
+    if (tile < tile_end) {
+      const int pi = tile / tiles_per_page;
+      const int page = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
+      if (page < 0 || page >= a.c.n_pages)
+        latch_error(a.status, kErrDevice);
+      else
+        tile_of = (static_cast<uint32_t>(page) * a.c.n_heads + h) * tiles_per_page +
+                  (tile - pi * tiles_per_page);
+    }
+  };
+  auto next = [&](uint32_t s) {
+    s += C::kSlot;
+    return s == ring + C::kRing * C::kSlot ? ring : s;
+  };
+  // Both scales of a tile go into its keys' slot: the keys' rows, then the values'.
+  auto copy_scales = [&](int it, int i, uint32_t tile, int r0, int r1) {
+    const uint32_t dst = fill + kScales + i * 2 * C::kTileScales;
+    const uint8_t* src = scale_src + static_cast<uint64_t>(tile) * C::kTileScales;
+    if constexpr (C::kScaleRow == 4) {
+      const int r = lane & 15;
+      cp_async4_n(dst + lane * 4, src, r >= r0 && r < r1 ? 4 : 0);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = (lane & 15) / 2 + 8 * e;
-          cp_async4_n(dst + (lane >> 4) * C::kTileScales + (lane & 15) * 4 + e * 64, src + e * 64,
-                      r >= r0 && r < r1 ? 4 : 0);
+      for (int e = 0; e < 2; ++e) {
+        const int r = (lane & 15) / 2 + 8 * e;
+        cp_async4_n(dst + (lane >> 4) * C::kTileScales + (lane & 15) * 4 + e * 64, src + e * 64,
+                    r >= r0 && r < r1 ? 4 : 0);
+      }
+    }
+  };
+  // whole_n steps from whole_a on are tiles in sight from end to end; once a page is left
+  // out none is, and bit (it S + i) % 32 of `hidden` says which tiles are.
+  auto issue = [&](int it, auto keys) {
+    constexpr bool K = decltype(keys)::value;
+    __syncwarp();
+    if (it < n_it) {
+      if (K && it >= batch + 32 / S) pages(it);
+      const char* pool = (K ? a.c.k : a.c.v) + lane * 16;
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const uint32_t tile = __shfl_sync(0xffffffffu, tile_of, (it - batch) * S + i);
+        if (K && tile == kNone) {
+          whole_n = 0;
+          hidden |= 1u << ((it * S + i) & 31);
+        } else if (K && hidden != 0) {
+          hidden &= ~(1u << ((it * S + i) & 31));
+        }
+        const uint32_t dst = fill + i * C::kTileBytes;
+        if (static_cast<unsigned>(it - whole_a) < whole_n) {
+          const char* src = pool + static_cast<uint64_t>(tile) * tile_bytes;
+          if (a.c.row_bytes == C::kRow)
+            copy_tile<C, FMT, K>(dst, K ? put_k : put_v, src);
+          else
+            copy_narrow<C, FMT, K>(dst, K ? put_k : put_v, src + narrow, a.c.row_bytes, lane);
+          if (K && kMx) copy_scales(it, i, tile, 0, kTile);
+        } else {
+          const uint32_t at = tile == kNone ? 0 : tile;
+          const int key = key0 + (it * (W * S) + i) * kTile;
+          const int r0 = start - key, r1 = tile == kNone ? 0 : key_end - key;
+          copy_part<C, FMT, K>(dst, K ? put_k : put_v,
+                               pool + static_cast<uint64_t>(at) * tile_bytes, a.c.row_bytes, r0,
+                               r1, lane);
+          if (K && kMx) copy_scales(it, i, at, r0, r1);
         }
       }
-    };
-    // whole_n steps from whole_a on are tiles in sight from end to end; once a page is left
-    // out none is, and bit (it S + i) % 32 of `hidden` says which tiles are.
-    auto issue = [&](int it, auto keys) {
-      constexpr bool K = decltype(keys)::value;
-      __syncwarp();
-      if (it < n_it) {
-        if (K && it >= batch + 32 / S) pages(it);
-        const char* pool = (K ? a.c.k : a.c.v) + lane * 16;
+    }
+    cp_async_commit();
+    fill = next(fill);
+  };
+  using Keys = std::integral_constant<bool, true>;
+  using Values = std::integral_constant<bool, false>;
+  // sets a segment up and starts its first copies
+  auto begin = [&]() {
+    const int x1 = places(sq.n) - x0 < u1 - u ? places(sq.n) : x0 + static_cast<int>(u1 - u);
+    t0 = max(x0 - C::kOpen, 0);
+    t1 = max(x1 - C::kOpen, 0);
+    h = hr / p.blocks;
+    row0 = (hr - h * p.blocks) * 8 * NT;
+    n_it = ((t1 - t0 + S - 1) / S - w + W - 1) / W;
+    start = a.window > 0 && sq.len > a.window ? sq.len - a.window : 0;
+    tile0 = sq.first + t0 + w * S;
+    tile_end = sq.first + t1;
+    key0 = tile0 * kTile;
+    key_end = min(sq.len, (sq.first + t1) * kTile);
+    whole_a = start > key0 ? 1 : 0;
+    whole_n = key_end - key0 >= S * kTile
+                  ? (key_end - key0 - S * kTile) / (W * S * kTile) + 1 - whole_a
+                  : 0;
+    batch = -32;
+    hidden = 0;
+    fill = ring;
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-          const uint32_t tile = __shfl_sync(0xffffffffu, tile_of, (it - batch) * S + i);
-          if (K && tile == kNone) {
-            whole_n = 0;
-            hidden |= 1u << ((it * S + i) & 31);
-          } else if (K && hidden != 0) {
-            hidden &= ~(1u << ((it * S + i) & 31));
-          }
-          const uint32_t dst = fill + i * C::kTileBytes;
-          if (static_cast<unsigned>(it - whole_a) < whole_n) {
-            const char* src = pool + static_cast<uint64_t>(tile) * tile_bytes;
-            if (a.c.row_bytes == C::kRow)
-              copy_tile<C, FMT, K>(dst, K ? put_k : put_v, src);
-            else
-              copy_narrow<C, FMT, K>(dst, K ? put_k : put_v, src + narrow, a.c.row_bytes, lane);
-            if (K && kMx) copy_scales(it, i, tile, 0, kTile);
-          } else {
-            const uint32_t at = tile == kNone ? 0 : tile;
-            const int key = key0 + (it * (W * S) + i) * kTile;
-            const int r0 = start - key, r1 = tile == kNone ? 0 : key_end - key;
-            copy_part<C, FMT, K>(dst, K ? put_k : put_v,
-                                 pool + static_cast<uint64_t>(at) * tile_bytes, a.c.row_bytes, r0,
-                                 r1, lane);
-            if (K && kMx) copy_scales(it, i, at, r0, r1);
-          }
-        }
-      }
-      cp_async_commit();
-      fill = next(fill);
-    };
-    using Keys = std::integral_constant<bool, true>;
-    using Values = std::integral_constant<bool, false>;
-    // sets a segment up and starts its first copies
-    auto begin = [&]() {
-      const int x1 = places(sq.n) - x0 < u1 - u ? places(sq.n) : x0 + static_cast<int>(u1 - u);
-      t0 = max(x0 - C::kOpen, 0);
-      t1 = max(x1 - C::kOpen, 0);
-      h = hr / p.blocks;
-      row0 = (hr - h * p.blocks) * 8 * NT;
-      n_it = ((t1 - t0 + S - 1) / S - w + W - 1) / W;
-      start = a.window > 0 && sq.len > a.window ? sq.len - a.window : 0;
-      tile0 = sq.first + t0 + w * S;
-      key0 = tile0 * kTile;
-      key_end = min(sq.len, (sq.first + t1) * kTile);
-      whole_a = start > key0 ? 1 : 0;
-      whole_n = key_end - key0 >= S * kTile
-                    ? (key_end - key0 - S * kTile) / (W * S * kTile) + 1 - whole_a
-                    : 0;
-      batch = -32;
-      hidden = 0;
-      fill = ring;
-#pragma unroll
-      for (int i = 0; i < kLead; ++i) {
-        issue(i, Keys());
-        issue(i, Values());
-      }
-    };
+    for (int i = 0; i < kLead; ++i) {
+      issue(i, Keys());
+      issue(i, Values());
+    }
+  };
   if (x0 + (u1 - u) <= C::kOpen) return;  // nothing but empty places
   begin();
   while (true) {
@@ -698,7 +714,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         const uint32_t tile = slot + i * C::kTileBytes;
         if constexpr (FMT == DT_BF16) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[i][nt][c] = 0.f;
 #pragma unroll
           for (int j = 0; j < DP / 16; ++j) {
             uint32_t k4[4];
@@ -916,7 +934,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
           for (int k = 0; k < 4; ++k) {      // keys 2t, 2t + 1, 2t + 8, 2t + 9
             const float e0 = __shfl_sync(0xffffffffu, x[0][nt][(k >> 1) * 2], src + (k & 1) * 4);
-            const float e1 = __shfl_sync(0xffffffffu, x[0][nt][(k >> 1) * 2 + 1], src + (k & 1) * 4);
+            const float e1 =
+                __shfl_sync(0xffffffffu, x[0][nt][(k >> 1) * 2 + 1], src + (k & 1) * 4);
             pf[nt][k] = g & 1 ? e1 : e0;
           }
         }
@@ -1073,7 +1092,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
                   for (int c = 0; c < 4; ++c) op[k][4 + c] = h4[c];
                 } else {
-                  const uint32_t e0 = lds32(further(at, off)), e1 = lds32(further(at, off + C::kRow));
+                  const uint32_t e0 = lds32(further(at, off));
+                  const uint32_t e1 = lds32(further(at, off + C::kRow));
                   e2m1x8_f16((e0 & 0x0f0f0f0fu) | ((e1 & 0x0f0f0f0fu) << 4), h4);
 #pragma unroll
                   for (int c = 0; c < 4; ++c) op[k][2 * c] = h4[c];
@@ -1190,59 +1210,59 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       }
     float* merge = reinterpret_cast<float*>(smem + C::kRingBytes) + lane;
     float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (slot1 ? 1 : 0)) * C::kPart;
-    constexpr int kHalf = DP / 32 * NT;  // groups (one MMA tile of 16 x 8 each) of half the registers
+    constexpr int kHalf = DP / 32 * NT;  // groups (MMA tiles of 16 x 8) of half the registers
 #pragma unroll
     for (int rd = 0; rd < 2; ++rd) {
 #pragma unroll
-    for (int i = 0; i < DP / 32; ++i)
+      for (int i = 0; i < DP / 32; ++i)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          merge[(w * kHalf + i * NT + nt) * 128 + c * 32] = acc[rd * (DP / 32) + i][nt][c];
-    __syncthreads();
-    // warp w adds the groups w, w + W, ... of all warps
-    for (int k0 = w; k0 < kHalf; k0 += W) {
-      const int gr = rd * kHalf + k0;
-      const int i = gr / NT, nt = gr - i * NT;
-      float o[4] = {0.f, 0.f, 0.f, 0.f}, sum[2] = {0.f, 0.f}, mx[2] = {-FLT_MAX, -FLT_MAX};
-      for (int k = 0; k < W; ++k) {
-        const float* src = merge + (k * kHalf + k0) * 128;
+          for (int c = 0; c < 4; ++c)
+            merge[(w * kHalf + i * NT + nt) * 128 + c * 32] = acc[rd * (DP / 32) + i][nt][c];
+      __syncthreads();
+      // warp w adds the groups w, w + W, ... of all warps
+      for (int k0 = w; k0 < kHalf; k0 += W) {
+        const int gr = rd * kHalf + k0;
+        const int i = gr / NT, nt = gr - i * NT;
+        float o[4] = {0.f, 0.f, 0.f, 0.f}, sum[2] = {0.f, 0.f}, mx[2] = {-FLT_MAX, -FLT_MAX};
+        for (int k = 0; k < W; ++k) {
+          const float* src = merge + (k * kHalf + k0) * 128;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] += src[c * 32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          sum[c] += s_l[k * 8 * NT + nt * 8 + 2 * t + c];
-          mx[c] = fmaxf(mx[c], s_m[k * 8 * NT + nt * 8 + 2 * t + c]);
-        }
-      }
-      if (!whole) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) part[gr * 128 + c * 32 + lane] = o[c];
-        if (i == 0 && g == 0) {
+          for (int c = 0; c < 4; ++c) o[c] += src[c * 32];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            part[C::kRegs * 32 + nt * 8 + 2 * t + c] = mx[c];
-            part[C::kRegs * 32 + 8 * NT + nt * 8 + 2 * t + c] = sum[c];
+            sum[c] += s_l[k * 8 * NT + nt * 8 + 2 * t + c];
+            mx[c] = fmaxf(mx[c], s_m[k * 8 * NT + nt * 8 + 2 * t + c]);
           }
         }
-      } else {
+        if (!whole) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int r = orow0 + nt * 8 + 2 * t + c;
-          if (r >= p.group) continue;
-          const int hq = oh * p.group + r;
-          const float inv = sum[c] == 0.f ? 0.f : 1.f / sum[c];
-          store_out<FMT == DT_BF16, kF32>(
-              a, static_cast<size_t>(ob) * a.out_stride + static_cast<size_t>(hq) * D, i, g,
-              sum[c] == 0.f ? 0.f : o[c] * inv, sum[c] == 0.f ? 0.f : o[c + 2] * inv);
-          if (a.lse != nullptr && i == 0 && g == 0)
-            a.lse[static_cast<size_t>(ob) * a.n_q_heads + hq] =
-                sum[c] == 0.f ? -INFINITY : (mx[c] + log2f(sum[c])) * 0.6931471805599453f;
+          for (int c = 0; c < 4; ++c) part[gr * 128 + c * 32 + lane] = o[c];
+          if (i == 0 && g == 0) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              part[C::kRegs * 32 + nt * 8 + 2 * t + c] = mx[c];
+              part[C::kRegs * 32 + 8 * NT + nt * 8 + 2 * t + c] = sum[c];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int r = orow0 + nt * 8 + 2 * t + c;
+            if (r >= p.group) continue;
+            const int hq = oh * p.group + r;
+            const float inv = sum[c] == 0.f ? 0.f : 1.f / sum[c];
+            store_out<FMT == DT_BF16, kF32>(
+                a, static_cast<size_t>(ob) * a.out_stride + static_cast<size_t>(hq) * D, i, g,
+                sum[c] == 0.f ? 0.f : o[c] * inv, sum[c] == 0.f ? 0.f : o[c + 2] * inv);
+            if (a.lse != nullptr && i == 0 && g == 0)
+              a.lse[static_cast<size_t>(ob) * a.n_q_heads + hq] =
+                  sum[c] == 0.f ? -INFINITY : (mx[c] + log2f(sum[c])) * 0.6931471805599453f;
+          }
         }
       }
-    }
-    __syncthreads();
+      __syncthreads();
     }
     if (opens && threadIdx.x == 0) {
       // the segment starts here and ends in a later block

@@ -131,7 +131,8 @@ def test_read_rejects():
 
 @pytest.mark.parametrize("kw,word", [
     (dict(B=-1), "B="), (dict(B=65536), "B="), (dict(q=None), "q must"),
-    (dict(q_stride=128), "stride"), (dict(out=FAKE), "must not be q"), (dict(out=FAKE + 4), "aligned"),
+    (dict(q_stride=128), "stride"), (dict(out=FAKE), "must not be q"),
+    (dict(out=FAKE + 4), "aligned"),
     (dict(block_table=None), "block_table"), (dict(seq_lens=None), "seq_lens"),
     (dict(max_pages=0), "max_pages"), (dict(max_pages=1 << 27), "max_pages"),
     (dict(cfg=moe.coli_attn_config(3, 0, 1.0)), "multiple"),

@@ -748,6 +748,37 @@ def test_other_stream_and_graph(fmt):
     assert torch.equal(out, want2)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_graph_of_a_cut_context(fmt):
+    """A captured call whose contexts are cut and joined (two kernels), replayed
+    after its lengths and queries changed, beside calls on another stream."""
+    lens = [5000, 0, 70, 3000]
+    c, table, sl, rows, g = make_context(fmt, lens, 2, 128, 16, seed=19)
+    q, q2 = (randn(g, 4, 8, 128, dtype=torch.bfloat16) for _ in range(2))
+    sl2 = torch.tensor([4000, 0, 16, 1]).int().cuda()
+    want, want2 = c.attend(q, table, sl), c.attend(q2, table, sl2)
+    side = torch.cuda.Stream()
+    x, n = q.clone(), sl.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c.attend(x, table, n)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = c.attend(x, table, n)
+    torch.cuda.current_stream().wait_stream(side)
+    side.wait_stream(torch.cuda.current_stream())
+    graph.replay()
+    others = [c.attend(q2, table, sl2, stream=side) for _ in range(5)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert all(torch.equal(o, want2) for o in others)
+    x.copy_(q2)
+    n.copy_(sl2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want2)
+
+
 def test_empty_calls():
     c = moe.PagedKVCache.empty(2, 16, 2, 64, moe.BF16)
     z = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
