@@ -2,8 +2,11 @@
 // type. One thread writes the same 16 bytes of the key and the value row (from
 // 16, 8 or 4 stored ones each) for up to four tokens, whose loads it has in
 // flight together; its head and place in the row stay the same over them. HBM
-// bound: 65536 MXFP8 tokens of 8 heads of 128 (407 MB) in 69 us, 5.9 TB/s. An MX
-// value is formed in fp32 (exact) and rounded once.
+// bound: 65536 MXFP8 tokens of 8 heads of 128 (407 MB) in 65.5 us, 6.2 TB/s. Blocks
+// an SM, 5 / 6, in us of back-to-back reads: MXFP8 71 / 67, MXFP4 65 / 61, BF16 84 / 87
+// and F32 160 / 166 (these have 16 bytes a load and then spill). Evict-first stores
+// took 64 for MXFP8, but the rows are read next. An MX value is formed in fp32
+// (exact) and rounded once.
 #include "attn.h"
 #include "common.cuh"
 #include "mx.cuh"
@@ -27,7 +30,8 @@ struct ReadArgs {
 };
 
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) k_kv_read(const ReadArgs p) {
+__global__ void __launch_bounds__(kThreads, FMT == DT_MXFP8 || FMT == DT_MXFP4 ? 6 : 5)
+    k_kv_read(const ReadArgs p) {
   // bytes a piece of 16 comes from
   constexpr int kSrc = FMT == DT_MXFP8 ? 8 : (FMT == DT_MXFP4 ? 4 : 16);
   const int out_row = p.c.head_dim * (FMT == DT_F32 ? 4 : 2);

@@ -15,12 +15,12 @@
 //           both are whole vectors (and, for an MX cache, whole blocks lie in
 //           four neighbouring lanes);
 //   kHalf   16 bytes a thread, partners read one by one: any other rot_dim.
-// Blocks are q's, then k's, then v's, so what a block does with its rows is
-// known to all its threads.
+// A block holds rows of q, of k or of v only, so what it does with them is known
+// to all its threads.
 //
 // What bounds it: HBM for prompts (16384 tokens of 32 + 8 heads of 128: rotation
-// 340 MB in 55.6 us, 6.1 TB/s; rotated and stored as MXFP8 379 MB in 70.4 us,
-// 5.4 TB/s, where the quantiser's shuffles and conversions also show); the chain
+// 340 MB in 55.6 us, 6.1 TB/s; rotated and stored as MXFP8 379 MB in 68.3 us,
+// 5.5 TB/s, where the quantiser's shuffles and conversions also show); the chain
 // position -> table row -> store for a decode batch (32 tokens: 4 us).
 #include "attn.h"
 #include "common.cuh"
@@ -40,7 +40,7 @@ struct RotateArgs {
   const int32_t* slots;
   int T, head_dim;
   int groups[3];        // threads' heads of each kind: n * groups + g, n < HPT
-  unsigned first[3];    // first block of k, of v, and past v
+  unsigned blocks[3];   // as many of k as of v, or none of v
   int page_shift;       // log2(page_size), or -1
   int* status;
 };
@@ -278,19 +278,31 @@ COLI_DEV void rotate_rows(const RotateArgs& p, unsigned block) {
 template <typename A, int FMT, int MODE, int HPT>
 __global__ void __launch_bounds__(kThreads, HPT > 1 && MODE != kHalf ? 4 : 1)
     k_rotate(const RotateArgs p) {
-  if (blockIdx.x < p.first[0])
-    rotate_rows<A, FMT, MODE, HPT, 0>(p, blockIdx.x);
-  else if (blockIdx.x < p.first[1])
-    rotate_rows<A, FMT, MODE, HPT, 1>(p, blockIdx.x - p.first[0]);
-  else if constexpr (FMT != kRowsOnly)
-    rotate_rows<A, FMT, MODE, HPT, 2>(p, blockIdx.x - p.first[1]);
+  if constexpr (FMT == kRowsOnly) {
+    if (blockIdx.x < p.blocks[0])
+      rotate_rows<A, FMT, MODE, HPT, 0>(p, blockIdx.x);
+    else
+      rotate_rows<A, FMT, MODE, HPT, 1>(p, blockIdx.x - p.blocks[0]);
+  } else {
+    // the blocks of k and v, with the quantiser's work, lie evenly among q's
+    const uint64_t i = blockIdx.x, others = p.blocks[1] + p.blocks[2], all = p.blocks[0] + others;
+    const unsigned j = static_cast<unsigned>(i * others / all);
+    if (j == static_cast<unsigned>((i + 1) * others / all))
+      rotate_rows<A, FMT, MODE, HPT, 0>(p, blockIdx.x - j);
+    else if (j % 2 == 0)
+      rotate_rows<A, FMT, MODE, HPT, 1>(p, j / 2);
+    else
+      rotate_rows<A, FMT, MODE, HPT, 2>(p, j / 2);
+  }
 }
 
 template <typename A, int FMT, int MODE>
 cudaError_t launch_hpt(RotateArgs& p, cudaStream_t st) {
   constexpr int CH = MODE == kPair ? 2 : 1;
-  // measured at 16384 tokens of 40 (48) heads of 128, us: pairs 2 / 4 heads a
-  // thread 75.9 / 70.4 (4 blocks an SM; 5: 80), neighbours 4 / 8 heads 59.5 / 55.8
+  // measured at 16384 tokens of 40 (stored: 48) heads of 128, us: pairs rotated and
+  // stored as MXFP8 2 / 3 / 4 heads a thread 75.4 / 71.6 / 67.8, neighbours 4 / 6 / 8
+  // heads 77.4 / 75.8 / 67.3. All with 4 blocks an SM, for which some spill a few
+  // registers; without spills at 3 blocks pairs take 69.4 and neighbours 73.4
   constexpr int kMany = MODE == kInter ? 8 : 4;
   const int rows = kThreads / (p.head_dim / (Chunk<A>::N * CH));
   int heads = 0;
@@ -303,9 +315,9 @@ cudaError_t launch_hpt(RotateArgs& p, cudaStream_t st) {
     p.groups[k] = (p.rows[k].n_heads + hpt - 1) / hpt;
     const int64_t ids = static_cast<int64_t>(p.T) * p.groups[k];
     if (ids + rows > INT32_MAX) return cudaErrorInvalidValue;
-    if (p.groups[k] == 0) p.groups[k] = 1;  // no heads: no blocks
-    else blocks += (ids + rows - 1) / rows;
-    p.first[k] = static_cast<unsigned>(blocks);
+    p.blocks[k] = static_cast<unsigned>((ids + rows - 1) / rows);
+    if (p.groups[k] == 0) p.groups[k] = 1, p.blocks[k] = 0;  // no heads: no blocks
+    blocks += p.blocks[k];
   }
   p.page_shift = -1;
   for (int i = 0; i < 13; ++i)
