@@ -42,6 +42,17 @@ COLI_DEV uint2 pack_e4m3x8(const float (&x)[8]) {
   return r;
 }
 
+COLI_DEV uint2 pack_e5m2x8(const float (&x)[8]) {
+  uint2 r;
+  asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 a, %3, %2;\n\tcvt.rn.satfinite.e5m2x2.f32 b, %5, %4;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 c, %7, %6;\n\tcvt.rn.satfinite.e5m2x2.f32 d, %9, %8;\n\t"
+      "mov.b32 %0, {a, b};\n\tmov.b32 %1, {c, d};\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
 COLI_DEV uint32_t pack_e2m1x8(const float (&x)[8]) {
   uint32_t r;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"

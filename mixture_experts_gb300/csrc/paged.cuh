@@ -165,9 +165,9 @@ COLI_DEV void mma_e4m3_16832(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-COLI_DEV void mma_e4m3_16832_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                               uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
+COLI_DEV void mma_e4m3_e5m2_16832_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e5m2.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -319,9 +319,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   using C = Cfg<FMT, DP, NT>;
   constexpr int W = C::kWarps, kJ = DP / 32, kV = DP / 64;
   constexpr bool kF32 = FMT == DT_F32, kMx = C::kMx;
-  // Weights rise to 2^kSlack over the running maximum before it is raised;
-  // fp16 weights (MX caches) are held 2^kLift higher, up to 2^15, so that they
-  // keep 9 bits or more down to 2^-30 of the largest.
+  // Weights are 2^kLift at a head's running maximum (m: the maximum - kLift) and rise to
+  // 2^kSlack times that before it is raised; fp16 weights (MX caches) so keep 9 bits or
+  // more down to 2^-30 of the largest.
   constexpr float kSlack = kMx ? 1.f : 8.f, kLift = kMx ? 14.f : 0.f;
   extern __shared__ __align__(128) char smem[];
   __shared__ long long s_scan[W + 2];
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   while (true) {
     float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
     // MX: acc holds O^T / 2^(ref - 127) of the lane's value block 2v + g/4; bias
-    // is 0x1000 - ref in both halves. Blocks past the head read scale 0 = ref.
+    // is 14 - ref in both halves. Blocks past the head read scale 0 = ref.
     int ref[kMx ? kV : 1];
     uint32_t bias[kMx ? kV : 1], mine[kMx ? kV : 1], hot = 0;
 #pragma unroll
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       for (int v = 0; v < kV; ++v) {
         const bool in = (v * 2 + (g >> 2)) * kMxBlock < D;
         ref[v] = in ? -1000 : 0;
-        bias[v] = (0x1000 - ref[v]) * 0x10001;
+        bias[v] = (14 - ref[v]) * 0x10001;
         mine[v] = in ? 0x00ff00ffu : 0u;
       }
     }
@@ -646,9 +646,10 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         // The head's largest element is brought to [2^kTop, 2^(kTop + 1)), an exact
         // power of two that goes into the scores' scale. MXFP4 keys meet fp16
         // queries (exact but for elements below 2^-28 of the largest). MXFP8 keys
-        // are an operand as they are: the query is cut in two e4m3 terms, the second
-        // 32 times what the first leaves. bf16's 8 bits fit the two exactly down to
-        // 2^-14 of the largest element; below, 2^-22 of it is lost at most.
+        // are an operand as they are: the query is cut in an e4m3 term and an e5m2 one,
+        // what the first leaves (at most half its last place: three bits). bf16's 8 bits
+        // fit the two exactly down to 2^-13 of the largest element; below, 2^-21 of it
+        // is lost at most.
         constexpr int kTop = FMT == DT_MXFP8 ? 7 : 14;
         uint32_t top = 0;
 #pragma unroll
@@ -676,8 +677,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             e4m3x8_f16(hi.x, hi.y, h4);
             f16x8_f32(h4, z);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = (y[i] - z[i]) * 32.f;
-            const uint2 lo = pack_e4m3x8(z);
+            for (int i = 0; i < 8; ++i) z[i] = y[i] - z[i];
+            const uint2 lo = pack_e5m2x8(z);
             q[nt][j] = make_uint4(hi.x, hi.y, lo.x, lo.y);
           } else {
             q[nt][j] = make_uint4(pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3]),
@@ -808,9 +809,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
               float d[4];
               const uint4 u = C::kQShared ? s_q[32 * (j * NT + nt)] : q[nt][j];
               if constexpr (FMT == DT_MXFP8) {
-                mma_e4m3_16832_z(d, k4[0], k4[1], k4[2], k4[3], u.z, u.w);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) d[c] *= 0.03125f;
+                mma_e4m3_e5m2_16832_z(d, k4[0], k4[1], k4[2], k4[3], u.z, u.w);
                 mma_e4m3_16832(d, k4[0], k4[1], k4[2], k4[3], u.x, u.y);
               } else {
                 mma_f16_16816_z(d, ka[0], kb[0], ka[1], kb[1], u.x, u.y);
@@ -831,13 +830,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         *r0 = start - key;
         *r1 = hidden >> ((it * S + i) & 31) & 1u ? 0 : key_end - key;
       };
-#pragma unroll
-      for (int i = 0; i < S; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[i][nt][c] *= xs[nt][c & 1];
-      if (part) {
+      // scores of keys out of sight
+      auto hide = [&](float(&s)[S][NT][4]) {
+        if (!part) return;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           int r0, r1;
@@ -845,48 +840,68 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           const bool in0 = g >= r0 && g < r1, in1 = g + 8 >= r0 && g + 8 < r1;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if (!in0) x[i][nt][0] = x[i][nt][1] = -INFINITY;
-            if (!in1) x[i][nt][2] = x[i][nt][3] = -INFINITY;
+            if (!in0) s[i][nt][0] = s[i][nt][1] = -INFINITY;
+            if (!in1) s[i][nt][2] = s[i][nt][3] = -INFINITY;
           }
         }
-      }
-      // ---- weights ---------------------------------------------------------------------
-      bool up = false, wide = false;  // wide (MX): a weight below 2^-30
-      float top[NT][2], low[NT][2];
+      };
+      // ---- weights: 2^y, y = scaled score - m ------------------------------------------
+      float y[S][NT][4];
+      auto exponents = [&]() {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < S; ++i)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          top[nt][c] = fmaxf(x[0][nt][c], x[0][nt][c + 2]);
-          low[nt][c] = fminf(x[0][nt][c], x[0][nt][c + 2]);
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 1; i < S; ++i) {
-            top[nt][c] = fmaxf(top[nt][c], fmaxf(x[i][nt][c], x[i][nt][c + 2]));
-            low[nt][c] = fminf(low[nt][c], fminf(x[i][nt][c], x[i][nt][c + 2]));
-          }
-          up |= top[nt][c] > m[nt][c] + kSlack;
-        }
-      if (__any_sync(0xffffffffu, up)) {
+            for (int c = 0; c < 4; ++c)
+              y[i][nt][c] = fmaf(x[i][nt][c], xs[nt][c & 1], -m[nt][c & 1]);
+        hide(y);
+      };
+      exponents();
+      float top = y[0][0][0];
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) top = fmaxf(top, y[i][nt][c]);
+      if (__any_sync(0xffffffffu, top > kLift + kSlack)) {
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[i][nt][c] = x[i][nt][c] * xs[nt][c & 1];
+        hide(y);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float v = top[nt][c];
+            float v = fmaxf(y[0][nt][c], y[0][nt][c + 2]);
+#pragma unroll
+            for (int i = 1; i < S; ++i) v = fmaxf(v, fmaxf(y[i][nt][c], y[i][nt][c + 2]));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            v = fmaxf(v, m[nt][c]);
+            v = fmaxf(v - kLift, m[nt][c]);
             const float f = ex2(m[nt][c] - v);
             m[nt][c] = v;
             l[nt][c] *= f;
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) acc[i][nt][c] *= f, acc[i][nt][c + 2] *= f;
           }
+        exponents();
       }
+      bool wide = false;  // MX: a weight below 2^-30 of the largest
       if constexpr (kMx) {
+        float low = y[0][0][0];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          wide |= low[nt][0] < m[nt][0] - (kLift + 16.f) || low[nt][1] < m[nt][1] - (kLift + 16.f);
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) low = fminf(low, y[i][nt][c]);
+        wide = low < -16.f;
       }
 #pragma unroll
       for (int i = 0; i < S; ++i)
@@ -894,7 +909,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            x[i][nt][c] = ex2(x[i][nt][c] - (m[nt][c & 1] - kLift));
+            x[i][nt][c] = ex2(y[i][nt][c]);
             l[nt][c & 1] += x[i][nt][c];
           }
       slot = next(slot);
@@ -977,10 +992,12 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         cp_async_wait<C::kRing - 1>();
         __syncwarp();
         // Value codes are exact in fp16, and so is a code times 2^(s - ref) for
-        // scales s in [ref - 14, ref + 7]: ref follows the largest scale of the
-        // lane's block (the four lanes of a g share it). sd holds s - ref + 0x1000
-        // for the keys of a pair in its halves. A step with a scale out of that
-        // range, a NaN one or a weight too small for fp16 is done with bf16 operands.
+        // scales s in [ref - 14, ref + 1]: ref follows the largest scale of the
+        // lane's block (the four lanes of a g share it). sd holds s - ref + 14
+        // for the keys of a pair in its halves: four bits, or the scale is out of that
+        // range (a borrow or carry between the halves only comes with such a one).
+        // A step with a scale below it, a NaN one or a weight too small for fp16 is
+        // done with bf16 operands.
         uint32_t sd[S][kV][2];
         uint32_t bad = 0;
 #pragma unroll
@@ -1002,14 +1019,14 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
               const uint32_t hi = row + 1 < r0 || row + 1 >= r1 ? 0xffff0000u : 0u;
 #pragma unroll
               for (int v = 0; v < kV; ++v)
-                sd[i][v][k] = (sd[i][v][k] & ~(lo | hi)) | (0x10001000u & (lo | hi));
+                sd[i][v][k] = (sd[i][v][k] & ~(lo | hi)) | (0x000e000eu & (lo | hi));
             }
 #pragma unroll
             for (int v = 0; v < kV; ++v)
-              bad |= (sd[i][v][k] - 0x0ff20ff2u) | (0x10071007u - sd[i][v][k]);
+              bad |= sd[i][v][k] & 0xfff0fff0u;
           }
         }
-        bad = (bad & 0x80008000u) | hot;
+        bad |= hot;
         if (__any_sync(0xffffffffu, bad != 0)) {
           // raise ref where a scale is above its range; is everything in range then?
           hot = 0;
@@ -1020,13 +1037,16 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             for (int i = 0; i < S; ++i)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                sv[i][k] = static_cast<int>(sd[i][v][k >> 1] >> (16 * (k & 1)) & 0xffffu) - 0x1000 +
-                           ref[v];
+                sv[i][k] = (vs[i][k >> 1][v / 2] >> 8 * (v & 1) & mine[v]) >> 16 * (k & 1) & 0xffu;
+                int r0, r1;
+                rows(i, &r0, &r1);
+                const int row = 2 * t + (k & 1) + (k >> 1) * 8;
+                if (row < r0 || row >= r1) sv[i][k] = -1;  // zeros, whatever the scale
                 if (sv[i][k] != 255) most = max(most, sv[i][k]);
               }
             most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            if (most > ref[v] + 7) {
+            if (most > ref[v] + 1) {
               const float f = ex2(static_cast<float>(ref[v] - most));
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -1035,24 +1055,21 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
                   for (int c = 0; c < 4; ++c) acc[v * 4 + i][nt][c] *= f;
               ref[v] = most;
-              bias[v] = (0x1000 - most) * 0x10001;
+              bias[v] = (14 - most) * 0x10001;
             }
             if (ref[v] > 247) hot = 1;  // a NaN scale would pass for 2^128
 #pragma unroll
             for (int i = 0; i < S; ++i) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                int r0, r1;
-                rows(i, &r0, &r1);
-                const int row = 2 * t + (k & 1) + (k >> 1) * 8;
-                if (row < r0 || row >= r1) sv[i][k] = ref[v];
+                if (sv[i][k] < 0) sv[i][k] = ref[v];
                 // below 2^-100 of ref nothing is left of a value beside the largest
                 const int e = max(sv[i][k] - ref[v], -100);
                 wide |= e < -14 || sv[i][k] == 255;
-                sv[i][k] = sv[i][k] == 255 ? 255 : e;  // 255: NaN (e is at most 7)
+                sv[i][k] = (sv[i][k] == 255 ? 255 : e) + 14;  // 255: NaN (e is at most 1)
               }
-              sd[i][v][0] = (sv[i][0] + 0x1000) | (sv[i][1] + 0x1000) << 16;
-              sd[i][v][1] = (sv[i][2] + 0x1000) | (sv[i][3] + 0x1000) << 16;
+              sd[i][v][0] = (sv[i][0] & 0xffffu) | sv[i][1] << 16;
+              sd[i][v][1] = (sv[i][2] & 0xffffu) | sv[i][3] << 16;
             }
           }
         }
@@ -1102,12 +1119,12 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
                   for (int c = 0; c < 4; ++c) op[k][2 * c + 1] = h4[c];
                 }
                 if constexpr (!kWide) {
-                  const uint32_t f = (sd[i][v][k] - 0x0ff10ff1u) << 10;  // 2^(s - ref), both keys
+                  const uint32_t f = sd[i][v][k] * 1024u + 0x04000400u;  // 2^(s - ref), both keys
 #pragma unroll
                   for (int c = 0; c < 8; ++c) op[k][c] = mul_f16x2(op[k][c], f);
                 } else {
-                  const int e0 = static_cast<int>(sd[i][v][k] & 0xffffu) - 0x1000;
-                  const int e1 = static_cast<int>(sd[i][v][k] >> 16) - 0x1000;
+                  const int e0 = static_cast<int16_t>(sd[i][v][k] & 0xffffu) - 14;
+                  const int e1 = static_cast<int16_t>(sd[i][v][k] >> 16) - 14;
                   const float f0 = __uint_as_float(e0 == 255 ? 0x7fc00000u : (e0 + 127u) << 23);
                   const float f1 = __uint_as_float(e1 == 255 ? 0x7fc00000u : (e1 + 127u) << 23);
 #pragma unroll
@@ -1181,11 +1198,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], i);
-        m[nt][c] = m[nt][c] == -FLT_MAX ? m[nt][c] : m[nt][c] - kLift;
-      }
     if (g == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
