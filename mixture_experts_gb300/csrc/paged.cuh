@@ -28,10 +28,11 @@
 // What bounds it (GB300, 32 query and 8 key heads of 128 unless said, against the
 // 6.8 TB/s of a copy): bf16 HBM: 6.9 TB/s on one context of 500009 tokens, 6.05 TB/s
 // on 32 ragged ones (586 MB, 97 us). fp32 HBM (6.6 TB/s, 8 heads, 7 x 26157 tokens).
-// MXFP8 5.5 TB/s on 64 contexts (1168 MB, 211 us): at 16 bytes of cache for every
-// 32 elements it is the ALU pipe (54% busy: widening value codes to fp16, their
-// scales) and instruction issue. MXFP4, 64 query heads on 4: 2.0 TB/s (282 MB,
-// 138 us): issue and latency of the same work at half the bytes and twice the heads.
+// MXFP8 5.6 TB/s on 64 contexts (1168 MB, 207 us): 463 instructions a tile, issue 53%
+// and the ALU pipe 45% busy (widening value codes to fp16, their scales), with three
+// warps a scheduler to cover the steps' own latency. MXFP4, 64 query heads on 4:
+// 2.1 TB/s (282 MB, 135 us): 597 instructions a tile, the same work at half the bytes
+// and twice the heads.
 
 #pragma once
 
@@ -65,7 +66,7 @@ struct Cfg {
   static constexpr int kScaleRow = kMx ? (DP > 128 ? 8 : 4) : 0;
   // Tiles a warp takes in one step: two of an MX cache, whose small tiles leave
   // the step's fixed work (pages, waits, votes) as long as the tile's own (64 MXFP8
-  // contexts: two 210 us, one 215 us; groups of 16 heads: two spill, 146 against 143 us).
+  // contexts: two 207 us, one 213 us; groups of 16 heads: two spill, 144 against 135 us).
   static constexpr int kStep = kMx && DP <= 128 && DP * NT <= 128 ? 2 : 1;
   static constexpr int kTileBytes = kTile * kRow, kTileScales = kTile * kScaleRow;
   // whole 128-byte lines: addresses within a line are XORed
@@ -74,8 +75,8 @@ struct Cfg {
   static constexpr int kOpen = 8;  // a segment's fixed cost, in tiles (3 us at 2.7 tiles a us)
   // Warps of a block and blocks of an SM: what the registers of the widest step allow
   // without many spills. MXFP8 heads of 128, 64 contexts: 12 warps of 168 registers
-  // 210 us, 16 of 128 236 us, 8 of 255 262 us; MXFP4 groups of 16 heads, 160 windowed
-  // contexts: 12 warps 143 us, 8 warps 153 us, 16 warps 195 us.
+  // 207 us, 8 of 255 228 us (16 warps: no room for their rings); MXFP4 groups of 16
+  // heads, 160 windowed contexts: 12 warps 135 us, 8 warps 146 us, 16 warps 221 us.
   static constexpr int kAcc = DP * NT;
   static constexpr int kWarps = kAcc == 512 ? (kMx ? 8 : 6)
                                 : kSlot > 8448 || (kMx && kAcc >= 128 && DP <= 128) ||
