@@ -446,6 +446,44 @@ def test_attention_large_values_under_tiny_weights(fmt, hq):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("step", [1, 2, 3, -1, -2])
+@pytest.mark.parametrize("hq,D", [(4, 64), (16, 128), (3, 256)])
+def test_attention_value_scales_that_climb_or_fall(hq, D, step, fmt):
+    """Every 16 keys the values grow (or shrink) by 2^step, each block of channels
+    by a binary step of its own beside that, so that scales pass every distance
+    from the largest seen before."""
+    g = gen(53, hq, D)
+    n = 720
+    k = torch.randn(n, 1, D, generator=g)
+    v = torch.randn(n, 1, D, generator=g)
+    block = torch.arange(D) // 32
+    first = -60 if step == 3 else 0  # 44 steps of 3 from 1 on would pass the largest bf16
+    v = v * torch.exp2((first + torch.arange(n) // 16 * step)[:, None, None] + block * 3.0)
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = randn(g, 1, hq, D, dtype=act(fmt))
+    got, lse = c.attend(q, table, sl, return_lse=True)
+    check(got, lse, attn_ref.attend(q, rows["k"], rows["v"], [n], 1, D ** -0.5), fmt)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_attention_queries_with_one_large_element(fmt):
+    """One element 2^10 times the rest, where the keys are zero: the scores come from
+    the small elements alone."""
+    g = gen(59)
+    n, D, hq = 500, 64, 8
+    k = torch.randn(n, 1, D, generator=g)
+    k[..., 5] = 0.0
+    v = torch.randn(n, 1, D, generator=g)
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = (1 + torch.rand(1, hq, D, generator=g)) * torch.where(
+        torch.rand(1, hq, D, generator=g) < 0.5, -1.0, 1.0)
+    q[..., 5] = 1.5 * 2.0 ** 10
+    q = q.to(act(fmt)).cuda()
+    got, lse = c.attend(q, table, sl, return_lse=True)
+    check(got, lse, attn_ref.attend(q, rows["k"], rows["v"], [n], 1, D ** -0.5), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
 def test_attention_extreme_scales(fmt):
     """Blocks at the ends of E8M0: keys of 2^100 and 2^-100 against queries of the other
     size, and values of 2^-120."""
