@@ -157,8 +157,8 @@ COLI_DEV void mma_f16_16816_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t 
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// e4m3 x e4m3, 32 indices: twice the f16 form's work an instruction, summed in
-// fp32 as exactly (checked to 24 bits within an instruction and across).
+// e4m3 x e4m3 (or e5m2), 32 indices: twice the f16 form's work an instruction, summed
+// in fp32 as exactly (e4m3 checked to 24 bits within an instruction and across).
 COLI_DEV void mma_e4m3_16832(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                              uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
