@@ -314,6 +314,108 @@ COLI_DEV Seq seq_of(const PagedArgs& a, int b, bool latch) {
   return {len, first, (len + kTile - 1) / kTile - first};
 }
 
+// One warp's tiles of an MX cache once more, in fp32 straight from memory: lane 4g + t takes
+// the channels 64 v + 8 g .. + 7 of heads 2t, 2t + 1 (+ 8 nt), one key after the other. For
+// numbers further apart than the operands of k_paged hold, which no trained model's are: sums
+// and products overflow where plain fp32 ones would. 25 times the steps' time (64 MXFP8
+// contexts: 5.3 ms). A call, not inlined: 64 contexts 210 us against 213, where none needs it.
+template <int DP, int NT>
+struct PlainSums {
+  float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
+};
+template <int FMT>
+COLI_DEV void decode8(const KvView& c, const char* pool, const uint8_t* scales, size_t row, int ch,
+                      float (&x)[8]) {
+  uint32_t h4[4];
+  if constexpr (FMT == DT_MXFP8) {
+    const uint2 u = *reinterpret_cast<const uint2*>(pool + row * c.row_bytes + ch);
+    e4m3x8_f16(u.x, u.y, h4);
+  } else {
+    e2m1x8_f16(*reinterpret_cast<const uint32_t*>(pool + row * c.row_bytes + ch / 2), h4);
+  }
+  f16x8_f32(h4, x);
+  const float f = e8m0_f32(scales[row * c.scale_stride + ch / kMxBlock]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= f;
+}
+template <int FMT, int DP, int NT>
+__device__ __noinline__ void plain_tiles(const PagedArgs a, int group, int b, int h, int row0,
+                                         int start, int key_end, int tile0, int tile_end, float sl,
+                                         PlainSums<DP, NT>* out) {
+  constexpr int S = Cfg<FMT, DP, NT>::kStep, W = Cfg<FMT, DP, NT>::kWarps;
+  const int g = lane_id() >> 2, t = lane_id() & 3, D = a.c.head_dim;
+  const int tiles_per_page = a.c.page_size / kTile;
+  float acc[DP / 16][NT][4] = {}, m[NT][2], l[NT][2] = {};
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -FLT_MAX;
+#pragma unroll 1
+  for (int n = 0;; ++n) {
+    const int tile = tile0 + n / S * (W * S) + n % S;
+    if (tile >= tile_end) break;
+    const int pi = tile / tiles_per_page;
+    const int page = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
+    if (page < 0 || page >= a.c.n_pages) continue;
+    const size_t at = kv_row(a.c, page, h, (tile - pi * tiles_per_page) * kTile);
+    const int r1 = min(kTile, key_end - tile * kTile);
+#pragma unroll 1
+    for (int r = max(start - tile * kTile, 0); r < r1; ++r) {
+      float s[NT][2] = {}, x[8];
+#pragma unroll 1
+      for (int ch = g * 8; ch < D; ch += 64) {
+        decode8<FMT>(a.c, a.c.k, a.c.k_scale, at + r, ch, x);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int hd = row0 + nt * 8 + 2 * t + c;
+            if (hd >= group) continue;
+            const uint4 u = ldg_keep(static_cast<const __nv_bfloat16*>(a.q) + b * a.q_stride +
+                                     static_cast<size_t>(h * group + hd) * D + ch);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              s[nt][c] = fmaf(bf16_lo(word_of(u, k)), x[2 * k], s[nt][c]);
+              s[nt][c] = fmaf(bf16_hi(word_of(u, k)), x[2 * k + 1], s[nt][c]);
+            }
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) s[nt][c] += __shfl_xor_sync(0xffffffffu, s[nt][c], k);
+          const float y = s[nt][c] * sl, top = fmaxf(m[nt][c], y), f = ex2(m[nt][c] - top);
+          m[nt][c] = top;
+          s[nt][c] = ex2(y - top);
+          l[nt][c] = l[nt][c] * f + (g == 0 ? s[nt][c] : 0.f);
+#pragma unroll
+          for (int i = 0; i < DP / 16; ++i) acc[i][nt][c] *= f, acc[i][nt][c + 2] *= f;
+        }
+#pragma unroll
+      for (int v = 0; v < DP / 64; ++v) {
+        if (v * 64 + g * 8 >= D) continue;
+        decode8<FMT>(a.c, a.c.v, a.c.v_scale, at + r, v * 64 + g * 8, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              acc[v * 4 + i][nt][c] =
+                  fmaf(s[nt][c & 1], x[2 * i + (c >> 1)], acc[v * 4 + i][nt][c]);
+      }
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i) out->acc[i][nt][c] = acc[i][nt][c];
+      if (c < 2) out->m[nt][c] = m[nt][c], out->l[nt][c] = l[nt][c];
+    }
+}
+
 template <int FMT, int DP, int NT>
 __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT>::kPerSm)
     k_paged(const Params p) {
@@ -578,9 +680,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   while (true) {
     float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
     // MX: acc holds O^T / 2^(ref - 127) of the lane's value block 2v + g/4; bias
-    // is 14 - ref in both halves. Blocks past the head read scale 0 = ref.
+    // is 14 - ref in both halves, byte v of ref0 the first ref. Blocks past the head
+    // read scale 0 = ref.
     int ref[kMx ? kV : 1];
-    uint32_t bias[kMx ? kV : 1], mine[kMx ? kV : 1], hot = 0;
+    uint32_t bias[kMx ? kV : 1], mine[kMx ? kV : 1], hot = 0, ref0 = 0;
+    bool odd = false;  // MX: numbers too far apart for these operands (plain_tiles)
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i)
 #pragma unroll
@@ -1011,7 +1115,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         // for the keys of a pair in its halves: four bits, or the scale is out of that
         // range (a borrow or carry between the halves only comes with such a one).
         // A step with a scale below it, a NaN one or a weight too small for fp16 is
-        // done with bf16 operands.
+        // done with bf16 operands. Values and earlier sums stay exact there for scales less than
+        // kFar below ref, and ref within kFar of the first one. Further off the smaller values
+        // may still be what counts, where the larger ones have no weight: such a warp
+        // takes its tiles again, in plain fp32.
+        constexpr int kFar = 48;
         uint32_t sd[S][kV][2];
         uint32_t bad = 0;
 #pragma unroll
@@ -1046,7 +1154,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           hot = 0;
 #pragma unroll
           for (int v = 0; v < kV; ++v) {
-            int sv[S][4], most = -1000;
+            int sv[S][4], most = -1;
 #pragma unroll
             for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -1060,7 +1168,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
               }
             most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            if (most > ref[v] + 1) {
+            if (most >= 0 && most > ref[v] + 1) {
+              if (ref[v] == -1000) ref0 |= most << 8 * v;
+              odd |= most > static_cast<int>(ref0 >> 8 * v & 0xffu) + kFar;
               const float f = ex2(static_cast<float>(ref[v] - most));
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -1077,8 +1187,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 if (sv[i][k] < 0) sv[i][k] = ref[v];
-                // below 2^-100 of ref nothing is left of a value beside the largest
-                const int e = max(sv[i][k] - ref[v], -100);
+                const int e = max(sv[i][k] - ref[v], -kFar);
                 wide |= e < -14 || sv[i][k] == 255;
                 sv[i][k] = (sv[i][k] == 255 ? 255 : e) + 14;  // 255: NaN (e is at most 1)
               }
@@ -1139,6 +1248,10 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
                 } else {
                   const int e0 = static_cast<int16_t>(sd[i][v][k] & 0xffffu) - 14;
                   const int e1 = static_cast<int16_t>(sd[i][v][k] >> 16) - 14;
+                  uint32_t any = 0;  // zeros lie at no distance
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) any |= op[k][c];
+                  odd |= (e0 == -kFar && (any & 0x7fffu)) || (e1 == -kFar && (any & 0x7fff0000u));
                   const float f0 = __uint_as_float(e0 == 255 ? 0x7fc00000u : (e0 + 127u) << 23);
                   const float f1 = __uint_as_float(e1 == 255 ? 0x7fc00000u : (e1 + 127u) << 23);
 #pragma unroll
@@ -1175,6 +1288,23 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           product(std::integral_constant<bool, false>());
       }
       slot = next(slot);
+    }
+
+    if constexpr (kMx) {
+      if (__any_sync(0xffffffffu, odd)) {
+        PlainSums<DP, NT> sums;
+        plain_tiles<FMT, DP, NT>(a, p.group, b, h, row0, start, key_end, tile0, tile_end, sl, &sums);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) acc[i][nt][c] = sums.acc[i][nt][c];
+            if (c < 2) m[nt][c] = sums.m[nt][c], l[nt][c] = sums.l[nt][c];
+          }
+#pragma unroll
+        for (int v = 0; v < kV; ++v) ref[v] = 127;
+      }
     }
 
     // ---- the next segment's first copies fly while this one is joined ------------------

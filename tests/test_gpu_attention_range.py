@@ -1,0 +1,117 @@
+"""Decode attention at the ends of what its types hold: values and scales of very
+different size, weights that vanish, keys and queries near the largest and smallest
+numbers, queries of a wide range (GPU)."""
+import math
+import os
+import sys
+
+import pytest
+import torch
+
+import mixture_experts_gb300 as moe
+
+sys.path.insert(0, os.path.dirname(__file__))
+import attn_ref  # noqa: E402
+import test_gpu_attention as base  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+FMT, act, randn, check, one_sequence = base.FMT, base.act, base.randn, base.check, base.one_sequence
+MX = ["mxfp8", "mxfp4"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    moe.build()
+    assert torch.cuda.is_available()
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    assert moe.coli_device_status() == moe.COLI_OK
+    yield
+    assert moe.coli_device_status() == moe.COLI_OK
+
+
+def gen(*key):
+    return torch.Generator().manual_seed(sum((i + 3) * 104729 * int(k) for i, k in enumerate(key)))
+
+
+def compare(c, table, sl, rows, q, fmt, scale=None):
+    """attend() against the 64-bit form, over all of one sequence."""
+    hk, D = c.n_kv_heads, c.head_dim
+    got, lse = c.attend(q, table, sl, scale=scale, return_lse=True)
+    check(got, lse, attn_ref.attend(q, rows["k"], rows["v"], sl.tolist(), hk,
+                                    D ** -0.5 if scale is None else scale), fmt)
+
+
+# ---- values whose scales lie further apart than a 16-bit operand's range ------------------
+HEADS = [(4, 64), (16, 128), (8, 128), (3, 256), (16, 256)]
+
+
+@pytest.mark.parametrize("fmt", MX)
+@pytest.mark.parametrize("place", [0, 137, 399])
+@pytest.mark.parametrize("hq,D", HEADS)
+def test_a_large_value_of_no_weight(hq, D, place, fmt):
+    """One value of 2^60 under a key whose weight is 0; the rest lie near 2^-60."""
+    g = gen(1, hq, D, place)
+    n = 400
+    k = 0.1 * torch.randn(n, 1, D, generator=g)
+    v = torch.randn(n, 1, D, generator=g) * 2.0 ** -60
+    k[place] = -20.0                                  # about -20 D^0.5 * 6: e^-900 and less
+    v[place] *= 2.0 ** 120
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = (6.0 + 0.1 * torch.randn(1, hq, D, generator=g)).bfloat16().cuda()
+    compare(c, table, sl, rows, q, fmt)
+
+
+@pytest.mark.parametrize("fmt", MX)
+@pytest.mark.parametrize("far", [40, 100, 150])
+def test_a_large_value_that_one_head_alone_sees(far, fmt):
+    """Heads of one group: for the even ones the large value decides, for the odd ones
+    it has no weight and the rest do."""
+    g = gen(2, far)
+    n, D, hq = 300, 64, 8
+    k = 0.1 * torch.randn(n, 1, D, generator=g)
+    v = torch.randn(n, 1, D, generator=g) * 2.0 ** (-far / 2)
+    k[50] = 20.0
+    v[50] *= 2.0 ** (far / 2)
+    v[50] *= 2.0 ** (far / 2)                         # (2^150 itself is past fp32)
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    sign = torch.where(torch.arange(hq) % 2 == 0, 1.0, -1.0)[None, :, None]
+    q = (sign * (6.0 + 0.1 * torch.randn(1, hq, D, generator=g))).bfloat16().cuda()
+    compare(c, table, sl, rows, q, fmt)
+
+
+@pytest.mark.parametrize("fmt", MX)
+@pytest.mark.parametrize("hq,D", HEADS)
+def test_values_that_shrink_as_the_scores_rise(hq, D, fmt):
+    """Large values first, at small scores; each later run of keys scores far higher and
+    holds values 2^45 times smaller, so every earlier sum loses its weight."""
+    g = gen(3, hq, D)
+    n = 800
+    run = torch.arange(n) // 200
+    k = (run[:, None, None] * 4.0 + 0.1 * torch.randn(n, 1, D, generator=g))
+    v = torch.randn(n, 1, D, generator=g) * torch.exp2(60.0 - 45.0 * run)[:, None, None]
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = (6.0 + 0.1 * torch.randn(1, hq, D, generator=g)).bfloat16().cuda()
+    compare(c, table, sl, rows, q, fmt)
+
+
+@pytest.mark.parametrize("fmt", MX)
+@pytest.mark.parametrize("byte", [0, 1, 200, 254])
+@pytest.mark.parametrize("hq,D", [(4, 64), (16, 128)])
+def test_zeros_under_any_scale(hq, D, byte, fmt):
+    """Value blocks of zeros count for nothing, whatever their scale byte says."""
+    g = gen(4, hq, D, byte)
+    n = 250
+    k = torch.randn(n, 1, D, generator=g)
+    v = torch.randn(n, 1, D, generator=g)
+    v[::3] = 0.0
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    at = torch.arange(0, n, 3).cuda() + 16
+    c.v_scale[at // 16, 0, at % 16, :D // 32] = byte
+    q = randn(g, 1, hq, D, dtype=torch.bfloat16)
+    compare(c, table, sl, rows, q, fmt)
+
+
