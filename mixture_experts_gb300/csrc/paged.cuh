@@ -768,6 +768,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e = static_cast<int>(top >> 23) - 127;
         e = e < -112 ? -112 : e;
+        // Against such queries key scales of 2^-127, which count as 0 below, or scores
+        // near the smallest numbers would show
+        odd |= top != 0 && (e > 80 || e < -80);
         const float up = __uint_as_float(static_cast<uint32_t>(kTop - e + 127) << 23);
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
@@ -1009,6 +1012,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c) low = fminf(low, y[i][nt][c]);
+        odd |= !part && low == -INFINITY;
         if (part) {
           low = 0.f;
 #pragma unroll
@@ -1016,8 +1020,10 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c) {
                 if (y[i][nt][c] > -128.f) low = fminf(low, y[i][nt][c]);
+                odd |= fabsf(x[i][nt][c]) == INFINITY;
+              }
         }
         wide = low < -16.f;
       }
@@ -1291,6 +1297,10 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     }
 
     if constexpr (kMx) {
+      // A block's partial score times its scale may overflow where the score itself does not:
+      // a score of infinity was seen above, or left NaN in the sums.
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) odd |= l[nt][0] != l[nt][0] || l[nt][1] != l[nt][1];
       if (__any_sync(0xffffffffu, odd)) {
         PlainSums<DP, NT> sums;
         plain_tiles<FMT, DP, NT>(a, p.group, b, h, row0, start, key_end, tile0, tile_end, sl, &sums);

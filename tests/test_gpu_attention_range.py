@@ -115,3 +115,48 @@ def test_zeros_under_any_scale(hq, D, byte, fmt):
     compare(c, table, sl, rows, q, fmt)
 
 
+# ---- keys and queries of opposite extremes -----------------------------------------------
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("e", [60, 100, 110, 118])
+@pytest.mark.parametrize("hq,D", [(4, 64), (16, 128), (8, 256)])
+def test_large_keys_and_small_queries(hq, D, e, fmt):
+    g = gen(7, hq, D, e)
+    n = 150
+    k = torch.randn(n, 1, D, generator=g) * 2.0 ** e
+    v = torch.randn(n, 1, D, generator=g)
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = (torch.randn(1, hq, D, generator=g) * 2.0 ** -e).to(act(fmt)).cuda()
+    compare(c, table, sl, rows, q, fmt)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("hq,D", [(4, 64), (16, 128), (8, 256)])
+def test_small_keys_and_large_queries(hq, D, fmt):
+    """Keys whose blocks take the smallest scale, 2^-127, against queries that bring the
+    scores back to ordinary size."""
+    g = gen(8, hq, D)
+    n = 150
+    e = 125 if fmt == "mxfp4" else 119
+    k = (torch.randn(n, 1, D, generator=g) * 0.2).clamp(-1, 1) * 2.0 ** -e
+    v = torch.randn(n, 1, D, generator=g)
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    if fmt in MX:
+        assert not c.k_scale[1, 0, :, :2].any()
+    q = (torch.randn(1, hq, D, generator=g).clamp(-3, 3) * 2.0 ** (e + 1)).to(act(fmt)).cuda()
+    compare(c, table, sl, rows, q, fmt)
+
+
+@pytest.mark.parametrize("fmt", MX)
+@pytest.mark.parametrize("what", ["inf", "nan"])
+def test_a_query_that_is_no_number_stays_in_its_head(what, fmt):
+    g = gen(10)
+    n, D = 200, 64
+    c, table, sl, rows = one_sequence(fmt, torch.randn(n, 1, D, generator=g),
+                                      torch.randn(n, 1, D, generator=g))
+    q = randn(g, 1, 4, D, dtype=torch.bfloat16)
+    want, _, tol, _ = attn_ref.attend(q, rows["k"], rows["v"], [n], 1, D ** -0.5)
+    q[0, 2, 7] = math.inf if what == "inf" else math.nan
+    got = c.attend(q, table, sl).cpu().double()
+    assert got[0, 2].isnan().all()
+    keep = torch.tensor([0, 1, 3])
+    assert ((got - want).abs() <= tol + 2.0 ** -8 * want.abs())[0, keep].all()
