@@ -91,18 +91,21 @@ struct Cfg {
   // column tiles of MX heads, whose registers are worth more warps
   static constexpr bool kQShared = FMT == DT_F32 || (NT == 2 && (kMx || DP == 256));
   static constexpr int kQBytes = FMT == DT_F32 ? DP / 8 * 512 : (kQShared ? NT * DP / 32 * 512 : 0);
+  // MXFP8: query elements that its two terms do not hold, in fp16
+  static constexpr int kFineBytes = FMT == DT_MXFP8 ? NT * DP / 32 * 512 : 0;
   // The warps' sums are joined half the registers at a time, beside the rings: the
   // next segment's copies are in flight meanwhile.
   static constexpr int kMergeBytes = kWarps * kRegs * 64;
   static constexpr int kState = kWarps * 8 * NT * 8;  // maxima and sums
   // shared memory of a block less the system's 1 KB and the static part
-  static constexpr int kBudget = 228 * 1024 / kPerSm - 1280 - kMergeBytes - kQBytes - kState;
+  static constexpr int kBudget =
+      228 * 1024 / kPerSm - 1280 - kMergeBytes - kQBytes - kFineBytes - kState;
   static constexpr int kFit = kBudget / (kWarps * kSlot);
   // odd, so key and value slots alternate through the ring with one lead
   static constexpr int kRing = kFit >= 7 ? 7 : (kFit >= 5 ? 5 : 3);
   static constexpr int kRingBytes = kRing * kWarps * kSlot;
   static constexpr int kMain = kRingBytes + kMergeBytes;
-  static constexpr int kSmem = kMain + kQBytes + kState;
+  static constexpr int kSmem = kMain + kQBytes + kFineBytes + kState;
   static_assert(kRingBytes <= kBudget, "ring does not fit");
   static constexpr int kPart = kRegs * 32 + 16 * NT;   // floats of a partial slot
 };
@@ -522,9 +525,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 
   const int D = a.c.head_dim;
   const uint32_t ring = smem_u32(smem) + w * (C::kRing * C::kSlot);
-  float* s_m = reinterpret_cast<float*>(smem + C::kMain + C::kQBytes);  // [W][8 NT] maxima, sums
-  float* s_l = s_m + W * 8 * NT;
   uint4* s_q = reinterpret_cast<uint4*>(smem + C::kMain) + lane;  // kQShared: piece f at s_q[32 f]
+  uint4* s_fine = s_q + C::kQBytes / 16;                          // MXFP8: the same
+  // [W][8 NT] maxima, sums
+  float* s_m = reinterpret_cast<float*>(smem + C::kMain + C::kQBytes + C::kFineBytes);
+  float* s_l = s_m + W * 8 * NT;
   const float sl = a.scale * 1.4426950408889634f;
   const int tiles_per_page = a.c.page_size / kTile;
   const uint32_t tile_bytes = kTile * a.c.row_bytes;
@@ -706,6 +711,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     // ---- the queries, head g's (+ 8 nt) elements in the order of the keys' reads ---------
     uint4 q[kF32 ? 1 : NT][kJ];
     float xs[NT][2];  // scale of the scores of this lane's columns (heads 2t, 2t + 1)
+    uint32_t fine = 0;  // MXFP8: bit j NT + nt: some of elements 32j .. + 31 are in s_fine
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row0 + nt * 8 + g;
@@ -750,20 +756,22 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       if constexpr (kMx) {
         // The head's largest element is brought to [2^kTop, 2^(kTop + 1)), an exact
         // power of two that goes into the scores' scale. MXFP4 keys meet fp16
-        // queries (exact but for elements below 2^-28 of the largest). MXFP8 keys
-        // are an operand as they are: the query is cut in an e4m3 term and an e5m2 one,
-        // what the first leaves (at most half its last place: three bits). bf16's 8 bits
-        // fit the two exactly down to 2^-13 of the largest element; below, 2^-21 of it
-        // is lost at most.
-        constexpr int kTop = FMT == DT_MXFP8 ? 7 : 14;
-        uint32_t top = 0;
+        // queries. MXFP8 keys are an operand as they are: the query is cut in an e4m3 term and
+        // an e5m2 one, what the first leaves (at most half its last place: three bits).
+        // bf16's 8 bits fit the two exactly down to 2^-13 of the largest element, and fp16 down
+        // to 2^-31. Smaller elements, few if any, meet MXFP8 keys in fp16 (`fine`), 2^7 larger;
+        // queries with elements below 2^-31 of the largest take the plain pass.
+        constexpr int kTop = FMT == DT_MXFP8 ? 7 : 14, kFit = FMT == DT_MXFP8 ? 13 : 31;
+        uint32_t most = 0, least = 0x7fff7fffu;
 #pragma unroll
         for (int j = 0; j < kJ; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t v = word_of(q[nt][j], i);
-            top = max(top, max((v << 16) & 0x7fff0000u, v & 0x7fff0000u));
+            const uint32_t v = word_of(q[nt][j], i) & 0x7fff7fffu;
+            most = __vmaxu2(most, v);
+            if (j * 32 < D) least = __vminu2(least, v);
           }
+        uint32_t top = max(most << 16, most & 0x7fff0000u);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e = static_cast<int>(top >> 23) - 127;
@@ -772,6 +780,33 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         // near the smallest numbers would show
         odd |= top != 0 && (e > 80 || e < -80);
         const float up = __uint_as_float(static_cast<uint32_t>(kTop - e + 127) << 23);
+        const uint32_t fit = static_cast<uint32_t>(e - kFit + 127) << 23;
+        if (__any_sync(0xffffffffu, r < p.group && min(least << 16, least & 0x7fff0000u) < fit)) {
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            uint32_t keep[4], rest[4];
+            bool some = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t v = word_of(q[nt][j], i), v0 = v << 16, v1 = v & 0xffff0000u;
+              const uint32_t a0 = v0 & 0x7fffffffu, a1 = v1 & 0x7fffffffu;
+              odd |= a0 - 1 < (fit - (31 - kFit) * 0x800000u) - 1 ||
+                     a1 - 1 < (fit - (31 - kFit) * 0x800000u) - 1;
+              const bool s0 = a0 < fit, s1 = a1 < fit;
+              some |= (s0 && a0 != 0) || (s1 && a1 != 0);
+              keep[i] = (s0 ? 0u : v0 >> 16) | (s1 ? 0u : v1);
+              rest[i] = pack_f16x2(s0 ? __uint_as_float(v0) * up * 0x1p7f : 0.f,
+                                   s1 ? __uint_as_float(v1) * up * 0x1p7f : 0.f);
+            }
+            if constexpr (FMT == DT_MXFP8) {
+              q[nt][j] = make_uint4(keep[0], keep[1], keep[2], keep[3]);
+              // every warp of the block writes the same values, and reads its own
+              s_fine[32 * (j * NT + nt)] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+              fine |= (__any_sync(0xffffffffu, some) ? 1u : 0u) << (j * NT + nt);
+            }
+          }
+          __syncwarp();
+        }
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
           const uint4 v = q[nt][j];
@@ -927,6 +962,32 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
               for (int c = 0; c < 4; ++c)
                 x[i][nt][c] = j == 0 ? d[c] * (c < 2 ? f0 : f1)
                                      : fmaf(d[c], c < 2 ? f0 : f1, x[i][nt][c]);
+            }
+          }
+          if constexpr (FMT == DT_MXFP8) {
+#pragma unroll 1
+            for (uint32_t todo = fine; todo != 0; todo &= todo - 1) {
+              const int f = __ffs(todo) - 1, j = f / NT;
+              const uint32_t s0 = DP > 128 && j >= 4 ? sc0[1] : sc0[0];
+              const uint32_t s1 = DP > 128 && j >= 4 ? sc1[1] : sc1[0];
+              const float f0 = __uint_as_float((s0 >> 8 * (j % 4) << 23 & 0x7f800000u) | 1u);
+              const float f1 = __uint_as_float((s1 >> 8 * (j % 4) << 23 & 0x7f800000u) | 1u);
+              uint32_t k4[4], h[4];
+              float d[4];
+              const uint4 u = s_fine[32 * f];
+              ldsm4(k4, further(tile + get_k, j * 32));
+              // a word of four codes: the product's indices 2t, 2t + 1 and 2t + 8, 2t + 9
+              e4m3x8_f16(k4[0], k4[1], h);
+              mma_f16_16816_z(d, h[0], h[2], h[1], h[3], u.x, u.y);
+              e4m3x8_f16(k4[2], k4[3], h);
+              mma_f16_16816(d, h[0], h[2], h[1], h[3], u.z, u.w);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (nt != f % NT) continue;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  x[i][nt][c] = fmaf(d[c] * 0x1p-7f, c < 2 ? f0 : f1, x[i][nt][c]);
+              }
             }
           }
         }

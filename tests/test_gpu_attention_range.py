@@ -146,6 +146,28 @@ def test_small_keys_and_large_queries(hq, D, fmt):
     compare(c, table, sl, rows, q, fmt)
 
 
+# ---- queries of a wide range -----------------------------------------------------------------
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("e", [13, 14, 16, 20, 28, 33, 40])
+@pytest.mark.parametrize("hq,D", [(8, 64), (16, 128), (4, 128), (12, 256)])
+def test_queries_with_large_elements_that_meet_zeros(hq, D, e, fmt):
+    """Elements 2^e times the rest, some heads' first or last, where the keys are zero:
+    the scores come from the small elements alone."""
+    g = gen(9, hq, D, e)
+    n = 300
+    k = torch.randn(n, 1, D, generator=g)
+    k[..., 5] = 0.0
+    k[..., D - 1] = 0.0
+    v = torch.randn(n, 1, D, generator=g)
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = (1 + torch.rand(1, hq, D, generator=g)) * torch.where(
+        torch.rand(1, hq, D, generator=g) < 0.5, -1.0, 1.0)
+    q[:, ::2, 5] = 1.5 * 2.0 ** e
+    q[:, 1::3, D - 1] = -1.25 * 2.0 ** e
+    q = q.to(act(fmt)).cuda()
+    compare(c, table, sl, rows, q, fmt)
+
+
 @pytest.mark.parametrize("fmt", MX)
 @pytest.mark.parametrize("what", ["inf", "nan"])
 def test_a_query_that_is_no_number_stays_in_its_head(what, fmt):
