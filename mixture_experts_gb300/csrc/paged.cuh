@@ -1009,8 +1009,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           const bool in0 = g >= r0 && g < r1, in1 = g + 8 >= r0 && g + 8 < r1;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if (!in0) s[i][nt][0] = s[i][nt][1] = -INFINITY;
-            if (!in1) s[i][nt][2] = s[i][nt][3] = -INFINITY;
+            if (!in0) s[i][nt][0] = s[i][nt][1] = kMx ? -FLT_MAX : -INFINITY;
+            if (!in1) s[i][nt][2] = s[i][nt][3] = kMx ? -FLT_MAX : -INFINITY;
           }
         }
       };
@@ -1073,7 +1073,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c) low = fminf(low, y[i][nt][c]);
-        odd |= !part && low == -INFINITY;
+        // a score of -inf: plain_tiles (keys out of sight of MX caches have the lowest finite one)
+        if (__any_sync(0xffffffffu, low == -INFINITY)) odd = true;
         if (part) {
           low = 0.f;
 #pragma unroll
@@ -1081,10 +1082,8 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
+              for (int c = 0; c < 4; ++c)
                 if (y[i][nt][c] > -128.f) low = fminf(low, y[i][nt][c]);
-                odd |= fabsf(x[i][nt][c]) == INFINITY;
-              }
         }
         wide = low < -16.f;
       }
