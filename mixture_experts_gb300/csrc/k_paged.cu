@@ -8,8 +8,9 @@ namespace paged {
 namespace {
 
 // Block (c, y) joins the segment that starts in block c of the main kernel and
-// ends in a later one: its partial sums o, l with maxima m, in the order of the
-// blocks, o = sum o_k 2^(m_k - m). A group of registers is one 16 x 8 tile of
+// ends in a later one: its partial means o with weight sums l at maxima m, in the order
+// of the blocks, o = sum o_k l_k 2^(m_k - m) / sum l_k 2^(m_k - m), four at a time and a mean
+// throughout (sums could overflow where the result does not). A group of registers is one 16 x 8 tile of
 // O^T. With gridDim.y = 1 a warp takes whole groups; otherwise block y takes
 // group y and its warps share the partials. Latency bound: 4 to 6 us, of which
 // the launch lies under the main kernel (one context of 500009 tokens: 38 partials
@@ -47,16 +48,28 @@ __global__ void __launch_bounds__(256) k_join(const Params p) {
         for (int c = 0; c < 4; ++c) po[e][c] = in ? src[gr * 128 + c * 32 + lane] : 0.f;
       }
 #pragma unroll
-      for (int e = 0; e < kBatch; ++e)
+      for (int c = 0; c < 2; ++c) {
+        float top = m[c];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float top = fmaxf(m[c], pm[e][c]);
-          const float f = ex2(m[c] - top), fk = ex2(pm[e][c] - top);
-          m[c] = top;
-          l[c] = l[c] * f + pl[e][c] * fk;
-          o[c] = o[c] * f + po[e][c] * fk;
-          o[c + 2] = o[c + 2] * f + po[e][c + 2] * fk;
+        for (int e = 0; e < kBatch; ++e) top = fmaxf(top, pm[e][c]);
+        const float f = l[c] * ex2(m[c] - top);
+        float sum = f;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          pl[e][c] *= ex2(pm[e][c] - top);
+          sum += pl[e][c];
         }
+        const float by = sum == 0.f ? 0.f : reciprocal(sum);
+        o[c] *= f * by;
+        o[c + 2] *= f * by;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          o[c] = fmaf(po[e][c], pl[e][c] * by, o[c]);
+          o[c + 2] = fmaf(po[e][c + 2], pl[e][c] * by, o[c + 2]);
+        }
+        m[c] = top;
+        l[c] = sum;
+      }
     }
     if (shared) {
 #pragma unroll
@@ -72,11 +85,12 @@ __global__ void __launch_bounds__(256) k_join(const Params p) {
         m[c] = -FLT_MAX;
         for (int k = 0; k < 8; ++k) m[c] = fmaxf(m[c], s_ml[k][t][c]);
         l[c] = o[c] = o[c + 2] = 0.f;
+        for (int k = 0; k < 8; ++k) l[c] += s_ml[k][t][2 + c] * ex2(s_ml[k][t][c] - m[c]);
+        const float by = l[c] == 0.f ? 0.f : reciprocal(l[c]);
         for (int k = 0; k < 8; ++k) {
-          const float f = ex2(s_ml[k][t][c] - m[c]);
-          l[c] += s_ml[k][t][2 + c] * f;
-          o[c] += s_o[k][c][lane] * f;
-          o[c + 2] += s_o[k][c + 2][lane] * f;
+          const float f = s_ml[k][t][2 + c] * ex2(s_ml[k][t][c] - m[c]) * by;
+          o[c] = fmaf(s_o[k][c][lane], f, o[c]);
+          o[c + 2] = fmaf(s_o[k][c + 2][lane], f, o[c + 2]);
         }
       }
     }
@@ -86,10 +100,9 @@ __global__ void __launch_bounds__(256) k_join(const Params p) {
       const int r = row0 + nt * 8 + 2 * t + c;
       if (r >= p.group) continue;
       const int hq = h * p.group + r;
-      const float inv = l[c] == 0.f ? 0.f : 1.f / l[c];
       store_out<IN_ORDER, F32>(
           a, static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(hq) * D, i, g,
-          l[c] == 0.f ? 0.f : o[c] * inv, l[c] == 0.f ? 0.f : o[c + 2] * inv);
+          l[c] == 0.f ? 0.f : o[c], l[c] == 0.f ? 0.f : o[c + 2]);
       if (a.lse != nullptr && i == 0 && g == 0)
         a.lse[static_cast<size_t>(b) * a.n_q_heads + hq] =
             l[c] == 0.f ? -INFINITY : (m[c] + log2f(l[c])) * 0.6931471805599453f;

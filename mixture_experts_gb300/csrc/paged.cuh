@@ -19,7 +19,7 @@
 // its start and join cost, and the line is cut into equal pieces, one per block,
 // so ragged lengths load every SM alike and tiny segments do not queue up. A
 // block that covers a whole segment writes its output; a segment cut by block
-// borders leaves partial sums that k_join adds in the order of the blocks (no
+// borders leaves partial means and weights that k_join joins in the order of the blocks (no
 // atomics: the same bits every time). Within a block warp w takes steps w, w + W,
 // ... with its own ring of shared-memory slots filled by cp.async (rows past the
 // context zero-filled), so no warp waits for another before the segment's end,
@@ -53,7 +53,7 @@ struct Params {
   PagedArgs a;
   int group;       // query heads of a key head
   int blocks;      // blocks of 8 * NT heads a group is cut into
-  float* part;     // partial sums, two slots a block
+  float* part;     // partial means with their weights, two slots a block
   int4* span;      // per block: the cut segment that starts in it
   int direct;      // one block a segment: nothing is cut, nothing joined
 };
@@ -114,6 +114,12 @@ struct Cfg {
 COLI_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Of a sum of weights: 2^-8 or more.
+COLI_DEV float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 COLI_DEV uint32_t pack_f16x2(float lo, float hi) {
@@ -426,9 +432,10 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   constexpr int W = C::kWarps, kJ = DP / 32, kV = DP / 64;
   constexpr bool kF32 = FMT == DT_F32, kMx = C::kMx;
   // Weights are 2^kLift at a head's running maximum (m: the maximum - kLift) and rise to
-  // 2^kSlack times that before it is raised; fp16 weights (MX caches) so keep 9 bits or
-  // more down to 2^-30 of the largest.
-  constexpr float kSlack = kMx ? 1.f : 8.f, kLift = kMx ? 14.f : 0.f;
+  // 2^kSlack times that before it is raised: to 1, so that sums overflow no sooner than plain
+  // ones; or, in fp16 (MX caches, whose sums are relative to a scale), to 2^15, which keeps
+  // 9 bits or more down to 2^-30 of the largest.
+  constexpr float kSlack = kMx ? 1.f : 8.f, kLift = kMx ? 14.f : -8.f;
   extern __shared__ __align__(128) char smem[];
   __shared__ long long s_scan[W + 2];
   const PagedArgs& a = p.a;
@@ -1397,24 +1404,36 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     }
 
     // ---- join the warps ------------------------------------------------------------------
-    if constexpr (kMx) {
-#pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        const float f = ref[v] == -1000 ? 0.f : e8m0_f32(ref[v]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[v * 4 + i][nt][c] *= f;
-      }
-    }
+    // Each warp's sums over its weights' sum first: means of values, which cannot overflow.
+    // MX: on a value scale of 1 or more the reciprocal goes on the scale, so that neither
+    // product leaves the range before the result does.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], i);
+    float inv[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) inv[nt][c] = l[nt][c] == 0.f ? 0.f : reciprocal(l[nt][c]);
+#pragma unroll
+    for (int v = 0; v < DP / 64; ++v) {
+      const float f = !kMx ? 1.f : ref[v] == -1000 ? 0.f : e8m0_f32(ref[v]);
+      const float f0 = f < 1.f ? 1.f : f, f1 = f < 1.f ? f : 1.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float by = inv[nt][c] * f0;
+#pragma unroll
+          for (int i = v * 4; i < v * 4 + 4; ++i) {
+            acc[i][nt][c] = acc[i][nt][c] * by * f1;
+            acc[i][nt][c + 2] = acc[i][nt][c + 2] * by * f1;
+          }
+        }
+    }
     if (g == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -1422,20 +1441,14 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         for (int c = 0; c < 2; ++c) s_m[w * 8 * NT + nt * 8 + 2 * t + c] = m[nt][c];
     }
     __syncthreads();  // maxima in place
-    float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        top[nt][c] = -FLT_MAX;
+        float top = -FLT_MAX;
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-          top[nt][c] = fmaxf(top[nt][c], s_m[k * 8 * NT + nt * 8 + 2 * t + c]);
-        const float f = ex2(m[nt][c] - top[nt][c]);
-        l[nt][c] *= f;
-#pragma unroll
-        for (int i = 0; i < DP / 16; ++i) acc[i][nt][c] *= f, acc[i][nt][c + 2] *= f;
-        if (g == 0) s_l[w * 8 * NT + nt * 8 + 2 * t + c] = l[nt][c];
+        for (int k = 0; k < W; ++k) top = fmaxf(top, s_m[k * 8 * NT + nt * 8 + 2 * t + c]);
+        if (g == 0) s_l[w * 8 * NT + nt * 8 + 2 * t + c] = l[nt][c] * ex2(m[nt][c] - top);
       }
     float* merge = reinterpret_cast<float*>(smem + C::kRingBytes) + lane;
     float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (slot1 ? 1 : 0)) * C::kPart;
@@ -1450,20 +1463,24 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           for (int c = 0; c < 4; ++c)
             merge[(w * kHalf + i * NT + nt) * 128 + c * 32] = acc[rd * (DP / 32) + i][nt][c];
       __syncthreads();
-      // warp w adds the groups w, w + W, ... of all warps
+      // warp w joins the groups w, w + W, ... of all warps
       for (int k0 = w; k0 < kHalf; k0 += W) {
         const int gr = rd * kHalf + k0;
         const int i = gr / NT, nt = gr - i * NT;
-        float o[4] = {0.f, 0.f, 0.f, 0.f}, sum[2] = {0.f, 0.f}, mx[2] = {-FLT_MAX, -FLT_MAX};
-        for (int k = 0; k < W; ++k) {
-          const float* src = merge + (k * kHalf + k0) * 128;
+        float o[4] = {0.f, 0.f, 0.f, 0.f}, sum[2] = {0.f, 0.f}, mx[2] = {-FLT_MAX, -FLT_MAX}, by[2];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) o[c] += src[c * 32];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 2; ++c) {
+          for (int k = 0; k < W; ++k) {
             sum[c] += s_l[k * 8 * NT + nt * 8 + 2 * t + c];
             mx[c] = fmaxf(mx[c], s_m[k * 8 * NT + nt * 8 + 2 * t + c]);
           }
+          by[c] = sum[c] == 0.f ? 0.f : reciprocal(sum[c]);
+        }
+        for (int k = 0; k < W; ++k) {
+          const float* src = merge + (k * kHalf + k0) * 128;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            o[c] = fmaf(src[c * 32], s_l[k * 8 * NT + nt * 8 + 2 * t + (c & 1)] * by[c & 1], o[c]);
         }
         if (!whole) {
 #pragma unroll
@@ -1481,10 +1498,9 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             const int r = orow0 + nt * 8 + 2 * t + c;
             if (r >= p.group) continue;
             const int hq = oh * p.group + r;
-            const float inv = sum[c] == 0.f ? 0.f : 1.f / sum[c];
             store_out<FMT == DT_BF16, kF32>(
                 a, static_cast<size_t>(ob) * a.out_stride + static_cast<size_t>(hq) * D, i, g,
-                sum[c] == 0.f ? 0.f : o[c] * inv, sum[c] == 0.f ? 0.f : o[c + 2] * inv);
+                sum[c] == 0.f ? 0.f : o[c], sum[c] == 0.f ? 0.f : o[c + 2]);
             if (a.lse != nullptr && i == 0 && g == 0)
               a.lse[static_cast<size_t>(ob) * a.n_q_heads + hq] =
                   sum[c] == 0.f ? -INFINITY : (mx[c] + log2f(sum[c])) * 0.6931471805599453f;

@@ -115,6 +115,34 @@ def test_zeros_under_any_scale(hq, D, byte, fmt):
     compare(c, table, sl, rows, q, fmt)
 
 
+# ---- sums near the largest number --------------------------------------------------------
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("n,top", [(3, 125), (200, 119), (12000, 112)])
+def test_sums_of_large_values_stay_finite(n, top, fmt):
+    """Equal weights over n values of about 2^top: their plain sum is finite, and so is
+    the result."""
+    g = gen(5, n, top)
+    D = 64
+    k = torch.zeros(n, 1, D)
+    v = (1.0 + torch.rand(n, 1, D, generator=g)) * 2.0 ** top
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = randn(g, 1, 4, D, dtype=act(fmt))
+    compare(c, table, sl, rows, q, fmt)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_large_values_under_rising_weights(fmt):
+    """Scores that rise by less than the running maximum's slack after the first keys."""
+    g = gen(6)
+    n, D = 512, 64
+    k = torch.zeros(n, 1, D)
+    k[256:] = 0.65                                    # 0.65 * 64 / 8 = 5.2: a factor of 2^7.5
+    v = (1.0 + torch.rand(n, 1, D, generator=g)) * 2.0 ** 118
+    c, table, sl, rows = one_sequence(fmt, k, v)
+    q = torch.ones(1, 4, D).to(act(fmt)).cuda()
+    compare(c, table, sl, rows, q, fmt)
+
+
 # ---- keys and queries of opposite extremes -----------------------------------------------
 @pytest.mark.parametrize("fmt", list(FMT))
 @pytest.mark.parametrize("e", [60, 100, 110, 118])
