@@ -107,3 +107,50 @@ def test_every_tile_counts_once(lens, hq, hk, D, page, window, fmt):
         tol, tol_lse = ab.flat_bound(fmt, out, n - first)
         assert ((got[b] - out).abs() <= tol).all()
         assert ((lse[b] - ab.log_of(n - first)).abs() <= tol_lse).all()
+
+
+LEFT_OUT = ["first", "last", "run", "alternate", "third", "all but one", "all"]
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("B,hq,hk,D,page,n,window", [
+    (1, 4, 1, 64, 16, 12000, 0), (1, 32, 2, 128, 32, 12000, 0), (3, 6, 2, 256, 16, 5000, 0),
+    (96, 16, 8, 64, 16, 9000, 0), (64, 32, 2, 128, 64, 9000, 2500), (20, 8, 2, 64, 48, 900, 0)])
+def test_left_out_pages_anywhere(B, hq, hk, D, page, n, window, fmt):
+    """Pages outside the pool at the ends of long contexts, in runs longer than a block's
+    piece, every second one: only they are missing, also where a warp takes more than 32 tiles.
+    All sequences draw from the same pages, whose tiles are marked as above."""
+    g = torch.Generator().manual_seed(B + n)
+    dt = torch.float32 if fmt == "f32" else torch.bfloat16
+    pages, per = 90, -(-n // page)
+    c = moe.PagedKVCache.empty(pages, page, hk, D, FMT[fmt])
+    j = torch.arange(pages * page)
+    v = torch.zeros(len(j), hk, D, dtype=dt)
+    v[j, :, j // 16 % D] = 1.0
+    c.append(torch.randn(len(j), hk, D, generator=g).to(dt).cuda(), v.cuda(), j.int().cuda())
+    table = torch.randint(0, pages, (B, per), generator=g).int()
+    lens = n - torch.arange(B) * 7 % 50
+    bad = torch.tensor([pages, -1, -7, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    for b in range(B):
+        at = torch.arange(per)
+        kind = LEFT_OUT[b % len(LEFT_OUT)] if B > 1 else "run"
+        out = {"first": at < 3, "last": at >= per - 2, "run": (at > per // 5) & (at < per // 2),
+               "alternate": at % 2 == 1, "third": at % 3 == b % 3, "all but one": at != per - 2,
+               "all": at >= 0}[kind]
+        table[b] = torch.where(out, bad[(at + b) % len(bad)], table[b])
+    q = torch.randn(B, hq, D, generator=g).to(dt).cuda()
+    got, lse = (x.cpu().double() for x in c.attend(
+        q, table.cuda(), lens.int().cuda(), scale=0.0, window=window, return_lse=True))
+    assert moe.coli_device_status() == moe.COLI_EDEVICE
+    for b in range(B):
+        m = int(lens[b])
+        key = torch.arange(max(0, m - window) if window else 0, m)
+        at = table[b, key // page].long()
+        key, at = key[(at >= 0) & (at < pages)], at[(at >= 0) & (at < pages)]
+        if len(key) == 0:
+            assert not got[b].any() and (lse[b] == -torch.inf).all()
+            continue
+        out = torch.bincount((at * page + key % page) // 16 % D, minlength=D).double() / len(key)
+        tol, tol_lse = ab.flat_bound(fmt, out, m)
+        assert ((got[b] - out).abs() <= tol).all()
+        assert ((lse[b] - ab.log_of(len(key))).abs() <= tol_lse).all()
