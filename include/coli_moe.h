@@ -314,22 +314,32 @@ typedef enum { COLI_ROPE_HALF = 0, COLI_ROPE_INTERLEAVED = 1 } coli_rope_layout;
  *   NTK     base replaced by base * factor^(rot_dim/(rot_dim-2));
  *   YARN    w_i * g_i + (w_i / factor) * (1 - g_i), where
  *           g_i = clamp((turns_i - beta_slow) / (beta_fast - beta_slow), 0, 1)
- *           and turns_i = original_positions * w_i / (2 pi). */
+ *           and turns_i = original_positions * w_i / (2 pi): the ramp runs over the turns,
+ *           as the method was published;
+ *   YARN_INDEX  the same blend with the ramp over the pair's index, as models
+ *           trained with the method's released code (and most servers) have it:
+ *           g_i = 1 - clamp((i - lo) / (hi - lo), 0, 1), where with
+ *           at(t) = rot_dim * ln(original_positions / (2 pi t)) / (2 ln base), the
+ *           index that makes t turns, lo = max(floor(at(beta_fast)), 0) and
+ *           hi = min(ceil(at(beta_slow)), rot_dim - 1), 0.001 more if hi = lo.
+ * The two differ by up to a factor of 3 in the frequencies between: a checkpoint needs
+ * the one it was trained with. */
 typedef enum {
   COLI_ROPE_NONE = 0,
   COLI_ROPE_LINEAR = 1,
   COLI_ROPE_NTK = 2,
-  COLI_ROPE_YARN = 3
+  COLI_ROPE_YARN = 3,
+  COLI_ROPE_YARN_INDEX = 16 + COLI_ROPE_YARN
 } coli_rope_scaling;
 
 typedef struct {
   int32_t rot_dim;            /* even, 2..256 */
   int32_t scaling;            /* coli_rope_scaling */
-  int32_t original_positions; /* YARN: trained context length (> 0) */
-  double base;                /* > 0 */
-  double factor;              /* LINEAR, NTK, YARN: context factor (> 0) */
-  double beta_fast;           /* YARN: turns above which w_i is kept (> beta_slow) */
-  double beta_slow;           /* YARN: turns below which w_i is divided */
+  int32_t original_positions; /* YARN, YARN_INDEX: trained context length (> 0) */
+  double base;                /* > 0 (YARN_INDEX: > 1) */
+  double factor;              /* all but NONE: context factor (> 0) */
+  double beta_fast;           /* YARN*: turns above which w_i is kept (> beta_slow) */
+  double beta_slow;           /* YARN*: turns below which w_i is divided (INDEX: > 0) */
   double amplitude;           /* factor on cosines and sines (1; YaRN: 0.1 ln(factor) + 1) */
 } coli_rope_config;
 

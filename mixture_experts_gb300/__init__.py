@@ -18,7 +18,7 @@ import threading
 F32, BF16, I4G128, MXFP8, MXFP4 = 0, 1, 2, 3, 4
 PATH_AUTO, PATH_DECODE, PATH_PREFILL = 0, 1, 2
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
-ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
+ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_YARN_INDEX = 0, 1, 2, 3, 19
 STATUS = {0: "COLI_OK", -1: "COLI_EINVAL", -2: "COLI_ENOMEM", -3: "COLI_ECUDA",
           -4: "COLI_EUNSUPPORTED", -5: "COLI_EDEVICE", -6: "COLI_ETIMEOUT"}
 COLI_OK, COLI_EINVAL, COLI_ENOMEM, COLI_ECUDA = 0, -1, -2, -3
@@ -488,7 +488,8 @@ class Rotary:
     def build(cls, rot_dim, n_positions, base=10000.0, layout="half", scaling=ROPE_NONE,
               factor=1.0, original_positions=0, beta_fast=32.0, beta_slow=1.0, amplitude=1.0,
               stream=None):
-        """Builds the table (coli_rope_table) and keeps it."""
+        """Builds the table (coli_rope_table) and keeps it. ROPE_YARN blends over the turns a
+        pair makes, as published; ROPE_YARN_INDEX over its index, as most checkpoints need."""
         torch = _t()
         if stream is not None:
             with _on(stream):

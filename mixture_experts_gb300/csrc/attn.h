@@ -16,7 +16,9 @@ constexpr int kMxBlock = 32;
 // ---- rotary positions ---------------------------------------------------------
 struct RopeFreq {
   int scaling;
-  double base, factor, turns_per_w, beta_slow, beta_span, amplitude;
+  // YARN: w_i is kept where turns_per_w w_i passes ramp_from + ramp_span; YARN_INDEX:
+  // divided where i does
+  double base, factor, turns_per_w, ramp_from, ramp_span, amplitude;
 };
 cudaError_t launch_rope_table(const RopeFreq& f, int rot_dim, int n_positions, float* table,
                               cudaStream_t st);

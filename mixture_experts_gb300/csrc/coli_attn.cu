@@ -133,17 +133,21 @@ int coli_rope_table(const coli_rope_config* cfg, int32_t n_positions, float* tab
                   n_positions);
   if (misaligned(table, 16)) return reject(COLI_EINVAL, "table must be 16-byte aligned");
   const int s = cfg->scaling;
-  if (s < COLI_ROPE_NONE || s > COLI_ROPE_YARN) return reject(COLI_EINVAL, "bad scaling %d", s);
+  const bool by_index = s == COLI_ROPE_YARN_INDEX;
+  if ((s < COLI_ROPE_NONE || s > COLI_ROPE_YARN) && !by_index)
+    return reject(COLI_EINVAL, "bad scaling %d", s);
   if (!(cfg->base > 0) || !isfinite(cfg->base) || !isfinite(cfg->amplitude))
     return reject(COLI_EINVAL, "base must be positive and finite, amplitude finite");
   if (s != COLI_ROPE_NONE && (!(cfg->factor > 0) || !isfinite(cfg->factor)))
     return reject(COLI_EINVAL, "factor must be positive and finite");
   if (s == COLI_ROPE_NTK && cfg->rot_dim == 2)
     return reject(COLI_EINVAL, "NTK scaling needs rot_dim above 2");
-  if (s == COLI_ROPE_YARN &&
+  if ((s == COLI_ROPE_YARN || by_index) &&
       (cfg->original_positions < 1 || !(cfg->beta_fast > cfg->beta_slow) ||
        !isfinite(cfg->beta_fast) || !isfinite(cfg->beta_slow)))
     return reject(COLI_EINVAL, "YaRN needs original_positions >= 1 and beta_fast > beta_slow");
+  if (by_index && (!(cfg->base > 1) || !(cfg->beta_slow > 0)))
+    return reject(COLI_EINVAL, "YaRN by index needs base > 1 and beta_slow > 0");
   RopeFreq f{};
   f.scaling = s;
   f.base = s == COLI_ROPE_NTK
@@ -151,8 +155,17 @@ int coli_rope_table(const coli_rope_config* cfg, int32_t n_positions, float* tab
                : cfg->base;
   f.factor = cfg->factor;
   f.turns_per_w = cfg->original_positions / 6.283185307179586476925;
-  f.beta_slow = cfg->beta_slow;
-  f.beta_span = cfg->beta_fast - cfg->beta_slow;
+  f.ramp_from = cfg->beta_slow;
+  f.ramp_span = cfg->beta_fast - cfg->beta_slow;
+  if (by_index) {
+    auto at = [&](double turns) {
+      return cfg->rot_dim * log(f.turns_per_w / turns) / (2 * log(cfg->base));
+    };
+    const double lo = fmax(floor(at(cfg->beta_fast)), 0.0);
+    const double hi = fmin(ceil(at(cfg->beta_slow)), cfg->rot_dim - 1.0);
+    f.ramp_from = lo;
+    f.ramp_span = hi == lo ? 0.001 : hi - lo;
+  }
   f.amplitude = cfg->amplitude;
   return launched(launch_rope_table(f, cfg->rot_dim, n_positions, table,
                                     static_cast<cudaStream_t>(stream)),

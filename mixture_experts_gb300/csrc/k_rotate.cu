@@ -22,6 +22,7 @@
 // 340 MB in 55.6 us, 6.1 TB/s; rotated and stored as MXFP8 379 MB in 68.3 us,
 // 5.5 TB/s, where the quantiser's shuffles and conversions also show); the chain
 // position -> table row -> store for a decode batch (32 tokens: 4 us).
+#include "../../include/coli_moe.h"
 #include "attn.h"
 #include "common.cuh"
 #include "mx.cuh"
@@ -348,10 +349,12 @@ __global__ void k_rope_table(RopeFreq f, int half, int n, float2* __restrict__ t
   if (e >= static_cast<uint32_t>(n) * half) return;
   const int pos = e / half, i = e % half;
   double w = pow(f.base, -static_cast<double>(i) / half);
-  if (f.scaling == 1) w /= f.factor;
-  if (f.scaling == 3) {
-    double keep = (f.turns_per_w * w - f.beta_slow) / f.beta_span;
+  if (f.scaling == COLI_ROPE_LINEAR) w /= f.factor;
+  if (f.scaling == COLI_ROPE_YARN || f.scaling == COLI_ROPE_YARN_INDEX) {
+    const bool by_index = f.scaling == COLI_ROPE_YARN_INDEX;
+    double keep = ((by_index ? i : f.turns_per_w * w) - f.ramp_from) / f.ramp_span;
     keep = fmin(fmax(keep, 0.0), 1.0);
+    if (by_index) keep = 1.0 - keep;
     w = w * keep + w / f.factor * (1.0 - keep);
   }
   double s, c;
