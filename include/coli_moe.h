@@ -297,8 +297,9 @@ int coli_permute_noalloc(const int32_t* topk_idx, const void* x, int32_t T, int3
  * weights-in-HBM serving loop as the layer above (the pages keep a KV cache
  * next to the experts: overview page section 3.4). Activations are bf16 or
  * f32 with fp32 arithmetic; the cache keeps keys and values in the library's
- * own formats. These calls take no handle: every buffer is the caller's, the
- * structs below are read during the call and may be temporary. Rows of heads
+ * own formats. These calls take no handle: every buffer is the caller's, on the
+ * current device (where the launch goes), the structs below are read during the
+ * call and may be temporary. Rows of heads
  * ([T][n_heads][head_dim]) take a stride in ELEMENTS between tokens, so a
  * slice of a fused projection's output can be passed as it is; pointers and
  * strides must keep every row 16-byte aligned. */

@@ -435,12 +435,32 @@ def _current_stream(x) -> int:
     return _torch._C._cuda_getCurrentRawStream(x.get_device())
 
 
-def _head_rows(name, x, n_heads, head_dim, dtype) -> int:
+def _current_device() -> int:
+    return _torch._C._cuda_getDevice()
+
+
+def _device_of(name, x) -> int:
+    """Index of x's device, which has to be the current one: that is where the library
+    launches, and a stream's raw handle does not say whose it is."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: need a CUDA tensor, got {x.device}")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is "
+                         f"cuda:{_current_device()}")
+    return dev
+
+
+def _head_rows(name, x, n_heads, head_dim, dtype, dev=None) -> int:
     """Token stride (elements) of x [T][n_heads][head_dim], whose heads are
-    contiguous; raises ValueError on anything the kernels would misread."""
-    if x.dim() != 3 or x.dtype is not dtype or not x.is_cuda:
+    contiguous; raises ValueError on anything the kernels would misread. dev: the
+    device of the call."""
+    at = x.get_device()
+    if x.dim() != 3 or x.dtype is not dtype or at < 0:
         raise ValueError(f"{name}: need a CUDA {dtype} tensor [T][heads][head_dim], got "
                          f"{x.device} {x.dtype} {tuple(x.shape)}")
+    if at != dev and dev is not None:
+        raise ValueError(f"{name} is on cuda:{at}, not on cuda:{dev}")
     T, h, d = x.shape
     if h != n_heads or d != head_dim:
         raise ValueError(f"{name}: shape {tuple(x.shape)} does not fit {n_heads} heads of "
@@ -451,12 +471,12 @@ def _head_rows(name, x, n_heads, head_dim, dtype) -> int:
     return s0 if T > 1 else h * d
 
 
-def _ids(name, x, n) -> int:
-    """Address of a contiguous int32 CUDA vector of n entries."""
-    if x.dtype is not _torch.int32 or not x.is_cuda or x.dim() != 1 or x.shape[0] != n or \
-            not x.is_contiguous():
-        raise ValueError(f"{name}: need a contiguous int32 CUDA vector of {n}, got {x.device} "
-                         f"{x.dtype} {tuple(x.shape)}")
+def _ids(name, x, n, dev) -> int:
+    """Address of a contiguous int32 vector of n entries on device dev."""
+    if x.dtype is not _torch.int32 or x.get_device() != dev or x.dim() != 1 or \
+            x.shape[0] != n or not x.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous int32 vector of {n} on cuda:{dev}, got "
+                         f"{x.device} {x.dtype} {tuple(x.shape)}")
     return x.data_ptr()
 
 
@@ -471,7 +491,8 @@ def _on(stream):
 
 class Rotary:
     """A rotary table ([n_positions][rot_dim/2][2] f32, cosines and sines) with
-    the layout it is applied in: "half" or "interleaved" (or ROPE_*)."""
+    the layout it is applied in: "half" or "interleaved" (or ROPE_*). It serves calls
+    on its own device, which has to be the current one."""
 
     def __init__(self, table, layout="half"):
         torch = _t()
@@ -479,7 +500,7 @@ class Rotary:
         if table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous() or \
                 table.dtype is not torch.float32 or not table.is_cuda:
             raise ValueError("table: need a contiguous f32 CUDA tensor [n_positions][rot/2][2]")
-        self.table = table
+        self.table, self._dev = table, table.get_device()
         self.c = coli_rotary(table.data_ptr(), table.shape[0], 2 * table.shape[1], lay, 0)
         self.c_inverse = coli_rotary(table.data_ptr(), table.shape[0], 2 * table.shape[1], lay, 1)
         self._ref, self._ref_inverse = ctypes.byref(self.c), ctypes.byref(self.c_inverse)
@@ -520,30 +541,34 @@ def rope(rotary: Rotary, positions, q, k=None, q_out=None, k_out=None, inverse=F
     if q.dim() != 3:
         raise ValueError(f"q: need [T][heads][head_dim], got {tuple(q.shape)}")
     T, hq, d = q.shape
-    qs = _head_rows("q", q, hq, d, dt)
+    dev = _device_of("q", q)
+    if rotary._dev != dev:
+        raise ValueError(f"the rotary table is on cuda:{rotary._dev}, not on cuda:{dev}")
+    qs = _head_rows("q", q, hq, d, dt, dev)
     if q_out is None:
         q_out = torch.empty((T, hq, d), dtype=dt, device=q.device)
         qos = hq * d
     else:
-        qos = _head_rows("q_out", q_out, hq, d, dt)
+        qos = _head_rows("q_out", q_out, hq, d, dt, dev)
         if q_out.shape[0] != T:
             raise ValueError("q and q_out need the same number of tokens")
+    pp = _ids("positions", positions, T, dev)
     kp = kop = None
     hk = ks = kos = 0
     if k is not None:
         hk = k.shape[1]
-        ks = _head_rows("k", k, hk, d, dt)
+        ks = _head_rows("k", k, hk, d, dt, dev)
         if k_out is None:
             k_out = torch.empty((k.shape[0], hk, d), dtype=dt, device=q.device)
             kos = hk * d
         else:
-            kos = _head_rows("k_out", k_out, hk, d, dt)
+            kos = _head_rows("k_out", k_out, hk, d, dt, dev)
         if k.shape[0] != T or k_out.shape[0] != T:
             raise ValueError("q and k need the same number of tokens")
         kp, kop = k.data_ptr(), k_out.data_ptr()
-    rc = lib().coli_rope_apply(rotary._ref_inverse if inverse else rotary._ref,
-                               _ids("positions", positions, T), T, d, act, q.data_ptr(), qs, hq,
-                               q_out.data_ptr(), qos, kp, ks, hk, kop, kos, _current_stream(q))
+    rc = lib().coli_rope_apply(rotary._ref_inverse if inverse else rotary._ref, pp, T, d, act,
+                               q.data_ptr(), qs, hq, q_out.data_ptr(), qos, kp, ks, hk, kop, kos,
+                               _current_stream(q))
     if rc:
         _check(rc, "coli_rope_apply")
     return q_out, k_out
@@ -553,14 +578,16 @@ class PagedKVCache:
     """Pages of keys and values in the caller's tensors: k, v
     [n_pages][n_kv_heads][page_size][row] of float32, bfloat16 or (MX) uint8,
     with MX scales [..][page_size][S] uint8, S = head_dim/32 rounded up to a
-    multiple of 4. The format follows from the type and the row length."""
+    multiple of 4. The format follows from the type and the row length. Calls take
+    tensors of the pages' device, which has to be the current one."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None, head_dim=None):
         torch = _t()
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or \
-                not (k.is_contiguous() and v.is_contiguous() and k.is_cuda and v.is_cuda):
+                not (k.is_contiguous() and v.is_contiguous() and k.is_cuda) or \
+                v.get_device() != k.get_device():
             raise ValueError("k and v: need equal contiguous CUDA tensors "
-                             "[n_pages][n_kv_heads][page_size][row]")
+                             "[n_pages][n_kv_heads][page_size][row] on one device")
         n_pages, hk, page, row = k.shape
         head_dim = row if head_dim is None else head_dim
         dtype = {(torch.float32, head_dim): F32, (torch.bfloat16, head_dim): BF16,
@@ -572,10 +599,12 @@ class PagedKVCache:
             want = (n_pages, hk, page, (head_dim // 32 + 3) // 4 * 4)
             for s in (k_scale, v_scale):
                 if s is None or tuple(s.shape) != want or s.dtype != torch.uint8 or \
-                        not s.is_contiguous() or not s.is_cuda:
-                    raise ValueError(f"k_scale and v_scale: need contiguous uint8 CUDA {want}")
+                        not s.is_contiguous() or s.get_device() != k.get_device():
+                    raise ValueError(f"k_scale and v_scale: need contiguous uint8 {want} on the "
+                                     "device of k and v")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_kv_heads, self.head_dim, self.page_size = hk, head_dim, page
+        self._dev = k.get_device()
         self.act_torch = torch.float32 if dtype == F32 else torch.bfloat16
         self.c = coli_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), n_pages, page, hk,
                                head_dim, dtype)
@@ -595,6 +624,13 @@ class PagedKVCache:
             pools += [torch.zeros(*shape, s, dtype=torch.uint8, device="cuda") for _ in range(2)]
         return cls(*pools, head_dim=head_dim)
 
+    def _device(self) -> int:
+        """The pool's device, which has to be the current one (see _device_of)."""
+        if self._dev != _current_device():
+            raise ValueError(f"the cache is on cuda:{self._dev}, but the current device is "
+                             f"cuda:{_current_device()}")
+        return self._dev
+
     def append(self, k, v, slots, rotary: Rotary = None, positions=None, q=None, q_out=None,
                stream=None):
         """Stores token t's k[t], v[t] at slots[t] (-1: skipped), keys rotated
@@ -603,30 +639,33 @@ class PagedKVCache:
             with _on(stream):
                 return self.append(k, v, slots, rotary, positions, q, q_out)
         T, hk, d, dt = k.shape[0], self.n_kv_heads, self.head_dim, self.act_torch
-        ks = _head_rows("k", k, hk, d, dt)
-        vs = _head_rows("v", v, hk, d, dt)
+        dev = self._device()
+        ks = _head_rows("k", k, hk, d, dt, dev)
+        vs = _head_rows("v", v, hk, d, dt, dev)
         if v.shape[0] != T:
             raise ValueError("k and v need the same number of tokens")
+        at = _ids("slots", slots, T, dev)
         rp = pp = qp = qop = None
         hq = qs = qos = 0
         if rotary is not None:
             if positions is None:
                 raise ValueError("a rotary needs positions")
-            rp, pp = rotary._ref, _ids("positions", positions, T)
+            if rotary._dev != dev:
+                raise ValueError(f"the rotary table is on cuda:{rotary._dev}, not on cuda:{dev}")
+            rp, pp = rotary._ref, _ids("positions", positions, T, dev)
         if q is not None:
             hq = q.shape[1]
-            qs = _head_rows("q", q, hq, d, dt)
+            qs = _head_rows("q", q, hq, d, dt, dev)
             if q_out is None:
                 q_out = _torch.empty((q.shape[0], hq, d), dtype=dt, device=q.device)
                 qos = hq * d
             else:
-                qos = _head_rows("q_out", q_out, hq, d, dt)
+                qos = _head_rows("q_out", q_out, hq, d, dt, dev)
             if q.shape[0] != T or q_out.shape[0] != T:
                 raise ValueError("q and k need the same number of tokens")
             qp, qop = q.data_ptr(), q_out.data_ptr()
-        rc = lib().coli_kv_append(self._ref, k.data_ptr(), ks, v.data_ptr(), vs,
-                                  _ids("slots", slots, T), T, rp, pp, qp, qs, hq, qop, qos,
-                                  _current_stream(k))
+        rc = lib().coli_kv_append(self._ref, k.data_ptr(), ks, v.data_ptr(), vs, at, T, rp, pp, qp,
+                                  qs, hq, qop, qos, _current_stream(k))
         if rc:
             _check(rc, "coli_kv_append")
         return q_out if q is not None else None
@@ -637,10 +676,11 @@ class PagedKVCache:
             with _on(stream):
                 return self.read(slots)
         N, h, d = slots.shape[0], self.n_kv_heads, self.head_dim
+        at = _ids("slots", slots, N, self._device())
         k = _torch.empty((N, h, d), dtype=self.act_torch, device=slots.device)
         v = _torch.empty((N, h, d), dtype=self.act_torch, device=slots.device)
-        rc = lib().coli_kv_read(self._ref, _ids("slots", slots, N), N, k.data_ptr(), h * d,
-                                v.data_ptr(), h * d, _current_stream(k))
+        rc = lib().coli_kv_read(self._ref, at, N, k.data_ptr(), h * d, v.data_ptr(), h * d,
+                                _current_stream(k))
         if rc:
             _check(rc, "coli_kv_read")
         return k, v
@@ -655,17 +695,21 @@ class PagedKVCache:
                 return self.attend(q, block_table, seq_lens, scale, window, out, return_lse)
         torch, d, dt = _torch, self.head_dim, self.act_torch
         B, hq = q.shape[0], q.shape[1]
-        qs = _head_rows("q", q, hq, d, dt)
+        dev = self._device()
+        qs = _head_rows("q", q, hq, d, dt, dev)
         if out is None:
             out = torch.empty((B, hq, d), dtype=dt, device=q.device)
             os_ = hq * d
         else:
-            os_ = _head_rows("out", out, hq, d, dt)
+            os_ = _head_rows("out", out, hq, d, dt, dev)
             if out.shape[0] != B:
                 raise ValueError("q and out need the same number of sequences")
-        if block_table.dim() != 2 or block_table.shape[0] != B or not block_table.is_cuda or \
-                block_table.dtype is not torch.int32 or not block_table.is_contiguous():
-            raise ValueError(f"block_table: need a contiguous int32 CUDA tensor [{B}][max_pages]")
+        if block_table.dim() != 2 or block_table.shape[0] != B or \
+                block_table.get_device() != dev or block_table.dtype is not torch.int32 or \
+                not block_table.is_contiguous():
+            raise ValueError(f"block_table: need a contiguous int32 tensor [{B}][max_pages] on "
+                             f"cuda:{dev}")
+        lens = _ids("seq_lens", seq_lens, B, dev)
         lse = torch.empty((B, hq), dtype=torch.float32, device=q.device) if return_lse else None
         L = lib()
         pages = block_table.shape[1]
@@ -680,8 +724,7 @@ class PagedKVCache:
         _, cfg_ref, n = call
         scratch = torch.empty((n,), dtype=torch.uint8, device=q.device) if n else None
         rc = L.coli_paged_attention(self._ref, cfg_ref, q.data_ptr(), qs, B,
-                                    block_table.data_ptr(), pages,
-                                    _ids("seq_lens", seq_lens, B), out.data_ptr(), os_,
+                                    block_table.data_ptr(), pages, lens, out.data_ptr(), os_,
                                     None if lse is None else lse.data_ptr(),
                                     None if scratch is None else scratch.data_ptr(), n,
                                     _current_stream(q))

@@ -25,3 +25,97 @@ def test_yarn_over_the_index_rejects(field, value):
     setattr(cfg, field, value)
     assert moe.coli_rope_table(cfg, 128, FAKE, stream=0) == moe.COLI_EINVAL
     assert moe.last_error()
+
+
+# ---- devices ----------------------------------------------------------------------------
+class Standin:
+    """What the wrappers ask of a tensor, on any device index; nothing is behind it."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, dev):
+        self.shape, self.dtype, self._dev, self.device = shape, dtype, dev, f"cuda:{dev}"
+
+    def get_device(self):
+        return self._dev
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        s = [1]
+        for n in self.shape[:0:-1]:
+            s.append(s[-1] * n)
+        return tuple(s[::-1])
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+
+@pytest.fixture
+def devices(monkeypatch):
+    """Makers of stand-ins, device 0 current, and a library that must not be called."""
+    import torch
+    moe._t()
+
+    def called():
+        raise AssertionError("the library was called")
+    monkeypatch.setattr(moe, "lib", called)
+    monkeypatch.setattr(moe, "_current_device", lambda: 0, raising=False)
+
+    def rows(dev, heads=2):
+        return Standin((3, heads, 64), torch.bfloat16, dev)
+
+    def ids(dev):
+        return Standin((3,), torch.int32, dev)
+
+    def cache(dev, scale_dev=None):
+        k, v = (Standin((4, 2, 16, 64), torch.uint8, dev) for _ in range(2))
+        s = [Standin((4, 2, 16, 4), torch.uint8, dev if scale_dev is None else scale_dev)
+             for _ in range(2)]
+        return moe.PagedKVCache(k, v, *s, head_dim=64)
+
+    def rotary(dev):
+        return moe.Rotary(Standin((8, 32, 2), torch.float32, dev))
+
+    def table(dev):
+        return Standin((3, 4), torch.int32, dev)
+    return rows, ids, cache, rotary, table
+
+
+def test_wrappers_refuse_other_devices(devices):
+    rows, ids, cache, rotary, table = devices
+    c, r = cache(0), rotary(0)
+    other = cache(1)
+    for bad in (
+            lambda: moe.rope(rotary(1), ids(1), rows(1)), lambda: moe.rope(r, ids(0), rows(1)),
+            lambda: moe.rope(rotary(1), ids(0), rows(0)),
+            lambda: moe.rope(r, ids(1), rows(0), q_out=rows(0)),
+            lambda: moe.rope(r, ids(0), rows(0), rows(1), q_out=rows(0)),
+            lambda: moe.rope(r, ids(0), rows(0), q_out=rows(1)),
+            lambda: moe.rope(r, ids(0), rows(0), rows(0), q_out=rows(0), k_out=rows(1)),
+            lambda: cache(0, 1), lambda: other.append(rows(1), rows(1), ids(1)),
+            lambda: c.append(rows(1), rows(0), ids(0)), lambda: c.append(rows(0), rows(1), ids(0)),
+            lambda: c.append(rows(0), rows(0), ids(1)),
+            lambda: c.append(rows(0), rows(0), ids(0), rotary=rotary(1), positions=ids(0)),
+            lambda: c.append(rows(0), rows(0), ids(0), rotary=r, positions=ids(1)),
+            lambda: c.append(rows(0), rows(0), ids(0), rotary=r, positions=ids(0), q=rows(1)),
+            lambda: c.append(rows(0), rows(0), ids(0), rotary=r, positions=ids(0), q=rows(0),
+                             q_out=rows(1)),
+            lambda: other.read(ids(1)), lambda: c.read(ids(1)),
+            lambda: other.attend(rows(1), table(1), ids(1)),
+            lambda: c.attend(rows(1), table(0), ids(0)),
+            lambda: c.attend(rows(0), table(1), ids(0), out=rows(0)),
+            lambda: c.attend(rows(0), table(0), ids(0), out=rows(1)),
+            lambda: c.attend(rows(0), table(0), ids(1), out=rows(0))):
+        with pytest.raises(ValueError, match="cuda:|device"):
+            bad()
+
+
+def test_pools_of_two_devices_are_refused(devices):
+    import torch
+    k, v = (Standin((4, 2, 16, 64), torch.bfloat16, d) for d in (0, 1))
+    with pytest.raises(ValueError, match="one device"):
+        moe.PagedKVCache(k, v)
