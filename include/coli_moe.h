@@ -302,7 +302,8 @@ int coli_permute_noalloc(const int32_t* topk_idx, const void* x, int32_t T, int3
  * call and may be temporary. Rows of heads
  * ([T][n_heads][head_dim]) take a stride in ELEMENTS between tokens, so a
  * slice of a fused projection's output can be passed as it is; pointers and
- * strides must keep every row 16-byte aligned. */
+ * strides must keep every row 16-byte aligned, vectors of positions, slots, pages,
+ * lengths and log-sum-exps 4-byte. */
 
 /* Pairs turned together: elements i and i + rot_dim/2 (HALF), or 2i and
  * 2i + 1 (INTERLEAVED), for i < rot_dim/2. Elements from rot_dim on are kept. */

@@ -45,6 +45,13 @@ int check_rows(const char* name, const void* p, size_t stride, int n_heads, int 
   return COLI_OK;
 }
 
+// A vector of 32-bit ids, lengths or results.
+int check_words(const char* name, const void* p) {
+  if (p == nullptr) return reject(COLI_EINVAL, "%s must be set", name);
+  if (misaligned(p, 4)) return reject(COLI_EINVAL, "%s must be 4-byte aligned", name);
+  return COLI_OK;
+}
+
 int check_heads(const char* name, int n) {
   return n >= 1 && n <= 1024 ? COLI_OK : reject(COLI_EINVAL, "%s=%d outside 1..1024", name, n);
 }
@@ -59,6 +66,7 @@ int check_head_dim(int head_dim) {
 int check_rotary(const coli_rotary* r, const int32_t* positions, int head_dim, RotaryView* out) {
   if (r->table == nullptr || positions == nullptr || misaligned(r->table, 16))
     return reject(COLI_EINVAL, "rotary table (16-byte aligned) and positions must be set");
+  if (int rc = check_words("positions", positions)) return rc;
   if (r->rot_dim < 2 || r->rot_dim > head_dim || r->rot_dim % 2)
     return reject(COLI_EINVAL, "rot_dim=%d is not even in 2..head_dim=%d", r->rot_dim, head_dim);
   if (r->layout != COLI_ROPE_HALF && r->layout != COLI_ROPE_INTERLEAVED)
@@ -219,7 +227,7 @@ int coli_kv_append(const coli_kv_cache* cache, const void* k, size_t k_stride, c
   if (int rc = check_tokens("T", T)) return rc;
   if (T == 0) return COLI_OK;
   const int act = act_of(c);
-  if (slots == nullptr) return reject(COLI_EINVAL, "slots must be set");
+  if (int rc = check_words("slots", slots)) return rc;
   if (int rc = check_rows("k", k, k_stride, c.n_heads, c.head_dim, act)) return rc;
   if (int rc = check_rows("v", v, v_stride, c.n_heads, c.head_dim, act)) return rc;
   RotaryView r{};
@@ -247,7 +255,7 @@ int coli_kv_read(const coli_kv_cache* cache, const int32_t* slots, int32_t N, vo
   if (int rc = check_cache(cache, &c)) return rc;
   if (int rc = check_tokens("N", N)) return rc;
   if (N == 0) return COLI_OK;
-  if (slots == nullptr) return reject(COLI_EINVAL, "slots must be set");
+  if (int rc = check_words("slots", slots)) return rc;
   if (k_out == nullptr && v_out == nullptr)
     return reject(COLI_EINVAL, "k_out or v_out must be set");
   const int act = act_of(c);
@@ -291,8 +299,10 @@ int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg
   if (int rc = check_rows("q", q, q_stride, cfg->n_q_heads, c.head_dim, act)) return rc;
   if (int rc = check_rows("out", out, out_stride, cfg->n_q_heads, c.head_dim, act)) return rc;
   if (q == out) return reject(COLI_EINVAL, "out must not be q");
-  if (block_table == nullptr || seq_lens == nullptr)
-    return reject(COLI_EINVAL, "block_table and seq_lens must be set");
+  if (int rc = check_words("block_table", block_table)) return rc;
+  if (int rc = check_words("seq_lens", seq_lens)) return rc;
+  if (lse != nullptr)
+    if (int rc = check_words("lse", lse)) return rc;
   if (max_pages < 1 || static_cast<int64_t>(max_pages) * c.page_size > INT32_MAX)
     return reject(COLI_EINVAL, "max_pages=%d: need 1 or more and max_pages * page_size < 2^31",
                   max_pages);

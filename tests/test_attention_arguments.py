@@ -119,3 +119,28 @@ def test_pools_of_two_devices_are_refused(devices):
     k, v = (Standin((4, 2, 16, 64), torch.bfloat16, d) for d in (0, 1))
     with pytest.raises(ValueError, match="one device"):
         moe.PagedKVCache(k, v)
+
+
+# ---- alignment ---------------------------------------------------------------------------
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_ids_and_results_have_to_be_aligned(off):
+    """A 32-bit vector off its boundary would fault in the kernel."""
+    odd = FAKE + off
+    c = moe.coli_kv_cache(FAKE, FAKE, FAKE, FAKE, 8, 16, 2, 64, moe.BF16)
+    r = moe.coli_rotary(FAKE, 100, 64, moe.ROPE_HALF, 0)
+    cfg = moe.coli_attn_config(4, 0, 0.125)
+
+    def attend(table=FAKE, lens=FAKE, lse=FAKE):
+        return moe.coli_paged_attention(c, cfg, FAKE, 256, 2, table, 4, lens, 2 * FAKE, 256, lse,
+                                        FAKE, 1 << 40, stream=0)
+    for what, call in (
+            ("positions", lambda: moe.coli_rope_apply(r, odd, 4, 64, moe.BF16, FAKE, 128, 2, FAKE,
+                                                      128, stream=0)),
+            ("positions", lambda: moe.coli_kv_append(c, FAKE, 128, FAKE, 128, FAKE, 4, r, odd,
+                                                     stream=0)),
+            ("slots", lambda: moe.coli_kv_append(c, FAKE, 128, FAKE, 128, odd, 4, stream=0)),
+            ("slots", lambda: moe.coli_kv_read(c, odd, 4, FAKE, 128, FAKE, 128, stream=0)),
+            ("block_table", lambda: attend(table=odd)), ("seq_lens", lambda: attend(lens=odd)),
+            ("lse", lambda: attend(lse=odd))):
+        assert call() == moe.COLI_EINVAL, what
+        assert what in moe.last_error()
