@@ -489,6 +489,15 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _used_here(*tensors):
+    """Tells the allocator that work on the current stream uses tensors of other streams,
+    whose memory it would otherwise give away as soon as their owner lets go of them."""
+    stream = _torch.cuda.current_stream()
+    for x in tensors:
+        if x is not None:
+            x.record_stream(stream)
+
+
 class Rotary:
     """A rotary table ([n_positions][rot_dim/2][2] f32, cosines and sines) with
     the layout it is applied in: "half" or "interleaved" (or ROPE_*). It serves calls
@@ -529,7 +538,9 @@ def rope(rotary: Rotary, positions, q, k=None, q_out=None, k_out=None, inverse=F
     inverse=True turns back, which is also the gradient with respect to q and k."""
     if stream is not None:
         with _on(stream):
-            return rope(rotary, positions, q, k, q_out, k_out, inverse)
+            out = rope(rotary, positions, q, k, q_out, k_out, inverse)
+            _used_here(rotary.table, positions, q, k, q_out, k_out)
+            return out
     torch = _torch
     dt = q.dtype
     if dt is torch.bfloat16:
@@ -624,6 +635,9 @@ class PagedKVCache:
             pools += [torch.zeros(*shape, s, dtype=torch.uint8, device="cuda") for _ in range(2)]
         return cls(*pools, head_dim=head_dim)
 
+    def _pools(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
     def _device(self) -> int:
         """The pool's device, which has to be the current one (see _device_of)."""
         if self._dev != _current_device():
@@ -637,7 +651,10 @@ class PagedKVCache:
         when `rotary` is given; returns the rotated q (None without q)."""
         if stream is not None:
             with _on(stream):
-                return self.append(k, v, slots, rotary, positions, q, q_out)
+                out = self.append(k, v, slots, rotary, positions, q, q_out)
+                _used_here(*self._pools(), k, v, slots, rotary and rotary.table, positions, q,
+                           q_out)
+                return out
         T, hk, d, dt = k.shape[0], self.n_kv_heads, self.head_dim, self.act_torch
         dev = self._device()
         ks = _head_rows("k", k, hk, d, dt, dev)
@@ -674,7 +691,9 @@ class PagedKVCache:
         """(k, v) rows [N][n_kv_heads][head_dim] of slots, zeros for -1."""
         if stream is not None:
             with _on(stream):
-                return self.read(slots)
+                out = self.read(slots)
+                _used_here(*self._pools(), slots)
+                return out
         N, h, d = slots.shape[0], self.n_kv_heads, self.head_dim
         at = _ids("slots", slots, N, self._device())
         k = _torch.empty((N, h, d), dtype=self.act_torch, device=slots.device)
@@ -692,7 +711,9 @@ class PagedKVCache:
         (and lse [B][n_q_heads] f32). scale defaults to head_dim^-0.5."""
         if stream is not None:
             with _on(stream):
-                return self.attend(q, block_table, seq_lens, scale, window, out, return_lse)
+                got = self.attend(q, block_table, seq_lens, scale, window, out, return_lse)
+                _used_here(*self._pools(), q, block_table, seq_lens, out)
+                return got
         torch, d, dt = _torch, self.head_dim, self.act_torch
         B, hq = q.shape[0], q.shape[1]
         dev = self._device()
