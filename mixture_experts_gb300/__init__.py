@@ -471,6 +471,11 @@ def _head_rows(name, x, n_heads, head_dim, dtype, dev=None) -> int:
     return s0 if T > 1 else h * d
 
 
+def _rank(name, x, n, shape):
+    if x.dim() != n:
+        raise ValueError(f"{name}: need {shape}, got {tuple(x.shape)}")
+
+
 def _ids(name, x, n, dev) -> int:
     """Address of a contiguous int32 vector of n entries on device dev."""
     if x.dtype is not _torch.int32 or x.get_device() != dev or x.dim() != 1 or \
@@ -506,6 +511,8 @@ class Rotary:
     def __init__(self, table, layout="half"):
         torch = _t()
         lay = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}.get(layout, layout)
+        if lay not in (ROPE_HALF, ROPE_INTERLEAVED):
+            raise ValueError(f"layout: {layout!r} is not 'half' or 'interleaved'")
         if table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous() or \
                 table.dtype is not torch.float32 or not table.is_cuda:
             raise ValueError("table: need a contiguous f32 CUDA tensor [n_positions][rot/2][2]")
@@ -549,8 +556,7 @@ def rope(rotary: Rotary, positions, q, k=None, q_out=None, k_out=None, inverse=F
         act = F32
     else:
         raise ValueError(f"q: need f32 or bf16, got {dt}")
-    if q.dim() != 3:
-        raise ValueError(f"q: need [T][heads][head_dim], got {tuple(q.shape)}")
+    _rank("q", q, 3, "[T][heads][head_dim]")
     T, hq, d = q.shape
     dev = _device_of("q", q)
     if rotary._dev != dev:
@@ -567,6 +573,7 @@ def rope(rotary: Rotary, positions, q, k=None, q_out=None, k_out=None, inverse=F
     kp = kop = None
     hk = ks = kos = 0
     if k is not None:
+        _rank("k", k, 3, "[T][heads][head_dim]")
         hk = k.shape[1]
         ks = _head_rows("k", k, hk, d, dt, dev)
         if k_out is None:
@@ -655,6 +662,7 @@ class PagedKVCache:
                 _used_here(*self._pools(), k, v, slots, rotary and rotary.table, positions, q,
                            q_out)
                 return out
+        _rank("k", k, 3, "[T][heads][head_dim]")
         T, hk, d, dt = k.shape[0], self.n_kv_heads, self.head_dim, self.act_torch
         dev = self._device()
         ks = _head_rows("k", k, hk, d, dt, dev)
@@ -671,6 +679,7 @@ class PagedKVCache:
                 raise ValueError(f"the rotary table is on cuda:{rotary._dev}, not on cuda:{dev}")
             rp, pp = rotary._ref, _ids("positions", positions, T, dev)
         if q is not None:
+            _rank("q", q, 3, "[T][heads][head_dim]")
             hq = q.shape[1]
             qs = _head_rows("q", q, hq, d, dt, dev)
             if q_out is None:
@@ -694,6 +703,7 @@ class PagedKVCache:
                 out = self.read(slots)
                 _used_here(*self._pools(), slots)
                 return out
+        _rank("slots", slots, 1, "a vector")
         N, h, d = slots.shape[0], self.n_kv_heads, self.head_dim
         at = _ids("slots", slots, N, self._device())
         k = _torch.empty((N, h, d), dtype=self.act_torch, device=slots.device)
@@ -715,6 +725,7 @@ class PagedKVCache:
                 _used_here(*self._pools(), q, block_table, seq_lens, out)
                 return got
         torch, d, dt = _torch, self.head_dim, self.act_torch
+        _rank("q", q, 3, "[B][heads][head_dim]")
         B, hq = q.shape[0], q.shape[1]
         dev = self._device()
         qs = _head_rows("q", q, hq, d, dt, dev)

@@ -144,3 +144,26 @@ def test_ids_and_results_have_to_be_aligned(off):
             ("lse", lambda: attend(lse=odd))):
         assert call() == moe.COLI_EINVAL, what
         assert what in moe.last_error()
+
+
+# ---- ranks and names ---------------------------------------------------------------------
+def test_wrappers_refuse_other_ranks_with_a_value_error(devices):
+    import torch
+    rows, ids, cache, rotary, table = devices
+    c, r = cache(0), rotary(0)
+
+    def flat(*shape, dtype=torch.bfloat16):
+        return Standin(shape, dtype, 0)
+    for bad in (
+            lambda: moe.rope(r, ids(0), flat(64)),
+            lambda: moe.rope(r, ids(0), rows(0), flat(64), q_out=rows(0)),
+            lambda: moe.rope(r, ids(0), rows(0), flat(), q_out=rows(0)),
+            lambda: c.append(flat(), rows(0), ids(0)), lambda: c.append(flat(3), rows(0), ids(0)),
+            lambda: c.append(rows(0), flat(3), ids(0)),
+            lambda: c.append(rows(0), rows(0), ids(0), rotary=r, positions=ids(0), q=flat(3)),
+            lambda: c.read(flat(dtype=torch.int32)), lambda: c.read(flat(3, 1, dtype=torch.int32)),
+            lambda: c.attend(flat(3), table(0), ids(0)), lambda: c.attend(flat(), table(0), ids(0)),
+            lambda: moe.Rotary(Standin((8, 32, 2), torch.float32, 0), "halves"),
+            lambda: moe.Rotary(Standin((8, 32, 2), torch.float32, 0), 2)):
+        with pytest.raises(ValueError):
+            bad()
