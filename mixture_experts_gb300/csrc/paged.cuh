@@ -212,11 +212,6 @@ COLI_DEV uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
-COLI_DEV uint32_t lds8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
 
 // Where 16-byte piece c of row r lies in a tile: the piece's place XORed, within
 // its 128 bytes, with a number of the row chosen so that the lanes of one
