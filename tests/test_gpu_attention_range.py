@@ -210,3 +210,37 @@ def test_a_query_that_is_no_number_stays_in_its_head(what, fmt):
     assert got[0, 2].isnan().all()
     keep = torch.tensor([0, 1, 3])
     assert ((got - want).abs() <= tol + 2.0 ** -8 * want.abs())[0, keep].all()
+
+
+@pytest.mark.parametrize("fmt", MX)
+@pytest.mark.parametrize("lens,hq,hk,D,page,window", [
+    ([3000, 0, 41, 777], 6, 2, 96, 48, 0), ([2500, 16, 1], 24, 2, 64, 16, 1000),
+    ([6000], 20, 1, 256, 32, 0), ([900, 900, 33], 4, 4, 160, 16, 300), ([400, 5, 60], 16, 1, 128, 64, 0)])
+def test_far_values_in_windows_cut_contexts_and_beside_left_out_pages(lens, hq, hk, D, page,
+                                                                      window, fmt):
+    """Some warps' tiles hold values of 2^60 under no weight, some pages are outside the pool."""
+    import test_gpu_attention_precise as precise
+    import attn_bound as ab
+    g = gen(11, hq, D, page)
+    n = sum(lens)
+    k = 0.1 * torch.randn(n, hk, D, generator=g)
+    v = torch.randn(n, hk, D, generator=g) * 2.0 ** -60
+    far = torch.rand(n, generator=g) < 0.01
+    k[far], v[far] = -20.0, v[far] * 2.0 ** 120
+    k, v = k.bfloat16(), v.bfloat16()
+    c, table, sl = precise.pool(fmt, k, v, lens, page, seed=5)
+    table[0, 1] = c.k.shape[0] + 3
+    q = (6.0 + 0.1 * torch.randn(len(lens), hq, D, generator=g)).bfloat16().cuda()
+    got, lse = c.attend(q, table, sl, window=window, return_lse=True)
+    # (a left-out page before the window is not looked up)
+    seen = max(0, lens[0] - window) if window else 0
+    assert moe.coli_device_status() == (moe.COLI_EDEVICE if seen < 2 * page else moe.COLI_OK)
+    k, v = ab.stored(k, fmt), ab.stored(v, fmt)
+    starts = [sum(lens[:b]) for b in range(len(lens))]
+    keep = []
+    for b, m in enumerate(lens):
+        j = torch.arange(max(0, m - window) if window else 0, m)
+        keep.append(starts[b] + (j[j // page != 1] if b == 0 else j))
+    ref = attn_ref.attend(q, lambda b, h: k[keep[b], h], lambda b, h: v[keep[b], h],
+                          [len(x) for x in keep], hk, D ** -0.5)
+    check(got, lse, ref, fmt)
