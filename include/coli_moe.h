@@ -436,7 +436,12 @@ typedef struct {
  * NaN. out must not overlap q. block_table is [B][max_pages]; entries past a sequence's last
  * page are not read. A page outside [0, n_pages) is left out, as are tokens
  * past max_pages pages; a negative length counts as 0; each latches
- * COLI_EDEVICE. Scores, softmax and sums are fp32 throughout. scratch:
+ * COLI_EDEVICE. Scores, softmax statistics and sums are fp32; the products take
+ * F32 queries, keys, values and weights in two tf32 parts each (about 21 bits),
+ * BF16 and MX queries, keys and values as they are, and softmax weights in 16 bits
+ * (BF16) or 11 (MX; 9 for those 2^-30 of the largest), beside the normaliser's
+ * unrounded ones: less than the bf16 output rounds away. Finite values whose plain
+ * fp32 sums are finite give a finite result. scratch:
  * 16-byte aligned, coli_paged_attention_scratch_bytes(...) bytes, contents
  * irrelevant; calls that may overlap need their own. It is not used, and may be
  * NULL, when max_pages * page_size <= COLI_PAGED_DIRECT_TOKENS. */

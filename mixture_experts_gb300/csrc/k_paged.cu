@@ -12,9 +12,9 @@ namespace {
 // of the blocks, o = sum o_k l_k 2^(m_k - m) / sum l_k 2^(m_k - m), four at a time and a mean
 // throughout (sums could overflow where the result does not). A group of registers is one 16 x 8 tile of
 // O^T. With gridDim.y = 1 a warp takes whole groups; otherwise block y takes
-// group y and its warps share the partials. Latency bound: 4 to 6 us, of which
-// the launch lies under the main kernel (one context of 500009 tokens: 38 partials
-// a segment, 6 us; 32 ragged contexts: 2 a segment, 4.5 us).
+// group y and its warps share the partials. Latency bound: 6 to 8 us by itself, of
+// which the launch lies under the main kernel (one context of 500009 tokens: 38
+// partials a segment, 7.4 us; 32 ragged contexts: 2 a segment, 6.0 us).
 template <int DP, int NT, bool F32, bool IN_ORDER>
 __global__ void __launch_bounds__(256) k_join(const Params p) {
   constexpr int kGroups = DP / 16 * NT, kRegs = kGroups * 4;
@@ -217,10 +217,21 @@ cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
   const int64_t segments = static_cast<int64_t>(a.B) * a.c.n_heads * f.blocks;
   const int64_t tiles = static_cast<int64_t>(a.max_pages) * (a.c.page_size / kTile);
   const int64_t pieces = (segments * (tiles + 8) + f.warps - 1) / f.warps;
-  // One block a segment, nothing cut, where the block table holds 1024 tokens at most,
-  // or 2048 and the segments fill the GPU. Direct against cut and joined, us, 32 / 8
-  // heads of 128, bf16: B 1, 300 tokens 6.6 / 9.3, 1000 9.7 / 9.8, 2000 14.4 / 9.8; B 16,
-  // 1000 10.3 / 13.9; B 128, 2000 104 / 117. MXFP4, 64 / 4 heads, B 64, 2000 41.7 / 34.4.
+  // One block a segment, nothing cut, where the block table holds 1024 tokens at most (which
+  // callers know, and need no scratch then), or 2048 and the segments fill the GPU. Direct
+  // against cut and joined, us, heads of 128, at 100 / 300 / 500 / 1000 tokens:
+  //   bf16  B 1, 32/8 heads   4.7-7.0   5.8-6.9   6.8-7.0   9.4-7.2
+  //         B 1, 8/1          4.9-5.9   6.2-6.7   6.9-6.7   9.5-6.8
+  //         B 4, 32/8         4.9-8.6   6.1-8.5   6.9-9.5   9.5-10.1
+  //         B 16, 32/8        5.2-8.7   6.6-10.8  9.9-14.0  14.8-18.6
+  //   MXFP8 B 1, 32/8         6.5-9.7   9.9-9.9   11.1-9.9  17.2-10.1
+  //         B 4, 32/8         6.7-12.1  10.1-12.2 11.7-12.7 18.5-13.2
+  //         B 16, 32/8        7.5-10.6  11.3-11.6 12.7-14.1 20.2-22.5
+  //   MXFP4 B 1, 64/4         7.8-9.8   11.0-10.0 14.2-10.3 21.8-10.6
+  //   f32   B 1, 16/8         7.2-9.6   12.7-9.6  16.2-9.6  27.4-9.9
+  // and bf16 at 2000, B 128: 104-117. So it is the faster form for short contexts and for
+  // full batches; a few sequences of 500 to 1000 tokens would be faster cut (up to 2.8
+  // times in fp32), which needs scratch that such a call may leave out.
   p.direct = paged_direct(a.c, a.max_pages) ||
              (static_cast<int64_t>(a.max_pages) * a.c.page_size <= 2 * COLI_PAGED_DIRECT_TOKENS &&
               segments >= most);

@@ -75,7 +75,7 @@ COLI_DEV void f16x8_f32(const uint32_t (&h)[4], float (&x)[8]) {
   }
 }
 
-// Byte offset of row (page, head, offset in the page) counted in rows.
+// Number of the row (page, head, offset in the page) in a pool.
 COLI_DEV size_t kv_row(const KvView& c, int page, int head, int off) {
   return (static_cast<size_t>(page) * c.n_heads + head) * c.page_size + off;
 }

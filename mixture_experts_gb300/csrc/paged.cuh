@@ -25,14 +25,25 @@
 // context zero-filled), so no warp waits for another before the segment's end,
 // and the next segment's first copies fly while the warps' sums are joined.
 //
+// Precision. Scores, softmax statistics and sums are fp32; the products' operands are not:
+//   scores  bf16 as it is; fp32 in two tf32 parts, low x low left out (21 bits); MX codes
+//           and queries as they are, in as many parts as that takes;
+//   values  weights in two tf32 parts (fp32, so are the values), in a bf16 number and one
+//           for its rounding (16 bits), in fp16 (MX: 11 bits, 9 at 2^-30 of the largest;
+//           bf16 in two parts below); the normaliser adds the unrounded ones. 11 bits lie
+//           below what the bf16 output rounds away (8), and fp16 takes half the products.
+// MX numbers further apart than these operands hold (scales, queries) take plain_tiles.
+//
 // What bounds it (GB300, 32 query and 8 key heads of 128 unless said, against the
-// 6.8 TB/s of a copy): bf16 HBM: 6.9 TB/s on one context of 500009 tokens, 6.05 TB/s
-// on 32 ragged ones (586 MB, 97 us). fp32 HBM (6.6 TB/s, 8 heads, 7 x 26157 tokens).
-// MXFP8 5.6 TB/s on 64 contexts (1168 MB, 207 us): 463 instructions a tile, issue 53%
-// and the ALU pipe 45% busy (widening value codes to fp16, their scales), with three
+// 6.8 TB/s of a copy): bf16 HBM: 6.9 TB/s on one context of 500009 tokens, 6.1 TB/s
+// on 32 ragged ones (586 MB, 96 us). fp32 HBM (6.6 TB/s, 8 heads, 7 x 26157 tokens).
+// MXFP8 5.5 TB/s on 64 contexts (1168 MB, 212 us): 480 instructions a tile, issue 56%
+// and the ALU pipe 50% busy (widening value codes to fp16, their scales), with three
 // warps a scheduler to cover the steps' own latency. MXFP4, 64 query heads on 4:
-// 2.1 TB/s (282 MB, 135 us): 597 instructions a tile, the same work at half the bytes
-// and twice the heads.
+// 2.0 TB/s (282 MB, 140 us): 636 instructions a tile, the same work at half the bytes
+// and twice the heads. A group of more than 16 query heads (fp32: 8) is cut in segments
+// that read the keys and values once each: 640000 keys, 16 / 32 / 64 heads on one key
+// head, bf16 67 / 113 / 186 us, MXFP8 66 / 115 / 197; fp32, 8 / 16 / 32: 108 / 197 / 375.
 
 #pragma once
 
@@ -66,7 +77,7 @@ struct Cfg {
   static constexpr int kScaleRow = kMx ? (DP > 128 ? 8 : 4) : 0;
   // Tiles a warp takes in one step: two of an MX cache, whose small tiles leave
   // the step's fixed work (pages, waits, votes) as long as the tile's own (64 MXFP8
-  // contexts: two 207 us, one 213 us; groups of 16 heads: two spill, 144 against 135 us).
+  // contexts: two 212 us, one 225 us; groups of 16 heads: two spill, 148 against 140 us).
   static constexpr int kStep = kMx && DP <= 128 && DP * NT <= 128 ? 2 : 1;
   static constexpr int kTileBytes = kTile * kRow, kTileScales = kTile * kScaleRow;
   // whole 128-byte lines: addresses within a line are XORed
@@ -75,8 +86,8 @@ struct Cfg {
   static constexpr int kOpen = 8;  // a segment's fixed cost, in tiles (3 us at 2.7 tiles a us)
   // Warps of a block and blocks of an SM: what the registers of the widest step allow
   // without many spills. MXFP8 heads of 128, 64 contexts: 12 warps of 168 registers
-  // 207 us, 8 of 255 228 us (16 warps: no room for their rings); MXFP4 groups of 16
-  // heads, 160 windowed contexts: 12 warps 135 us, 8 warps 146 us, 16 warps 221 us.
+  // 212 us, 8 of 255 240 us (16 warps: no room for their rings); MXFP4 groups of 16
+  // heads, 160 windowed contexts: 12 warps 140 us, 8 warps 148 us, 16 warps 203 us.
   static constexpr int kAcc = DP * NT;
   static constexpr int kWarps = kAcc == 512 ? (kMx ? 8 : 6)
                                 : kSlot > 8448 || (kMx && kAcc >= 128 && DP <= 128) ||
@@ -167,7 +178,8 @@ COLI_DEV void mma_f16_16816_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t 
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // e4m3 x e4m3 (or e5m2), 32 indices: twice the f16 form's work an instruction, summed
-// in fp32 as exactly (e4m3 checked to 24 bits within an instruction and across).
+// as exactly: off by at most 10 x 2^-24 of the largest term (e5m2: 8; f16 and bf16: 7;
+// tf32: 8), over 38400 random and one-signed sums a form.
 COLI_DEV void mma_e4m3_16832(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                              uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
@@ -322,7 +334,7 @@ COLI_DEV Seq seq_of(const PagedArgs& a, int b, bool latch) {
 // the channels 64 v + 8 g .. + 7 of heads 2t, 2t + 1 (+ 8 nt), one key after the other. For
 // numbers further apart than the operands of k_paged hold, which no trained model's are: sums
 // and products overflow where plain fp32 ones would. 25 times the steps' time (64 MXFP8
-// contexts: 5.3 ms). A call, not inlined: 64 contexts 210 us against 213, where none needs it.
+// contexts: 5.3 ms). Called or inlined, the steps themselves take the same (212 us).
 template <int DP, int NT>
 struct PlainSums {
   float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
