@@ -401,8 +401,8 @@ typedef struct {
  * elements rounded to nearest even and saturated; a block with a NaN or an
  * infinity gets scale byte 255, which reads back as NaN throughout. Slots
  * outside the pool and positions outside the table are not written and latch
- * COLI_EDEVICE (q is copied unrotated there). Two tokens with one slot in one
- * call leave either's row. */
+ * COLI_EDEVICE (q is copied unrotated where its position is). Two tokens with one
+ * slot in one call leave a mix of their rows. */
 int coli_kv_append(const coli_kv_cache* cache, const void* k, size_t k_stride, const void* v,
                    size_t v_stride, const int32_t* slots, int32_t T, const coli_rotary* rotary,
                    const int32_t* positions, const void* q, size_t q_stride, int32_t n_q_heads,
