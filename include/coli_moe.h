@@ -454,6 +454,102 @@ int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg
                          size_t out_stride, float* lse, void* scratch, size_t scratch_bytes,
                          void* stream);
 
+/* ---- long contexts: shared prefixes, chosen pages, eviction -------------------
+ * Three ways to read less of the cache at a decode step. Arrays are the caller's, as
+ * above; q, out, strides, block_table, seq_lens, lse and what is skipped and
+ * latched are as for coli_paged_attention where not said otherwise. */
+
+/* Attention of one new token a sequence, B sequences behind one shared prefix:
+ * sequence b sees the prefix_len tokens of the pages prefix_pages [ceil(prefix_len /
+ * page_size)], then its own seq_lens[b] tokens (0 or more; the new one among
+ * them) in block_table[b]. Same result as coli_paged_attention over both, but the
+ * prefix is read once for all sequences. prefix_len is a host number (0: no
+ * prefix, prefix_pages may be NULL); own tokens begin a page of their own.
+ * cfg->window has to be 0. A prefix page outside the pool is left out and latches
+ * COLI_EDEVICE. The prefix's products take bf16 and MX operands as bf16 (MX keys
+ * and values outside bf16's range are rounded to it, as coli_kv_read does) or,
+ * for few rows (B * n_q_heads / n_kv_heads) and F32, as coli_paged_attention
+ * does; softmax weights in 16 bits. scratch: 16-byte aligned, the bytes that
+ * coli_shared_attention_scratch_bytes says, contents irrelevant; calls that may
+ * overlap need their own. */
+size_t coli_shared_attention_scratch_bytes(const coli_kv_cache* cache, int32_t B,
+                                           int32_t n_q_heads);
+int coli_shared_attention(const coli_kv_cache* cache, const coli_attn_config* cfg, const void* q,
+                          size_t q_stride, int32_t B, const int32_t* prefix_pages,
+                          int32_t prefix_len, const int32_t* block_table, int32_t max_pages,
+                          const int32_t* seq_lens, void* out, size_t out_stride, float* lse,
+                          void* scratch, size_t scratch_bytes, void* stream);
+
+/* Bounds of pages: bounds[pages[i]][h] = (least, largest) key of each channel
+ * among the first fills[i] tokens (1..page_size) of the page, for the N pages
+ * listed. bounds is [n_pages][n_kv_heads][2][head_dim] in the act dtype, 16-byte
+ * aligned: the values that coli_kv_read gives, so exact where those are. A NaN key
+ * makes its channel's bounds NaN. A page of -1 is skipped; other pages outside
+ * the pool and fills outside 1..page_size are skipped and latch COLI_EDEVICE. A decode
+ * step calls it for the pages it has just written to, a prompt for all of its pages. */
+int coli_page_bounds(const coli_kv_cache* cache, const int32_t* pages, const int32_t* fills,
+                     int32_t N, void* bounds, void* stream);
+
+/* Chooses, for each sequence and key head, the `keep` pages of its context to attend to:
+ * the first `first` and last `last` (at least 1: the last page may be part
+ * filled) of the sequence's ceil(seq_lens[b] / page_size) pages, and of the others those of the
+ * largest
+ *   score(p) = max over the key head's query heads of sum_d (q_d > 0 ? q_d largest_d :
+ *              q_d < 0 ? q_d least_d : 0),
+ * which no key of the page exceeds (q . k, for a positive scale). Equal scores: the
+ * earlier page. The choice is that of exact scores: they are compared in fp64
+ * where fp32 ones lie too near to each other. A page whose score is NaN, or that
+ * lies outside the pool, counts as -inf and latches COLI_EDEVICE. pages [B][n_kv_heads][keep]
+ * receives the pool's page numbers in the context's order (-1 from the last on), lens [B]
+ * the tokens they hold; all pages where there are no more than `keep`. bounds as
+ * above; keep >= first + last. q has n_q_heads heads. scratch: 16-byte aligned,
+ * coli_select_pages_scratch_bytes(...) bytes; calls that may overlap need their own. */
+size_t coli_select_pages_scratch_bytes(const coli_kv_cache* cache, int32_t B, int32_t max_pages);
+int coli_select_pages(const coli_kv_cache* cache, const void* bounds, const void* q,
+                      size_t q_stride, int32_t n_q_heads, int32_t B, const int32_t* block_table,
+                      int32_t max_pages, const int32_t* seq_lens, int32_t keep, int32_t first,
+                      int32_t last, int32_t* pages, int32_t* lens, void* scratch,
+                      size_t scratch_bytes, void* stream);
+
+/* coli_paged_attention with pages of its own for each key head: pages
+ * [B][n_kv_heads][max_pages], lens [B] tokens in them (the last listed page may
+ * be part filled), as coli_select_pages leaves them. cfg->window has to be 0. */
+int coli_selected_attention(const coli_kv_cache* cache, const coli_attn_config* cfg,
+                            const void* q, size_t q_stride, int32_t B, const int32_t* pages,
+                            int32_t max_pages, const int32_t* lens, void* out, size_t out_stride,
+                            float* lse, void* scratch, size_t scratch_bytes, void* stream);
+
+/* Adds what each cached token weighed in a decode step: for every token j in
+ * sight of sequence b and every key head h,
+ *   mass(j, h) += sum over the key head's query heads of exp(scale * q . k_j - lse),
+ * lse [B][n_q_heads] as coli_paged_attention returned it for the same call. mass is
+ * [n_pages][n_kv_heads][page_size] f32, the pages' own layout, so it follows the
+ * tokens. Tokens j >= known[b] start from 0 (a decode step passes seq_lens - 1: its
+ * new token's place may hold an earlier one's mass); known NULL: all are added to.
+ * A row whose lse is -inf adds nothing. Sums of one token are added in a
+ * fixed order unless sequences share its page. */
+int coli_attention_mass(const coli_kv_cache* cache, const coli_attn_config* cfg, const void* q,
+                        size_t q_stride, int32_t B, const int32_t* block_table,
+                        int32_t max_pages, const int32_t* seq_lens, const float* lse,
+                        const int32_t* known, float* mass, void* stream);
+
+/* Cuts sequences down to `keep` tokens a key head: of a sequence of more, each
+ * key head keeps its first `first` and last `recent` tokens and of the others those of
+ * the largest mass (equal: the earlier; NaN counts as -inf), in their order.
+ * Their keys, values, scales and masses are copied, bit for bit, to the first places of
+ * the pages into[b] ([B][into_pages], into_pages * page_size >= keep); sequences
+ * of up to `keep` tokens are copied whole. into NULL or block_table itself: in
+ * place. Otherwise the pages of `into` must be no sequence's own. kept
+ * [B][n_kv_heads][keep] receives the old places, -1 from the last on, new_lens [B]
+ * (not seq_lens itself) min(seq_lens[b], keep). What lies behind the kept rows
+ * stays as it was. Rotated keys keep their positions: new tokens go on from
+ * the old length. Pages of another sequence of the call must not be cut in place.
+ * Pages outside the pool are left out (mass -inf) and latch COLI_EDEVICE. */
+int coli_kv_evict(const coli_kv_cache* cache, float* mass, int32_t B, const int32_t* block_table,
+                  int32_t max_pages, const int32_t* seq_lens, int32_t keep, int32_t first,
+                  int32_t recent, const int32_t* into, int32_t into_pages, int32_t* kept,
+                  int32_t* new_lens, void* stream);
+
 /* ---- fault-handling self-test ------------------------------------------ */
 /* Launches one block that waits on a shared-memory barrier nothing will ever
  * complete, giving up after spin_limit polls: it latches COLI_ETIMEOUT and

@@ -111,6 +111,18 @@ _SIGS = {
     "coli_paged_attention_scratch_bytes": ("Z", ["P", "I", "I"]),
     "coli_paged_attention": ("I", ["P", "P", "P", "Z", "I", "P", "I", "P", "P", "Z", "P", "P",
                                    "Z", "P"]),
+    "coli_shared_attention_scratch_bytes": ("Z", ["P", "I", "I"]),
+    "coli_shared_attention": ("I", ["P", "P", "P", "Z", "I", "P", "I", "P", "I", "P", "P", "Z",
+                                    "P", "P", "Z", "P"]),
+    "coli_page_bounds": ("I", ["P", "P", "P", "I", "P", "P"]),
+    "coli_select_pages_scratch_bytes": ("Z", ["P", "I", "I"]),
+    "coli_select_pages": ("I", ["P", "P", "P", "Z", "I", "I", "P", "I", "P", "I", "I", "I", "P",
+                                "P", "P", "Z", "P"]),
+    "coli_selected_attention": ("I", ["P", "P", "P", "Z", "I", "P", "I", "P", "P", "Z", "P", "P",
+                                      "Z", "P"]),
+    "coli_attention_mass": ("I", ["P", "P", "P", "Z", "I", "P", "I", "P", "P", "P", "P", "P"]),
+    "coli_kv_evict": ("I", ["P", "P", "I", "P", "I", "P", "I", "I", "I", "P", "I", "P", "P",
+                            "P"]),
 }
 _CT = {"P": ctypes.c_void_p, "I": ctypes.c_int32, "Z": ctypes.c_size_t, "s": ctypes.c_char_p,
        None: None}
@@ -337,6 +349,61 @@ def coli_paged_attention(cache: coli_kv_cache, cfg: coli_attn_config, q, q_strid
                                       _stream(stream))
 
 
+def coli_shared_attention_scratch_bytes(cache: coli_kv_cache, B: int, n_q_heads: int) -> int:
+    return lib().coli_shared_attention_scratch_bytes(_ref(cache), B, n_q_heads)
+
+
+def coli_shared_attention(cache: coli_kv_cache, cfg: coli_attn_config, q, q_stride, B,
+                          prefix_pages, prefix_len, block_table, max_pages, seq_lens, out,
+                          out_stride, lse=None, scratch=None, scratch_bytes=0,
+                          stream=None) -> int:
+    return lib().coli_shared_attention(_ref(cache), _ref(cfg), _ptr(q), q_stride, B,
+                                       _ptr(prefix_pages), prefix_len, _ptr(block_table),
+                                       max_pages, _ptr(seq_lens), _ptr(out), out_stride,
+                                       _ptr(lse), _ptr(scratch), scratch_bytes, _stream(stream))
+
+
+def coli_page_bounds(cache: coli_kv_cache, pages, fills, N, bounds, stream=None) -> int:
+    return lib().coli_page_bounds(_ref(cache), _ptr(pages), _ptr(fills), N, _ptr(bounds),
+                                  _stream(stream))
+
+
+def coli_select_pages_scratch_bytes(cache: coli_kv_cache, B: int, max_pages: int) -> int:
+    return lib().coli_select_pages_scratch_bytes(_ref(cache), B, max_pages)
+
+
+def coli_select_pages(cache: coli_kv_cache, bounds, q, q_stride, n_q_heads, B, block_table,
+                      max_pages, seq_lens, keep, first, last, pages, lens, scratch=None,
+                      scratch_bytes=0, stream=None) -> int:
+    return lib().coli_select_pages(_ref(cache), _ptr(bounds), _ptr(q), q_stride, n_q_heads, B,
+                                   _ptr(block_table), max_pages, _ptr(seq_lens), keep, first,
+                                   last, _ptr(pages), _ptr(lens), _ptr(scratch), scratch_bytes,
+                                   _stream(stream))
+
+
+def coli_selected_attention(cache: coli_kv_cache, cfg: coli_attn_config, q, q_stride, B, pages,
+                            max_pages, lens, out, out_stride, lse=None, scratch=None,
+                            scratch_bytes=0, stream=None) -> int:
+    return lib().coli_selected_attention(_ref(cache), _ref(cfg), _ptr(q), q_stride, B,
+                                         _ptr(pages), max_pages, _ptr(lens), _ptr(out),
+                                         out_stride, _ptr(lse), _ptr(scratch), scratch_bytes,
+                                         _stream(stream))
+
+
+def coli_attention_mass(cache: coli_kv_cache, cfg: coli_attn_config, q, q_stride, B, block_table,
+                        max_pages, seq_lens, lse, known, mass, stream=None) -> int:
+    return lib().coli_attention_mass(_ref(cache), _ref(cfg), _ptr(q), q_stride, B,
+                                     _ptr(block_table), max_pages, _ptr(seq_lens), _ptr(lse),
+                                     _ptr(known), _ptr(mass), _stream(stream))
+
+
+def coli_kv_evict(cache: coli_kv_cache, mass, B, block_table, max_pages, seq_lens, keep, first,
+                  recent, into, into_pages, kept, new_lens, stream=None) -> int:
+    return lib().coli_kv_evict(_ref(cache), _ptr(mass), B, _ptr(block_table), max_pages,
+                               _ptr(seq_lens), keep, first, recent, _ptr(into), into_pages,
+                               _ptr(kept), _ptr(new_lens), _stream(stream))
+
+
 # ---- convenience -------------------------------------------------------------------
 class MoELayer:
     """One MoE layer on the current CUDA device (weights copied at creation).
@@ -483,6 +550,21 @@ def _ids(name, x, n, dev) -> int:
         raise ValueError(f"{name}: need a contiguous int32 vector of {n} on cuda:{dev}, got "
                          f"{x.device} {x.dtype} {tuple(x.shape)}")
     return x.data_ptr()
+
+
+def _table(name, x, B, dev, shape="[{}][max_pages]"):
+    """Checks a contiguous int32 table of B rows on device dev."""
+    if x.dim() != 2 or x.shape[0] != B or x.get_device() != dev or \
+            x.dtype is not _torch.int32 or not x.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous int32 tensor {shape.format(B)} on cuda:{dev}")
+
+
+def _shaped(name, x, shape, dtype, dev):
+    """Checks a contiguous tensor of a given shape and type on device dev."""
+    if tuple(x.shape) != shape or x.dtype is not dtype or x.get_device() != dev or \
+            not x.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor {list(shape)} on cuda:{dev}, "
+                         f"got {x.device} {x.dtype} {tuple(x.shape)}")
 
 
 def _on(stream):
@@ -736,11 +818,7 @@ class PagedKVCache:
             os_ = _head_rows("out", out, hq, d, dt, dev)
             if out.shape[0] != B:
                 raise ValueError("q and out need the same number of sequences")
-        if block_table.dim() != 2 or block_table.shape[0] != B or \
-                block_table.get_device() != dev or block_table.dtype is not torch.int32 or \
-                not block_table.is_contiguous():
-            raise ValueError(f"block_table: need a contiguous int32 tensor [{B}][max_pages] on "
-                             f"cuda:{dev}")
+        _table("block_table", block_table, B, dev)
         lens = _ids("seq_lens", seq_lens, B, dev)
         lse = torch.empty((B, hq), dtype=torch.float32, device=q.device) if return_lse else None
         L = lib()
@@ -763,3 +841,212 @@ class PagedKVCache:
         if rc:
             _check(rc, "coli_paged_attention")
         return (out, lse) if return_lse else out
+
+    def _queries(self, q, out, dev):
+        """(B, heads, q's stride, out, its stride) of a call's queries and output."""
+        d, dt = self.head_dim, self.act_torch
+        _rank("q", q, 3, "[B][heads][head_dim]")
+        B, hq = q.shape[0], q.shape[1]
+        qs = _head_rows("q", q, hq, d, dt, dev)
+        if out is None:
+            return B, hq, qs, _torch.empty((B, hq, d), dtype=dt, device=q.device), hq * d
+        os_ = _head_rows("out", out, hq, d, dt, dev)
+        if out.shape[0] != B:
+            raise ValueError("q and out need the same number of sequences")
+        return B, hq, qs, out, os_
+
+    def _config(self, key, hq, window, scale, scratch_bytes):
+        """The settings and scratch size of a kind of call, kept for the next step."""
+        call = self._calls.get(key)
+        if call is None:
+            cfg = coli_attn_config(hq, window, self.head_dim ** -0.5 if scale is None else scale)
+            if len(self._calls) >= 64:
+                self._calls.clear()
+            call = self._calls[key] = (cfg, ctypes.byref(cfg), scratch_bytes())
+        return call[1], call[2]
+
+    def attend_shared(self, q, prefix_pages, prefix_len, block_table, seq_lens, scale=None,
+                      out=None, return_lse=False, stream=None):
+        """attend for B sequences behind one prefix of prefix_len tokens (a host number)
+        in prefix_pages [pages] int32 (None without a prefix), which is read once for all;
+        block_table and seq_lens are the sequences' own tokens behind it."""
+        if stream is not None:
+            with _on(stream):
+                got = self.attend_shared(q, prefix_pages, prefix_len, block_table, seq_lens,
+                                         scale, out, return_lse)
+                _used_here(*self._pools(), q, prefix_pages, block_table, seq_lens, out)
+                return got
+        torch, dev = _torch, self._device()
+        B, hq, qs, out, os_ = self._queries(q, out, dev)
+        _table("block_table", block_table, B, dev)
+        lens = _ids("seq_lens", seq_lens, B, dev)
+        at = None
+        if prefix_len > 0:
+            _rank("prefix_pages", prefix_pages, 1, "a vector")
+            n = prefix_pages.shape[0]
+            if n * self.page_size < prefix_len:
+                raise ValueError(f"prefix_pages: {n} pages of {self.page_size} tokens hold no "
+                                 f"prefix of {prefix_len}")
+            at = _ids("prefix_pages", prefix_pages, n, dev)
+        lse = torch.empty((B, hq), dtype=torch.float32, device=q.device) if return_lse else None
+        L = lib()
+        cfg, n = self._config(
+            ("shared", hq, scale, B), hq, 0, scale,
+            lambda: L.coli_shared_attention_scratch_bytes(self._ref, B, hq) if B else 0)
+        scratch = torch.empty((n,), dtype=torch.uint8, device=q.device)
+        rc = L.coli_shared_attention(self._ref, cfg, q.data_ptr(), qs, B, at, prefix_len,
+                                     block_table.data_ptr(), block_table.shape[1], lens,
+                                     out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
+                                     scratch.data_ptr(), n, _current_stream(q))
+        if rc:
+            _check(rc, "coli_shared_attention")
+        return (out, lse) if return_lse else out
+
+    def new_bounds(self):
+        """Zeroed bounds of the pool's pages [n_pages][n_kv_heads][2][head_dim]."""
+        n_pages = self.k.shape[0]
+        return _t().zeros(n_pages, self.n_kv_heads, 2, self.head_dim, dtype=self.act_torch,
+                          device=self.k.device)
+
+    def page_bounds(self, bounds, pages, fills, stream=None):
+        """Sets bounds[pages[i]] to the least and largest key of each channel among the
+        first fills[i] tokens of the page (pages of -1 are skipped)."""
+        if stream is not None:
+            with _on(stream):
+                self.page_bounds(bounds, pages, fills)
+                _used_here(*self._pools(), bounds, pages, fills)
+                return bounds
+        dev = self._device()
+        _rank("pages", pages, 1, "a vector")
+        N = pages.shape[0]
+        at, fp = _ids("pages", pages, N, dev), _ids("fills", fills, N, dev)
+        _shaped("bounds", bounds, (self.c.n_pages, self.n_kv_heads, 2, self.head_dim),
+                self.act_torch, dev)
+        rc = lib().coli_page_bounds(self._ref, at, fp, N, bounds.data_ptr(),
+                                    _current_stream(bounds))
+        if rc:
+            _check(rc, "coli_page_bounds")
+        return bounds
+
+    def select_pages(self, q, bounds, block_table, seq_lens, keep, first=1, last=1, stream=None):
+        """The `keep` pages of each sequence and key head to attend to: the first and last
+        ones and those whose bounds allow the highest score. Returns (pages
+        [B][n_kv_heads][keep] int32, -1 behind the last, lens [B] int32 tokens in them)."""
+        if stream is not None:
+            with _on(stream):
+                got = self.select_pages(q, bounds, block_table, seq_lens, keep, first, last)
+                _used_here(*self._pools(), q, bounds, block_table, seq_lens)
+                return got
+        torch, dev, hk, d = _torch, self._device(), self.n_kv_heads, self.head_dim
+        _rank("q", q, 3, "[B][heads][head_dim]")
+        B, hq = q.shape[0], q.shape[1]
+        qs = _head_rows("q", q, hq, d, self.act_torch, dev)
+        _shaped("bounds", bounds, (self.c.n_pages, hk, 2, d), self.act_torch, dev)
+        _table("block_table", block_table, B, dev)
+        at = _ids("seq_lens", seq_lens, B, dev)
+        n = block_table.shape[1]
+        if keep < 1:
+            raise ValueError(f"keep: need 1 or more, got {keep}")
+        pages = torch.empty((B, hk, keep), dtype=torch.int32, device=q.device)
+        lens = torch.empty((B,), dtype=torch.int32, device=q.device)
+        scratch = torch.empty((B, hk, n, 2), dtype=torch.float32, device=q.device)
+        rc = lib().coli_select_pages(self._ref, bounds.data_ptr(), q.data_ptr(), qs, hq, B,
+                                     block_table.data_ptr(), n, at, keep, first, last,
+                                     pages.data_ptr(), lens.data_ptr(), scratch.data_ptr(),
+                                     scratch.numel() * 4, _current_stream(q))
+        if rc:
+            _check(rc, "coli_select_pages")
+        return pages, lens
+
+    def attend_selected(self, q, pages, lens, scale=None, out=None, return_lse=False,
+                        stream=None):
+        """attend over pages of each key head's own, as select_pages returns them."""
+        if stream is not None:
+            with _on(stream):
+                got = self.attend_selected(q, pages, lens, scale, out, return_lse)
+                _used_here(*self._pools(), q, pages, lens, out)
+                return got
+        torch, dev = _torch, self._device()
+        B, hq, qs, out, os_ = self._queries(q, out, dev)
+        _rank("pages", pages, 3, "[B][n_kv_heads][pages]")
+        n = pages.shape[2]
+        _shaped("pages", pages, (B, self.n_kv_heads, n), torch.int32, dev)
+        at = _ids("lens", lens, B, dev)
+        lse = torch.empty((B, hq), dtype=torch.float32, device=q.device) if return_lse else None
+        L = lib()
+        cfg, size = self._config(
+            ("selected", hq, scale, B, n), hq, 0, scale,
+            lambda: 0 if B == 0 or n * self.page_size <= COLI_PAGED_DIRECT_TOKENS else
+            L.coli_paged_attention_scratch_bytes(self._ref, B, hq))
+        scratch = torch.empty((size,), dtype=torch.uint8, device=q.device) if size else None
+        rc = L.coli_selected_attention(self._ref, cfg, q.data_ptr(), qs, B, pages.data_ptr(), n,
+                                       at, out.data_ptr(), os_,
+                                       None if lse is None else lse.data_ptr(),
+                                       None if scratch is None else scratch.data_ptr(), size,
+                                       _current_stream(q))
+        if rc:
+            _check(rc, "coli_selected_attention")
+        return (out, lse) if return_lse else out
+
+    def new_mass(self):
+        """Zeroed masses of the pool's tokens [n_pages][n_kv_heads][page_size] f32."""
+        return _t().zeros(self.k.shape[:3], dtype=_torch.float32, device=self.k.device)
+
+    def accumulate(self, mass, q, block_table, seq_lens, lse, known=None, scale=None, window=0,
+                   stream=None):
+        """Adds what each token in sight weighed in a decode step to its mass: the call's
+        arguments and the lse that attend returned for them. Tokens from known[b] on (None: no
+        token) start from 0."""
+        if stream is not None:
+            with _on(stream):
+                self.accumulate(mass, q, block_table, seq_lens, lse, known, scale, window)
+                _used_here(*self._pools(), mass, q, block_table, seq_lens, lse, known)
+                return mass
+        dev = self._device()
+        _rank("q", q, 3, "[B][heads][head_dim]")
+        B, hq = q.shape[0], q.shape[1]
+        qs = _head_rows("q", q, hq, self.head_dim, self.act_torch, dev)
+        _table("block_table", block_table, B, dev)
+        lens = _ids("seq_lens", seq_lens, B, dev)
+        _shaped("lse", lse, (B, hq), _torch.float32, dev)
+        _shaped("mass", mass, tuple(self.k.shape[:3]), _torch.float32, dev)
+        kp = None if known is None else _ids("known", known, B, dev)
+        cfg, _ = self._config(("mass", hq, window, scale), hq, window, scale, lambda: 0)
+        rc = lib().coli_attention_mass(self._ref, cfg, q.data_ptr(), qs, B,
+                                       block_table.data_ptr(), block_table.shape[1], lens,
+                                       lse.data_ptr(), kp, mass.data_ptr(), _current_stream(q))
+        if rc:
+            _check(rc, "coli_attention_mass")
+        return mass
+
+    def evict(self, mass, block_table, seq_lens, keep, first=0, recent=0, into=None,
+              stream=None):
+        """Cuts sequences down to `keep` tokens a key head: the first and most recent ones
+        and those of the largest mass, copied together to the front of their pages, or of the
+        pages `into` [B][pages] int32 (which must be no sequence's). Returns (kept
+        [B][n_kv_heads][keep] int32 old places, -1 behind the last, new lens [B] int32)."""
+        if stream is not None:
+            with _on(stream):
+                got = self.evict(mass, block_table, seq_lens, keep, first, recent, into)
+                _used_here(*self._pools(), mass, block_table, seq_lens, into)
+                return got
+        torch, dev = _torch, self._device()
+        _rank("block_table", block_table, 2, "[B][max_pages]")
+        B = block_table.shape[0]
+        _table("block_table", block_table, B, dev)
+        lens = _ids("seq_lens", seq_lens, B, dev)
+        _shaped("mass", mass, tuple(self.k.shape[:3]), torch.float32, dev)
+        ip, n = None, 0
+        if into is not None:
+            _table("into", into, B, dev, "[{}][pages]")
+            ip, n = into.data_ptr(), into.shape[1]
+        if keep < 1:
+            raise ValueError(f"keep: need 1 or more, got {keep}")
+        kept = torch.empty((B, self.n_kv_heads, keep), dtype=torch.int32, device=mass.device)
+        new_lens = torch.empty((B,), dtype=torch.int32, device=mass.device)
+        rc = lib().coli_kv_evict(self._ref, mass.data_ptr(), B, block_table.data_ptr(),
+                                 block_table.shape[1], lens, keep, first, recent, ip, n,
+                                 kept.data_ptr(), new_lens.data_ptr(), _current_stream(mass))
+        if rc:
+            _check(rc, "coli_kv_evict")
+        return kept, new_lens

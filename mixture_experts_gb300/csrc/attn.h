@@ -74,9 +74,72 @@ struct PagedArgs {
   float scale;
   float* scratch;
   int* status;
+  int head_tables;  // 1: block_table is [B][n_kv_heads][max_pages], pages for each key head
+  int fixed_len;    // > 0: every sequence's length, seq_lens unused
+  int fold;         // > 0: one sequence (B = 1) stands for several, whose queries' key heads
+                    // have `fold` heads each: q, out and lse are [..][n_kv_heads * fold]
+  int raw;          // 1: out is fp32 and lse float2 pairs (m, l): the row's weights are
+                    // 2^(x - m) and sum to l, out is their mean
 };
 size_t paged_scratch_bytes(const KvView& c, int B, int n_q_heads);
 bool paged_direct(const KvView& c, int max_pages);  // needs no scratch
 cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st);
+int sm_count();  // of the current device
+
+// ---- attention behind a shared prefix ------------------------------------------------
+struct SharedArgs {
+  PagedArgs own;  // the sequences' own tokens; q, out, lse of the whole call
+  const int32_t* prefix_pages;
+  int prefix_len;
+  void* scratch;
+};
+size_t shared_scratch_bytes(const KvView& c, int B, int n_q_heads);
+cudaError_t launch_shared_attention(const SharedArgs& a, cudaStream_t st);
+
+// ---- pages chosen by a cheap score --------------------------------------------------------
+cudaError_t launch_page_bounds(const KvView& c, const int32_t* pages, const int32_t* fills, int N,
+                               void* bounds, int* status, cudaStream_t st);
+struct SelectArgs {
+  KvView c;
+  const void* bounds;  // [n_pages][n_kv_heads][2][head_dim] act dtype
+  const void* q;
+  size_t q_stride;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int B, max_pages, n_q_heads, keep, first, last;
+  int32_t* pages;  // [B][n_kv_heads][keep]
+  int32_t* lens;   // [B]
+  float2* scores;  // [B][n_kv_heads][max_pages]: score, how far off it may be
+  int* status;
+};
+cudaError_t launch_select_pages(const SelectArgs& a, cudaStream_t st);
+
+// ---- eviction by accumulated attention weight ----------------------------------------------
+struct MassArgs {
+  KvView c;
+  const void* q;
+  size_t q_stride;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* lse;       // [B][n_q_heads]
+  const int32_t* known;   // [B], or nullptr
+  float* mass;            // [n_pages][n_kv_heads][page_size]
+  int B, max_pages, n_q_heads, window;
+  float scale;
+  int* status;
+};
+cudaError_t launch_attention_mass(const MassArgs& a, cudaStream_t st);
+struct EvictArgs {
+  KvView c;
+  float* mass;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* into;  // [B][into_pages]; block_table: in place
+  int B, max_pages, into_pages, keep, first, recent;
+  int32_t* kept;        // [B][n_kv_heads][keep]
+  int32_t* new_lens;    // [B]
+  int* status;
+};
+cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st);
 
 }  // namespace coli

@@ -1,0 +1,210 @@
+// Eviction by accumulated weight: each key head of a sequence keeps its first and
+// last tokens and those of the largest mass, whose rows are then copied together.
+//
+// k_evict_pick: a block a (sequence, key head); the masses come through the page table into
+// shared memory as ordered keys (tokens that are kept anyway: the largest key), and
+// pick.cuh finds the keep-th largest and lists the kept places in rising order.
+// k_evict_copy: into other pages, a block takes 64 kept tokens of a (sequence, key head),
+// keys and values and their scales and masses, 16 bytes a thread and step.
+// k_evict_pack: in place. A kept row moves to an earlier place or stays, so rows copied
+// in order, each batch read before it is written, never overwrite one that is still to be
+// read. A block takes 64 bytes of all of a head's rows (or its scales, or masses):
+// blocks share no byte.
+#include "mx.cuh"
+#include "pick.cuh"
+
+namespace coli {
+namespace {
+
+constexpr int kMostCached = 200 * 1024;  // bytes of keys that shared memory holds
+
+template <int THREADS, bool CACHED>
+__global__ void __launch_bounds__(THREADS) k_evict_pick(const EvictArgs p) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ PickShared s;
+  const int b = blockIdx.x / p.c.n_heads, h = blockIdx.x - b * p.c.n_heads;
+  const int page = p.c.page_size;
+  const int n = context_len(p.seq_lens, b, p.max_pages, page, p.status, threadIdx.x == 0);
+  int32_t* out = p.kept + static_cast<size_t>(blockIdx.x) * p.keep;
+  if (h == 0 && threadIdx.x == 0) p.new_lens[b] = min(n, p.keep);
+  const int32_t* table = p.block_table + static_cast<size_t>(b) * p.max_pages;
+  if (n <= p.keep) {
+    for (int i = threadIdx.x; i < p.keep; i += THREADS) out[i] = i < n ? i : -1;
+    return;
+  }
+  auto load = [&](int i) {
+    if (i < p.first || i >= n - p.recent) return 0xffffffffu;
+    const int pi = i / page, at = __ldg(table + pi);
+    if (at < 0 || at >= p.c.n_pages) {
+      latch_error(p.status, kErrDevice);
+      return order_key(-INFINITY);
+    }
+    return order_key(__ldg(p.mass + kv_row(p.c, at, h, i - pi * page)));
+  };
+  if constexpr (CACHED) {
+    for (int i = threadIdx.x; i < n; i += THREADS) s_keys[i] = load(i);
+    __syncthreads();
+  }
+  auto key = [&](int i) {
+    if constexpr (CACHED) return s_keys[i];
+    return load(i);
+  };
+  const Cut<uint32_t> cut = radix_cut<THREADS, true, uint32_t>(n, p.keep, key, s);
+  chosen<THREADS, uint32_t>(n, cut, key, [&](int r, int i) { out[r] = i; }, s);
+}
+
+// Row of the kept token of rank r, and the one it goes to; false where either page is none
+// of the pool's.
+COLI_DEV bool rows_of(const EvictArgs& p, int b, int h, int from, int r, size_t* src,
+                      size_t* dst) {
+  const int page = p.c.page_size;
+  const int sp = from / page, dp = r / page;
+  const int sa = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + sp);
+  const int da = __ldg(p.into + static_cast<size_t>(b) * p.into_pages + dp);
+  if (sa < 0 || sa >= p.c.n_pages || da < 0 || da >= p.c.n_pages) {
+    latch_error(p.status, kErrDevice);
+    return false;
+  }
+  *src = kv_row(p.c, sa, h, from - sp * page);
+  *dst = kv_row(p.c, da, h, r - dp * page);
+  return true;
+}
+
+constexpr int kCopyThreads = 256, kRanks = 64, kUnits = 4;
+
+__global__ void __launch_bounds__(kCopyThreads) k_evict_copy(const EvictArgs p, int chunks) {
+  __shared__ size_t s_src[kRanks], s_dst[kRanks];
+  __shared__ int s_in[kRanks];
+  const int bh = blockIdx.x / chunks, r0 = (blockIdx.x - bh * chunks) * kRanks;
+  const int b = bh / p.c.n_heads, h = bh - b * p.c.n_heads;
+  const int32_t* kept = p.kept + static_cast<size_t>(bh) * p.keep;
+  if (threadIdx.x < kRanks) {
+    const int r = r0 + threadIdx.x, from = r < p.keep ? kept[r] : -1;
+    s_in[threadIdx.x] =
+        from >= 0 && rows_of(p, b, h, from, r, &s_src[threadIdx.x], &s_dst[threadIdx.x]);
+    if (s_in[threadIdx.x]) p.mass[s_dst[threadIdx.x]] = p.mass[s_src[threadIdx.x]];
+  }
+  __syncthreads();
+  if (kept[r0] < 0) return;
+  const int U = p.c.row_bytes / 16, n = kRanks * U;
+#pragma unroll
+  for (int pool = 0; pool < 2; ++pool) {
+    char* base = pool ? p.c.v : p.c.k;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kCopyThreads * kUnits) {
+      uint4 v[kUnits];
+      size_t to[kUnits];
+#pragma unroll
+      for (int e = 0; e < kUnits; ++e) {
+        const int i = i0 + e * kCopyThreads, r = i / U, u = i - r * U;
+        to[e] = ~size_t(0);
+        if (i < n && s_in[r]) {
+          v[e] = *reinterpret_cast<const uint4*>(base + s_src[r] * p.c.row_bytes + u * 16);
+          to[e] = s_dst[r] * p.c.row_bytes + u * 16;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kUnits; ++e)
+        if (to[e] != ~size_t(0)) *reinterpret_cast<uint4*>(base + to[e]) = v[e];
+    }
+    if (p.c.scale_stride) {
+      uint8_t* sc = pool ? p.c.v_scale : p.c.k_scale;
+      const int words = p.c.scale_stride / 4;
+      for (int i = threadIdx.x; i < kRanks * words; i += kCopyThreads) {
+        const int r = i / words, u = i - r * words;
+        if (s_in[r])
+          *reinterpret_cast<uint32_t*>(sc + s_dst[r] * p.c.scale_stride + u * 4) =
+              *reinterpret_cast<const uint32_t*>(sc + s_src[r] * p.c.scale_stride + u * 4);
+      }
+    }
+  }
+}
+
+// sizeof(T) bytes a thread, `units` of them side by side from byte `off` of each
+// row of `base`.
+template <class T>
+COLI_DEV void pack_rows(const EvictArgs& p, int b, int h, char* base, int row, int off, int units) {
+  constexpr int kDeep = 4;
+  const int32_t* kept = p.kept + (static_cast<size_t>(b) * p.c.n_heads + h) * p.keep;
+  const int per = kCopyThreads / units, local = threadIdx.x / units;
+  const int u = threadIdx.x - local * units;
+  for (int r0 = 0; r0 < p.keep; r0 += per * kDeep) {
+    T v[kDeep];
+    size_t to[kDeep];
+    bool some = false;
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const int r = r0 + e * per + local, from = local < per && r < p.keep ? kept[r] : -1;
+      size_t src, dst;
+      to[e] = ~size_t(0);
+      some |= from >= 0;
+      if (from > r && rows_of(p, b, h, from, r, &src, &dst)) {
+        v[e] = *reinterpret_cast<const T*>(base + src * row + off + u * sizeof(T));
+        to[e] = dst * row + off + u * sizeof(T);
+      }
+    }
+    const bool go = __syncthreads_or(some);
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e)
+      if (to[e] != ~size_t(0)) *reinterpret_cast<T*>(base + to[e]) = v[e];
+    if (!go) return;
+    __syncthreads();
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) k_evict_pack(const EvictArgs p, int slices) {
+  const int kinds = 2 * slices + 1 + (p.c.scale_stride ? 2 : 0);
+  const int bh = blockIdx.x / kinds, x = blockIdx.x - bh * kinds;
+  const int b = bh / p.c.n_heads, h = bh - b * p.c.n_heads;
+  // a sequence that is kept whole stays where it is
+  if (context_len(p.seq_lens, b, p.max_pages, p.c.page_size, p.status, false) <= p.keep) return;
+  if (x < 2 * slices) {
+    const int off = x % slices * 64;
+    pack_rows<uint4>(p, b, h, x < slices ? p.c.k : p.c.v, p.c.row_bytes, off,
+                     min(64, p.c.row_bytes - off) / 16);
+  } else if (x == 2 * slices) {
+    pack_rows<uint32_t>(p, b, h, reinterpret_cast<char*>(p.mass), 4, 0, 1);
+  } else {
+    pack_rows<uint32_t>(p, b, h,
+                        reinterpret_cast<char*>(x == 2 * slices + 1 ? p.c.k_scale : p.c.v_scale),
+                        p.c.scale_stride, 0, p.c.scale_stride / 4);
+  }
+}
+
+template <int THREADS, bool CACHED>
+cudaError_t launch_pick(const EvictArgs& a, size_t smem, cudaStream_t st) {
+  if (CACHED) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_evict_pick<THREADS, CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostCached);
+    if (e != cudaSuccess) return e;
+  }
+  k_evict_pick<THREADS, CACHED><<<a.B * a.c.n_heads, THREADS, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
+  const int64_t most = static_cast<int64_t>(a.max_pages) * a.c.page_size;
+  cudaError_t e;
+  if (most * 4 > kMostCached)
+    e = launch_pick<1024, false>(a, 0, st);
+  else if (most > 8192)
+    e = launch_pick<1024, true>(a, most * 4, st);
+  else
+    e = launch_pick<256, true>(a, most * 4, st);
+  if (e != cudaSuccess) return e;
+  const int rows = a.B * a.c.n_heads;
+  if (a.into != a.block_table) {
+    const int chunks = (a.keep + kRanks - 1) / kRanks;
+    k_evict_copy<<<static_cast<unsigned>(static_cast<int64_t>(rows) * chunks), kCopyThreads, 0,
+                   st>>>(a, chunks);
+  } else {
+    const int slices = (a.c.row_bytes + 63) / 64;
+    const int kinds = 2 * slices + 1 + (a.c.scale_stride ? 2 : 0);
+    k_evict_pack<<<static_cast<unsigned>(static_cast<int64_t>(rows) * kinds), kCopyThreads, 0,
+                   st>>>(a, slices);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace coli

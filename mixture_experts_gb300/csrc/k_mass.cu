@@ -1,0 +1,274 @@
+// What each cached token weighed in a decode step, added to its mass.
+//
+// mass(j) += sum over the key head's query heads of exp(scale q.k_j - lse): with the
+// log-sum-exp known the weights need no maximum and no second pass, only the keys.
+//
+// A warp takes 16 tokens of a (sequence, key head) at once on the warp MMA: tokens are its 16
+// rows, 8 query heads its columns (NT column tiles, more heads in further passes over the
+// keys). The keys come from memory straight into the operand's registers: of every 32
+// channels lane 4g + t has 8t .. + 7 of rows g and g + 8, on both operands. bf16 queries
+// and keys are operands as they are; MX codes are widened to bf16 (exact) and a block's scale
+// goes on its partial score; fp32 runs in three tf32 products of operands in two parts.
+// HBM bound by the keys, a third of what the attention itself reads with its values.
+#include "mx.cuh"
+#include "paged.cuh"
+#include "pick.cuh"
+
+namespace coli {
+namespace {
+
+using namespace paged;
+
+constexpr int kMassWarps = 4;
+
+struct MassGrid {
+  MassArgs m;
+  int chunks;  // blocks of a (sequence, key head)
+};
+
+// Bytes of 8 channels in the cache.
+template <int FMT>
+constexpr int bytes8() {
+  return FMT == DT_F32 ? 32 : FMT == DT_BF16 ? 16 : FMT == DT_MXFP8 ? 8 : 4;
+}
+template <int FMT>
+struct Raw8 {
+  uint32_t w[bytes8<FMT>() / 4];
+};
+template <int FMT>
+COLI_DEV Raw8<FMT> load8(const char* p) {
+  Raw8<FMT> r;
+  if constexpr (FMT == DT_F32) {
+    const uint4 a = ldg_stream(p), b = ldg_stream(p + 16);
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+    r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+  } else if constexpr (FMT == DT_BF16) {
+    const uint4 a = ldg_stream(p);
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+  } else if constexpr (FMT == DT_MXFP8) {
+    const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+    r.w[0] = a.x, r.w[1] = a.y;
+  } else {
+    r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  }
+  return r;
+}
+// 8 codes as bf16 pairs (exact).
+template <int FMT>
+COLI_DEV void widen8(const Raw8<FMT>& r, uint32_t (&o)[4]) {
+  uint32_t h[4];
+  float x[8];
+  if constexpr (FMT == DT_MXFP8)
+    e4m3x8_f16(r.w[0], r.w[1], h);
+  else
+    e2m1x8_f16(r.w[0], h);
+  f16x8_f32(h, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+}
+
+// An fp32 score by itself: where infinities met the parts of the split products.
+__device__ __noinline__ float plain_score(const float* q, const float* k, int D) {
+  float x = 0.f;
+  for (int d = 0; d < D; ++d) x = fmaf(q[d], k[d], x);
+  return x;
+}
+
+template <int FMT, int DP, int NT>
+__global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
+  constexpr int kJ = DP / 32;
+  constexpr bool kF32 = FMT == DT_F32, kMx = FMT == DT_MXFP8 || FMT == DT_MXFP4;
+  const MassArgs& p = a.m;
+  const int bh = blockIdx.x / a.chunks, chunk = blockIdx.x - bh * a.chunks;
+  const int b = bh / p.c.n_heads, h = bh - b * p.c.n_heads;
+  const int lane = lane_id(), w = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
+  const int D = p.c.head_dim, group = p.n_q_heads / p.c.n_heads, page_size = p.c.page_size;
+  const int len = context_len(p.seq_lens, b, p.max_pages, page_size, p.status,
+                              h == 0 && chunk == 0 && threadIdx.x == 0);
+  const int start = p.window > 0 && len > p.window ? len - p.window : 0;
+  const int known = p.known == nullptr ? INT32_MAX : __ldg(p.known + b);
+  const int32_t* table = p.block_table + static_cast<size_t>(b) * p.max_pages;
+  const int tiles = (len + kTile - 1) / kTile, per_page = page_size / kTile;
+  const int t0 = start / kTile + chunk * kMassWarps + w, step = a.chunks * kMassWarps;
+  if (t0 >= tiles) return;
+
+  for (int r0 = 0; r0 < group; r0 += 8 * NT) {
+    // head r0 + 8 nt + g's elements; scales and lse of heads 2t, 2t + 1
+    uint32_t q[NT][kJ][kF32 ? 8 : 4];
+    float lse[NT][2];
+    bool live[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + nt * 8 + g;
+      const size_t at =
+          static_cast<size_t>(b) * p.q_stride + static_cast<size_t>(h * group + r) * D + t * 8;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const bool in = r < group && j * 32 + t * 8 < D;
+        const char* src = static_cast<const char*>(p.q) + (at + j * 32) * (kF32 ? 4 : 2);
+#pragma unroll
+        for (int e = 0; e < (kF32 ? 2 : 1); ++e) {
+          const uint4 u = in ? ldg_keep(src + 16 * e) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q[nt][j][4 * e + k] = word_of(u, k);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int head = r0 + nt * 8 + 2 * t + c;
+        lse[nt][c] = head < group
+                         ? __ldg(p.lse + static_cast<size_t>(b) * p.n_q_heads + h * group + head)
+                         : -INFINITY;
+        live[nt][c] = lse[nt][c] != -INFINITY;
+      }
+    }
+    for (int tile = t0; tile < tiles; tile += step) {
+      const int pi = tile / per_page, page = __ldg(table + pi);
+      if (page < 0 || page >= p.c.n_pages) {
+        if (lane == 0) latch_error(p.status, kErrDevice);
+        continue;
+      }
+      const size_t row = kv_row(p.c, page, h, (tile - pi * per_page) * kTile);
+      const char* src = p.c.k + (row + g) * p.c.row_bytes + t * bytes8<FMT>();
+      Raw8<FMT> raw[kJ][2];
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          raw[j][e] = Raw8<FMT>{};
+          if (j * 32 + t * 8 < D)
+            raw[j][e] = load8<FMT>(src + static_cast<size_t>(e) * 8 * p.c.row_bytes +
+                                   j * 4 * bytes8<FMT>());
+        }
+      uint32_t sc[2][2] = {};
+      if constexpr (kMx) {
+        const uint8_t* s = p.c.k_scale + (row + g) * p.c.scale_stride;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sc[e][0] = __ldg(reinterpret_cast<const uint32_t*>(s + e * 8 * p.c.scale_stride));
+          if (DP > 128 && p.c.scale_stride > 4)
+            sc[e][1] = __ldg(reinterpret_cast<const uint32_t*>(s + e * 8 * p.c.scale_stride + 4));
+        }
+      }
+      float x[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[nt][c] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        if constexpr (kF32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float hi[4], lo[4];
+            split_tf32(__uint_as_float(raw[j][0].w[2 * e]), &hi[0], &lo[0]);
+            split_tf32(__uint_as_float(raw[j][1].w[2 * e]), &hi[1], &lo[1]);
+            split_tf32(__uint_as_float(raw[j][0].w[2 * e + 1]), &hi[2], &lo[2]);
+            split_tf32(__uint_as_float(raw[j][1].w[2 * e + 1]), &hi[3], &lo[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float qh[2], ql[2];
+              split_tf32(__uint_as_float(q[nt][j][2 * e]), &qh[0], &ql[0]);
+              split_tf32(__uint_as_float(q[nt][j][2 * e + 1]), &qh[1], &ql[1]);
+              mma_tf32_1688(x[nt], lo, qh);
+              mma_tf32_1688(x[nt], hi, ql);
+              mma_tf32_1688(x[nt], hi, qh);
+            }
+          }
+        } else if constexpr (!kMx) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16_16816(x[nt], raw[j][0].w[0], raw[j][1].w[0], raw[j][0].w[1], raw[j][1].w[1],
+                           q[nt][j][0], q[nt][j][1]);
+            mma_bf16_16816(x[nt], raw[j][0].w[2], raw[j][1].w[2], raw[j][0].w[3], raw[j][1].w[3],
+                           q[nt][j][2], q[nt][j][3]);
+          }
+        } else {
+          if (j * 32 >= D) break;  // scale bytes there may hold anything
+          uint32_t k0[4], k1[4];
+          widen8<FMT>(raw[j][0], k0);
+          widen8<FMT>(raw[j][1], k1);
+          const float f0 = e8m0_f32(sc[0][j / 4] >> 8 * (j % 4) & 0xffu);
+          const float f1 = e8m0_f32(sc[1][j / 4] >> 8 * (j % 4) & 0xffu);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float d[4];
+            mma_bf16_16816_z(d, k0[0], k1[0], k0[1], k1[1], q[nt][j][0], q[nt][j][1]);
+            mma_bf16_16816(d, k0[2], k1[2], k0[3], k1[3], q[nt][j][2], q[nt][j][3]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(d[c], c < 2 ? f0 : f1, x[nt][c]);
+          }
+        }
+      }
+      if constexpr (kF32) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (x[nt][c] != x[nt][c] && live[nt][c & 1])
+              x[nt][c] = plain_score(
+                  static_cast<const float*>(p.q) + static_cast<size_t>(b) * p.q_stride +
+                      static_cast<size_t>(h * group + r0 + nt * 8 + 2 * t + (c & 1)) * D,
+                  reinterpret_cast<const float*>(p.c.k) + (row + g + (c >> 1) * 8) * D, D);
+      }
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float y = fmaf(x[nt][c], p.scale, -lse[nt][c & 1]) * 1.4426950408889634f;
+          sum[c >> 1] += live[nt][c & 1] ? ex2(y) : 0.f;
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int k = 1; k < 4; k <<= 1) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], k);
+      const int at = g + (t & 1) * 8, j = tile * kTile + at;
+      if (t < 2 && j >= start && j < len) {
+        float* m = p.mass + row + at;
+        const float v = t ? sum[1] : sum[0];
+        if (j >= known && r0 == 0)
+          *m = v;
+        else
+          atomicAdd(m, v);
+      }
+    }
+  }
+}
+
+template <int FMT, int DP>
+void launch_group(const MassGrid& p, unsigned grid, cudaStream_t st) {
+  if (p.m.n_q_heads / p.m.c.n_heads <= 8)
+    k_mass<FMT, DP, 1><<<grid, kMassWarps * 32, 0, st>>>(p);
+  else
+    k_mass<FMT, DP, 2><<<grid, kMassWarps * 32, 0, st>>>(p);
+}
+template <int FMT>
+void launch_heads(const MassGrid& p, unsigned grid, cudaStream_t st) {
+  if (p.m.c.head_dim <= 64)
+    launch_group<FMT, 64>(p, grid, st);
+  else if (p.m.c.head_dim <= 128)
+    launch_group<FMT, 128>(p, grid, st);
+  else
+    launch_group<FMT, 256>(p, grid, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_mass(const MassArgs& a, cudaStream_t st) {
+  const int rows = a.B * a.c.n_heads;
+  const int64_t tiles = static_cast<int64_t>(a.max_pages) * (a.c.page_size / kTile);
+  const int64_t most = (tiles + kMassWarps - 1) / kMassWarps;
+  const int fill = (sm_count() * 16 + rows - 1) / rows;
+  const MassGrid p{a, static_cast<int>(most < fill ? most : fill)};
+  const unsigned grid = static_cast<unsigned>(rows) * p.chunks;
+  switch (a.c.dtype) {
+    case DT_F32: launch_heads<DT_F32>(p, grid, st); break;
+    case DT_BF16: launch_heads<DT_BF16>(p, grid, st); break;
+    case DT_MXFP8: launch_heads<DT_MXFP8>(p, grid, st); break;
+    default: launch_heads<DT_MXFP4>(p, grid, st);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace coli

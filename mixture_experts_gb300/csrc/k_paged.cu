@@ -99,13 +99,9 @@ __global__ void __launch_bounds__(256) k_join(const Params p) {
     for (int c = 0; c < 2; ++c) {
       const int r = row0 + nt * 8 + 2 * t + c;
       if (r >= p.group) continue;
-      const int hq = h * p.group + r;
-      store_out<IN_ORDER, F32>(
-          a, static_cast<size_t>(b) * a.out_stride + static_cast<size_t>(hq) * D, i, g,
-          l[c] == 0.f ? 0.f : o[c], l[c] == 0.f ? 0.f : o[c + 2]);
-      if (a.lse != nullptr && i == 0 && g == 0)
-        a.lse[static_cast<size_t>(b) * a.n_q_heads + hq] =
-            l[c] == 0.f ? -INFINITY : (m[c] + log2f(l[c])) * 0.6931471805599453f;
+      store_out<IN_ORDER, F32>(a, row_at(a, p.group, b, h, r, a.out_stride, D), i, g,
+                               l[c] == 0.f ? 0.f : o[c], l[c] == 0.f ? 0.f : o[c + 2]);
+      if (a.lse != nullptr && i == 0 && g == 0) store_lse(a, p.group, b, h, r, m[c], l[c]);
     }
   }
 }
@@ -124,16 +120,6 @@ cudaError_t launch_join(const Params& p, int grid, int ys, cudaStream_t st) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k_join<DP, NT, F32, IN_ORDER>, p);
-}
-
-int sm_count() {
-  static int n[128] = {};
-  int dev = 0, v = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 152;
-  if (n[dev] == 0 &&
-      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
-    n[dev] = v;
-  return n[dev] ? n[dev] : 152;
 }
 
 struct Form {
@@ -193,9 +179,19 @@ cudaError_t launch_joins(const Params& p, const Form& f, int grid, int ys, cudaS
 }  // namespace
 }  // namespace paged
 
+int sm_count() {
+  static int n[128] = {};
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 152;
+  if (n[dev] == 0 &&
+      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    n[dev] = v;
+  return n[dev] ? n[dev] : 152;
+}
+
 size_t paged_scratch_bytes(const KvView& c, int B, int n_q_heads) {
   const paged::Form f = paged::form_of(c, n_q_heads);
-  const size_t blocks = static_cast<size_t>(paged::sm_count()) * f.per_sm;
+  const size_t blocks = static_cast<size_t>(sm_count()) * f.per_sm;
   return blocks * (2 * f.part * sizeof(float) + sizeof(int4));
 }
 

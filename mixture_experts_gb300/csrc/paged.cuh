@@ -242,11 +242,35 @@ template <bool IN_ORDER>
 COLI_DEV int channel(int i, int g, int c) {
   return IN_ORDER ? i * 16 + g + (c >> 1) * 8 : (i >> 2) * 64 + g * 8 + (i & 3) * 2 + (c >> 1);
 }
+// Place of query row r of key head h of sequence b in rows of heads `width` apart, tokens
+// `stride` apart: head h group + r of the sequence, or, where a.fold sequences' queries of a key
+// head follow each other as one group, head h fold + r % fold of sequence r / fold.
+COLI_DEV size_t row_at(const PagedArgs& a, int group, int b, int h, int r, size_t stride,
+                       int width) {
+  if (a.fold > 0) {
+    const int s = r / a.fold;
+    return s * stride + static_cast<size_t>(h * a.fold + r - s * a.fold) * width;
+  }
+  return b * stride + static_cast<size_t>(h * group + r) * width;
+}
+// log sum of a row's weights 2^(x - m), or with a.raw the pair (m, sum) for a later join.
+COLI_DEV void store_lse(const PagedArgs& a, int group, int b, int h, int r, float m, float sum) {
+  const int n = a.fold > 0 ? a.fold * a.c.n_heads : a.n_q_heads;
+  const size_t at = row_at(a, group, b, h, r, n, 1);
+  if (a.raw)
+    reinterpret_cast<float2*>(a.lse)[at] = make_float2(m, sum);
+  else
+    a.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+}
 // Two outputs (channels of c and c + 2) of one head.
 template <bool IN_ORDER, bool F32>
 COLI_DEV void store_out(const PagedArgs& a, size_t row, int i, int g, float y0, float y1) {
   const int d = channel<IN_ORDER>(i, g, 0), e = channel<IN_ORDER>(i, g, 2), D = a.c.head_dim;
-  if constexpr (IN_ORDER) {
+  if (!F32 && a.raw) {  // fp32 means, for a later join
+    float* o = static_cast<float*>(a.out) + row;
+    if (d < D) o[d] = y0;
+    if (e < D) o[e] = y1;
+  } else if constexpr (IN_ORDER) {
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + row;
     if (d < D) o[d] = __float2bfloat16_rn(y0);
     if (e < D) o[e] = __float2bfloat16_rn(y1);
@@ -313,13 +337,19 @@ COLI_DEV long long quotient(long long a, long long b) {
   return a / b;
 }
 
+// Where the pages of a sequence's key head are listed: the sequence's row, or its own.
+COLI_DEV size_t table_at(const PagedArgs& a, int b, int h) {
+  const size_t row = a.head_tables ? static_cast<size_t>(b) * a.c.n_heads + h : b;
+  return row * a.max_pages;
+}
+
 // The line of work: tiles of sequence b, in tiles of 16 keys counted from the
 // context's start.
 struct Seq {
   int len, first, n;  // length, first tile, number of tiles
 };
 COLI_DEV Seq seq_of(const PagedArgs& a, int b, bool latch) {
-  int len = __ldg(a.seq_lens + b);
+  int len = a.fixed_len > 0 ? a.fixed_len : __ldg(a.seq_lens + b);
   const int most = a.max_pages * a.c.page_size;
   if (len < 0 || len > most) {
     if (latch) latch_error(a.status, kErrDevice);
@@ -369,7 +399,7 @@ __device__ __noinline__ void plain_tiles(const PagedArgs a, int group, int b, in
     const int tile = tile0 + n / S * (W * S) + n % S;
     if (tile >= tile_end) break;
     const int pi = tile / tiles_per_page;
-    const int page = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
+    const int page = __ldg(a.block_table + table_at(a, b, h) + pi);
     if (page < 0 || page >= a.c.n_pages) continue;
     const size_t at = kv_row(a.c, page, h, (tile - pi * tiles_per_page) * kTile);
     const int r1 = min(kTile, key_end - tile * kTile);
@@ -385,8 +415,8 @@ __device__ __noinline__ void plain_tiles(const PagedArgs a, int group, int b, in
           for (int c = 0; c < 2; ++c) {
             const int hd = row0 + nt * 8 + 2 * t + c;
             if (hd >= group) continue;
-            const uint4 u = ldg_keep(static_cast<const __nv_bfloat16*>(a.q) + b * a.q_stride +
-                                     static_cast<size_t>(h * group + hd) * D + ch);
+            const uint4 u = ldg_keep(static_cast<const __nv_bfloat16*>(a.q) +
+                                     row_at(a, group, b, h, hd, a.q_stride, D) + ch);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               s[nt][c] = fmaf(bf16_lo(word_of(u, k)), x[2 * k], s[nt][c]);
@@ -527,13 +557,13 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   // sequences with nothing to see: zeros, lse -inf
   for (int e = blockIdx.x; e < a.B; e += gridDim.x) {
     if (seq_of(a, e, false).n > 0) continue;
-    const int bytes = a.n_q_heads * a.c.head_dim * (kF32 ? 4 : 2);
-    char* o = static_cast<char*>(a.out) + static_cast<size_t>(e) * a.out_stride * (kF32 ? 4 : 2);
+    const int wide = kF32 || a.raw ? 4 : 2, bytes = a.n_q_heads * a.c.head_dim * wide;
+    char* o = static_cast<char*>(a.out) + static_cast<size_t>(e) * a.out_stride * wide;
     for (int i = threadIdx.x * 16; i < bytes; i += W * 32 * 16)
       *reinterpret_cast<uint4*>(o + i) = make_uint4(0, 0, 0, 0);
     if (a.lse != nullptr)
       for (int i = threadIdx.x; i < a.n_q_heads; i += W * 32)
-        a.lse[static_cast<size_t>(e) * a.n_q_heads + i] = -INFINITY;
+        store_lse(a, a.n_q_heads, e, 0, i, -FLT_MAX, 0.f);
   }
   if (u0 >= total) return;
 
@@ -599,7 +629,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     tile_of = kNone;
     if (tile < tile_end) {
       const int pi = tile / tiles_per_page;
-      const int page = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pi);
+      const int page = __ldg(a.block_table + table_at(a, b, h) + pi);
       if (page < 0 || page >= a.c.n_pages)
         latch_error(a.status, kErrDevice);
       else
@@ -729,8 +759,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row0 + nt * 8 + g;
-      const size_t at = static_cast<size_t>(b) * a.q_stride +
-                        static_cast<size_t>(h * p.group + r) * D;
+      const size_t at = row_at(a, p.group, b, h, r, a.q_stride, D);
       xs[nt][0] = xs[nt][1] = sl;
       if constexpr (kF32) {
         // in shared memory, once a block: per 8 elements t and t + 4 in two tf32 parts
@@ -1504,13 +1533,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           for (int c = 0; c < 2; ++c) {
             const int r = orow0 + nt * 8 + 2 * t + c;
             if (r >= p.group) continue;
-            const int hq = oh * p.group + r;
-            store_out<FMT == DT_BF16, kF32>(
-                a, static_cast<size_t>(ob) * a.out_stride + static_cast<size_t>(hq) * D, i, g,
-                sum[c] == 0.f ? 0.f : o[c], sum[c] == 0.f ? 0.f : o[c + 2]);
+            store_out<FMT == DT_BF16, kF32>(a, row_at(a, p.group, ob, oh, r, a.out_stride, D), i, g,
+                                            sum[c] == 0.f ? 0.f : o[c],
+                                            sum[c] == 0.f ? 0.f : o[c + 2]);
             if (a.lse != nullptr && i == 0 && g == 0)
-              a.lse[static_cast<size_t>(ob) * a.n_q_heads + hq] =
-                  sum[c] == 0.f ? -INFINITY : (mx[c] + log2f(sum[c])) * 0.6931471805599453f;
+              store_lse(a, p.group, ob, oh, r, mx[c], sum[c]);
           }
         }
       }

@@ -1,0 +1,136 @@
+// The K largest of n keys by one block: a radix select on 11-bit digits, then the
+// places of the chosen ones in rising order; of equal keys the earlier places.
+#pragma once
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace coli {
+
+// Tokens of sequence b: within the table, else latched and cut.
+COLI_DEV int context_len(const int32_t* seq_lens, int b, int max_pages, int page_size, int* status,
+                         bool latch) {
+  int len = __ldg(seq_lens + b);
+  const int most = max_pages * page_size;
+  if (len < 0 || len > most) {
+    if (latch) latch_error(status, kErrDevice);
+    len = len < 0 ? 0 : most;
+  }
+  return len;
+}
+
+// Unsigned keys in the numbers' order; NaN counts as -infinity.
+COLI_DEV uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x != x ? -INFINITY : x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+COLI_DEV uint64_t order_key(double x) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x != x ? -INFINITY : x));
+  return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+
+constexpr int kDigit = 11, kBins = 1 << kDigit;
+
+struct PickShared {
+  int bins[kBins];
+  int warp[2][32];
+  int bin, above, in_bin;
+};
+
+// What is chosen: keys from `from` on, but of those equal to it only the first `equal`.
+template <class Key>
+struct Cut {
+  Key from;
+  int equal;
+};
+
+// 1 <= K <= n; key(i) for i < n. Every thread of the block calls it. EARLY: a bin that is
+// chosen whole ends the search (`from` is then the bin's least key, not one of the n).
+template <int THREADS, bool EARLY, class Key, class F>
+COLI_DEV Cut<Key> radix_cut(int n, int K, F key, PickShared& s) {
+  constexpr int kBits = sizeof(Key) * 8, kPasses = (kBits + kDigit - 1) / kDigit;
+  Key prefix = 0;
+  int need = K;
+#pragma unroll 1
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int shift = kBits - (pass + 1) * kDigit > 0 ? kBits - (pass + 1) * kDigit : 0;
+    const int width = kBits - pass * kDigit - shift, high = shift + width;
+    for (int i = threadIdx.x; i < kBins; i += THREADS) s.bins[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+      const Key k = key(i);
+      if (high >= kBits || (k >> (high & (kBits - 1))) == prefix)
+        atomicAdd(&s.bins[static_cast<int>(k >> shift) & ((1 << width) - 1)], 1);
+    }
+    __syncthreads();
+    // thread t: the bins from kBins - (t + 1) * kEach up; counts of the bins above
+    constexpr int kEach = kBins / THREADS;
+    const int lane = lane_id(), w = threadIdx.x / 32, low = kBins - (threadIdx.x + 1) * kEach;
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) sum += s.bins[low + i];
+    int upto = sum;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, i);
+      if (lane >= i) upto += o;
+    }
+    if (lane == 31) s.warp[0][w] = upto;
+    __syncthreads();
+    for (int i = 0; i < w; ++i) upto += s.warp[0][i];
+    if (upto >= need && upto - sum < need) {
+      int above = upto - sum;
+      for (int i = kEach - 1; i >= 0; --i) {
+        const int c = s.bins[low + i];
+        if (above + c >= need) {
+          s.bin = low + i;
+          s.above = above;
+          s.in_bin = c;
+          break;
+        }
+        above += c;
+      }
+    }
+    __syncthreads();
+    prefix = static_cast<Key>(prefix << width) | static_cast<Key>(s.bin);
+    need -= s.above;
+    const int in_bin = s.in_bin;
+    __syncthreads();
+    if (EARLY && in_bin == need) return {static_cast<Key>(prefix << shift), n};  // the whole bin
+  }
+  return {prefix, need};
+}
+
+// put(rank, i) for the chosen places i in rising order.
+template <int THREADS, class Key, class F, class P>
+COLI_DEV void chosen(int n, const Cut<Key>& cut, F key, P put, PickShared& s) {
+  constexpr int kW = THREADS / 32;
+  const int lane = lane_id(), w = threadIdx.x / 32;
+  const int each = ((n + kW - 1) / kW + 31) / 32 * 32;  // places of a warp
+  const int i0 = w * each, i1 = min(n, i0 + each);
+  int over = 0, same = 0;
+  for (int i = i0; i < i1; i += 32) {
+    const Key k = i + lane < i1 ? key(i + lane) : 0;
+    const bool in = i + lane < i1;
+    over += __popc(__ballot_sync(0xffffffffu, in && k > cut.from));
+    same += __popc(__ballot_sync(0xffffffffu, in && k == cut.from));
+  }
+  if (lane == 0) s.warp[0][w] = over, s.warp[1][w] = same;
+  __syncthreads();
+  int a = 0, b = 0;  // chosen above and equal ones before this warp's places
+  for (int i = 0; i < w; ++i) a += s.warp[0][i], b += s.warp[1][i];
+  for (int i = i0; i < i1; i += 32) {
+    const Key k = i + lane < i1 ? key(i + lane) : 0;
+    const bool in = i + lane < i1;
+    const uint32_t hi = __ballot_sync(0xffffffffu, in && k > cut.from);
+    const uint32_t eq = __ballot_sync(0xffffffffu, in && k == cut.from);
+    const uint32_t below = (1u << lane) - 1;
+    const int ra = a + __popc(hi & below), rb = b + __popc(eq & below);
+    if (in && (k > cut.from || (k == cut.from && rb < cut.equal)))
+      put(ra + min(rb, cut.equal), i + lane);
+    a += __popc(hi);
+    b += __popc(eq);
+  }
+}
+
+}  // namespace coli
