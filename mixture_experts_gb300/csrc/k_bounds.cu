@@ -46,35 +46,9 @@ COLI_DEV uint32_t max_f32(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Words of the act dtype that 16 stored bytes make.
-template <int FMT>
-constexpr int words() {
-  return FMT == DT_MXFP8 ? 8 : (FMT == DT_MXFP4 ? 16 : 4);
-}
-template <int FMT>
-COLI_DEV void decode16(const uint4& raw, uint32_t scale, uint32_t (&w)[words<FMT>()]) {
-  if constexpr (FMT == DT_F32 || FMT == DT_BF16) {
-    w[0] = raw.x, w[1] = raw.y, w[2] = raw.z, w[3] = raw.w;
-  } else {
-    const float f = e8m0_f32(scale);
-#pragma unroll
-    for (int i = 0; i < words<FMT>() / 4; ++i) {
-      uint32_t h[4];
-      float x[8];
-      if constexpr (FMT == DT_MXFP8)
-        e4m3x8_f16(word_of(raw, 2 * i), word_of(raw, 2 * i + 1), h);
-      else
-        e2m1x8_f16(word_of(raw, i), h);
-      f16x8_f32(h, x);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[4 * i + k] = pack_bf16x2(x[2 * k] * f, x[2 * k + 1] * f);
-    }
-  }
-}
-
 template <int FMT>
 __global__ void __launch_bounds__(kWarps * 32) k_page_bounds(const BoundsArgs p) {
-  constexpr int W = words<FMT>();
+  constexpr int W = words16<FMT>();
   constexpr bool kF32 = FMT == DT_F32, kMx = FMT == DT_MXFP8 || FMT == DT_MXFP4;
   const int lane = lane_id();
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;

@@ -7,8 +7,8 @@
 // rows, 8 query heads its columns (NT column tiles, more heads in further passes over the
 // keys). The keys come from memory straight into the operand's registers: of every 32
 // channels lane 4g + t has 8t .. + 7 of rows g and g + 8, on both operands. bf16 queries
-// and keys are operands as they are; MX codes are widened to bf16 (exact) and a block's scale
-// goes on its partial score; fp32 runs in three tf32 products of operands in two parts.
+// and keys are operands as they are; MX keys are widened to bf16 with their scale (exact within
+// bf16's range); fp32 runs in three tf32 products of operands in two parts.
 // HBM bound by the keys, a third of what the attention itself reads with its values.
 #include "mx.cuh"
 #include "paged.cuh"
@@ -53,20 +53,6 @@ COLI_DEV Raw8<FMT> load8(const char* p) {
   }
   return r;
 }
-// 8 codes as bf16 pairs (exact).
-template <int FMT>
-COLI_DEV void widen8(const Raw8<FMT>& r, uint32_t (&o)[4]) {
-  uint32_t h[4];
-  float x[8];
-  if constexpr (FMT == DT_MXFP8)
-    e4m3x8_f16(r.w[0], r.w[1], h);
-  else
-    e2m1x8_f16(r.w[0], h);
-  f16x8_f32(h, x);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-}
-
 // An fp32 score by itself: where infinities met the parts of the split products.
 __device__ __noinline__ float plain_score(const float* q, const float* k, int D) {
   float x = 0.f;
@@ -175,7 +161,7 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
               mma_tf32_1688(x[nt], hi, qh);
             }
           }
-        } else if constexpr (!kMx) {
+        } else if constexpr (FMT == DT_BF16) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_bf16_16816(x[nt], raw[j][0].w[0], raw[j][1].w[0], raw[j][0].w[1], raw[j][1].w[1],
@@ -183,22 +169,46 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
             mma_bf16_16816(x[nt], raw[j][0].w[2], raw[j][1].w[2], raw[j][0].w[3], raw[j][1].w[3],
                            q[nt][j][2], q[nt][j][3]);
           }
-        } else {
-          if (j * 32 >= D) break;  // scale bytes there may hold anything
-          uint32_t k0[4], k1[4];
-          widen8<FMT>(raw[j][0], k0);
-          widen8<FMT>(raw[j][1], k1);
-          const float f0 = e8m0_f32(sc[0][j / 4] >> 8 * (j % 4) & 0xffu);
-          const float f1 = e8m0_f32(sc[1][j / 4] >> 8 * (j % 4) & 0xffu);
+        }
+      }
+      if constexpr (kMx) {
+        // MX codes under their scale as bf16 operands, the fast way where the lane's codes allow it
+        uint32_t odd = 0;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float d[4];
-            mma_bf16_16816_z(d, k0[0], k1[0], k0[1], k1[1], q[nt][j][0], q[nt][j][1]);
-            mma_bf16_16816(d, k0[2], k1[2], k0[3], k1[3], q[nt][j][2], q[nt][j][3]);
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(d[c], c < 2 ? f0 : f1, x[nt][c]);
+          for (int i = 0; i < (DP > 128 ? 2 : 1); ++i) {
+            const int n = D / kMxBlock - 4 * i;  // bytes past the head's blocks may hold anything
+            sc[e][i] &= n >= 4 ? 0xffffffffu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
+            odd |= __vcmpgtu4(sc[e][i], kMxFast * 0x01010101u);
+          }
+          if constexpr (FMT == DT_MXFP8) {
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+              odd |= e4m3_nans(raw[j][e].w[0]) | e4m3_nans(raw[j][e].w[1]);
           }
         }
+        auto products = [&](auto fast) {
+          constexpr bool kFast = decltype(fast)::value;
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            uint32_t k0[4], k1[4];
+            const int last = bytes8<FMT>() / 4 - 1;
+            mx8_bf16<FMT, kFast>(raw[j][0].w[0], raw[j][0].w[last],
+                                 sc[0][j / 4] >> 8 * (j % 4) & 0xffu, k0);
+            mx8_bf16<FMT, kFast>(raw[j][1].w[0], raw[j][1].w[last],
+                                 sc[1][j / 4] >> 8 * (j % 4) & 0xffu, k1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_bf16_16816(x[nt], k0[0], k1[0], k0[1], k1[1], q[nt][j][0], q[nt][j][1]);
+              mma_bf16_16816(x[nt], k0[2], k1[2], k0[3], k1[3], q[nt][j][2], q[nt][j][3]);
+            }
+          }
+        };
+        if (!__any_sync(0xffffffffu, odd != 0))
+          products(std::integral_constant<bool, true>());
+        else
+          products(std::integral_constant<bool, false>());
       }
       if constexpr (kF32) {
 #pragma unroll
@@ -238,10 +248,14 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
 
 template <int FMT, int DP>
 void launch_group(const MassGrid& p, unsigned grid, cudaStream_t st) {
-  if (p.m.n_q_heads / p.m.c.n_heads <= 8)
-    k_mass<FMT, DP, 1><<<grid, kMassWarps * 32, 0, st>>>(p);
-  else
-    k_mass<FMT, DP, 2><<<grid, kMassWarps * 32, 0, st>>>(p);
+  // two column tiles where there are heads for them and registers (fp32 heads of 256 spill)
+  constexpr bool kTwo = FMT != DT_F32 || DP < 256;
+  if constexpr (kTwo)
+    if (p.m.n_q_heads / p.m.c.n_heads > 8) {
+      k_mass<FMT, DP, 2><<<grid, kMassWarps * 32, 0, st>>>(p);
+      return;
+    }
+  k_mass<FMT, DP, 1><<<grid, kMassWarps * 32, 0, st>>>(p);
 }
 template <int FMT>
 void launch_heads(const MassGrid& p, unsigned grid, cudaStream_t st) {

@@ -1,0 +1,553 @@
+// Attention of many sequences' queries over one shared prefix, on the tcgen05 tensor cores.
+//
+// Mathematics. The queries of all sequences that share a key head are the rows of one matrix
+// (R = B * heads of a group), so the prefix is attention with R queries: S = Q K^T,
+// P = 2^(s x - m), O += P V with a running maximum m, the prefix read once for 128 rows
+// instead of once for each sequence.
+//
+// A block takes 128 rows of a key head and a run of 128-key tiles. Its tiles alternate between
+// two streams, each with its own S, O, m and l in tensor memory and registers of its own
+// warpgroup (columns 0-127 and 128-255 S, 256-511 O), so one stream's softmax runs under the
+// other's products: the MMA warp issues S(0) S(1) PV(0) S(2) PV(1) ... in order. P goes back
+// over S's columns as two bf16 terms, the weight and what its rounding left (16 bits together),
+// and is the second product's A operand from tensor memory; V is its B operand as it lies
+// (keys by channels, "transposed"). m is raised only where a score passes it (weights are
+// 2^-8 at a new maximum and rise to 1), so O is rarely rescaled.
+//
+// Loader warps bring K and V tiles to 128-byte swizzled shared memory: bf16 by cp.async, MX
+// codes widened to bf16 with their scale (exact within bf16's range, which is fp32's). Rows
+// past the prefix and of pages that are left out are zeros there and -inf in the scores.
+//
+// Work split: the tiles of all (key head, 128 rows) segments lie on one line that is cut into
+// equal pieces, one a block; a piece's part of a segment gives a partial mean with (m, l), in
+// slot (block + segment), which k_shared_join joins in the line's order with each sequence's
+// own tokens.
+#include "tcgen05.cuh"
+
+#include "mx.cuh"
+#include "paged.cuh"
+#include "prefix.h"
+
+namespace coli {
+namespace {
+
+using paged::cp_async16_n;
+using paged::ex2;
+
+constexpr int kSub = kPrefixRows * 128;  // bytes of 128 rows of 64 channels
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoad0 = 9;
+constexpr int kStagesK = 3, kStagesV = 2;
+constexpr uint32_t kOCol = 256;          // O of the streams; S at 0 and 128
+constexpr uint32_t kNone = 0xffffffffu;
+
+template <int FMT>
+constexpr int load_warps() {
+  return FMT == DT_BF16 ? 4 : 8;
+}
+template <int FMT>
+constexpr int threads() {
+  return (kLoad0 + load_warps<FMT>()) * 32;
+}
+
+struct Ctrl {
+  uint64_t kfull[kStagesK], kfree[kStagesK], vfull[kStagesV], vfree[kStagesV];
+  uint64_t q_full, q_free, s_full[2], p_full[2], o_full, o_free, ml_full;
+  uint32_t tmem;
+  int abort;
+  float2 ml[2][2][kPrefixRows];  // by piece's parity, stream
+};
+
+template <int DP>
+constexpr int smem_bytes() {
+  return 1024 + DP / 64 * kSub * (1 + kStagesK + kStagesV) + static_cast<int>(sizeof(Ctrl));
+}
+
+// B operand as it lies: 16-bit elements, reduction rows of 128 bytes (64 columns), 8 rows 1024
+// bytes apart, the next 64 columns a sub-tile further; 128-byte swizzle.
+COLI_DEV uint64_t sw128_desc_mn(uint32_t addr) {
+  uint64_t d = static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kSub >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// Waits for a phase; gives up, and has the block do so, after kWaitTimeoutNs.
+COLI_DEV bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t deadline = global_timer_ns() + kWaitTimeoutNs;
+  return wait_bar(bar, parity, deadline, abort);
+}
+
+COLI_DEV void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+COLI_DEV void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// Place of 16-byte chunk c of row r in a tile of 64-channel sub-tiles, 128-byte swizzle.
+COLI_DEV uint32_t place(int r, int c) {
+  return (c >> 3) * kSub + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// Bits i: keys 16 i .. of the tile are in sight (lanes 0-7 look their pages up).
+COLI_DEV uint32_t groups_in_sight(const PrefixArgs& p, int key0) {
+  const int key = key0 + (lane_id() & 7) * 16;
+  bool in = key < p.len;
+  if (in) {
+    const int page = __ldg(p.pages + key / p.c.page_size);
+    in = page >= 0 && page < p.c.n_pages;
+  }
+  return __ballot_sync(0xffffffffu, in) & 0xffu;
+}
+
+// A block's pieces: segment by segment along its part of the line.
+struct Walk {
+  int64_t pos, end;
+  int seg, t0, n;
+  COLI_DEV Walk(const PrefixArgs& p) {
+    pos = blockIdx.x * p.per;
+    end = pos + p.per < p.total ? pos + p.per : p.total;
+  }
+  COLI_DEV bool next(const PrefixArgs& p) {
+    if (pos >= end) return false;
+    seg = static_cast<int>(pos / p.tiles);
+    t0 = static_cast<int>(pos - static_cast<int64_t>(seg) * p.tiles);
+    const int64_t left = end - pos;
+    n = left < p.tiles - t0 ? static_cast<int>(left) : p.tiles - t0;
+    pos += n;
+    return true;
+  }
+};
+
+template <int FMT, int DP>
+__global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p) {
+  constexpr int kTileBytes = DP / 64 * kSub;
+  constexpr int LT = load_warps<FMT>() * 32;
+  extern __shared__ char smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t s_q = base, s_k = base + kTileBytes, s_v = s_k + kStagesK * kTileBytes;
+  Ctrl& C = *reinterpret_cast<Ctrl*>(smem_raw + (base - smem_u32(smem_raw)) +
+                                     kTileBytes * (1 + kStagesK + kStagesV));
+  volatile int* abort = &C.abort;
+  const int warp = threadIdx.x / 32, lane = lane_id();
+  const int D = p.c.head_dim;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStagesK; ++i) {
+      mbar_init(smem_u32(&C.kfull[i]), LT);
+      mbar_init(smem_u32(&C.kfree[i]), 1);
+    }
+    for (int i = 0; i < kStagesV; ++i) {
+      mbar_init(smem_u32(&C.vfull[i]), LT);
+      mbar_init(smem_u32(&C.vfree[i]), 1);
+    }
+    mbar_init(smem_u32(&C.q_full), LT);
+    mbar_init(smem_u32(&C.q_free), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&C.s_full[i]), 1);
+      mbar_init(smem_u32(&C.p_full[i]), kSoftWarps / 2);
+    }
+    mbar_init(smem_u32(&C.o_full), 1);
+    mbar_init(smem_u32(&C.o_free), kSoftWarps);
+    mbar_init(smem_u32(&C.ml_full), kSoftWarps);
+    C.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&C.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = C.tmem;
+
+  if (warp < kSoftWarps) {
+    // ---- softmax: warpgroup X has stream X, thread (warp % 4, lane) row 32 (warp % 4) + lane
+    const int X = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t t_s = lanes + X * 128, t_o = lanes + kOCol + X * 128;
+    const float sl = fabsf(p.scale) * 1.4426950408889634f;  // the sign went into Q
+    uint32_t s_phase = 0;
+    int piece = 0;
+    Walk walk(p);
+    for (; walk.next(p) && !*abort; ++piece) {
+      float m = -FLT_MAX, l = 0.f;
+      bool ok = true;
+      for (int j = X; j < walk.n; j += 2) {
+        const int key0 = (walk.t0 + j) * kPrefixKeys;
+        const uint32_t groups = groups_in_sight(p, key0);
+        const bool part = groups != 0xffu || key0 + kPrefixKeys > p.len;
+        ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.s_full[X]), s_phase, abort));
+        if (!ok) break;
+        s_phase ^= 1u;
+        tc_fence_after();
+        // key 32 c + i of the tile is in sight
+        auto seen = [&](int c, int i) {
+          return (groups >> (2 * c + (i >> 4)) & 1u) && key0 + 32 * c + i < p.len;
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(t_s + 32 * c, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!part || seen(c, i)) top = fmaxf(top, __uint_as_float(v[i]));
+        }
+        const bool raise = fmaf(top, sl, -m) > 0.f;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float to = raise ? fmaf(top, sl, 8.f) : m;
+          const float f = raise ? ex2(m - to) : 1.f;
+          m = to;
+          l *= f;
+          if (j >= 2) {
+#pragma unroll 1
+            for (int c = 0; c < DP / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(t_o + 32 * c, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+              tmem_st32(t_o + 32 * c, v);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(t_s + 32 * c, v);
+          float x[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            x[i] = ex2(fmaf(__uint_as_float(v[i]), sl, -m));
+            if (part && !seen(c, i)) x[i] = 0.f;
+            l += x[i];
+          }
+          // columns 32 c ..: 16 of the weights in bf16, 16 of what the rounding left
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t h = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+            v[i] = h;
+            v[16 + i] = pack_bf16x2(x[2 * i] - bf16_lo(h), x[2 * i + 1] - bf16_hi(h));
+          }
+          tmem_st32(t_s + 32 * c, v);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&C.p_full[X]));
+      }
+      if (!ok) break;
+      // ---- the piece's end: both streams' means joined, half of the channels each
+      C.ml[piece & 1][X][row] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&C.ml_full));
+      ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.ml_full), piece & 1, abort) &&
+                                       wait_for(smem_u32(&C.o_full), piece & 1, abort));
+      if (!ok) break;
+      tc_fence_after();
+      const float2 a = C.ml[piece & 1][0][row], b = C.ml[piece & 1][1][row];
+      const float mm = fmaxf(a.x, b.x);
+      const float wa = a.y * ex2(a.x - mm), wb = b.y * ex2(b.x - mm), sum = wa + wb;
+      // sums over their own weights first: means cannot overflow
+      const float fa = wa == 0.f ? 0.f : wa / sum, ia = wa == 0.f ? 0.f : 1.f / a.y;
+      const float fb = wb == 0.f ? 0.f : wb / sum, ib = wb == 0.f ? 0.f : 1.f / b.y;
+      const int rt = walk.seg % p.row_tiles, r = rt * kPrefixRows + row;
+      const size_t slot = (static_cast<size_t>(blockIdx.x) + walk.seg) * kPrefixRows + row;
+      float* out = p.mean + slot * D;
+#pragma unroll 1
+      for (int c = 0; c < DP / 64; ++c) {
+        const int col = (X * (DP / 64) + c) * 32;
+        uint32_t v[32], u[32];
+        tmem_ld32(lanes + kOCol + col, v);
+        tmem_ld32(lanes + kOCol + 128 + col, u);
+        if (r < p.rows) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            if (col + i >= D) break;
+            float o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // a stream without weight may have no sums at all
+              const float oa = wa == 0.f ? 0.f : __uint_as_float(v[i + k]) * ia * fa;
+              const float ob = wb == 0.f ? 0.f : __uint_as_float(u[i + k]) * ib * fb;
+              o[k] = oa + ob;
+            }
+            *reinterpret_cast<float4*>(out + col + i) = make_float4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      if (X == 0 && r < p.rows) p.ml[slot] = make_float2(mm, sum);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&C.o_free));
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdS = idesc_bf16(kPrefixRows, kPrefixKeys);
+      constexpr uint32_t kIdO = idesc_bf16(kPrefixRows, DP) | 1u << 16;  // B as it lies
+      int ks = 0, vs = 0, piece = 0;
+      uint32_t kp = 0, vp = 0, pp[2] = {0, 0};
+      bool ok = true;
+      Walk walk(p);
+      for (; ok && walk.next(p) && !*abort; ++piece) {
+        if (!wait_for(smem_u32(&C.q_full), piece & 1, abort)) break;
+        tc_fence_after();
+        for (int j = 0; j <= walk.n; ++j) {
+          if (j < walk.n) {
+            if (!(ok = wait_for(smem_u32(&C.kfull[ks]), kp, abort))) break;
+            tc_fence_after();
+            const uint32_t k0 = s_k + ks * kTileBytes;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+              const uint32_t off = k / 4 * kSub + k % 4 * 32;
+              umma_ss(tmem + (j & 1) * 128, sw128_desc(s_q + off), sw128_desc(k0 + off), kIdS,
+                      k != 0 ? 1u : 0u);
+            }
+            umma_commit(smem_u32(&C.kfree[ks]));
+            umma_commit(smem_u32(&C.s_full[j & 1]));
+            if (j == walk.n - 1) umma_commit(smem_u32(&C.q_free));
+            if (++ks == kStagesK) ks = 0, kp ^= 1u;
+          }
+          if (j == 0) continue;
+          const int X = (j - 1) & 1;
+          // the piece before has been read out of O
+          if (j == 1 && !(ok = wait_for(smem_u32(&C.o_free), (piece & 1) ^ 1u, abort))) break;
+          if (!(ok = wait_for(smem_u32(&C.vfull[vs]), vp, abort) &&
+                     wait_for(smem_u32(&C.p_full[X]), pp[X], abort)))
+            break;
+          pp[X] ^= 1u;
+          tc_fence_after();
+          const uint32_t v0 = s_v + vs * kTileBytes;
+#pragma unroll
+          for (int k = 0; k < kPrefixKeys / 16; ++k) {
+            const uint64_t b = sw128_desc_mn(v0 + k * 16 * 128);
+            const uint32_t a = tmem + X * 128 + k / 2 * 32 + k % 2 * 8;
+            umma_ts(tmem + kOCol + X * 128, a, b, kIdO, j > 2 || k > 0 ? 1u : 0u);
+            umma_ts(tmem + kOCol + X * 128, a + 16, b, kIdO, 1u);
+          }
+          umma_commit(smem_u32(&C.vfree[vs]));
+          if (++vs == kStagesV) vs = 0, vp ^= 1u;
+        }
+        if (ok) umma_commit(smem_u32(&C.o_full));
+      }
+    }
+  } else {
+    // ---- loaders
+    const int lt = threadIdx.x - kLoad0 * 32;
+    const int tiles_per_page = p.c.page_size / 16;
+    int ks = 0, vs = 0, piece = 0;
+    uint32_t kp = 0, vp = 0;
+    bool ok = true;
+    // lane g < 8: the pool's tile (16 rows) of keys 16 g .. of a tile
+    auto look_up = [&](int h, int key0) {
+      const int key = key0 + (lane & 7) * 16;
+      uint32_t at = kNone;
+      if (key < p.len) {
+        const int pi = key / p.c.page_size, page = __ldg(p.pages + pi);
+        if (page < 0 || page >= p.c.n_pages)
+          latch_error(p.status, kErrDevice);
+        else
+          at = (static_cast<uint32_t>(page) * p.c.n_heads + h) * tiles_per_page +
+               (key - pi * p.c.page_size) / 16;
+      }
+      return at;
+    };
+    Walk walk(p);
+    // arrivals that wait for their copies (bf16)
+    uint32_t owed[3];
+    int n_owed = 0;
+    for (; ok && walk.next(p) && !*abort; ++piece) {
+      const int h = walk.seg / p.row_tiles, r0 = (walk.seg - h * p.row_tiles) * kPrefixRows;
+      uint32_t tile_of = look_up(h, walk.t0 * kPrefixKeys);
+      if constexpr (FMT == DT_BF16) {
+        // nothing may stay owed over a wait
+        cp_async_wait<0>();
+        proxy_fence();
+        for (int i = 0; i < n_owed; ++i) mbar_arrive(owed[i]);
+        n_owed = 0;
+      }
+      ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.q_free), (piece & 1) ^ 1u, abort));
+      if (!ok) break;
+      const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+      for (int i = lt; i < kPrefixRows * (DP / 8); i += LT) {
+        const int r = i / (DP / 8), c = i - r * (DP / 8), at = r0 + r;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (at < p.rows && c * 8 < D) {
+          const int b = at / p.group, g = at - b * p.group;
+          v = ldg_keep(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride +
+                       static_cast<size_t>(h * p.group + g) * D + c * 8);
+          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+        }
+        sts128(s_q + place(r, c), v);
+      }
+      proxy_fence();
+      mbar_arrive(smem_u32(&C.q_full));
+
+      if constexpr (FMT == DT_BF16) {
+        constexpr int kC = DP / 8, kStep = LT / kC, kN = kPrefixRows / kStep;
+        const int c = lt % kC, r = lt / kC;
+        const bool in_row = c * 8 < D;
+        const uint32_t to = place(r, c);  // rows kStep apart keep their swizzle: 8 divides it
+        static_assert(kStep % 8 == 0, "rows of a thread share r % 8");
+        auto copy = [&](uint32_t dst, const char* pool, int key0, uint32_t free_bar,
+                        uint32_t parity, uint32_t full_bar) {
+          if (!__all_sync(0xffffffffu, mbar_try_wait(free_bar, parity))) {
+            cp_async_wait<0>();
+            proxy_fence();
+            for (int i = 0; i < n_owed; ++i) mbar_arrive(owed[i]);
+            n_owed = 0;
+            if (!__all_sync(0xffffffffu, wait_for(free_bar, parity, abort))) return false;
+          }
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const int rr = r + i * kStep;
+            const uint32_t at = __shfl_sync(0xffffffffu, tile_of, rr / 16);
+            const bool in = in_row && at != kNone && key0 + rr < p.len;
+            const char* src =
+                in ? pool + (static_cast<size_t>(at) * 16 + rr % 16) * p.c.row_bytes + c * 16 : pool;
+            cp_async16_n(dst + to + i * kStep * 128, src, in ? 16 : 0);
+          }
+          cp_async_commit();
+          owed[n_owed++] = full_bar;
+          if (n_owed == 3) {
+            cp_async_wait<2>();
+            proxy_fence();
+            mbar_arrive(owed[0]);
+            owed[0] = owed[1];
+            owed[1] = owed[2];
+            n_owed = 2;
+          }
+          return true;
+        };
+        for (int j = 0; j < walk.n && ok; ++j) {
+          const int key0 = (walk.t0 + j) * kPrefixKeys;
+          const uint32_t next = j + 1 < walk.n ? look_up(h, key0 + kPrefixKeys) : kNone;
+          ok = copy(s_k + ks * kTileBytes, p.c.k, key0, smem_u32(&C.kfree[ks]), kp ^ 1u,
+                    smem_u32(&C.kfull[ks]));
+          if (!ok) break;
+          if (++ks == kStagesK) ks = 0, kp ^= 1u;
+          ok = copy(s_v + vs * kTileBytes, p.c.v, key0, smem_u32(&C.vfree[vs]), vp ^ 1u,
+                    smem_u32(&C.vfull[vs]));
+          if (!ok) break;
+          if (++vs == kStagesV) vs = 0, vp ^= 1u;
+          tile_of = next;
+        }
+      } else {
+        // 16 bytes of codes: CH channels, CH / 8 chunks of shared memory
+        constexpr int CH = FMT == DT_MXFP8 ? 16 : 32, kU = DP / CH, kStep = LT / kU;
+        constexpr int kN = kPrefixRows / kStep;
+        const int u = lt % kU, r = lt / kU;
+        const bool in_row = u * CH < D;
+        struct Raw {
+          uint4 v[kN];
+          uint32_t s[kN];
+        };
+        auto fetch = [&](Raw& x, const char* pool, const uint8_t* scales, int key0) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const int rr = r + i * kStep;
+            const uint32_t at = __shfl_sync(0xffffffffu, tile_of, rr / 16);
+            x.v[i] = make_uint4(0, 0, 0, 0);
+            x.s[i] = 127;
+            if (in_row && at != kNone && key0 + rr < p.len) {
+              const size_t row = static_cast<size_t>(at) * 16 + rr % 16;
+              x.v[i] = ldg_stream(pool + row * p.c.row_bytes + u * 16);
+              x.s[i] = __ldg(scales + row * p.c.scale_stride + u * CH / kMxBlock);
+            }
+          }
+        };
+        auto put = [&](const Raw& x, uint32_t dst, uint32_t full_bar) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            uint32_t w[CH / 2];
+            decode16<FMT>(x.v[i], x.s[i], w);
+            const int rr = r + i * kStep;
+#pragma unroll
+            for (int e = 0; e < CH / 8; ++e) {
+              // the threads of a row start at different chunks: fewer bank conflicts
+              const int k = (e + (u * CH / 64)) % (CH / 8);
+              uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+              for (int z = 1; z < CH / 8; ++z)
+                if (k == z) v = make_uint4(w[4 * z], w[4 * z + 1], w[4 * z + 2], w[4 * z + 3]);
+              sts128(dst + place(rr, u * (CH / 8) + k), v);
+            }
+          }
+          proxy_fence();
+          mbar_arrive(full_bar);
+        };
+        Raw k, v;
+        fetch(k, p.c.k, p.c.k_scale, walk.t0 * kPrefixKeys);
+        for (int j = 0; j < walk.n; ++j) {
+          const int key0 = (walk.t0 + j) * kPrefixKeys;
+          const uint32_t next = j + 1 < walk.n ? look_up(h, key0 + kPrefixKeys) : kNone;
+          fetch(v, p.c.v, p.c.v_scale, key0);
+          ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.kfree[ks]), kp ^ 1u, abort));
+          if (!ok) break;
+          put(k, s_k + ks * kTileBytes, smem_u32(&C.kfull[ks]));
+          if (++ks == kStagesK) ks = 0, kp ^= 1u;
+          tile_of = next;
+          if (j + 1 < walk.n) fetch(k, p.c.k, p.c.k_scale, key0 + kPrefixKeys);
+          ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.vfree[vs]), vp ^ 1u, abort));
+          if (!ok) break;
+          put(v, s_v + vs * kTileBytes, smem_u32(&C.vfull[vs]));
+          if (++vs == kStagesV) vs = 0, vp ^= 1u;
+        }
+      }
+    }
+    if constexpr (FMT == DT_BF16) {
+      cp_async_wait<0>();
+      proxy_fence();
+      for (int i = 0; i < n_owed; ++i) mbar_arrive(owed[i]);
+    }
+  }
+
+  __syncthreads();
+  if (C.abort && threadIdx.x == 0) {
+    latch_error(p.status, kErrTimeout);
+    const uint64_t t0 = global_timer_ns();  // let products in flight end
+    while (global_timer_ns() - t0 < 1000000ull) {
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int FMT, int DP>
+cudaError_t launch(const PrefixArgs& p, int grid, cudaStream_t st) {
+  static bool ready[128] = {};  // the shared-memory limit is raised once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 128 || !ready[dev]) {
+    e = cudaFuncSetAttribute(k_prefix<FMT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem_bytes<DP>());
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128) ready[dev] = true;
+  }
+  k_prefix<FMT, DP><<<grid, threads<FMT>(), smem_bytes<DP>(), st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_heads(const PrefixArgs& p, int grid, cudaStream_t st) {
+  return p.c.head_dim <= 64 ? launch<FMT, 64>(p, grid, st) : launch<FMT, 128>(p, grid, st);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix(const PrefixArgs& p, int grid, cudaStream_t st) {
+  switch (p.c.dtype) {
+    case DT_BF16: return launch_heads<DT_BF16>(p, grid, st);
+    case DT_MXFP8: return launch_heads<DT_MXFP8>(p, grid, st);
+    default: return launch_heads<DT_MXFP4>(p, grid, st);
+  }
+}
+
+}  // namespace coli

@@ -1,52 +1,101 @@
 // Attention behind a shared prefix: the prefix once for the queries of all sequences, each
 // sequence's own tokens as ever, and a join.
 #include "paged.cuh"
+#include "prefix.h"
 
 namespace coli {
 namespace {
 
 using namespace paged;
 
+// The parts of a row: its sequence's own tokens, and those of the prefix. The prefix's lie
+// in one array of rows like the own ones (n_parts 1) or in the slots of k_prefix's pieces.
 struct JoinArgs {
-  const float* mean[2];   // prefix, own: [rows][head_dim] fp32
-  const float2* ml[2];    // (m, l): weights are 2^(x - m), their sum l
+  const float* own;      // [rows][D] means
+  const float2* own_ml;  // (m, l): weights are 2^(x - m), their sum l
+  const float* mean;     // of the prefix
+  const float2* ml;
+  int64_t tiles, per;    // of a segment and a block on k_prefix's line; 0: rows as above
+  int row_tiles;
+  int group;
   void* out;
   float* lse;
   size_t out_stride;
-  int rows, heads, D;     // rows = B * heads
+  int rows, heads, D;    // rows = B * heads
 };
 
 constexpr int kJoinWarps = 8;
 
+// A warp a row, its lanes along the channels. Every factor is a part's share of the weights, so
+// a mean stays one; parts are added in their order.
 template <class T>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const JoinArgs p) {
   const int row = blockIdx.x * kJoinWarps + threadIdx.x / 32, lane = lane_id();
   if (row >= p.rows) return;
-  float w[2], l = 0.f, top = -FLT_MAX;
-  float2 ml[2];
+  const int b = row / p.heads, hq = row - b * p.heads;
+  size_t first = row;  // part i: row first + i * step
+  int n = 1, step = 0;
+  if (p.per > 0) {
+    const int h = hq / p.group, r = b * p.group + hq - h * p.group;
+    const int64_t seg = static_cast<int64_t>(h) * p.row_tiles + r / kPrefixRows;
+    const int64_t c0 = seg * p.tiles / p.per, c1 = ((seg + 1) * p.tiles - 1) / p.per;
+    first = static_cast<size_t>(c0 + seg) * kPrefixRows + r % kPrefixRows;
+    n = static_cast<int>(c1 - c0) + 1;
+    step = kPrefixRows;
+  }
+  const float2 own = p.own_ml[row];
+  float top = own.x;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.ml[first + static_cast<size_t>(i) * step].x);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    ml[i] = p.ml[i][row];
-    top = fmaxf(top, ml[i].x);
+  for (int k = 1; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+  const float w0 = own.y * ex2(own.x - top);
+  float l = 0.f;
+  for (int i = lane; i < n; i += 32) {
+    const float2 v = p.ml[first + static_cast<size_t>(i) * step];
+    l += v.y * ex2(v.x - top);
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    w[i] = ml[i].y * ex2(ml[i].x - top);
-    l += w[i];
-  }
-  const int b = row / p.heads, h = row - b * p.heads;
-  T* out = static_cast<T*>(p.out) + b * p.out_stride + static_cast<size_t>(h) * p.D;
-  for (int d = lane * 4; d < p.D; d += 128) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (ml[i].y == 0.f) continue;
-      const float4 v =
-          *reinterpret_cast<const float4*>(p.mean[i] + static_cast<size_t>(row) * p.D + d);
-      const float f = w[i] / l;
+  for (int k = 1; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+  l += w0;
+  T* out = static_cast<T*>(p.out) + b * p.out_stride + static_cast<size_t>(hq) * p.D;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int d0 = 0; d0 < p.D; d0 += 128) {
+    const int d = d0 + lane * 4;
+    const bool in = d < p.D;
+    float4 o = zero;
+    auto add = [&](const float4& v, float w) {
+      const float f = w / l;
       o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y);
       o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+    };
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float w = 0.f;
+      if (i0 + lane < n) {
+        const float2 v = p.ml[first + static_cast<size_t>(i0 + lane) * step];
+        w = v.y * ex2(v.x - top);
+      }
+      constexpr int kDeep = 4;
+      const int i1 = min(n - i0, 32);
+      for (int i = 0; i < i1; i += kDeep) {
+        float4 v[kDeep];
+        float f[kDeep];
+#pragma unroll
+        for (int e = 0; e < kDeep; ++e) {
+          f[e] = __shfl_sync(0xffffffffu, w, min(i + e, 31));
+          if (i + e >= i1) f[e] = 0.f;
+          v[e] = in && f[e] != 0.f
+                     ? *reinterpret_cast<const float4*>(
+                           p.mean + (first + static_cast<size_t>(i0 + i + e) * step) * p.D + d)
+                     : zero;
+        }
+#pragma unroll
+        for (int e = 0; e < kDeep; ++e)
+          if (f[e] != 0.f) add(v[e], f[e]);
+      }
     }
+    if (w0 != 0.f && in)
+      add(*reinterpret_cast<const float4*>(p.own + static_cast<size_t>(row) * p.D + d), w0);
+    if (!in) continue;
     if constexpr (sizeof(T) == 4)
       *reinterpret_cast<float4*>(out + d) = o;
     else
@@ -58,9 +107,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const JoinArgs 
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 
-// Of one side's means and (m, l) pairs.
-size_t side_bytes(const KvView& c, int64_t rows) {
-  return align16(rows * c.head_dim * sizeof(float)) + align16(rows * sizeof(float2));
+// Of means and (m, l) pairs.
+size_t mean_bytes(const KvView& c, int64_t rows) { return align16(rows * c.head_dim * 4); }
+size_t part_bytes(const KvView& c, int64_t rows) { return mean_bytes(c, rows) + align16(rows * 8); }
+
+// Whether k_prefix takes the prefix: it serves 128 queries of a key head at the price of one
+// to 128, the decode kernel reads the prefix once for every 16.
+bool on_tensor_cores(const KvView& c, int rows_of_head) {
+  return c.dtype != DT_F32 && c.head_dim <= 128 && rows_of_head > 16;
+}
+
+// Rows of the prefix's partial results.
+int64_t prefix_rows(const KvView& c, int B, int n_q_heads) {
+  const int rows = B * (n_q_heads / c.n_heads);
+  if (!on_tensor_cores(c, rows)) return static_cast<int64_t>(B) * n_q_heads;
+  const int64_t segments =
+      static_cast<int64_t>(c.n_heads) * ((rows + kPrefixRows - 1) / kPrefixRows);
+  return (segments + sm_count()) * kPrefixRows;
 }
 
 }  // namespace
@@ -69,47 +132,68 @@ size_t shared_scratch_bytes(const KvView& c, int B, int n_q_heads) {
   const int64_t rows = static_cast<int64_t>(B) * n_q_heads;
   const size_t one = paged_scratch_bytes(c, 1, static_cast<int>(rows));
   const size_t own = paged_scratch_bytes(c, B, n_q_heads);
-  return 2 * side_bytes(c, rows) + align16(one > own ? one : own);
+  return part_bytes(c, rows) + part_bytes(c, prefix_rows(c, B, n_q_heads)) +
+         align16(one > own ? one : own);
 }
 
 cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
   const KvView& c = s.own.c;
-  const int rows = s.own.B * s.own.n_q_heads;
-  const size_t side = side_bytes(c, rows);
-  char* at = static_cast<char*>(s.scratch);
-  JoinArgs j{};
-  for (int i = 0; i < 2; ++i) {
-    j.mean[i] = reinterpret_cast<float*>(at + i * side);
-    j.ml[i] = reinterpret_cast<float2*>(at + i * side + align16(size_t(rows) * c.head_dim * 4));
-  }
+  const int B = s.own.B, heads = s.own.n_q_heads, rows = B * heads, group = heads / c.n_heads;
+  const int64_t parts = prefix_rows(c, B, heads);
+  char* own = static_cast<char*>(s.scratch);
+  char* prefix = own + part_bytes(c, rows);
+  float* own_mean = reinterpret_cast<float*>(own);
+  float2* own_ml = reinterpret_cast<float2*>(own + mean_bytes(c, rows));
+  float* mean = reinterpret_cast<float*>(prefix);
+  float2* ml = reinterpret_cast<float2*>(prefix + mean_bytes(c, parts));
   PagedArgs a = s.own;
-  a.scratch = reinterpret_cast<float*>(at + 2 * side);
+  a.scratch = reinterpret_cast<float*>(prefix + part_bytes(c, parts));
   if (s.prefix_len == 0) return launch_paged_attention(a, st);
-  a.out_stride = static_cast<size_t>(a.n_q_heads) * c.head_dim;
+
+  JoinArgs j{own_mean, own_ml, mean, ml, 0, 0, 0, group, a.out, a.lse, a.out_stride, rows, heads,
+             c.head_dim};
   a.raw = 1;
-  {
+  a.out_stride = static_cast<size_t>(heads) * c.head_dim;
+  cudaError_t e;
+  if (on_tensor_cores(c, B * group)) {
+    PrefixArgs p{};
+    p.c = c;
+    p.q = a.q;
+    p.q_stride = a.q_stride;
+    p.pages = s.prefix_pages;
+    p.len = s.prefix_len;
+    p.group = group;
+    p.rows = B * group;
+    p.row_tiles = (p.rows + kPrefixRows - 1) / kPrefixRows;
+    p.tiles = (p.len + kPrefixKeys - 1) / kPrefixKeys;
+    p.total = static_cast<int64_t>(c.n_heads) * p.row_tiles * p.tiles;
+    const int grid = p.total < sm_count() ? static_cast<int>(p.total) : sm_count();
+    p.per = (p.total + grid - 1) / grid;
+    p.scale = a.scale;
+    p.mean = mean;
+    p.ml = ml;
+    p.status = a.status;
+    j.tiles = p.tiles;
+    j.per = p.per;
+    j.row_tiles = p.row_tiles;
+    e = launch_prefix(p, grid, st);
+  } else {
     PagedArgs f = a;
-    f.out = const_cast<float*>(j.mean[0]);
-    f.lse = reinterpret_cast<float*>(const_cast<float2*>(j.ml[0]));
+    f.out = mean;
+    f.lse = reinterpret_cast<float*>(ml);
     f.block_table = s.prefix_pages;
     f.max_pages = (s.prefix_len + c.page_size - 1) / c.page_size;
     f.fixed_len = s.prefix_len;
-    f.fold = a.n_q_heads / c.n_heads;
+    f.fold = group;
     f.n_q_heads = rows;
     f.B = 1;
-    const cudaError_t e = launch_paged_attention(f, st);
-    if (e != cudaSuccess) return e;
+    e = launch_paged_attention(f, st);
   }
-  a.out = const_cast<float*>(j.mean[1]);
-  a.lse = reinterpret_cast<float*>(const_cast<float2*>(j.ml[1]));
-  const cudaError_t e = launch_paged_attention(a, st);
   if (e != cudaSuccess) return e;
-  j.out = s.own.out;
-  j.lse = s.own.lse;
-  j.out_stride = s.own.out_stride;
-  j.rows = rows;
-  j.heads = a.n_q_heads;
-  j.D = c.head_dim;
+  a.out = own_mean;
+  a.lse = reinterpret_cast<float*>(own_ml);
+  e = launch_paged_attention(a, st);
+  if (e != cudaSuccess) return e;
   const unsigned grid = (rows + kJoinWarps - 1) / kJoinWarps;
   if (c.dtype == DT_F32)
     k_shared_join<float><<<grid, kJoinWarps * 32, 0, st>>>(j);

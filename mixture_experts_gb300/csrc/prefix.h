@@ -1,0 +1,28 @@
+// The tensor-core kernel for many queries over one shared prefix, and its work line.
+#pragma once
+
+#include "attn.h"
+
+namespace coli {
+
+constexpr int kPrefixRows = 128, kPrefixKeys = 128;  // of a block's tile
+
+struct PrefixArgs {
+  KvView c;
+  const void* q;
+  size_t q_stride;
+  const int32_t* pages;
+  int len;             // tokens of the prefix
+  int group;           // query heads of a key head
+  int rows;            // B * group
+  int row_tiles;       // 128-row tiles of a key head: segment = head * row_tiles + tile
+  int tiles;           // 128-key tiles of a segment
+  int64_t total, per;  // tiles in all, of a block
+  float scale;
+  float* mean;         // [blocks + segments][128][head_dim]
+  float2* ml;          // [blocks + segments][128]
+  int* status;
+};
+cudaError_t launch_prefix(const PrefixArgs& p, int grid, cudaStream_t st);
+
+}  // namespace coli
