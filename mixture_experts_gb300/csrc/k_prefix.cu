@@ -14,9 +14,11 @@
 // (keys by channels, "transposed"). m is raised only where a score passes it (weights are
 // 2^-8 at a new maximum and rise to 1), so O is rarely rescaled.
 //
-// Loader warps bring K and V tiles to 128-byte swizzled shared memory: bf16 by cp.async, MX
-// codes widened to bf16 with their scale (exact within bf16's range, which is fp32's). Rows
-// past the prefix and of pages that are left out are zeros there and -inf in the scores.
+// Loader warps bring K and V tiles to 128-byte swizzled shared memory: bf16 by TMA, a box a
+// page or the part of it that the tile has (rows past the pool read as zeros, which stands for
+// pages that are left out; the 16 rows that the prefix ends in are copied by hand, zeros behind
+// it), MX codes widened to bf16 with their scale (exact within bf16's range, which is fp32's).
+// Scores of keys out of sight are set to -inf.
 //
 // Work split: the tiles of all (key head, 128 rows) segments lie on one line that is cut into
 // equal pieces, one a block; a piece's part of a segment gives a partial mean with (m, l), in
@@ -31,7 +33,6 @@
 namespace coli {
 namespace {
 
-using paged::cp_async16_n;
 using paged::ex2;
 
 constexpr int kSub = kPrefixRows * 128;  // bytes of 128 rows of 64 channels
@@ -42,12 +43,16 @@ constexpr uint32_t kNone = 0xffffffffu;
 
 template <int FMT>
 constexpr int load_warps() {
-  return FMT == DT_BF16 ? 4 : 8;
+  return FMT == DT_BF16 ? 2 : 8;
 }
 template <int FMT>
-constexpr int threads() {
-  return (kLoad0 + load_warps<FMT>()) * 32;
+constexpr int threads() {  // bf16: one more, so that 3 warps of each scheduler share its registers
+  return (kLoad0 + load_warps<FMT>() + (FMT == DT_BF16 ? 1 : 0)) * 32;
 }
+
+struct PrefixMaps {  // bf16 pools as rows: boxes of a page's rows (p.box), of 16 rows
+  CUtensorMap k, v, k16, v16;
+};
 
 struct Ctrl {
   uint64_t kfull[kStagesK], kfree[kStagesK], vfull[kStagesV], vfree[kStagesV];
@@ -73,11 +78,19 @@ COLI_DEV uint64_t sw128_desc_mn(uint32_t addr) {
   return d;
 }
 
-// Waits for a phase; gives up, and has the block do so, after kWaitTimeoutNs.
+// Waits for a phase; gives up, and has the block do so, after about kWaitTimeoutNs. By the SM's
+// clock: reading the global timer, as waits of milliseconds may, costs a microsecond.
 COLI_DEV bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t deadline = global_timer_ns() + kWaitTimeoutNs;
-  return wait_bar(bar, parity, deadline, abort);
+  const long long begin = clock64();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - begin > static_cast<long long>(2 * kWaitTimeoutNs)) {
+      *abort = 1;
+      return false;
+    }
+  }
 }
 
 COLI_DEV void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -91,6 +104,21 @@ COLI_DEV void sts128(uint32_t addr, const uint4& v) {
 // Place of 16-byte chunk c of row r in a tile of 64-channel sub-tiles, 128-byte swizzle.
 COLI_DEV uint32_t place(int r, int c) {
   return (c >> 3) * kSub + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// Two fp32 numbers in one register pair, and what the SM does with both at once.
+COLI_DEV uint64_t pair(uint32_t a, uint32_t b) { return static_cast<uint64_t>(b) << 32 | a; }
+COLI_DEV float low(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+COLI_DEV float high(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+COLI_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+COLI_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Bits i: keys 16 i .. of the tile are in sight (lanes 0-7 look their pages up).
@@ -124,7 +152,7 @@ struct Walk {
 };
 
 template <int FMT, int DP>
-__global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p) {
+__global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p, const __grid_constant__ PrefixMaps maps) {
   constexpr int kTileBytes = DP / 64 * kSub;
   constexpr int LT = load_warps<FMT>() * 32;
   extern __shared__ char smem_raw[];
@@ -137,12 +165,13 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
   const int D = p.c.head_dim;
 
   if (threadIdx.x == 0) {
+    constexpr int kFull = FMT == DT_BF16 ? 2 : LT;  // TMA: the bytes announced, the edge by hand
     for (int i = 0; i < kStagesK; ++i) {
-      mbar_init(smem_u32(&C.kfull[i]), LT);
+      mbar_init(smem_u32(&C.kfull[i]), kFull);
       mbar_init(smem_u32(&C.kfree[i]), 1);
     }
     for (int i = 0; i < kStagesV; ++i) {
-      mbar_init(smem_u32(&C.vfull[i]), LT);
+      mbar_init(smem_u32(&C.vfull[i]), kFull);
       mbar_init(smem_u32(&C.vfree[i]), 1);
     }
     mbar_init(smem_u32(&C.q_full), LT);
@@ -183,18 +212,26 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         if (!ok) break;
         s_phase ^= 1u;
         tc_fence_after();
-        // key 32 c + i of the tile is in sight
-        auto seen = [&](int c, int i) {
-          return (groups >> (2 * c + (i >> 4)) & 1u) && key0 + 32 * c + i < p.len;
-        };
+        if (part) {  // scores out of sight: -inf
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32(t_s + 32 * c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(groups >> (2 * c + (i >> 4)) & 1u) || key0 + 32 * c + i >= p.len)
+                v[i] = 0xff800000u;
+            tmem_st32(t_s + 32 * c, v);
+          }
+          tmem_st_wait();
+        }
         float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tmem_ld32(t_s + 32 * c, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!part || seen(c, i)) top = fmaxf(top, __uint_as_float(v[i]));
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
         }
         const bool raise = fmaf(top, sl, -m) > 0.f;
         if (__any_sync(0xffffffffu, raise)) {
@@ -213,26 +250,27 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
             }
           }
         }
+        const uint64_t sl2 = pair(__float_as_uint(sl), __float_as_uint(sl));
+        const uint64_t neg_m = pair(__float_as_uint(-m), __float_as_uint(-m));
+        uint64_t l2 = 0;  // of even and odd keys
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tmem_ld32(t_s + 32 * c, v);
-          float x[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            x[i] = ex2(fmaf(__uint_as_float(v[i]), sl, -m));
-            if (part && !seen(c, i)) x[i] = 0.f;
-            l += x[i];
-          }
           // columns 32 c ..: 16 of the weights in bf16, 16 of what the rounding left
+          uint32_t o[32];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const uint32_t h = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-            v[i] = h;
-            v[16 + i] = pack_bf16x2(x[2 * i] - bf16_lo(h), x[2 * i + 1] - bf16_hi(h));
+            const uint64_t y = fma_f32x2(pair(v[2 * i], v[2 * i + 1]), sl2, neg_m);
+            const float x0 = ex2(low(y)), x1 = ex2(high(y));
+            l2 = add_f32x2(l2, pair(__float_as_uint(x0), __float_as_uint(x1)));
+            const uint32_t h = pack_bf16x2(x0, x1);
+            o[i] = h;
+            o[16 + i] = pack_bf16x2(x0 - bf16_lo(h), x1 - bf16_hi(h));
           }
-          tmem_st32(t_s + 32 * c, v);
+          tmem_st32(t_s + 32 * c, o);
         }
+        l += low(l2) + high(l2);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -334,7 +372,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         if (ok) umma_commit(smem_u32(&C.o_full));
       }
     }
-  } else {
+  } else if (warp < kLoad0 + load_warps<FMT>()) {
     // ---- loaders
     const int lt = threadIdx.x - kLoad0 * 32;
     const int tiles_per_page = p.c.page_size / 16;
@@ -356,83 +394,81 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       return at;
     };
     Walk walk(p);
-    // arrivals that wait for their copies (bf16)
-    uint32_t owed[3];
-    int n_owed = 0;
     for (; ok && walk.next(p) && !*abort; ++piece) {
       const int h = walk.seg / p.row_tiles, r0 = (walk.seg - h * p.row_tiles) * kPrefixRows;
       uint32_t tile_of = look_up(h, walk.t0 * kPrefixKeys);
-      if constexpr (FMT == DT_BF16) {
-        // nothing may stay owed over a wait
-        cp_async_wait<0>();
-        proxy_fence();
-        for (int i = 0; i < n_owed; ++i) mbar_arrive(owed[i]);
-        n_owed = 0;
-      }
       ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.q_free), (piece & 1) ^ 1u, abort));
       if (!ok) break;
       const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
-      for (int i = lt; i < kPrefixRows * (DP / 8); i += LT) {
-        const int r = i / (DP / 8), c = i - r * (DP / 8), at = r0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (at < p.rows && c * 8 < D) {
-          const int b = at / p.group, g = at - b * p.group;
-          v = ldg_keep(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride +
-                       static_cast<size_t>(h * p.group + g) * D + c * 8);
-          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+      constexpr int kQ = kPrefixRows * (DP / 8) / LT;
+      constexpr int kQBatch = kQ < 8 ? kQ : 8;  // loads in flight
+#pragma unroll 1
+      for (int i0 = 0; i0 < kQ; i0 += kQBatch) {
+        uint4 v[kQBatch];
+#pragma unroll
+        for (int e = 0; e < kQBatch; ++e) {
+          const int i = lt + (i0 + e) * LT, r = i / (DP / 8), c = i - r * (DP / 8), at = r0 + r;
+          v[e] = make_uint4(0, 0, 0, 0);
+          if (at < p.rows && c * 8 < D) {
+            const int b = at / p.group, g = at - b * p.group;
+            v[e] = ldg_keep(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride +
+                            static_cast<size_t>(h * p.group + g) * D + c * 8);
+            v[e].x ^= flip, v[e].y ^= flip, v[e].z ^= flip, v[e].w ^= flip;
+          }
         }
-        sts128(s_q + place(r, c), v);
+#pragma unroll
+        for (int e = 0; e < kQBatch; ++e) {
+          const int i = lt + (i0 + e) * LT, r = i / (DP / 8), c = i - r * (DP / 8);
+          sts128(s_q + place(r, c), v[e]);
+        }
       }
       proxy_fence();
       mbar_arrive(smem_u32(&C.q_full));
 
       if constexpr (FMT == DT_BF16) {
-        constexpr int kC = DP / 8, kStep = LT / kC, kN = kPrefixRows / kStep;
-        const int c = lt % kC, r = lt / kC;
-        const bool in_row = c * 8 < D;
-        const uint32_t to = place(r, c);  // rows kStep apart keep their swizzle: 8 divides it
-        static_assert(kStep % 8 == 0, "rows of a thread share r % 8");
-        auto copy = [&](uint32_t dst, const char* pool, int key0, uint32_t free_bar,
-                        uint32_t parity, uint32_t full_bar) {
-          if (!__all_sync(0xffffffffu, mbar_try_wait(free_bar, parity))) {
-            cp_async_wait<0>();
-            proxy_fence();
-            for (int i = 0; i < n_owed; ++i) mbar_arrive(owed[i]);
-            n_owed = 0;
-            if (!__all_sync(0xffffffffu, wait_for(free_bar, parity, abort))) return false;
-          }
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const int rr = r + i * kStep;
-            const uint32_t at = __shfl_sync(0xffffffffu, tile_of, rr / 16);
-            const bool in = in_row && at != kNone && key0 + rr < p.len;
-            const char* src =
-                in ? pool + (static_cast<size_t>(at) * 16 + rr % 16) * p.c.row_bytes + c * 16 : pool;
-            cp_async16_n(dst + to + i * kStep * 128, src, in ? 16 : 0);
-          }
-          cp_async_commit();
-          owed[n_owed++] = full_bar;
-          if (n_owed == 3) {
-            cp_async_wait<2>();
-            proxy_fence();
-            mbar_arrive(owed[0]);
-            owed[0] = owed[1];
-            owed[1] = owed[2];
-            n_owed = 2;
-          }
-          return true;
-        };
-        for (int j = 0; j < walk.n && ok; ++j) {
+        // warp 0 of the loaders brings the keys, warp 1 the values, lane i the i-th box of rows
+        const bool keys = warp == kLoad0;
+        const char* pool = keys ? p.c.k : p.c.v;
+        int& stage = keys ? ks : vs;
+        uint32_t& phase = keys ? kp : vp;
+        for (int j = 0; j < walk.n; ++j) {
           const int key0 = (walk.t0 + j) * kPrefixKeys;
           const uint32_t next = j + 1 < walk.n ? look_up(h, key0 + kPrefixKeys) : kNone;
-          ok = copy(s_k + ks * kTileBytes, p.c.k, key0, smem_u32(&C.kfree[ks]), kp ^ 1u,
-                    smem_u32(&C.kfull[ks]));
+          const uint32_t full = smem_u32(keys ? &C.kfull[stage] : &C.vfull[stage]);
+          const uint32_t dst = (keys ? s_k : s_v) + stage * kTileBytes;
+          ok = __all_sync(0xffffffffu, wait_for(smem_u32(keys ? &C.kfree[stage] : &C.vfree[stage]),
+                                                phase ^ 1u, abort));
           if (!ok) break;
-          if (++ks == kStagesK) ks = 0, kp ^= 1u;
-          ok = copy(s_v + vs * kTileBytes, p.c.v, key0, smem_u32(&C.vfree[vs]), vp ^ 1u,
-                    smem_u32(&C.vfull[vs]));
-          if (!ok) break;
-          if (++vs == kStagesV) vs = 0, vp ^= 1u;
+          // a tile that the prefix ends in: boxes of 16 rows, the one it ends in by hand
+          const bool part = key0 + kPrefixKeys > p.len;
+          const int box = part ? 16 : p.box, edge = part ? (p.len - key0) / 16 : kPrefixKeys;
+          const bool by_hand = part && p.len % 16 != 0;
+          if (lane == 0)
+            mbar_arrive_expect_tx(full, kTileBytes - (by_hand ? DP / 64 * 16 * 128 : 0));
+          __syncwarp();
+          const CUtensorMap* map = part ? (keys ? &maps.k16 : &maps.v16) : (keys ? &maps.k : &maps.v);
+          const uint32_t at = __shfl_sync(0xffffffffu, tile_of, lane * box / 16 & 7);
+          if (lane < kPrefixKeys / box && !(by_hand && lane == edge)) {
+            const int row = at == kNone ? p.pool_rows : static_cast<int>(at) * 16;  // past it: zeros
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c)
+              tma_load_2d(dst + c * kSub + lane * box * 128, map, full, c * 64, row);
+          }
+          if (by_hand) {
+            const uint32_t last = __shfl_sync(0xffffffffu, tile_of, edge);
+#pragma unroll 4
+            for (int i = lane; i < 16 * (DP / 8); i += 32) {
+              const int r = i / (DP / 8), c = i - r * (DP / 8);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (last != kNone && c * 8 < D && r < p.len % 16)
+                v = ldg_keep(pool + (static_cast<size_t>(last) * 16 + r) * p.c.row_bytes + c * 16);
+              sts128(dst + place(edge * 16 + r, c), v);
+            }
+            proxy_fence();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(full);
+          if (++stage == (keys ? kStagesK : kStagesV)) stage = 0, phase ^= 1u;
           tile_of = next;
         }
       } else {
@@ -498,11 +534,6 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         }
       }
     }
-    if constexpr (FMT == DT_BF16) {
-      cp_async_wait<0>();
-      proxy_fence();
-      for (int i = 0; i < n_owed; ++i) mbar_arrive(owed[i]);
-    }
   }
 
   __syncthreads();
@@ -531,7 +562,20 @@ cudaError_t launch(const PrefixArgs& p, int grid, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) ready[dev] = true;
   }
-  k_prefix<FMT, DP><<<grid, threads<FMT>(), smem_bytes<DP>(), st>>>(p);
+  PrefixMaps maps{};
+  if (FMT == DT_BF16) {
+    auto encode = [&](CUtensorMap* m, const void* pool, int rows) {
+      if (e == cudaSuccess)
+        e = encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, p.pool_rows,
+                           p.c.head_dim, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    encode(&maps.k, p.c.k, p.box);
+    encode(&maps.v, p.c.v, p.box);
+    encode(&maps.k16, p.c.k, 16);
+    encode(&maps.v16, p.c.v, 16);
+    if (e != cudaSuccess) return e;
+  }
+  k_prefix<FMT, DP><<<grid, threads<FMT>(), smem_bytes<DP>(), st>>>(p, maps);
   return cudaGetLastError();
 }
 

@@ -112,9 +112,11 @@ size_t mean_bytes(const KvView& c, int64_t rows) { return align16(rows * c.head_
 size_t part_bytes(const KvView& c, int64_t rows) { return mean_bytes(c, rows) + align16(rows * 8); }
 
 // Whether k_prefix takes the prefix: it serves 128 queries of a key head at the price of one
-// to 128, the decode kernel reads the prefix once for every 16.
+// to 128, the decode kernel reads the prefix once for every 16. (It numbers the pool's rows in
+// 31 bits.)
 bool on_tensor_cores(const KvView& c, int rows_of_head) {
-  return c.dtype != DT_F32 && c.head_dim <= 128 && rows_of_head > 16;
+  return c.dtype != DT_F32 && c.head_dim <= 128 && rows_of_head > 16 &&
+         static_cast<int64_t>(c.n_pages) * c.n_heads * c.page_size < INT32_MAX;
 }
 
 // Rows of the prefix's partial results.
@@ -169,6 +171,9 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
     p.total = static_cast<int64_t>(c.n_heads) * p.row_tiles * p.tiles;
     const int grid = p.total < sm_count() ? static_cast<int>(p.total) : sm_count();
     p.per = (p.total + grid - 1) / grid;
+    p.box = c.page_size & -c.page_size;
+    p.box = p.box > kPrefixKeys ? kPrefixKeys : p.box;
+    p.pool_rows = c.n_pages * c.n_heads * c.page_size;
     p.scale = a.scale;
     p.mean = mean;
     p.ml = ml;

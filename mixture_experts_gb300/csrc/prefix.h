@@ -18,6 +18,8 @@ struct PrefixArgs {
   int row_tiles;       // 128-row tiles of a key head: segment = head * row_tiles + tile
   int tiles;           // 128-key tiles of a segment
   int64_t total, per;  // tiles in all, of a block
+  int box;             // rows of a TMA box: the power of two that divides page_size, to 128
+  int pool_rows;       // n_pages * n_kv_heads * page_size
   float scale;
   float* mean;         // [blocks + segments][128][head_dim]
   float2* ml;          // [blocks + segments][128]
