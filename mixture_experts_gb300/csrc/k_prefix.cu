@@ -43,11 +43,11 @@ constexpr uint32_t kNone = 0xffffffffu;
 
 template <int FMT>
 constexpr int load_warps() {
-  return FMT == DT_BF16 ? 2 : 8;
+  return FMT == DT_BF16 ? 2 : 7;
 }
 template <int FMT>
-constexpr int threads() {  // bf16: one more, so that 3 warps of each scheduler share its registers
-  return (kLoad0 + load_warps<FMT>() + (FMT == DT_BF16 ? 1 : 0)) * 32;
+constexpr int threads() {  // a multiple of four warps: what a scheduler's share of registers goes by
+  return FMT == DT_BF16 ? 12 * 32 : 16 * 32;
 }
 
 struct PrefixMaps {  // bf16 pools as rows: boxes of a page's rows (p.box), of 16 rows
@@ -91,6 +91,31 @@ COLI_DEV bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort) {
       return false;
     }
   }
+}
+
+// The products, issued by one lane of a converged warp: with the operands in uniform registers an
+// instruction takes less to issue than to run (a single lane's code needs 110 cycles an
+// instruction to move them there, the product of 128 x 128 x 16 takes 64).
+COLI_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+COLI_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+COLI_DEV void mma_commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+COLI_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
 }
 
 COLI_DEV void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -174,7 +199,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       mbar_init(smem_u32(&C.vfull[i]), kFull);
       mbar_init(smem_u32(&C.vfree[i]), 1);
     }
-    mbar_init(smem_u32(&C.q_full), LT);
+    mbar_init(smem_u32(&C.q_full), kSoftWarps * 32);
     mbar_init(smem_u32(&C.q_free), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&C.s_full[i]), 1);
@@ -198,9 +223,35 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + X * 128, t_o = lanes + kOCol + X * 128;
     const float sl = fabsf(p.scale) * 1.4426950408889634f;  // the sign went into Q
+    // the piece's queries: 128 rows by all softmax warps, their sign that of the scale
+    auto load_queries = [&](const Walk& w) {
+      const int h = w.seg / p.row_tiles, r0 = (w.seg - h * p.row_tiles) * kPrefixRows;
+      const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+      constexpr int kQ = kPrefixRows * (DP / 8) / (kSoftWarps * 32);
+      uint4 v[kQ];
+#pragma unroll
+      for (int e = 0; e < kQ; ++e) {
+        const int i = threadIdx.x + e * kSoftWarps * 32, r = i / (DP / 8), c = i - r * (DP / 8);
+        v[e] = make_uint4(0, 0, 0, 0);
+        if (r0 + r < p.rows && c * 8 < D) {
+          const int b = (r0 + r) / p.group, g = r0 + r - b * p.group;
+          v[e] = ldg_keep(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride +
+                          static_cast<size_t>(h * p.group + g) * D + c * 8);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kQ; ++e) {
+        const int i = threadIdx.x + e * kSoftWarps * 32, r = i / (DP / 8), c = i - r * (DP / 8);
+        v[e].x ^= flip, v[e].y ^= flip, v[e].z ^= flip, v[e].w ^= flip;
+        sts128(s_q + place(r, c), v[e]);
+      }
+      proxy_fence();
+      mbar_arrive(smem_u32(&C.q_full));
+    };
     uint32_t s_phase = 0;
     int piece = 0;
-    Walk walk(p);
+    Walk walk(p), ahead(p);
+    if (ahead.next(p)) load_queries(ahead);
     for (; walk.next(p) && !*abort; ++piece) {
       float m = -FLT_MAX, l = 0.f;
       bool ok = true;
@@ -277,7 +328,12 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         if (lane == 0) mbar_arrive(smem_u32(&C.p_full[X]));
       }
       if (!ok) break;
-      // ---- the piece's end: both streams' means joined, half of the channels each
+      // ---- the piece's end: the next one's queries once the last scores are formed, then both
+      // streams' means joined, half of the channels each
+      if (ahead.next(p)) {
+        if (!__all_sync(0xffffffffu, wait_for(smem_u32(&C.q_free), piece & 1, abort))) break;
+        load_queries(ahead);
+      }
       C.ml[piece & 1][X][row] = make_float2(m, l);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&C.ml_full));
@@ -322,55 +378,52 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       if (lane == 0) mbar_arrive(smem_u32(&C.o_free));
     }
   } else if (warp == kMmaWarp) {
-    // ---- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kIdS = idesc_bf16(kPrefixRows, kPrefixKeys);
-      constexpr uint32_t kIdO = idesc_bf16(kPrefixRows, DP) | 1u << 16;  // B as it lies
-      int ks = 0, vs = 0, piece = 0;
-      uint32_t kp = 0, vp = 0, pp[2] = {0, 0};
-      bool ok = true;
-      Walk walk(p);
-      for (; ok && walk.next(p) && !*abort; ++piece) {
-        if (!wait_for(smem_u32(&C.q_full), piece & 1, abort)) break;
-        tc_fence_after();
-        for (int j = 0; j <= walk.n; ++j) {
-          if (j < walk.n) {
-            if (!(ok = wait_for(smem_u32(&C.kfull[ks]), kp, abort))) break;
-            tc_fence_after();
-            const uint32_t k0 = s_k + ks * kTileBytes;
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-              const uint32_t off = k / 4 * kSub + k % 4 * 32;
-              umma_ss(tmem + (j & 1) * 128, sw128_desc(s_q + off), sw128_desc(k0 + off), kIdS,
-                      k != 0 ? 1u : 0u);
-            }
-            umma_commit(smem_u32(&C.kfree[ks]));
-            umma_commit(smem_u32(&C.s_full[j & 1]));
-            if (j == walk.n - 1) umma_commit(smem_u32(&C.q_free));
-            if (++ks == kStagesK) ks = 0, kp ^= 1u;
-          }
-          if (j == 0) continue;
-          const int X = (j - 1) & 1;
-          // the piece before has been read out of O
-          if (j == 1 && !(ok = wait_for(smem_u32(&C.o_free), (piece & 1) ^ 1u, abort))) break;
-          if (!(ok = wait_for(smem_u32(&C.vfull[vs]), vp, abort) &&
-                     wait_for(smem_u32(&C.p_full[X]), pp[X], abort)))
-            break;
-          pp[X] ^= 1u;
+    // ---- products
+    constexpr uint32_t kIdS = idesc_bf16(kPrefixRows, kPrefixKeys);
+    constexpr uint32_t kIdO = idesc_bf16(kPrefixRows, DP) | 1u << 16;  // B as it lies
+    int ks = 0, vs = 0, piece = 0;
+    uint32_t kp = 0, vp = 0, p_phase = 0;  // bit X: of stream X
+    bool ok = true;
+    Walk walk(p);
+    for (; ok && walk.next(p); ++piece) {
+      if (!warp_wait(smem_u32(&C.q_full), piece & 1, abort)) break;
+      tc_fence_after();
+      for (int j = 0; j <= walk.n; ++j) {
+        if (j < walk.n) {
+          if (!(ok = warp_wait(smem_u32(&C.kfull[ks]), kp, abort))) break;
           tc_fence_after();
-          const uint32_t v0 = s_v + vs * kTileBytes;
+          const uint32_t k0 = s_k + ks * kTileBytes;
 #pragma unroll
-          for (int k = 0; k < kPrefixKeys / 16; ++k) {
-            const uint64_t b = sw128_desc_mn(v0 + k * 16 * 128);
-            const uint32_t a = tmem + X * 128 + k / 2 * 32 + k % 2 * 8;
-            umma_ts(tmem + kOCol + X * 128, a, b, kIdO, j > 2 || k > 0 ? 1u : 0u);
-            umma_ts(tmem + kOCol + X * 128, a + 16, b, kIdO, 1u);
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint32_t off = k / 4 * kSub + k % 4 * 32;
+            mma_ss(tmem + (j & 1) * 128, sw128_desc(s_q + off), sw128_desc(k0 + off), kIdS,
+                   k != 0 ? 1u : 0u);
           }
-          umma_commit(smem_u32(&C.vfree[vs]));
-          if (++vs == kStagesV) vs = 0, vp ^= 1u;
+          mma_commit(smem_u32(&C.kfree[ks]));
+          mma_commit(smem_u32(&C.s_full[j & 1]));
+          if (j == walk.n - 1) mma_commit(smem_u32(&C.q_free));
+          if (++ks == kStagesK) ks = 0, kp ^= 1u;
         }
-        if (ok) umma_commit(smem_u32(&C.o_full));
+        if (j == 0) continue;
+        const int X = (j - 1) & 1;
+        // the piece before has been read out of O
+        if (j == 1 && !(ok = warp_wait(smem_u32(&C.o_free), (piece & 1) ^ 1u, abort))) break;
+        if (!(ok = warp_wait(smem_u32(&C.vfull[vs]), vp, abort))) break;
+        if (!(ok = warp_wait(smem_u32(&C.p_full[X]), p_phase >> X & 1u, abort))) break;
+        p_phase ^= 1u << X;
+        tc_fence_after();
+        const uint32_t v0 = s_v + vs * kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kPrefixKeys / 16; ++k) {
+          const uint64_t b = sw128_desc_mn(v0 + k * 16 * 128);
+          const uint32_t a = tmem + X * 128 + k / 2 * 32 + k % 2 * 8;
+          mma_ts(tmem + kOCol + X * 128, a, b, kIdO, j > 2 || k > 0 ? 1u : 0u);
+          mma_ts(tmem + kOCol + X * 128, a + 16, b, kIdO, 1u);
+        }
+        mma_commit(smem_u32(&C.vfree[vs]));
+        if (++vs == kStagesV) vs = 0, vp ^= 1u;
       }
+      if (ok) mma_commit(smem_u32(&C.o_full));
     }
   } else if (warp < kLoad0 + load_warps<FMT>()) {
     // ---- loaders
@@ -393,38 +446,19 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       }
       return at;
     };
+    // Tiles kAhead further on are brought to the L2: memory's latency is more than the stages in
+    // shared memory cover. Lanes from line0 on, `lines` apart, take the 128-byte lines of 16 rows.
+    constexpr int kAhead = 5;
+    auto prefetch = [&](const char* pool, uint32_t at, int line0, int lines) {
+      if (at == kNone) return;
+      const char* rows = pool + static_cast<size_t>(at) * 16 * p.c.row_bytes;
+      for (int i = line0; i * 128 < 16 * p.c.row_bytes; i += lines)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(rows + i * 128));
+    };
     Walk walk(p);
     for (; ok && walk.next(p) && !*abort; ++piece) {
-      const int h = walk.seg / p.row_tiles, r0 = (walk.seg - h * p.row_tiles) * kPrefixRows;
+      const int h = walk.seg / p.row_tiles;
       uint32_t tile_of = look_up(h, walk.t0 * kPrefixKeys);
-      ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.q_free), (piece & 1) ^ 1u, abort));
-      if (!ok) break;
-      const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
-      constexpr int kQ = kPrefixRows * (DP / 8) / LT;
-      constexpr int kQBatch = kQ < 8 ? kQ : 8;  // loads in flight
-#pragma unroll 1
-      for (int i0 = 0; i0 < kQ; i0 += kQBatch) {
-        uint4 v[kQBatch];
-#pragma unroll
-        for (int e = 0; e < kQBatch; ++e) {
-          const int i = lt + (i0 + e) * LT, r = i / (DP / 8), c = i - r * (DP / 8), at = r0 + r;
-          v[e] = make_uint4(0, 0, 0, 0);
-          if (at < p.rows && c * 8 < D) {
-            const int b = at / p.group, g = at - b * p.group;
-            v[e] = ldg_keep(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride +
-                            static_cast<size_t>(h * p.group + g) * D + c * 8);
-            v[e].x ^= flip, v[e].y ^= flip, v[e].z ^= flip, v[e].w ^= flip;
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < kQBatch; ++e) {
-          const int i = lt + (i0 + e) * LT, r = i / (DP / 8), c = i - r * (DP / 8);
-          sts128(s_q + place(r, c), v[e]);
-        }
-      }
-      proxy_fence();
-      mbar_arrive(smem_u32(&C.q_full));
-
       if constexpr (FMT == DT_BF16) {
         // warp 0 of the loaders brings the keys, warp 1 the values, lane i the i-th box of rows
         const bool keys = warp == kLoad0;
@@ -434,6 +468,8 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         for (int j = 0; j < walk.n; ++j) {
           const int key0 = (walk.t0 + j) * kPrefixKeys;
           const uint32_t next = j + 1 < walk.n ? look_up(h, key0 + kPrefixKeys) : kNone;
+          const uint32_t far =
+              j + kAhead < walk.n ? look_up(h, key0 + kAhead * kPrefixKeys) : kNone;
           const uint32_t full = smem_u32(keys ? &C.kfull[stage] : &C.vfull[stage]);
           const uint32_t dst = (keys ? s_k : s_v) + stage * kTileBytes;
           ok = __all_sync(0xffffffffu, wait_for(smem_u32(keys ? &C.kfree[stage] : &C.vfree[stage]),
@@ -468,15 +504,15 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
             __syncwarp();
           }
           if (lane == 0) mbar_arrive(full);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) prefetch(pool, __shfl_sync(0xffffffffu, far, i), lane, 32);
           if (++stage == (keys ? kStagesK : kStagesV)) stage = 0, phase ^= 1u;
           tile_of = next;
         }
       } else {
         // 16 bytes of codes: CH channels, CH / 8 chunks of shared memory
-        constexpr int CH = FMT == DT_MXFP8 ? 16 : 32, kU = DP / CH, kStep = LT / kU;
-        constexpr int kN = kPrefixRows / kStep;
-        const int u = lt % kU, r = lt / kU;
-        const bool in_row = u * CH < D;
+        constexpr int CH = FMT == DT_MXFP8 ? 16 : 32, kU = DP / CH;
+        constexpr int kUnits = kPrefixKeys * kU, kN = (kUnits + LT - 1) / LT;
         struct Raw {
           uint4 v[kN];
           uint32_t s[kN];
@@ -484,11 +520,11 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         auto fetch = [&](Raw& x, const char* pool, const uint8_t* scales, int key0) {
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
-            const int rr = r + i * kStep;
-            const uint32_t at = __shfl_sync(0xffffffffu, tile_of, rr / 16);
+            const int n = lt + i * LT, rr = n / kU, u = n % kU;
+            const uint32_t at = __shfl_sync(0xffffffffu, tile_of, rr / 16 & 7);
             x.v[i] = make_uint4(0, 0, 0, 0);
             x.s[i] = 127;
-            if (in_row && at != kNone && key0 + rr < p.len) {
+            if (n < kUnits && u * CH < D && at != kNone && key0 + rr < p.len) {
               const size_t row = static_cast<size_t>(at) * 16 + rr % 16;
               x.v[i] = ldg_stream(pool + row * p.c.row_bytes + u * 16);
               x.s[i] = __ldg(scales + row * p.c.scale_stride + u * CH / kMxBlock);
@@ -499,8 +535,9 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
             uint32_t w[CH / 2];
+            const int n = lt + i * LT, rr = n / kU, u = n % kU;
+            if (n >= kUnits) break;
             decode16<FMT>(x.v[i], x.s[i], w);
-            const int rr = r + i * kStep;
 #pragma unroll
             for (int e = 0; e < CH / 8; ++e) {
               // the threads of a row start at different chunks: fewer bank conflicts
@@ -520,6 +557,10 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         for (int j = 0; j < walk.n; ++j) {
           const int key0 = (walk.t0 + j) * kPrefixKeys;
           const uint32_t next = j + 1 < walk.n ? look_up(h, key0 + kPrefixKeys) : kNone;
+          const uint32_t far =
+              j + kAhead < walk.n ? look_up(h, key0 + kAhead * kPrefixKeys) : kNone;
+          for (int i = warp - kLoad0; i < 8; i += load_warps<FMT>())
+            prefetch(lane < 16 ? p.c.k : p.c.v, __shfl_sync(0xffffffffu, far, i), lane & 15, 16);
           fetch(v, p.c.v, p.c.v_scale, key0);
           ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.kfree[ks]), kp ^ 1u, abort));
           if (!ok) break;
