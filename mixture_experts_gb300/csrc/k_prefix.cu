@@ -17,8 +17,8 @@
 // Loader warps bring K and V tiles to 128-byte swizzled shared memory: bf16 by TMA, a box a
 // page or the part of it that the tile has (rows past the pool read as zeros, which stands for
 // pages that are left out; the 16 rows that the prefix ends in are copied by hand, zeros behind
-// it), MX codes widened to bf16 with their scale (exact within bf16's range, which is fp32's).
-// Scores of keys out of sight are set to -inf.
+// it); MX codes by TMA as they are, then widened to bf16 with their scale by eight warps (exact
+// within bf16's range, which is fp32's). Scores of keys out of sight are set to -inf.
 //
 // Work split: the tiles of all (key head, 128 rows) segments lie on one line that is cut into
 // equal pieces, one a block; a piece's part of a segment gives a partial mean with (m, l), in
@@ -37,34 +37,43 @@ using paged::ex2;
 
 constexpr int kSub = kPrefixRows * 128;  // bytes of 128 rows of 64 channels
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoad0 = 9;
-constexpr int kStagesK = 3, kStagesV = 2;
+constexpr int kConv0 = 12, kConvWarps = 8;  // MX: the warps that widen
 constexpr uint32_t kOCol = 256;          // O of the streams; S at 0 and 128
 constexpr uint32_t kNone = 0xffffffffu;
 
+constexpr int kStagesV = 2, kMostK = 3, kRaw = 3;
+
 template <int FMT>
-constexpr int load_warps() {
-  return FMT == DT_BF16 ? 2 : 7;
+constexpr int stages_k() {
+  return FMT == DT_BF16 ? 3 : 2;
 }
 template <int FMT>
 constexpr int threads() {  // a multiple of four warps: what a scheduler's share of registers goes by
-  return FMT == DT_BF16 ? 12 * 32 : 16 * 32;
+  return (FMT == DT_BF16 ? kConv0 : kConv0 + kConvWarps) * 32;
+}
+// MX: a tile as it is stored, 128 rows of codes and of scale words
+template <int FMT, int DP>
+constexpr int raw_bytes() {
+  return FMT == DT_BF16 ? 0 : kPrefixKeys * (DP * (FMT == DT_MXFP8 ? 8 : 4) / 8 + 4);
 }
 
-struct PrefixMaps {  // bf16 pools as rows: boxes of a page's rows (p.box), of 16 rows
+struct PrefixMaps {  // the pools as rows: boxes of a page's rows (p.box); bf16: also of 16 rows
   CUtensorMap k, v, k16, v16;
 };
 
 struct Ctrl {
-  uint64_t kfull[kStagesK], kfree[kStagesK], vfull[kStagesV], vfree[kStagesV];
+  uint64_t kfull[kMostK], kfree[kMostK], vfull[kStagesV], vfree[kStagesV];
+  uint64_t raw_full[kRaw], raw_free[kRaw];
   uint64_t q_full, q_free, s_full[2], p_full[2], o_full, o_free, ml_full;
   uint32_t tmem;
   int abort;
   float2 ml[2][2][kPrefixRows];  // by piece's parity, stream
 };
 
-template <int DP>
+template <int FMT, int DP>
 constexpr int smem_bytes() {
-  return 1024 + DP / 64 * kSub * (1 + kStagesK + kStagesV) + static_cast<int>(sizeof(Ctrl));
+  return 1024 + DP / 64 * kSub * (1 + stages_k<FMT>() + kStagesV) + kRaw * raw_bytes<FMT, DP>() +
+         static_cast<int>(sizeof(Ctrl));
 }
 
 // B operand as it lies: 16-bit elements, reduction rows of 128 bytes (64 columns), 8 rows 1024
@@ -179,18 +188,24 @@ struct Walk {
 template <int FMT, int DP>
 __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p, const __grid_constant__ PrefixMaps maps) {
   constexpr int kTileBytes = DP / 64 * kSub;
-  constexpr int LT = load_warps<FMT>() * 32;
+  constexpr int kStagesK = stages_k<FMT>();
   extern __shared__ char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t s_q = base, s_k = base + kTileBytes, s_v = s_k + kStagesK * kTileBytes;
-  Ctrl& C = *reinterpret_cast<Ctrl*>(smem_raw + (base - smem_u32(smem_raw)) +
-                                     kTileBytes * (1 + kStagesK + kStagesV));
+  const uint32_t s_raw = s_v + kStagesV * kTileBytes;
+  Ctrl& C = *reinterpret_cast<Ctrl*>(smem_raw + (s_raw - smem_u32(smem_raw)) +
+                                     kRaw * raw_bytes<FMT, DP>());
   volatile int* abort = &C.abort;
   const int warp = threadIdx.x / 32, lane = lane_id();
   const int D = p.c.head_dim;
 
   if (threadIdx.x == 0) {
-    constexpr int kFull = FMT == DT_BF16 ? 2 : LT;  // TMA: the bytes announced, the edge by hand
+    // TMA: the bytes announced, the edge by hand; MX: the warps that widen
+    constexpr int kFull = FMT == DT_BF16 ? 2 : kConvWarps;
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(smem_u32(&C.raw_full[i]), 33);  // the bytes announced, each lane's scales
+      mbar_init(smem_u32(&C.raw_free[i]), kConvWarps);
+    }
     for (int i = 0; i < kStagesK; ++i) {
       mbar_init(smem_u32(&C.kfull[i]), kFull);
       mbar_init(smem_u32(&C.kfree[i]), 1);
@@ -425,12 +440,10 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       }
       if (ok) mma_commit(smem_u32(&C.o_full));
     }
-  } else if (warp < kLoad0 + load_warps<FMT>()) {
+  } else if (warp < kLoad0 + (FMT == DT_BF16 ? 2 : 1)) {
     // ---- loaders
-    const int lt = threadIdx.x - kLoad0 * 32;
     const int tiles_per_page = p.c.page_size / 16;
-    int ks = 0, vs = 0, piece = 0;
-    uint32_t kp = 0, vp = 0;
+    int piece = 0;
     bool ok = true;
     // lane g < 8: the pool's tile (16 rows) of keys 16 g .. of a tile
     auto look_up = [&](int h, int key0) {
@@ -446,25 +459,24 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       }
       return at;
     };
-    // Tiles kAhead further on are brought to the L2: memory's latency is more than the stages in
-    // shared memory cover. Lanes from line0 on, `lines` apart, take the 128-byte lines of 16 rows.
-    constexpr int kAhead = 5;
-    auto prefetch = [&](const char* pool, uint32_t at, int line0, int lines) {
-      if (at == kNone) return;
-      const char* rows = pool + static_cast<size_t>(at) * 16 * p.c.row_bytes;
-      for (int i = line0; i * 128 < 16 * p.c.row_bytes; i += lines)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(rows + i * 128));
+    // the row of the pool where lane i's box of a tile starts; past the pool (zeros) for none
+    auto box_row = [&](uint32_t tile_of, int box) {
+      const uint32_t at = __shfl_sync(0xffffffffu, tile_of, lane * box / 16 & 7);
+      return at == kNone ? p.pool_rows : static_cast<int>(at) * 16;
     };
+    int stage = 0;
+    uint32_t phase = 0;
     Walk walk(p);
-    for (; ok && walk.next(p) && !*abort; ++piece) {
-      const int h = walk.seg / p.row_tiles;
-      uint32_t tile_of = look_up(h, walk.t0 * kPrefixKeys);
-      if constexpr (FMT == DT_BF16) {
-        // warp 0 of the loaders brings the keys, warp 1 the values, lane i the i-th box of rows
-        const bool keys = warp == kLoad0;
-        const char* pool = keys ? p.c.k : p.c.v;
-        int& stage = keys ? ks : vs;
-        uint32_t& phase = keys ? kp : vp;
+    if constexpr (FMT == DT_BF16) {
+      // Warp 0 of the loaders brings the keys, warp 1 the values, lane i the i-th box of rows.
+      // Tiles kAhead further on are brought to the L2: memory's latency is more than the stages
+      // in shared memory cover.
+      constexpr int kAhead = 5;
+      const bool keys = warp == kLoad0;
+      const char* pool = keys ? p.c.k : p.c.v;
+      for (; ok && walk.next(p) && !*abort; ++piece) {
+        const int h = walk.seg / p.row_tiles;
+        uint32_t tile_of = look_up(h, walk.t0 * kPrefixKeys);
         for (int j = 0; j < walk.n; ++j) {
           const int key0 = (walk.t0 + j) * kPrefixKeys;
           const uint32_t next = j + 1 < walk.n ? look_up(h, key0 + kPrefixKeys) : kNone;
@@ -472,8 +484,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
               j + kAhead < walk.n ? look_up(h, key0 + kAhead * kPrefixKeys) : kNone;
           const uint32_t full = smem_u32(keys ? &C.kfull[stage] : &C.vfull[stage]);
           const uint32_t dst = (keys ? s_k : s_v) + stage * kTileBytes;
-          ok = __all_sync(0xffffffffu, wait_for(smem_u32(keys ? &C.kfree[stage] : &C.vfree[stage]),
-                                                phase ^ 1u, abort));
+          ok = warp_wait(smem_u32(keys ? &C.kfree[stage] : &C.vfree[stage]), phase ^ 1u, abort);
           if (!ok) break;
           // a tile that the prefix ends in: boxes of 16 rows, the one it ends in by hand
           const bool part = key0 + kPrefixKeys > p.len;
@@ -483,9 +494,8 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
             mbar_arrive_expect_tx(full, kTileBytes - (by_hand ? DP / 64 * 16 * 128 : 0));
           __syncwarp();
           const CUtensorMap* map = part ? (keys ? &maps.k16 : &maps.v16) : (keys ? &maps.k : &maps.v);
-          const uint32_t at = __shfl_sync(0xffffffffu, tile_of, lane * box / 16 & 7);
+          const int row = box_row(tile_of, box);
           if (lane < kPrefixKeys / box && !(by_hand && lane == edge)) {
-            const int row = at == kNone ? p.pool_rows : static_cast<int>(at) * 16;  // past it: zeros
 #pragma unroll
             for (int c = 0; c < DP / 64; ++c)
               tma_load_2d(dst + c * kSub + lane * box * 128, map, full, c * 64, row);
@@ -504,73 +514,109 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
             __syncwarp();
           }
           if (lane == 0) mbar_arrive(full);
+          // a line of 16 rows a lane
 #pragma unroll
-          for (int i = 0; i < 8; ++i) prefetch(pool, __shfl_sync(0xffffffffu, far, i), lane, 32);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t at = __shfl_sync(0xffffffffu, far, i);
+            if (at != kNone && lane * 128 < 16 * p.c.row_bytes)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                  pool + static_cast<size_t>(at) * 16 * p.c.row_bytes + lane * 128));
+          }
           if (++stage == (keys ? kStagesK : kStagesV)) stage = 0, phase ^= 1u;
           tile_of = next;
         }
-      } else {
-        // 16 bytes of codes: CH channels, CH / 8 chunks of shared memory
-        constexpr int CH = FMT == DT_MXFP8 ? 16 : 32, kU = DP / CH;
-        constexpr int kUnits = kPrefixKeys * kU, kN = (kUnits + LT - 1) / LT;
-        struct Raw {
-          uint4 v[kN];
-          uint32_t s[kN];
-        };
-        auto fetch = [&](Raw& x, const char* pool, const uint8_t* scales, int key0) {
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const int n = lt + i * LT, rr = n / kU, u = n % kU;
-            const uint32_t at = __shfl_sync(0xffffffffu, tile_of, rr / 16 & 7);
-            x.v[i] = make_uint4(0, 0, 0, 0);
-            x.s[i] = 127;
-            if (n < kUnits && u * CH < D && at != kNone && key0 + rr < p.len) {
-              const size_t row = static_cast<size_t>(at) * 16 + rr % 16;
-              x.v[i] = ldg_stream(pool + row * p.c.row_bytes + u * 16);
-              x.s[i] = __ldg(scales + row * p.c.scale_stride + u * CH / kMxBlock);
-            }
-          }
-        };
-        auto put = [&](const Raw& x, uint32_t dst, uint32_t full_bar) {
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            uint32_t w[CH / 2];
-            const int n = lt + i * LT, rr = n / kU, u = n % kU;
-            if (n >= kUnits) break;
-            decode16<FMT>(x.v[i], x.s[i], w);
-#pragma unroll
-            for (int e = 0; e < CH / 8; ++e) {
-              // the threads of a row start at different chunks: fewer bank conflicts
-              const int k = (e + (u * CH / 64)) % (CH / 8);
-              uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
-#pragma unroll
-              for (int z = 1; z < CH / 8; ++z)
-                if (k == z) v = make_uint4(w[4 * z], w[4 * z + 1], w[4 * z + 2], w[4 * z + 3]);
-              sts128(dst + place(rr, u * (CH / 8) + k), v);
-            }
-          }
-          proxy_fence();
-          mbar_arrive(full_bar);
-        };
-        Raw k, v;
-        fetch(k, p.c.k, p.c.k_scale, walk.t0 * kPrefixKeys);
-        for (int j = 0; j < walk.n; ++j) {
+      }
+    } else {
+      // codes by TMA, lane i the i-th box; scale words by the lanes
+      for (; ok && walk.next(p) && !*abort; ++piece) {
+        const int h = walk.seg / p.row_tiles;
+        uint32_t tile_of = look_up(h, walk.t0 * kPrefixKeys);
+        for (int j = 0; ok && j < walk.n; ++j) {
           const int key0 = (walk.t0 + j) * kPrefixKeys;
           const uint32_t next = j + 1 < walk.n ? look_up(h, key0 + kPrefixKeys) : kNone;
-          const uint32_t far =
-              j + kAhead < walk.n ? look_up(h, key0 + kAhead * kPrefixKeys) : kNone;
-          for (int i = warp - kLoad0; i < 8; i += load_warps<FMT>())
-            prefetch(lane < 16 ? p.c.k : p.c.v, __shfl_sync(0xffffffffu, far, i), lane & 15, 16);
-          fetch(v, p.c.v, p.c.v_scale, key0);
-          ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.kfree[ks]), kp ^ 1u, abort));
-          if (!ok) break;
-          put(k, s_k + ks * kTileBytes, smem_u32(&C.kfull[ks]));
-          if (++ks == kStagesK) ks = 0, kp ^= 1u;
+          const int row = box_row(tile_of, p.box);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = warp_wait(smem_u32(&C.raw_free[stage]), phase ^ 1u, abort);
+            if (!ok) break;
+            const uint32_t full = smem_u32(&C.raw_full[stage]);
+            const uint32_t dst = s_raw + stage * raw_bytes<FMT, DP>();
+            const uint32_t scales = dst + raw_bytes<FMT, DP>() - kPrefixKeys * 4;
+            if (lane == 0) mbar_arrive_expect_tx(full, kPrefixKeys * p.c.row_bytes);
+            __syncwarp();
+            if (lane < kPrefixKeys / p.box)
+              tma_load_2d(dst + lane * p.box * p.c.row_bytes, kv ? &maps.v : &maps.k, full, 0, row);
+            const uint8_t* sc = kv ? p.c.v_scale : p.c.k_scale;
+#pragma unroll
+            for (int i = 0; i < kPrefixKeys / 32; ++i) {
+              const int r = i * 32 + lane;
+              const uint32_t at = __shfl_sync(0xffffffffu, tile_of, r / 16);
+              const size_t from = at == kNone ? 0 : static_cast<size_t>(at) * 16 + r % 16;
+              paged::cp_async4_n(scales + r * 4, sc + from * 4, at == kNone ? 0 : 4);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full)
+                         : "memory");
+            if (++stage == kRaw) stage = 0, phase ^= 1u;
+          }
           tile_of = next;
-          if (j + 1 < walk.n) fetch(k, p.c.k, p.c.k_scale, key0 + kPrefixKeys);
-          ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.vfree[vs]), vp ^ 1u, abort));
+        }
+      }
+      cp_async_wait<0>();
+    }
+  } else if (warp >= kConv0) {
+    if constexpr (FMT != DT_BF16) {
+      // ---- codes to bf16: 16 bytes, CH channels, CH / 8 chunks of an operand's row at a time
+      constexpr int CH = FMT == DT_MXFP8 ? 16 : 32, kU = DP / CH;
+      constexpr int kStep = kConvWarps * 32 / kU, kN = kPrefixKeys / kStep;
+      const int ct = threadIdx.x - kConv0 * 32, u = ct % kU, r0 = ct / kU;
+      const bool in_row = u * CH < D;
+      // the units of a row's second 64 channels start with their second half: no bank is met
+      // twice by the eight lanes that store together
+      const bool swap = u * CH >= 64;
+      int raw = 0, ks = 0, vs = 0;
+      uint32_t raw_phase = 0, kp = 0, vp = 0;
+      bool ok = true;
+      auto widen = [&](uint32_t dst, uint32_t full, int valid) {
+        const uint32_t src = s_raw + raw * raw_bytes<FMT, DP>();
+        const uint32_t scales = src + raw_bytes<FMT, DP>() - kPrefixKeys * 4;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int r = r0 + i * kStep;
+          uint32_t w[CH / 2];
+          uint4 v = make_uint4(0, 0, 0, 0);
+          uint32_t sc = 0;
+          if (in_row && r < valid) {
+            v = lds128(src + r * p.c.row_bytes + u * 16);
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(scales + r * 4 + u * CH / 32));
+          }
+          if (swap) v = make_uint4(v.z, v.w, v.x, v.y);
+          decode16<FMT>(v, sc, w);
+#pragma unroll
+          for (int k = 0; k < CH / 8; ++k)
+            sts128(dst + place(r, u * (CH / 8) + (swap ? k ^ (CH / 16) : k)),
+                   make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+        }
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full);
+          mbar_arrive(smem_u32(&C.raw_free[raw]));
+        }
+        if (++raw == kRaw) raw = 0, raw_phase ^= 1u;
+      };
+      Walk walk(p);
+      while (ok && walk.next(p) && !*abort) {
+        for (int j = 0; j < walk.n; ++j) {
+          const int valid = p.len - (walk.t0 + j) * kPrefixKeys;
+          ok = warp_wait(smem_u32(&C.raw_full[raw]), raw_phase, abort) &&
+               warp_wait(smem_u32(&C.kfree[ks]), kp ^ 1u, abort);
           if (!ok) break;
-          put(v, s_v + vs * kTileBytes, smem_u32(&C.vfull[vs]));
+          widen(s_k + ks * kTileBytes, smem_u32(&C.kfull[ks]), valid);
+          if (++ks == kStagesK) ks = 0, kp ^= 1u;
+          ok = warp_wait(smem_u32(&C.raw_full[raw]), raw_phase, abort) &&
+               warp_wait(smem_u32(&C.vfree[vs]), vp ^ 1u, abort);
+          if (!ok) break;
+          widen(s_v + vs * kTileBytes, smem_u32(&C.vfull[vs]), valid);
           if (++vs == kStagesV) vs = 0, vp ^= 1u;
         }
       }
@@ -599,24 +645,28 @@ cudaError_t launch(const PrefixArgs& p, int grid, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 128 || !ready[dev]) {
     e = cudaFuncSetAttribute(k_prefix<FMT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem_bytes<DP>());
+                             smem_bytes<FMT, DP>());
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) ready[dev] = true;
   }
   PrefixMaps maps{};
+  auto encode = [&](CUtensorMap* m, const void* pool, int rows) {
+    if (e != cudaSuccess) return;
+    if (FMT == DT_BF16)
+      e = encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, p.pool_rows, p.c.head_dim,
+                         64, rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    else
+      e = encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pool, p.pool_rows, p.c.row_bytes,
+                         p.c.row_bytes, rows, CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  encode(&maps.k, p.c.k, p.box);
+  encode(&maps.v, p.c.v, p.box);
   if (FMT == DT_BF16) {
-    auto encode = [&](CUtensorMap* m, const void* pool, int rows) {
-      if (e == cudaSuccess)
-        e = encode_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, p.pool_rows,
-                           p.c.head_dim, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B);
-    };
-    encode(&maps.k, p.c.k, p.box);
-    encode(&maps.v, p.c.v, p.box);
     encode(&maps.k16, p.c.k, 16);
     encode(&maps.v16, p.c.v, 16);
-    if (e != cudaSuccess) return e;
   }
-  k_prefix<FMT, DP><<<grid, threads<FMT>(), smem_bytes<DP>(), st>>>(p, maps);
+  if (e != cudaSuccess) return e;
+  k_prefix<FMT, DP><<<grid, threads<FMT>(), smem_bytes<FMT, DP>(), st>>>(p, maps);
   return cudaGetLastError();
 }
 
