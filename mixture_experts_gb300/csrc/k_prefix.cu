@@ -291,8 +291,10 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
           }
           tmem_st_wait();
         }
+        // (Loops of 32 keys: unrolled, the roles' code together is more than the instruction
+        // caches hold, and every warp waited for instructions.)
         float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tmem_ld32(t_s + 32 * c, v);
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         const uint64_t sl2 = pair(__float_as_uint(sl), __float_as_uint(sl));
         const uint64_t neg_m = pair(__float_as_uint(-m), __float_as_uint(-m));
         uint64_t l2 = 0;  // of even and odd keys
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tmem_ld32(t_s + 32 * c, v);
@@ -573,13 +575,13 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       // the units of a row's second 64 channels start with their second half: no bank is met
       // twice by the eight lanes that store together
       const bool swap = u * CH >= 64;
-      int raw = 0, ks = 0, vs = 0;
-      uint32_t raw_phase = 0, kp = 0, vp = 0;
+      int raw = 0, at[2] = {0, 0};
+      uint32_t raw_phase = 0, phases = 0;  // bit 0: of the keys' stages, 1: of the values'
       bool ok = true;
       auto widen = [&](uint32_t dst, uint32_t full, int valid) {
         const uint32_t src = s_raw + raw * raw_bytes<FMT, DP>();
         const uint32_t scales = src + raw_bytes<FMT, DP>() - kPrefixKeys * 4;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kN; ++i) {
           const int r = r0 + i * kStep;
           uint32_t w[CH / 2];
@@ -606,18 +608,22 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       };
       Walk walk(p);
       while (ok && walk.next(p) && !*abort) {
-        for (int j = 0; j < walk.n; ++j) {
-          const int valid = p.len - (walk.t0 + j) * kPrefixKeys;
+#pragma unroll 1
+        for (int i = 0; ok && i < 2 * walk.n; ++i) {
+          const int kv = i & 1, stage = kv ? at[1] : at[0];
           ok = warp_wait(smem_u32(&C.raw_full[raw]), raw_phase, abort) &&
-               warp_wait(smem_u32(&C.kfree[ks]), kp ^ 1u, abort);
+               warp_wait(smem_u32(kv ? &C.vfree[stage] : &C.kfree[stage]),
+                         (phases >> kv & 1u) ^ 1u, abort);
           if (!ok) break;
-          widen(s_k + ks * kTileBytes, smem_u32(&C.kfull[ks]), valid);
-          if (++ks == kStagesK) ks = 0, kp ^= 1u;
-          ok = warp_wait(smem_u32(&C.raw_full[raw]), raw_phase, abort) &&
-               warp_wait(smem_u32(&C.vfree[vs]), vp ^ 1u, abort);
-          if (!ok) break;
-          widen(s_v + vs * kTileBytes, smem_u32(&C.vfull[vs]), valid);
-          if (++vs == kStagesV) vs = 0, vp ^= 1u;
+          widen((kv ? s_v : s_k) + stage * kTileBytes,
+                smem_u32(kv ? &C.vfull[stage] : &C.kfull[stage]),
+                p.len - (walk.t0 + i / 2) * kPrefixKeys);
+          const bool round = stage + 1 == (kv ? kStagesV : kStagesK);
+          if (kv)
+            at[1] = round ? 0 : stage + 1;
+          else
+            at[0] = round ? 0 : stage + 1;
+          phases ^= (round ? 1u : 0u) << kv;
         }
       }
     }
