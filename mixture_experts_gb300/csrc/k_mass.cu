@@ -172,43 +172,28 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
         }
       }
       if constexpr (kMx) {
-        // MX codes under their scale as bf16 operands, the fast way where the lane's codes allow it
-        uint32_t odd = 0;
+        // bytes past the head's blocks may hold anything
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int i = 0; i < (DP > 128 ? 2 : 1); ++i) {
-            const int n = D / kMxBlock - 4 * i;  // bytes past the head's blocks may hold anything
+            const int n = D / kMxBlock - 4 * i;
             sc[e][i] &= n >= 4 ? 0xffffffffu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
-            odd |= __vcmpgtu4(sc[e][i], kMxFast * 0x01010101u);
           }
-          if constexpr (FMT == DT_MXFP8) {
 #pragma unroll
-            for (int j = 0; j < kJ; ++j)
-              odd |= e4m3_nans(raw[j][e].w[0]) | e4m3_nans(raw[j][e].w[1]);
+        for (int j = 0; j < kJ; ++j) {
+          uint32_t k0[4], k1[4];
+          const int last = bytes8<FMT>() / 4 - 1;
+          mx8_bf16<FMT>(raw[j][0].w[0], raw[j][0].w[last],
+                        e8m0_f32(sc[0][j / 4] >> 8 * (j % 4) & 0xffu), k0);
+          mx8_bf16<FMT>(raw[j][1].w[0], raw[j][1].w[last],
+                        e8m0_f32(sc[1][j / 4] >> 8 * (j % 4) & 0xffu), k1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16_16816(x[nt], k0[0], k1[0], k0[1], k1[1], q[nt][j][0], q[nt][j][1]);
+            mma_bf16_16816(x[nt], k0[2], k1[2], k0[3], k1[3], q[nt][j][2], q[nt][j][3]);
           }
         }
-        auto products = [&](auto fast) {
-          constexpr bool kFast = decltype(fast)::value;
-#pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            uint32_t k0[4], k1[4];
-            const int last = bytes8<FMT>() / 4 - 1;
-            mx8_bf16<FMT, kFast>(raw[j][0].w[0], raw[j][0].w[last],
-                                 sc[0][j / 4] >> 8 * (j % 4) & 0xffu, k0);
-            mx8_bf16<FMT, kFast>(raw[j][1].w[0], raw[j][1].w[last],
-                                 sc[1][j / 4] >> 8 * (j % 4) & 0xffu, k1);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16_16816(x[nt], k0[0], k1[0], k0[1], k1[1], q[nt][j][0], q[nt][j][1]);
-              mma_bf16_16816(x[nt], k0[2], k1[2], k0[3], k1[3], q[nt][j][2], q[nt][j][3]);
-            }
-          }
-        };
-        if (!__any_sync(0xffffffffu, odd != 0))
-          products(std::integral_constant<bool, true>());
-        else
-          products(std::integral_constant<bool, false>());
       }
       if constexpr (kF32) {
 #pragma unroll

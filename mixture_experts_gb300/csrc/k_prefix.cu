@@ -41,10 +41,10 @@ constexpr int kConv0 = 12, kConvWarps = 8;  // MX: the warps that widen
 constexpr uint32_t kOCol = 256;          // O of the streams; S at 0 and 128
 constexpr uint32_t kNone = 0xffffffffu;
 
-constexpr int kStagesV = 2, kMostK = 3, kRaw = 3;
+constexpr int kMost = 3, kRaw = 3;
 
 template <int FMT>
-constexpr int stages_k() {
+constexpr int stages() {  // of keys, and of values
   return FMT == DT_BF16 ? 3 : 2;
 }
 template <int FMT>
@@ -62,17 +62,17 @@ struct PrefixMaps {  // the pools as rows: boxes of a page's rows (p.box); bf16:
 };
 
 struct Ctrl {
-  uint64_t kfull[kMostK], kfree[kMostK], vfull[kStagesV], vfree[kStagesV];
+  uint64_t kfull[kMost], kfree[kMost], vfull[kMost], vfree[kMost];
   uint64_t raw_full[kRaw], raw_free[kRaw];
   uint64_t q_full, q_free, s_full[2], p_full[2], o_full, o_free, ml_full;
   uint32_t tmem;
   int abort;
-  float2 ml[2][2][kPrefixRows];  // by piece's parity, stream
+  float2 ml[2][kPrefixRows];  // of the streams
 };
 
 template <int FMT, int DP>
 constexpr int smem_bytes() {
-  return 1024 + DP / 64 * kSub * (1 + stages_k<FMT>() + kStagesV) + kRaw * raw_bytes<FMT, DP>() +
+  return DP / 64 * kSub * (1 + 2 * stages<FMT>()) + kRaw * raw_bytes<FMT, DP>() +
          static_cast<int>(sizeof(Ctrl));
 }
 
@@ -188,11 +188,15 @@ struct Walk {
 template <int FMT, int DP>
 __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p, const __grid_constant__ PrefixMaps maps) {
   constexpr int kTileBytes = DP / 64 * kSub;
-  constexpr int kStagesK = stages_k<FMT>();
-  extern __shared__ char smem_raw[];
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t s_q = base, s_k = base + kTileBytes, s_v = s_k + kStagesK * kTileBytes;
-  const uint32_t s_raw = s_v + kStagesV * kTileBytes;
+  constexpr int kStages = stages<FMT>();
+  extern __shared__ __align__(1024) char smem_raw[];  // there is no room to align it by hand
+  const uint32_t base = smem_u32(smem_raw);
+  if (base & 1023u) {
+    if (threadIdx.x == 0) latch_error(p.status, kErrDevice);
+    return;
+  }
+  const uint32_t s_q = base, s_k = base + kTileBytes, s_v = s_k + kStages * kTileBytes;
+  const uint32_t s_raw = s_v + kStages * kTileBytes;
   Ctrl& C = *reinterpret_cast<Ctrl*>(smem_raw + (s_raw - smem_u32(smem_raw)) +
                                      kRaw * raw_bytes<FMT, DP>());
   volatile int* abort = &C.abort;
@@ -206,11 +210,11 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       mbar_init(smem_u32(&C.raw_full[i]), 33);  // the bytes announced, each lane's scales
       mbar_init(smem_u32(&C.raw_free[i]), kConvWarps);
     }
-    for (int i = 0; i < kStagesK; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&C.kfull[i]), kFull);
       mbar_init(smem_u32(&C.kfree[i]), 1);
     }
-    for (int i = 0; i < kStagesV; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&C.vfull[i]), kFull);
       mbar_init(smem_u32(&C.vfree[i]), 1);
     }
@@ -351,14 +355,16 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         if (!__all_sync(0xffffffffu, wait_for(smem_u32(&C.q_free), piece & 1, abort))) break;
         load_queries(ahead);
       }
-      C.ml[piece & 1][X][row] = make_float2(m, l);
+      // (the piece before has been read out of it, as it has out of O)
+      if (!warp_wait(smem_u32(&C.o_free), (piece & 1) ^ 1u, abort)) break;
+      C.ml[X][row] = make_float2(m, l);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&C.ml_full));
       ok = __all_sync(0xffffffffu, wait_for(smem_u32(&C.ml_full), piece & 1, abort) &&
                                        wait_for(smem_u32(&C.o_full), piece & 1, abort));
       if (!ok) break;
       tc_fence_after();
-      const float2 a = C.ml[piece & 1][0][row], b = C.ml[piece & 1][1][row];
+      const float2 a = C.ml[0][row], b = C.ml[1][row];
       const float mm = fmaxf(a.x, b.x);
       const float wa = a.y * ex2(a.x - mm), wb = b.y * ex2(b.x - mm), sum = wa + wb;
       // sums over their own weights first: means cannot overflow
@@ -419,7 +425,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
           mma_commit(smem_u32(&C.kfree[ks]));
           mma_commit(smem_u32(&C.s_full[j & 1]));
           if (j == walk.n - 1) mma_commit(smem_u32(&C.q_free));
-          if (++ks == kStagesK) ks = 0, kp ^= 1u;
+          if (++ks == kStages) ks = 0, kp ^= 1u;
         }
         if (j == 0) continue;
         const int X = (j - 1) & 1;
@@ -438,7 +444,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
           mma_ts(tmem + kOCol + X * 128, a + 16, b, kIdO, 1u);
         }
         mma_commit(smem_u32(&C.vfree[vs]));
-        if (++vs == kStagesV) vs = 0, vp ^= 1u;
+        if (++vs == kStages) vs = 0, vp ^= 1u;
       }
       if (ok) mma_commit(smem_u32(&C.o_full));
     }
@@ -524,7 +530,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
               asm volatile("prefetch.global.L2 [%0];" ::"l"(
                   pool + static_cast<size_t>(at) * 16 * p.c.row_bytes + lane * 128));
           }
-          if (++stage == (keys ? kStagesK : kStagesV)) stage = 0, phase ^= 1u;
+          if (++stage == kStages) stage = 0, phase ^= 1u;
           tile_of = next;
         }
       }
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
           widen((kv ? s_v : s_k) + stage * kTileBytes,
                 smem_u32(kv ? &C.vfull[stage] : &C.kfull[stage]),
                 p.len - (walk.t0 + i / 2) * kPrefixKeys);
-          const bool round = stage + 1 == (kv ? kStagesV : kStagesK);
+          const bool round = stage + 1 == kStages;
           if (kv)
             at[1] = round ? 0 : stage + 1;
           else

@@ -2,8 +2,6 @@
 // quantised and decoded by the lanes that hold them.
 #pragma once
 
-#include <type_traits>
-
 #include "attn.h"
 #include "common.cuh"
 
@@ -78,35 +76,22 @@ COLI_DEV void f16x8_f32(const uint32_t (&h)[4], float (&x)[8]) {
 }
 
 // ---- stored rows to bf16 pairs, for products and comparisons in bf16 ------------
-// An MX value is exact in bf16 within its range (fp32's) and rounded once to it beyond, as
-// the cache's read rounds it. The fast way: an element's fp16 form with its bits moved down
-// by three is the value times 2^-112 in bf16, and the factor 2^(s - 15) undoes that together
-// with the scale. It serves scale bytes up to 142 and no NaN codes.
-constexpr uint32_t kMxFast = 142;
-
-// Whether a word of four E4M3 codes holds a NaN (its seven low bits all set), as bits.
-COLI_DEV uint32_t e4m3_nans(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
-// 8 codes (MXFP8: both words, MXFP4: w0) under one scale, element 0 lowest.
-template <int FMT, bool FAST>
-COLI_DEV void mx8_bf16(uint32_t w0, uint32_t w1, uint32_t scale, uint32_t (&o)[4]) {
+// 8 codes (MXFP8: both words, MXFP4: w0) times their scale, element 0 lowest: exact in bf16
+// within its range (fp32's) and rounded once to it beyond, as the cache's read rounds them.
+// Through fp32: the fp16 forms' bits moved to bf16's places and multiplied there take fewer
+// steps, but of the integer pipe, which is what such kernels run out of (bounds of 4099 pages
+// 78 against 65 us), and no NaN codes.
+template <int FMT>
+COLI_DEV void mx8_bf16(uint32_t w0, uint32_t w1, float scale, uint32_t (&o)[4]) {
   uint32_t h[4];
+  float x[8];
   if constexpr (FMT == DT_MXFP8)
     e4m3x8_f16(w0, w1, h);
   else
     e2m1x8_f16(w0, h);
-  if constexpr (FAST) {
-    const uint32_t f = (scale + 112u) * 0x00800080u;
+  f16x8_f32(h, x);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      o[k] = fma_bf16x2(((h[k] & 0x7fff7fffu) >> 3) | (h[k] & 0x80008000u), f, 0x80008000u);
-  } else {
-    float x[8];
-    f16x8_f32(h, x);
-    const float f = e8m0_f32(scale);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = pack_bf16x2(x[2 * k] * f, x[2 * k + 1] * f);
-  }
+  for (int k = 0; k < 4; ++k) o[k] = pack_bf16x2(x[2 * k] * scale, x[2 * k + 1] * scale);
 }
 
 // Words that 16 stored bytes make: bf16 pairs, or fp32 as it is.
@@ -119,26 +104,17 @@ COLI_DEV void decode16(const uint4& raw, uint32_t scale, uint32_t (&w)[words16<F
   if constexpr (FMT == DT_F32 || FMT == DT_BF16) {
     w[0] = raw.x, w[1] = raw.y, w[2] = raw.z, w[3] = raw.w;
   } else {
-    uint32_t odd = scale > kMxFast;
-    if constexpr (FMT == DT_MXFP8)
-      odd |= e4m3_nans(raw.x) | e4m3_nans(raw.y) | e4m3_nans(raw.z) | e4m3_nans(raw.w);
-    auto all = [&](auto fast) {
-      constexpr bool kFast = decltype(fast)::value;
+    const float f = e8m0_f32(scale);
 #pragma unroll
-      for (int i = 0; i < words16<FMT>() / 4; ++i) {
-        uint32_t o[4];
-        if constexpr (FMT == DT_MXFP8)
-          mx8_bf16<FMT, kFast>(word_of(raw, 2 * i), word_of(raw, 2 * i + 1), scale, o);
-        else
-          mx8_bf16<FMT, kFast>(word_of(raw, i), 0, scale, o);
+    for (int i = 0; i < words16<FMT>() / 4; ++i) {
+      uint32_t o[4];
+      if constexpr (FMT == DT_MXFP8)
+        mx8_bf16<FMT>(word_of(raw, 2 * i), word_of(raw, 2 * i + 1), f, o);
+      else
+        mx8_bf16<FMT>(word_of(raw, i), 0, f, o);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[4 * i + k] = o[k];
-      }
-    };
-    if (!odd)
-      all(std::integral_constant<bool, true>());
-    else
-      all(std::integral_constant<bool, false>());
+      for (int k = 0; k < 4; ++k) w[4 * i + k] = o[k];
+    }
   }
 }
 
