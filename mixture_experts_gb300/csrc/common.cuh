@@ -183,6 +183,23 @@ COLI_DEV uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   return r;
 }
 
+// Two fp32 numbers in a register pair, for the instructions that take both at once.
+COLI_DEV uint64_t f32x2(float a, float b) {
+  return static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+COLI_DEV float f32x2_lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+COLI_DEV float f32x2_hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+COLI_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+COLI_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 COLI_DEV uint32_t lane_id() { return threadIdx.x & 31u; }
 
 // ---- OCP Microscaling element codes ------------------------------------------

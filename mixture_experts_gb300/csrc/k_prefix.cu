@@ -142,18 +142,9 @@ COLI_DEV uint32_t place(int r, int c) {
   return (c >> 3) * kSub + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-// Two fp32 numbers in one register pair, and what the SM does with both at once.
-COLI_DEV uint64_t pair(uint32_t a, uint32_t b) { return static_cast<uint64_t>(b) << 32 | a; }
-COLI_DEV float low(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-COLI_DEV float high(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-COLI_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-COLI_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+COLI_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -299,14 +290,16 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         }
         // (Loops of 32 keys: unrolled, the roles' code together is more than the instruction
         // caches hold, and every warp waited for instructions.)
-        float top = -INFINITY;
+        float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tmem_ld32(t_s + 32 * c, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+          for (int i = 0; i < 16; ++i)
+            tops[i & 1] = max3(tops[i & 1], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
         }
+        const float top = fmaxf(tops[0], tops[1]);
         const bool raise = fmaf(top, sl, -m) > 0.f;
         if (__any_sync(0xffffffffu, raise)) {
           const float to = raise ? fmaf(top, sl, 8.f) : m;
@@ -324,8 +317,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
             }
           }
         }
-        const uint64_t sl2 = pair(__float_as_uint(sl), __float_as_uint(sl));
-        const uint64_t neg_m = pair(__float_as_uint(-m), __float_as_uint(-m));
+        const uint64_t sl2 = f32x2(sl, sl), neg_m = f32x2(-m, -m), minus = f32x2(-1.f, -1.f);
         uint64_t l2 = 0;  // of even and odd keys
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -335,16 +327,19 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
           uint32_t o[32];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const uint64_t y = fma_f32x2(pair(v[2 * i], v[2 * i + 1]), sl2, neg_m);
-            const float x0 = ex2(low(y)), x1 = ex2(high(y));
-            l2 = add_f32x2(l2, pair(__float_as_uint(x0), __float_as_uint(x1)));
+            const uint64_t y = fma_f32x2(
+                f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sl2, neg_m);
+            const float x0 = ex2(f32x2_lo(y)), x1 = ex2(f32x2_hi(y));
+            const uint64_t x = f32x2(x0, x1);
+            l2 = add_f32x2(l2, x);
             const uint32_t h = pack_bf16x2(x0, x1);
+            const uint64_t rest = fma_f32x2(f32x2(bf16_lo(h), bf16_hi(h)), minus, x);
             o[i] = h;
-            o[16 + i] = pack_bf16x2(x0 - bf16_lo(h), x1 - bf16_hi(h));
+            o[16 + i] = pack_bf16x2(f32x2_lo(rest), f32x2_hi(rest));
           }
           tmem_st32(t_s + 32 * c, o);
         }
-        l += low(l2) + high(l2);
+        l += f32x2_lo(l2) + f32x2_hi(l2);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -578,6 +573,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       // ---- codes to bf16: 16 bytes, CH channels, CH / 8 chunks of an operand's row at a time
       constexpr int CH = FMT == DT_MXFP8 ? 16 : 32, kU = DP / CH;
       constexpr int kStep = kConvWarps * 32 / kU, kN = kPrefixKeys / kStep;
+      static_assert(kStep % 8 == 0, "rows of a thread share r % 8");
       const int ct = threadIdx.x - kConv0 * 32, u = ct % kU, r0 = ct / kU;
       const bool in_row = u * CH < D;
       // the units of a row's second 64 channels start with their second half: no bank is met
@@ -586,25 +582,33 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       int raw = 0, at[2] = {0, 0};
       uint32_t raw_phase = 0, phases = 0;  // bit 0: of the keys' stages, 1: of the values'
       bool ok = true;
+      // where the unit's chunks go in row r0: rows kStep apart keep their swizzle, 8 divides it
+      uint32_t to[CH / 8];
+#pragma unroll
+      for (int k = 0; k < CH / 8; ++k)
+        to[k] = place(r0, u * (CH / 8) + (swap ? k ^ (CH / 16) : k));
+      const uint32_t from = r0 * p.c.row_bytes + u * 16, half = swap ? 8 : 0;
+      const uint32_t scale_at = raw_bytes<FMT, DP>() - kPrefixKeys * 4 + r0 * 4 + u * CH / kMxBlock;
       auto widen = [&](uint32_t dst, uint32_t full, int valid) {
-        const uint32_t src = s_raw + raw * raw_bytes<FMT, DP>();
-        const uint32_t scales = src + raw_bytes<FMT, DP>() - kPrefixKeys * 4;
+        uint32_t src = s_raw + raw * raw_bytes<FMT, DP>() + from;
+        uint32_t sc_src = s_raw + raw * raw_bytes<FMT, DP>() + scale_at;
 #pragma unroll 1
         for (int i = 0; i < kN; ++i) {
-          const int r = r0 + i * kStep;
           uint32_t w[CH / 2];
-          uint4 v = make_uint4(0, 0, 0, 0);
+          uint2 a = make_uint2(0, 0), b = make_uint2(0, 0);
           uint32_t sc = 0;
-          if (in_row && r < valid) {
-            v = lds128(src + r * p.c.row_bytes + u * 16);
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(scales + r * 4 + u * CH / 32));
+          if (in_row && r0 + i * kStep < valid) {
+            a = lds64(src + half);
+            b = lds64(src + 8 - half);
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(sc_src));
           }
-          if (swap) v = make_uint4(v.z, v.w, v.x, v.y);
-          decode16<FMT>(v, sc, w);
+          decode16<FMT>(make_uint4(a.x, a.y, b.x, b.y), sc, w);
 #pragma unroll
           for (int k = 0; k < CH / 8; ++k)
-            sts128(dst + place(r, u * (CH / 8) + (swap ? k ^ (CH / 16) : k)),
-                   make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+            sts128(dst + to[k], make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+          src += kStep * p.c.row_bytes;
+          sc_src += kStep * 4;
+          dst += kStep * 128;
         }
         proxy_fence();
         __syncwarp();
