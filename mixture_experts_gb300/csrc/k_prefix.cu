@@ -5,10 +5,12 @@
 // P = 2^(s x - m), O += P V with a running maximum m, the prefix read once for 128 rows
 // instead of once for each sequence.
 //
-// A block takes 128 rows of a key head and a run of 128-key tiles. Its tiles alternate between
-// two streams, each with its own S, O, m and l in tensor memory and registers of its own
-// warpgroup (columns 0-127 and 128-255 S, 256-511 O), so one stream's softmax runs under the
-// other's products: the MMA warp issues S(0) S(1) PV(0) S(2) PV(1) ... in order. P goes back
+// A block takes 128 or (PAIR) 256 rows of a key head and a run of 128-key tiles. It has two
+// streams, each with its own S, O, m and l in tensor memory and registers of its own warpgroup
+// (columns 0-127 and 128-255 S, 256-511 O), so one stream's softmax runs under the other's
+// products: the MMA warp issues S(0) S(1) PV(0) S(2) PV(1) ... in order. The streams take the
+// tiles by turns, and their sums are joined at the end; or, with 256 rows, 128 rows each and
+// every tile, so that a tile is loaded (and widened) for twice the products. P goes back
 // over S's columns as two bf16 terms, the weight and what its rounding left (16 bits together),
 // and is the second product's A operand from tensor memory; V is its B operand as it lies
 // (keys by channels, "transposed"). m is raised only where a score passes it (weights are
@@ -45,9 +47,13 @@ constexpr uint32_t kNone = 0xffffffffu;
 
 constexpr int kMost = 3, kRaw = 3;
 
-template <int FMT>
+template <int FMT, bool PAIR>
 constexpr int stages() {  // of keys, and of values
-  return FMT == DT_BF16 ? 3 : 2;
+  return FMT == DT_BF16 && !PAIR ? 3 : 2;
+}
+template <bool PAIR>
+constexpr int raw_stages() {
+  return PAIR ? 2 : kRaw;
 }
 template <int FMT>
 constexpr int threads() {  // a multiple of four warps: what a scheduler's share of registers goes by
@@ -63,19 +69,20 @@ struct PrefixMaps {  // the pools as rows: boxes of a page's rows (p.box); bf16:
   CUtensorMap k, v, k16, v16;
 };
 
+template <bool PAIR>
 struct Ctrl {
   uint64_t kfull[kMost], kfree[kMost], vfull[kMost], vfree[kMost];
   uint64_t raw_full[kRaw], raw_free[kRaw];
   uint64_t q_full, q_free, s_full[2], p_full[2], o_full, o_free, ml_full;
   uint32_t tmem;
   int abort;
-  float2 ml[2][kPrefixRows];  // of the streams
+  float2 ml[PAIR ? 1 : 2][PAIR ? 1 : kPrefixRows];  // of the streams, where they are joined
 };
 
-template <int FMT, int DP>
+template <int FMT, int DP, bool PAIR>
 constexpr int smem_bytes() {
-  return DP / 64 * kSub * (1 + 2 * stages<FMT>()) + kRaw * raw_bytes<FMT, DP>() +
-         static_cast<int>(sizeof(Ctrl));
+  return DP / 64 * kSub * ((PAIR ? 2 : 1) + 2 * stages<FMT, PAIR>()) +
+         raw_stages<PAIR>() * raw_bytes<FMT, DP>() + static_cast<int>(sizeof(Ctrl<PAIR>));
 }
 
 // B operand as it lies: 16-bit elements, reduction rows of 128 bytes (64 columns), 8 rows 1024
@@ -178,20 +185,21 @@ struct Walk {
   }
 };
 
-template <int FMT, int DP>
+template <int FMT, int DP, bool PAIR>
 __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p, const __grid_constant__ PrefixMaps maps) {
   constexpr int kTileBytes = DP / 64 * kSub;
-  constexpr int kStages = stages<FMT>();
+  constexpr int kStages = stages<FMT, PAIR>(), kRaws = raw_stages<PAIR>();
+  constexpr int kQTiles = PAIR ? 2 : 1, kSegRows = kQTiles * kPrefixRows;
   extern __shared__ __align__(1024) char smem_raw[];  // there is no room to align it by hand
   const uint32_t base = smem_u32(smem_raw);
   if (base & 1023u) {
     if (threadIdx.x == 0) latch_error(p.status, kErrDevice);
     return;
   }
-  const uint32_t s_q = base, s_k = base + kTileBytes, s_v = s_k + kStages * kTileBytes;
+  const uint32_t s_q = base, s_k = base + kQTiles * kTileBytes, s_v = s_k + kStages * kTileBytes;
   const uint32_t s_raw = s_v + kStages * kTileBytes;
-  Ctrl& C = *reinterpret_cast<Ctrl*>(smem_raw + (s_raw - smem_u32(smem_raw)) +
-                                     kRaw * raw_bytes<FMT, DP>());
+  Ctrl<PAIR>& C = *reinterpret_cast<Ctrl<PAIR>*>(smem_raw + (s_raw - base) +
+                                                 kRaws * raw_bytes<FMT, DP>());
   volatile int* abort = &C.abort;
   const int warp = threadIdx.x / 32, lane = lane_id();
   const int D = p.c.head_dim;
@@ -199,7 +207,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
   if (threadIdx.x == 0) {
     // TMA: the bytes announced, the edge by hand; MX: the warps that widen
     constexpr int kFull = FMT == DT_BF16 ? 2 : kConvWarps;
-    for (int i = 0; i < kRaw; ++i) {
+    for (int i = 0; i < kRaws; ++i) {
       mbar_init(smem_u32(&C.raw_full[i]), 33);  // the bytes announced, each lane's scales
       mbar_init(smem_u32(&C.raw_free[i]), kConvWarps);
     }
@@ -237,25 +245,29 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
     const float sl = fabsf(p.scale) * 1.4426950408889634f;  // the sign went into Q
     // the piece's queries: 128 rows by all softmax warps, their sign that of the scale
     auto load_queries = [&](const Walk& w) {
-      const int h = w.seg / p.row_tiles, r0 = (w.seg - h * p.row_tiles) * kPrefixRows;
+      const int h = w.seg / p.row_tiles, r0 = (w.seg - h * p.row_tiles) * kSegRows;
       const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
-      constexpr int kQ = kPrefixRows * (DP / 8) / (kSoftWarps * 32);
-      uint4 v[kQ];
+      constexpr int kQ = kPrefixRows * (DP / 8) / (kSoftWarps * 32);  // loads in flight
+#pragma unroll 1
+      for (int t = 0; t < kQTiles; ++t) {
+        uint4 v[kQ];
 #pragma unroll
-      for (int e = 0; e < kQ; ++e) {
-        const int i = threadIdx.x + e * kSoftWarps * 32, r = i / (DP / 8), c = i - r * (DP / 8);
-        v[e] = make_uint4(0, 0, 0, 0);
-        if (r0 + r < p.rows && c * 8 < D) {
-          const int b = (r0 + r) / p.group, g = r0 + r - b * p.group;
-          v[e] = ldg_keep(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride +
-                          static_cast<size_t>(h * p.group + g) * D + c * 8);
+        for (int e = 0; e < kQ; ++e) {
+          const int i = threadIdx.x + e * kSoftWarps * 32, r = i / (DP / 8), c = i - r * (DP / 8);
+          const int at = r0 + t * kPrefixRows + r;
+          v[e] = make_uint4(0, 0, 0, 0);
+          if (at < p.rows && c * 8 < D) {
+            const int b = at / p.group, g = at - b * p.group;
+            v[e] = ldg_keep(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_stride +
+                            static_cast<size_t>(h * p.group + g) * D + c * 8);
+          }
         }
-      }
 #pragma unroll
-      for (int e = 0; e < kQ; ++e) {
-        const int i = threadIdx.x + e * kSoftWarps * 32, r = i / (DP / 8), c = i - r * (DP / 8);
-        v[e].x ^= flip, v[e].y ^= flip, v[e].z ^= flip, v[e].w ^= flip;
-        sts128(s_q + place(r, c), v[e]);
+        for (int e = 0; e < kQ; ++e) {
+          const int i = threadIdx.x + e * kSoftWarps * 32, r = i / (DP / 8), c = i - r * (DP / 8);
+          v[e].x ^= flip, v[e].y ^= flip, v[e].z ^= flip, v[e].w ^= flip;
+          sts128(s_q + t * kTileBytes + place(r, c), v[e]);
+        }
       }
       proxy_fence();
       mbar_arrive(smem_u32(&C.q_full));
@@ -267,7 +279,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
     for (; walk.next(p) && !*abort; ++piece) {
       float m = -FLT_MAX, l = 0.f;
       bool ok = true;
-      for (int j = X; j < walk.n; j += 2) {
+      for (int j = PAIR ? 0 : X; j < walk.n; j += PAIR ? 1 : 2) {
         const int key0 = (walk.t0 + j) * kPrefixKeys;
         const uint32_t groups = groups_in_sight(p, key0);
         const bool part = groups != 0xffu || key0 + kPrefixKeys > p.len;
@@ -306,7 +318,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
           const float f = raise ? ex2(m - to) : 1.f;
           m = to;
           l *= f;
-          if (j >= 2) {
+          if (j >= (PAIR ? 1 : 2)) {  // its stream's first product overwrites O
 #pragma unroll 1
             for (int c = 0; c < DP / 32; ++c) {
               uint32_t v[32];
@@ -352,6 +364,32 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         if (!__all_sync(0xffffffffu, wait_for(smem_u32(&C.q_free), piece & 1, abort))) break;
         load_queries(ahead);
       }
+      const int rt = walk.seg % p.row_tiles, r = rt * kSegRows + (PAIR ? X * kPrefixRows : 0) + row;
+      const size_t slot = (static_cast<size_t>(blockIdx.x) + walk.seg) * kSegRows +
+                          (PAIR ? X * kPrefixRows : 0) + row;
+      float* out = p.mean + slot * D;
+      if constexpr (PAIR) {
+        // the streams are rows of their own
+        if (!warp_wait(smem_u32(&C.o_full), piece & 1, abort)) break;
+        tc_fence_after();
+        const float by = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int c = 0; c < DP / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(t_o + c * 32, v);
+          if (r < p.rows) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              if (c * 32 + i >= D) break;
+              float o[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[k] = l == 0.f ? 0.f : __uint_as_float(v[i + k]) * by;
+              *reinterpret_cast<float4*>(out + c * 32 + i) = make_float4(o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+        if (r < p.rows) p.ml[slot] = make_float2(m, l);
+      } else {
       // (the piece before has been read out of it, as it has out of O)
       if (!warp_wait(smem_u32(&C.o_free), (piece & 1) ^ 1u, abort)) break;
       C.ml[X][row] = make_float2(m, l);
@@ -367,9 +405,6 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       // sums over their own weights first: means cannot overflow
       const float fa = wa == 0.f ? 0.f : wa / sum, ia = wa == 0.f ? 0.f : 1.f / a.y;
       const float fb = wb == 0.f ? 0.f : wb / sum, ib = wb == 0.f ? 0.f : 1.f / b.y;
-      const int rt = walk.seg % p.row_tiles, r = rt * kPrefixRows + row;
-      const size_t slot = (static_cast<size_t>(blockIdx.x) + walk.seg) * kPrefixRows + row;
-      float* out = p.mean + slot * D;
 #pragma unroll 1
       for (int c = 0; c < DP / 64; ++c) {
         const int col = (X * (DP / 64) + c) * 32;
@@ -393,6 +428,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         }
       }
       if (X == 0 && r < p.rows) p.ml[slot] = make_float2(mm, sum);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&C.o_free));
@@ -408,27 +444,33 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
     for (; ok && walk.next(p); ++piece) {
       if (!warp_wait(smem_u32(&C.q_full), piece & 1, abort)) break;
       tc_fence_after();
-      for (int j = 0; j <= walk.n; ++j) {
-        if (j < walk.n) {
-          if (!(ok = warp_wait(smem_u32(&C.kfull[ks]), kp, abort))) break;
+      // unit u: stream u % 2; its tile is the u-th, or (PAIR) the streams take each in turn
+      const int units = PAIR ? 2 * walk.n : walk.n;
+      for (int u = 0; u <= units; ++u) {
+        if (u < units) {
+          if (!PAIR || u % 2 == 0)
+            if (!(ok = warp_wait(smem_u32(&C.kfull[ks]), kp, abort))) break;
           tc_fence_after();
-          const uint32_t k0 = s_k + ks * kTileBytes;
+          const uint32_t k0 = s_k + ks * kTileBytes, q0 = s_q + (PAIR ? (u & 1) * kTileBytes : 0);
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k) {
             const uint32_t off = k / 4 * kSub + k % 4 * 32;
-            mma_ss(tmem + (j & 1) * 128, sw128_desc(s_q + off), sw128_desc(k0 + off), kIdS,
+            mma_ss(tmem + (u & 1) * 128, sw128_desc(q0 + off), sw128_desc(k0 + off), kIdS,
                    k != 0 ? 1u : 0u);
           }
-          mma_commit(smem_u32(&C.kfree[ks]));
-          mma_commit(smem_u32(&C.s_full[j & 1]));
-          if (j == walk.n - 1) mma_commit(smem_u32(&C.q_free));
-          if (++ks == kStages) ks = 0, kp ^= 1u;
+          mma_commit(smem_u32(&C.s_full[u & 1]));
+          if (u == units - 1) mma_commit(smem_u32(&C.q_free));
+          if (!PAIR || u % 2 == 1) {
+            mma_commit(smem_u32(&C.kfree[ks]));
+            if (++ks == kStages) ks = 0, kp ^= 1u;
+          }
         }
-        if (j == 0) continue;
-        const int X = (j - 1) & 1;
+        if (u == 0) continue;
+        const int X = (u - 1) & 1;
         // the piece before has been read out of O
-        if (j == 1 && !(ok = warp_wait(smem_u32(&C.o_free), (piece & 1) ^ 1u, abort))) break;
-        if (!(ok = warp_wait(smem_u32(&C.vfull[vs]), vp, abort))) break;
+        if (u == 1 && !(ok = warp_wait(smem_u32(&C.o_free), (piece & 1) ^ 1u, abort))) break;
+        if (!PAIR || X == 0)
+          if (!(ok = warp_wait(smem_u32(&C.vfull[vs]), vp, abort))) break;
         if (!(ok = warp_wait(smem_u32(&C.p_full[X]), p_phase >> X & 1u, abort))) break;
         p_phase ^= 1u << X;
         tc_fence_after();
@@ -437,11 +479,13 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         for (int k = 0; k < kPrefixKeys / 16; ++k) {
           const uint64_t b = sw128_desc_mn(v0 + k * 16 * 128);
           const uint32_t a = tmem + X * 128 + k / 2 * 32 + k % 2 * 8;
-          mma_ts(tmem + kOCol + X * 128, a, b, kIdO, j > 2 || k > 0 ? 1u : 0u);
+          mma_ts(tmem + kOCol + X * 128, a, b, kIdO, u > 2 || k > 0 ? 1u : 0u);
           mma_ts(tmem + kOCol + X * 128, a + 16, b, kIdO, 1u);
         }
-        mma_commit(smem_u32(&C.vfree[vs]));
-        if (++vs == kStages) vs = 0, vp ^= 1u;
+        if (!PAIR || X == 1) {
+          mma_commit(smem_u32(&C.vfree[vs]));
+          if (++vs == kStages) vs = 0, vp ^= 1u;
+        }
       }
       if (ok) mma_commit(smem_u32(&C.o_full));
     }
@@ -562,7 +606,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full)
                          : "memory");
-            if (++stage == kRaw) stage = 0, phase ^= 1u;
+            if (++stage == kRaws) stage = 0, phase ^= 1u;
           }
         }
       }
@@ -592,7 +636,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       auto widen = [&](uint32_t dst, uint32_t full, int valid) {
         uint32_t src = s_raw + raw * raw_bytes<FMT, DP>() + from;
         uint32_t sc_src = s_raw + raw * raw_bytes<FMT, DP>() + scale_at;
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < kN; ++i) {
           uint32_t w[CH / 2];
           uint2 a = make_uint2(0, 0), b = make_uint2(0, 0);
@@ -616,7 +660,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
           mbar_arrive(full);
           mbar_arrive(smem_u32(&C.raw_free[raw]));
         }
-        if (++raw == kRaw) raw = 0, raw_phase ^= 1u;
+        if (++raw == kRaws) raw = 0, raw_phase ^= 1u;
       };
       Walk walk(p);
       while (ok && walk.next(p) && !*abort) {
@@ -655,15 +699,15 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
   }
 }
 
-template <int FMT, int DP>
+template <int FMT, int DP, bool PAIR>
 cudaError_t launch(const PrefixArgs& p, int grid, cudaStream_t st) {
   static bool ready[128] = {};  // the shared-memory limit is raised once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 128 || !ready[dev]) {
-    e = cudaFuncSetAttribute(k_prefix<FMT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem_bytes<FMT, DP>());
+    e = cudaFuncSetAttribute(k_prefix<FMT, DP, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem_bytes<FMT, DP, PAIR>());
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) ready[dev] = true;
   }
@@ -684,13 +728,17 @@ cudaError_t launch(const PrefixArgs& p, int grid, cudaStream_t st) {
     encode(&maps.v16, p.c.v, 16);
   }
   if (e != cudaSuccess) return e;
-  k_prefix<FMT, DP><<<grid, threads<FMT>(), smem_bytes<FMT, DP>(), st>>>(p, maps);
+  k_prefix<FMT, DP, PAIR><<<grid, threads<FMT>(), smem_bytes<FMT, DP, PAIR>(), st>>>(p, maps);
   return cudaGetLastError();
 }
 
 template <int FMT>
 cudaError_t launch_heads(const PrefixArgs& p, int grid, cudaStream_t st) {
-  return p.c.head_dim <= 64 ? launch<FMT, 64>(p, grid, st) : launch<FMT, 128>(p, grid, st);
+  if (p.pair)
+    return p.c.head_dim <= 64 ? launch<FMT, 64, true>(p, grid, st)
+                              : launch<FMT, 128, true>(p, grid, st);
+  return p.c.head_dim <= 64 ? launch<FMT, 64, false>(p, grid, st)
+                            : launch<FMT, 128, false>(p, grid, st);
 }
 
 }  // namespace

@@ -16,7 +16,7 @@ struct JoinArgs {
   const float* mean;     // of the prefix
   const float2* ml;
   int64_t tiles, per;    // of a segment and a block on k_prefix's line; 0: rows as above
-  int row_tiles;
+  int row_tiles, seg_rows;
   int group;
   void* out;
   float* lse;
@@ -37,11 +37,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const JoinArgs 
   int n = 1, step = 0;
   if (p.per > 0) {
     const int h = hq / p.group, r = b * p.group + hq - h * p.group;
-    const int64_t seg = static_cast<int64_t>(h) * p.row_tiles + r / kPrefixRows;
+    const int64_t seg = static_cast<int64_t>(h) * p.row_tiles + r / p.seg_rows;
     const int64_t c0 = seg * p.tiles / p.per, c1 = ((seg + 1) * p.tiles - 1) / p.per;
-    first = static_cast<size_t>(c0 + seg) * kPrefixRows + r % kPrefixRows;
+    first = static_cast<size_t>(c0 + seg) * p.seg_rows + r % p.seg_rows;
     n = static_cast<int>(c1 - c0) + 1;
-    step = kPrefixRows;
+    step = p.seg_rows;
   }
   const float2 own = p.own_ml[row];
   float top = own.x;
@@ -119,13 +119,22 @@ bool on_tensor_cores(const KvView& c, int rows_of_head) {
          static_cast<int64_t>(c.n_pages) * c.n_heads * c.page_size < INT32_MAX;
 }
 
+// Rows of a segment of k_prefix: 256 where a key head has them. With an odd number of 128-row
+// tiles half of the last one is idle; bf16 then takes 128 rows up to three tiles (a tile's time
+// is 1.2 us in pairs and 1.2 alone; MX tiles, widened once for both, TODO).
+int segment_rows(const KvView& c, int rows_of_head) {
+  const int tiles = (rows_of_head + kPrefixRows - 1) / kPrefixRows;
+  const bool pair = tiles > 1 && (c.dtype != DT_BF16 || tiles % 2 == 0 || tiles > 4);
+  return pair ? 2 * kPrefixRows : kPrefixRows;
+}
+
 // Rows of the prefix's partial results.
 int64_t prefix_rows(const KvView& c, int B, int n_q_heads) {
   const int rows = B * (n_q_heads / c.n_heads);
   if (!on_tensor_cores(c, rows)) return static_cast<int64_t>(B) * n_q_heads;
-  const int64_t segments =
-      static_cast<int64_t>(c.n_heads) * ((rows + kPrefixRows - 1) / kPrefixRows);
-  return (segments + sm_count()) * kPrefixRows;
+  const int seg_rows = segment_rows(c, rows);
+  const int64_t segments = static_cast<int64_t>(c.n_heads) * ((rows + seg_rows - 1) / seg_rows);
+  return (segments + sm_count()) * seg_rows;
 }
 
 }  // namespace
@@ -152,7 +161,7 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
   a.scratch = reinterpret_cast<float*>(prefix + part_bytes(c, parts));
   if (s.prefix_len == 0) return launch_paged_attention(a, st);
 
-  JoinArgs j{own_mean, own_ml, mean, ml, 0, 0, 0, group, a.out, a.lse, a.out_stride, rows, heads,
+  JoinArgs j{own_mean, own_ml, mean, ml, 0, 0, 0, 0, group, a.out, a.lse, a.out_stride, rows, heads,
              c.head_dim};
   a.raw = 1;
   a.out_stride = static_cast<size_t>(heads) * c.head_dim;
@@ -166,7 +175,9 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
     p.len = s.prefix_len;
     p.group = group;
     p.rows = B * group;
-    p.row_tiles = (p.rows + kPrefixRows - 1) / kPrefixRows;
+    const int seg_rows = segment_rows(c, p.rows);
+    p.pair = seg_rows == 2 * kPrefixRows;
+    p.row_tiles = (p.rows + seg_rows - 1) / seg_rows;
     p.tiles = (p.len + kPrefixKeys - 1) / kPrefixKeys;
     p.total = static_cast<int64_t>(c.n_heads) * p.row_tiles * p.tiles;
     const int grid = p.total < sm_count() ? static_cast<int>(p.total) : sm_count();
@@ -181,6 +192,7 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
     j.tiles = p.tiles;
     j.per = p.per;
     j.row_tiles = p.row_tiles;
+    j.seg_rows = seg_rows;
     e = launch_prefix(p, grid, st);
   } else {
     PagedArgs f = a;

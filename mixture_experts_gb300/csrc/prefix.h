@@ -15,14 +15,15 @@ struct PrefixArgs {
   int len;             // tokens of the prefix
   int group;           // query heads of a key head
   int rows;            // B * group
-  int row_tiles;       // 128-row tiles of a key head: segment = head * row_tiles + tile
+  int pair;            // 1: a segment is 256 rows of a key head, else 128
+  int row_tiles;       // segments of a key head: segment = head * row_tiles + tile
   int tiles;           // 128-key tiles of a segment
   int64_t total, per;  // tiles in all, of a block
   int box;             // rows of a TMA box: the power of two that divides page_size, to 128
   int pool_rows;       // n_pages * n_kv_heads * page_size
   float scale;
-  float* mean;         // [blocks + segments][128][head_dim]
-  float2* ml;          // [blocks + segments][128]
+  float* mean;         // [blocks + segments][128 or 256][head_dim]
+  float2* ml;          // [blocks + segments][128 or 256]
   int* status;
 };
 cudaError_t launch_prefix(const PrefixArgs& p, int grid, cudaStream_t st);
