@@ -41,8 +41,33 @@ __global__ void __launch_bounds__(THREADS) k_evict_pick(const EvictArgs p) {
     }
     return order_key(__ldg(p.mass + kv_row(p.c, at, h, i - pi * page)));
   };
-  if constexpr (CACHED) {
-    for (int i = threadIdx.x; i < n; i += THREADS) s_keys[i] = load(i);
+  if constexpr (CACHED) {  // eight in flight: a page's number, then the mass
+    constexpr int kDeep = 8;
+    const uint32_t per = 0xffffffffu / page + 1;  // i / page = i * per / 2^32, or one less
+    for (int i0 = threadIdx.x; i0 < n; i0 += THREADS * kDeep) {
+      int row[kDeep], off[kDeep];
+      float m[kDeep];
+#pragma unroll
+      for (int e = 0; e < kDeep; ++e) {
+        const int i = i0 + e * THREADS;
+        int pi = __umulhi(i, per);
+        if (pi * page > i) --pi;
+        off[e] = i - pi * page;
+        row[e] = i < n ? __ldg(table + pi) : 0;
+      }
+#pragma unroll
+      for (int e = 0; e < kDeep; ++e) {
+        const bool in = row[e] >= 0 && row[e] < p.c.n_pages;
+        if (!in) latch_error(p.status, kErrDevice);
+        m[e] = in && i0 + e * THREADS < n ? __ldg(p.mass + kv_row(p.c, row[e], h, off[e]))
+                                          : -INFINITY;
+      }
+#pragma unroll
+      for (int e = 0; e < kDeep; ++e) {
+        const int i = i0 + e * THREADS;
+        if (i < n) s_keys[i] = i < p.first || i >= n - p.recent ? 0xffffffffu : order_key(m[e]);
+      }
+    }
     __syncthreads();
   }
   auto key = [&](int i) {

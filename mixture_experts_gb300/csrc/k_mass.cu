@@ -7,8 +7,8 @@
 // rows, 8 query heads its columns (NT column tiles, more heads in further passes over the
 // keys). The keys come from memory straight into the operand's registers: of every 32
 // channels lane 4g + t has 8t .. + 7 of rows g and g + 8, on both operands. bf16 queries
-// and keys are operands as they are; MX keys are widened to bf16 with their scale (exact within
-// bf16's range); fp32 runs in three tf32 products of operands in two parts.
+// and keys are operands as they are; MX codes are widened to fp16, against fp16 queries, and a
+// block's scale goes on its sum (queries that fp16 does not hold meet bf16 keys); fp32 runs in three tf32 products of operands in two parts.
 // HBM bound by the keys, a third of what the attention itself reads with its values.
 #include "mx.cuh"
 #include "paged.cuh"
@@ -108,34 +108,110 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
         live[nt][c] = lse[nt][c] != -INFINITY;
       }
     }
-    for (int tile = t0; tile < tiles; tile += step) {
-      const int pi = tile / per_page, page = __ldg(table + pi);
-      if (page < 0 || page >= p.c.n_pages) {
-        if (lane == 0) latch_error(p.status, kErrDevice);
-        continue;
+    // MX: queries in fp16, the head's largest element at 2^14, where that is exact (no element
+    // but 0 below 2^-31 of it): codes are fp16 numbers, and their scale goes on a block's sum
+    float scale[NT][2];
+    bool half = kMx;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) scale[nt][0] = scale[nt][1] = p.scale;
+    if constexpr (kMx) {
+      int e[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) most = __vmaxu2(most, q[nt][j][i] & 0x7fff7fffu);
+        uint32_t top = max(most << 16, most & 0x7fff0000u);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        e[nt] = top == 0 ? 0 : static_cast<int>(top >> 23) - 127;
+        half = half && e[nt] <= 80 && e[nt] >= -80;
+        const uint32_t least = static_cast<uint32_t>(max(e[nt], -80) - 31 + 127) << 23;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = q[nt][j][i] << 16 & 0x7fffffffu, a1 = q[nt][j][i] & 0x7fff0000u;
+            half = half && a0 - 1 >= least - 1 && a1 - 1 >= least - 1;  // 0 wraps round
+          }
       }
-      const size_t row = kv_row(p.c, page, h, (tile - pi * per_page) * kTile);
-      const char* src = p.c.k + (row + g) * p.c.row_bytes + t * bytes8<FMT>();
+      half = __all_sync(0xffffffffu, half);
+      if (half) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float up = __uint_as_float(static_cast<uint32_t>(14 - e[nt] + 127) << 23);
+#pragma unroll
+          for (int j = 0; j < kJ; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              q[nt][j][i] = pack_f16x2(bf16_lo(q[nt][j][i]) * up, bf16_hi(q[nt][j][i]) * up);
+          const float down = __uint_as_float(static_cast<uint32_t>(e[nt] - 14 + 127) << 23);
+          // block scales below carry a factor 1 + 2^-23
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            scale[nt][c] = p.scale * __shfl_sync(0xffffffffu, down, 8 * t + 4 * c) * (1.f - 0x1p-23f);
+        }
+      }
+    }
+
+    // a tile's keys, MX ones a tile ahead: 1 or 2 KB a warp are too few in flight
+    struct Keys {
       Raw8<FMT> raw[kJ][2];
+      uint32_t sc[2][2];
+      size_t row;
+      bool in;
+    };
+    auto page_of = [&](int tile) { return tile < tiles ? __ldg(table + tile / per_page) : 0; };
+    auto fetch = [&](Keys& k, int tile, int page) {
+      k.in = tile < tiles && page >= 0 && page < p.c.n_pages;
+      if (!k.in) {
+        if (tile < tiles && lane == 0) latch_error(p.status, kErrDevice);
+        return;
+      }
+      k.row = kv_row(p.c, page, h, tile % per_page * kTile);
+      const char* src = p.c.k + (k.row + g) * p.c.row_bytes + t * bytes8<FMT>();
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          raw[j][e] = Raw8<FMT>{};
+          k.raw[j][e] = Raw8<FMT>{};
           if (j * 32 + t * 8 < D)
-            raw[j][e] = load8<FMT>(src + static_cast<size_t>(e) * 8 * p.c.row_bytes +
-                                   j * 4 * bytes8<FMT>());
+            k.raw[j][e] = load8<FMT>(src + static_cast<size_t>(e) * 8 * p.c.row_bytes +
+                                     j * 4 * bytes8<FMT>());
         }
-      uint32_t sc[2][2] = {};
       if constexpr (kMx) {
-        const uint8_t* s = p.c.k_scale + (row + g) * p.c.scale_stride;
+        const uint8_t* s = p.c.k_scale + (k.row + g) * p.c.scale_stride;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          sc[e][0] = __ldg(reinterpret_cast<const uint32_t*>(s + e * 8 * p.c.scale_stride));
+          k.sc[e][0] = __ldg(reinterpret_cast<const uint32_t*>(s + e * 8 * p.c.scale_stride));
+          k.sc[e][1] = 0;
           if (DP > 128 && p.c.scale_stride > 4)
-            sc[e][1] = __ldg(reinterpret_cast<const uint32_t*>(s + e * 8 * p.c.scale_stride + 4));
+            k.sc[e][1] = __ldg(reinterpret_cast<const uint32_t*>(s + e * 8 * p.c.scale_stride + 4));
         }
       }
+    };
+    Keys ahead;
+    int page = page_of(t0);
+    if constexpr (kMx) {
+      fetch(ahead, t0, page);
+      page = page_of(t0 + step);
+    }
+    for (int tile = t0; tile < tiles; tile += step) {
+      Keys now;
+      if constexpr (kMx) {
+        now = ahead;
+        fetch(ahead, tile + step, page);
+        page = page_of(tile + 2 * step);
+      } else {
+        fetch(now, tile, page);
+        page = page_of(tile + step);
+      }
+      if (!now.in) continue;
+      auto& raw = now.raw;
+      auto& sc = now.sc;
+      const size_t row = now.row;
       float x[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -180,18 +256,59 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
             const int n = D / kMxBlock - 4 * i;
             sc[e][i] &= n >= 4 ? 0xffffffffu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
           }
+        if (half) {
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          uint32_t k0[4], k1[4];
-          const int last = bytes8<FMT>() / 4 - 1;
-          mx8_bf16<FMT>(raw[j][0].w[0], raw[j][0].w[last],
-                        e8m0_f32(sc[0][j / 4] >> 8 * (j % 4) & 0xffu), k0);
-          mx8_bf16<FMT>(raw[j][1].w[0], raw[j][1].w[last],
-                        e8m0_f32(sc[1][j / 4] >> 8 * (j % 4) & 0xffu), k1);
+          for (int j = 0; j < kJ; ++j) {
+            // as fp32 bits with the last one set: byte 255 is then NaN by itself (and byte 0,
+            // 2^-127, counts as 0)
+            const int up = 23 - 8 * (j % 4);
+            const float f0 = __uint_as_float(
+                ((up > 0 ? sc[0][j / 4] << (up & 31) : sc[0][j / 4] >> 1) & 0x7f800000u) | 1u);
+            const float f1 = __uint_as_float(
+                ((up > 0 ? sc[1][j / 4] << (up & 31) : sc[1][j / 4] >> 1) & 0x7f800000u) | 1u);
+            uint32_t k0[4], k1[4];
+            if constexpr (FMT == DT_MXFP8) {
+              e4m3x8_f16(raw[j][0].w[0], raw[j][0].w[1], k0);
+              e4m3x8_f16(raw[j][1].w[0], raw[j][1].w[1], k1);
+            } else {
+              e2m1x8_f16(raw[j][0].w[0], k0);
+              e2m1x8_f16(raw[j][1].w[0], k1);
+            }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16_16816(x[nt], k0[0], k1[0], k0[1], k1[1], q[nt][j][0], q[nt][j][1]);
-            mma_bf16_16816(x[nt], k0[2], k1[2], k0[3], k1[3], q[nt][j][2], q[nt][j][3]);
+            for (int nt = 0; nt < NT; ++nt) {
+              float d[4];
+              mma_f16_16816_z(d, k0[0], k1[0], k0[1], k1[1], q[nt][j][0], q[nt][j][1]);
+              mma_f16_16816(d, k0[2], k1[2], k0[3], k1[3], q[nt][j][2], q[nt][j][3]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(d[c], c < 2 ? f0 : f1, x[nt][c]);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kJ; ++j) {  // rare: widened to bf16 with their scale
+            uint32_t w[2][2], k0[4], k1[4], qj[NT][4];
+            const int last = bytes8<FMT>() / 4 - 1;
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < kJ; ++i) {
+              if (i != j) continue;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                w[e][0] = raw[i][e].w[0], w[e][1] = raw[i][e].w[last];
+                f[e] = e8m0_f32(sc[e][i / 4] >> 8 * (i % 4) & 0xffu);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) qj[nt][k] = q[nt][i][k];
+            }
+            mx8_bf16<FMT>(w[0][0], w[0][1], f[0], k0);
+            mx8_bf16<FMT>(w[1][0], w[1][1], f[1], k1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_bf16_16816(x[nt], k0[0], k1[0], k0[1], k1[1], qj[nt][0], qj[nt][1]);
+              mma_bf16_16816(x[nt], k0[2], k1[2], k0[3], k1[3], qj[nt][2], qj[nt][3]);
+            }
           }
         }
       }
@@ -211,7 +328,7 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float y = fmaf(x[nt][c], p.scale, -lse[nt][c & 1]) * 1.4426950408889634f;
+          const float y = fmaf(x[nt][c], scale[nt][c & 1], -lse[nt][c & 1]) * 1.4426950408889634f;
           sum[c >> 1] += live[nt][c & 1] ? ex2(y) : 0.f;
         }
 #pragma unroll

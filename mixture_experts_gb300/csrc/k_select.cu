@@ -8,8 +8,8 @@
 // heads its columns, the bounds come from memory straight into the operand's registers: a lane's
 // 16 bytes are elements 8t .. + 7 of every 32 on both operands). A third product, |q| with
 // the larger magnitude, says how far the fp32 sums may be off: 8 x 2^-24 of the sum
-// of magnitudes an instruction, 32 of them for heads of 256: 2^-16. fp32 caches: plain
-// FMAs, chains of at most 24 roundings: 2^-18.
+// of magnitudes an instruction, DP / 8 of them a score. fp32 caches: plain FMAs, chains of at
+// most 24 roundings: 2^-18.
 // k_page_pick: a block a (sequence, key head) finds the keep-th largest score T. Scores further
 // than twice the largest error from T are settled; where the others are not just as many
 // as are still wanted, they are computed again in fp64 and ranked by that.
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_page_scores(const ScoreArg
       for (int c = 0; c < 4; ++c) {
         if (nt * 8 + 2 * t + (c & 1) >= group) continue;
         best[c >> 1] = fmaxf(best[c >> 1], x[c]);
-        off[c >> 1] = fmaxf(off[c >> 1], score_error(x[c], m[c], 0x1p-16f));
+        off[c >> 1] = fmaxf(off[c >> 1], score_error(x[c], m[c], DP / 8 * 0x1p-21f));
       }
     }
 #pragma unroll
@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_page_scores_f32(const Scor
   }
 }
 
-constexpr int kPickThreads = 256, kList = 1024;
+constexpr int kList = 1024, kFew = 256;
+constexpr int kMostCached = 160 * 1024;  // bytes of keys that shared memory holds
 
 // The score of a page in fp64 (a warp; every lane gets it).
 template <class T>
@@ -180,14 +181,26 @@ COLI_DEV double score64(const SelectArgs& p, int b, int h, int page) {
   const T* box =
       static_cast<const T*>(p.bounds) + (static_cast<size_t>(page) * p.c.n_heads + h) * 2 * D;
   const T* q = static_cast<const T*>(p.q) + b * p.q_stride + static_cast<size_t>(h) * group * D;
+  float lo[8], hi[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int d = k * 32 + static_cast<int>(lane_id());
+    lo[k] = d < D ? to_f32(box[d]) : 0.f;
+    hi[k] = d < D ? to_f32(box[D + d]) : 0.f;
+  }
   double best = -INFINITY;
   bool nan = false;
   for (int r = 0; r < group; ++r) {
-    double x = 0.;
-    for (int d = lane_id(); d < D; d += 32) {
-      const float v = to_f32(q[static_cast<size_t>(r) * D + d]);
-      if (v != 0.f) x = fma(double(v), double(to_f32(v > 0.f ? box[D + d] : box[d])), x);
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int d = k * 32 + static_cast<int>(lane_id());
+      v[k] = d < D ? to_f32(q[static_cast<size_t>(r) * D + d]) : 0.f;
     }
+    double x = 0.;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k * 32 < D && v[k] != 0.f) x = fma(double(v[k]), double(v[k] > 0.f ? hi[k] : lo[k]), x);
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
     nan |= x != x;
@@ -200,10 +213,12 @@ COLI_DEV double score64(const SelectArgs& p, int b, int h, int page) {
   return best;
 }
 
-template <class T>
+template <class T, int kPickThreads, bool CACHED>
 __global__ void __launch_bounds__(kPickThreads) k_page_pick(const SelectArgs p) {
+  extern __shared__ uint32_t s_keys[];
   __shared__ PickShared s;
   __shared__ int s_list[kList], s_n;
+  __shared__ double s_exact[kFew];
   __shared__ float s_off[kPickThreads / 32];
   const int b = blockIdx.x / p.c.n_heads, h = blockIdx.x - b * p.c.n_heads;
   const int lane = lane_id(), w = threadIdx.x / 32, page = p.c.page_size;
@@ -220,14 +235,36 @@ __global__ void __launch_bounds__(kPickThreads) k_page_pick(const SelectArgs p) 
   float2* row = p.scores + static_cast<size_t>(blockIdx.x) * p.max_pages;
   auto forced = [&](int i) { return i < p.first || i >= n - p.last; };
   auto put = [&](int r, int i) { out[r] = __ldg(table + i); };
-  auto key = [&](int i) { return forced(i) ? 0xffffffffu : order_key(row[i].x); };
-  // T and the largest error
+  // ordered scores, four loads in flight, and the largest error
   float off = 0.f;
-  for (int i = threadIdx.x; i < n; i += kPickThreads)
-    if (!forced(i)) off = fmaxf(off, row[i].y);
+  constexpr int kDeep = 4;
+  for (int i0 = threadIdx.x; i0 < n; i0 += kPickThreads * kDeep) {
+    float2 v[kDeep];
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const int i = i0 + e * kPickThreads;
+      v[e] = i < n ? row[i] : make_float2(0.f, 0.f);
+    }
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const int i = i0 + e * kPickThreads;
+      if (i >= n) break;
+      if (!forced(i)) off = fmaxf(off, v[e].y);
+      if constexpr (CACHED) s_keys[i] = forced(i) ? 0xffffffffu : order_key(v[e].x);
+    }
+  }
+  auto key = [&](int i) {
+    if constexpr (CACHED) return s_keys[i];
+    return forced(i) ? 0xffffffffu : order_key(row[i].x);
+  };
+  auto score = [&](int i) {  // of a page that is not forced (NaN: -infinity; all are open then)
+    const uint32_t k = key(i);
+    return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k);
+  };
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) off = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, k));
   if (lane == 0) s_off[w] = off;
+  __syncthreads();
   const Cut<uint32_t> cut = radix_cut<kPickThreads, false, uint32_t>(n, p.keep, key, s);
 #pragma unroll
   for (int k = 0; k < kPickThreads / 32; ++k) off = fmaxf(off, s_off[k]);
@@ -238,9 +275,11 @@ __global__ void __launch_bounds__(kPickThreads) k_page_pick(const SelectArgs p) 
   const float at = __uint_as_float(cut.from >> 31 ? cut.from ^ 0x80000000u : ~cut.from);
   const float over = __fadd_ru(at, 2.f * off), under = __fadd_rd(at, -2.f * off);
   // scores that are neither surely chosen nor surely not
-  auto open = [&](int i) { return !forced(i) && !(row[i].x > over) && !(row[i].x < under); };
+  auto open = [&](int i) {
+    return !forced(i) && !(score(i) > over) && !(score(i) < under);
+  };
   int mine = 0;  // all but the surely left out
-  for (int i = threadIdx.x; i < n; i += kPickThreads) mine += forced(i) || !(row[i].x < under);
+  for (int i = threadIdx.x; i < n; i += kPickThreads) mine += forced(i) || !(score(i) < under);
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, k);
   if (lane == 0) s.warp[0][w] = mine;
@@ -253,7 +292,36 @@ __global__ void __launch_bounds__(kPickThreads) k_page_pick(const SelectArgs p) 
     chosen<kPickThreads, uint32_t>(n, Cut<uint32_t>{order_key(under), n}, key, put, s);
     return;
   }
-  // the open ones in fp64, in the scores' place: +-infinity for the others
+  // Few are open: they are ranked in fp64 by themselves, and their keys say who is chosen.
+  if constexpr (CACHED) {
+    if (threadIdx.x == 0) s_n = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kPickThreads)
+      if (open(i)) {
+        const int e = atomicAdd(&s_n, 1);
+        if (e < kFew) s_list[e] = i;
+      }
+    __syncthreads();
+    const int m = s_n;
+    if (m <= kFew) {
+      for (int e = w; e < m; e += kPickThreads / 32) {
+        const double x = score64<T>(p, b, h, __ldg(table + s_list[e]));
+        if (lane == 0) s_exact[e] = x != x ? -INFINITY : x;
+      }
+      __syncthreads();
+      const int left = p.keep - (within - m);  // places for them
+      for (int e = threadIdx.x; e < m; e += kPickThreads) {
+        int better = 0;
+        for (int k = 0; k < m; ++k)
+          better += s_exact[k] > s_exact[e] || (s_exact[k] == s_exact[e] && s_list[k] < s_list[e]);
+        s_keys[s_list[e]] = better < left ? 0xffffffffu : 0u;
+      }
+      __syncthreads();
+      chosen<kPickThreads, uint32_t>(n, Cut<uint32_t>{order_key(over), 0}, key, put, s);
+      return;
+    }
+  }
+  // Else the open ones in fp64 in the scores' place, +-infinity for the others, and all are ranked.
   double* exact = reinterpret_cast<double*>(row);
   for (int i0 = 0; i0 < n; i0 += kList) {
     if (threadIdx.x == 0) s_n = 0;
@@ -262,7 +330,7 @@ __global__ void __launch_bounds__(kPickThreads) k_page_pick(const SelectArgs p) 
       if (open(i))
         s_list[atomicAdd(&s_n, 1)] = i;
       else
-        exact[i] = forced(i) || row[i].x > over ? INFINITY : -INFINITY;
+        exact[i] = forced(i) || score(i) > over ? INFINITY : -INFINITY;
     }
     __syncthreads();
     for (int e = w; e < s_n; e += kPickThreads / 32) {
@@ -274,6 +342,25 @@ __global__ void __launch_bounds__(kPickThreads) k_page_pick(const SelectArgs p) 
   auto key64 = [&](int i) { return forced(i) ? ~0ull : order_key(exact[i]); };
   const Cut<uint64_t> cut64 = radix_cut<kPickThreads, true, uint64_t>(n, p.keep, key64, s);
   chosen<kPickThreads, uint64_t>(n, cut64, key64, put, s);
+}
+
+template <class T, int THREADS, bool CACHED>
+cudaError_t pick_with(const SelectArgs& a, size_t smem, cudaStream_t st) {
+  if (CACHED && smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_page_pick<T, THREADS, CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostCached);
+    if (e != cudaSuccess) return e;
+  }
+  k_page_pick<T, THREADS, CACHED><<<a.B * a.c.n_heads, THREADS, smem, st>>>(a);
+  return cudaGetLastError();
+}
+// Long lists by 1024 threads; what shared memory does not hold is read again from memory.
+template <class T>
+cudaError_t launch_pick(const SelectArgs& a, cudaStream_t st) {
+  const size_t keys = static_cast<size_t>(a.max_pages) * 4;
+  if (keys > kMostCached) return pick_with<T, 1024, false>(a, 0, st);
+  if (a.max_pages > 4096) return pick_with<T, 1024, true>(a, keys, st);
+  return pick_with<T, 256, true>(a, keys, st);
 }
 
 }  // namespace
@@ -298,11 +385,7 @@ cudaError_t launch_select_pages(const SelectArgs& a, cudaStream_t st) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (a.c.dtype == DT_F32)
-    k_page_pick<float><<<rows, kPickThreads, 0, st>>>(a);
-  else
-    k_page_pick<__nv_bfloat16><<<rows, kPickThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return a.c.dtype == DT_F32 ? launch_pick<float>(a, st) : launch_pick<__nv_bfloat16>(a, st);
 }
 
 }  // namespace coli

@@ -31,6 +31,7 @@ constexpr int kJoinWarps = 8;
 template <class T>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const JoinArgs p) {
   const int row = blockIdx.x * kJoinWarps + threadIdx.x / 32, lane = lane_id();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= p.rows) return;
   const int b = row / p.heads, hq = row - b * p.heads;
   size_t first = row;  // part i: row first + i * step
@@ -44,14 +45,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const JoinArgs 
     step = p.seg_rows;
   }
   const float2 own = p.own_ml[row];
-  float top = own.x;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.ml[first + static_cast<size_t>(i) * step].x);
+  float top = own.x, l = 0.f;
+  // (m, l) of up to 32 parts at once, a part a lane
+  auto part = [&](int i) {
+    return i < n ? p.ml[first + static_cast<size_t>(i) * step] : make_float2(-FLT_MAX, 0.f);
+  };
+  const float2 mine = part(lane);
+  top = fmaxf(top, mine.x);
+  for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, part(i).x);
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
   const float w0 = own.y * ex2(own.x - top);
-  float l = 0.f;
-  for (int i = lane; i < n; i += 32) {
-    const float2 v = p.ml[first + static_cast<size_t>(i) * step];
+  l = mine.y * ex2(mine.x - top);
+  for (int i = lane + 32; i < n; i += 32) {
+    const float2 v = part(i);
     l += v.y * ex2(v.x - top);
   }
 #pragma unroll
@@ -68,33 +75,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const JoinArgs 
       o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y);
       o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
     };
+    const float4 last =
+        in ? *reinterpret_cast<const float4*>(p.own + static_cast<size_t>(row) * p.D + d) : zero;
     for (int i0 = 0; i0 < n; i0 += 32) {
-      float w = 0.f;
-      if (i0 + lane < n) {
-        const float2 v = p.ml[first + static_cast<size_t>(i0 + lane) * step];
-        w = v.y * ex2(v.x - top);
-      }
-      constexpr int kDeep = 4;
+      const float2 ml = i0 == 0 ? mine : part(i0 + lane);
+      const float w = ml.y * ex2(ml.x - top);
+      constexpr int kDeep = 8;  // loads in flight
       const int i1 = min(n - i0, 32);
       for (int i = 0; i < i1; i += kDeep) {
         float4 v[kDeep];
-        float f[kDeep];
 #pragma unroll
-        for (int e = 0; e < kDeep; ++e) {
-          f[e] = __shfl_sync(0xffffffffu, w, min(i + e, 31));
-          if (i + e >= i1) f[e] = 0.f;
-          v[e] = in && f[e] != 0.f
+        for (int e = 0; e < kDeep; ++e)
+          v[e] = in && i + e < i1
                      ? *reinterpret_cast<const float4*>(
                            p.mean + (first + static_cast<size_t>(i0 + i + e) * step) * p.D + d)
                      : zero;
-        }
 #pragma unroll
-        for (int e = 0; e < kDeep; ++e)
-          if (f[e] != 0.f) add(v[e], f[e]);
+        for (int e = 0; e < kDeep; ++e) {
+          // (a part without weight may hold anything)
+          const float f = i + e < i1 ? __shfl_sync(0xffffffffu, w, i + e) : 0.f;
+          if (f != 0.f) add(v[e], f);
+        }
       }
     }
-    if (w0 != 0.f && in)
-      add(*reinterpret_cast<const float4*>(p.own + static_cast<size_t>(row) * p.D + d), w0);
+    if (w0 != 0.f) add(last, w0);
     if (!in) continue;
     if constexpr (sizeof(T) == 4)
       *reinterpret_cast<float4*>(out + d) = o;
@@ -164,6 +168,7 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
   JoinArgs j{own_mean, own_ml, mean, ml, 0, 0, 0, 0, group, a.out, a.lse, a.out_stride, rows, heads,
              c.head_dim};
   a.raw = 1;
+  a.fine = 1;
   a.out_stride = static_cast<size_t>(heads) * c.head_dim;
   cudaError_t e;
   if (on_tensor_cores(c, B * group)) {
@@ -211,12 +216,18 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
   a.lse = reinterpret_cast<float*>(own_ml);
   e = launch_paged_attention(a, st);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (rows + kJoinWarps - 1) / kJoinWarps;
-  if (c.dtype == DT_F32)
-    k_shared_join<float><<<grid, kJoinWarps * 32, 0, st>>>(j);
-  else
-    k_shared_join<__nv_bfloat16><<<grid, kJoinWarps * 32, 0, st>>>(j);
-  return cudaGetLastError();
+  // its blocks are placed while the kernel before drains, and wait for its end
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((rows + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return c.dtype == DT_F32 ? cudaLaunchKernelEx(&cfg, k_shared_join<float>, j)
+                           : cudaLaunchKernelEx(&cfg, k_shared_join<__nv_bfloat16>, j);
 }
 
 }  // namespace coli

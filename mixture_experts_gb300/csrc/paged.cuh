@@ -462,7 +462,9 @@ __device__ __noinline__ void plain_tiles(const PagedArgs a, int group, int b, in
     }
 }
 
-template <int FMT, int DP, int NT>
+// FINE (fp32): the tensor core's sums, which it cuts to 24 bits at every step, are short ones
+// that are added up in fp32 as it should be: four times as exact.
+template <int FMT, int DP, int NT, bool FINE = false>
 __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT>::kPerSm)
     k_paged(const Params p) {
   using C = Cfg<FMT, DP, NT>;
@@ -942,11 +944,18 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
               }
               mma_tf32_1688(d, lo, qh);
               mma_tf32_1688(d, hi, ql);
+              if constexpr (FINE) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  x[i][0][c] = j == 0 ? d[c] : x[i][0][c] + d[c];
+                  d[c] = 0.f;
+                }
+              }
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              x[i][0][c] = d[c];
-              nan |= d[c] != d[c];
+              if constexpr (!FINE) x[i][0][c] = d[c];
+              nan |= x[i][0][c] != x[i][0][c];
             }
             if (!__any_sync(0xffffffffu, nan)) break;
           }
@@ -1206,10 +1215,16 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
                   float ph[2], plo[2];
                   split_tf32(pf[nt][2 * s], &ph[0], &plo[0]);
                   split_tf32(pf[nt][2 * s + 1], &ph[1], &plo[1]);
-                  float(&d)[4] = acc[v * 4 + hf * 2 + i][nt];
+                  float(&sum)[4] = acc[v * 4 + hf * 2 + i][nt];
+                  float part[4] = {0.f, 0.f, 0.f, 0.f};
+                  float(&d)[4] = FINE ? part : sum;
                   mma_tf32_1688(d, lo, ph);
                   mma_tf32_1688(d, hi, plo);
                   mma_tf32_1688(d, hi, ph);
+                  if constexpr (FINE) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sum[c] += part[c];
+                  }
                 }
               }
             }

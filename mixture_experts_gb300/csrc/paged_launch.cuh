@@ -7,7 +7,7 @@ namespace coli {
 namespace paged {
 
 
-template <int FMT, int DP, int NT>
+template <int FMT, int DP, int NT, bool FINE = false>
 cudaError_t launch_main(const Params& p, int grid, cudaStream_t st) {
   using C = Cfg<FMT, DP, NT>;
   static bool ready[128] = {};  // the shared-memory limit is raised once per device
@@ -15,12 +15,12 @@ cudaError_t launch_main(const Params& p, int grid, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 128 || !ready[dev]) {
-    e = cudaFuncSetAttribute(k_paged<FMT, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(k_paged<FMT, DP, NT, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) ready[dev] = true;
   }
-  k_paged<FMT, DP, NT><<<grid, C::kWarps * 32, C::kSmem, st>>>(p);
+  k_paged<FMT, DP, NT, FINE><<<grid, C::kWarps * 32, C::kSmem, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -29,6 +29,11 @@ cudaError_t launch_main(const Params& p, int grid, cudaStream_t st) {
 // column tiles where the registers hold them.
 template <int FMT>
 cudaError_t launch_format(const Params& p, int dp, int nt, int grid, cudaStream_t st) {
+  if constexpr (FMT == DT_F32)
+    if (p.a.fine)
+      return dp == 64    ? launch_main<FMT, 64, 1, true>(p, grid, st)
+             : dp == 128 ? launch_main<FMT, 128, 1, true>(p, grid, st)
+                         : launch_main<FMT, 256, 1, true>(p, grid, st);
   if (dp == 64) {
     if constexpr (FMT != DT_F32)
       if (nt == 2) return launch_main<FMT, 64, 2>(p, grid, st);
