@@ -80,6 +80,7 @@ struct PagedArgs {
                     // have `fold` heads each: q, out and lse are [..][n_kv_heads * fold]
   int raw;          // 1: out is fp32 and lse float2 pairs (m, l): the row's weights are
                     // 2^(x - m) and sum to l, out is their mean
+  int overlap;      // 1: the kernel before in the stream lets this one start beside it
   int fine;         // 1, fp32 caches: the sums in short pieces (see k_paged)
 };
 size_t paged_scratch_bytes(const KvView& c, int B, int n_q_heads);

@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
   const int warp = threadIdx.x / 32, lane = lane_id();
   const int D = p.c.head_dim;
 
+  asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
     // TMA: the bytes announced, the edge by hand; MX: the warps that widen
     constexpr int kFull = FMT == DT_BF16 ? 2 : kConvWarps;

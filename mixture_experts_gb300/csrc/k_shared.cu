@@ -199,6 +199,7 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
     j.row_tiles = p.row_tiles;
     j.seg_rows = seg_rows;
     e = launch_prefix(p, grid, st);
+    a.overlap = 1;  // the own tokens need none of its results
   } else {
     PagedArgs f = a;
     f.out = mean;

@@ -567,7 +567,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       for (int i = threadIdx.x; i < a.n_q_heads; i += W * 32)
         store_lse(a, a.n_q_heads, e, 0, i, -FLT_MAX, 0.f);
   }
-  if (u0 >= total) return;
+  // launched while the kernel before still runs: this one's end has to imply that one's
+  auto end = [&]() {
+    if (a.overlap) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
+  if (u0 >= total) return end();
 
   const int D = a.c.head_dim;
   const uint32_t ring = smem_u32(smem) + w * (C::kRing * C::kSlot);
@@ -726,7 +730,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       issue(i, Values());
     }
   };
-  if (x0 + (u1 - u) <= C::kOpen) return;  // nothing but empty places
+  if (x0 + (u1 - u) <= C::kOpen) return end();  // nothing but empty places
   begin();
   while (true) {
     float acc[DP / 16][NT][4], m[NT][2], l[NT][2];
@@ -1565,6 +1569,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     }
     if (!more) break;
   }
+  end();
 }
 
 }  // namespace paged

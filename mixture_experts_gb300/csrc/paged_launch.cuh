@@ -20,8 +20,17 @@ cudaError_t launch_main(const Params& p, int grid, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) ready[dev] = true;
   }
-  k_paged<FMT, DP, NT, FINE><<<grid, C::kWarps * 32, C::kSmem, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::kWarps * 32);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.a.overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_paged<FMT, DP, NT, FINE>, p);
 }
 
 // Head sizes run on the next of 64, 128, 256 (a smaller head's missing elements
