@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_page_bounds(const BoundsArgs p)
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) {
           const int at = min(r + e * S, fill - 1);  // past the end: the last row again
-          raw[e] = ldg_stream(src + static_cast<size_t>(at) * p.c.row_bytes);
-          s[e] = kMx ? __ldg(sc + at * p.c.scale_stride) : 0;
+          raw[e] = ldg_stream(src + static_cast<uint32_t>(at * p.c.row_bytes));
+          s[e] = kMx ? __ldg(sc + static_cast<uint32_t>(at * p.c.scale_stride)) : 0;
         }
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) {

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
   const int32_t* table = p.block_table + static_cast<size_t>(b) * p.max_pages;
   const int tiles = (len + kTile - 1) / kTile, per_page = page_size / kTile;
   const int t0 = start / kTile + chunk * kMassWarps + w, step = a.chunks * kMassWarps;
-  if (t0 >= tiles) return;
+  if (t0 >= tiles) return;  // (tile numbers stay below 2^28, and steps far below that)
 
   for (int r0 = 0; r0 < group; r0 += 8 * NT) {
     // head r0 + 8 nt + g's elements; scales and lse of heads 2t, 2t + 1
@@ -163,14 +163,27 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
       size_t row;
       bool in;
     };
-    auto page_of = [&](int tile) { return tile < tiles ? __ldg(table + tile / per_page) : 0; };
-    auto fetch = [&](Keys& k, int tile, int page) {
-      k.in = tile < tiles && page >= 0 && page < p.c.n_pages;
+    // the tile whose page is looked up next: its number, page in the table, place in it
+    int next = t0, next_pi = t0 / per_page, next_sub = t0 - next_pi * per_page;
+    const int step_pi = step / per_page, step_sub = step - step_pi * per_page;
+    struct Spot {
+      int tile, page, sub;
+    };
+    auto look_up = [&]() {
+      const Spot s{next, next < tiles ? __ldg(table + next_pi) : 0, next_sub};
+      next = next < tiles ? next + step : next;
+      next_pi += step_pi;
+      next_sub += step_sub;
+      if (next_sub >= per_page) next_sub -= per_page, ++next_pi;
+      return s;
+    };
+    auto fetch = [&](Keys& k, const Spot& s) {
+      k.in = s.tile < tiles && s.page >= 0 && s.page < p.c.n_pages;
       if (!k.in) {
-        if (tile < tiles && lane == 0) latch_error(p.status, kErrDevice);
+        if (s.tile < tiles && lane == 0) latch_error(p.status, kErrDevice);
         return;
       }
-      k.row = kv_row(p.c, page, h, tile % per_page * kTile);
+      k.row = kv_row(p.c, s.page, h, s.sub * kTile);
       const char* src = p.c.k + (k.row + g) * p.c.row_bytes + t * bytes8<FMT>();
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
@@ -193,21 +206,20 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
       }
     };
     Keys ahead;
-    int page = page_of(t0);
+    Spot spot = look_up();
     if constexpr (kMx) {
-      fetch(ahead, t0, page);
-      page = page_of(t0 + step);
+      fetch(ahead, spot);
+      spot = look_up();
     }
     for (int tile = t0; tile < tiles; tile += step) {
       Keys now;
       if constexpr (kMx) {
         now = ahead;
-        fetch(ahead, tile + step, page);
-        page = page_of(tile + 2 * step);
+        fetch(ahead, spot);
       } else {
-        fetch(now, tile, page);
-        page = page_of(tile + step);
+        fetch(now, spot);
       }
+      spot = look_up();
       if (!now.in) continue;
       auto& raw = now.raw;
       auto& sc = now.sc;
