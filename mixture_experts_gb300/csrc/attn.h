@@ -80,6 +80,7 @@ struct PagedArgs {
                     // have `fold` heads each: q, out and lse are [..][n_kv_heads * fold]
   int raw;          // 1: out is fp32 and lse float2 pairs (m, l): the row's weights are
                     // 2^(x - m) and sum to l, out is their mean
+  int may_cut;      // 1: scratch is there whatever paged_direct says
   int overlap;      // 1: the kernel before in the stream lets this one start beside it
   int fine;         // 1, fp32 caches: the sums in short pieces (see k_paged)
 };
@@ -87,6 +88,16 @@ size_t paged_scratch_bytes(const KvView& c, int B, int n_q_heads);
 bool paged_direct(const KvView& c, int max_pages);  // needs no scratch
 cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st);
 int sm_count();  // of the current device
+// Raises a kernel's dynamic shared memory limit once per device; `ready` is the kernel's own.
+template <class K>
+cudaError_t raise_shared(K* kernel, int bytes, bool (&ready)[128]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < 128 && ready[dev])) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 128) ready[dev] = true;
+  return e;
+}
 
 // ---- attention behind a shared prefix ------------------------------------------------
 struct SharedArgs {

@@ -41,26 +41,29 @@ __global__ void __launch_bounds__(THREADS) k_evict_pick(const EvictArgs p) {
     }
     return order_key(__ldg(p.mass + kv_row(p.c, at, h, i - pi * page)));
   };
-  if constexpr (CACHED) {  // eight in flight: a page's number, then the mass
-    constexpr int kDeep = 8;
+  if constexpr (CACHED) {  // sixteen or eight in flight: a page's number, then the mass
+    constexpr int kDeep = THREADS == 1024 ? 16 : 8;
     const uint32_t per = 0xffffffffu / page + 1;  // i / page = i * per / 2^32, or one less
+    auto page_in_table = [&](int i) {
+      const int pi = __umulhi(i, per);
+      return pi * page > i ? pi - 1 : pi;
+    };
     for (int i0 = threadIdx.x; i0 < n; i0 += THREADS * kDeep) {
-      int row[kDeep], off[kDeep];
+      int row[kDeep];
       float m[kDeep];
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
         const int i = i0 + e * THREADS;
-        int pi = __umulhi(i, per);
-        if (pi * page > i) --pi;
-        off[e] = i - pi * page;
-        row[e] = i < n ? __ldg(table + pi) : 0;
+        row[e] = i < n ? __ldg(table + page_in_table(i)) : 0;
       }
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
+        const int i = i0 + e * THREADS;
         const bool in = row[e] >= 0 && row[e] < p.c.n_pages;
         if (!in) latch_error(p.status, kErrDevice);
-        m[e] = in && i0 + e * THREADS < n ? __ldg(p.mass + kv_row(p.c, row[e], h, off[e]))
-                                          : -INFINITY;
+        m[e] = in && i < n
+                   ? __ldg(p.mass + kv_row(p.c, row[e], h, i - page_in_table(i) * page))
+                   : -INFINITY;
       }
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
@@ -197,9 +200,9 @@ __global__ void __launch_bounds__(kCopyThreads) k_evict_pack(const EvictArgs p, 
 
 template <int THREADS, bool CACHED>
 cudaError_t launch_pick(const EvictArgs& a, size_t smem, cudaStream_t st) {
-  if (CACHED) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_evict_pick<THREADS, CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostCached);
+  static bool ready[128] = {};
+  if (CACHED && smem > 32 * 1024) {
+    const cudaError_t e = raise_shared(k_evict_pick<THREADS, CACHED>, kMostCached, ready);
     if (e != cudaSuccess) return e;
   }
   k_evict_pick<THREADS, CACHED><<<a.B * a.c.n_heads, THREADS, smem, st>>>(a);

@@ -231,6 +231,12 @@ cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
   p.direct = paged_direct(a.c, a.max_pages) ||
              (static_cast<int64_t>(a.max_pages) * a.c.page_size <= 2 * COLI_PAGED_DIRECT_TOKENS &&
               segments >= most);
+  // A caller that has the scratch in any case: too few segments for the GPU are cut from the
+  // lengths on where the table above has it faster.
+  const int64_t tokens = static_cast<int64_t>(a.max_pages) * a.c.page_size;
+  if (a.may_cut && segments < most &&
+      tokens >= (a.c.dtype == DT_F32 ? 192 : a.c.dtype == DT_BF16 ? 512 : 320))
+    p.direct = 0;
   const int grid = p.direct ? static_cast<int>(segments)
                             : (pieces < most ? static_cast<int>(pieces) : most);
   cudaError_t e;

@@ -702,16 +702,9 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
 
 template <int FMT, int DP, bool PAIR>
 cudaError_t launch(const PrefixArgs& p, int grid, cudaStream_t st) {
-  static bool ready[128] = {};  // the shared-memory limit is raised once per device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static bool ready[128] = {};
+  cudaError_t e = raise_shared(k_prefix<FMT, DP, PAIR>, smem_bytes<FMT, DP, PAIR>(), ready);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 128 || !ready[dev]) {
-    e = cudaFuncSetAttribute(k_prefix<FMT, DP, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem_bytes<FMT, DP, PAIR>());
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 128) ready[dev] = true;
-  }
   PrefixMaps maps{};
   auto encode = [&](CUtensorMap* m, const void* pool, int rows) {
     if (e != cudaSuccess) return;

@@ -170,55 +170,65 @@ __global__ void __launch_bounds__(kScoreWarps * 32) k_page_scores_f32(const Scor
   }
 }
 
-constexpr int kList = 1024, kFew = 256;
+constexpr int kFew = 256;  // pages ranked at once
 constexpr int kMostCached = 160 * 1024;  // bytes of keys that shared memory holds
 
-// The score of a page in fp64 (a warp; every lane gets it).
+// The score of head r of the group in a page, in fp64 (a warp; every lane gets it).
 template <class T>
-COLI_DEV double score64(const SelectArgs& p, int b, int h, int page) {
+COLI_DEV double score64(const SelectArgs& p, int b, int h, int r, int page) {
   const int D = p.c.head_dim, group = p.n_q_heads / p.c.n_heads;
   if (page < 0 || page >= p.c.n_pages) return -INFINITY;
   const T* box =
       static_cast<const T*>(p.bounds) + (static_cast<size_t>(page) * p.c.n_heads + h) * 2 * D;
-  const T* q = static_cast<const T*>(p.q) + b * p.q_stride + static_cast<size_t>(h) * group * D;
-  float lo[8], hi[8];
+  const T* q = static_cast<const T*>(p.q) + b * p.q_stride + static_cast<size_t>(h * group + r) * D;
+  float v[8], to[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int d = k * 32 + static_cast<int>(lane_id());
-    lo[k] = d < D ? to_f32(box[d]) : 0.f;
-    hi[k] = d < D ? to_f32(box[D + d]) : 0.f;
+    v[k] = d < D ? to_f32(q[d]) : 0.f;
+    const float lo = d < D ? to_f32(box[d]) : 0.f, hi = d < D ? to_f32(box[D + d]) : 0.f;
+    to[k] = v[k] > 0.f ? hi : lo;
   }
-  double best = -INFINITY;
-  bool nan = false;
-  for (int r = 0; r < group; ++r) {
-    float v[8];
+  double x = 0.;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int d = k * 32 + static_cast<int>(lane_id());
-      v[k] = d < D ? to_f32(q[static_cast<size_t>(r) * D + d]) : 0.f;
+  for (int k = 0; k < 8; ++k)
+    if (k * 32 < D && v[k] != 0.f) x = fma(double(v[k]), double(to[k]), x);
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+  return x;
+}
+
+// The listed pages' scores as ordered keys, a warp a page and head; those with a NaN: -infinity.
+template <class T, int THREADS>
+COLI_DEV void exact_scores(const SelectArgs& p, int b, int h, const int32_t* table,
+                           const int* list, int m, unsigned long long* keys, int* nan) {
+  const int group = p.n_q_heads / p.c.n_heads;
+  for (int e = threadIdx.x; e < m; e += THREADS) keys[e] = 0, nan[e] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x / 32; i < m * group; i += THREADS / 32) {
+    const int e = i / group;
+    const double x = score64<T>(p, b, h, i - e * group, __ldg(table + list[e]));
+    if (lane_id() != 0) continue;
+    if (x != x) {
+      nan[e] = 1;
+      latch_error(p.status, kErrDevice);
+    } else {
+      atomicMax(&keys[e], static_cast<unsigned long long>(order_key(x)));
     }
-    double x = 0.;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k * 32 < D && v[k] != 0.f) x = fma(double(v[k]), double(v[k] > 0.f ? hi[k] : lo[k]), x);
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-    nan |= x != x;
-    best = fmax(best, x);
   }
-  if (nan) {
-    latch_error(p.status, kErrDevice);
-    return -INFINITY;
-  }
-  return best;
+  __syncthreads();
+  for (int e = threadIdx.x; e < m; e += THREADS)
+    if (nan[e]) keys[e] = order_key(-double(INFINITY));
+  __syncthreads();
 }
 
 template <class T, int kPickThreads, bool CACHED>
 __global__ void __launch_bounds__(kPickThreads) k_page_pick(const SelectArgs p) {
   extern __shared__ uint32_t s_keys[];
   __shared__ PickShared s;
-  __shared__ int s_list[kList], s_n;
-  __shared__ double s_exact[kFew];
+  __shared__ int s_list[kFew], s_n;
+  __shared__ unsigned long long s_exact[kFew];
+  __shared__ int s_nan[kFew];
   __shared__ float s_off[kPickThreads / 32];
   const int b = blockIdx.x / p.c.n_heads, h = blockIdx.x - b * p.c.n_heads;
   const int lane = lane_id(), w = threadIdx.x / 32, page = p.c.page_size;
@@ -304,11 +314,7 @@ __global__ void __launch_bounds__(kPickThreads) k_page_pick(const SelectArgs p) 
     __syncthreads();
     const int m = s_n;
     if (m <= kFew) {
-      for (int e = w; e < m; e += kPickThreads / 32) {
-        const double x = score64<T>(p, b, h, __ldg(table + s_list[e]));
-        if (lane == 0) s_exact[e] = x != x ? -INFINITY : x;
-      }
-      __syncthreads();
+      exact_scores<T, kPickThreads>(p, b, h, table, s_list, m, s_exact, s_nan);
       const int left = p.keep - (within - m);  // places for them
       for (int e = threadIdx.x; e < m; e += kPickThreads) {
         int better = 0;
@@ -321,34 +327,32 @@ __global__ void __launch_bounds__(kPickThreads) k_page_pick(const SelectArgs p) 
       return;
     }
   }
-  // Else the open ones in fp64 in the scores' place, +-infinity for the others, and all are ranked.
-  double* exact = reinterpret_cast<double*>(row);
-  for (int i0 = 0; i0 < n; i0 += kList) {
+  // Else the open ones' keys go in the scores' place, +-infinity for the others, and all are ranked.
+  unsigned long long* exact = reinterpret_cast<unsigned long long*>(row);
+  for (int i0 = 0; i0 < n; i0 += kFew) {
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
-    for (int i = i0 + threadIdx.x; i < min(n, i0 + kList); i += kPickThreads) {
+    for (int i = i0 + threadIdx.x; i < min(n, i0 + kFew); i += kPickThreads) {
       if (open(i))
         s_list[atomicAdd(&s_n, 1)] = i;
       else
-        exact[i] = forced(i) || score(i) > over ? INFINITY : -INFINITY;
+        exact[i] = order_key(forced(i) || score(i) > over ? double(INFINITY) : -double(INFINITY));
     }
     __syncthreads();
-    for (int e = w; e < s_n; e += kPickThreads / 32) {
-      const double x = score64<T>(p, b, h, __ldg(table + s_list[e]));
-      if (lane == 0) exact[s_list[e]] = x;
-    }
+    exact_scores<T, kPickThreads>(p, b, h, table, s_list, s_n, s_exact, s_nan);
+    for (int e = threadIdx.x; e < s_n; e += kPickThreads) exact[s_list[e]] = s_exact[e];
     __syncthreads();
   }
-  auto key64 = [&](int i) { return forced(i) ? ~0ull : order_key(exact[i]); };
+  auto key64 = [&](int i) { return forced(i) ? ~0ull : static_cast<uint64_t>(exact[i]); };
   const Cut<uint64_t> cut64 = radix_cut<kPickThreads, true, uint64_t>(n, p.keep, key64, s);
   chosen<kPickThreads, uint64_t>(n, cut64, key64, put, s);
 }
 
 template <class T, int THREADS, bool CACHED>
 cudaError_t pick_with(const SelectArgs& a, size_t smem, cudaStream_t st) {
+  static bool ready[128] = {};
   if (CACHED && smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_page_pick<T, THREADS, CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostCached);
+    const cudaError_t e = raise_shared(k_page_pick<T, THREADS, CACHED>, kMostCached, ready);
     if (e != cudaSuccess) return e;
   }
   k_page_pick<T, THREADS, CACHED><<<a.B * a.c.n_heads, THREADS, smem, st>>>(a);

@@ -169,6 +169,7 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
              c.head_dim};
   a.raw = 1;
   a.fine = 1;
+  a.may_cut = 1;
   a.out_stride = static_cast<size_t>(heads) * c.head_dim;
   cudaError_t e;
   if (on_tensor_cores(c, B * group)) {

@@ -67,12 +67,12 @@ COLI_DEV Cut<Key> radix_cut(int n, int K, F key, PickShared& s) {
   const int lane = lane_id(), w = threadIdx.x / 32;
   Key low = kAll, top = 0;
   int sure = 0;
+#pragma unroll 4
   for (int i = threadIdx.x; i < n; i += THREADS) {
     const Key k = key(i);
     sure += k == kAll;
-    if (k == kAll) continue;
-    low = k < low ? k : low;
-    top = k > top ? k : top;
+    low = k < low ? k : low;  // (kAll, the largest, changes nothing here)
+    top = k > top && k != kAll ? k : top;
   }
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
@@ -106,6 +106,7 @@ COLI_DEV Cut<Key> radix_cut(int n, int K, F key, PickShared& s) {
     const int width = high < kDigit ? high : kDigit, shift = high - width;
     for (int i = threadIdx.x; i < kBins; i += THREADS) s.bins[i] = 0;
     __syncthreads();
+#pragma unroll 4
     for (int i = threadIdx.x; i < n; i += THREADS) {
       const Key k = key(i);
       if (k != kAll && (high >= kBits || (k >> (high & (kBits - 1))) == prefix))
@@ -163,6 +164,7 @@ COLI_DEV void chosen(int n, const Cut<Key>& cut, F key, P put, PickShared& s) {
   const int each = ((n + kW - 1) / kW + 31) / 32 * 32;  // places of a warp
   const int i0 = w * each, i1 = min(n, i0 + each);
   int over = 0, same = 0;
+#pragma unroll 4
   for (int i = i0 + lane; i < i1; i += 32) {
     const Key k = key(i);
     over += k > cut.from;
@@ -178,6 +180,7 @@ COLI_DEV void chosen(int n, const Cut<Key>& cut, F key, P put, PickShared& s) {
   // chosen above and equal ones before this warp's places
   int a = before<kW>(s.warp[0], w), b = before<kW>(s.warp[1], w);
   if (over == 0 && (same == 0 || b >= cut.equal)) return;
+#pragma unroll 2
   for (int i = i0; i < i1; i += 32) {
     const Key k = i + lane < i1 ? key(i + lane) : 0;
     const bool in = i + lane < i1;

@@ -58,6 +58,14 @@ SHARED = [  # fmt, B, hq, hk, D, page, prefix, own
     ("mxfp4", 6, 32, 2, 64, 16, 320, [5, 0, 16, 17, 1, 31]),
     ("mxfp4", 48, 16, 2, 128, 32, 1300, [b for b in range(48)]),
     ("mxfp4", 30, 12, 2, 32, 128, 901, [b for b in range(30)]),
+    # several tiles a block, blocks that end one key head's tiles and begin the next one's
+    ("bf16", 20, 32, 16, 64, 16, 3100, [b % 4 for b in range(20)]),
+    ("bf16", 160, 32, 16, 32, 48, 1400, [1] * 160),
+    ("mxfp8", 80, 32, 8, 64, 16, 3050, [b % 3 for b in range(80)]),
+    ("mxfp4", 33, 32, 32, 64, 64, 2000, [b % 3 for b in range(33)]),
+    # more segments than blocks
+    ("bf16", 20, 200, 200, 16, 16, 100, [0] * 20),
+    ("mxfp8", 150, 200, 200, 32, 16, 130, [b % 2 for b in range(150)]),
 ]
 
 
@@ -475,6 +483,187 @@ def test_evict_with_bad_pages():
                                  torch.tensor([bad], dtype=torch.int32).cuda(), 48)
         assert moe.coli_device_status() == moe.COLI_EDEVICE
         assert held.item() == (0 if bad < 0 else 48)
+
+
+def test_select_from_a_very_long_table():
+    # more pages than shared memory holds keys for, and each page many times: equal scores
+    g = ref.gen(79)
+    n_pages, count, D = 200, 45001, 64
+    cache, _, _ = ref.pool(g, "bf16", n_pages, 16, 1, D)
+    bounds = cache.new_bounds()
+    bounds.copy_(torch.randn(n_pages, 1, 2, D, generator=g).sort(2).values)
+    table = torch.randint(0, n_pages, (1, count), generator=g).int()
+    q = torch.randn(1, 3, D, generator=g).bfloat16().cuda()
+    lens = torch.tensor([count * 16 - 3], dtype=torch.int32).cuda()
+    box, qd = bounds.double().cpu(), q.double().cpu()
+    by_page = [ref.score(qd[0], box[p, 0]) for p in range(n_pages)]
+    scores = [by_page[p] for p in table[0].tolist()]
+    for keep in (3, 700, 20000):
+        got, held = cache.select_pages(q, bounds, table.cuda(), lens, keep, first=1, last=2)
+        want = [int(table[0, j]) for j in ref.largest(scores, keep, 1, 2)]
+        assert got[0, 0].tolist() == want and held.item() == keep * 16 - 3
+
+
+# ---- streams, graphs, refusals -------------------------------------------------------------------
+def all_calls(cache, q, own, lens, pre, prefix, bounds, mass, into):
+    """One of each, on what one decode step has in hand."""
+    out, lse = cache.attend_shared(q, pre, prefix, own, lens, return_lse=True)
+    cache.page_bounds(bounds, own.flatten().contiguous(),
+                      torch.full((own.numel(),), cache.page_size, dtype=torch.int32,
+                                 device="cuda"))
+    pages, held = cache.select_pages(q, bounds, own, lens, 3)
+    sparse = cache.attend_selected(q, pages, held)
+    cache.accumulate(mass, q, own, lens, lse)
+    kept, new = cache.evict(mass, own, lens, 20, recent=2, into=into)
+    return out, lse, pages, held, sparse, kept, new
+
+
+def step_inputs(fmt, B=40, hq=8, hk=2, D=64, page=16, prefix=333):
+    g = ref.gen(123)
+    n_pre = -(-prefix // page)
+    cache, _, _ = ref.pool(g, fmt, n_pre + B * 10, page, hk, D)
+    pre = torch.arange(n_pre, dtype=torch.int32).cuda()
+    ids = (n_pre + torch.randperm(B * 10, generator=g)).int()
+    own = ids[:B * 8].reshape(B, 8).contiguous().cuda()
+    into = ids[B * 8:].reshape(B, 2).contiguous().cuda()
+    lens = torch.randint(0, 129, (B,), generator=g).int().cuda()
+    q = torch.randn(B, hq, D, generator=g).to(ref.act(fmt)).cuda()
+    return cache, q, own, lens, pre, prefix, cache.new_bounds(), cache.new_mass(), into
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "f32"])
+def test_captured_and_replayed(fmt):
+    a = step_inputs(fmt)
+    cache, q, own, lens, mass = a[0], a[1], a[2], a[3], a[7]
+    pools = [x for x in (cache.k, cache.v, cache.k_scale, cache.v_scale, mass) if x is not None]
+    was = [x.clone() for x in pools]
+    all_calls(*a)                                        # kernels loaded before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = all_calls(*a)
+    for turn in range(3):
+        for x, y in zip(pools, was):
+            x.copy_(y)
+        q.copy_(torch.randn(q.shape, generator=ref.gen(turn)).to(q.dtype))
+        lens.copy_(torch.randint(0, 129, lens.shape, generator=ref.gen(turn, 1)))
+        graph.replay()
+        torch.cuda.synchronize()
+        after = [x.clone() for x in pools]
+        results = [x.clone() for x in got]
+        for x, y in zip(pools, was):
+            x.copy_(y)
+        eager = all_calls(*a)
+        for x, y in zip(results, eager):
+            assert torch.equal(x, y)
+        for x, y in zip(after, pools):
+            assert torch.equal(x, y)
+
+
+def test_two_streams_at_once():
+    a, b = step_inputs("bf16"), step_inputs("mxfp8")
+    want = [all_calls(*a), all_calls(*b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for x in (a, b):
+            x[7].zero_()
+        torch.cuda.synchronize()
+        for s, x in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                got.append(all_calls(*x))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
+STREAM_CALLS = {
+    "attend_shared": lambda c, x, t, n, s: c.attend_shared(x, t[0], 16, t, n, stream=s),
+    "select_pages": lambda c, x, t, n, s: c.select_pages(x, c.boxes, t, n, 1, first=0, stream=s),
+    "attend_selected": lambda c, x, t, n, s: c.attend_selected(
+        x, t[:, None].expand(-1, 4, -1).contiguous(), n, stream=s),
+    "accumulate": lambda c, x, t, n, s: c.accumulate(c.masses, x, t, n, c.lses, stream=s),
+}
+
+
+@pytest.mark.parametrize("name", list(STREAM_CALLS))
+def test_inputs_let_go_of_are_not_given_away(name):
+    B, h, D = 4096, 4, 64
+    c = moe.PagedKVCache.empty(B // 16, 16, h, D, moe.BF16)
+    c.boxes, c.masses = c.new_bounds(), c.new_mass()
+    c.lses = torch.zeros(B, h, device="cuda")
+    ids = (torch.arange(B, device="cuda") % 16).int()
+    table = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    STREAM_CALLS[name](c, torch.randn(B, h, D, device="cuda").bfloat16(), table, ids, None)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    x = torch.ones(B, h, D, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)            # the call waits some 50 ms for its turn
+    STREAM_CALLS[name](c, x, table, ids, side)
+    where = x.data_ptr()
+    del x
+    others = [torch.empty(B, h, D, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    assert all(o.data_ptr() != where for o in others)
+    assert not side.query()                       # the work was indeed still to come
+    torch.cuda.synchronize()
+
+
+def test_wrappers_refuse_what_does_not_fit():
+    cache, q, own, lens, pre, prefix, bounds, mass, into = step_inputs("bf16")
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    pages = torch.zeros(40, 2, 3, dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: cache.attend_shared(q.float(), pre, prefix, own, lens),
+        lambda: cache.attend_shared(q, pre[:5], prefix, own, lens),          # too few pages
+        lambda: cache.attend_shared(q, pre.long(), prefix, own, lens),
+        lambda: cache.attend_shared(q, pre.cpu(), prefix, own, lens),
+        lambda: cache.attend_shared(q, pre, prefix, own[:3], lens),
+        lambda: cache.attend_shared(q, pre, prefix, own, lens[:3]),
+        lambda: cache.attend_shared(q, pre, prefix, own, lens, out=q[:3]),
+        lambda: cache.page_bounds(bounds[:3], pre, pre),
+        lambda: cache.page_bounds(bounds.float(), pre, pre),
+        lambda: cache.page_bounds(bounds, pre, pre[:3]),
+        lambda: cache.page_bounds(bounds, own, own),
+        lambda: cache.select_pages(q, bounds.float(), own, lens, 3),
+        lambda: cache.select_pages(q, bounds, own.t(), lens, 3),
+        lambda: cache.select_pages(q, bounds, own, lens, 0),
+        lambda: cache.attend_selected(q, pages[:, :1], lens),
+        lambda: cache.attend_selected(q, pages[0], lens),
+        lambda: cache.attend_selected(q, pages.long(), lens),
+        lambda: cache.accumulate(mass[:3], q, own, lens, lse),
+        lambda: cache.accumulate(mass, q, own, lens, lse[:, :3]),
+        lambda: cache.accumulate(mass, q, own, lens, lse, known=lens[:3]),
+        lambda: cache.evict(mass.double(), own, lens, 20),
+        lambda: cache.evict(mass, own[0], lens, 20),
+        lambda: cache.evict(mass, own, lens, 0),
+        lambda: cache.evict(mass, own, lens, 20, into=into[:3]),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: cache.select_pages(q, bounds, own, lens, 3, first=2, last=2),
+                 lambda: cache.evict(mass, own, lens, 20, first=10, recent=11),
+                 lambda: cache.evict(mass, own, lens, 40, into=into),        # no room for 40
+                 lambda: cache.attend_shared(q, pre, -1, own, lens)):
+        with pytest.raises(moe.ColiError):
+            call()
+
+
+def test_no_sequences():
+    cache, q, own, lens, pre, prefix, bounds, mass, into = step_inputs("bf16")
+    z, zt, zl = q[:0], own[:0], lens[:0]
+    assert cache.attend_shared(z, pre, prefix, zt, zl).shape == (0, 8, 64)
+    pages, held = cache.select_pages(z, bounds, zt, zl, 3)
+    assert pages.shape == (0, 2, 3) and held.shape == (0,)
+    assert cache.attend_selected(z, pages, held).shape == (0, 8, 64)
+    cache.accumulate(mass, z, zt, zl, torch.zeros(0, 8, device="cuda"))
+    kept, new = cache.evict(mass, zt, zl, 5)
+    assert kept.shape == (0, 2, 5) and new.shape == (0,)
+    cache.page_bounds(bounds, zl, zl)
 
 
 # ---- together ------------------------------------------------------------------------------------
