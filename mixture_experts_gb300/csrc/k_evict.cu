@@ -8,7 +8,7 @@
 // keys and values and their scales and masses, 16 bytes a thread and step.
 // k_evict_pack: in place. A kept row moves to an earlier place or stays, so rows copied
 // in order, each batch read before it is written, never overwrite one that is still to be
-// read. A block takes 64 bytes of all of a head's rows (or its scales, or masses):
+// read. A block takes 128 bytes of all of a head's rows (or its scales, or masses):
 // blocks share no byte.
 #include "mx.cuh"
 #include "pick.cuh"
@@ -147,38 +147,52 @@ __global__ void __launch_bounds__(kCopyThreads) k_evict_copy(const EvictArgs p, 
   }
 }
 
-// sizeof(T) bytes a thread, `units` of them side by side from byte `off` of each
-// row of `base`.
+// Pieces of sizeof(T) bytes, `units` (a power of two up to 8) side by side from byte `off` of
+// each row of `base`, kPackRanks rows at a time: their places come a batch ahead through shared
+// memory, all pieces of a batch are read before one is written.
+constexpr int kPackRanks = 128, kSlice = 128;
+
 template <class T>
 COLI_DEV void pack_rows(const EvictArgs& p, int b, int h, char* base, int row, int off, int units) {
-  constexpr int kDeep = 4;
+  __shared__ size_t s_src[2][kPackRanks], s_dst[2][kPackRanks];
+  constexpr size_t kStay = ~size_t(0);
+  constexpr int kDeep = kPackRanks * 8 / kCopyThreads;
   const int32_t* kept = p.kept + (static_cast<size_t>(b) * p.c.n_heads + h) * p.keep;
-  const int per = kCopyThreads / units, local = threadIdx.x / units;
-  const int u = threadIdx.x - local * units;
-  for (int r0 = 0; r0 < p.keep; r0 += per * kDeep) {
+  auto places = [&](int r0, int buf) {
+    if (threadIdx.x >= kPackRanks) return;
+    const int r = r0 + threadIdx.x, from = r < p.keep ? kept[r] : -1;
+    size_t src, dst;
+    // (a row that stays is not touched)
+    const bool move = from > r && rows_of(p, b, h, from, r, &src, &dst);
+    s_src[buf][threadIdx.x] = move ? src : kStay;
+    s_dst[buf][threadIdx.x] = move ? dst : 0;
+  };
+  places(0, 0);
+  __syncthreads();
+  int buf = 0;
+  const int shift = __ffs(units) - 1, each = kPackRanks << shift;
+  for (int r0 = 0; r0 < p.keep; r0 += kPackRanks, buf ^= 1) {
     T v[kDeep];
     size_t to[kDeep];
-    bool some = false;
 #pragma unroll
     for (int e = 0; e < kDeep; ++e) {
-      const int r = r0 + e * per + local, from = local < per && r < p.keep ? kept[r] : -1;
-      size_t src, dst;
-      to[e] = ~size_t(0);
-      some |= from >= 0;
-      if (from > r && rows_of(p, b, h, from, r, &src, &dst)) {
+      const int i = threadIdx.x + e * kCopyThreads, r = i >> shift, u = i & (units - 1);
+      const size_t src = i < each ? s_src[buf][r] : kStay;
+      to[e] = kStay;
+      if (src != kStay) {
         v[e] = *reinterpret_cast<const T*>(base + src * row + off + u * sizeof(T));
-        to[e] = dst * row + off + u * sizeof(T);
+        to[e] = s_dst[buf][r] * row + off + u * sizeof(T);
       }
     }
-    const bool go = __syncthreads_or(some);
+    places(r0 + kPackRanks, buf ^ 1);
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < kDeep; ++e)
-      if (to[e] != ~size_t(0)) *reinterpret_cast<T*>(base + to[e]) = v[e];
-    if (!go) return;
-    __syncthreads();
+      if (to[e] != kStay) *reinterpret_cast<T*>(base + to[e]) = v[e];
   }
 }
 
+// Slices of kSlice bytes of the keys' rows, then of the values'; masses; scales.
 __global__ void __launch_bounds__(kCopyThreads) k_evict_pack(const EvictArgs p, int slices) {
   const int kinds = 2 * slices + 1 + (p.c.scale_stride ? 2 : 0);
   const int bh = blockIdx.x / kinds, x = blockIdx.x - bh * kinds;
@@ -186,9 +200,15 @@ __global__ void __launch_bounds__(kCopyThreads) k_evict_pack(const EvictArgs p, 
   // a sequence that is kept whole stays where it is
   if (context_len(p.seq_lens, b, p.max_pages, p.c.page_size, p.status, false) <= p.keep) return;
   if (x < 2 * slices) {
-    const int off = x % slices * 64;
-    pack_rows<uint4>(p, b, h, x < slices ? p.c.k : p.c.v, p.c.row_bytes, off,
-                     min(64, p.c.row_bytes - off) / 16);
+    // the row's last slice may be narrower: a row is a multiple of 16 bytes
+    char* base = x < slices ? p.c.k : p.c.v;
+    int off = x % slices * kSlice, left = min(kSlice, p.c.row_bytes - off);
+    for (int width = kSlice; width >= 16; width /= 2)
+      if (left & width) {
+        pack_rows<uint4>(p, b, h, base, p.c.row_bytes, off, width / 16);
+        off += width;
+        __syncthreads();
+      }
   } else if (x == 2 * slices) {
     pack_rows<uint32_t>(p, b, h, reinterpret_cast<char*>(p.mass), 4, 0, 1);
   } else {
@@ -227,7 +247,7 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
     k_evict_copy<<<static_cast<unsigned>(static_cast<int64_t>(rows) * chunks), kCopyThreads, 0,
                    st>>>(a, chunks);
   } else {
-    const int slices = (a.c.row_bytes + 63) / 64;
+    const int slices = (a.c.row_bytes + kSlice - 1) / kSlice;
     const int kinds = 2 * slices + 1 + (a.c.scale_stride ? 2 : 0);
     k_evict_pack<<<static_cast<unsigned>(static_cast<int64_t>(rows) * kinds), kCopyThreads, 0,
                    st>>>(a, slices);
