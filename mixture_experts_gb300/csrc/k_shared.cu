@@ -115,20 +115,33 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 size_t mean_bytes(const KvView& c, int64_t rows) { return align16(rows * c.head_dim * 4); }
 size_t part_bytes(const KvView& c, int64_t rows) { return mean_bytes(c, rows) + align16(rows * 8); }
 
-// Whether k_prefix takes the prefix: it serves 128 queries of a key head at the price of one
-// to 128, the decode kernel reads the prefix once for every 16. (It numbers the pool's rows in
-// 31 bits.)
+// Whether k_prefix takes the prefix: 128 queries of a key head cost it as much as one, the decode
+// kernel reads the prefix once for every 8 or 16. Behind 32768 tokens, 8 key heads, us, at 8 /
+// 16 / 24 / 64 queries of a key head: bf16 heads of 128 43 / 44 / 44 / 47 against 45 / 56 /
+// 57 / 81, MXFP8 44 / 51 / 50 / 52 against 43 / 57 / 82 / 116, MXFP4 heads of 64 42 / 42 / 42 /
+// 42 against 34 / 38 / 45 / 60; behind 1024 both are bound by the host (28 to 31). (It numbers
+// the pool's rows in 31 bits.)
 bool on_tensor_cores(const KvView& c, int rows_of_head) {
-  return c.dtype != DT_F32 && c.head_dim <= 128 && rows_of_head > 16 &&
+  return c.dtype != DT_F32 && c.head_dim <= 128 && rows_of_head > 8 &&
          static_cast<int64_t>(c.n_pages) * c.n_heads * c.page_size < INT32_MAX;
 }
 
-// Rows of a segment of k_prefix: 256 where a key head has them. With an odd number of 128-row
-// tiles half of the last one is idle; bf16 then takes 128 rows up to three tiles (a tile's time
-// is 1.2 us in pairs and 1.2 alone; MX tiles, widened once for both, TODO).
+// Rows of a segment of k_prefix: 256, two 128-row tiles that share the loads of keys and values, or
+// 128, whose two streams take the tiles by turns. Of an odd number of tiles the last pair is
+// half idle. The whole call behind 32768 tokens with 8 key heads, us, in pairs / alone:
+//   rows of a head      256          384          512          640
+//   bf16, heads of 128  71 / 75    100 / 86    113 / 121   146 / 133
+//   bf16, 64            54 / 50     81 / 67     89 / 85    118 / 104
+//   MXFP8, 128          78 / 84    109 / 112   123 / 143   157 / 173
+//   MXFP8, 64           64 / 68     97 / 93    107 / 118   143 / 144
+//   MXFP4, 128          76 / 75    106 / 100   118 / 128   153 / 154
+// A pair saves 4 us (bf16) to 20 (MX, whose tiles are widened once for both), an idle half
+// costs 20.
 int segment_rows(const KvView& c, int rows_of_head) {
   const int tiles = (rows_of_head + kPrefixRows - 1) / kPrefixRows;
-  const bool pair = tiles > 1 && (c.dtype != DT_BF16 || tiles % 2 == 0 || tiles > 4);
+  const bool mx = c.dtype != DT_BF16;
+  const bool pair =
+      tiles > 1 && (tiles % 2 == 0 ? mx || c.head_dim > 64 : tiles >= (mx ? 5 : 11));
   return pair ? 2 * kPrefixRows : kPrefixRows;
 }
 
