@@ -527,7 +527,8 @@ int coli_selected_attention(const coli_kv_cache* cache, const coli_attn_config* 
  * tokens. Tokens j >= known[b] start from 0 (a decode step passes seq_lens - 1: its
  * new token's place may hold an earlier one's mass); known NULL: all are added to.
  * A row whose lse is -inf adds nothing. Sums of one token are added in a
- * fixed order unless sequences share its page. */
+ * fixed order unless sequences share its page (in any order then, and none of
+ * them may start it from 0). */
 int coli_attention_mass(const coli_kv_cache* cache, const coli_attn_config* cfg, const void* q,
                         size_t q_stride, int32_t B, const int32_t* block_table,
                         int32_t max_pages, const int32_t* seq_lens, const float* lse,

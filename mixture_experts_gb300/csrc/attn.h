@@ -74,6 +74,8 @@ struct PagedArgs {
   float scale;
   float* scratch;
   int* status;
+  // ---- other calls than the plain decode attention; read where ext is 1
+  int ext;
   int head_tables;  // 1: block_table is [B][n_kv_heads][max_pages], pages for each key head
   int fixed_len;    // > 0: every sequence's length, seq_lens unused
   int fold;         // > 0: one sequence (B = 1) stands for several, whose queries' key heads
@@ -82,7 +84,6 @@ struct PagedArgs {
                     // 2^(x - m) and sum to l, out is their mean
   int may_cut;      // 1: scratch is there whatever paged_direct says
   int overlap;      // 1: the kernel before in the stream lets this one start beside it
-  int fine;         // 1, fp32 caches: the sums in short pieces (see k_paged)
 };
 size_t paged_scratch_bytes(const KvView& c, int B, int n_q_heads);
 bool paged_direct(const KvView& c, int max_pages);  // needs no scratch

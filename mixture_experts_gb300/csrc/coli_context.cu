@@ -178,7 +178,7 @@ int coli_selected_attention(const coli_kv_cache* cache, const coli_attn_config* 
                                lse);
   a.scratch = static_cast<float*>(scratch);
   a.head_tables = 1;
-  a.fine = 1;
+  a.ext = 1;
   return launched(launch_paged_attention(a, static_cast<cudaStream_t>(stream)),
                   "attention over chosen pages");
 }

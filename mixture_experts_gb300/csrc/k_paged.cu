@@ -15,7 +15,7 @@ namespace {
 // group y and its warps share the partials. Latency bound: 6 to 8 us by itself, of
 // which the launch lies under the main kernel (one context of 500009 tokens: 38
 // partials a segment, 7.4 us; 32 ragged contexts: 2 a segment, 6.0 us).
-template <int DP, int NT, bool F32, bool IN_ORDER>
+template <int DP, int NT, bool F32, bool IN_ORDER, bool EXT>
 __global__ void __launch_bounds__(256) k_join(const Params p) {
   constexpr int kGroups = DP / 16 * NT, kRegs = kGroups * 4;
   constexpr int kPart = kRegs * 32 + 16 * NT;
@@ -99,16 +99,16 @@ __global__ void __launch_bounds__(256) k_join(const Params p) {
     for (int c = 0; c < 2; ++c) {
       const int r = row0 + nt * 8 + 2 * t + c;
       if (r >= p.group) continue;
-      store_out<IN_ORDER, F32>(a, row_at(a, p.group, b, h, r, a.out_stride, D), i, g,
+      store_out<IN_ORDER, F32, EXT>(a, row_at<EXT>(a, p.group, b, h, r, a.out_stride, D), i, g,
                                l[c] == 0.f ? 0.f : o[c], l[c] == 0.f ? 0.f : o[c + 2]);
-      if (a.lse != nullptr && i == 0 && g == 0) store_lse(a, p.group, b, h, r, m[c], l[c]);
+      if (a.lse != nullptr && i == 0 && g == 0) store_lse<EXT>(a, p.group, b, h, r, m[c], l[c]);
     }
   }
 }
 
 // The join is launched so that its blocks may be placed while the main kernel
 // drains; they wait for its end (griddepcontrol.wait) before they read.
-template <int DP, int NT, bool F32, bool IN_ORDER>
+template <int DP, int NT, bool F32, bool IN_ORDER, bool EXT>
 cudaError_t launch_join(const Params& p, int grid, int ys, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, ys);
@@ -119,7 +119,7 @@ cudaError_t launch_join(const Params& p, int grid, int ys, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_join<DP, NT, F32, IN_ORDER>, p);
+  return cudaLaunchKernelEx(&cfg, k_join<DP, NT, F32, IN_ORDER, EXT>, p);
 }
 
 struct Form {
@@ -163,17 +163,37 @@ Form form_of(const KvView& c, int n_q_heads) {
   return f;
 }
 
-template <bool F32, bool IN_ORDER>
+template <bool F32, bool IN_ORDER, bool EXT>
 cudaError_t launch_joins(const Params& p, const Form& f, int grid, int ys, cudaStream_t st) {
   if constexpr (!F32) {
     if (f.nt == 2)
-      return f.dp == 64    ? launch_join<64, 2, F32, IN_ORDER>(p, grid, ys, st)
-             : f.dp == 128 ? launch_join<128, 2, F32, IN_ORDER>(p, grid, ys, st)
-                           : launch_join<256, 2, F32, IN_ORDER>(p, grid, ys, st);
+      return f.dp == 64    ? launch_join<64, 2, F32, IN_ORDER, EXT>(p, grid, ys, st)
+             : f.dp == 128 ? launch_join<128, 2, F32, IN_ORDER, EXT>(p, grid, ys, st)
+                           : launch_join<256, 2, F32, IN_ORDER, EXT>(p, grid, ys, st);
   }
-  if (f.dp == 64) return launch_join<64, 1, F32, IN_ORDER>(p, grid, ys, st);
-  if (f.dp == 128) return launch_join<128, 1, F32, IN_ORDER>(p, grid, ys, st);
-  return launch_join<256, 1, F32, IN_ORDER>(p, grid, ys, st);
+  if (f.dp == 64) return launch_join<64, 1, F32, IN_ORDER, EXT>(p, grid, ys, st);
+  if (f.dp == 128) return launch_join<128, 1, F32, IN_ORDER, EXT>(p, grid, ys, st);
+  return launch_join<256, 1, F32, IN_ORDER, EXT>(p, grid, ys, st);
+}
+
+template <bool EXT>
+cudaError_t run(const Params& p, const Form& f, int grid, int64_t segments, cudaStream_t st) {
+  cudaError_t e;
+  switch (p.a.c.dtype) {
+    case DT_F32: e = (EXT ? launch_f32_ext : launch_f32)(p, f.dp, f.nt, grid, st); break;
+    case DT_BF16: e = (EXT ? launch_bf16_ext : launch_bf16)(p, f.dp, f.nt, grid, st); break;
+    case DT_MXFP8: e = (EXT ? launch_mxfp8_ext : launch_mxfp8)(p, f.dp, f.nt, grid, st); break;
+    default: e = (EXT ? launch_mxfp4_ext : launch_mxfp4)(p, f.dp, f.nt, grid, st); break;
+  }
+  if (e != cudaSuccess || p.direct) return e;
+  // long segments (many partials each): the warps of a block share a group
+  const int groups = f.dp / 16 * f.nt;
+  const int ys = segments * 4 < grid ? groups : 1;
+  switch (p.a.c.dtype) {
+    case DT_F32: return launch_joins<true, false, EXT>(p, f, grid, ys, st);
+    case DT_BF16: return launch_joins<false, true, EXT>(p, f, grid, ys, st);
+    default: return launch_joins<false, false, EXT>(p, f, grid, ys, st);
+  }
 }
 
 }  // namespace
@@ -234,27 +254,12 @@ cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st) {
   // A caller that has the scratch in any case: too few segments for the GPU are cut from the
   // lengths on where the table above has it faster.
   const int64_t tokens = static_cast<int64_t>(a.max_pages) * a.c.page_size;
-  if (a.may_cut && segments < most &&
+  if (a.ext && a.may_cut && segments < most &&
       tokens >= (a.c.dtype == DT_F32 ? 192 : a.c.dtype == DT_BF16 ? 512 : 320))
     p.direct = 0;
   const int grid = p.direct ? static_cast<int>(segments)
                             : (pieces < most ? static_cast<int>(pieces) : most);
-  cudaError_t e;
-  switch (a.c.dtype) {
-    case DT_F32: e = launch_f32(p, f.dp, f.nt, grid, st); break;
-    case DT_BF16: e = launch_bf16(p, f.dp, f.nt, grid, st); break;
-    case DT_MXFP8: e = launch_mxfp8(p, f.dp, f.nt, grid, st); break;
-    default: e = launch_mxfp4(p, f.dp, f.nt, grid, st); break;
-  }
-  if (e != cudaSuccess || p.direct) return e;
-  // long segments (many partials each): the warps of a block share a group
-  const int groups = f.dp / 16 * f.nt;
-  const int ys = segments * 4 < grid ? groups : 1;
-  switch (a.c.dtype) {
-    case DT_F32: return launch_joins<true, false>(p, f, grid, ys, st);
-    case DT_BF16: return launch_joins<false, true>(p, f, grid, ys, st);
-    default: return launch_joins<false, false>(p, f, grid, ys, st);
-  }
+  return a.ext ? run<true>(p, f, grid, segments, st) : run<false>(p, f, grid, segments, st);
 }
 
 }  // namespace coli

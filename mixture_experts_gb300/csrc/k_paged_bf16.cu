@@ -5,7 +5,7 @@ namespace coli {
 namespace paged {
 
 cudaError_t launch_bf16(const Params& p, int dp, int nt, int grid, cudaStream_t st) {
-  return launch_format<DT_BF16>(p, dp, nt, grid, st);
+  return launch_format<DT_BF16, false>(p, dp, nt, grid, st);
 }
 
 }  // namespace paged

@@ -5,7 +5,7 @@ namespace coli {
 namespace paged {
 
 cudaError_t launch_mxfp8(const Params& p, int dp, int nt, int grid, cudaStream_t st) {
-  return launch_format<DT_MXFP8>(p, dp, nt, grid, st);
+  return launch_format<DT_MXFP8, false>(p, dp, nt, grid, st);
 }
 
 }  // namespace paged

@@ -181,7 +181,7 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
   JoinArgs j{own_mean, own_ml, mean, ml, 0, 0, 0, 0, group, a.out, a.lse, a.out_stride, rows, heads,
              c.head_dim};
   a.raw = 1;
-  a.fine = 1;
+  a.ext = 1;
   a.may_cut = 1;
   a.out_stride = static_cast<size_t>(heads) * c.head_dim;
   cudaError_t e;

@@ -242,31 +242,38 @@ template <bool IN_ORDER>
 COLI_DEV int channel(int i, int g, int c) {
   return IN_ORDER ? i * 16 + g + (c >> 1) * 8 : (i >> 2) * 64 + g * 8 + (i & 3) * 2 + (c >> 1);
 }
+// EXT: the forms that other calls than the plain decode attention use (page lists for each key
+// head, many sequences' queries as one group, means and (m, l) pairs for a later join, a start
+// beside the kernel before). They are instantiations of their own: as branches they cost
+// the plain call 1%.
+//
 // Place of query row r of key head h of sequence b in rows of heads `width` apart, tokens
-// `stride` apart: head h group + r of the sequence, or, where a.fold sequences' queries of a key
-// head follow each other as one group, head h fold + r % fold of sequence r / fold.
+// `stride` apart: head h group + r of the sequence, or, where a.fold heads of each sequence
+// follow each other as one group, head h fold + r % fold of sequence r / fold.
+template <bool EXT>
 COLI_DEV size_t row_at(const PagedArgs& a, int group, int b, int h, int r, size_t stride,
                        int width) {
-  if (a.fold > 0) {
+  if (EXT && a.fold > 0) {
     const int s = r / a.fold;
     return s * stride + static_cast<size_t>(h * a.fold + r - s * a.fold) * width;
   }
   return b * stride + static_cast<size_t>(h * group + r) * width;
 }
 // log sum of a row's weights 2^(x - m), or with a.raw the pair (m, sum) for a later join.
+template <bool EXT>
 COLI_DEV void store_lse(const PagedArgs& a, int group, int b, int h, int r, float m, float sum) {
-  const int n = a.fold > 0 ? a.fold * a.c.n_heads : a.n_q_heads;
-  const size_t at = row_at(a, group, b, h, r, n, 1);
-  if (a.raw)
+  const int n = EXT && a.fold > 0 ? a.fold * a.c.n_heads : a.n_q_heads;
+  const size_t at = row_at<EXT>(a, group, b, h, r, n, 1);
+  if (EXT && a.raw)
     reinterpret_cast<float2*>(a.lse)[at] = make_float2(m, sum);
   else
     a.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
 }
 // Two outputs (channels of c and c + 2) of one head.
-template <bool IN_ORDER, bool F32>
+template <bool IN_ORDER, bool F32, bool EXT>
 COLI_DEV void store_out(const PagedArgs& a, size_t row, int i, int g, float y0, float y1) {
   const int d = channel<IN_ORDER>(i, g, 0), e = channel<IN_ORDER>(i, g, 2), D = a.c.head_dim;
-  if (!F32 && a.raw) {  // fp32 means, for a later join
+  if (EXT && !F32 && a.raw) {  // fp32 means, for a later join
     float* o = static_cast<float*>(a.out) + row;
     if (d < D) o[d] = y0;
     if (e < D) o[e] = y1;
@@ -338,8 +345,9 @@ COLI_DEV long long quotient(long long a, long long b) {
 }
 
 // Where the pages of a sequence's key head are listed: the sequence's row, or its own.
+template <bool EXT>
 COLI_DEV size_t table_at(const PagedArgs& a, int b, int h) {
-  const size_t row = a.head_tables ? static_cast<size_t>(b) * a.c.n_heads + h : b;
+  const size_t row = EXT && a.head_tables ? static_cast<size_t>(b) * a.c.n_heads + h : b;
   return row * a.max_pages;
 }
 
@@ -348,8 +356,9 @@ COLI_DEV size_t table_at(const PagedArgs& a, int b, int h) {
 struct Seq {
   int len, first, n;  // length, first tile, number of tiles
 };
+template <bool EXT>
 COLI_DEV Seq seq_of(const PagedArgs& a, int b, bool latch) {
-  int len = a.fixed_len > 0 ? a.fixed_len : __ldg(a.seq_lens + b);
+  int len = EXT && a.fixed_len > 0 ? a.fixed_len : __ldg(a.seq_lens + b);
   const int most = a.max_pages * a.c.page_size;
   if (len < 0 || len > most) {
     if (latch) latch_error(a.status, kErrDevice);
@@ -384,7 +393,7 @@ COLI_DEV void decode8(const KvView& c, const char* pool, const uint8_t* scales, 
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] *= f;
 }
-template <int FMT, int DP, int NT>
+template <int FMT, int DP, int NT, bool EXT>
 __device__ __noinline__ void plain_tiles(const PagedArgs a, int group, int b, int h, int row0,
                                          int start, int key_end, int tile0, int tile_end, float sl,
                                          PlainSums<DP, NT>* out) {
@@ -399,7 +408,7 @@ __device__ __noinline__ void plain_tiles(const PagedArgs a, int group, int b, in
     const int tile = tile0 + n / S * (W * S) + n % S;
     if (tile >= tile_end) break;
     const int pi = tile / tiles_per_page;
-    const int page = __ldg(a.block_table + table_at(a, b, h) + pi);
+    const int page = __ldg(a.block_table + table_at<EXT>(a, b, h) + pi);
     if (page < 0 || page >= a.c.n_pages) continue;
     const size_t at = kv_row(a.c, page, h, (tile - pi * tiles_per_page) * kTile);
     const int r1 = min(kTile, key_end - tile * kTile);
@@ -416,7 +425,7 @@ __device__ __noinline__ void plain_tiles(const PagedArgs a, int group, int b, in
             const int hd = row0 + nt * 8 + 2 * t + c;
             if (hd >= group) continue;
             const uint4 u = ldg_keep(static_cast<const __nv_bfloat16*>(a.q) +
-                                     row_at(a, group, b, h, hd, a.q_stride, D) + ch);
+                                     row_at<EXT>(a, group, b, h, hd, a.q_stride, D) + ch);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               s[nt][c] = fmaf(bf16_lo(word_of(u, k)), x[2 * k], s[nt][c]);
@@ -462,14 +471,14 @@ __device__ __noinline__ void plain_tiles(const PagedArgs a, int group, int b, in
     }
 }
 
-// FINE (fp32): the tensor core's sums, which it cuts to 24 bits at every step, are short ones
-// that are added up in fp32 as it should be: four times as exact.
-template <int FMT, int DP, int NT, bool FINE = false>
+// EXT with fp32: the tensor core's sums, which it cuts to 24 bits at every step, are short ones
+// that are added up in fp32 as it should be (kFine): four times as exact.
+template <int FMT, int DP, int NT, bool EXT = false>
 __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT>::kPerSm)
     k_paged(const Params p) {
   using C = Cfg<FMT, DP, NT>;
   constexpr int W = C::kWarps, kJ = DP / 32, kV = DP / 64;
-  constexpr bool kF32 = FMT == DT_F32, kMx = C::kMx;
+  constexpr bool kF32 = FMT == DT_F32, kMx = C::kMx, kFine = EXT && kF32;
   // Weights are 2^kLift at a head's running maximum (m: the maximum - kLift) and rise to
   // 2^kSlack times that before it is raised: to 1, so that sums overflow no sooner than plain
   // ones; or, in fp16 (MX caches, whose sums are relative to a scale), to 2^15, which keeps
@@ -493,12 +502,12 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   long long u0 = 0, u1 = 0, per = 0;
   if (p.direct) {
     b = blockIdx.x / hr_n;
-    const int n = places(seq_of(a, b, threadIdx.x == 0 && blockIdx.x % hr_n == 0).n);
+    const int n = places(seq_of<EXT>(a, b, threadIdx.x == 0 && blockIdx.x % hr_n == 0).n);
     u0 = static_cast<long long>(blockIdx.x - b * hr_n) * n;  // counted from the sequence's start
     u1 = total = u0 + n;
     per = n;
   } else if (a.B <= 32) {  // every warp scans the lengths itself
-    const int n = lane < a.B ? places(seq_of(a, lane, blockIdx.x == 0 && w == 0).n) : 0;
+    const int n = lane < a.B ? places(seq_of<EXT>(a, lane, blockIdx.x == 0 && w == 0).n) : 0;
     long long s = n;
 #pragma unroll
     for (int i = 1; i < 32; i <<= 1) {
@@ -519,7 +528,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       long long sum = 0;
       for (int base = 0; base < a.B; base += W * 32) {
         const int i = base + threadIdx.x;
-        const int n = i < a.B ? places(seq_of(a, i, blockIdx.x == 0 && pass == 0).n) : 0;
+        const int n = i < a.B ? places(seq_of<EXT>(a, i, blockIdx.x == 0 && pass == 0).n) : 0;
         long long s = n;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
@@ -558,18 +567,18 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
   }
   // sequences with nothing to see: zeros, lse -inf
   for (int e = blockIdx.x; e < a.B; e += gridDim.x) {
-    if (seq_of(a, e, false).n > 0) continue;
-    const int wide = kF32 || a.raw ? 4 : 2, bytes = a.n_q_heads * a.c.head_dim * wide;
+    if (seq_of<EXT>(a, e, false).n > 0) continue;
+    const int wide = kF32 || (EXT && a.raw) ? 4 : 2, bytes = a.n_q_heads * a.c.head_dim * wide;
     char* o = static_cast<char*>(a.out) + static_cast<size_t>(e) * a.out_stride * wide;
     for (int i = threadIdx.x * 16; i < bytes; i += W * 32 * 16)
       *reinterpret_cast<uint4*>(o + i) = make_uint4(0, 0, 0, 0);
     if (a.lse != nullptr)
       for (int i = threadIdx.x; i < a.n_q_heads; i += W * 32)
-        store_lse(a, a.n_q_heads, e, 0, i, -FLT_MAX, 0.f);
+        store_lse<EXT>(a, a.n_q_heads, e, 0, i, -FLT_MAX, 0.f);
   }
   // launched while the kernel before still runs: this one's end has to imply that one's
   auto end = [&]() {
-    if (a.overlap) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (EXT && a.overlap) asm volatile("griddepcontrol.wait;" ::: "memory");
   };
   if (u0 >= total) return end();
 
@@ -610,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     live[i] = n >= 4 ? 0xffffffffu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
   }
 
-  Seq sq = seq_of(a, b, false);
+  Seq sq = seq_of<EXT>(a, b, false);
   long long into = u0 - before * hr_n;
   int hr = static_cast<int>(quotient(into, places(sq.n)));
   // place of the segment at hand where this block starts (tile + kOpen)
@@ -635,7 +644,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
     tile_of = kNone;
     if (tile < tile_end) {
       const int pi = tile / tiles_per_page;
-      const int page = __ldg(a.block_table + table_at(a, b, h) + pi);
+      const int page = __ldg(a.block_table + table_at<EXT>(a, b, h) + pi);
       if (page < 0 || page >= a.c.n_pages)
         latch_error(a.status, kErrDevice);
       else
@@ -765,7 +774,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row0 + nt * 8 + g;
-      const size_t at = row_at(a, p.group, b, h, r, a.q_stride, D);
+      const size_t at = row_at<EXT>(a, p.group, b, h, r, a.q_stride, D);
       xs[nt][0] = xs[nt][1] = sl;
       if constexpr (kF32) {
         // in shared memory, once a block: per 8 elements t and t + 4 in two tf32 parts
@@ -948,7 +957,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
               }
               mma_tf32_1688(d, lo, qh);
               mma_tf32_1688(d, hi, ql);
-              if constexpr (FINE) {
+              if constexpr (kFine) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                   x[i][0][c] = j == 0 ? d[c] : x[i][0][c] + d[c];
@@ -958,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              if constexpr (!FINE) x[i][0][c] = d[c];
+              if constexpr (!kFine) x[i][0][c] = d[c];
               nan |= x[i][0][c] != x[i][0][c];
             }
             if (!__any_sync(0xffffffffu, nan)) break;
@@ -1221,11 +1230,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
                   split_tf32(pf[nt][2 * s + 1], &ph[1], &plo[1]);
                   float(&sum)[4] = acc[v * 4 + hf * 2 + i][nt];
                   float part[4] = {0.f, 0.f, 0.f, 0.f};
-                  float(&d)[4] = FINE ? part : sum;
+                  float(&d)[4] = kFine ? part : sum;
                   mma_tf32_1688(d, lo, ph);
                   mma_tf32_1688(d, hi, plo);
                   mma_tf32_1688(d, hi, ph);
-                  if constexpr (FINE) {
+                  if constexpr (kFine) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) sum[c] += part[c];
                   }
@@ -1425,7 +1434,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       for (int nt = 0; nt < NT; ++nt) odd |= l[nt][0] != l[nt][0] || l[nt][1] != l[nt][1];
       if (__any_sync(0xffffffffu, odd)) {
         PlainSums<DP, NT> sums;
-        plain_tiles<FMT, DP, NT>(a, p.group, b, h, row0, start, key_end, tile0, tile_end, sl, &sums);
+        plain_tiles<FMT, DP, NT, EXT>(a, p.group, b, h, row0, start, key_end, tile0, tile_end, sl, &sums);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1452,7 +1461,7 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
       if (++hr == hr_n) {
         hr = 0;
         do {
-          sq = seq_of(a, ++b, false);
+          sq = seq_of<EXT>(a, ++b, false);
         } while (sq.n == 0);
       }
       begin();
@@ -1552,11 +1561,11 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
           for (int c = 0; c < 2; ++c) {
             const int r = orow0 + nt * 8 + 2 * t + c;
             if (r >= p.group) continue;
-            store_out<FMT == DT_BF16, kF32>(a, row_at(a, p.group, ob, oh, r, a.out_stride, D), i, g,
+            store_out<FMT == DT_BF16, kF32, EXT>(a, row_at<EXT>(a, p.group, ob, oh, r, a.out_stride, D), i, g,
                                             sum[c] == 0.f ? 0.f : o[c],
                                             sum[c] == 0.f ? 0.f : o[c + 2]);
             if (a.lse != nullptr && i == 0 && g == 0)
-              store_lse(a, p.group, ob, oh, r, mx[c], sum[c]);
+              store_lse<EXT>(a, p.group, ob, oh, r, mx[c], sum[c]);
           }
         }
       }

@@ -19,13 +19,13 @@ COLI_DEV int context_len(const int32_t* seq_lens, int b, int max_pages, int page
   return len;
 }
 
-// Unsigned keys in the numbers' order; NaN counts as -infinity.
+// Unsigned keys in the numbers' order; NaN counts as -infinity, -0 as 0.
 COLI_DEV uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x != x ? -INFINITY : x);
+  const uint32_t u = __float_as_uint(x != x ? -INFINITY : x + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 COLI_DEV uint64_t order_key(double x) {
-  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x != x ? -INFINITY : x));
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x != x ? -INFINITY : x + 0.));
   return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
 

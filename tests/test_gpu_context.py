@@ -466,6 +466,19 @@ def test_evict(fmt, B, hk, D, page, lens, keep, first, recent, in_place):
         assert torch.equal(x.cpu().view(torch.uint8), y.view(torch.uint8))
 
 
+def test_evict_ties_of_zeros():
+    # -0 and 0 are equal: the earlier ones stay
+    g = ref.gen(42)
+    cache, _, _ = ref.pool(g, "bf16", 8, 16, 1, 64)
+    mass = torch.zeros(8, 1, 16)
+    mass[::2] = -0.0
+    mass[3, 0, 5] = 1.0
+    table = torch.arange(8, dtype=torch.int32)[None].cuda()
+    kept, _ = cache.evict(mass.cuda(), table, torch.tensor([128], dtype=torch.int32).cuda(), 40,
+                          recent=1)
+    assert kept[0, 0].tolist() == list(range(38)) + [53, 127]
+
+
 def test_evict_with_bad_pages():
     g = ref.gen(41)
     cache, _, _ = ref.pool(g, "bf16", 8, 16, 1, 64)
