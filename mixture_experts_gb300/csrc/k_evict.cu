@@ -20,7 +20,7 @@ constexpr int kMostCached = 200 * 1024;  // bytes of keys that shared memory hol
 
 template <int THREADS, bool CACHED>
 __global__ void __launch_bounds__(THREADS) k_evict_pick(const EvictArgs p) {
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ PickShared s;
   const int b = blockIdx.x / p.c.n_heads, h = blockIdx.x - b * p.c.n_heads;
   const int page = p.c.page_size;
@@ -41,34 +41,47 @@ __global__ void __launch_bounds__(THREADS) k_evict_pick(const EvictArgs p) {
     }
     return order_key(__ldg(p.mass + kv_row(p.c, at, h, i - pi * page)));
   };
-  if constexpr (CACHED) {  // sixteen or eight in flight: a page's number, then the mass
-    constexpr int kDeep = THREADS == 1024 ? 16 : 8;
+  if constexpr (CACHED) {  // four tokens of a page at once, eight such loads in flight
+    constexpr int kDeep = THREADS == 1024 ? 8 : 4;
     const uint32_t per = 0xffffffffu / page + 1;  // i / page = i * per / 2^32, or one less
-    auto page_in_table = [&](int i) {
-      const int pi = __umulhi(i, per);
-      return pi * page > i ? pi - 1 : pi;
-    };
-    for (int i0 = threadIdx.x; i0 < n; i0 += THREADS * kDeep) {
-      int row[kDeep];
-      float m[kDeep];
+    const bool whole = (reinterpret_cast<uintptr_t>(p.mass) & 15) == 0;
+    for (int i0 = threadIdx.x * 4; i0 < n; i0 += THREADS * 4 * kDeep) {
+      int at[kDeep], off[kDeep];
+      float4 m[kDeep];
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
-        const int i = i0 + e * THREADS;
-        row[e] = i < n ? __ldg(table + page_in_table(i)) : 0;
+        const int i = i0 + e * THREADS * 4;
+        int pi = __umulhi(i, per);
+        if (pi * page > i) --pi;
+        off[e] = i - pi * page;
+        at[e] = i < n ? __ldg(table + pi) : 0;
       }
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
-        const int i = i0 + e * THREADS;
-        const bool in = row[e] >= 0 && row[e] < p.c.n_pages;
+        const bool in = at[e] >= 0 && at[e] < p.c.n_pages;
         if (!in) latch_error(p.status, kErrDevice);
-        m[e] = in && i < n
-                   ? __ldg(p.mass + kv_row(p.c, row[e], h, i - page_in_table(i) * page))
-                   : -INFINITY;
+        m[e] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (!in || i0 + e * THREADS * 4 >= n) continue;
+        const float* src = p.mass + kv_row(p.c, at[e], h, off[e]);
+        if (whole)
+          m[e] = __ldg(reinterpret_cast<const float4*>(src));
+        else
+          m[e] = make_float4(__ldg(src), __ldg(src + 1), __ldg(src + 2), __ldg(src + 3));
       }
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
-        const int i = i0 + e * THREADS;
-        if (i < n) s_keys[i] = i < p.first || i >= n - p.recent ? 0xffffffffu : order_key(m[e]);
+        const int i = i0 + e * THREADS * 4;
+        if (i >= n) break;
+        uint4 k = make_uint4(order_key(m[e].x), order_key(m[e].y), order_key(m[e].z),
+                             order_key(m[e].w));
+        if (i < p.first || i + 4 > n - p.recent) {  // kept anyway
+          auto forced = [&](int t) { return t < p.first || t >= n - p.recent; };
+          k.x = forced(i) ? 0xffffffffu : k.x;
+          k.y = forced(i + 1) ? 0xffffffffu : k.y;
+          k.z = forced(i + 2) ? 0xffffffffu : k.z;
+          k.w = forced(i + 3) ? 0xffffffffu : k.w;
+        }
+        *reinterpret_cast<uint4*>(s_keys + i) = k;  // past the last token: room, never read
       }
     }
     __syncthreads();
