@@ -4,12 +4,15 @@
 // k_evict_pick: a block a (sequence, key head); the masses come through the page table into
 // shared memory as ordered keys (tokens that are kept anyway: the largest key), and
 // pick.cuh finds the keep-th largest and lists the kept places in rising order.
+// A block's choice takes 14 us of 2176 tokens and 25 of 32768: loads of pages and masses, a pass
+// for the range, up to three over the digits, two to list.
 // k_evict_copy: into other pages, a block takes 64 kept tokens of a (sequence, key head),
-// keys and values and their scales and masses, 16 bytes a thread and step.
+// keys and values and their scales and masses, 16 bytes a thread and step (64 sequences of 2048
+// bf16 tokens, 8 heads of 128, 1.1 GB read and written: 164 us, 6.6 TB/s).
 // k_evict_pack: in place. A kept row moves to an earlier place or stays, so rows copied
 // in order, each batch read before it is written, never overwrite one that is still to be
 // read. A block takes 128 bytes of all of a head's rows (or its scales, or masses):
-// blocks share no byte.
+// blocks share no byte. The same sequences in place: 222 us with the choice, against 183.
 #include "mx.cuh"
 #include "pick.cuh"
 

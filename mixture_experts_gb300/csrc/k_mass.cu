@@ -9,7 +9,11 @@
 // channels lane 4g + t has 8t .. + 7 of rows g and g + 8, on both operands. bf16 queries
 // and keys are operands as they are; MX codes are widened to fp16, against fp16 queries, and a
 // block's scale goes on its sum (queries that fp16 does not hold meet bf16 keys); fp32 runs in three tf32 products of operands in two parts.
-// HBM bound by the keys, a third of what the attention itself reads with its values.
+//
+// 32 bf16 contexts of up to 8192 tokens, 32 heads on 8 of 128 (302 MB): 51 us, 5.9 TB/s, HBM
+// bound. 16 MXFP4 contexts of up to 60000, 64 heads on 4 (145 MB): 64 us, 2.3 TB/s: a quarter of
+// the bytes at twice the heads, bound by the steps' instructions and their latency with 16
+// warps an SM (128 registers; a second tile fetched ahead leaves 12 warps: 79 us).
 #include "mx.cuh"
 #include "paged.cuh"
 #include "pick.cuh"

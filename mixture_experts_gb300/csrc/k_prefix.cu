@@ -26,6 +26,14 @@
 // equal pieces, one a block; a piece's part of a segment gives a partial mean with (m, l), in
 // slot (block + segment), which k_shared_join joins in the line's order with each sequence's
 // own tokens.
+//
+// What bounds it (GB300, heads of 128): the products. 24 instructions of 128 x 128 x 16 a unit
+// (128 rows by 128 keys) take 2460 cycles, 100 each where 64 is the pipe's rate: the first
+// product's operands are all of a shared-memory port's 128 bytes a clock. 64 sequences of 32
+// heads on 8 behind 32768 bf16 tokens 54 us, 128 of 64 on 8 behind 40009 MXFP8 ones 201 us (845
+// TFLOP/s, 1270 with the second weight term), which ncu has at 43% to 50% of the tensor pipe. The
+// second term costs a third of the products; without it the output's error would be 1.2 times
+// the rounding's own. What a block does once (queries, first tiles, the last means) takes 8 us.
 #include <limits.h>
 
 #include "tcgen05.cuh"

@@ -12,7 +12,12 @@
 // most 24 roundings: 2^-18.
 // k_page_pick: a block a (sequence, key head) finds the keep-th largest score T. Scores further
 // than twice the largest error from T are settled; where the others are not just as many
-// as are still wanted, they are computed again in fp64 and ranked by that.
+// as are still wanted, they are computed again in fp64 and ranked by that (two to four pages of
+// thousands, by themselves; all of a list where more than kFew are open, as with equal pages).
+//
+// 32 contexts of up to 65536 tokens in pages of 32, 8 heads of 128 (134 MB of bounds): scores 27
+// us (4.8 TB/s, 16 warps an SM: 126 registers), choice of 64 pages 15 us. One context of 7813 pages: 10
+// and 14 us; a block's choice is a chain of short steps between barriers.
 #include "mx.cuh"
 #include "paged.cuh"
 #include "pick.cuh"
