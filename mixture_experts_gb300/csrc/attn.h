@@ -89,6 +89,23 @@ size_t paged_scratch_bytes(const KvView& c, int B, int n_q_heads);
 bool paged_direct(const KvView& c, int max_pages);  // needs no scratch
 cudaError_t launch_paged_attention(const PagedArgs& a, cudaStream_t st);
 int sm_count();  // of the current device
+// Launches a kernel whose blocks may be placed while the one before in the stream drains: it
+// has to wait for its end (griddepcontrol.wait) before it reads anything of it.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, size_t smem,
+                         cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 // Raises a kernel's dynamic shared memory limit once per device; `ready` is the kernel's own.
 template <class K>
 cudaError_t raise_shared(K* kernel, int bytes, bool (&ready)[128]) {

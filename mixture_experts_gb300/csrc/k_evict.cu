@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_evict_copy(const EvictArgs p, 
   __shared__ size_t s_src[kRanks], s_dst[kRanks];
   __shared__ int s_in[kRanks];
   const int bh = blockIdx.x / chunks, r0 = (blockIdx.x - bh * chunks) * kRanks;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = bh / p.c.n_heads, h = bh - b * p.c.n_heads;
   const int32_t* kept = p.kept + static_cast<size_t>(bh) * p.keep;
   if (threadIdx.x < kRanks) {
@@ -211,6 +212,7 @@ COLI_DEV void pack_rows(const EvictArgs& p, int b, int h, char* base, int row, i
 // Slices of kSlice bytes of the keys' rows, then of the values'; masses; scales.
 __global__ void __launch_bounds__(kCopyThreads) k_evict_pack(const EvictArgs p, int slices) {
   const int kinds = 2 * slices + 1 + (p.c.scale_stride ? 2 : 0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int bh = blockIdx.x / kinds, x = blockIdx.x - bh * kinds;
   const int b = bh / p.c.n_heads, h = bh - b * p.c.n_heads;
   // a sequence that is kept whole stays where it is
@@ -260,15 +262,14 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
   const int rows = a.B * a.c.n_heads;
   if (a.into != a.block_table) {
     const int chunks = (a.keep + kRanks - 1) / kRanks;
-    k_evict_copy<<<static_cast<unsigned>(static_cast<int64_t>(rows) * chunks), kCopyThreads, 0,
-                   st>>>(a, chunks);
+    return launch_after(k_evict_copy, static_cast<unsigned>(static_cast<int64_t>(rows) * chunks),
+                        kCopyThreads, 0, st, a, chunks);
   } else {
     const int slices = (a.c.row_bytes + kSlice - 1) / kSlice;
     const int kinds = 2 * slices + 1 + (a.c.scale_stride ? 2 : 0);
-    k_evict_pack<<<static_cast<unsigned>(static_cast<int64_t>(rows) * kinds), kCopyThreads, 0,
-                   st>>>(a, slices);
+    return launch_after(k_evict_pack, static_cast<unsigned>(static_cast<int64_t>(rows) * kinds),
+                        kCopyThreads, 0, st, a, slices);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace coli

@@ -234,18 +234,10 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
   a.lse = reinterpret_cast<float*>(own_ml);
   e = launch_paged_attention(a, st);
   if (e != cudaSuccess) return e;
-  // its blocks are placed while the kernel before drains, and wait for its end
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((rows + kJoinWarps - 1) / kJoinWarps);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return c.dtype == DT_F32 ? cudaLaunchKernelEx(&cfg, k_shared_join<float>, j)
-                           : cudaLaunchKernelEx(&cfg, k_shared_join<__nv_bfloat16>, j);
+  const unsigned grid = (rows + kJoinWarps - 1) / kJoinWarps;
+  return c.dtype == DT_F32
+             ? launch_after(k_shared_join<float>, grid, kJoinWarps * 32, 0, st, j)
+             : launch_after(k_shared_join<__nv_bfloat16>, grid, kJoinWarps * 32, 0, st, j);
 }
 
 }  // namespace coli
