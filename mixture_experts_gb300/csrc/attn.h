@@ -92,10 +92,10 @@ int sm_count();  // of the current device
 // Launches a kernel whose blocks may be placed while the one before in the stream drains: it
 // has to wait for its end (griddepcontrol.wait) before it reads anything of it.
 template <class... P, class... A>
-cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, size_t smem,
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
                          cudaStream_t st, A&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

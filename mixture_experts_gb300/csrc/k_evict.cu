@@ -12,7 +12,7 @@
 // k_evict_pack: in place. A kept row moves to an earlier place or stays, so rows copied
 // in order, each batch read before it is written, never overwrite one that is still to be
 // read. A block takes 128 bytes of all of a head's rows (or its scales, or masses):
-// blocks share no byte. The same sequences in place: 222 us with the choice, against 183.
+// blocks share no byte. The same sequences in place: 222 us with the choice, against 180.
 #include "mx.cuh"
 #include "pick.cuh"
 

@@ -22,6 +22,9 @@
 // it); MX codes by TMA as they are, then widened to bf16 with their scale by eight warps (exact
 // within bf16's range, which is fp32's). Scores of keys out of sight are set to -inf.
 //
+// Heads above 128 (bf16): two accumulators of 256 columns and the scores are more than tensor
+// memory holds, so a segment has half of the values' channels and forms the scores for itself.
+//
 // Work split: the tiles of all (key head, 128 rows) segments lie on one line that is cut into
 // equal pieces, one a block; a piece's part of a segment gives a partial mean with (m, l), in
 // slot (block + segment), which k_shared_join joins in the line's order with each sequence's
@@ -34,6 +37,8 @@
 // TFLOP/s, 1270 with the second weight term), which ncu has at 43% to 50% of the tensor pipe. The
 // second term costs a third of the products; without it the output's error would be 1.2 times
 // the rounding's own. What a block does once (queries, first tiles, the last means) takes 8 us.
+// Heads of 256: 64 instructions for 128 rows by 128 keys, a quarter of them the scores formed
+// twice; the call of 64 sequences of 32 heads on 8 behind 32768 tokens 161 us.
 #include <limits.h>
 
 #include "tcgen05.cuh"
@@ -55,9 +60,23 @@ constexpr uint32_t kNone = 0xffffffffu;
 
 constexpr int kMost = 3, kRaw = 3;
 
-template <int FMT, bool PAIR>
-constexpr int stages() {  // of keys, and of values
+// Heads above 128 (DP 256): a segment has all of them for its scores and half of the values'
+// channels, and keys come in two parts of 128.
+template <int DP>
+constexpr int halves() {
+  return DP > 128 ? 2 : 1;
+}
+template <int DP>
+constexpr int part_bytes() {  // of a stage: 128 rows of up to 128 channels
+  return DP / 64 * kSub / halves<DP>();
+}
+template <int FMT, int DP, bool PAIR>
+constexpr int stages_k() {
   return FMT == DT_BF16 && !PAIR ? 3 : 2;
+}
+template <int FMT, int DP, bool PAIR>
+constexpr int stages_v() {
+  return DP > 128 ? 2 : stages_k<FMT, DP, PAIR>();
 }
 template <bool PAIR>
 constexpr int raw_stages() {
@@ -89,7 +108,8 @@ struct Ctrl {
 
 template <int FMT, int DP, bool PAIR>
 constexpr int smem_bytes() {
-  return DP / 64 * kSub * ((PAIR ? 2 : 1) + 2 * stages<FMT, PAIR>()) +
+  return DP / 64 * kSub * (PAIR ? 2 : 1) +
+         part_bytes<DP>() * (stages_k<FMT, DP, PAIR>() + stages_v<FMT, DP, PAIR>()) +
          raw_stages<PAIR>() * raw_bytes<FMT, DP>() + static_cast<int>(sizeof(Ctrl<PAIR>));
 }
 
@@ -195,8 +215,10 @@ struct Walk {
 
 template <int FMT, int DP, bool PAIR>
 __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p, const __grid_constant__ PrefixMaps maps) {
-  constexpr int kTileBytes = DP / 64 * kSub;
-  constexpr int kStages = stages<FMT, PAIR>(), kRaws = raw_stages<PAIR>();
+  constexpr int kTileBytes = part_bytes<DP>(), kQBytes = DP / 64 * kSub;
+  constexpr int kHalves = halves<DP>(), DV = DP / kHalves;  // channels of a stage
+  constexpr int kStagesK = stages_k<FMT, DP, PAIR>(), kStagesV = stages_v<FMT, DP, PAIR>();
+  constexpr int kRaws = raw_stages<PAIR>();
   constexpr int kQTiles = PAIR ? 2 : 1, kSegRows = kQTiles * kPrefixRows;
   extern __shared__ __align__(1024) char smem_raw[];  // there is no room to align it by hand
   const uint32_t base = smem_u32(smem_raw);
@@ -204,13 +226,17 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
     if (threadIdx.x == 0) latch_error(p.status, kErrDevice);
     return;
   }
-  const uint32_t s_q = base, s_k = base + kQTiles * kTileBytes, s_v = s_k + kStages * kTileBytes;
-  const uint32_t s_raw = s_v + kStages * kTileBytes;
+  const uint32_t s_q = base, s_k = base + kQTiles * kQBytes, s_v = s_k + kStagesK * kTileBytes;
+  const uint32_t s_raw = s_v + kStagesV * kTileBytes;
   Ctrl<PAIR>& C = *reinterpret_cast<Ctrl<PAIR>*>(smem_raw + (s_raw - base) +
                                                  kRaws * raw_bytes<FMT, DP>());
   volatile int* abort = &C.abort;
   const int warp = threadIdx.x / 32, lane = lane_id();
   const int D = p.c.head_dim;
+  // a segment's key head, row tile and half of the values
+  auto head_of = [&](const Walk& w) { return w.seg / (p.row_tiles * kHalves); };
+  auto tile_of = [&](const Walk& w) { return w.seg / kHalves % p.row_tiles; };
+  auto half_of = [&](const Walk& w) { return w.seg % kHalves; };
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
@@ -220,11 +246,11 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       mbar_init(smem_u32(&C.raw_full[i]), 33);  // the bytes announced, each lane's scales
       mbar_init(smem_u32(&C.raw_free[i]), kConvWarps);
     }
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kStagesK; ++i) {
       mbar_init(smem_u32(&C.kfull[i]), kFull);
       mbar_init(smem_u32(&C.kfree[i]), 1);
     }
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kStagesV; ++i) {
       mbar_init(smem_u32(&C.vfull[i]), kFull);
       mbar_init(smem_u32(&C.vfree[i]), 1);
     }
@@ -254,16 +280,17 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
     const float sl = fabsf(p.scale) * 1.4426950408889634f;  // the sign went into Q
     // the piece's queries: 128 rows by all softmax warps, their sign that of the scale
     auto load_queries = [&](const Walk& w) {
-      const int h = w.seg / p.row_tiles, r0 = (w.seg - h * p.row_tiles) * kSegRows;
+      const int h = head_of(w), r0 = tile_of(w) * kSegRows;
       const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
-      constexpr int kQ = kPrefixRows * (DP / 8) / (kSoftWarps * 32);  // loads in flight
+      constexpr int kQ = kPrefixRows * (DV / 8) / (kSoftWarps * 32);  // loads in flight
 #pragma unroll 1
-      for (int t = 0; t < kQTiles; ++t) {
+      for (int t = 0; t < kQTiles * kHalves; ++t) {  // a row tile, or half of one
         uint4 v[kQ];
 #pragma unroll
         for (int e = 0; e < kQ; ++e) {
-          const int i = threadIdx.x + e * kSoftWarps * 32, r = i / (DP / 8), c = i - r * (DP / 8);
-          const int at = r0 + t * kPrefixRows + r;
+          const int i = threadIdx.x + e * kSoftWarps * 32, r = i / (DV / 8);
+          const int c = i - r * (DV / 8) + (PAIR ? 0 : t * (DV / 8));
+          const int at = r0 + (PAIR ? t * kPrefixRows : 0) + r;
           v[e] = make_uint4(0, 0, 0, 0);
           if (at < p.rows && c * 8 < D) {
             const int b = at / p.group, g = at - b * p.group;
@@ -273,9 +300,10 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         }
 #pragma unroll
         for (int e = 0; e < kQ; ++e) {
-          const int i = threadIdx.x + e * kSoftWarps * 32, r = i / (DP / 8), c = i - r * (DP / 8);
+          const int i = threadIdx.x + e * kSoftWarps * 32, r = i / (DV / 8);
+          const int c = i - r * (DV / 8) + (PAIR ? 0 : t * (DV / 8));
           v[e].x ^= flip, v[e].y ^= flip, v[e].z ^= flip, v[e].w ^= flip;
-          sts128(s_q + t * kTileBytes + place(r, c), v[e]);
+          sts128(s_q + (PAIR ? t * kQBytes : 0) + place(r, c), v[e]);
         }
       }
       proxy_fence();
@@ -329,7 +357,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
           l *= f;
           if (j >= (PAIR ? 1 : 2)) {  // its stream's first product overwrites O
 #pragma unroll 1
-            for (int c = 0; c < DP / 32; ++c) {
+            for (int c = 0; c < DV / 32; ++c) {
               uint32_t v[32];
               tmem_ld32(t_o + 32 * c, v);
 #pragma unroll
@@ -373,7 +401,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         if (!__all_sync(0xffffffffu, wait_for(smem_u32(&C.q_free), piece & 1, abort))) break;
         load_queries(ahead);
       }
-      const int rt = walk.seg % p.row_tiles, r = rt * kSegRows + (PAIR ? X * kPrefixRows : 0) + row;
+      const int r = tile_of(walk) * kSegRows + (PAIR ? X * kPrefixRows : 0) + row;
       const size_t slot = (static_cast<size_t>(blockIdx.x) + walk.seg) * kSegRows +
                           (PAIR ? X * kPrefixRows : 0) + row;
       float* out = p.mean + slot * D;
@@ -415,15 +443,15 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       const float fa = wa == 0.f ? 0.f : wa / sum, ia = wa == 0.f ? 0.f : 1.f / a.y;
       const float fb = wb == 0.f ? 0.f : wb / sum, ib = wb == 0.f ? 0.f : 1.f / b.y;
 #pragma unroll 1
-      for (int c = 0; c < DP / 64; ++c) {
-        const int col = (X * (DP / 64) + c) * 32;
+      for (int c = 0; c < DV / 64; ++c) {
+        const int col = (X * (DV / 64) + c) * 32, to = half_of(walk) * DV + col;
         uint32_t v[32], u[32];
         tmem_ld32(lanes + kOCol + col, v);
         tmem_ld32(lanes + kOCol + 128 + col, u);
         if (r < p.rows) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
-            if (col + i >= D) break;
+            if (to + i >= D) break;
             float o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -432,7 +460,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
               const float ob = wb == 0.f ? 0.f : __uint_as_float(u[i + k]) * ib * fb;
               o[k] = oa + ob;
             }
-            *reinterpret_cast<float4*>(out + col + i) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4*>(out + to + i) = make_float4(o[0], o[1], o[2], o[3]);
           }
         }
       }
@@ -445,7 +473,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
   } else if (warp == kMmaWarp) {
     // ---- products
     constexpr uint32_t kIdS = idesc_bf16(kPrefixRows, kPrefixKeys);
-    constexpr uint32_t kIdO = idesc_bf16(kPrefixRows, DP) | 1u << 16;  // B as it lies
+    constexpr uint32_t kIdO = idesc_bf16(kPrefixRows, DV) | 1u << 16;  // B as it lies
     int ks = 0, vs = 0, piece = 0;
     uint32_t kp = 0, vp = 0, p_phase = 0;  // bit X: of stream X
     bool ok = true;
@@ -457,22 +485,27 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       const int units = PAIR ? 2 * walk.n : walk.n;
       for (int u = 0; u <= units; ++u) {
         if (u < units) {
-          if (!PAIR || u % 2 == 0)
-            if (!(ok = warp_wait(smem_u32(&C.kfull[ks]), kp, abort))) break;
-          tc_fence_after();
-          const uint32_t k0 = s_k + ks * kTileBytes, q0 = s_q + (PAIR ? (u & 1) * kTileBytes : 0);
+          const uint32_t q0 = s_q + (PAIR ? (u & 1) * kQBytes : 0);
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {
-            const uint32_t off = k / 4 * kSub + k % 4 * 32;
-            mma_ss(tmem + (u & 1) * 128, sw128_desc(q0 + off), sw128_desc(k0 + off), kIdS,
-                   k != 0 ? 1u : 0u);
+          for (int part = 0; part < kHalves; ++part) {
+            if (!PAIR || u % 2 == 0)
+              if (!(ok = warp_wait(smem_u32(&C.kfull[ks]), kp, abort))) break;
+            tc_fence_after();
+            const uint32_t k0 = s_k + ks * kTileBytes;
+#pragma unroll
+            for (int k = 0; k < DV / 16; ++k) {
+              const uint32_t off = k / 4 * kSub + k % 4 * 32;
+              mma_ss(tmem + (u & 1) * 128, sw128_desc(q0 + part * kTileBytes + off),
+                     sw128_desc(k0 + off), kIdS, part != 0 || k != 0 ? 1u : 0u);
+            }
+            if (!PAIR || u % 2 == 1) {
+              mma_commit(smem_u32(&C.kfree[ks]));
+              if (++ks == kStagesK) ks = 0, kp ^= 1u;
+            }
           }
+          if (!ok) break;
           mma_commit(smem_u32(&C.s_full[u & 1]));
           if (u == units - 1) mma_commit(smem_u32(&C.q_free));
-          if (!PAIR || u % 2 == 1) {
-            mma_commit(smem_u32(&C.kfree[ks]));
-            if (++ks == kStages) ks = 0, kp ^= 1u;
-          }
         }
         if (u == 0) continue;
         const int X = (u - 1) & 1;
@@ -493,7 +526,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
         }
         if (!PAIR || X == 1) {
           mma_commit(smem_u32(&C.vfree[vs]));
-          if (++vs == kStages) vs = 0, vp ^= 1u;
+          if (++vs == kStagesV) vs = 0, vp ^= 1u;
         }
       }
       if (ok) mma_commit(smem_u32(&C.o_full));
@@ -545,12 +578,15 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
       // warp 0 of the loaders brings the keys, warp 1 the values, lane i the i-th box of rows
       const bool keys = warp == kLoad0;
       const char* pool = keys ? p.c.k : p.c.v;
+      const int parts = keys ? kHalves : 1;
       for (; ok && walk.next(p) && !*abort; ++piece) {
-        const int h = walk.seg / p.row_tiles;
+        const int h = head_of(walk);
         start(h, walk.t0 * kPrefixKeys);
-        for (int j = 0; j < walk.n; ++j) {
+        for (int i = 0; i < walk.n * parts; ++i) {
+          const int j = keys ? i / kHalves : i;
+          const int ch0 = (keys ? i % kHalves : half_of(walk)) * DV;  // first channel
           const int key0 = (walk.t0 + j) * kPrefixKeys;
-          if (j > 0 && j % 4 == 0) advance(h, key0);
+          if (i > 0 && i % (4 * parts) == 0) advance(h, key0);
           const uint32_t full = smem_u32(keys ? &C.kfull[stage] : &C.vfull[stage]);
           const uint32_t dst = (keys ? s_k : s_v) + stage * kTileBytes;
           ok = warp_wait(smem_u32(keys ? &C.kfree[stage] : &C.vfree[stage]), phase ^ 1u, abort);
@@ -560,36 +596,37 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
           const int box = part ? 16 : p.box, edge = part ? (p.len - key0) / 16 : kPrefixKeys;
           const bool by_hand = part && p.len % 16 != 0;
           if (lane == 0)
-            mbar_arrive_expect_tx(full, kTileBytes - (by_hand ? DP / 64 * 16 * 128 : 0));
+            mbar_arrive_expect_tx(full, kTileBytes - (by_hand ? DV / 64 * 16 * 128 : 0));
           __syncwarp();
           const CUtensorMap* map = part ? (keys ? &maps.k16 : &maps.v16) : (keys ? &maps.k : &maps.v);
           const int row = box_row(j, box);
           if (lane < kPrefixKeys / box && !(by_hand && lane == edge)) {
 #pragma unroll
-            for (int c = 0; c < DP / 64; ++c)
-              tma_load_2d(dst + c * kSub + lane * box * 128, map, full, c * 64, row);
+            for (int c = 0; c < DV / 64; ++c)
+              tma_load_2d(dst + c * kSub + lane * box * 128, map, full, ch0 + c * 64, row);
           }
           if (by_hand) {
             const uint32_t last = __shfl_sync(0xffffffffu, cur, (j & 3) * 8 + edge);
 #pragma unroll 4
-            for (int i = lane; i < 16 * (DP / 8); i += 32) {
-              const int r = i / (DP / 8), c = i - r * (DP / 8);
+            for (int e = lane; e < 16 * (DV / 8); e += 32) {
+              const int r = e / (DV / 8), c = e - r * (DV / 8);
               uint4 v = make_uint4(0, 0, 0, 0);
-              if (last != kNone && c * 8 < D && r < p.len % 16)
-                v = ldg_keep(pool + (static_cast<size_t>(last) * 16 + r) * p.c.row_bytes + c * 16);
+              if (last != kNone && ch0 + c * 8 < D && r < p.len % 16)
+                v = ldg_keep(pool + (static_cast<size_t>(last) * 16 + r) * p.c.row_bytes +
+                             ch0 * 2 + c * 16);
               sts128(dst + place(edge * 16 + r, c), v);
             }
             proxy_fence();
             __syncwarp();
           }
           if (lane == 0) mbar_arrive(full);
-          if (++stage == kStages) stage = 0, phase ^= 1u;
+          if (++stage == (keys ? kStagesK : kStagesV)) stage = 0, phase ^= 1u;
         }
       }
     } else {
       // codes by TMA, lane i the i-th box; scale words by the lanes
       for (; ok && walk.next(p) && !*abort; ++piece) {
-        const int h = walk.seg / p.row_tiles;
+        const int h = head_of(walk);
         start(h, walk.t0 * kPrefixKeys);
         for (int j = 0; ok && j < walk.n; ++j) {
           if (j > 0 && j % 4 == 0) advance(h, (walk.t0 + j) * kPrefixKeys);
@@ -683,7 +720,7 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
           widen((kv ? s_v : s_k) + stage * kTileBytes,
                 smem_u32(kv ? &C.vfull[stage] : &C.kfull[stage]),
                 p.len - (walk.t0 + i / 2) * kPrefixKeys);
-          const bool round = stage + 1 == kStages;
+          const bool round = stage + 1 == (kv ? kStagesV : kStagesK);
           if (kv)
             at[1] = round ? 0 : stage + 1;
           else
@@ -736,6 +773,8 @@ cudaError_t launch(const PrefixArgs& p, int grid, cudaStream_t st) {
 
 template <int FMT>
 cudaError_t launch_heads(const PrefixArgs& p, int grid, cudaStream_t st) {
+  if constexpr (FMT == DT_BF16)
+    if (p.c.head_dim > 128) return launch<FMT, 256, false>(p, grid, st);
   if (p.pair)
     return p.c.head_dim <= 64 ? launch<FMT, 64, true>(p, grid, st)
                               : launch<FMT, 128, true>(p, grid, st);

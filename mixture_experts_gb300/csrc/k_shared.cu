@@ -19,7 +19,7 @@ struct JoinArgs {
   const float* mean;     // of the prefix
   const float2* ml;
   int64_t tiles, per;    // of a segment and a block on k_prefix's line; 0: rows as above
-  int row_tiles, seg_rows;
+  int row_tiles, seg_rows, halves;
   int group;
   void* out;
   float* lse;
@@ -29,7 +29,8 @@ struct JoinArgs {
 
 constexpr int kJoinWarps = 8;
 
-// A warp a row, its lanes along the channels. Every factor is a part's share of the weights, so
+// A warp a row (and half of its channels, blockIdx.y, where those have segments of their own),
+// its lanes along the channels. Every factor is a part's share of the weights, so
 // a mean stays one; parts are added in their order.
 template <class T>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const JoinArgs p) {
@@ -41,7 +42,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const JoinArgs 
   int n = 1, step = 0;
   if (p.per > 0) {
     const int h = hq / p.group, r = b * p.group + hq - h * p.group;
-    const int64_t seg = static_cast<int64_t>(h) * p.row_tiles + r / p.seg_rows;
+    const int64_t seg =
+        (static_cast<int64_t>(h) * p.row_tiles + r / p.seg_rows) * p.halves + blockIdx.y;
     const int64_t c0 = seg * p.tiles / p.per, c1 = ((seg + 1) * p.tiles - 1) / p.per;
     first = static_cast<size_t>(c0 + seg) * p.seg_rows + r % p.seg_rows;
     n = static_cast<int>(c1 - c0) + 1;
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const JoinArgs 
   l += w0;
   T* out = static_cast<T*>(p.out) + b * p.out_stride + static_cast<size_t>(hq) * p.D;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int d0 = 0; d0 < p.D; d0 += 128) {
+  for (int d0 = blockIdx.y * 128; d0 < p.D; d0 += gridDim.y * 128) {
     const int d = d0 + lane * 4;
     const bool in = d < p.D;
     float4 o = zero;
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_shared_join(const JoinArgs 
     else
       *reinterpret_cast<uint2*>(out + d) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
   }
-  if (p.lse != nullptr && lane == 0)
+  if (p.lse != nullptr && blockIdx.y == 0 && lane == 0)
     p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -122,10 +124,13 @@ size_t part_bytes(const KvView& c, int64_t rows) { return mean_bytes(c, rows) + 
 // kernel reads the prefix once for every 8 or 16. Behind 32768 tokens, 8 key heads, us, at 8 /
 // 16 / 24 / 64 queries of a key head: bf16 heads of 128 43 / 44 / 44 / 47 against 45 / 56 /
 // 57 / 81, MXFP8 44 / 51 / 50 / 52 against 43 / 57 / 82 / 116, MXFP4 heads of 64 42 / 42 / 42 /
-// 42 against 34 / 38 / 45 / 60; behind 1024 both are bound by the host (28 to 31). (It numbers
-// the pool's rows in 31 bits.)
+// 42 against 34 / 38 / 45 / 60; behind 1024 both are bound by the host (28 to 31). bf16 heads of
+// 256 at 12 / 32 / 128 / 256 queries 83 / 83 / 96 / 161 against 91 / 126 / 344 / 606, behind 2048
+// (12, 32) 27 / 28 against 34 / 38; heads of 160 73 / 72 (12, 32) against 74 / 108. MX heads above
+// 128, whose codes would not fit beside what they are widened to, stay with the decode kernel.
+// (k_prefix numbers the pool's rows in 31 bits.)
 bool on_tensor_cores(const KvView& c, int rows_of_head) {
-  return c.dtype != DT_F32 && c.head_dim <= 128 && rows_of_head > 8 &&
+  return c.dtype != DT_F32 && (c.head_dim <= 128 || c.dtype == DT_BF16) && rows_of_head > 8 &&
          static_cast<int64_t>(c.n_pages) * c.n_heads * c.page_size < INT32_MAX;
 }
 
@@ -139,12 +144,12 @@ bool on_tensor_cores(const KvView& c, int rows_of_head) {
 //   MXFP8, 64           64 / 68     97 / 93    107 / 118   143 / 144
 //   MXFP4, 128          76 / 75    106 / 100   118 / 128   153 / 154
 // A pair saves 4 us (bf16) to 20 (MX, whose tiles are widened once for both), an idle half
-// costs 20.
+// costs 20. (Two tiles' queries of heads above 128 leave no room for keys.)
 int segment_rows(const KvView& c, int rows_of_head) {
   const int tiles = (rows_of_head + kPrefixRows - 1) / kPrefixRows;
   const bool mx = c.dtype != DT_BF16;
-  const bool pair =
-      tiles > 1 && (tiles % 2 == 0 ? mx || c.head_dim > 64 : tiles >= (mx ? 5 : 11));
+  const bool pair = tiles > 1 && c.head_dim <= 128 &&
+                    (tiles % 2 == 0 ? mx || c.head_dim > 64 : tiles >= (mx ? 5 : 11));
   return pair ? 2 * kPrefixRows : kPrefixRows;
 }
 
@@ -153,7 +158,8 @@ int64_t prefix_rows(const KvView& c, int B, int n_q_heads) {
   const int rows = B * (n_q_heads / c.n_heads);
   if (!on_tensor_cores(c, rows)) return static_cast<int64_t>(B) * n_q_heads;
   const int seg_rows = segment_rows(c, rows);
-  const int64_t segments = static_cast<int64_t>(c.n_heads) * ((rows + seg_rows - 1) / seg_rows);
+  const int64_t segments = static_cast<int64_t>(c.n_heads) *
+                           ((rows + seg_rows - 1) / seg_rows) * prefix_halves(c.head_dim);
   return (segments + sm_count()) * seg_rows;
 }
 
@@ -181,8 +187,8 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
   a.scratch = reinterpret_cast<float*>(prefix + part_bytes(c, parts));
   if (s.prefix_len == 0) return launch_paged_attention(a, st);
 
-  JoinArgs j{own_mean, own_ml, mean, ml, 0, 0, 0, 0, group, a.out, a.lse, a.out_stride, rows, heads,
-             c.head_dim};
+  JoinArgs j{own_mean, own_ml, mean, ml, 0, 0, 0, 0, 1, group, a.out, a.lse, a.out_stride, rows,
+             heads, c.head_dim};
   a.raw = 1;
   a.ext = 1;
   a.may_cut = 1;
@@ -201,7 +207,7 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
     p.pair = seg_rows == 2 * kPrefixRows;
     p.row_tiles = (p.rows + seg_rows - 1) / seg_rows;
     p.tiles = (p.len + kPrefixKeys - 1) / kPrefixKeys;
-    p.total = static_cast<int64_t>(c.n_heads) * p.row_tiles * p.tiles;
+    p.total = static_cast<int64_t>(c.n_heads) * p.row_tiles * prefix_halves(c.head_dim) * p.tiles;
     const int grid = p.total < sm_count() ? static_cast<int>(p.total) : sm_count();
     p.per = (p.total + grid - 1) / grid;
     p.box = c.page_size & -c.page_size;
@@ -215,6 +221,7 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
     j.per = p.per;
     j.row_tiles = p.row_tiles;
     j.seg_rows = seg_rows;
+    j.halves = prefix_halves(c.head_dim);
     e = launch_prefix(p, grid, st);
     a.overlap = 1;  // the own tokens need none of its results
   } else {
@@ -234,7 +241,7 @@ cudaError_t launch_shared_attention(const SharedArgs& s, cudaStream_t st) {
   a.lse = reinterpret_cast<float*>(own_ml);
   e = launch_paged_attention(a, st);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (rows + kJoinWarps - 1) / kJoinWarps;
+  const dim3 grid((rows + kJoinWarps - 1) / kJoinWarps, j.halves);
   return c.dtype == DT_F32
              ? launch_after(k_shared_join<float>, grid, kJoinWarps * 32, 0, st, j)
              : launch_after(k_shared_join<__nv_bfloat16>, grid, kJoinWarps * 32, 0, st, j);

@@ -7,6 +7,9 @@ namespace coli {
 
 constexpr int kPrefixRows = 128, kPrefixKeys = 128;  // of a block's tile
 
+// Parts that the values' channels of a head are cut in, a segment each.
+inline int prefix_halves(int head_dim) { return head_dim > 128 ? 2 : 1; }
+
 struct PrefixArgs {
   KvView c;
   const void* q;
@@ -16,7 +19,7 @@ struct PrefixArgs {
   int group;           // query heads of a key head
   int rows;            // B * group
   int pair;            // 1: a segment is 256 rows of a key head, else 128
-  int row_tiles;       // segments of a key head: segment = head * row_tiles + tile
+  int row_tiles;       // of a key head: segment = (head * row_tiles + tile) * halves + half
   int tiles;           // 128-key tiles of a segment
   int64_t total, per;  // tiles in all, of a block
   int box;             // rows of a TMA box: the power of two that divides page_size, to 128

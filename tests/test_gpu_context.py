@@ -63,6 +63,11 @@ SHARED = [  # fmt, B, hq, hk, D, page, prefix, own
     ("bf16", 160, 32, 16, 32, 48, 1400, [1] * 160),
     ("mxfp8", 80, 32, 8, 64, 16, 3050, [b % 3 for b in range(80)]),
     ("mxfp4", 33, 32, 32, 64, 64, 2000, [b % 3 for b in range(33)]),
+    # heads above 128, whose values two segments share
+    ("bf16", 20, 16, 8, 160, 16, 3100, [b % 4 for b in range(20)]),
+    ("bf16", 160, 16, 8, 256, 48, 1400, [1] * 160),
+    ("bf16", 33, 6, 6, 136, 64, 1999, [b % 3 for b in range(33)]),
+    ("bf16", 20, 100, 100, 192, 16, 140, [0] * 20),
     # more segments than blocks
     ("bf16", 20, 200, 200, 16, 16, 100, [0] * 20),
     ("mxfp8", 150, 200, 200, 32, 16, 130, [b % 2 for b in range(150)]),
