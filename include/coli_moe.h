@@ -468,8 +468,8 @@ int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg
  * cfg->window has to be 0. A prefix page outside the pool is left out and latches
  * COLI_EDEVICE. The prefix's products take bf16 and MX operands as bf16 (MX keys
  * and values outside bf16's range are rounded to it, as coli_kv_read does) or,
- * for few rows (B * n_q_heads / n_kv_heads) and F32, as coli_paged_attention
- * does; softmax weights in 16 bits. scratch: 16-byte aligned, the bytes that
+ * for few rows (B * n_q_heads / n_kv_heads), F32 and MX heads above 128, as
+ * coli_paged_attention does; softmax weights in 16 bits. scratch: 16-byte aligned, the bytes that
  * coli_shared_attention_scratch_bytes says, contents irrelevant; calls that may
  * overlap need their own. */
 size_t coli_shared_attention_scratch_bytes(const coli_kv_cache* cache, int32_t B,
@@ -485,8 +485,8 @@ int coli_shared_attention(const coli_kv_cache* cache, const coli_attn_config* cf
  * listed. bounds is [n_pages][n_kv_heads][2][head_dim] in the act dtype, 16-byte
  * aligned: the values that coli_kv_read gives, so exact where those are. A NaN key
  * makes its channel's bounds NaN. A page of -1 is skipped; other pages outside
- * the pool and fills outside 1..page_size are skipped and latch COLI_EDEVICE. A decode
- * step calls it for the pages it has just written to, a prompt for all of its pages. */
+ * the pool and fills outside 1..page_size are skipped and latch COLI_EDEVICE; a page
+ * listed twice needs the same fill. A decode step calls it for the pages it has just written to, a prompt for all of its pages. */
 int coli_page_bounds(const coli_kv_cache* cache, const int32_t* pages, const int32_t* fills,
                      int32_t N, void* bounds, void* stream);
 
