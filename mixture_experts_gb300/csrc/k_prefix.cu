@@ -277,7 +277,9 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
     const int X = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + X * 128, t_o = lanes + kOCol + X * 128;
-    const float sl = fabsf(p.scale) * 1.4426950408889634f;  // the sign went into Q
+    // the sign went into Q; never 0, which times a hidden score's -inf is NaN (2^-149 times any
+    // finite score is below 2^-21, which weights do not show)
+    const float sl = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 0x1p-149f);
     // the piece's queries: 128 rows by all softmax warps, their sign that of the scale
     auto load_queries = [&](const Walk& w) {
       const int h = head_of(w), r0 = tile_of(w) * kSegRows;

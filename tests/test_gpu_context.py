@@ -184,6 +184,27 @@ def test_shared_prefix_of_large_scores_and_values(fmt):
 
 
 # ---- bounds and choice of pages ------------------------------------------------------------
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-45])
+@pytest.mark.parametrize("fmt,B,D", [("bf16", 40, 128), ("bf16", 80, 128), ("bf16", 40, 192),
+                                     ("bf16", 1, 64), ("mxfp8", 80, 64), ("f32", 40, 64)])
+def test_shared_prefix_without_scale(fmt, B, D, scale):
+    # every token in sight weighs the same, what is behind the prefix in its last tile nothing
+    g = ref.gen(B, D)
+    cache, k, v = ref.pool(g, fmt, 40, 16, 1, D)
+    q = queries(g, B, 4, D, fmt)
+    pre = torch.arange(40, dtype=torch.int32)
+    table = torch.full((B, 1), -1, dtype=torch.int32).cuda()
+    lens = torch.zeros(B, dtype=torch.int32).cuda()
+    for n in (601, 130, 7):
+        rows = [ref.context(x, pre.tolist(), 0, n) for x in (k, v)]
+        want, wl, tol, tl = attn_ref.attend(q, lambda b, h: rows[0], lambda b, h: rows[1], [n] * B,
+                                            1, scale)
+        out, lse = cache.attend_shared(q, pre.cuda(), n, table, lens, scale=scale, return_lse=True)
+        tol = tol * (1 + out_step(fmt)) + out_step(fmt) * want.abs()
+        assert ((out.cpu().double() - want).abs() <= tol).all()
+        assert ((lse.cpu().double() - wl).abs() <= tl).all()
+
+
 @pytest.mark.parametrize("fmt", list(ref.FMT))
 @pytest.mark.parametrize("page,hk,D", [(16, 1, 8), (16, 2, 64), (48, 3, 80), (64, 2, 128),
                                        (32, 1, 256), (128, 2, 96), (16, 4, 32)])
