@@ -500,14 +500,16 @@ __global__ void __launch_bounds__(threads<FMT>(), 1) k_prefix(const PrefixArgs p
               mma_ss(tmem + (u & 1) * 128, sw128_desc(q0 + part * kTileBytes + off),
                      sw128_desc(k0 + off), kIdS, part != 0 || k != 0 ? 1u : 0u);
             }
+            if (part == kHalves - 1) {
+              mma_commit(smem_u32(&C.s_full[u & 1]));
+              if (u == units - 1) mma_commit(smem_u32(&C.q_free));
+            }
             if (!PAIR || u % 2 == 1) {
               mma_commit(smem_u32(&C.kfree[ks]));
               if (++ks == kStagesK) ks = 0, kp ^= 1u;
             }
           }
           if (!ok) break;
-          mma_commit(smem_u32(&C.s_full[u & 1]));
-          if (u == units - 1) mma_commit(smem_u32(&C.q_free));
         }
         if (u == 0) continue;
         const int X = (u - 1) & 1;

@@ -125,7 +125,7 @@ size_t part_bytes(const KvView& c, int64_t rows) { return mean_bytes(c, rows) + 
 // 16 / 24 / 64 queries of a key head: bf16 heads of 128 43 / 44 / 44 / 47 against 45 / 56 /
 // 57 / 81, MXFP8 44 / 51 / 50 / 52 against 43 / 57 / 82 / 116, MXFP4 heads of 64 42 / 42 / 42 /
 // 42 against 34 / 38 / 45 / 60; behind 1024 both are bound by the host (28 to 31). bf16 heads of
-// 256 at 12 / 32 / 128 / 256 queries 83 / 83 / 96 / 161 against 91 / 126 / 344 / 606, behind 2048
+// 256 at 12 / 32 / 128 / 256 queries 79 / 80 / 92 / 161 against 91 / 126 / 344 / 606, behind 2048
 // (12, 32) 27 / 28 against 34 / 38; heads of 160 73 / 72 (12, 32) against 74 / 108. MX heads above
 // 128, whose codes would not fit beside what they are widened to, stay with the decode kernel.
 // (k_prefix numbers the pool's rows in 31 bits.)
