@@ -2,7 +2,7 @@
 // or the decode kernel with all queries as one group), each sequence's own tokens by the decode
 // kernel, whose first blocks start under k_prefix's last, and a join. 64 sequences behind
 // 32768 bf16 tokens with up to 512 of their own: 76 us, of which k_prefix 54; 128 behind 40009
-// MXFP8 ones with up to 1000: 264 us, 201 of them k_prefix.
+// MXFP8 ones with up to 1000: 266 us, 201 of them k_prefix.
 #include "paged.cuh"
 #include "prefix.h"
 
