@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(kPickThreads) k_page_pick(const SelectArgs p) 
       }
     __syncthreads();
     const int m = s_n;
+    __syncthreads();  // (every warp has read it before the loop below starts it again)
     if (m <= kFew) {
       exact_scores<T, kPickThreads>(p, b, h, table, s_list, m, s_exact, s_nan);
       const int left = p.keep - (within - m);  // places for them
