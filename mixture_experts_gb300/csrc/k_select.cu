@@ -32,8 +32,9 @@ struct ScoreArgs {
   int chunks;  // blocks of a (sequence, key head)
 };
 
+// (2^-116: what sums below fp32's normal range lose, 512 products of 2^-126 at most)
 COLI_DEV float score_error(float score, float sum, float unit) {
-  return score != score || fabsf(score) == INFINITY ? INFINITY : sum * unit;
+  return score != score || fabsf(score) == INFINITY ? INFINITY : fmaf(sum, unit, 0x1p-116f);
 }
 
 template <int DP>

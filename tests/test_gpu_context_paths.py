@@ -92,3 +92,22 @@ def test_select_with_more_equal_pages_than_are_ranked_at_once(B, hk, count, fmt)
                                        first, last)
             assert torch.equal(got, want.int())
             assert held.tolist() == [int(n) - max(0, -(-int(n) // 16) - keep) * 16 for n in lens]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f32", "mxfp8"])
+@pytest.mark.parametrize("count", [100, 2000])
+def test_select_among_scores_that_fp32_does_not_hold(fmt, count):
+    # products of 2^-140 and below: fp32 sums of them are a few multiples of 2^-149, or 0
+    g = ref.gen(count, 5)
+    D, keep = 64, 20
+    cache, _, _ = ref.pool(g, fmt, count, 16, 1, D)
+    bounds = cache.new_bounds()
+    bounds.copy_(torch.randn(count, 1, 2, D, generator=g).sort(2).values * 2.0 ** -76)
+    q = (torch.randn(2, 3, D, generator=g) * 2.0 ** -70).to(ref.act(fmt))
+    table = torch.stack([torch.randperm(count, generator=g) for _ in range(2)]).int()
+    lens = torch.tensor([count * 16, count * 16 - 7], dtype=torch.int32)
+    scores = page_scores(q, bounds)
+    want = torch.tensor([[best_pages(scores[b, 0], table[b], count, keep, 1, 1)]
+                         for b in range(2)])
+    got, _ = choose_guarded(cache, q.cuda(), bounds, table.cuda(), lens.cuda(), keep, 1, 1)
+    assert torch.equal(got, want.int())
