@@ -463,8 +463,8 @@ int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg
  * sequence b sees the prefix_len tokens of the pages prefix_pages [ceil(prefix_len /
  * page_size)], then its own seq_lens[b] tokens (0 or more; the new one among
  * them) in block_table[b]. Same result as coli_paged_attention over both, but the
- * prefix is read once for all sequences. prefix_len is a host number (0: no
- * prefix, prefix_pages may be NULL); own tokens begin a page of their own.
+ * prefix is read once for all sequences. prefix_len is a host number, up to
+ * 2^31 - 2^16 (0: no prefix, prefix_pages may be NULL); own tokens begin a page of their own.
  * cfg->window has to be 0. A prefix page outside the pool is left out and latches
  * COLI_EDEVICE. The prefix's products take bf16 and MX operands as bf16 (MX keys
  * and values outside bf16's range are rounded to it, as coli_kv_read does) or,

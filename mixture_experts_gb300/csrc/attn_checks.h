@@ -125,6 +125,10 @@ inline int check_tokens(const char* name, int T) {
   return COLI_OK;
 }
 
+// Tokens or entries of a list that the calls for long contexts take: their kernels count up to
+// a block's stride or a look-ahead past the last one, in 32 bits.
+constexpr int64_t kMostPlaces = (int64_t{1} << 31) - (1 << 16);
+
 // One call's sequences: their number, the query heads and the tables of their pages.
 inline int check_sequences(const KvView& c, int B, int n_q_heads, const int32_t* block_table,
                            int max_pages, const int32_t* seq_lens) {

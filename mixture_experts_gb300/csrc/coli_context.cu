@@ -77,8 +77,8 @@ int coli_shared_attention(const coli_kv_cache* cache, const coli_attn_config* cf
   if (int rc = check_cache(cache, &c)) return rc;
   if (int rc = check_attention(c, cfg, q, q_stride, B, block_table, max_pages, seq_lens))
     return rc;
-  if (prefix_len < 0 || prefix_len > INT32_MAX - c.page_size)
-    return reject(COLI_EINVAL, "prefix_len=%d outside [0, 2^31 - page_size)", prefix_len);
+  if (prefix_len < 0 || prefix_len > kMostPlaces)
+    return reject(COLI_EINVAL, "prefix_len=%d outside [0, 2^31 - 2^16]", prefix_len);
   if (B == 0) return COLI_OK;
   if (prefix_len > 0)
     if (int rc = check_words("prefix_pages", prefix_pages)) return rc;
