@@ -142,9 +142,9 @@ inline int check_sequences(const KvView& c, int B, int n_q_heads, const int32_t*
     return reject(COLI_EINVAL, "B=%d sequences of %d heads are too many", B, n_q_heads);
   if (int rc = check_words("block_table", block_table)) return rc;
   if (int rc = check_words("seq_lens", seq_lens)) return rc;
-  if (max_pages < 1 || static_cast<int64_t>(max_pages) * c.page_size > INT32_MAX)
-    return reject(COLI_EINVAL, "max_pages=%d: need 1 or more and max_pages * page_size < 2^31",
-                  max_pages);
+  if (max_pages < 1 || static_cast<int64_t>(max_pages) * c.page_size > kMostPlaces)
+    return reject(COLI_EINVAL, "max_pages=%d: need 1 or more and max_pages * page_size up to "
+                  "2^31 - 2^16", max_pages);
   return COLI_OK;
 }
 

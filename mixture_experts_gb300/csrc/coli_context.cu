@@ -113,7 +113,7 @@ int coli_page_bounds(const coli_kv_cache* cache, const int32_t* pages, const int
 size_t coli_select_pages_scratch_bytes(const coli_kv_cache* cache, int32_t B, int32_t max_pages) {
   KvView c;
   if (check_cache(cache, &c) || B < 1 || B > 65535 || max_pages < 1 ||
-      static_cast<int64_t>(max_pages) * c.page_size > INT32_MAX)
+      static_cast<int64_t>(max_pages) * c.page_size > kMostPlaces)
     return 0;
   return static_cast<size_t>(B) * c.n_heads * max_pages * sizeof(float2);
 }

@@ -31,3 +31,18 @@ def refused(name, c=None, **kw):
 def test_prefixes_near_two_to_the_31(dtype, length):
     # tiles of 128 tokens are counted, and pages looked up 512 tokens ahead, past the last token
     refused("coli_shared_attention", c=cache(dtype=dtype), prefix_len=length)
+
+
+@pytest.mark.parametrize("page,max_pages", [(16, 2 ** 27 - 4095), (16, 2 ** 27 - 1),
+                                            (48, (2 ** 31 - 1) // 48), (4096, 2 ** 19 - 15),
+                                            (4096, 2 ** 19 - 1)])
+@pytest.mark.parametrize("name", ["coli_shared_attention", "coli_select_pages",
+                                  "coli_selected_attention", "coli_attention_mass",
+                                  "coli_kv_evict"])
+def test_contexts_near_two_to_the_31(name, page, max_pages):
+    # a context's pages are counted from its last token + page_size - 1, and its tokens by strides
+    # of up to 1024 past the last
+    refused(name, c=cache(page_size=page, n_pages=4), max_pages=max_pages)
+    assert moe.coli_select_pages_scratch_bytes(cache(page_size=page, n_pages=4), 1, max_pages) == 0
+    assert moe.coli_select_pages_scratch_bytes(cache(page_size=page, n_pages=4), 1,
+                                               MOST // page) == 2 * 8 * (MOST // page)
