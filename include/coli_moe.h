@@ -458,7 +458,7 @@ int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg
  * Three ways to read less of the cache at a decode step. Arrays are the caller's, as
  * above; q, out, strides, block_table, seq_lens, lse and what is skipped and
  * latched are as for coli_paged_attention where not said otherwise; max_pages *
- * page_size is 2^31 - 2^16 at most. */
+ * page_size is 2^31 - 2^16 at most, and so are lists (`keep`). */
 
 /* Attention of one new token a sequence, B sequences behind one shared prefix:
  * sequence b sees the prefix_len tokens of the pages prefix_pages [ceil(prefix_len /

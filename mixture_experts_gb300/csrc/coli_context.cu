@@ -49,6 +49,8 @@ int check_out(const KvView& c, const coli_attn_config* cfg, const void* q, const
 
 // A list of `keep` entries for each sequence and key head.
 int check_list(const char* name, int keep, int B, const KvView& c) {
+  if (keep > kMostPlaces)
+    return reject(COLI_EINVAL, "%s=%d is above 2^31 - 2^16", name, keep);
   if (static_cast<int64_t>(keep) * B * c.n_heads > INT32_MAX)
     return reject(COLI_EINVAL, "%s=%d for %d sequences of %d key heads: 2^31 entries or more", name,
                   keep, B, c.n_heads);
@@ -217,10 +219,10 @@ int coli_kv_evict(const coli_kv_cache* cache, float* mass, int32_t B, const int3
     into_pages = max_pages;
   } else {
     if (int rc = check_words("into", into)) return rc;
-    if (into_pages < 1 || static_cast<int64_t>(into_pages) * c.page_size > INT32_MAX ||
+    if (into_pages < 1 || static_cast<int64_t>(into_pages) * c.page_size > kMostPlaces ||
         static_cast<int64_t>(into_pages) * c.page_size < keep)
-      return reject(COLI_EINVAL, "into_pages=%d pages of %d tokens: need room for keep=%d and less "
-                    "than 2^31", into_pages, c.page_size, keep);
+      return reject(COLI_EINVAL, "into_pages=%d pages of %d tokens: need room for keep=%d and "
+                    "2^31 - 2^16 at most", into_pages, c.page_size, keep);
   }
   if (B == 0) return COLI_OK;
   if (int rc = check_list("keep", keep, B, c)) return rc;

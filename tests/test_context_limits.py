@@ -46,3 +46,17 @@ def test_contexts_near_two_to_the_31(name, page, max_pages):
     assert moe.coli_select_pages_scratch_bytes(cache(page_size=page, n_pages=4), 1, max_pages) == 0
     assert moe.coli_select_pages_scratch_bytes(cache(page_size=page, n_pages=4), 1,
                                                MOST // page) == 2 * 8 * (MOST // page)
+
+
+@pytest.mark.parametrize("keep", [MOST + 1, 2 ** 31 - 1024, 2 ** 31 - 64, 2 ** 31 - 1])
+def test_lists_near_two_to_the_31(keep):
+    # a block walks a list in strides of up to 1024 entries
+    one = dict(c=cache(n_kv_heads=1), B=1, keep=keep)
+    refused("coli_select_pages", n_q_heads=4, **one)
+    refused("coli_kv_evict", into=None, **one)
+    refused("coli_kv_evict", into=None, max_pages=1, first=0, recent=0, **one)
+
+
+@pytest.mark.parametrize("into_pages", [2 ** 27 - 4095, 2 ** 27 - 1])
+def test_new_pages_near_two_to_the_31(into_pages):
+    refused("coli_kv_evict", c=cache(n_kv_heads=1), B=1, into_pages=into_pages)
