@@ -111,3 +111,105 @@ def test_select_among_scores_that_fp32_does_not_hold(fmt, count):
                          for b in range(2)])
     got, _ = choose_guarded(cache, q.cuda(), bounds, table.cuda(), lens.cuda(), keep, 1, 1)
     assert torch.equal(got, want.int())
+
+
+@pytest.mark.parametrize("fmt,B,hk,D,count", [("bf16", 32, 8, 64, 1300), ("bf16", 64, 8, 128, 1100),
+                                              ("bf16", 40, 8, 192, 1500), ("f32", 32, 8, 80, 900)])
+def test_select_of_many_long_lists(fmt, B, hk, D, count):
+    # more pages than the blocks of a list take at a time
+    g = ref.gen(B, hk, D, count)
+    n_pages = 2500
+    keys = torch.zeros(n_pages, hk, 16, D, dtype=ref.act(fmt), device="cuda")    # not read
+    cache = moe.PagedKVCache(keys, keys, head_dim=D)
+    bounds = cache.new_bounds()
+    bounds.copy_(torch.randn(n_pages, hk, 2, D, generator=g).sort(2).values)
+    table = torch.stack([torch.randperm(n_pages, generator=g)[:count] for _ in range(B)]).int()
+    lens = torch.randint(count // 3, count, (B,), generator=g).int() * 16 + 3
+    lens[1] = count * 16
+    q = torch.randn(B, 3 * hk, D, generator=g).to(ref.act(fmt))
+    scores = page_scores(q, bounds)
+    keep, first, last = 50, 1, 2
+    want = torch.tensor([[best_pages(scores[b, h], table[b], -(-int(lens[b]) // 16), keep, first,
+                                     last) for h in range(hk)] for b in range(B)])
+    got, held = choose_guarded(cache, q.cuda(), bounds, table.cuda(), lens.cuda(), keep, first,
+                               last)
+    assert torch.equal(got, want.int())
+    assert held.tolist() == [int(n) - max(0, -(-int(n) // 16) - keep) * 16 for n in lens]
+
+
+# ---- attention mass --------------------------------------------------------------------------
+def masses(cache, k, q, table, lens, window, scale, known, before):
+    """(want, tolerance) of accumulate over `before`, fp64 [n_pages][n_kv_heads][page_size]."""
+    n_pages, hk, page = before.shape
+    G = q.shape[1] // hk
+    _, lse = cache.attend(q, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                          window=window, scale=scale, return_lse=True)
+    want, tol = before.double(), torch.zeros(before.shape, dtype=torch.float64)
+    qd, ld = q.double().cpu(), lse.double().cpu()
+    for b, n in enumerate(lens):
+        lo = max(0, n - window) if window else 0
+        j = torch.arange(lo, n)
+        at = table[b].long()[j // page]
+        for h in range(hk):
+            r = slice(h * G, (h + 1) * G)
+            w, t = ref.mass(qd[b, r], k[at, h, j % page], ld[b, r], scale)
+            old = torch.where(j >= known[b], 0.0, want[at, h, j % page])
+            want[at, h, j % page] = old + w
+            # groups are added 8 or 16 heads at a time
+            tol[at, h, j % page] = t + (1 + G // 8) * 2.0 ** -24 * (old + w)
+    return want, tol, lse
+
+
+MASS = [  # fmt, B, hq, hk, D, page, longest, window: several tiles a warp
+    ("bf16", 64, 16, 8, 64, 16, 1500, 0), ("bf16", 64, 32, 8, 128, 48, 1100, 0),
+    ("bf16", 150, 20, 1, 80, 128, 3000, 1777), ("f32", 64, 16, 8, 64, 48, 1000, 0),
+    ("f32", 100, 20, 2, 128, 16, 1900, 900), ("f32", 64, 8, 4, 256, 128, 800, 0),
+    ("mxfp8", 64, 16, 8, 64, 48, 1500, 0), ("mxfp8", 64, 8, 4, 128, 16, 1300, 1000),
+    ("mxfp8", 100, 40, 2, 256, 128, 1400, 0), ("mxfp4", 64, 32, 8, 64, 128, 1600, 0),
+    ("mxfp4", 150, 18, 1, 128, 48, 3000, 0), ("mxfp4", 64, 24, 4, 96, 16, 1200, 700)]
+
+
+@pytest.mark.parametrize("fmt,B,hq,hk,D,page,longest,window", MASS)
+def test_attention_mass_of_many_contexts(fmt, B, hq, hk, D, page, longest, window):
+    g = ref.gen(B, hq, D, page)
+    lens = torch.randint(0, longest + 1, (B,), generator=g).tolist()
+    lens[:4] = [longest, 0, 1, longest - 1]
+    n_pages = sum(-(-n // page) for n in lens) + 2
+    cache, k, _ = ref.pool(g, fmt, n_pages, page, hk, D)
+    table = ref.tables(g, lens, page, n_pages)
+    q = torch.randn(B, hq, D, generator=g).to(ref.act(fmt)).cuda()
+    before = torch.rand(n_pages, hk, page, generator=g)
+    known = [max(0, n - 1 - b % 30) for b, n in enumerate(lens)]
+    want, tol, lse = masses(cache, k, q, table, lens, window, D ** -0.5, known, before)
+    tl, tk = (torch.tensor(x, dtype=torch.int32).cuda() for x in (lens, known))
+    got = cache.accumulate(before.cuda(), q, table.cuda(), tl, lse, window=window, known=tk)
+    assert ((got.cpu().double() - want).abs() <= tol).all()
+    again = cache.accumulate(before.cuda(), q, table.cuda(), tl, lse, window=window, known=tk)
+    assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("hq,D", [(3, 64), (20, 128), (6, 256), (12, 96)])
+@pytest.mark.parametrize("kind", ["spread", "small", "large"])
+def test_attention_mass_of_queries_beyond_fp16(kind, hq, D, fmt):
+    # elements 2^35 apart, or heads of 2^-90 or 2^90: fp16 holds no multiple of them
+    g = ref.gen(hq, D, 4)
+    lens = [700, 33]
+    cache, k, _ = ref.pool(g, fmt, 60, 16, 1, D)
+    table = ref.tables(g, lens, 16, 60)
+    q = torch.randn(2, hq, D, generator=g)
+    scale = D ** -0.5
+    if kind == "spread":
+        q[..., ::2] *= 2.0 ** 20
+        q[..., 1::2] *= 2.0 ** -15
+        scale *= 2.0 ** -20
+    else:
+        e = 90.0 if kind == "large" else -90.0
+        q *= 2.0 ** e
+        scale *= 2.0 ** -e
+    q = q.bfloat16().cuda()
+    before = torch.rand(60, 1, 16, generator=g)
+    want, tol, lse = masses(cache, k, q, table, lens, 0, scale, lens, before)
+    got = cache.accumulate(before.cuda(), q, table.cuda(),
+                           torch.tensor(lens, dtype=torch.int32).cuda(), lse, scale=scale)
+    assert ((got.cpu().double() - want).abs() <= tol).all()
