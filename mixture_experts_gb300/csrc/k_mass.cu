@@ -8,7 +8,8 @@
 // keys). The keys come from memory straight into the operand's registers: of every 32
 // channels lane 4g + t has 8t .. + 7 of rows g and g + 8, on both operands. bf16 queries
 // and keys are operands as they are; MX codes are widened to fp16, against fp16 queries, and a
-// block's scale goes on its sum (queries that fp16 does not hold meet bf16 keys); fp32 runs in three tf32 products of operands in two parts.
+// block's scale goes on its sum (queries that fp16 does not hold, or far from 1, meet bf16 keys);
+// fp32 runs in three tf32 products of operands in two parts.
 //
 // 32 bf16 contexts of up to 8192 tokens, 32 heads on 8 of 128 (302 MB): 51 us, 5.9 TB/s, HBM
 // bound. 16 MXFP4 contexts of up to 60000, 64 heads on 4 (145 MB): 64 us, 2.3 TB/s: a quarter of
@@ -113,9 +114,13 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
       }
     }
     // MX: queries in fp16, the head's largest element at 2^14, where that is exact (no element
-    // but 0 below 2^-31 of it): codes are fp16 numbers, and their scale goes on a block's sum
+    // but 0 below 2^-31 of it): codes are fp16 numbers, and their scale goes on a block's sum.
+    // For heads of 2^-24 to 2^40 and scales of 2^-24 to 2^24: a block's sum, up to 2^29, passes
+    // fp32's range then only where scores are 2^(96 - 24 - 24) and more, and the least block
+    // scale, which counts as 0, is worth 2^(41 + 24 - 127 + 9 + 8) at most.
     float scale[NT][2];
-    bool half = kMx;
+    const float size = fabsf(p.scale);
+    bool half = kMx && size >= 0x1p-24f && size <= 0x1p24f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) scale[nt][0] = scale[nt][1] = p.scale;
     if constexpr (kMx) {
@@ -131,8 +136,8 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         e[nt] = top == 0 ? 0 : static_cast<int>(top >> 23) - 127;
-        half = half && e[nt] <= 80 && e[nt] >= -80;
-        const uint32_t least = static_cast<uint32_t>(max(e[nt], -80) - 31 + 127) << 23;
+        half = half && e[nt] <= 40 && e[nt] >= -24;
+        const uint32_t least = static_cast<uint32_t>(max(e[nt], -24) - 31 + 127) << 23;
 #pragma unroll
         for (int j = 0; j < kJ; ++j)
 #pragma unroll
@@ -156,6 +161,15 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
 #pragma unroll
           for (int c = 0; c < 2; ++c)
             scale[nt][c] = p.scale * __shfl_sync(0xffffffffu, down, 8 * t + 4 * c) * (1.f - 0x1p-23f);
+        }
+      } else {
+        // keys below bf16's normal range, which show against large heads or scales, go in times 2^64
+        bool large = size > 0x1p24f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) large = large || e[nt] > 40;
+        if (__any_sync(0xffffffffu, large) && size >= 0x1p-24f) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) scale[nt][0] = scale[nt][1] = p.scale * 0x1p-64f;
         }
       }
     }
@@ -302,6 +316,7 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
         } else {
 #pragma unroll 1
           for (int j = 0; j < kJ; ++j) {  // rare: widened to bf16 with their scale
+            const float up = scale[0][0] == p.scale ? 1.f : 0x1p64f;
             uint32_t w[2][2], k0[4], k1[4], qj[NT][4];
             const int last = bytes8<FMT>() / 4 - 1;
             float f[2];
@@ -311,7 +326,7 @@ __global__ void __launch_bounds__(kMassWarps * 32) k_mass(const MassGrid a) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 w[e][0] = raw[i][e].w[0], w[e][1] = raw[i][e].w[last];
-                f[e] = e8m0_f32(sc[e][i / 4] >> 8 * (i % 4) & 0xffu);
+                f[e] = e8m0_f32(sc[e][i / 4] >> 8 * (i % 4) & 0xffu) * up;
               }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)

@@ -138,12 +138,14 @@ def test_select_of_many_long_lists(fmt, B, hk, D, count):
 
 
 # ---- attention mass --------------------------------------------------------------------------
-def masses(cache, k, q, table, lens, window, scale, known, before):
-    """(want, tolerance) of accumulate over `before`, fp64 [n_pages][n_kv_heads][page_size]."""
+def masses(cache, k, q, table, lens, window, scale, known, before, lse=None):
+    """(want, tolerance) of accumulate over `before`, fp64 [n_pages][n_kv_heads][page_size],
+    and the lse that it is given (None: attend's)."""
     n_pages, hk, page = before.shape
     G = q.shape[1] // hk
-    _, lse = cache.attend(q, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
-                          window=window, scale=scale, return_lse=True)
+    if lse is None:
+        _, lse = cache.attend(q, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                              window=window, scale=scale, return_lse=True)
     want, tol = before.double(), torch.zeros(before.shape, dtype=torch.float64)
     qd, ld = q.double().cpu(), lse.double().cpu()
     for b, n in enumerate(lens):
@@ -212,4 +214,37 @@ def test_attention_mass_of_queries_beyond_fp16(kind, hq, D, fmt):
     want, tol, lse = masses(cache, k, q, table, lens, 0, scale, lens, before)
     got = cache.accumulate(before.cuda(), q, table.cuda(),
                            torch.tensor(lens, dtype=torch.int32).cuda(), lse, scale=scale)
+    assert ((got.cpu().double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("kind", ["far keys", "small scale", "least keys"])
+def test_attention_mass_of_extreme_scales(kind, fmt):
+    # scores of ordinary size from factors at the ends of their ranges
+    g = ref.gen(91)
+    D, lens = 64, [100, 17]
+    cache, _, _ = ref.pool(g, fmt, 12, 16, 1, D)
+    q = torch.randn(2, 4, D, generator=g)
+    scale = D ** -0.5
+    if kind == "far keys":
+        cache.k_scale[..., :2] = 127 + 112
+        q *= 2.0 ** -77
+        scale *= 2.0 ** -35
+    elif kind == "small scale":
+        cache.k_scale[..., :2] = 127 + 112
+        scale *= 2.0 ** -112
+    else:                                            # 2^-127, the least scale there is
+        cache.k_scale[..., :2] = 0
+        q *= 2.0 ** 77
+        scale *= 2.0 ** 50
+    k = attn_ref.decode(cache.k, cache.k_scale, fmt)
+    table = ref.tables(g, lens, 16, 12)
+    q = q.bfloat16().cuda()
+    before = torch.rand(12, 1, 16, generator=g)
+    lse = torch.stack([torch.logsumexp(scale * q[b].double().cpu() @ ref.context(
+        k, table[b].tolist(), 0, n).T, -1) for b, n in enumerate(lens)]).float().cuda()
+    want, tol, _ = masses(cache, k, q, table, lens, 0, scale, lens, before, lse)
+    got = cache.accumulate(before.cuda(), q, table.cuda(),
+                           torch.tensor(lens, dtype=torch.int32).cuda(), lse, scale=scale)
+    assert torch.isfinite(got).all()
     assert ((got.cpu().double() - want).abs() <= tol).all()
