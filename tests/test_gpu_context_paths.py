@@ -248,3 +248,336 @@ def test_attention_mass_of_extreme_scales(kind, fmt):
                            torch.tensor(lens, dtype=torch.int32).cuda(), lse, scale=scale)
     assert torch.isfinite(got).all()
     assert ((got.cpu().double() - want).abs() <= tol).all()
+
+
+# ---- shared prefix ---------------------------------------------------------------------------
+def shared_case(fmt, hq, hk, D, page, prefix, own):
+    """(cache, q, prefix pages, table, lens, k_of, v_of) of a batch behind a prefix."""
+    g = ref.gen(len(own), hq, D, prefix)
+    n_pre = -(-prefix // page)
+    n_pages = n_pre + sum(-(-n // page) for n in own) + 2
+    cache, k, v = ref.pool(g, fmt, n_pages, page, hk, D)
+    pre = torch.randperm(n_pages, generator=g)[:n_pre].int()
+    table = ref.tables(g, own, page, n_pages, pre.tolist())
+    q = torch.randn(len(own), hq, D, generator=g).to(ref.act(fmt)).cuda()
+    ahead = [[ref.context(x, pre.tolist(), h, prefix) for h in range(hk)] for x in (k, v)]
+
+    def of(rows, first):
+        return lambda b, h: torch.cat([first[h], ref.context(rows, table[b].tolist(), h, own[b])])
+
+    return (cache, q, pre.cuda(), table.cuda(), torch.tensor(own, dtype=torch.int32).cuda(),
+            of(k, ahead[0]), of(v, ahead[1]))
+
+
+def held(out, lse, want, want_lse, tol, tol_lse, fmt):
+    tol = tol * (1 + out_step(fmt)) + out_step(fmt) * want.abs()
+    return ((out.cpu().double() - want).abs() <= tol).all() and \
+        ((lse.cpu().double() - want_lse).abs() <= tol_lse).all()
+
+
+SOME = [0, 1, 700, 3000, 17, 16, 513, 0, 1200]
+OWN_CUT = [  # fmt, hq, hk, D, page, prefix, own: the own tokens are cut in pieces
+    ("bf16", 32, 8, 64, 16, 5000, SOME), ("bf16", 16, 2, 128, 48, 20001, SOME[:3]),
+    ("bf16", 12, 1, 256, 16, 3000, [2999]), ("bf16", 24, 2, 80, 64, 1000, SOME * 4),
+    ("mxfp8", 32, 8, 64, 16, 5000, SOME), ("mxfp8", 16, 2, 128, 48, 20001, [700, 400, 0]),
+    ("mxfp8", 24, 2, 96, 64, 1000, SOME * 4), ("mxfp4", 32, 8, 64, 32, 5000, SOME),
+    ("mxfp4", 64, 4, 128, 16, 9000, SOME), ("mxfp4", 24, 2, 32, 64, 1000, SOME * 4),
+    # few queries a key head, and fp32: the decode kernel takes the prefix too
+    ("bf16", 8, 8, 64, 16, 3000, [900, 0, 2500]), ("mxfp8", 4, 4, 128, 16, 3000, [900, 0, 2500]),
+    ("f32", 12, 4, 64, 16, 3000, SOME), ("f32", 8, 2, 128, 48, 900, SOME * 4)]
+
+
+@pytest.mark.parametrize("fmt,hq,hk,D,page,prefix,own", OWN_CUT)
+def test_shared_prefix_with_long_own_contexts(fmt, hq, hk, D, page, prefix, own):
+    cache, q, pre, table, lens, k_of, v_of = shared_case(fmt, hq, hk, D, page, prefix, own)
+    want = attn_ref.attend(q, k_of, v_of, [prefix + n for n in own], hk, D ** -0.5)
+    call = lambda: cache.attend_shared(q, pre, prefix, table, lens, return_lse=True)
+    out, lse = call()
+    assert held(out, lse, *want, fmt)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = call()
+    for _ in range(3):
+        again[0].fill_(7), again[1].fill_(7)
+        graph.replay()
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+        assert all(torch.equal(x, y) for x, y in zip(call(), (out, lse)))
+
+
+@pytest.mark.parametrize("fmt,own", [("bf16", [0, 1, 700, 3000] + [300] * 40), ("mxfp8", [600, 1] * 20),
+                                     ("mxfp4", [0, 2100] * 6)])
+def test_shared_prefix_that_outlasts_the_own_tokens(fmt, own):
+    # the own tokens are done while the prefix's products still run
+    hq, hk, D, page, prefix = 32, 4, 64, 64, 40000
+    cache, q, pre, table, lens, k_of, v_of = shared_case(fmt, hq, hk, D, page, prefix, own)
+    want = attn_ref.attend(q, k_of, v_of, [prefix + n for n in own], hk, D ** -0.5)
+    first = cache.attend_shared(q, pre, prefix, table, lens, return_lse=True)
+    assert held(*first, *want, fmt)
+    for _ in range(10):
+        again = cache.attend_shared(q, pre, prefix, table, lens, return_lse=True)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
+MANY_ROWS = [  # fmt, B, hq, hk, D, page, prefix: prefixes that the decode kernel reads
+    ("f32", 40, 32, 4, 64, 16, 1500), ("f32", 130, 8, 2, 128, 48, 700),
+    ("f32", 33, 24, 1, 256, 16, 401), ("f32", 100, 3, 3, 80, 64, 2000),
+    ("mxfp8", 40, 16, 2, 160, 16, 900), ("mxfp8", 9, 4, 4, 256, 64, 2100),
+    ("mxfp4", 33, 8, 1, 256, 48, 777), ("mxfp4", 100, 10, 2, 192, 16, 300),
+    ("mxfp4", 3, 12, 4, 224, 32, 5000), ("mxfp8", 150, 40, 2, 192, 128, 200)]
+
+
+@pytest.mark.parametrize("fmt,B,hq,hk,D,page,prefix", MANY_ROWS)
+def test_shared_prefix_of_many_rows_on_the_decode_kernel(fmt, B, hq, hk, D, page, prefix):
+    own = [b % 37 for b in range(B)]
+    cache, q, pre, table, lens, k_of, v_of = shared_case(fmt, hq, hk, D, page, prefix, own)
+    want = attn_ref.attend(q, k_of, v_of, [prefix + n for n in own], hk, D ** -0.5)
+    out, lse = cache.attend_shared(q, pre, prefix, table, lens, return_lse=True)
+    assert held(out, lse, *want, fmt)
+    # pages that are left out
+    pre = torch.full_like(pre, -1)
+    out, lse = cache.attend_shared(q, pre, prefix, table, torch.zeros_like(lens), return_lse=True)
+    assert moe.coli_device_status() == moe.COLI_EDEVICE
+    assert not out.any() and (lse == -math.inf).all()
+
+
+ODD = [("bf16", 40, 64), ("bf16", 80, 128), ("bf16", 40, 256), ("bf16", 1, 64), ("f32", 40, 64)]
+
+
+@pytest.mark.parametrize("fmt,B,D", ODD)
+def test_shared_prefix_of_infinite_scores(fmt, B, D):
+    # keys of -inf weigh 0 (nothing else: zeros, -inf), keys of +inf and NaN make their own key
+    # head's rows NaN, wherever in the prefix they lie
+    g = ref.gen(B, D, 6)
+    dt, n = ref.act(fmt), 300
+    k = torch.ones(19, 5, 16, D, dtype=dt, device="cuda")
+    v = torch.randn(19, 5, 16, D, generator=g).to(dt).cuda()
+    k[:, 0] = -math.inf
+    k[3:11, 1], k[18, 1, 3] = -math.inf, -math.inf
+    k[17, 2, 5] = math.inf
+    k[9, 3, 2, 1] = math.nan
+    k[18, 4, 12:], v[18, 4, 12:] = math.nan, math.inf                # behind the prefix
+    cache = moe.PagedKVCache(k, v, head_dim=D)
+    q = torch.ones(B, 10, D, dtype=dt, device="cuda")
+    pre = torch.arange(19, dtype=torch.int32, device="cuda")
+    table = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    out, lse = cache.attend_shared(q, pre, n, table, lens, return_lse=True)
+    assert not out[:, :2].any() and (lse[:, :2] == -math.inf).all()
+    assert out[:, 4:8].isnan().all() and lse[:, 4:8].isnan().all()
+    for h, gone in ((1, list(range(48, 176)) + [18 * 16 + 3]), (4, [])):
+        keep = [j for j in range(n) if j not in gone]
+        rows = v[:, h].reshape(-1, D)[keep].double().cpu()
+        tol = 2.0 ** -8 if fmt == "bf16" else 2.0 ** -18
+        err = (out[:, 2 * h:2 * h + 2].double().cpu() - rows.mean(0)).abs()
+        assert (err <= tol * rows.abs().mean(0) + out_step(fmt) * rows.mean(0).abs()).all()
+        want = math.log(len(keep)) + D ** 0.5
+        assert ((lse[:, 2 * h:2 * h + 2] - want).abs() <= 2.0 ** -16 * want).all()
+
+
+@pytest.mark.parametrize("fmt,B,D", ODD)
+def test_shared_prefix_of_odd_values_and_queries(fmt, B, D):
+    # an infinite value makes its element infinite or NaN and no other; a NaN query its own row
+    cache, q, pre, table, lens, _, _ = shared_case(fmt, 8, 2, D, 16, 777, [b % 20 for b in range(B)])
+    want, want_lse = cache.attend_shared(q, pre, 777, table, lens, return_lse=True)
+    at = int(pre[30])
+    cache.v[at, 0, 5, 3], cache.v[at, 1, 6, D - 1] = math.inf, math.nan
+    out, lse = cache.attend_shared(q, pre, 777, table, lens, return_lse=True)
+    assert torch.equal(lse, want_lse)
+    hit = torch.zeros(8, D, dtype=torch.bool, device="cuda")
+    hit[:4, 3], hit[4:, D - 1] = True, True
+    assert not torch.isfinite(out[:, hit]).any() and torch.equal(out[:, ~hit], want[:, ~hit])
+    cache.v[at, 0, 5, 3], cache.v[at, 1, 6, D - 1] = 1.0, 1.0
+    want, want_lse = cache.attend_shared(q, pre, 777, table, lens, return_lse=True)
+    q[0, 1, 7] = math.nan
+    out, lse = cache.attend_shared(q, pre, 777, table, lens, return_lse=True)
+    assert out[0, 1].isnan().all() and lse[0, 1].isnan()
+    out[0, 1], lse[0, 1] = want[0, 1], want_lse[0, 1]
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("B,D", [(40, 64), (80, 128), (1, 64), (20, 256)])
+def test_shared_prefix_of_nan_blocks_and_codes(B, D, fmt):
+    own = [b % 20 for b in range(B)]
+    cache, q, pre, table, lens, k_of, v_of = shared_case(fmt, 8, 2, D, 16, 777, own)
+    exact = attn_ref.attend(q, k_of, v_of, [777 + n for n in own], 2, D ** -0.5)
+    call = lambda: cache.attend_shared(q, pre, 777, table, lens, return_lse=True)
+    want, want_lse = call()
+    at, old = int(pre[30]), cache.v_scale[int(pre[30]), 0, 5, 1].clone()
+    cache.v_scale[at, 0, 5, 1] = 255                                 # channels 32 to 63
+    out, lse = call()
+    assert out[:, :4, 32:64].isnan().all() and torch.equal(lse, want_lse)
+    out[:, :4, 32:64] = want[:, :4, 32:64]
+    assert held(out, lse, *exact, fmt)
+    cache.v_scale[at, 0, 5, 1] = old
+    if fmt == "mxfp8":
+        old = cache.v[at, 1, 9, 6].clone()
+        cache.v[at, 1, 9, 6] = 0x7f
+        out, lse = call()
+        assert out[:, 4:, 6].isnan().all() and torch.equal(lse, want_lse)
+        out[:, 4:, 6] = want[:, 4:, 6]
+        assert held(out, lse, *exact, fmt)
+        cache.v[at, 1, 9, 6] = old
+        old = cache.k[at, 1, 9, 6].clone()
+        cache.k[at, 1, 9, 6] = 0xff
+        out, lse = call()
+        assert out[:, 4:].isnan().all() and lse[:, 4:].isnan().all()
+        assert torch.equal(out[:, :4], want[:, :4]) and torch.equal(lse[:, :4], want_lse[:, :4])
+        cache.k[at, 1, 9, 6] = old
+    cache.k_scale[at, 0, 5, 0] = 255
+    out, lse = call()
+    assert out[:, :4].isnan().all() and lse[:, :4].isnan().all()
+    assert torch.equal(out[:, 4:], want[:, 4:]) and torch.equal(lse[:, 4:], want_lse[:, 4:])
+
+
+# ---- selected attention ----------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", list(ref.FMT))
+@pytest.mark.parametrize("n", [40, 1500])
+def test_selected_attention_of_odd_scores(fmt, n):
+    # each key head has pages of its own: what is odd in one of them stays with its head
+    hk, D, page, B = 4, 64, 16, 2
+    g = ref.gen(n, 8)
+    per = -(-n // page)
+    cache, k, v = ref.pool(g, fmt, B * hk * per, page, hk, D)
+    pages = torch.randperm(B * hk * per, generator=g).view(B, hk, per).int()
+    lens = torch.full((B,), n, dtype=torch.int32)
+    q = torch.randn(B, 3 * hk, D, generator=g).to(ref.act(fmt)).cuda()
+    of = lambda rows: lambda b, h: ref.context(rows, pages[b, h].tolist(), h, n)
+    exact = attn_ref.attend(q, of(k), of(v), [n] * B, hk, D ** -0.5)
+    call = lambda x=q: cache.attend_selected(x, pages.cuda(), lens.cuda(), return_lse=True)
+    want, want_lse = call()
+    assert held(want, want_lse, *exact, fmt)
+    # where a page lies in another head's list it is none of this one's keys
+    at = int(pages[0, 1, 2])
+    if fmt in attn_ref.EMAX:
+        old, old_v = cache.k_scale[at].clone(), cache.v_scale[at].clone()
+        cache.k_scale[at, :, 3, 0] = 255
+    else:
+        old, old_v = cache.k[at].clone(), cache.v[at].clone()
+        cache.k[at, :, 3, 0] = math.nan
+    out, lse = call()
+    assert out[0, 3:6].isnan().all() and lse[0, 3:6].isnan().all()
+    out[0, 3:6], lse[0, 3:6] = want[0, 3:6], want_lse[0, 3:6]
+    assert held(out, lse, *exact, fmt)
+    if fmt in attn_ref.EMAX:
+        # block sums past fp32's range whose scores are not: keys of 2^100 against 2^-100
+        cache.k_scale[at] = old
+        cache.k_scale[:, 1, :, :2] += 110
+        kk = k.clone()
+        kk[:, 1] *= 2.0 ** 110
+        x = q.clone()
+        x[:, 3:6] *= 2.0 ** -105
+        exact = attn_ref.attend(x, of(kk), of(v), [n] * B, hk, D ** -0.5)
+        assert held(*call(x), *exact, fmt)
+    else:
+        # -inf scores weigh nothing, a list of them gives zeros
+        cache.k[at] = old
+        cache.k[pages[1, 2].long(), 2] = -math.inf
+        cache.k[int(pages[0, 0, 1]), 0] = -math.inf
+        x = q.abs()
+        out, lse = call(x)
+        assert not out[1, 6:9].any() and (lse[1, 6:9] == -math.inf).all()
+        def seen(rows):
+            def f(b, h):
+                y = of(rows)(b, h)
+                return torch.cat([y[:16], y[32:]]) if (b, h) == (0, 0) else y
+            return f
+        exact = [attn_ref.attend(x[b:b + 1], lambda _, h: seen(k)(b, h), lambda _, h: seen(v)(b, h),
+                                 [n], hk, D ** -0.5) for b in range(B)]
+        exact = [torch.cat(y) for y in zip(*exact)]
+        for y, z in zip((out, lse), exact):
+            y[1, 6:9] = z[1, 6:9].to(y)
+        assert held(out, lse, *exact, fmt)
+
+
+# ---- eviction --------------------------------------------------------------------------------
+@pytest.mark.parametrize("lens", [[300, 500, 40], [9000, 4000, 8500], [60000, 10, 55000]])
+def test_evict_with_masses_of_any_alignment(lens):
+    # masses 4 bytes past a 16-byte boundary; `into` that is the table itself
+    g = ref.gen(*lens)
+    page, keep = 48, 33
+    n_pages = sum(-(-n // page) for n in lens)
+    cache, _, _ = ref.pool(g, "bf16", n_pages, page, 2, 8)
+    table = ref.tables(g, lens, page, n_pages)
+    wide = torch.rand(n_pages * 2 * page + 3, generator=g).cuda()
+    tl = torch.tensor(lens, dtype=torch.int32).cuda()
+    runs = []
+    for off in (0, 1, 3):
+        flat = wide.clone()
+        flat[off:off + n_pages * 2 * page] = wide[:n_pages * 2 * page]
+        mass = flat[off:off + n_pages * 2 * page].view(n_pages, 2, page)
+        pools = [cache.k.clone(), cache.v.clone()]
+        t = table.cuda()
+        kept, held_ = cache.evict(mass, t, tl, keep, first=2, recent=5, into=t if off else None)
+        runs.append([kept, held_, mass.clone(), cache.k.clone(), cache.v.clone()])
+        cache.k.copy_(pools[0]), cache.v.copy_(pools[1])
+    for b, n in enumerate(lens):
+        for h in range(2):
+            m = [float(wide[(int(table[b, j // page]) * 2 + h) * page + j % page])
+                 for j in range(min(n, 600))] if n <= 600 else \
+                wide.cpu()[(table[b].long()[torch.arange(n) // page] * 2 + h) * page +
+                           torch.arange(n) % page].tolist()
+            want = ref.largest(m, keep, 2, 5)
+            assert runs[0][0][b, h, :len(want)].tolist() == want
+    for run in runs[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(run, runs[0]))
+
+
+# ---- streams ---------------------------------------------------------------------------------
+@pytest.mark.parametrize("name", ["page_bounds", "evict", "evict into"])
+def test_inputs_on_another_stream_are_not_given_away(name):
+    n_pages, page, hk, D, B = 4096, 16, 4, 64, 512
+    cache = moe.PagedKVCache(*[torch.ones(n_pages, hk, page, D, dtype=torch.bfloat16,
+                                          device="cuda") for _ in range(2)], head_dim=D)
+    side = torch.cuda.Stream()
+    ids = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    bounds, mass = cache.new_bounds(), cache.new_mass()
+
+    def call(stream):
+        # the tensor that is let go of
+        if name == "page_bounds":
+            x = torch.full((1 << 20,), -1, dtype=torch.int32, device="cuda")
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream())
+            cache.page_bounds(bounds, x, torch.ones_like(x) if stream is None else fills,
+                              stream=stream)
+        else:
+            x = torch.zeros(B, 512, dtype=torch.int32, device="cuda")
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream())
+            cache.evict(mass, x, lens, 4, into=into if name == "evict into" else None,
+                        stream=stream)
+        return x.data_ptr(), x.numel()
+
+    fills, lens, into = torch.ones(1 << 20, dtype=torch.int32, device="cuda"), ids(B), ids(B)[:, None]
+    call(None)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    where, n = call(side)
+    others = [torch.empty(n, dtype=torch.int32, device="cuda") for _ in range(3)]
+    assert all(o.data_ptr() != where for o in others)
+    assert not side.query()
+    torch.cuda.synchronize()
+
+
+def test_bounds_and_evictions_on_another_stream():
+    g = ref.gen(15)
+    cache, k, _ = ref.pool(g, "bf16", 64, 16, 2, 64)
+    side = torch.cuda.Stream()
+    pages = torch.randperm(64, generator=g).int().cuda()
+    fills = torch.full((64,), 16, dtype=torch.int32, device="cuda")
+    want = cache.page_bounds(cache.new_bounds(), pages, fills)
+    table, lens = pages[None].contiguous(), torch.tensor([1000], dtype=torch.int32, device="cuda")
+    mass = torch.rand(64, 2, 16, generator=g).cuda()
+    box = cache.new_bounds()
+    torch.cuda.synchronize()
+    cache.page_bounds(box, pages, fills, stream=side)
+    kept, held_ = cache.evict(mass.clone(), table, lens, 100, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(box, want)
+    m = mass.cpu()[pages.long().cpu()].permute(1, 0, 2).reshape(2, -1)[:, :1000]
+    for h in range(2):
+        assert kept[0, h].tolist() == ref.largest(m[h].tolist(), 100, 0, 0)
+    assert held_.tolist() == [100]
