@@ -567,6 +567,13 @@ def _shaped(name, x, shape, dtype, dev):
                          f"got {x.device} {x.dtype} {tuple(x.shape)}")
 
 
+def _fits(**counts):
+    """Checks that numbers are ones of 32 bits: the call would take them modulo 2^32."""
+    for name, n in counts.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError(f"{name}={n} is no number of 32 bits")
+
+
 def _on(stream):
     """Context in which `stream` (a torch stream or a raw handle) is the current
     one, so that what a call allocates belongs to the stream that uses it."""
@@ -880,6 +887,7 @@ class PagedKVCache:
         B, hq, qs, out, os_ = self._queries(q, out, dev)
         _table("block_table", block_table, B, dev)
         lens = _ids("seq_lens", seq_lens, B, dev)
+        _fits(prefix_len=prefix_len)
         at = None
         if prefix_len > 0:
             _rank("prefix_pages", prefix_pages, 1, "a vector")
@@ -945,6 +953,7 @@ class PagedKVCache:
         _table("block_table", block_table, B, dev)
         at = _ids("seq_lens", seq_lens, B, dev)
         n = block_table.shape[1]
+        _fits(keep=keep, first=first, last=last)
         if keep < 1:
             raise ValueError(f"keep: need 1 or more, got {keep}")
         pages = torch.empty((B, hk, keep), dtype=torch.int32, device=q.device)
@@ -1011,6 +1020,7 @@ class PagedKVCache:
         _shaped("lse", lse, (B, hq), _torch.float32, dev)
         _shaped("mass", mass, tuple(self.k.shape[:3]), _torch.float32, dev)
         kp = None if known is None else _ids("known", known, B, dev)
+        _fits(window=window)
         cfg, _ = self._config(("mass", hq, window, scale), hq, window, scale, lambda: 0)
         rc = lib().coli_attention_mass(self._ref, cfg, q.data_ptr(), qs, B,
                                        block_table.data_ptr(), block_table.shape[1], lens,
@@ -1040,6 +1050,7 @@ class PagedKVCache:
         if into is not None:
             _table("into", into, B, dev, "[{}][pages]")
             ip, n = into.data_ptr(), into.shape[1]
+        _fits(keep=keep, first=first, recent=recent)
         if keep < 1:
             raise ValueError(f"keep: need 1 or more, got {keep}")
         kept = torch.empty((B, self.n_kv_heads, keep), dtype=torch.int32, device=mass.device)

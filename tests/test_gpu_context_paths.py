@@ -581,3 +581,22 @@ def test_bounds_and_evictions_on_another_stream():
     for h in range(2):
         assert kept[0, h].tolist() == ref.largest(m[h].tolist(), 100, 0, 0)
     assert held_.tolist() == [100]
+
+
+# ---- refusals --------------------------------------------------------------------------------
+def test_wrappers_refuse_numbers_of_more_than_32_bits():
+    # taken modulo 2^32, each of them would pass for another one
+    cache, q, pre, table, lens, _, _ = shared_case("bf16", 8, 2, 64, 4096, 300, [40, 20])
+    bounds, mass = cache.new_bounds(), cache.new_mass()
+    lse = torch.zeros(2, 8, device="cuda")
+    pre = torch.zeros(2 ** 20 + 1, dtype=torch.int32, device="cuda")
+    was = mass.clone()
+    for call in (lambda: cache.attend_shared(q, pre, 2 ** 32 + 300, table, lens),
+                 lambda: cache.select_pages(q, bounds, table, lens, 3, first=2 ** 32),
+                 lambda: cache.select_pages(q, bounds, table, lens, 3, last=2 ** 32 + 1),
+                 lambda: cache.accumulate(mass, q, table, lens, lse, window=2 ** 32 + 5),
+                 lambda: cache.evict(mass, table, lens, 10, first=2 ** 32 + 1),
+                 lambda: cache.evict(mass, table, lens, 10, recent=-2 ** 32 + 1)):
+        with pytest.raises(ValueError):
+            call()
+    assert torch.equal(mass, was)
