@@ -779,9 +779,11 @@ template <int FMT>
 cudaError_t launch_heads(const PrefixArgs& p, int grid, cudaStream_t st) {
   if constexpr (FMT == DT_BF16)
     if (p.c.head_dim > 128) return launch<FMT, 256, false>(p, grid, st);
-  if (p.pair)
-    return p.c.head_dim <= 64 ? launch<FMT, 64, true>(p, grid, st)
-                              : launch<FMT, 128, true>(p, grid, st);
+  if (p.pair) {
+    if constexpr (FMT != DT_BF16)  // (bf16 heads to 64 are never paired)
+      if (p.c.head_dim <= 64) return launch<FMT, 64, true>(p, grid, st);
+    return launch<FMT, 128, true>(p, grid, st);
+  }
   return p.c.head_dim <= 64 ? launch<FMT, 64, false>(p, grid, st)
                             : launch<FMT, 128, false>(p, grid, st);
 }

@@ -136,20 +136,22 @@ bool on_tensor_cores(const KvView& c, int rows_of_head) {
 
 // Rows of a segment of k_prefix: 256, two 128-row tiles that share the loads of keys and values, or
 // 128, whose two streams take the tiles by turns. Of an odd number of tiles the last pair is
-// half idle. The whole call behind 32768 tokens with 8 key heads, us, in pairs / alone:
-//   rows of a head      256          384          512          640
-//   bf16, heads of 128  71 / 75    100 / 86    113 / 121   146 / 133
-//   bf16, 64            54 / 50     81 / 67     89 / 85    118 / 104
-//   MXFP8, 128          78 / 84    109 / 112   123 / 143   157 / 173
-//   MXFP8, 64           64 / 68     97 / 93    107 / 118   143 / 144
-//   MXFP4, 128          76 / 75    106 / 100   118 / 128   153 / 154
-// A pair saves 4 us (bf16) to 20 (MX, whose tiles are widened once for both), an idle half
-// costs 20. (Two tiles' queries of heads above 128 leave no room for keys.)
+// half idle. The call behind 32768 tokens with 8 key heads, us, in pairs / alone:
+//   tiles of a head     2        3         4         5         6         11         13
+//   bf16, heads of 128  68 / 71  98 / 83   111 / 116 144 / 130 151 / 162 269 / 255  305 / 312
+//   bf16, 64            50 / 47  78 / 64   86 / 82   115 / 100 120 / 116 219 / 203  255 / 237
+//   MXFP8, 128          75 / 81  106 / 111 118 / 141 154 / 171 163 / 200 293 / 355  339 / 409
+//   MXFP8, 64           60 / 70  94 / 99   103 / 128 139 / 156 145 / 178 266 / 316  310 / 370
+//   MXFP4, 128          74 / 74  103 / 100 115 / 129 151 / 157 157 / 185 284 / 329  328 / 381
+//   MXFP4, 64           60 / 68  94 / 96   103 / 124 139 / 152 145 / 178 266 / 314  310 / 368
+// A pair saves bf16 tiles, whose loads both halves share, 1 to 2 us a tile, and MX ones, which are
+// widened once for both, 2 to 7; an idle half costs what a tile does. bf16 heads to 64 lose in pairs
+// throughout (40 tiles: 719 / 707). (Two tiles' queries of heads above 128 leave no room for keys.)
 int segment_rows(const KvView& c, int rows_of_head) {
   const int tiles = (rows_of_head + kPrefixRows - 1) / kPrefixRows;
-  const bool mx = c.dtype != DT_BF16;
-  const bool pair = tiles > 1 && c.head_dim <= 128 &&
-                    (tiles % 2 == 0 ? mx || c.head_dim > 64 : tiles >= (mx ? 5 : 11));
+  const bool even = tiles % 2 == 0;
+  const bool pair = c.dtype == DT_BF16 ? c.head_dim > 64 && c.head_dim <= 128 && (even || tiles >= 13)
+                                       : even || tiles >= 5;
   return pair ? 2 * kPrefixRows : kPrefixRows;
 }
 

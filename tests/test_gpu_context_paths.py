@@ -600,3 +600,13 @@ def test_wrappers_refuse_numbers_of_more_than_32_bits():
         with pytest.raises(ValueError):
             call()
     assert torch.equal(mass, was)
+
+
+@pytest.mark.parametrize("fmt,D", [("bf16", 64), ("bf16", 128), ("mxfp8", 64), ("mxfp4", 128)])
+@pytest.mark.parametrize("B", [161, 344, 370, 410])
+def test_shared_prefix_of_many_row_tiles(B, fmt, D):
+    # 6, 11, 12 and 13 tiles of 128 rows a key head, alone or in pairs
+    cache, q, pre, table, lens, k_of, v_of = shared_case(fmt, 8, 2, D, 16, 700, [b % 3 for b in range(B)])
+    want = attn_ref.attend(q, k_of, v_of, [700 + b % 3 for b in range(B)], 2, D ** -0.5)
+    out, lse = cache.attend_shared(q, pre, 700, table, lens, return_lse=True)
+    assert held(out, lse, *want, fmt)
