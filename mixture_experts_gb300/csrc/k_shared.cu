@@ -121,14 +121,20 @@ size_t mean_bytes(const KvView& c, int64_t rows) { return align16(rows * c.head_
 size_t part_bytes(const KvView& c, int64_t rows) { return mean_bytes(c, rows) + align16(rows * 8); }
 
 // Whether k_prefix takes the prefix: 128 queries of a key head cost it as much as one, the decode
-// kernel reads the prefix once for every 8 or 16. Behind 32768 tokens, 8 key heads, us, at 8 /
-// 16 / 24 / 64 queries of a key head: bf16 heads of 128 43 / 44 / 44 / 47 against 45 / 56 /
-// 57 / 81, MXFP8 44 / 51 / 50 / 52 against 43 / 57 / 82 / 116, MXFP4 heads of 64 42 / 42 / 42 /
-// 42 against 34 / 38 / 45 / 60; behind 1024 both are bound by the host (28 to 31). bf16 heads of
-// 256 at 12 / 32 / 128 / 256 queries 79 / 80 / 92 / 161 against 91 / 126 / 344 / 606, behind 2048
-// (12, 32) 27 / 28 against 34 / 38; heads of 160 73 / 72 (12, 32) against 74 / 108. MX heads above
-// 128, whose codes would not fit beside what they are widened to, stay with the decode kernel.
-// (k_prefix numbers the pool's rows in 31 bits.)
+// kernel reads the prefix once for every 8 or 16. The call replayed, us, k_prefix / decode
+// kernel at 8, 9, 16, 24, 64 queries of a key head, 8 key heads:
+//   behind 32768  bf16, heads of 128  40 / 39  41 / 50  40 / 51  39 / 53   41 / 74
+//                 bf16, 256           76 / 62  76 / 82  76 / 82  77 / 121  79 / 193
+//                 MXFP8, 128          42 / 36  47 / 47  47 / 49  47 / 68   48 / 109
+//                 MXFP8, 64           40 / 29  40 / 35  41 / 36  41 / 48   41 / 68
+//                 MXFP4, 64           40 / 27  40 / 31  40 / 31  40 / 38   41 / 52
+//   behind 4096   bf16, 128           15 / 19  15 / 25  15 / 25  15 / 26   20 / 32
+//                 MXFP8, 64           15 / 19  15 / 24  15 / 24  15 / 25   21 / 32
+//                 MXFP4, 64           14 / 18  14 / 22  15 / 22  15 / 23   20 / 29
+// One threshold for all lengths: the scratch is sized before the prefix's is known. It costs MX
+// heads of 64 with 9 to 16 queries 5 to 9 us behind the longest prefixes and saves them 7 to 9
+// behind short ones. MX heads above 128, whose codes would not fit beside what they are
+// widened to, stay with the decode kernel. (k_prefix numbers the pool's rows in 31 bits.)
 bool on_tensor_cores(const KvView& c, int rows_of_head) {
   return c.dtype != DT_F32 && (c.head_dim <= 128 || c.dtype == DT_BF16) && rows_of_head > 8 &&
          static_cast<int64_t>(c.n_pages) * c.n_heads * c.page_size < INT32_MAX;
