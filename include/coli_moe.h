@@ -464,8 +464,10 @@ int coli_paged_attention(const coli_kv_cache* cache, const coli_attn_config* cfg
  * sequence b sees the prefix_len tokens of the pages prefix_pages [ceil(prefix_len /
  * page_size)], then its own seq_lens[b] tokens (0 or more; the new one among
  * them) in block_table[b]. Same result as coli_paged_attention over both, but the
- * prefix is read once for all sequences. prefix_len is a host number, up to
- * 2^31 - 2^16 (0: no prefix, prefix_pages may be NULL); own tokens begin a page of their own.
+ * prefix is read once for 128 or 256 query rows of a key head (the heads of all
+ * sequences on it), or, F32 and MX heads above 128 or up to 8 rows, for 8 or 16.
+ * prefix_len is a host number, up to 2^31 - 2^16 (0: no prefix, prefix_pages may
+ * be NULL); own tokens begin a page of their own.
  * cfg->window has to be 0. A prefix page outside the pool is left out and latches
  * COLI_EDEVICE. The prefix's products take bf16 and MX operands as bf16 (MX keys
  * and values outside bf16's range are rounded to it, as coli_kv_read does) or,
@@ -545,7 +547,8 @@ int coli_attention_mass(const coli_kv_cache* cache, const coli_attn_config* cfg,
  * [B][n_kv_heads][keep] receives the old places, -1 from the last on, new_lens [B]
  * (not seq_lens itself) min(seq_lens[b], keep). What lies behind the kept rows
  * stays as it was. Rotated keys keep their positions: new tokens go on from
- * the old length. Pages of another sequence of the call must not be cut in place.
+ * the old length. In place, a page of a sequence that is cut must be in no other
+ * sequence of the call.
  * Pages outside the pool are left out (mass -inf) and latch COLI_EDEVICE. */
 int coli_kv_evict(const coli_kv_cache* cache, float* mass, int32_t B, const int32_t* block_table,
                   int32_t max_pages, const int32_t* seq_lens, int32_t keep, int32_t first,

@@ -875,7 +875,7 @@ class PagedKVCache:
     def attend_shared(self, q, prefix_pages, prefix_len, block_table, seq_lens, scale=None,
                       out=None, return_lse=False, stream=None):
         """attend for B sequences behind one prefix of prefix_len tokens (a host number)
-        in prefix_pages [pages] int32 (None without a prefix), which is read once for all;
+        in prefix_pages [pages] int32 (None without a prefix), read for many queries at once;
         block_table and seq_lens are the sequences' own tokens behind it."""
         if stream is not None:
             with _on(stream):

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(THREADS) k_evict_pick(const EvictArgs p) {
   };
   if constexpr (CACHED) {  // four tokens of a page at once, eight such loads in flight
     constexpr int kDeep = THREADS == 1024 ? 8 : 4;
-    const uint32_t per = 0xffffffffu / page + 1;  // i / page = i * per / 2^32, or one less
+    const uint32_t per = 0xffffffffu / page + 1;  // i * per / 2^32 is i / page, or one more
     const bool whole = (reinterpret_cast<uintptr_t>(p.mass) & 15) == 0;
     for (int i0 = threadIdx.x * 4; i0 < n; i0 += THREADS * 4 * kDeep) {
       int at[kDeep], off[kDeep];

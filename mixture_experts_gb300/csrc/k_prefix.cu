@@ -30,15 +30,20 @@
 // slot (block + segment), which k_shared_join joins in the line's order with each sequence's
 // own tokens.
 //
-// What bounds it (GB300, heads of 128): the products. 24 instructions of 128 x 128 x 16 a unit
-// (128 rows by 128 keys) take 2460 cycles, 100 each where 64 is the pipe's rate: the first
-// product's operands are all of a shared-memory port's 128 bytes a clock. 64 sequences of 32
-// heads on 8 behind 32768 bf16 tokens 54 us, 128 of 64 on 8 behind 40009 MXFP8 ones 201 us (845
-// TFLOP/s, 1270 with the second weight term), which ncu has at 43% to 50% of the tensor pipe. The
+// What bounds it (GB300, heads of 128): the products, 24 instructions of 128 x 128 x 16 a unit
+// (128 rows by 128 keys). By the SM's clock a unit of paired bf16 rows takes 2330 cycles, of which
+// the warp that issues the products waits 220 for weights and 250 for tiles; in the rest the tensor
+// cores take an instruction every 78, where the pipe's rate is 64. A stream goes from
+// its scores to its weights in 2130 cycles and then waits 1900 for the next scores. MXFP8: 2640 a
+// unit, 190 and 300 of them waits, 2440 from scores to weights. 128 rows alone load a tile for half the
+// products: 2850, 920 of them waits for tiles. 64 sequences of 32 heads on 8 behind 32768 bf16 tokens
+// 54 us, 128 of 64 on 8 behind 40009 MXFP8 ones 201 us (835 TFLOP/s, 1250 with the second
+// weight term); ncu has the tensor pipe at 43% to 50%, starts and ends included. The
 // second term costs a third of the products; without it the output's error would be 1.2 times
 // the rounding's own. What a block does once (queries, first tiles, the last means) takes 8 us.
 // Heads of 256: 64 instructions for 128 rows by 128 keys, a quarter of them the scores formed
-// twice; the call of 64 sequences of 32 heads on 8 behind 32768 tokens 161 us.
+// twice, and keys loaded for 128 rows and half of the values: 4060 cycles a unit, 1740 of them waits
+// for tiles; the call of 64 sequences of 32 heads on 8 behind 32768 tokens 161 us.
 #include <limits.h>
 
 #include "tcgen05.cuh"
