@@ -890,6 +890,8 @@ class PagedKVCache:
         _fits(prefix_len=prefix_len)
         at = None
         if prefix_len > 0:
+            if prefix_pages is None:
+                raise ValueError(f"prefix_pages: need those of a prefix of {prefix_len} tokens")
             _rank("prefix_pages", prefix_pages, 1, "a vector")
             n = prefix_pages.shape[0]
             if n * self.page_size < prefix_len:

@@ -610,3 +610,81 @@ def test_shared_prefix_of_many_row_tiles(B, fmt, D):
     want = attn_ref.attend(q, k_of, v_of, [700 + b % 3 for b in range(B)], 2, D ** -0.5)
     out, lse = cache.attend_shared(q, pre, 700, table, lens, return_lse=True)
     assert held(out, lse, *want, fmt)
+
+
+def test_a_prefix_without_pages_is_refused():
+    cache, q, pre, table, lens, _, _ = shared_case("bf16", 8, 2, 64, 16, 30, [4, 2])
+    with pytest.raises(ValueError):
+        cache.attend_shared(q, None, 30, table, lens)
+
+
+# ---- outputs and pages -----------------------------------------------------------------------
+@pytest.mark.parametrize("fmt,hq,hk,D", [("bf16", 16, 2, 64), ("bf16", 4, 4, 72), ("mxfp8", 16, 2, 64),
+                                         ("bf16", 12, 1, 256), ("f32", 8, 2, 80), ("mxfp4", 4, 4, 96)])
+def test_outputs_in_wider_rows(fmt, hq, hk, D):
+    own = [40, 0, 700, 1, 16] * 3
+    cache, q, pre, table, lens, _, _ = shared_case(fmt, hq, hk, D, 16, 333, own)
+    pages, seen = cache.select_pages(q, cache.new_bounds(), table, lens, 4)
+    for call in (lambda **kw: cache.attend_shared(q, pre, 333, table, lens, **kw),
+                 lambda **kw: cache.attend_shared(q, None, 0, table, lens, **kw),
+                 lambda **kw: cache.attend_selected(q, pages, seen, **kw)):
+        want = call()
+        wide = torch.full((len(own), hq + 3, D), 9.0, dtype=q.dtype, device="cuda")
+        out, lse = call(out=wide[:, 1:1 + hq] if D * q.element_size() % 16 == 0 else wide[:, :hq],
+                        return_lse=True)
+        assert torch.equal(out, want) and out.data_ptr() != want.data_ptr()
+        assert (wide[:, 0] == 9).all() and (wide[:, 1 + hq:] == 9).all()
+        assert lse.shape == (len(own), hq)
+
+
+@pytest.mark.parametrize("fmt", list(ref.FMT))
+@pytest.mark.parametrize("B", [3, 40])
+def test_own_and_chosen_pages_outside_the_pool_are_left_out(B, fmt):
+    own, prefix = [60, 33, 0, 2000 if B == 3 else 90] * (B // 3), 100
+    own = own[:B]
+    cache, q, pre, table, lens, k_of, v_of = shared_case(fmt, 8, 2, 64, 16, prefix, own)
+    bad = table.clone()
+    n_pages = cache.k.shape[0]
+    bad[0, 1], bad[1, 0] = n_pages, -5
+    gone = {0: [prefix + j for j in range(16, 32)], 1: [prefix + j for j in range(16)]}
+
+    def left(rows):
+        def f(b, h):
+            x = rows(b, h)
+            keep = [j for j in range(len(x)) if j not in gone.get(b, [])]
+            return x[keep]
+        return f
+
+    n = [prefix + m - len(gone.get(b, [])) for b, m in enumerate(own)]
+    want = attn_ref.attend(q, left(k_of), left(v_of), n, 2, 0.125)
+    got = cache.attend_shared(q, pre, prefix, bad, lens, return_lse=True)
+    assert moe.coli_device_status() == moe.COLI_EDEVICE
+    assert held(*got, *want, fmt)
+    # the same for lists of each key head's own, and for lengths that are none
+    only = [lambda b, h, r=r: left(r)(b, h)[prefix:] for r in (k_of, v_of)]
+    want = attn_ref.attend(q, *only, [m - prefix for m in n], 2, 0.125)
+    lists = bad[:, None].expand(-1, 2, -1).contiguous()
+    out, lse = cache.attend_selected(q, lists, lens, return_lse=True)
+    assert moe.coli_device_status() == moe.COLI_EDEVICE
+    none = torch.isinf(want[1])
+    assert torch.equal(torch.isinf(lse).cpu(), none) and not out[none.cuda()].any()
+    lse[none.cuda()], want[1][none] = 0, 0
+    assert held(out, lse, *want, fmt)
+    odd = lens.clone()
+    odd[0], odd[1] = -7, table.shape[1] * 16 + 1
+    whole = table.clamp(min=0)
+    fine = odd.clamp(0, table.shape[1] * 16)
+    a = cache.attend_shared(q, pre, prefix, whole, fine, return_lse=True)
+    p0, s0 = cache.select_pages(q, cache.new_bounds(), whole, fine, 3)
+    m0 = cache.accumulate(cache.new_mass(), q, whole, fine, a[1])
+    assert moe.coli_device_status() == moe.COLI_OK
+    b = cache.attend_shared(q, pre, prefix, whole, odd, return_lse=True)
+    assert moe.coli_device_status() == moe.COLI_EDEVICE
+    p1, s1 = cache.select_pages(q, cache.new_bounds(), whole, odd, 3)
+    assert moe.coli_device_status() == moe.COLI_EDEVICE
+    m1 = cache.accumulate(cache.new_mass(), q, whole, odd, a[1])
+    assert moe.coli_device_status() == moe.COLI_EDEVICE
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert torch.equal(p0, p1) and torch.equal(s0, s1)
+    # (pages of several sequences: sums in any order)
+    assert torch.allclose(m0, m1, rtol=2.0 ** -20, atol=0)
