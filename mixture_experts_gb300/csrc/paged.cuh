@@ -834,9 +834,10 @@ __global__ void __launch_bounds__(Cfg<FMT, DP, NT>::kWarps * 32, Cfg<FMT, DP, NT
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e = static_cast<int>(top >> 23) - 127;
         e = e < -112 ? -112 : e;
-        // Against such queries key scales of 2^-127, which count as 0 below, or scores
-        // near the smallest numbers would show
-        odd |= top != 0 && (e > 80 || e < -80);
+        // Against such queries (or such a scale) key scales of 2^-127, which count as 0 below, or
+        // scores near the smallest numbers would show
+        odd |= top != 0 && (max(e, e + static_cast<int>(__float_as_uint(sl) >> 23 & 255u) - 127) > 80 ||
+                            e < -80);
         const float up = __uint_as_float(static_cast<uint32_t>(kTop - e + 127) << 23);
         const uint32_t fit = static_cast<uint32_t>(e - kFit + 127) << 23;
         if (__any_sync(0xffffffffu, r < p.group && min(least << 16, least & 0x7fff0000u) < fit)) {

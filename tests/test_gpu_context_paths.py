@@ -688,3 +688,25 @@ def test_own_and_chosen_pages_outside_the_pool_are_left_out(B, fmt):
     assert torch.equal(p0, p1) and torch.equal(s0, s1)
     # (pages of several sequences: sums in any order)
     assert torch.allclose(m0, m1, rtol=2.0 ** -20, atol=0)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_decode_attention_of_the_least_key_scales(fmt):
+    # keys of 2^-127 against queries of 2^77 under a scale that makes ordinary scores of them
+    g = ref.gen(92)
+    D, lens, scale = 64, [100, 17], 2.0 ** 47
+    cache, _, v = ref.pool(g, fmt, 12, 16, 1, D)
+    cache.k_scale[..., :2] = 0
+    k = attn_ref.decode(cache.k, cache.k_scale, fmt)
+    table = ref.tables(g, lens, 16, 12)
+    q = (torch.randn(2, 4, D, generator=g) * 2.0 ** 76).bfloat16().cuda()
+    tl = torch.tensor(lens, dtype=torch.int32).cuda()
+    rows = [lambda b, h, x=x: ref.context(x, table[b].tolist(), h, lens[b]) for x in (k, v)]
+    want = list(attn_ref.attend(q, *rows, lens, 1, scale))
+    # scores lie hundreds apart: a weight below 2^-126, the least normal fp32 number, may count as
+    # 0, which is worth 2^-126 sum |v| at most (e^-124 here is 2^-179, an output of 3.6e-54)
+    want[2] = want[2] + 2.0 ** -126 * torch.stack(
+        [rows[1](b, 0).abs().sum(0) for b in range(2)])[:, None]
+    assert held(*cache.attend(q, table.cuda(), tl, scale=scale, return_lse=True), *want, fmt)
+    assert held(*cache.attend_selected(q, table[:, None].contiguous().cuda(), tl, scale=scale,
+                                       return_lse=True), *want, fmt)
