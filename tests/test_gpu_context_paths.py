@@ -710,3 +710,44 @@ def test_decode_attention_of_the_least_key_scales(fmt):
     assert held(*cache.attend(q, table.cuda(), tl, scale=scale, return_lse=True), *want, fmt)
     assert held(*cache.attend_selected(q, table[:, None].contiguous().cuda(), tl, scale=scale,
                                        return_lse=True), *want, fmt)
+
+
+# ---- captured calls --------------------------------------------------------------------------
+@pytest.mark.parametrize("before", ["nothing", "memset", "copy", "fork"])
+def test_calls_captured_behind_other_work(before):
+    # each call as the first of a graph, or behind a node that is no kernel
+    own = [50, 0, 130, 16] * 10
+    cache, q, pre, table, lens, _, _ = shared_case("bf16", 16, 4, 64, 16, 333, own)
+    g = ref.gen(17)
+    bounds = cache.new_bounds()
+    bounds.copy_(torch.randn(bounds.shape, generator=g).sort(2).values)
+    table = table.clamp(min=0)
+    mass = torch.rand(cache.new_mass().shape, generator=g).cuda()
+    some, host = torch.empty(1 << 20, device="cuda"), torch.empty(1 << 20).pin_memory()
+    calls = {
+        "all": lambda: cache.select_pages(q, bounds, table, lens, table.shape[1]),
+        "few": lambda: cache.select_pages(q, bounds, table, lens, 3),
+        "shared": lambda: cache.attend_shared(q, pre, 333, table, lens, return_lse=True),
+        "selected": lambda: cache.attend_selected(q, table[:, None].expand(-1, 4, -1).contiguous(),
+                                                  lens, return_lse=True),
+        "evict": lambda: cache.evict(mass, table, lens.clamp(max=12), 12)}
+    for name, call in calls.items():
+        want = call()
+        torch.cuda.synchronize()
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph):
+            if before == "memset":
+                some.zero_()
+            elif before == "copy":
+                some.copy_(host, non_blocking=True)
+            elif before == "fork":
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    some.add_(1)
+                torch.cuda.current_stream().wait_stream(side)
+            got = call()
+        for _ in range(2):
+            for x in got:
+                x.fill_(5)
+            graph.replay()
+            assert all(torch.equal(x, y) for x, y in zip(got, want)), name
